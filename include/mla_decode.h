@@ -333,6 +333,209 @@ MLA_API int mla_decode_kvcache_noalloc(const void *q, const void *kcache, int64_
                                        const int32_t *num_splits, int num_parts, float softmax_scale,
                                        int causal, void *o, float *lse, struct CUstream_st *stream);
 
+/* largest |scale| of an e4m3 token that the decode accepts (exclusive) */
+#define MLA_FP8_SCALE_LIMIT 255
+
+/*
+ * mla_cache_write — write the rows of new tokens into the paged bf16 cache.
+ *
+ * Input row r is the latent part latent[r][0..512) followed, for d = 576, by
+ * the RoPE part k_rope[r][0..64).  It belongs to sequence b with
+ * cu_rows[b] <= r < cu_rows[b + 1] and becomes the cached row at position
+ * starts[b] + r - cu_rows[b] of that sequence.  Rows at or behind
+ * cu_rows[batch] (a padded input buffer) and rows before cu_rows[0] are ignored.
+ *   latent, k_rope   device bf16, rows latent_stride / k_rope_stride elements
+ *                    apart (multiples of 8; 0 repeats one row); 16-byte aligned.
+ *                    d = 512: k_rope is not read and may be NULL
+ *   num_rows         rows of the input, >= 0 (0: nothing is launched)
+ *   cu_rows          device int32 [batch + 1], non-decreasing, or NULL: every
+ *                    sequence has num_rows / batch rows (batch divides num_rows)
+ *   starts           device int32 [batch]: position of the sequence's first row
+ *   kcache           device bf16 [num_blocks][64][1][d], in/out; 16-byte aligned
+ *   block_table      device int32 [batch][max_blocks_per_seq]
+ *   d                576 or 512
+ * Nothing but the named rows is touched.  A position outside
+ * [0, 64 * max_blocks_per_seq) sets MLA_DEVERR_SEQLEN and a block id outside
+ * [0, num_blocks) MLA_DEVERR_BLOCK_ID; the row is then skipped.  Two rows that
+ * name the same place in one call leave either row's values, piece by piece.
+ * One kernel is enqueued as a programmatic dependent launch; it can be captured
+ * in a CUDA graph once any call of the library has run on the device.
+ * Errors: MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED, MLA_ERR_CUDA.
+ */
+MLA_API int mla_cache_write(const void *latent, int64_t latent_stride, const void *k_rope, int64_t k_rope_stride,
+                            int64_t num_rows, const int32_t *cu_rows, const int32_t *starts, int batch, void *kcache,
+                            int64_t num_blocks, const int32_t *block_table, int max_blocks_per_seq, int d,
+                            struct CUstream_st *stream);
+
+/*
+ * mla_cache_write_fp8 — the same into packed e4m3 pages, quantised per token
+ * (d = 576 only; the page layout of mla_decode_kvcache_fp8):
+ *   c_j = max |x| / 448 over the row (1 for a row of zeros), code = e4m3(x / c_j)
+ * with both quotients in fp32 (IEEE) and round to nearest even.  A row whose
+ * scale reaches MLA_FP8_SCALE_LIMIT, or that holds a NaN or an infinity (its
+ * scale becomes NaN), sets MLA_DEVERR_SCALE: the decode would report it too.
+ */
+MLA_API int mla_cache_write_fp8(const void *latent, int64_t latent_stride, const void *k_rope, int64_t k_rope_stride,
+                                int64_t num_rows, const int32_t *cu_rows, const int32_t *starts, int batch,
+                                void *kv_pages, int64_t num_blocks, const int32_t *block_table, int max_blocks_per_seq,
+                                int d, struct CUstream_st *stream);
+
+/*
+ * mla_cache_read — read a range of each sequence's cached rows back into
+ * contiguous rows (what the prompt path up-projects): output row r of sequence
+ * b (cu_rows as for mla_cache_write) is the cached row at position
+ * starts[b] + r - cu_rows[b], its first 512 dims into latent[r] and, for
+ * d = 576, its last 64 into k_rope[r].
+ *   latent, k_rope   device bf16, out; strides as for mla_cache_write, but at
+ *                    least 512 / 64 (rows must not overlap)
+ * Output rows of no sequence, and rows that are skipped as in mla_cache_write,
+ * are left as they were.  The rest as for mla_cache_write.
+ */
+MLA_API int mla_cache_read(const void *kcache, int64_t num_blocks, const int32_t *block_table, int max_blocks_per_seq,
+                           const int32_t *starts, const int32_t *cu_rows, int batch, int64_t num_rows, void *latent,
+                           int64_t latent_stride, void *k_rope, int64_t k_rope_stride, int d,
+                           struct CUstream_st *stream);
+
+/*
+ * mla_cache_read_fp8 — the same from packed e4m3 pages (d = 576): every value is
+ * c_j * e4m3(code) in fp32, rounded to bf16 (nearest even).
+ */
+MLA_API int mla_cache_read_fp8(const void *kv_pages, int64_t num_blocks, const int32_t *block_table,
+                               int max_blocks_per_seq, const int32_t *starts, const int32_t *cu_rows, int batch,
+                               int64_t num_rows, void *latent, int64_t latent_stride, void *k_rope,
+                               int64_t k_rope_stride, int d, struct CUstream_st *stream);
+
+/*
+ * mla_update_page_keys — recompute the page keys that mla_decode_kvcache_blocks
+ * scores, for every page that the positions [starts[b], cache_seqlens[b]) of
+ * some sequence touch (the whole page is summarised, from its first row to the
+ * sequence's end).  For a page with n rows inside its sequence:
+ *   mean  = (sum of its n rows) / n   in fp32, summed as a balanced tree over the
+ *           64 rows (neighbours first, absent rows 0)
+ *   scale = max |mean| / 127 (1 for a mean of zeros),  key = rint(mean / scale)
+ * (IEEE fp32 quotients).  A mean that is not finite gives key 0 and scale NaN.
+ *   cache_seqlens  device int32 [batch], as for mla_decode_kvcache
+ *   starts         device int32 [batch] (e.g. the lengths before the last write),
+ *                  or NULL: every page of every sequence
+ *   page_keys      device int8 [num_blocks][d], in/out; 16-byte aligned
+ *   page_scales    device fp32 [num_blocks], in/out
+ * Entries of other pages are left as they were.  A page shared by two sequences
+ * must have the same rows in both.  Lengths outside [0, 64 *
+ * max_blocks_per_seq] and bad block ids set status bits, as for the decode.
+ * Launches, capture and errors: as for mla_cache_write.
+ */
+MLA_API int mla_update_page_keys(const void *kcache, int64_t num_blocks, const int32_t *block_table,
+                                 int max_blocks_per_seq, const int32_t *cache_seqlens, const int32_t *starts, int batch,
+                                 int d, int8_t *page_keys, float *page_scales, struct CUstream_st *stream);
+/* the same over packed e4m3 pages (d = 576): the rows c_j * e4m3(code) in fp32 */
+MLA_API int mla_update_page_keys_fp8(const void *kv_pages, int64_t num_blocks, const int32_t *block_table,
+                                     int max_blocks_per_seq, const int32_t *cache_seqlens, const int32_t *starts,
+                                     int batch, int d, int8_t *page_keys, float *page_scales,
+                                     struct CUstream_st *stream);
+
+/*
+ * mla_blocks_workspace_bytes — device scratch of mla_decode_kvcache_blocks
+ * (num_parts from mla_num_sm_parts(device, h_q, h_kv)).  0 on invalid arguments.
+ */
+MLA_API size_t mla_blocks_workspace_bytes(int batch, int s_q, int h_q, int h_kv, int dv, int max_blocks_per_seq,
+                                          int topk_pages, int num_parts);
+
+/*
+ * mla_decode_kvcache_blocks — sparse decode over whole pages: each query token
+ * attends to topk_pages pages that a score against the page keys selects for it.
+ *
+ * Query token i of sequence b sees positions < L (L = T_b, or the causal
+ * T_b - s_q + i + 1), on ceil(L / 64) pages.  With at most topk_pages of them it
+ * takes all; otherwise the first sink_pages, the last local_pages, and of the
+ * rest those with the highest scores, ties to the lowest page:
+ *   u_h   = max |q_h| / 127 (1 for a head of zeros),  qi_h = rint(q_h / u_h)
+ *   score = page_scales[blk] * max_h (u_h * <qi_h, page_keys[blk]>)
+ * The integer product is exact and each of the two fp32 products is rounded
+ * once, so the selection does not depend on how it is computed.  A NaN score
+ * (a query or a mean that is not finite) ranks highest.  o and lse are then
+ * those of mla_decode_kvcache over the rows of the selected pages that lie
+ * before L; a token with L <= 0 gets o = 0, lse = -inf and no pages.
+ *   q, kcache, block_table, cache_seqlens, o, lse
+ *                  as for mla_decode_kvcache (d = 576 or 512; batch * s_q <= 65535)
+ *   page_keys, page_scales
+ *                  from mla_update_page_keys; 16-byte aligned keys
+ *   topk_pages     pages per query token, >= sink_pages + local_pages
+ *   sink_pages, local_pages
+ *                  >= 0 and >= 1 (the last visible page, which may be partial, is
+ *                  always taken)
+ *   num_parts      split-KV parts of the decode: mla_num_sm_parts(device, h_q, h_kv)
+ *   softmax_scale  > 0
+ *   causal         nonzero: the causal rule above
+ *   pages          device int32 [batch][s_q][topk_pages], out: the selected
+ *                  pages of each token (logical, ascending), -1 behind them
+ *   workspace      device scratch of at least mla_blocks_workspace_bytes(...)
+ *                  bytes, 256-byte aligned
+ * Five kernels are enqueued on `stream` (scores, selection, partition, split-KV,
+ * combine).  Stream order, graph capture, status bits and errors: as for
+ * mla_decode_kvcache.
+ */
+MLA_API int mla_decode_kvcache_blocks(const void *q, const void *kcache, int64_t num_blocks,
+                                      const int32_t *block_table, int max_blocks_per_seq,
+                                      const int32_t *cache_seqlens, const int8_t *page_keys, const float *page_scales,
+                                      int topk_pages, int sink_pages, int local_pages, int batch, int s_q, int h_q,
+                                      int h_kv, int d, int dv, int num_parts, float softmax_scale, int causal, void *o,
+                                      float *lse, int32_t *pages, void *workspace, size_t workspace_bytes,
+                                      struct CUstream_st *stream);
+/* the same over packed e4m3 pages (d = 576; precision as for mla_decode_kvcache_fp8) */
+MLA_API int mla_decode_kvcache_blocks_fp8(const void *q, const void *kv_pages, int64_t num_blocks,
+                                          const int32_t *block_table, int max_blocks_per_seq,
+                                          const int32_t *cache_seqlens, const int8_t *page_keys,
+                                          const float *page_scales, int topk_pages, int sink_pages, int local_pages,
+                                          int batch, int s_q, int h_q, int h_kv, int d, int dv, int num_parts,
+                                          float softmax_scale, int causal, void *o, float *lse, int32_t *pages,
+                                          void *workspace, size_t workspace_bytes, struct CUstream_st *stream);
+
+/*
+ * mla_tree_mask — the masks of draft trees from their parent lists.
+ *
+ *   parents    device int32 [batch][s_q]: the parent of each node, a node before
+ *              it, or -1 (a root).  Any other value sets MLA_DEVERR_SEQLEN and
+ *              counts as -1
+ *   tree_mask  device int32 [batch][s_q][ceil(s_q / 32)], out: bit j % 32 of word
+ *              j / 32 of row i is set when j is node i or an ancestor of it
+ * Errors: MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED (s_q > 65536), MLA_ERR_CUDA.
+ */
+MLA_API int mla_tree_mask(const int32_t *parents, int batch, int s_q, int32_t *tree_mask, struct CUstream_st *stream);
+
+/*
+ * mla_decode_kvcache_tree — decode of a tree of drafted tokens.
+ *
+ * The last n_b = tree_lens[b] of the T_b cached rows of sequence b are drafted
+ * nodes (written before the call), and query token i < n_b is node i.  It sees
+ * every position before the nodes, and node j (position T_b - n_b + j) exactly
+ * where bit j % 32 of word j / 32 of tree_mask[b][i] is set; its own bit too is
+ * the mask's to set.  A row that sees nothing, and every row of a token
+ * i >= n_b (a padded batch), gets o = 0 and lse = -inf.
+ *   tree_mask  device int32 [batch][s_q][ceil(s_q / 32)] (mla_tree_mask, or any bits)
+ *   tree_lens  device int32 [batch], 0 <= n_b <= s_q, or NULL: s_q everywhere.
+ *              A value outside sets MLA_DEVERR_SEQLEN and is clamped
+ *   everything else as for mla_decode_kvcache (d = 576 or 512; no causal
+ *   argument: a chain's mask is the causal one).  T_b < n_b drops the nodes that
+ *   would lie before the sequence.
+ * A cached row that some query token of its sequence sees must be finite (a
+ * non-finite one makes that token's output NaN, and may make that of the tokens
+ * of the same 128-row tile); a node's row that no token sees may hold any bits.
+ */
+MLA_API int mla_decode_kvcache_tree(const void *q, const void *kcache, int64_t num_blocks, const int32_t *block_table,
+                                    int max_blocks_per_seq, const int32_t *cache_seqlens, const int32_t *tree_mask,
+                                    const int32_t *tree_lens, int batch, int s_q, int h_q, int h_kv, int d, int dv,
+                                    const int32_t *tile_scheduler_metadata, const int32_t *num_splits, int num_parts,
+                                    float softmax_scale, void *o, float *lse, void *workspace, size_t workspace_bytes,
+                                    struct CUstream_st *stream);
+/* the same over packed e4m3 pages (d = 576; precision and scales as for mla_decode_kvcache_fp8) */
+MLA_API int mla_decode_kvcache_tree_fp8(const void *q, const void *kv_pages, int64_t num_blocks,
+                                        const int32_t *block_table, int max_blocks_per_seq,
+                                        const int32_t *cache_seqlens, const int32_t *tree_mask,
+                                        const int32_t *tree_lens, int batch, int s_q, int h_q, int h_kv, int d, int dv,
+                                        const int32_t *tile_scheduler_metadata, const int32_t *num_splits,
+                                        int num_parts, float softmax_scale, void *o, float *lse, void *workspace,
+                                        size_t workspace_bytes, struct CUstream_st *stream);
+
 /*
  * mla_device_status — read the device status word of the current device.
  *

@@ -25,6 +25,8 @@ MLA_HEAD_DIM = 576
 MLA_V_DIM = 512
 MLA_METADATA_INTS = 8
 
+MLA_FP8_SCALE_LIMIT = 255
+
 MLA_NOALLOC_SCRATCH_BYTES = 64 * 1024 * 1024
 
 
@@ -52,6 +54,22 @@ SIGNATURES = {
                                        _P, _P, _P, _SZ, _P]),
     "mla_decode_kvcache_noalloc": (_I, [_P, _P, _I64, _P, _I, _P, _I, _I, _I, _I, _I, _I, _P, _P, _I, _F, _I, _P,
                                         _P, _P]),
+    "mla_cache_write": (_I, [_P, _I64, _P, _I64, _I64, _P, _P, _I, _P, _I64, _P, _I, _I, _P]),
+    "mla_cache_write_fp8": (_I, [_P, _I64, _P, _I64, _I64, _P, _P, _I, _P, _I64, _P, _I, _I, _P]),
+    "mla_cache_read": (_I, [_P, _I64, _P, _I, _P, _P, _I, _I64, _P, _I64, _P, _I64, _I, _P]),
+    "mla_cache_read_fp8": (_I, [_P, _I64, _P, _I, _P, _P, _I, _I64, _P, _I64, _P, _I64, _I, _P]),
+    "mla_update_page_keys": (_I, [_P, _I64, _P, _I, _P, _P, _I, _I, _P, _P, _P]),
+    "mla_update_page_keys_fp8": (_I, [_P, _I64, _P, _I, _P, _P, _I, _I, _P, _P, _P]),
+    "mla_blocks_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I, _I, _I]),
+    "mla_decode_kvcache_blocks": (_I, [_P, _P, _I64, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I, _F,
+                                       _I, _P, _P, _P, _P, _SZ, _P]),
+    "mla_decode_kvcache_blocks_fp8": (_I, [_P, _P, _I64, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I,
+                                           _F, _I, _P, _P, _P, _P, _SZ, _P]),
+    "mla_tree_mask": (_I, [_P, _I, _I, _P, _P]),
+    "mla_decode_kvcache_tree": (_I, [_P, _P, _I64, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _I, _F, _P,
+                                     _P, _P, _SZ, _P]),
+    "mla_decode_kvcache_tree_fp8": (_I, [_P, _P, _I64, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _I, _F,
+                                         _P, _P, _P, _SZ, _P]),
     "mla_device_status": (_I, [ctypes.POINTER(ctypes.c_int), _I]),
     "mla_set_timing_events": (_I, [_P, _P]),
     "mla_set_cluster_multicast": (_I, [_I]),

@@ -136,10 +136,10 @@ def _dense_decode_args(q, kcache, block_table, cache_seqlens, dv, tile_scheduler
     return b, s_q, h_q, d, num_blocks, h_kv, tile_scheduler_metadata.shape[0], out, lse
 
 
-def _same_device(dev: torch.device, **tensors) -> None:
+def _same_device(dev: torch.device, of: str = "q", **tensors) -> None:
     for name, t in tensors.items():
         if t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, but q is on {dev}")
+            raise ValueError(f"{name} is on {t.device}, but {of} is on {dev}")
 
 
 def mla_decode_kvcache(q: torch.Tensor, kcache: torch.Tensor, block_table: torch.Tensor,
@@ -314,6 +314,366 @@ def mla_decode_kvcache_noalloc(q: torch.Tensor, kcache: torch.Tensor, block_tabl
             num_splits.data_ptr(), num_parts, float(softmax_scale), int(bool(causal)),
             out.data_ptr(), lse.data_ptr(), _stream_handle(dev))
     check("mla_decode_kvcache_noalloc", st)
+
+
+# ---------------------------------------------------------------- cache rows
+def _need_rows(name: str, t: torch.Tensor, cols: int, written: bool) -> int:
+    """bf16 [n, cols] with unit inner stride, 16-byte aligned rows; returns the row stride in elements."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.dim() != 2 or t.shape[1] != cols or t.stride(1) != 1:
+        raise ValueError(f"{name} must be [rows, {cols}] with contiguous rows")
+    if t.shape[0] <= 1:
+        stride = cols
+    else:
+        stride = t.stride(0)
+        if stride % 8 or (written and stride < cols):
+            raise ValueError(f"{name}: the row stride must be a multiple of 8 elements"
+                             + (" and rows must not overlap" if written else ""))
+    if t.data_ptr() % 16:
+        raise ValueError(f"{name} must be 16-byte aligned")
+    return stride
+
+
+def _paged_args(cache, block_table, fp8):
+    """Check a paged cache and its table; returns (num_blocks, d)."""
+    _need_cuda("block_table", block_table, torch.int32)
+    if block_table.dim() != 2 or block_table.shape[0] < 1 or block_table.shape[1] < 1:
+        raise ValueError("block_table must be [b, max_blocks], neither of them 0")
+    if fp8:
+        _need_cuda("kv_pages", cache, torch.uint8)
+        d = _lib.MLA_HEAD_DIM
+        if cache.dim() != 2 or cache.shape[1] != _lib.MLA_FP8_PAGE_BYTES(d):
+            raise ValueError(f"kv_pages must be [num_blocks, {_lib.MLA_FP8_PAGE_BYTES(d)}]")
+    else:
+        _need_cuda("kcache", cache, torch.bfloat16)
+        if cache.dim() != 4 or cache.shape[1] != _lib.MLA_PAGE_SIZE or cache.shape[2] != 1:
+            raise ValueError("kcache must be [num_blocks, 64, 1, d]")
+        d = cache.shape[3]
+    return cache.shape[0], d
+
+
+def _need_vector(name: str, t: torch.Tensor, n: int) -> None:
+    _need_cuda(name, t, torch.int32)
+    if t.dim() != 1 or t.shape[0] != n:
+        raise ValueError(f"{name} must be [{n}]")
+
+
+def _cache_rows(call, cache, block_table, starts, num_rows, cu_rows, latent, k_rope, fp8, write):
+    num_blocks, d = _paged_args(cache, block_table, fp8)
+    b, max_blocks = block_table.shape
+    dev = cache.device
+    _need_vector("starts", starts, b)
+    if cu_rows is not None:
+        _need_vector("cu_rows", cu_rows, b + 1)
+    elif num_rows % b:
+        raise ValueError("without cu_rows every sequence has the same number of rows: b must divide them")
+    ls = _need_rows("latent", latent, MLA_V_DIM, not write)
+    if latent.shape[0] != num_rows:
+        raise ValueError(f"latent must have {num_rows} rows")
+    rope_dims = d - MLA_V_DIM
+    rs, rope_ptr = 0, None
+    if rope_dims > 0:
+        rs = _need_rows("k_rope", k_rope, rope_dims, not write)
+        if k_rope.shape[0] != num_rows:
+            raise ValueError(f"k_rope must have {num_rows} rows")
+        rope_ptr = k_rope.data_ptr()
+        _same_device(dev, "cache", k_rope=k_rope)
+    elif k_rope is not None:
+        raise ValueError("a cache of 512-wide rows has no RoPE part: k_rope must be None")
+    _same_device(dev, "cache", block_table=block_table, starts=starts, latent=latent)
+    if cu_rows is not None:
+        _same_device(dev, "cache", cu_rows=cu_rows)
+    cu_ptr = None if cu_rows is None else cu_rows.data_ptr()
+    with torch.cuda.device(dev):
+        if write:
+            st = getattr(load(), call)(latent.data_ptr(), ls, rope_ptr, rs, num_rows, cu_ptr, starts.data_ptr(), b,
+                                       cache.data_ptr(), num_blocks, block_table.data_ptr(), max_blocks, d,
+                                       _stream_handle(dev))
+        else:
+            st = getattr(load(), call)(cache.data_ptr(), num_blocks, block_table.data_ptr(), max_blocks,
+                                       starts.data_ptr(), cu_ptr, b, num_rows, latent.data_ptr(), ls, rope_ptr, rs, d,
+                                       _stream_handle(dev))
+    check(call, st)
+
+
+def mla_cache_write(latent: torch.Tensor, k_rope: Optional[torch.Tensor], kcache: torch.Tensor,
+                    block_table: torch.Tensor, starts: torch.Tensor, cu_rows: Optional[torch.Tensor] = None) -> None:
+    """Write new tokens' rows into the bf16 cache, in place.
+
+    Rows ``cu_rows[b] .. cu_rows[b + 1]`` of ``latent`` bf16 [n, 512] and
+    ``k_rope`` bf16 [n, 64] (None for a cache of 512-wide rows) go to positions
+    ``starts[b], starts[b] + 1, ...`` of sequence b; without ``cu_rows`` every
+    sequence has n / b rows.  Rows behind ``cu_rows[b]`` are ignored.  The
+    inputs may be slices of wider rows (strides of a multiple of 8 elements)."""
+    _cache_rows("mla_cache_write", kcache, block_table, starts, latent.shape[0], cu_rows, latent, k_rope, False, True)
+
+
+def mla_cache_write_fp8(latent: torch.Tensor, k_rope: torch.Tensor, kv_pages: torch.Tensor,
+                        block_table: torch.Tensor, starts: torch.Tensor, cu_rows: Optional[torch.Tensor] = None) -> None:
+    """``mla_cache_write`` into packed e4m3 pages (uint8 [num_blocks, MLA_FP8_PAGE_BYTES(576)]): each row is
+    quantised as it is written, with its own scale max |x| / 448."""
+    _cache_rows("mla_cache_write_fp8", kv_pages, block_table, starts, latent.shape[0], cu_rows, latent, k_rope, True,
+                True)
+
+
+def _cache_read(call, cache, block_table, starts, num_rows, cu_rows, latent, k_rope, fp8):
+    _, d = _paged_args(cache, block_table, fp8)
+    num_rows = int(num_rows)
+    if num_rows < 0:
+        raise ValueError("num_rows must not be negative")
+    if latent is None:
+        latent = torch.empty((num_rows, MLA_V_DIM), dtype=torch.bfloat16, device=cache.device)
+    if k_rope is None and d > MLA_V_DIM:
+        k_rope = torch.empty((num_rows, d - MLA_V_DIM), dtype=torch.bfloat16, device=cache.device)
+    _cache_rows(call, cache, block_table, starts, num_rows, cu_rows, latent, k_rope, fp8, False)
+    return latent, k_rope
+
+
+def mla_cache_read(kcache: torch.Tensor, block_table: torch.Tensor, starts: torch.Tensor, num_rows: int,
+                   cu_rows: Optional[torch.Tensor] = None, latent: Optional[torch.Tensor] = None,
+                   k_rope: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Read ranges of the bf16 cache back to contiguous rows: (latent bf16
+    [num_rows, 512], k_rope bf16 [num_rows, 64], None for 512-wide rows).
+
+    Output rows ``cu_rows[b] .. cu_rows[b + 1]`` are positions ``starts[b],
+    starts[b] + 1, ...`` of sequence b (without ``cu_rows``: num_rows / b each).
+    Rows behind ``cu_rows[b]`` are left as they were (unset in outputs that the
+    call allocates)."""
+    return _cache_read("mla_cache_read", kcache, block_table, starts, num_rows, cu_rows, latent, k_rope, False)
+
+
+def mla_cache_read_fp8(kv_pages: torch.Tensor, block_table: torch.Tensor, starts: torch.Tensor, num_rows: int,
+                       cu_rows: Optional[torch.Tensor] = None, latent: Optional[torch.Tensor] = None,
+                       k_rope: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """``mla_cache_read`` from packed e4m3 pages: scale * code, rounded to bf16."""
+    return _cache_read("mla_cache_read_fp8", kv_pages, block_table, starts, num_rows, cu_rows, latent, k_rope, True)
+
+
+# ---------------------------------------------------------------- page keys and page selection
+def _page_key_args(cache, num_blocks, d, page_keys, page_scales):
+    _need_cuda("page_keys", page_keys, torch.int8)
+    _need_cuda("page_scales", page_scales, torch.float32)
+    if tuple(page_keys.shape) != (num_blocks, d) or tuple(page_scales.shape) != (num_blocks,):
+        raise ValueError(f"page_keys must be [{num_blocks}, {d}] and page_scales [{num_blocks}]")
+    _same_device(cache.device, "cache", page_keys=page_keys, page_scales=page_scales)
+
+
+def _update_page_keys(call, cache, block_table, cache_seqlens, page_keys, page_scales, starts, fp8):
+    num_blocks, d = _paged_args(cache, block_table, fp8)
+    b, max_blocks = block_table.shape
+    dev = cache.device
+    _need_vector("cache_seqlens", cache_seqlens, b)
+    _page_key_args(cache, num_blocks, d, page_keys, page_scales)
+    _same_device(dev, "cache", block_table=block_table, cache_seqlens=cache_seqlens)
+    if starts is not None:
+        _need_vector("starts", starts, b)
+        _same_device(dev, "cache", starts=starts)
+    with torch.cuda.device(dev):
+        st = getattr(load(), call)(cache.data_ptr(), num_blocks, block_table.data_ptr(), max_blocks,
+                                   cache_seqlens.data_ptr(), None if starts is None else starts.data_ptr(), b, d,
+                                   page_keys.data_ptr(), page_scales.data_ptr(), _stream_handle(dev))
+    check(call, st)
+
+
+def mla_update_page_keys(kcache: torch.Tensor, block_table: torch.Tensor, cache_seqlens: torch.Tensor,
+                         page_keys: torch.Tensor, page_scales: torch.Tensor,
+                         starts: Optional[torch.Tensor] = None) -> None:
+    """Recompute the keys of the pages that positions ``starts[b] .. cache_seqlens[b]`` touch (every page
+    without ``starts``), in place: ``page_keys`` int8 [num_blocks, d] and ``page_scales`` fp32 [num_blocks] hold
+    the mean of each page's rows, quantised per page; see ``include/mla_decode.h``."""
+    _update_page_keys("mla_update_page_keys", kcache, block_table, cache_seqlens, page_keys, page_scales, starts,
+                      False)
+
+
+def mla_update_page_keys_fp8(kv_pages: torch.Tensor, block_table: torch.Tensor, cache_seqlens: torch.Tensor,
+                             page_keys: torch.Tensor, page_scales: torch.Tensor,
+                             starts: Optional[torch.Tensor] = None) -> None:
+    """``mla_update_page_keys`` over packed e4m3 pages."""
+    _update_page_keys("mla_update_page_keys_fp8", kv_pages, block_table, cache_seqlens, page_keys, page_scales,
+                      starts, True)
+
+
+def mla_blocks_workspace_bytes(batch: int, s_q: int, h_q: int, h_kv: int, dv: int, max_blocks: int, topk_pages: int,
+                               num_parts: int) -> int:
+    n = load().mla_blocks_workspace_bytes(batch, s_q, h_q, h_kv, dv, max_blocks, topk_pages, num_parts)
+    if n == 0:
+        raise ValueError("invalid shape for the workspace of a decode over selected pages")
+    return int(n)
+
+
+def _outputs(b, s_q, h_q, dv, dev, out, lse):
+    if out is None:
+        out = torch.empty((b, s_q, h_q, dv), dtype=torch.bfloat16, device=dev)
+    if lse is None:
+        lse = torch.empty((b, s_q, h_q), dtype=torch.float32, device=dev)
+    _need_cuda("out", out, torch.bfloat16)
+    _need_cuda("lse", lse, torch.float32)
+    if tuple(out.shape) != (b, s_q, h_q, dv) or tuple(lse.shape) != (b, s_q, h_q):
+        raise ValueError("out must be [b, s_q, h_q, dv] and lse [b, s_q, h_q]")
+    return out, lse
+
+
+def _query_args(q, cache, block_table, cache_seqlens, fp8):
+    """Check the query against a paged cache; returns (b, s_q, h_q, d, num_blocks, max_blocks)."""
+    num_blocks, d = _paged_args(cache, block_table, fp8)
+    _need_cuda("q", q, torch.bfloat16)
+    if q.dim() != 4 or q.shape[3] != d:
+        raise ValueError(f"q must be [b, s_q, h_q, {d}]")
+    b, s_q, h_q, _ = q.shape
+    if block_table.shape[0] != b:
+        raise ValueError("batch size differs between q and block_table")
+    _need_vector("cache_seqlens", cache_seqlens, b)
+    return b, s_q, h_q, d, num_blocks, block_table.shape[1]
+
+
+def _decode_blocks(call, q, cache, block_table, cache_seqlens, page_keys, page_scales, topk_pages, dv, sink_pages,
+                   local_pages, softmax_scale, causal, out, lse, pages, workspace, fp8):
+    b, s_q, h_q, d, num_blocks, max_blocks = _query_args(q, cache, block_table, cache_seqlens, fp8)
+    dev = q.device
+    _page_key_args(cache, num_blocks, d, page_keys, page_scales)
+    topk_pages, sink_pages, local_pages = int(topk_pages), int(sink_pages), int(local_pages)
+    if sink_pages < 0 or local_pages < 1 or topk_pages < sink_pages + local_pages:
+        raise ValueError("topk_pages must cover sink_pages (>= 0) and local_pages (>= 1)")
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(d)
+    num_parts = mla_num_sm_parts(h_q, 1, dev)
+    ws_need = mla_blocks_workspace_bytes(b, s_q, h_q, 1, dv, max_blocks, topk_pages, num_parts)
+    out, lse = _outputs(b, s_q, h_q, dv, dev, out, lse)
+    if pages is None:
+        pages = torch.empty((b, s_q, topk_pages), dtype=torch.int32, device=dev)
+    _need_cuda("pages", pages, torch.int32)
+    if tuple(pages.shape) != (b, s_q, topk_pages):
+        raise ValueError("pages must be [b, s_q, topk_pages]")
+    if workspace is None:
+        workspace = torch.empty((ws_need,), dtype=torch.uint8, device=dev)
+    _need_cuda("workspace", workspace, torch.uint8)
+    _same_device(dev, cache=cache, block_table=block_table, cache_seqlens=cache_seqlens, out=out, lse=lse, pages=pages,
+                 workspace=workspace)
+    with torch.cuda.device(dev):
+        st = getattr(load(), call)(
+            q.data_ptr(), cache.data_ptr(), num_blocks, block_table.data_ptr(), max_blocks, cache_seqlens.data_ptr(),
+            page_keys.data_ptr(), page_scales.data_ptr(), topk_pages, sink_pages, local_pages, b, s_q, h_q, 1, d, dv,
+            num_parts, float(softmax_scale), int(bool(causal)), out.data_ptr(), lse.data_ptr(), pages.data_ptr(),
+            workspace.data_ptr(), workspace.numel(), _stream_handle(dev))
+    check(call, st)
+    return out, lse, pages
+
+
+def mla_decode_kvcache_blocks(q: torch.Tensor, kcache: torch.Tensor, block_table: torch.Tensor,
+                              cache_seqlens: torch.Tensor, page_keys: torch.Tensor, page_scales: torch.Tensor,
+                              topk_pages: int, dv: int, sink_pages: int = 1, local_pages: int = 1,
+                              softmax_scale: Optional[float] = None, causal: bool = False,
+                              out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                              pages: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None
+                              ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Decode over the pages that each query token selects: the first ``sink_pages``, the last ``local_pages``
+    and, up to ``topk_pages``, those whose key (``mla_update_page_keys``) scores highest against its heads.
+    Returns (o bf16 [b, s_q, h_q, dv], lse fp32 [b, s_q, h_q], pages int32 [b, s_q, topk_pages]: the
+    selected pages, ascending, -1 behind them); see ``include/mla_decode.h``."""
+    return _decode_blocks("mla_decode_kvcache_blocks", q, kcache, block_table, cache_seqlens, page_keys, page_scales,
+                          topk_pages, dv, sink_pages, local_pages, softmax_scale, causal, out, lse, pages, workspace,
+                          False)
+
+
+def mla_decode_kvcache_blocks_fp8(q: torch.Tensor, kv_pages: torch.Tensor, block_table: torch.Tensor,
+                                  cache_seqlens: torch.Tensor, page_keys: torch.Tensor, page_scales: torch.Tensor,
+                                  topk_pages: int, dv: int, sink_pages: int = 1, local_pages: int = 1,
+                                  softmax_scale: Optional[float] = None, causal: bool = False,
+                                  out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                                  pages: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None
+                                  ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """``mla_decode_kvcache_blocks`` over packed e4m3 pages."""
+    return _decode_blocks("mla_decode_kvcache_blocks_fp8", q, kv_pages, block_table, cache_seqlens, page_keys,
+                          page_scales, topk_pages, dv, sink_pages, local_pages, softmax_scale, causal, out, lse, pages,
+                          workspace, True)
+
+
+# ---------------------------------------------------------------- draft trees
+def mla_tree_mask(parents: torch.Tensor) -> torch.Tensor:
+    """The masks of draft trees, int32 [b, s_q, ceil(s_q / 32)], from their parent lists (int32 [b, s_q]: a node
+    before it, or -1): bit j of row i is set when node j is node i or one of its ancestors."""
+    _need_cuda("parents", parents, torch.int32)
+    if parents.dim() != 2:
+        raise ValueError("parents must be [b, s_q]")
+    b, s_q = parents.shape
+    dev = parents.device
+    mask = torch.empty((b, s_q, (s_q + 31) // 32), dtype=torch.int32, device=dev)
+    with torch.cuda.device(dev):
+        st = load().mla_tree_mask(parents.data_ptr(), b, s_q, mask.data_ptr(), _stream_handle(dev))
+    check("mla_tree_mask", st)
+    return mask
+
+
+def _decode_tree(call, q, cache, block_table, cache_seqlens, tree_mask, dv, tile_scheduler_metadata, num_splits,
+                 tree_lens, softmax_scale, out, lse, workspace, fp8):
+    b, s_q, h_q, d, num_blocks, max_blocks = _query_args(q, cache, block_table, cache_seqlens, fp8)
+    dev = q.device
+    _need_cuda("tree_mask", tree_mask, torch.int32)
+    if tuple(tree_mask.shape) != (b, s_q, (s_q + 31) // 32):
+        raise ValueError("tree_mask must be [b, s_q, ceil(s_q / 32)]")
+    if tree_lens is not None:
+        _need_vector("tree_lens", tree_lens, b)
+        _same_device(dev, tree_lens=tree_lens)
+    if (tile_scheduler_metadata is None) != (num_splits is None):
+        raise ValueError("tile_scheduler_metadata and num_splits come together")
+    if tile_scheduler_metadata is None:
+        tile_scheduler_metadata, num_splits = mla_get_metadata(cache_seqlens, s_q * h_q, 1)
+    _need_cuda("tile_scheduler_metadata", tile_scheduler_metadata, torch.int32)
+    _need_vector("num_splits", num_splits, b + 1)
+    if tile_scheduler_metadata.dim() != 2 or tile_scheduler_metadata.shape[1] != MLA_METADATA_INTS:
+        raise ValueError("tile_scheduler_metadata must be [num_parts, 8]")
+    num_parts = tile_scheduler_metadata.shape[0]
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(d)
+    ws_need = mla_workspace_bytes(b, s_q, h_q, 1, dv, num_parts)
+    out, lse = _outputs(b, s_q, h_q, dv, dev, out, lse)
+    if workspace is None:
+        workspace = torch.empty((ws_need,), dtype=torch.uint8, device=dev)
+    _need_cuda("workspace", workspace, torch.uint8)
+    _same_device(dev, cache=cache, block_table=block_table, cache_seqlens=cache_seqlens, tree_mask=tree_mask,
+                 tile_scheduler_metadata=tile_scheduler_metadata, num_splits=num_splits, out=out, lse=lse,
+                 workspace=workspace)
+    with torch.cuda.device(dev):
+        st = getattr(load(), call)(
+            q.data_ptr(), cache.data_ptr(), num_blocks, block_table.data_ptr(), max_blocks, cache_seqlens.data_ptr(),
+            tree_mask.data_ptr(), None if tree_lens is None else tree_lens.data_ptr(), b, s_q, h_q, 1, d, dv,
+            tile_scheduler_metadata.data_ptr(), num_splits.data_ptr(), num_parts, float(softmax_scale), out.data_ptr(),
+            lse.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream_handle(dev))
+    check(call, st)
+    return out, lse
+
+
+def mla_decode_kvcache_tree(q: torch.Tensor, kcache: torch.Tensor, block_table: torch.Tensor,
+                            cache_seqlens: torch.Tensor, tree_mask: torch.Tensor, dv: int,
+                            tile_scheduler_metadata: Optional[torch.Tensor] = None,
+                            num_splits: Optional[torch.Tensor] = None, tree_lens: Optional[torch.Tensor] = None,
+                            softmax_scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                            lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None
+                            ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Decode of draft trees: the last ``tree_lens[b]`` (default s_q) cached rows of each sequence are drafted
+    nodes, query token i is node i, and it sees every position before the nodes and the nodes of its row of
+    ``tree_mask`` (``mla_tree_mask``).  Rows behind a shorter tree get o = 0, lse = -inf.  The work partition is
+    that of a dense decode (``mla_get_metadata``) and is computed when not given.  Returns (o, lse) as
+    ``mla_decode_kvcache``."""
+    return _decode_tree("mla_decode_kvcache_tree", q, kcache, block_table, cache_seqlens, tree_mask, dv,
+                        tile_scheduler_metadata, num_splits, tree_lens, softmax_scale, out, lse, workspace, False)
+
+
+def mla_decode_kvcache_tree_fp8(q: torch.Tensor, kv_pages: torch.Tensor, block_table: torch.Tensor,
+                                cache_seqlens: torch.Tensor, tree_mask: torch.Tensor, dv: int,
+                                tile_scheduler_metadata: Optional[torch.Tensor] = None,
+                                num_splits: Optional[torch.Tensor] = None, tree_lens: Optional[torch.Tensor] = None,
+                                softmax_scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                                lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None
+                                ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """``mla_decode_kvcache_tree`` over packed e4m3 pages."""
+    return _decode_tree("mla_decode_kvcache_tree_fp8", q, kv_pages, block_table, cache_seqlens, tree_mask, dv,
+                        tile_scheduler_metadata, num_splits, tree_lens, softmax_scale, out, lse, workspace, True)
 
 
 def mla_device_status(clear: bool = True) -> int:

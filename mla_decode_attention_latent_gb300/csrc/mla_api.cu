@@ -19,19 +19,6 @@ constexpr int kMaxDevices = 64;
 unsigned int *g_status_addr[kMaxDevices] = {};
 std::mutex g_status_mutex;
 
-int status_address(unsigned int **out) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return MLA_ERR_CUDA;
-    std::lock_guard<std::mutex> lock(g_status_mutex);
-    if (!g_status_addr[dev]) {
-        void *ptr = nullptr;
-        if (cudaGetSymbolAddress(&ptr, g_status_word) != cudaSuccess) return MLA_ERR_CUDA;
-        g_status_addr[dev] = static_cast<unsigned int *>(ptr);
-    }
-    *out = g_status_addr[dev];
-    return MLA_OK;
-}
-
 // NVTX range over a call's host side (argument checks and launches), so that
 // a profiler timeline ties the kernels to the call that enqueued them; free
 // when no tool is attached
@@ -55,6 +42,34 @@ constexpr int kMaxRows = 65536;
 
 }  // namespace
 
+int status_address(unsigned int **out) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return MLA_ERR_CUDA;
+    std::lock_guard<std::mutex> lock(g_status_mutex);
+    if (!g_status_addr[dev]) {
+        void *ptr = nullptr;
+        if (cudaGetSymbolAddress(&ptr, g_status_word) != cudaSuccess) return MLA_ERR_CUDA;
+        g_status_addr[dev] = static_cast<unsigned int *>(ptr);
+    }
+    *out = g_status_addr[dev];
+    return MLA_OK;
+}
+
+cudaError_t device_sm_count(int *sms) {
+    static std::atomic<int> known[kMaxDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    int n = known[dev].load();
+    if (n == 0) {
+        if ((e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+        known[dev].store(n);
+    }
+    *sms = n;
+    return cudaSuccess;
+}
+
 size_t workspace_bytes(int batch, int rows, int num_parts) {
     const size_t splits = (size_t)batch + (size_t)num_parts;
     return align_up(splits * rows * kDv * sizeof(float)) + align_up(splits * rows * sizeof(float));
@@ -76,15 +91,20 @@ extern "C" {
 int mla_num_sm_parts(int device, int num_q_rows, int h_kv, int *num_parts) {
     if (!num_parts || num_q_rows < 1 || h_kv < 1) return MLA_ERR_INVALID_ARG;
     if (h_kv != 1) return MLA_ERR_UNSUPPORTED;
-    int prev = 0;
-    if (cudaGetDevice(&prev) != cudaSuccess) return MLA_ERR_CUDA;
-    if (device != prev && cudaSetDevice(device) != cudaSuccess) return MLA_ERR_CUDA;
-    // one CTA pair (two SMs) per part and row tile: as many pairs as fit at once
-    int pairs = 0;
-    cudaError_t e = split_kv_tc_max_pairs<576, false>(&pairs);  // every variant fits one CTA per SM
-    if (device != prev) cudaSetDevice(prev);
-    if (e != cudaSuccess) return MLA_ERR_CUDA;
-    if (pairs < 1) pairs = 1;
+    // one CTA pair (two SMs) per part and row tile: as many pairs as fit at
+    // once (asked of each device once: the occupancy query takes microseconds)
+    static std::atomic<int> known[kMaxDevices];
+    int pairs = device >= 0 && device < kMaxDevices ? known[device].load() : 0;
+    if (pairs == 0) {
+        int prev = 0;
+        if (cudaGetDevice(&prev) != cudaSuccess) return MLA_ERR_CUDA;
+        if (device != prev && cudaSetDevice(device) != cudaSuccess) return MLA_ERR_CUDA;
+        cudaError_t e = split_kv_tc_max_pairs<576, false>(&pairs);  // every variant fits one CTA per SM
+        if (device != prev) cudaSetDevice(prev);
+        if (e != cudaSuccess) return MLA_ERR_CUDA;
+        if (pairs < 1) pairs = 1;
+        if (device >= 0 && device < kMaxDevices) known[device].store(pairs);
+    }
     const int tiles = (num_q_rows + kRowsPerTile - 1) / kRowsPerTile;
     const int parts = pairs / tiles;
     *num_parts = parts > 0 ? parts : 1;
@@ -134,14 +154,20 @@ struct Lists {
     const int32_t *list_lens = nullptr;  // [batch]: the lengths the work partition was computed on
 };
 
+// Draft tree of the tree decode (unused otherwise).
+struct Tree {
+    const uint32_t *mask = nullptr;  // [batch][s_q][ceil(s_q / 32)]
+    const int32_t *lens = nullptr;   // [batch], or null: s_q nodes everywhere
+};
+
 // The decode behind every cache format: validation, then split + combine.
 int decode(const void *q, const void *kcache, Kind kind, int64_t num_blocks, const int32_t *block_table,
            int max_blocks_per_seq, const int32_t *cache_seqlens, int batch, int s_q, int h_q, int h_kv, int d, int dv,
            const int32_t *tile_scheduler_metadata, const int32_t *num_splits, int num_parts, float softmax_scale,
            int causal, void *o, float *lse, void *workspace, size_t ws_bytes, struct CUstream_st *stream,
-           const Lists &lists = Lists()) {
+           const Lists &lists = Lists(), const Tree &tree = Tree()) {
     const bool e4m3 = kind == Kind::kE4m3, sparse = kind == Kind::kSparse;
-    Range range(sparse ? "mla_decode_kvcache_sparse" : e4m3 ? "mla_decode_kvcache_fp8" : "mla_decode_kvcache");
+    Range range(tree.mask ? "mla_decode_kvcache_tree" : sparse ? "mla_decode_kvcache_sparse" : e4m3 ? "mla_decode_kvcache_fp8" : "mla_decode_kvcache");
     if (!q || !kcache || !block_table || !cache_seqlens || !tile_scheduler_metadata || !num_splits || !o || !lse ||
         !workspace)
         return MLA_ERR_INVALID_ARG;
@@ -184,6 +210,9 @@ int decode(const void *q, const void *kcache, Kind kind, int64_t num_blocks, con
     p.indices = lists.indices;
     p.topk = lists.topk;
     p.kv_lens = cache_seqlens;
+    p.tree_mask = tree.mask;
+    p.tree_words = (s_q + 31) / 32;
+    p.tree_lens = tree.lens;
     p.o = static_cast<uint16_t *>(o);
     p.lse = lse;
     carve_workspace(workspace, batch, rows, num_parts, &p.o_accum, &p.lse_accum);
@@ -197,7 +226,10 @@ int decode(const void *q, const void *kcache, Kind kind, int64_t num_blocks, con
         ev_end = g_split_end;
     }
     if (ev_begin && cudaEventRecord(ev_begin, s) != cudaSuccess) return MLA_ERR_CUDA;
-    cudaError_t e = sparse ? (g_cluster_multicast.load() ? launch_split_kv_tc_sparse(p, s)
+    cudaError_t e = tree.mask ? (e4m3 ? launch_split_kv_tc_tree<576, true>(p, s)
+                                 : d == kDqk ? launch_split_kv_tc_tree<576, false>(p, s)
+                                             : launch_split_kv_tc_tree<512, false>(p, s))
+                    : sparse ? (g_cluster_multicast.load() ? launch_split_kv_tc_sparse(p, s)
                                                          : launch_split_kv_tc_sparse_local(p, s))
                     : e4m3 ? launch_split_kv_tc<576, true>(p, s)
                            : (d == kDqk ? launch_split_kv_tc<576, false>(p, s) : launch_split_kv_tc<512, false>(p, s));
@@ -244,6 +276,47 @@ int mla_decode_kvcache_sparse(const void *q, const void *kcache, int64_t num_blo
     return decode(q, kcache, Kind::kSparse, num_blocks, block_table, max_blocks_per_seq, cache_seqlens, batch, s_q,
                   h_q, h_kv, d, dv, tile_scheduler_metadata, num_splits, num_parts, softmax_scale, 0, o, lse,
                   workspace, ws_bytes, stream, lists);
+}
+
+int mla_tree_mask(const int32_t *parents, int batch, int s_q, int32_t *tree_mask, struct CUstream_st *stream) {
+    if (!parents || !tree_mask || batch < 1 || s_q < 1) return MLA_ERR_INVALID_ARG;
+    if ((long long)batch * s_q > 0x7fffffffLL - 127 || s_q > kMaxRows) return MLA_ERR_UNSUPPORTED;
+    Range range("mla_tree_mask");
+    unsigned int *status = nullptr;
+    if (status_address(&status) != MLA_OK) return MLA_ERR_CUDA;
+    cudaError_t e = launch_tree_mask(parents, batch, s_q, reinterpret_cast<uint32_t *>(tree_mask), status,
+                                     reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+int mla_decode_kvcache_tree(const void *q, const void *kcache, int64_t num_blocks, const int32_t *block_table,
+                            int max_blocks_per_seq, const int32_t *cache_seqlens, const int32_t *tree_mask,
+                            const int32_t *tree_lens, int batch, int s_q, int h_q, int h_kv, int d, int dv,
+                            const int32_t *tile_scheduler_metadata, const int32_t *num_splits, int num_parts,
+                            float softmax_scale, void *o, float *lse, void *workspace, size_t ws_bytes,
+                            struct CUstream_st *stream) {
+    if (!tree_mask) return MLA_ERR_INVALID_ARG;
+    Tree tree;
+    tree.mask = reinterpret_cast<const uint32_t *>(tree_mask);
+    tree.lens = tree_lens;
+    return decode(q, kcache, Kind::kBf16, num_blocks, block_table, max_blocks_per_seq, cache_seqlens, batch, s_q, h_q,
+                  h_kv, d, dv, tile_scheduler_metadata, num_splits, num_parts, softmax_scale, 0, o, lse, workspace,
+                  ws_bytes, stream, Lists(), tree);
+}
+
+int mla_decode_kvcache_tree_fp8(const void *q, const void *kv_pages, int64_t num_blocks, const int32_t *block_table,
+                                int max_blocks_per_seq, const int32_t *cache_seqlens, const int32_t *tree_mask,
+                                const int32_t *tree_lens, int batch, int s_q, int h_q, int h_kv, int d, int dv,
+                                const int32_t *tile_scheduler_metadata, const int32_t *num_splits, int num_parts,
+                                float softmax_scale, void *o, float *lse, void *workspace, size_t ws_bytes,
+                                struct CUstream_st *stream) {
+    if (!tree_mask) return MLA_ERR_INVALID_ARG;
+    Tree tree;
+    tree.mask = reinterpret_cast<const uint32_t *>(tree_mask);
+    tree.lens = tree_lens;
+    return decode(q, kv_pages, Kind::kE4m3, num_blocks, block_table, max_blocks_per_seq, cache_seqlens, batch, s_q, h_q,
+                  h_kv, d, dv, tile_scheduler_metadata, num_splits, num_parts, softmax_scale, 0, o, lse, workspace,
+                  ws_bytes, stream, Lists(), tree);
 }
 
 int mla_device_status(int *status, int clear) {

@@ -42,6 +42,61 @@ struct DecodeParams {
     const int32_t *indices;       // [batch][s_q][topk] token positions per query token
     int topk;
     const int32_t *kv_lens;       // [batch] cache lengths: positions >= kv_lens[b] are ignored
+    // draft-tree decode only
+    const uint32_t *tree_mask;    // [batch][s_q][tree_words]: bit j of row i: node i sees node j
+    int tree_words;               // ceil(s_q / 32)
+    const int32_t *tree_lens;     // [batch] nodes of each sequence, or null: s_q everywhere
+};
+
+// One call that writes or reads ragged rows of the paged cache.
+struct CacheRowsParams {
+    uint16_t *latent;             // [num_rows] rows of 512 bf16 (input of a write, output of a read)
+    int64_t latent_stride;        // elements between rows
+    uint16_t *rope;               // [num_rows] rows of 64 bf16 (d = 576)
+    int64_t rope_stride;
+    int64_t num_rows;
+    const int32_t *cu_rows;       // [batch + 1] first row of each sequence, or null: rows_per_seq each
+    int64_t rows_per_seq;
+    const int32_t *starts;        // [batch] position of each sequence's first row
+    int batch;
+    void *cache;                  // bf16 [num_blocks][64][d] or packed e4m3 pages
+    int64_t num_blocks;
+    const int32_t *block_table;   // [batch][max_blocks]
+    int max_blocks;
+    unsigned int *status;
+};
+
+// One call that recomputes the keys of the pages that [starts[b], seqlens[b]) touches.
+struct PageKeysParams {
+    const void *cache;
+    int64_t num_blocks;
+    const int32_t *block_table;   // [batch][max_blocks]
+    int max_blocks;
+    const int32_t *seqlens;       // [batch]
+    const int32_t *starts;        // [batch], or null: 0 everywhere
+    int batch;
+    int8_t *keys;                 // [num_blocks][d]
+    float *scales;                // [num_blocks]
+    unsigned int *status;
+};
+
+// One call that scores the pages of each query token and selects topk of them.
+struct SelectParams {
+    const uint16_t *q;            // [batch][s_q][h_q][d] bf16
+    const int8_t *keys;           // [num_blocks][d]
+    const float *scales;          // [num_blocks]
+    int64_t num_blocks;
+    const int32_t *block_table;   // [batch][max_blocks]
+    int max_blocks;
+    const int32_t *seqlens;       // [batch]
+    int batch, s_q, h_q, d;
+    int topk, sink, local;
+    int causal;
+    float *scores;                // workspace [batch * s_q][max_blocks]
+    int32_t *sel_table;           // workspace [batch * s_q][topk]: physical pages, the block table of the decode
+    int32_t *sel_lens;            // workspace [batch * s_q]: lengths over the selected pages
+    int32_t *pages;               // [batch][s_q][topk], out: logical pages, ascending, -1 behind them
+    unsigned int *status;
 };
 
 // Workspace carve-up shared by the API, the split kernel and the combine.
@@ -64,5 +119,37 @@ int split_kv_tc_tile_rows();
 template <int D, bool E4M3>
 cudaError_t split_kv_tc_max_pairs(int *pairs);
 cudaError_t launch_combine(const DecodeParams &p, cudaStream_t stream);
+// the same kernel with a draft tree's mask over the last rows of each sequence
+template <int D, bool E4M3>
+cudaError_t launch_split_kv_tc_tree(const DecodeParams &p, cudaStream_t stream);
+
+cudaError_t launch_cache_rows(const CacheRowsParams &p, int d, bool e4m3, bool write, cudaStream_t stream);
+cudaError_t launch_page_keys(const PageKeysParams &p, int d, bool e4m3, cudaStream_t stream);
+cudaError_t launch_select_pages(const SelectParams &p, cudaStream_t stream);
+cudaError_t launch_tree_mask(const int32_t *parents, int batch, int s_q, uint32_t *mask, unsigned int *status,
+                             cudaStream_t stream);
+
+// address of the status word on the current device (MLA_OK or MLA_ERR_CUDA)
+int status_address(unsigned int **out);
+// multiprocessors of the current device
+cudaError_t device_sm_count(int *sms);
+
+// Launch a kernel that may be scheduled while the one before it on the stream
+// finishes; the kernel waits (griddepcontrol.wait) before it touches memory.
+template <typename... Params, typename... Args>
+cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                         const Args &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
 
 }  // namespace mla

@@ -62,6 +62,14 @@
 // upper half of each V stage, zeroing the rows past a sequence's end, and runs
 // P V in f16 with P multiplied by the token's scale, so the accumulators see
 // c_j * code_j as the dequantized row.
+//
+// Draft trees (MLA_SPLIT_TREE = 1): the last n_b cached rows of sequence b are
+// drafted nodes, query token i is node i, and it sees every position before the
+// nodes and the nodes that its bit mask names.  Only the pages that reach past
+// position T_b - n_b look at masks: a row warp cuts its row's 64 bits of the page
+// out of the mask words and takes the masked path below; every other page runs
+// as in a dense decode.  A node's row that no query token of the tile sees is
+// zeroed in V (its weight is 0 in every row, but 0 times a NaN would not be).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
@@ -98,6 +106,12 @@ constexpr bool kSparse = MLA_SPLIT_SPARSE != 0;  // keys gathered row by row fro
 // sparse lists: the CTA pair splits each page's row gathers and multicasts
 // them to both CTAs (1), or each CTA gathers every chunk it uses itself (0)
 constexpr bool kPairGather = kSparse && MLA_SPARSE_MULTICAST != 0;
+#ifndef MLA_SPLIT_TREE
+#define MLA_SPLIT_TREE 0
+#endif
+constexpr bool kTree = MLA_SPLIT_TREE != 0;      // the last rows of a sequence are a draft tree's nodes
+constexpr bool kMask = kSparse || kTree;         // pages carry a 64-bit mask of their visible rows
+static_assert(!(kSparse && kTree), "a sparse list has no tree");
 static_assert(!(kSparse && kFp8) && (!kSparse || MLA_SPLIT_D == 576), "sparse decode: 576-wide bf16 rows");
 constexpr bool kRing = kFp8 || kSparse;          // a per-step side ring (e4m3: token scales; sparse: key masks)
 
@@ -306,10 +320,10 @@ __host__ __device__ constexpr uint32_t idesc_op(int m, int n, bool a_mn_major, b
 // group's kGroup threads reads all of its kItems 16-byte items first (item
 // g = i * kGroup + tid: row g / 4, codes 16 (g % 4) .. + 15), then `sync()`
 // must order every read of the group before any write, then the rows are
-// written.  Rows R with R % 64 >= keep are written as zeros.  Returns false,
-// having written nothing, when `sync()` does.
-template <int kItems, int kGroup, typename Sync>
-__device__ __forceinline__ bool widen_e4m3(uint32_t base, uint32_t land, int tid, int keep, Sync sync) {
+// written.  Rows R for which keep(R % 64) is false are written as zeros.  Returns
+// false, having written nothing, when `sync()` does.
+template <int kItems, int kGroup, typename Keep, typename Sync>
+__device__ __forceinline__ bool widen_e4m3(uint32_t base, uint32_t land, int tid, Keep keep, Sync sync) {
     uint4 x[kItems];
 #pragma unroll
     for (int i = 0; i < kItems; ++i) x[i] = lds128(land + 16u * (uint32_t)(i * kGroup + tid));
@@ -322,7 +336,7 @@ __device__ __forceinline__ bool widen_e4m3(uint32_t base, uint32_t land, int tid
         uint32_t w[8] = {e4m3x2_to_f16x2(x[i].x), e4m3x2_to_f16x2(x[i].x >> 16), e4m3x2_to_f16x2(x[i].y),
                          e4m3x2_to_f16x2(x[i].y >> 16), e4m3x2_to_f16x2(x[i].z), e4m3x2_to_f16x2(x[i].z >> 16),
                          e4m3x2_to_f16x2(x[i].w), e4m3x2_to_f16x2(x[i].w >> 16)};
-        if ((R & (kPage - 1)) >= keep) {
+        if (!keep(R & (kPage - 1))) {
 #pragma unroll
             for (int t = 0; t < 8; ++t) w[t] = 0u;
         }
@@ -330,6 +344,42 @@ __device__ __forceinline__ bool widen_e4m3(uint32_t base, uint32_t land, int tid
         sts128(row + 16u * (uint32_t)((2 * piece + 1) ^ (R & 7)), w[4], w[5], w[6], w[7]);
     }
     return true;
+}
+
+// -------------------------------------------------------------- draft trees
+__device__ __forceinline__ int tree_nodes(const DecodeParams &p, int b) {
+    const int n = p.tree_lens ? p.tree_lens[b] : p.s_q;
+    if (n < 0 || n > p.s_q) {
+        atomicOr(p.status, MLA_DEVERR_SEQLEN);
+        return n < 0 ? 0 : p.s_q;
+    }
+    return n;
+}
+
+// Rows of page pg that node `i` of sequence b sees (bit j: position 64 pg + j),
+// for a sequence of length T whose nodes start at position `base` (negative
+// when the sequence is shorter than its tree).  Bits past the length may be set.
+__device__ __forceinline__ uint64_t tree_page_mask(const DecodeParams &p, int b, int i, int base, int pg) {
+    const int o = pg * kPage - base;  // node index of the page's first row
+    if (o <= -kPage) return ~0ull;
+    const uint32_t *row = p.tree_mask + ((size_t)b * p.s_q + i) * p.tree_words;
+    const int bit = o > 0 ? o : 0, w = bit >> 5;
+    uint32_t x[3];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) x[k] = w + k < p.tree_words ? __ldg(row + w + k) : 0u;
+    const uint64_t m = (uint64_t)__funnelshift_r(x[0], x[1], bit & 31) |
+                       ((uint64_t)__funnelshift_r(x[1], x[2], bit & 31) << 32);
+    return o >= 0 ? m : (m << -o) | ~(~0ull << -o);
+}
+
+// Rows of page pg that some query token of the tile sees (whole warp).
+__device__ __forceinline__ uint64_t tree_tile_mask(const DecodeParams &p, int b, int tile, int nodes, int base, int pg) {
+    const int first = tile * kTileRows / p.h_q;
+    const int last = (min(tile * kTileRows + kTileRows, p.rows) - 1) / p.h_q;
+    uint64_t m = 0;
+    for (int i = first + (int)(threadIdx.x & 31); i <= last && i < nodes; i += 32) m |= tree_page_mask(p, b, i, base, pg);
+    return (uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)m) |
+           ((uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(m >> 32)) << 32);
 }
 
 // -------------------------------------------------------------- roles
@@ -845,7 +895,13 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
     Segment s;
     uint32_t it = 0, step = 0, seg = 0;
     while (walk.next(p, s)) {
-        const int T_row = p.causal ? s.T - p.s_q + qi + 1 : s.T;
+        int T_row = p.causal ? s.T - p.s_q + qi + 1 : s.T;
+        int tree_base = 0;  // position of the sequence's first node
+        if constexpr (kTree) {
+            const int nodes = tree_nodes(p, s.b);
+            tree_base = s.T - nodes;
+            if (qi >= nodes) T_row = 0;  // a row behind the tree sees nothing
+        }
         // both MMA issuers have seen the previous segment's Q (and, having
         // consumed all its S buffers, the MMAs reading it are done)
         if (seg > 0 && !warp_wait(c, B_QACK, (seg - 1) & 1)) return;
@@ -1013,8 +1069,13 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
             // keys of this page visible to this row
             int nvalid = row_ok ? T_row - pg * kPage : 0;
             nvalid = nvalid < 0 ? 0 : (nvalid > kPage ? kPage : nvalid);
-            // sparse decode: the page's valid list entries (gathered rows)
+            // sparse decode: the page's valid list entries (gathered rows);
+            // draft trees: the rows that this row's node sees
             uint64_t vmask = ~0ull;
+            if constexpr (kTree) {
+                if ((pg + 1) * kPage > tree_base && nvalid > 0) vmask = tree_page_mask(p, s.b, qi, tree_base, pg);
+                if (nvalid < kPage) vmask &= nvalid > 0 ? (~0ull >> (kPage - nvalid)) : 0ull;
+            }
             if constexpr (kSparse) {
                 const uint32_t ms = smem_u32(c.base + kScaleOff) + (uint32_t)scs * kScBytes + (uint32_t)q2 * 8;
                 vmask = (uint64_t)lds32(ms) | ((uint64_t)lds32(ms + 4) << 32);
@@ -1034,9 +1095,10 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
                     cs[4 * j + 2] = __uint_as_float(c4.z);
                     cs[4 * j + 3] = __uint_as_float(c4.w);
                 }
-                if (nvalid < kPage) {
+                if (kTree ? vmask != ~0ull : nvalid < kPage) {
 #pragma unroll
-                    for (int j = 0; j < kPage; ++j) cs[j] = j < nvalid ? cs[j] : 0.f;
+                    for (int j = 0; j < kPage; ++j)
+                        cs[j] = (kTree ? ((vmask >> j) & 1ull) != 0 : j < nvalid) ? cs[j] : 0.f;
                 }
             }
             tmem_wait_ld();
@@ -1066,13 +1128,13 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
             // (scaling is monotone there) and folds the scale into one FMA per
             // exponent below; otherwise the scaled, masked scores (-inf past
             // the visible keys) replace the raw ones and the FMA scale is 1.
-            const bool raw = nvalid == kPage && sc > 0.f && (!kSparse || vmask == ~0ull);
+            const bool raw = nvalid == kPage && sc > 0.f && (!kMask || vmask == ~0ull);
             const float fsc = raw ? sc : 1.f;
             float mx4[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
             if (!raw) {
 #pragma unroll
                 for (int j = 0; j < 64; ++j) {
-                    const bool vis = kSparse ? ((vmask >> j) & 1ull) != 0 : j < nvalid;
+                    const bool vis = kMask ? ((vmask >> j) & 1ull) != 0 : j < nvalid;
                     sr[j] = __float_as_uint(vis ? __uint_as_float(sr[j]) * sc : -CUDART_INF_F);
                 }
             }
@@ -1172,18 +1234,32 @@ __device__ void value_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
     uint32_t it = 0, oseg = 0;  // oseg: segments with pages so far
     while (walk.next(p, s)) {
         float inv_l = 0.f;
+        int nodes = 0, tree_base = 0;
+        if constexpr (kTree) {
+            nodes = tree_nodes(p, s.b);
+            tree_base = s.T - nodes;
+        }
         for (int pg = s.p0; pg < s.p1; ++pg, ++it) {
             const int pb = it % kPBufs, st = it % kVStages;
+            // draft trees: the rows of this page that the tile sees at all
+            uint64_t tmask = ~0ull;
+            if constexpr (kTree) {
+                if ((pg + 1) * kPage > tree_base) tmask = tree_tile_mask(p, s.b, tile, nodes, tree_base, pg);
+            }
             if constexpr (kFp8) {
                 // widen the page's V codes in place as soon as they land (rows
                 // past the sequence's end become zeros); the 128 threads' reads
                 // all come before any write through B_VREAD, a bounded barrier
                 if (!warp_wait(c, B_VLAND + st, (it / kVStages) & 1)) return;
                 const uint32_t stage = smem_u32(c.base + kVRingOff + st * kVStageBytes);
-                const bool ok = widen_e4m3<16, 128>(stage, stage + kVLandOff, tid, min(s.T - pg * kPage, kPage), [&] {
-                    mbar_arrive(c.bar(B_VREAD));
-                    return warp_wait(c, B_VREAD, it & 1);
-                });
+                const int keep = min(s.T - pg * kPage, kPage);
+                const bool ok = widen_e4m3<16, 128>(
+                    stage, stage + kVLandOff, tid,
+                    [&](int row) { return row < keep && (!kTree || ((tmask >> row) & 1ull) != 0); },
+                    [&] {
+                        mbar_arrive(c.bar(B_VREAD));
+                        return warp_wait(c, B_VREAD, it & 1);
+                    });
                 if (!ok) return;
                 fence_proxy_async_smem();
                 mbar_arrive(c.bar(B_VFULL + st));
@@ -1195,7 +1271,7 @@ __device__ void value_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
             // rows past the sequence's end in its last page: zero them in V so
             // that garbage (even NaN) times a zero weight stays zero
             const int tail = s.T - pg * kPage;
-            if (!kFp8 && tail < kPage) {
+            if (!kFp8 && (tail < kPage || (kTree && tmask != ~0ull))) {
                 if constexpr (kSparse) {
                     for (int ch = 0; ch < kVChunks; ++ch)
                         if (!warp_wait(c, B_CHUNK + st * kKChunks + ch, (it / kVStages) & 1)) return;
@@ -1206,7 +1282,8 @@ __device__ void value_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
                 // + 16, ... in every chunk (whole 128-byte rows, so the swizzle
                 // does not matter)
                 const uint32_t vt = smem_u32(c.base + kVRingOff + st * kVStageBytes) + 16u * (uint32_t)(tid & 7);
-                for (int rr = (tail > 0 ? tail : 0) + (tid >> 3); rr < kPage; rr += 16)
+                for (int rr = (kTree ? 0 : (tail > 0 ? tail : 0)) + (tid >> 3); rr < kPage; rr += 16)
+                    if (!kTree || rr >= tail || ((tmask >> rr) & 1ull) == 0)
 #pragma unroll
                     for (int ch = 0; ch < kVChunks; ++ch) sts128(vt + ch * kChunkBytes + rr * 128, 0u, 0u, 0u, 0u);
                 fence_proxy_async_smem();
@@ -1517,7 +1594,7 @@ cudaError_t prepare(int dev) {
 
 }  // namespace
 
-#if !MLA_SPLIT_SPARSE
+#if !MLA_SPLIT_SPARSE && !MLA_SPLIT_TREE
 template <>
 cudaError_t split_kv_tc_max_pairs<kD, kFp8>(int *pairs) {
     int dev = 0;
@@ -1554,6 +1631,9 @@ cudaError_t split_kv_tc_max_pairs<kD, kFp8>(int *pairs) {
 cudaError_t launch_split_kv_tc_sparse(const DecodeParams &p, cudaStream_t stream) {
 #elif MLA_SPLIT_SPARSE
 cudaError_t launch_split_kv_tc_sparse_local(const DecodeParams &p, cudaStream_t stream) {
+#elif MLA_SPLIT_TREE
+template <>
+cudaError_t launch_split_kv_tc_tree<kD, kFp8>(const DecodeParams &p, cudaStream_t stream) {
 #else
 template <>
 cudaError_t launch_split_kv_tc<kD, kFp8>(const DecodeParams &p, cudaStream_t stream) {
