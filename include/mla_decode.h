@@ -80,6 +80,7 @@ struct CUstream_st;
 #define MLA_HEAD_DIM 576
 #define MLA_V_DIM 512
 #define MLA_METADATA_INTS 8
+#define MLA_TILE_ROWS 128  /* query rows of one tensor-core tile */
 /* fixed cost of one split-KV segment, in pages, used by the work partition */
 #define MLA_SCHED_FIXED_COST_PAGES 8
 /* cost, in pages, that the partition charges for needing the combine pass */
@@ -503,6 +504,26 @@ MLA_API int mla_decode_kvcache_blocks_fp8(const void *q, const void *kv_pages, i
 MLA_API int mla_tree_mask(const int32_t *parents, int batch, int s_q, int32_t *tree_mask, struct CUstream_st *stream);
 
 /*
+ * mla_get_metadata_tree — split-KV work partition of a draft-tree decode.
+ *
+ * As mla_get_metadata, over the 128-row tiles of every sequence (tile t holds
+ * rows 128 t .. of its s_q * h_q rows; tiles = ceil(s_q * h_q / 128)) instead of
+ * over whole sequences, so that every CTA pair gets its share whatever the
+ * number of tiles, and a tile that holds only rows behind its tree costs
+ * nothing.  Computed once per step, used by every layer.
+ *   tree_lens   as for mla_decode_kvcache_tree (the same values), or NULL
+ *   num_parts   mla_num_sm_parts(device, 1, 1): one part per CTA pair
+ *   tile_scheduler_metadata  device int32 [num_parts][MLA_METADATA_INTS], out
+ *   num_splits  device int32 [batch * tiles + 1], out
+ * Errors: as mla_get_metadata; batch * tiles above 2^24: MLA_ERR_UNSUPPORTED.
+ */
+MLA_API int mla_get_metadata_tree(const int32_t *cache_seqlens, const int32_t *tree_lens, int batch, int s_q, int h_q,
+                                  int h_kv, int num_parts, int32_t *tile_scheduler_metadata, int32_t *num_splits,
+                                  struct CUstream_st *stream);
+/* device scratch of mla_decode_kvcache_tree; 0 on invalid arguments */
+MLA_API size_t mla_tree_workspace_bytes(int batch, int s_q, int h_q, int h_kv, int dv, int num_parts);
+
+/*
  * mla_decode_kvcache_tree — decode of a tree of drafted tokens.
  *
  * The last n_b = tree_lens[b] of the T_b cached rows of sequence b are drafted
@@ -514,6 +535,9 @@ MLA_API int mla_tree_mask(const int32_t *parents, int batch, int s_q, int32_t *t
  *   tree_mask  device int32 [batch][s_q][ceil(s_q / 32)] (mla_tree_mask, or any bits)
  *   tree_lens  device int32 [batch], 0 <= n_b <= s_q, or NULL: s_q everywhere.
  *              A value outside sets MLA_DEVERR_SEQLEN and is clamped
+ *   tile_scheduler_metadata, num_splits, num_parts
+ *              from mla_get_metadata_tree with the same lengths and tree lengths
+ *   workspace  at least mla_tree_workspace_bytes(...) bytes, 256-byte aligned
  *   everything else as for mla_decode_kvcache (d = 576 or 512; no causal
  *   argument: a chain's mask is the causal one).  T_b < n_b drops the nodes that
  *   would lie before the sequence.

@@ -16,7 +16,8 @@ from .api import (flash_mla_with_kvcache, get_mla_metadata, mla_blocks_workspace
                   mla_decode_kvcache_blocks, mla_decode_kvcache_blocks_fp8, mla_decode_kvcache_fp8,
                   mla_decode_kvcache_noalloc, mla_decode_kvcache_sparse, mla_decode_kvcache_tree,
                   mla_decode_kvcache_tree_fp8, mla_device_status, mla_get_metadata, mla_get_metadata_sparse,
-                  mla_num_sm_parts, mla_set_cluster_multicast, mla_set_timing_events, mla_tree_mask,
+                  mla_get_metadata_tree, mla_num_sm_parts, mla_set_cluster_multicast, mla_set_timing_events, mla_tree_mask,
+                  mla_tree_workspace_bytes,
                   mla_update_page_keys, mla_update_page_keys_fp8, mla_workspace_bytes)
 
 __all__ = ["mla_get_metadata", "mla_get_metadata_sparse", "mla_decode_kvcache", "mla_decode_kvcache_fp8",
@@ -24,7 +25,7 @@ __all__ = ["mla_get_metadata", "mla_get_metadata_sparse", "mla_decode_kvcache", 
            "mla_cache_write", "mla_cache_write_fp8", "mla_cache_read", "mla_cache_read_fp8",
            "mla_update_page_keys", "mla_update_page_keys_fp8", "mla_decode_kvcache_blocks",
            "mla_decode_kvcache_blocks_fp8", "mla_blocks_workspace_bytes",
-           "mla_tree_mask", "mla_decode_kvcache_tree", "mla_decode_kvcache_tree_fp8",
+           "mla_tree_mask", "mla_get_metadata_tree", "mla_tree_workspace_bytes", "mla_decode_kvcache_tree", "mla_decode_kvcache_tree_fp8",
            "mla_num_sm_parts", "mla_workspace_bytes", "mla_device_status", "mla_set_timing_events",
            "mla_set_cluster_multicast",
            "get_mla_metadata", "flash_mla_with_kvcache"]

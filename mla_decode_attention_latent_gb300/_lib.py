@@ -24,6 +24,7 @@ MLA_PAGE_SIZE = 64
 MLA_HEAD_DIM = 576
 MLA_V_DIM = 512
 MLA_METADATA_INTS = 8
+MLA_TILE_ROWS = 128
 
 MLA_FP8_SCALE_LIMIT = 255
 
@@ -65,6 +66,8 @@ SIGNATURES = {
                                        _I, _P, _P, _P, _P, _SZ, _P]),
     "mla_decode_kvcache_blocks_fp8": (_I, [_P, _P, _I64, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I,
                                            _F, _I, _P, _P, _P, _P, _SZ, _P]),
+    "mla_get_metadata_tree": (_I, [_P, _P, _I, _I, _I, _I, _I, _P, _P, _P]),
+    "mla_tree_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I]),
     "mla_tree_mask": (_I, [_P, _I, _I, _P, _P]),
     "mla_decode_kvcache_tree": (_I, [_P, _P, _I64, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _I, _F, _P,
                                      _P, _P, _SZ, _P]),

@@ -609,6 +609,42 @@ def mla_tree_mask(parents: torch.Tensor) -> torch.Tensor:
     return mask
 
 
+def _row_tiles(s_q: int, h_q: int) -> int:
+    return (s_q * h_q + _lib.MLA_TILE_ROWS - 1) // _lib.MLA_TILE_ROWS
+
+
+def mla_get_metadata_tree(cache_seqlens: torch.Tensor, s_q: int, h_q: int, tree_lens: Optional[torch.Tensor] = None,
+                          num_parts: Optional[int] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The work partition of a draft-tree decode, over the 128-row tiles of every sequence:
+    (tile_scheduler_metadata int32 [P, 8], num_splits int32 [b * ceil(s_q * h_q / 128) + 1]).  It depends on the
+    lengths and shapes only: one call serves every layer of a step."""
+    _need_cuda("cache_seqlens", cache_seqlens, torch.int32)
+    dev = cache_seqlens.device
+    b = cache_seqlens.numel()
+    s_q, h_q = int(s_q), int(h_q)
+    if b < 1 or s_q < 1 or h_q < 1:
+        raise ValueError("cache_seqlens, s_q and h_q must not be empty or 0")
+    if tree_lens is not None:
+        _need_vector("tree_lens", tree_lens, b)
+        _same_device(dev, "cache_seqlens", tree_lens=tree_lens)
+    if num_parts is None:
+        num_parts = mla_num_sm_parts(1, 1, dev)
+    md = torch.empty((num_parts, MLA_METADATA_INTS), dtype=torch.int32, device=dev)
+    ns = torch.empty((b * _row_tiles(s_q, h_q) + 1,), dtype=torch.int32, device=dev)
+    with torch.cuda.device(dev):
+        st = load().mla_get_metadata_tree(cache_seqlens.data_ptr(), None if tree_lens is None else tree_lens.data_ptr(), b,
+                                          s_q, h_q, 1, int(num_parts), md.data_ptr(), ns.data_ptr(), _stream_handle(dev))
+    check("mla_get_metadata_tree", st)
+    return md, ns
+
+
+def mla_tree_workspace_bytes(batch: int, s_q: int, h_q: int, h_kv: int, dv: int, num_parts: int) -> int:
+    n = load().mla_tree_workspace_bytes(batch, s_q, h_q, h_kv, dv, num_parts)
+    if n == 0:
+        raise ValueError("invalid shape for the workspace of a draft-tree decode")
+    return int(n)
+
+
 def _decode_tree(call, q, cache, block_table, cache_seqlens, tree_mask, dv, tile_scheduler_metadata, num_splits,
                  tree_lens, softmax_scale, out, lse, workspace, fp8):
     b, s_q, h_q, d, num_blocks, max_blocks = _query_args(q, cache, block_table, cache_seqlens, fp8)
@@ -622,15 +658,15 @@ def _decode_tree(call, q, cache, block_table, cache_seqlens, tree_mask, dv, tile
     if (tile_scheduler_metadata is None) != (num_splits is None):
         raise ValueError("tile_scheduler_metadata and num_splits come together")
     if tile_scheduler_metadata is None:
-        tile_scheduler_metadata, num_splits = mla_get_metadata(cache_seqlens, s_q * h_q, 1)
+        tile_scheduler_metadata, num_splits = mla_get_metadata_tree(cache_seqlens, s_q, h_q, tree_lens)
     _need_cuda("tile_scheduler_metadata", tile_scheduler_metadata, torch.int32)
-    _need_vector("num_splits", num_splits, b + 1)
+    _need_vector("num_splits", num_splits, b * _row_tiles(s_q, h_q) + 1)
     if tile_scheduler_metadata.dim() != 2 or tile_scheduler_metadata.shape[1] != MLA_METADATA_INTS:
         raise ValueError("tile_scheduler_metadata must be [num_parts, 8]")
     num_parts = tile_scheduler_metadata.shape[0]
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(d)
-    ws_need = mla_workspace_bytes(b, s_q, h_q, 1, dv, num_parts)
+    ws_need = mla_tree_workspace_bytes(b, s_q, h_q, 1, dv, num_parts)
     out, lse = _outputs(b, s_q, h_q, dv, dev, out, lse)
     if workspace is None:
         workspace = torch.empty((ws_need,), dtype=torch.uint8, device=dev)
@@ -657,8 +693,8 @@ def mla_decode_kvcache_tree(q: torch.Tensor, kcache: torch.Tensor, block_table: 
                             ) -> Tuple[torch.Tensor, torch.Tensor]:
     """Decode of draft trees: the last ``tree_lens[b]`` (default s_q) cached rows of each sequence are drafted
     nodes, query token i is node i, and it sees every position before the nodes and the nodes of its row of
-    ``tree_mask`` (``mla_tree_mask``).  Rows behind a shorter tree get o = 0, lse = -inf.  The work partition is
-    that of a dense decode (``mla_get_metadata``) and is computed when not given.  Returns (o, lse) as
+    ``tree_mask`` (``mla_tree_mask``).  Rows behind a shorter tree get o = 0, lse = -inf.  The work partition
+    (``mla_get_metadata_tree``) is computed when not given.  Returns (o, lse) as
     ``mla_decode_kvcache``."""
     return _decode_tree("mla_decode_kvcache_tree", q, kcache, block_table, cache_seqlens, tree_mask, dv,
                         tile_scheduler_metadata, num_splits, tree_lens, softmax_scale, out, lse, workspace, False)

@@ -32,13 +32,14 @@ size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-constexpr int kRowsPerTile = 128;  // query rows per tensor-core tile
+constexpr int kRowsPerTile = MLA_TILE_ROWS;  // query rows per tensor-core tile
 
 std::mutex g_timing_mutex;
 // sparse decode: pair-split gathers with cluster multicast (1) or local gathers (0)
 std::atomic<int> g_cluster_multicast{1};
 cudaEvent_t g_split_begin = nullptr, g_split_end = nullptr;
 constexpr int kMaxRows = 65536;
+constexpr int kMaxTreeEntries = 1 << 24;  // row tiles of all sequences of one draft-tree call
 
 }  // namespace
 
@@ -188,7 +189,11 @@ int decode(const void *q, const void *kcache, Kind kind, int64_t num_blocks, con
     if ((long long)max_blocks_per_seq * kPage > 0x7fffffffLL) return MLA_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(kcache) || !aligned16(o) || !aligned16(workspace)) return MLA_ERR_INVALID_ARG;
     const int rows = s_q * h_q;
-    if (ws_bytes < workspace_bytes(batch, rows, num_parts)) return MLA_ERR_WORKSPACE;
+    const int tiles = (rows + kRowsPerTile - 1) / kRowsPerTile;
+    // a draft tree's work entries are row tiles, and a workspace slot holds one
+    if (tree.mask && (long long)batch * tiles > kMaxTreeEntries) return MLA_ERR_UNSUPPORTED;
+    const int entries = tree.mask ? batch * tiles : batch, slot = tree.mask ? kRowsPerTile : rows;
+    if (ws_bytes < workspace_bytes(entries, slot, num_parts)) return MLA_ERR_WORKSPACE;
 
     DecodeParams p{};
     p.q = static_cast<const uint16_t *>(q);
@@ -204,7 +209,7 @@ int decode(const void *q, const void *kcache, Kind kind, int64_t num_blocks, con
     p.metadata = tile_scheduler_metadata;
     p.num_splits = num_splits;
     p.num_parts = num_parts;
-    p.max_splits = batch + num_parts;
+    p.max_splits = entries + num_parts;
     p.scale_log2 = softmax_scale * 1.4426950408889634f;
     p.causal = (causal != 0 && s_q > 1 && !sparse) ? 1 : 0;
     p.indices = lists.indices;
@@ -213,9 +218,10 @@ int decode(const void *q, const void *kcache, Kind kind, int64_t num_blocks, con
     p.tree_mask = tree.mask;
     p.tree_words = (s_q + 31) / 32;
     p.tree_lens = tree.lens;
+    p.tiles = tiles;
     p.o = static_cast<uint16_t *>(o);
     p.lse = lse;
-    carve_workspace(workspace, batch, rows, num_parts, &p.o_accum, &p.lse_accum);
+    carve_workspace(workspace, entries, slot, num_parts, &p.o_accum, &p.lse_accum);
     if (status_address(&p.status) != MLA_OK) return MLA_ERR_CUDA;
 
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -235,7 +241,7 @@ int decode(const void *q, const void *kcache, Kind kind, int64_t num_blocks, con
                            : (d == kDqk ? launch_split_kv_tc<576, false>(p, s) : launch_split_kv_tc<512, false>(p, s));
     if (e != cudaSuccess) return MLA_ERR_CUDA;
     if (ev_end && cudaEventRecord(ev_end, s) != cudaSuccess) return MLA_ERR_CUDA;
-    e = launch_combine(p, s);
+    e = tree.mask ? launch_combine_tree(p, kRowsPerTile, s) : launch_combine(p, s);
     return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
@@ -276,6 +282,31 @@ int mla_decode_kvcache_sparse(const void *q, const void *kcache, int64_t num_blo
     return decode(q, kcache, Kind::kSparse, num_blocks, block_table, max_blocks_per_seq, cache_seqlens, batch, s_q,
                   h_q, h_kv, d, dv, tile_scheduler_metadata, num_splits, num_parts, softmax_scale, 0, o, lse,
                   workspace, ws_bytes, stream, lists);
+}
+
+int mla_get_metadata_tree(const int32_t *cache_seqlens, const int32_t *tree_lens, int batch, int s_q, int h_q, int h_kv,
+                          int num_parts, int32_t *tile_scheduler_metadata, int32_t *num_splits,
+                          struct CUstream_st *stream) {
+    if (!cache_seqlens || !tile_scheduler_metadata || !num_splits) return MLA_ERR_INVALID_ARG;
+    if (batch < 1 || s_q < 1 || h_q < 1 || h_kv < 1 || num_parts < 1) return MLA_ERR_INVALID_ARG;
+    if (h_kv != 1 || (long long)s_q * h_q > kMaxRows) return MLA_ERR_UNSUPPORTED;
+    const int tiles = (s_q * h_q + kRowsPerTile - 1) / kRowsPerTile;
+    if ((long long)batch * tiles > kMaxTreeEntries) return MLA_ERR_UNSUPPORTED;
+    Range range("mla_get_metadata_tree");
+    unsigned int *status = nullptr;
+    if (status_address(&status) != MLA_OK) return MLA_ERR_CUDA;
+    cudaError_t e = launch_schedule_tree(cache_seqlens, tree_lens, batch, tiles, kRowsPerTile, h_q, num_parts,
+                                         tile_scheduler_metadata, num_splits, status,
+                                         reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+size_t mla_tree_workspace_bytes(int batch, int s_q, int h_q, int h_kv, int dv, int num_parts) {
+    if (batch < 1 || s_q < 1 || h_q < 1 || h_kv != 1 || num_parts < 1 || dv != kDv) return 0;
+    if ((long long)s_q * h_q > kMaxRows) return 0;
+    const int tiles = (s_q * h_q + kRowsPerTile - 1) / kRowsPerTile;
+    if ((long long)batch * tiles > kMaxTreeEntries) return 0;
+    return workspace_bytes(batch * tiles, kRowsPerTile, num_parts);
 }
 
 int mla_tree_mask(const int32_t *parents, int batch, int s_q, int32_t *tree_mask, struct CUstream_st *stream) {

@@ -31,15 +31,21 @@ namespace {
 constexpr int kCombineWarps = 8;
 constexpr int kCombineUnroll = 2;  // partials whose loads are in flight together
 
+// kTiles: the work entries are 128-row tiles of sequences of `seq_rows` rows
+// (draft trees), so a slot holds 128 rows and entry b's row 0 is row
+// 128 (b % tiles) of sequence b / tiles.
+template <bool kTiles>
 __global__ void __launch_bounds__(kCombineWarps * 32)
 combine_kernel(const float *__restrict__ o_accum, const float *__restrict__ lse_accum,
                const int32_t *__restrict__ num_splits, int rows, int max_splits,
-               uint16_t *__restrict__ o, float *__restrict__ lse, unsigned int *status) {
+               uint16_t *__restrict__ o, float *__restrict__ lse, unsigned int *status, int tiles, int seq_rows) {
     const int lane = threadIdx.x & 31;
-    const int row = blockIdx.x * kCombineWarps + (threadIdx.x >> 5);
-    const int b = blockIdx.y;
+    const int blocks = kTiles ? rows / kCombineWarps : 1;  // tiles: both indices in blockIdx.x
+    const int row = (kTiles ? blockIdx.x % blocks : blockIdx.x) * kCombineWarps + (threadIdx.x >> 5);
+    const int b = kTiles ? blockIdx.x / blocks : blockIdx.y;
     sm103::griddep_wait();  // the split-KV kernel's partials (programmatic launch)
     if (row >= rows) return;
+    if (kTiles && (b % tiles) * rows + row >= seq_rows) return;
     const int first = num_splits[b];
     const int n = num_splits[b + 1] - first;
     if (n <= 1) return;  // written directly by the split-KV kernel
@@ -55,7 +61,7 @@ combine_kernel(const float *__restrict__ o_accum, const float *__restrict__ lse_
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
 
-    const size_t out_row = (size_t)b * rows + row;
+    const size_t out_row = kTiles ? (size_t)(b / tiles) * seq_rows + (b % tiles) * rows + row : (size_t)b * rows + row;
     float4 acc[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -116,8 +122,15 @@ cudaError_t launch_combine(const DecodeParams &p, cudaStream_t stream) {
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, combine_kernel, (const float *)p.o_accum, (const float *)p.lse_accum,
-                              (const int32_t *)p.num_splits, p.rows, p.max_splits, p.o, p.lse, p.status);
+    return cudaLaunchKernelEx(&cfg, combine_kernel<false>, (const float *)p.o_accum, (const float *)p.lse_accum,
+                              (const int32_t *)p.num_splits, p.rows, p.max_splits, p.o, p.lse, p.status, 1, p.rows);
+}
+
+cudaError_t launch_combine_tree(const DecodeParams &p, int tile_rows, cudaStream_t stream) {
+    const unsigned entries = (unsigned)p.batch * (unsigned)p.tiles;
+    return launch_after(combine_kernel<true>, dim3(entries * (unsigned)(tile_rows / kCombineWarps)), dim3(kCombineWarps * 32), 0,
+                        stream, (const float *)p.o_accum, (const float *)p.lse_accum, (const int32_t *)p.num_splits, tile_rows,
+                        p.max_splits, p.o, p.lse, p.status, p.tiles, p.rows);
 }
 
 }  // namespace mla

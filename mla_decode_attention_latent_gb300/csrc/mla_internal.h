@@ -45,6 +45,7 @@ struct DecodeParams {
     // draft-tree decode only
     const uint32_t *tree_mask;    // [batch][s_q][tree_words]: bit j of row i: node i sees node j
     int tree_words;               // ceil(s_q / 32)
+    int tiles;                    // 128-row tiles of a sequence: the work line's entries
     const int32_t *tree_lens;     // [batch] nodes of each sequence, or null: s_q everywhere
 };
 
@@ -119,6 +120,11 @@ int split_kv_tc_tile_rows();
 template <int D, bool E4M3>
 cudaError_t split_kv_tc_max_pairs(int *pairs);
 cudaError_t launch_combine(const DecodeParams &p, cudaStream_t stream);
+// draft trees: work entries are row tiles (entry e: tile e % tiles of sequence e / tiles)
+cudaError_t launch_schedule_tree(const int32_t *seqlens, const int32_t *tree_lens, int batch, int tiles, int tile_rows,
+                                 int h_q, int num_parts, int32_t *metadata, int32_t *num_splits, unsigned int *status,
+                                 cudaStream_t stream);
+cudaError_t launch_combine_tree(const DecodeParams &p, int tile_rows, cudaStream_t stream);
 // the same kernel with a draft tree's mask over the last rows of each sequence
 template <int D, bool E4M3>
 cudaError_t launch_split_kv_tc_tree(const DecodeParams &p, cudaStream_t stream);

@@ -23,6 +23,23 @@ namespace {
 
 constexpr int kSchedThreads = 512;
 
+// Lengths of the work line's entries.  A dense or sparse decode has one entry
+// per sequence; a draft-tree decode one per row tile (entry e is tile
+// e % tiles of sequence e / tiles), whose length is 0 when the tile holds only
+// rows behind the sequence's tree.
+struct Entries {
+    const int32_t *seqlens;
+    int tiles;                 // 1: entries are sequences
+    int tile_rows, h_q;        // rows of a tile, rows of a query token
+    const int32_t *tree_lens;  // or null: no row is behind a tree
+    __device__ __forceinline__ int operator[](int e) const {
+        if (tiles == 1 && !tree_lens) return seqlens[e];
+        const int b = e / tiles, tile = e - b * tiles;
+        const int t = seqlens[b];
+        return tree_lens && t > 0 && tile * tile_rows / h_q >= tree_lens[b] ? 0 : t;
+    }
+};
+
 __device__ __forceinline__ int pages_of(int t) { return t <= 0 ? 0 : t / kPage + (t % kPage != 0); }
 
 // Exclusive prefix sum over the block; *total receives the block total.
@@ -59,7 +76,7 @@ __device__ T block_exclusive_scan(T v, T *s_warp, T *total) {
 // first unit, so a unit is located by a binary search over the chunks and a
 // short walk inside one.
 __global__ void __launch_bounds__(kSchedThreads)
-schedule_kernel(const int32_t *__restrict__ seqlens, int batch, int num_parts, int fixed_cost, int combine_cost,
+schedule_kernel(const Entries seqlens, int batch, int num_parts, int fixed_cost, int combine_cost,
                 int32_t *__restrict__ metadata, int32_t *__restrict__ num_splits,
                 unsigned int *status) {
     __shared__ long long s_start[kSchedThreads + 1];  // first unit of every chunk; [kSchedThreads] = total
@@ -186,7 +203,17 @@ schedule_kernel(const int32_t *__restrict__ seqlens, int batch, int num_parts, i
 
 cudaError_t launch_schedule(const int32_t *seqlens, int batch, int num_parts, int fixed_cost, int combine_cost,
                             int32_t *metadata, int32_t *num_splits, unsigned int *status, cudaStream_t stream) {
-    schedule_kernel<<<1, kSchedThreads, 0, stream>>>(seqlens, batch, num_parts, fixed_cost, combine_cost, metadata,
+    const Entries entries{seqlens, 1, 1, 1, nullptr};
+    schedule_kernel<<<1, kSchedThreads, 0, stream>>>(entries, batch, num_parts, fixed_cost, combine_cost, metadata,
+                                                     num_splits, status);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_schedule_tree(const int32_t *seqlens, const int32_t *tree_lens, int batch, int tiles, int tile_rows,
+                                 int h_q, int num_parts, int32_t *metadata, int32_t *num_splits, unsigned int *status,
+                                 cudaStream_t stream) {
+    const Entries entries{seqlens, tiles, tile_rows, h_q, tree_lens};
+    schedule_kernel<<<1, kSchedThreads, 0, stream>>>(entries, batch * tiles, num_parts, kFixedCost, kCombineCost, metadata,
                                                      num_splits, status);
     return cudaGetLastError();
 }

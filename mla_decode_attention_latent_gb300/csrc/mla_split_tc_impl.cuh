@@ -223,7 +223,25 @@ static_assert(kRingSlots * kScoreIssuers == kKSlots && kSBufs % kScoreIssuers ==
 // -------------------------------------------------------------- work walk
 struct Segment {
     int b, T, n_pages, p0, p1, split, n_split;
+    int entry;  // index into num_splits: the sequence, or (draft trees) its row tile
+    int tile;   // draft trees: the row tile of the segment
 };
+
+// Draft trees: the work line's entries are row tiles, not sequences (entry
+// e is tile e % tiles of sequence e / tiles), so that a part walks tiles of
+// equal cost, every CTA pair gets its share whatever the number of tiles, and
+// the tiles that hold only rows behind a tree cost nothing.
+__device__ __forceinline__ int tree_nodes(const DecodeParams &p, int b) {
+    const int n = p.tree_lens ? p.tree_lens[b] : p.s_q;
+    if (n < 0 || n > p.s_q) {
+        atomicOr(p.status, MLA_DEVERR_SEQLEN);
+        return n < 0 ? 0 : p.s_q;
+    }
+    return n;
+}
+__device__ __forceinline__ int work_entries(const DecodeParams &p) { return kTree ? p.batch * p.tiles : p.batch; }
+// rows of one work entry: what a workspace slot holds
+__device__ __forceinline__ int slot_rows(const DecodeParams &p) { return kTree ? kTileRows : p.rows; }
 
 struct PartWalk {
     int bb, bp, eb, ep, bs, b;
@@ -234,15 +252,22 @@ struct PartWalk {
         eb = md[2];
         ep = md[3];
         bs = md[4];
-        b = (bb == eb && bp == ep) ? p.batch : bb;  // an empty part walks nothing
-        if (b < 0) b = p.batch;
+        b = (bb == eb && bp == ep) ? work_entries(p) : bb;  // an empty part walks nothing
+        if (b < 0) b = work_entries(p);
     }
     __device__ bool next(const DecodeParams &p, Segment &s) {
-        if (b >= p.batch || b > eb || (b == eb && ep == 0)) return false;
-        int T = p.seqlens[b];  // sparse decode: the length of the sequence's lists
+        if (b >= work_entries(p) || b > eb || (b == eb && ep == 0)) return false;
+        const int seq = kTree ? b / p.tiles : b;
+        int T = p.seqlens[seq];  // sparse decode: the length of the sequence's lists
+        s.tile = 0;
+        if constexpr (kTree) {
+            s.tile = b - seq * p.tiles;
+            if (s.tile * kTileRows / p.h_q >= tree_nodes(p, seq)) T = 0;  // only rows behind the tree
+        }
         if (T < 0) T = 0;
         if (!kSparse && T > p.max_blocks * kPage) T = p.max_blocks * kPage;
-        s.b = b;
+        s.b = seq;
+        s.entry = b;
         s.T = T;
         s.n_pages = (T + kPage - 1) / kPage;
         s.p1 = (b == eb) ? min(ep, s.n_pages) : s.n_pages;
@@ -347,15 +372,6 @@ __device__ __forceinline__ bool widen_e4m3(uint32_t base, uint32_t land, int tid
 }
 
 // -------------------------------------------------------------- draft trees
-__device__ __forceinline__ int tree_nodes(const DecodeParams &p, int b) {
-    const int n = p.tree_lens ? p.tree_lens[b] : p.s_q;
-    if (n < 0 || n > p.s_q) {
-        atomicOr(p.status, MLA_DEVERR_SEQLEN);
-        return n < 0 ? 0 : p.s_q;
-    }
-    return n;
-}
-
 // Rows of page pg that node `i` of sequence b sees (bit j: position 64 pg + j),
 // for a sequence of length T whose nodes start at position `base` (negative
 // when the sequence is shorter than its tree).  Bits past the length may be set.
@@ -400,11 +416,10 @@ __device__ void score_producer(const DecodeParams &p, const Ctx &c, const CUtens
         // walk reads the sequence lengths (one dependent round trip fewer
         // before the first chunk load)
         const int32_t *md = p.metadata + (size_t)part * kMdInts;
-        const int bb = md[0], bp = md[1];
+        const int bb = kTree ? md[0] / p.tiles : md[0], bp = md[1];
         if (bb >= 0 && bb < p.batch && bp >= 0 && bp < p.max_blocks)
             prefetch_line_l1(p.block_table + (size_t)bb * p.max_blocks + bp);
     }
-    const int rows = min(kTileRows, p.rows - tile * kTileRows);
     walk.init(p, part);
     uint32_t ring_it = 0;  // chunks issued into this producer's ring
     uint32_t step = 0;
@@ -413,6 +428,8 @@ __device__ void score_producer(const DecodeParams &p, const Ctx &c, const CUtens
         // producer 0 asks L2 for the segment's Q rows as it reaches the
         // segment, a few pages before the row warps load them (a prefetch at
         // the part's start would be evicted by the pages streamed meanwhile)
+        if constexpr (kTree) tile = s.tile;
+        const int rows = min(kTileRows, p.rows - tile * kTileRows);
         if (r == 0 && s.p1 > s.p0 && rows > 0)
             prefetch_l2(p.q + ((size_t)s.b * p.rows + (size_t)tile * kTileRows) * kD, (uint32_t)rows * kD * 2);
         for (int pg = s.p0; ok && pg < s.p1; pg += 2, ++step) {
@@ -885,9 +902,9 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = 32 * (warp & 3) + lane;                // tile row = TMEM lane
     const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
-    const int gr = tile * kTileRows + r;                 // row within the sequence's rows
-    const bool row_ok = gr < p.rows;
-    const int qi = row_ok ? gr / p.h_q : 0;              // query token index
+    int gr = tile * kTileRows + r;                       // row within the sequence's rows
+    bool row_ok = gr < p.rows;
+    int qi = row_ok ? gr / p.h_q : 0;                    // query token index
     const uint32_t peer_buf = mapa(smem_u32(c.base + kPBufOff), c.peer);
     const uint32_t peer_pfull = mapa(smem_u32(c.bar(B_PFULL)), c.peer);
     PartWalk walk;
@@ -898,6 +915,9 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
         int T_row = p.causal ? s.T - p.s_q + qi + 1 : s.T;
         int tree_base = 0;  // position of the sequence's first node
         if constexpr (kTree) {
+            gr = s.tile * kTileRows + r;
+            row_ok = gr < p.rows;
+            qi = row_ok ? gr / p.h_q : 0;
             const int nodes = tree_nodes(p, s.b);
             tree_base = s.T - nodes;
             if (qi >= nodes) T_row = 0;  // a row behind the tree sees nothing
@@ -1208,8 +1228,8 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
             if (s.n_split <= 1) {
                 p.lse[(size_t)s.b * p.rows + gr] = lse_row;
             } else {
-                const int slot = p.num_splits[s.b] + s.split;
-                if (slot >= 0 && slot < p.max_splits) p.lse_accum[(size_t)slot * p.rows + gr] = lse_row;
+                const int slot = p.num_splits[s.entry] + s.split;
+                if (slot >= 0 && slot < p.max_splits) p.lse_accum[(size_t)slot * slot_rows(p) + (kTree ? r : gr)] = lse_row;
                 else atomicOr(p.status, MLA_DEVERR_SEQLEN);
             }
         }
@@ -1236,6 +1256,7 @@ __device__ void value_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
         float inv_l = 0.f;
         int nodes = 0, tree_base = 0;
         if constexpr (kTree) {
+            tile = s.tile;
             nodes = tree_nodes(p, s.b);
             tree_base = s.T - nodes;
         }
@@ -1323,7 +1344,7 @@ __device__ void value_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
         const bool split = s.n_split > 1;
         int slot = 0;
         if (split) {
-            slot = p.num_splits[s.b] + s.split;
+            slot = p.num_splits[s.entry] + s.split;
             if (slot < 0 || slot >= p.max_splits) {
                 if (tid == 0) atomicOr(p.status, MLA_DEVERR_SEQLEN);
                 slot = -1;
@@ -1379,7 +1400,7 @@ __device__ void value_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
                     for (int k = 0; k < 16; ++k) {
                         const int g = tile * kTileRows + wrow0 + 2 * k + (lane >> 4);
                         if (g < p.rows)
-                            reinterpret_cast<uint4 *>(p.o_accum + ((size_t)slot * p.rows + g) * kDv + ch * kEpiCols)[lane & 15] = x[k];
+                            reinterpret_cast<uint4 *>(p.o_accum + ((size_t)slot * slot_rows(p) + (kTree ? g - tile * kTileRows : g)) * kDv + ch * kEpiCols)[lane & 15] = x[k];
                     }
                 } else {
                     // bf16: 128 B per row chunk, four rows per warp store
@@ -1647,7 +1668,7 @@ cudaError_t launch_split_kv_tc<kD, kFp8>(const DecodeParams &p, cudaStream_t str
     if (!make_kv_map(&map, &map2, p.kcache, p.num_blocks)) return cudaErrorInvalidValue;
     const int tiles = (p.rows + kTileRows - 1) / kTileRows;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * p.num_parts, tiles, 1);
+    cfg.gridDim = dim3(2 * p.num_parts, kTree ? 1 : tiles, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.dynamicSmemBytes = kSmemBytes;
     cfg.stream = stream;

@@ -164,3 +164,20 @@ def test_selection_of_known_scores():
 def test_mask_words_of_a_known_tree():
     assert R.mask_words(R.ancestors([-1, 0, 0, 2])).tolist() == [[1], [3], [5], [13]]
     assert R.mask_words(R.ancestors(list(range(-1, 31)) + [31]))[32].tolist() == [-1, 1]
+
+
+def test_tree_partition(lib):
+    for args, code in (((None, None, 2, 4, 16, 1, 3, 256, 256), BAD), ((256, None, 2, 4, 16, 1, 3, None, 256), BAD),
+                       ((256, None, 2, 4, 16, 1, 3, 256, None), BAD), ((256, None, 0, 4, 16, 1, 3, 256, 256), BAD),
+                       ((256, None, 2, 0, 16, 1, 3, 256, 256), BAD), ((256, None, 2, 4, 0, 1, 3, 256, 256), BAD),
+                       ((256, None, 2, 4, 16, 1, 0, 256, 256), BAD), ((256, None, 2, 4, 16, 2, 3, 256, 256), UNSUP),
+                       ((256, None, 2, 8192, 16, 1, 3, 256, 256), UNSUP), ((256, None, 65535, 512, 128, 1, 3, 256, 256), UNSUP)):
+        assert lib.mla_get_metadata_tree(*args, None) == code
+    # a slot holds one 128-row tile: 3 tiles of 2 sequences, 5 parts
+    n = lib.mla_tree_workspace_bytes(2, 3, 100, 1, 512, 5)
+    assert n % 256 == 0 and n >= (2 * 3 + 5) * 128 * 513 * 4 > n - 512
+    for bad in ((0, 3, 100, 1, 512, 5), (2, 0, 100, 1, 512, 5), (2, 3, 0, 1, 512, 5), (2, 3, 100, 2, 512, 5),
+                (2, 3, 100, 1, 576, 5), (2, 3, 100, 1, 512, 0), (2, 8192, 16, 1, 512, 5), (65535, 512, 128, 1, 512, 5)):
+        assert lib.mla_tree_workspace_bytes(*bad) == 0
+    assert tree(lib, b=2, s=3, h=100, parts=5, bytes=n - 1) == WS
+    assert tree(lib, b=65535, s=512, h=128) == UNSUP

@@ -57,7 +57,9 @@ def decode(dev, q, cache, table, lens, sees, nodes=None, num_parts=None, **k):
     call = mla.mla_decode_kvcache_tree if cache.dtype == torch.bfloat16 else mla.mla_decode_kvcache_tree_fp8
     sl = torch.tensor(lens, dtype=torch.int32, device=dev)
     if num_parts:
-        k["tile_scheduler_metadata"], k["num_splits"] = mla.mla_get_metadata(sl, q.shape[1] * q.shape[2], 1, num_parts=num_parts)
+        k["tile_scheduler_metadata"], k["num_splits"] = mla.mla_get_metadata_tree(
+            sl, q.shape[1], q.shape[2], None if nodes is None else torch.tensor(nodes, dtype=torch.int32, device=dev),
+            num_parts=num_parts)
     return call(q.to(dev), cache.to(dev), table.to(dev), sl, words(sees).to(dev), 512,
                 tree_lens=None if nodes is None else torch.tensor(nodes, dtype=torch.int32, device=dev), **k)
 
@@ -128,17 +130,17 @@ def test_any_mask(dev, fp8):
     assert not o[0, 5].any() and bool(torch.isneginf(lse[0, 5]).all())
 
 
-@pytest.mark.parametrize("d,fp8", FORMATS)
+@pytest.mark.parametrize("d", [576, 512])
 @pytest.mark.parametrize("s_q,h", [(8, 128), (40, 16)])
-def test_a_chain_is_the_causal_decode(dev, d, fp8, s_q, h):
+def test_a_chain_is_the_causal_decode(dev, d, s_q, h):
+    """Bit for bit, where no sequence is cut between parts."""
     lens = [300, 128, 64, 41]
-    q, cache, table, _ = make(lens, s_q, h, d, fp8)
+    q, cache, table, _ = make(lens, s_q, h, d)
     sees = np.stack([np.tril(np.ones((s_q, s_q), bool))] * 4)
-    o, lse = decode(dev, q, cache, table, lens, sees)
+    o, lse = decode(dev, q, cache, table, lens, sees, num_parts=1)
     sl = torch.tensor(lens, dtype=torch.int32, device=dev)
-    md, ns = mla.mla_get_metadata(sl, s_q * h, 1)
-    call = mla.mla_decode_kvcache_fp8 if fp8 else mla.mla_decode_kvcache
-    o2, lse2 = call(q.to(dev), cache.to(dev), table.to(dev), sl, 512, md, ns, causal=True)
+    md, ns = mla.mla_get_metadata(sl, s_q * h, 1, num_parts=1)
+    o2, lse2 = mla.mla_decode_kvcache(q.to(dev), cache.to(dev), table.to(dev), sl, 512, md, ns, causal=True)
     assert torch.equal(o, o2) and torch.equal(lse, lse2) and mla.mla_device_status() == 0
 
 
@@ -277,3 +279,20 @@ def test_in_a_graph_and_on_another_stream(dev):
         torch.cuda.synchronize()
         R.assert_attention(o, lse, *want[i], False)
     assert mla.mla_device_status() == 0
+
+
+def test_partition_over_row_tiles(dev):
+    """mla_get_metadata_tree is the decode's partition of the tiles' lengths, bit for bit."""
+    import oracle
+    rng = np.random.default_rng(6)
+    for b, s_q, h, parts in ((1, 1, 16, 76), (3, 13, 64, 76), (16, 32, 128, 76), (5, 33, 100, 3), (300, 9, 128, 11)):
+        lens = rng.integers(0, 3000, b)
+        nodes = rng.integers(0, s_q + 1, b)
+        tiles = -(-s_q * h // 128)
+        for given in (None, nodes):
+            flat = [0 if given is not None and t * 128 // h >= given[i] else lens[i] for i in range(b) for t in range(tiles)]
+            want = oracle.schedule(np.array(flat), parts)
+            got = mla.mla_get_metadata_tree(torch.tensor(lens, dtype=torch.int32, device=dev), s_q, h,
+                                            None if given is None else torch.tensor(nodes, dtype=torch.int32, device=dev),
+                                            num_parts=parts)
+            assert np.array_equal(got[0].cpu().numpy(), want[0]) and np.array_equal(got[1].cpu().numpy(), want[1])
