@@ -436,7 +436,7 @@ MLA_API int mla_update_page_keys_fp8(const void *kv_pages, int64_t num_blocks, c
 
 /*
  * mla_blocks_workspace_bytes — device scratch of mla_decode_kvcache_blocks
- * (num_parts from mla_num_sm_parts(device, h_q, h_kv)).  0 on invalid arguments.
+ * (num_parts from mla_num_sm_parts(device, 1, 1)).  0 on invalid arguments.
  */
 MLA_API size_t mla_blocks_workspace_bytes(int batch, int s_q, int h_q, int h_kv, int dv, int max_blocks_per_seq,
                                           int topk_pages, int num_parts);
@@ -457,14 +457,16 @@ MLA_API size_t mla_blocks_workspace_bytes(int batch, int s_q, int h_q, int h_kv,
  * those of mla_decode_kvcache over the rows of the selected pages that lie
  * before L; a token with L <= 0 gets o = 0, lse = -inf and no pages.
  *   q, kcache, block_table, cache_seqlens, o, lse
- *                  as for mla_decode_kvcache (d = 576 or 512; batch * s_q <= 65535)
+ *                  as for mla_decode_kvcache (d = 576 or 512; batch * s_q <= 65535,
+ *                  h_q <= 16384)
  *   page_keys, page_scales
  *                  from mla_update_page_keys; 16-byte aligned keys
  *   topk_pages     pages per query token, >= sink_pages + local_pages
  *   sink_pages, local_pages
  *                  >= 0 and >= 1 (the last visible page, which may be partial, is
  *                  always taken)
- *   num_parts      split-KV parts of the decode: mla_num_sm_parts(device, h_q, h_kv)
+ *   num_parts      split-KV parts of the decode: mla_num_sm_parts(device, 1, 1), one
+ *                  per CTA pair
  *   softmax_scale  > 0
  *   causal         nonzero: the causal rule above
  *   pages          device int32 [batch][s_q][topk_pages], out: the selected
@@ -482,7 +484,7 @@ MLA_API int mla_decode_kvcache_blocks(const void *q, const void *kcache, int64_t
                                       int h_kv, int d, int dv, int num_parts, float softmax_scale, int causal, void *o,
                                       float *lse, int32_t *pages, void *workspace, size_t workspace_bytes,
                                       struct CUstream_st *stream);
-/* the same over packed e4m3 pages (d = 576; precision as for mla_decode_kvcache_fp8) */
+/* the same over packed e4m3 pages (d = 576; precision as for mla_decode_kvcache_tree_fp8) */
 MLA_API int mla_decode_kvcache_blocks_fp8(const void *q, const void *kv_pages, int64_t num_blocks,
                                           const int32_t *block_table, int max_blocks_per_seq,
                                           const int32_t *cache_seqlens, const int8_t *page_keys,
@@ -551,7 +553,14 @@ MLA_API int mla_decode_kvcache_tree(const void *q, const void *kcache, int64_t n
                                     const int32_t *tile_scheduler_metadata, const int32_t *num_splits, int num_parts,
                                     float softmax_scale, void *o, float *lse, void *workspace, size_t workspace_bytes,
                                     struct CUstream_st *stream);
-/* the same over packed e4m3 pages (d = 576; precision and scales as for mla_decode_kvcache_fp8) */
+/*
+ * mla_decode_kvcache_tree_fp8 — the same over packed e4m3 pages (d = 576).
+ *
+ * Scales as for mla_decode_kvcache_fp8.  Precision: both products run on the fp8
+ * tensor cores.  q is held exactly, but for elements below 2^-11 of their row's
+ * largest (to 2^-19 of it); a softmax weight times its token's scale is held to
+ * 2^-8 of itself, or to 2^-15 of the row's largest where that is more.
+ */
 MLA_API int mla_decode_kvcache_tree_fp8(const void *q, const void *kv_pages, int64_t num_blocks,
                                         const int32_t *block_table, int max_blocks_per_seq,
                                         const int32_t *cache_seqlens, const int32_t *tree_mask,

@@ -541,7 +541,7 @@ def _decode_blocks(call, q, cache, block_table, cache_seqlens, page_keys, page_s
         raise ValueError("topk_pages must cover sink_pages (>= 0) and local_pages (>= 1)")
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(d)
-    num_parts = mla_num_sm_parts(h_q, 1, dev)
+    num_parts = mla_num_sm_parts(1, 1, dev)
     ws_need = mla_blocks_workspace_bytes(b, s_q, h_q, 1, dv, max_blocks, topk_pages, num_parts)
     out, lse = _outputs(b, s_q, h_q, dv, dev, out, lse)
     if pages is None:

@@ -155,8 +155,10 @@ struct Lists {
     const int32_t *list_lens = nullptr;  // [batch]: the lengths the work partition was computed on
 };
 
-// Draft tree of the tree decode (unused otherwise).
+// Draft tree of the tree decode; `tiled` alone runs its kernels without masks
+// (the decode over selected pages).
 struct Tree {
+    bool tiled = false;              // work entries are row tiles
     const uint32_t *mask = nullptr;  // [batch][s_q][ceil(s_q / 32)]
     const int32_t *lens = nullptr;   // [batch], or null: s_q nodes everywhere
 };
@@ -168,7 +170,7 @@ int decode(const void *q, const void *kcache, Kind kind, int64_t num_blocks, con
            int causal, void *o, float *lse, void *workspace, size_t ws_bytes, struct CUstream_st *stream,
            const Lists &lists = Lists(), const Tree &tree = Tree()) {
     const bool e4m3 = kind == Kind::kE4m3, sparse = kind == Kind::kSparse;
-    Range range(tree.mask ? "mla_decode_kvcache_tree" : sparse ? "mla_decode_kvcache_sparse" : e4m3 ? "mla_decode_kvcache_fp8" : "mla_decode_kvcache");
+    Range range(tree.tiled ? "mla_decode_kvcache_tree" : sparse ? "mla_decode_kvcache_sparse" : e4m3 ? "mla_decode_kvcache_fp8" : "mla_decode_kvcache");
     if (!q || !kcache || !block_table || !cache_seqlens || !tile_scheduler_metadata || !num_splits || !o || !lse ||
         !workspace)
         return MLA_ERR_INVALID_ARG;
@@ -191,8 +193,8 @@ int decode(const void *q, const void *kcache, Kind kind, int64_t num_blocks, con
     const int rows = s_q * h_q;
     const int tiles = (rows + kRowsPerTile - 1) / kRowsPerTile;
     // a draft tree's work entries are row tiles, and a workspace slot holds one
-    if (tree.mask && (long long)batch * tiles > kMaxTreeEntries) return MLA_ERR_UNSUPPORTED;
-    const int entries = tree.mask ? batch * tiles : batch, slot = tree.mask ? kRowsPerTile : rows;
+    if (tree.tiled && (long long)batch * tiles > kMaxTreeEntries) return MLA_ERR_UNSUPPORTED;
+    const int entries = tree.tiled ? batch * tiles : batch, slot = tree.tiled ? kRowsPerTile : rows;
     if (ws_bytes < workspace_bytes(entries, slot, num_parts)) return MLA_ERR_WORKSPACE;
 
     DecodeParams p{};
@@ -232,20 +234,33 @@ int decode(const void *q, const void *kcache, Kind kind, int64_t num_blocks, con
         ev_end = g_split_end;
     }
     if (ev_begin && cudaEventRecord(ev_begin, s) != cudaSuccess) return MLA_ERR_CUDA;
-    cudaError_t e = tree.mask ? (e4m3 ? launch_split_kv_tc_tree<576, true>(p, s)
-                                 : d == kDqk ? launch_split_kv_tc_tree<576, false>(p, s)
-                                             : launch_split_kv_tc_tree<512, false>(p, s))
+    cudaError_t e = tree.tiled ? (e4m3 ? launch_split_kv_tc_tree<576, true>(p, s)
+                                  : d == kDqk ? launch_split_kv_tc_tree<576, false>(p, s)
+                                              : launch_split_kv_tc_tree<512, false>(p, s))
                     : sparse ? (g_cluster_multicast.load() ? launch_split_kv_tc_sparse(p, s)
                                                          : launch_split_kv_tc_sparse_local(p, s))
                     : e4m3 ? launch_split_kv_tc<576, true>(p, s)
                            : (d == kDqk ? launch_split_kv_tc<576, false>(p, s) : launch_split_kv_tc<512, false>(p, s));
     if (e != cudaSuccess) return MLA_ERR_CUDA;
     if (ev_end && cudaEventRecord(ev_end, s) != cudaSuccess) return MLA_ERR_CUDA;
-    e = tree.mask ? launch_combine_tree(p, kRowsPerTile, s) : launch_combine(p, s);
+    e = tree.tiled ? launch_combine_tree(p, kRowsPerTile, s) : launch_combine(p, s);
     return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
 }  // namespace
+
+namespace mla {
+int decode_tiled(const void *q, const void *cache, bool e4m3, int64_t num_blocks, const int32_t *block_table, int max_blocks,
+                 const int32_t *seqlens, int batch, int h_q, int d, const int32_t *metadata, const int32_t *num_splits,
+                 int num_parts, float softmax_scale, void *o, float *lse, void *workspace, size_t ws_bytes,
+                 struct CUstream_st *stream) {
+    Tree tree;
+    tree.tiled = true;
+    return decode(q, cache, e4m3 ? Kind::kE4m3 : Kind::kBf16, num_blocks, block_table, max_blocks, seqlens, batch, 1, h_q, 1,
+                  d, kDv, metadata, num_splits, num_parts, softmax_scale, 0, o, lse, workspace, ws_bytes, stream, Lists(),
+                  tree);
+}
+}  // namespace mla
 
 extern "C" {
 
@@ -328,6 +343,7 @@ int mla_decode_kvcache_tree(const void *q, const void *kcache, int64_t num_block
                             struct CUstream_st *stream) {
     if (!tree_mask) return MLA_ERR_INVALID_ARG;
     Tree tree;
+    tree.tiled = true;
     tree.mask = reinterpret_cast<const uint32_t *>(tree_mask);
     tree.lens = tree_lens;
     return decode(q, kcache, Kind::kBf16, num_blocks, block_table, max_blocks_per_seq, cache_seqlens, batch, s_q, h_q,
@@ -343,6 +359,7 @@ int mla_decode_kvcache_tree_fp8(const void *q, const void *kv_pages, int64_t num
                                 struct CUstream_st *stream) {
     if (!tree_mask) return MLA_ERR_INVALID_ARG;
     Tree tree;
+    tree.tiled = true;
     tree.mask = reinterpret_cast<const uint32_t *>(tree_mask);
     tree.lens = tree_lens;
     return decode(q, kv_pages, Kind::kE4m3, num_blocks, block_table, max_blocks_per_seq, cache_seqlens, batch, s_q, h_q,

@@ -17,6 +17,7 @@ constexpr size_t kAlign = 256;
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 constexpr int kMaxDecodeBatch = 65535;  // sequences of one decode call
+constexpr int kMaxDecodeHeads = 16384;  // 128 row tiles each: below the 2^24 tiles of one call
 
 int result(cudaError_t e) { return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA; }
 
@@ -100,8 +101,9 @@ BlocksLayout blocks_layout(int tokens, int h_q, int max_blocks, int topk, int nu
     l.table = take((size_t)tokens * topk * sizeof(int32_t));
     l.lens = take((size_t)tokens * sizeof(int32_t));
     l.metadata = take((size_t)num_parts * kMdInts * sizeof(int32_t));
-    l.splits = take(((size_t)tokens + 1) * sizeof(int32_t));
-    l.decode = take(workspace_bytes(tokens, h_q, num_parts));
+    const int entries = tokens * ((h_q + MLA_TILE_ROWS - 1) / MLA_TILE_ROWS);
+    l.splits = take(((size_t)entries + 1) * sizeof(int32_t));
+    l.decode = take(workspace_bytes(entries, MLA_TILE_ROWS, num_parts));
     l.total = at;
     return l;
 }
@@ -121,7 +123,7 @@ int decode_blocks(const void *q, const void *cache, int64_t num_blocks, const in
     if (!aligned16(q) || !aligned16(page_keys) || !aligned16(o) || (reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)))
         return MLA_ERR_INVALID_ARG;
     if (dv != kDv || h_kv != 1) return MLA_ERR_UNSUPPORTED;
-    if ((long long)batch * s_q > kMaxDecodeBatch || h_q > 65536 || (long long)topk * kPage > 0x7fffffffLL)
+    if ((long long)batch * s_q > kMaxDecodeBatch || h_q > kMaxDecodeHeads || (long long)topk * kPage > 0x7fffffffLL)
         return MLA_ERR_UNSUPPORTED;
     const int tokens = batch * s_q;
     const BlocksLayout l = blocks_layout(tokens, h_q, max_blocks, topk, num_parts);
@@ -152,11 +154,10 @@ int decode_blocks(const void *q, const void *cache, int64_t num_blocks, const in
     if (launch_select_pages(p, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return MLA_ERR_CUDA;
     // one "sequence" per query token over its own block table
     int32_t *md = reinterpret_cast<int32_t *>(ws + l.metadata), *ns = reinterpret_cast<int32_t *>(ws + l.splits);
-    st = mla_get_metadata(p.sel_lens, tokens, h_q, 1, num_parts, md, ns, stream);
+    st = mla_get_metadata_tree(p.sel_lens, nullptr, tokens, 1, h_q, 1, num_parts, md, ns, stream);
     if (st != MLA_OK) return st;
-    auto *run = e4m3 ? mla_decode_kvcache_fp8 : mla_decode_kvcache;
-    return run(q, cache, num_blocks, p.sel_table, topk, p.sel_lens, tokens, 1, h_q, 1, d, dv, md, ns, num_parts,
-               softmax_scale, 0, o, lse, ws + l.decode, ws_bytes - l.decode, stream);
+    return decode_tiled(q, cache, e4m3, num_blocks, p.sel_table, topk, p.sel_lens, tokens, h_q, d, md, ns, num_parts,
+                        softmax_scale, o, lse, ws + l.decode, ws_bytes - l.decode, stream);
 }
 
 }  // namespace
@@ -214,7 +215,7 @@ size_t mla_blocks_workspace_bytes(int batch, int s_q, int h_q, int h_kv, int dv,
                                   int num_parts) {
     if (batch < 1 || s_q < 1 || h_q < 1 || h_kv != 1 || dv != kDv || max_blocks_per_seq < 1 || topk_pages < 1 || num_parts < 1)
         return 0;
-    if ((long long)batch * s_q > kMaxDecodeBatch || h_q > 65536) return 0;
+    if ((long long)batch * s_q > kMaxDecodeBatch || h_q > kMaxDecodeHeads) return 0;
     return blocks_layout(batch * s_q, h_q, max_blocks_per_seq, topk_pages, num_parts).total;
 }
 

@@ -125,7 +125,8 @@ cudaError_t launch_schedule_tree(const int32_t *seqlens, const int32_t *tree_len
                                  int h_q, int num_parts, int32_t *metadata, int32_t *num_splits, unsigned int *status,
                                  cudaStream_t stream);
 cudaError_t launch_combine_tree(const DecodeParams &p, int tile_rows, cudaStream_t stream);
-// the same kernel with a draft tree's mask over the last rows of each sequence
+// the same kernel over row tiles, with a draft tree's mask over the last rows of
+// each sequence (tree_mask null: no masks)
 template <int D, bool E4M3>
 cudaError_t launch_split_kv_tc_tree(const DecodeParams &p, cudaStream_t stream);
 
@@ -134,6 +135,13 @@ cudaError_t launch_page_keys(const PageKeysParams &p, int d, bool e4m3, cudaStre
 cudaError_t launch_select_pages(const SelectParams &p, cudaStream_t stream);
 cudaError_t launch_tree_mask(const int32_t *parents, int batch, int s_q, uint32_t *mask, unsigned int *status,
                              cudaStream_t stream);
+
+// decode of one query token per sequence on the tree kernels, without masks:
+// work entries are row tiles (partition: launch_schedule_tree)
+int decode_tiled(const void *q, const void *cache, bool e4m3, int64_t num_blocks, const int32_t *block_table, int max_blocks,
+                 const int32_t *seqlens, int batch, int h_q, int d, const int32_t *metadata, const int32_t *num_splits,
+                 int num_parts, float softmax_scale, void *o, float *lse, void *workspace, size_t ws_bytes,
+                 struct CUstream_st *stream);
 
 // address of the status word on the current device (MLA_OK or MLA_ERR_CUDA)
 int status_address(unsigned int **out);

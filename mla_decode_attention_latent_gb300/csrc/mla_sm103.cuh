@@ -234,8 +234,8 @@ __device__ __forceinline__ uint64_t desc_sw64(uint32_t smem_addr) {
 }
 
 // instruction descriptor: kind::f8f6f4 with e4m3 A and B (format fields 0), fp32 accumulator
-__host__ __device__ constexpr uint32_t idesc_e4m3(int m, int n) {
-    return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+__host__ __device__ constexpr uint32_t idesc_e4m3(int m, int n, bool b_mn_major = false) {
+    return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
 // instruction descriptor: kind::f16 with f16 A and B (format field 0), fp32 accumulator
@@ -458,6 +458,19 @@ __device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
     asm("{\n\t.reg .b16 t;\n\tcvt.rn.satfinite.e4m3x2.f32 t, %1, %2;\n\tcvt.u32.u16 %0, t;\n\t}"
         : "=r"(r)
         : "f"(hi), "f"(lo));
+    return r;
+}
+
+// the same from two f16 values
+__device__ __forceinline__ uint32_t pack_e4m3x2_f16(uint32_t x) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 t;\n\tcvt.rn.satfinite.e4m3x2.f16x2 t, %1;\n\tcvt.u32.u16 %0, t;\n\t}" : "=r"(r) : "r"(x));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t f16x2_sub(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 

@@ -70,6 +70,20 @@
 // out of the mask words and takes the masked path below; every other page runs
 // as in a dense decode.  A node's row that no query token of the tile sees is
 // zeroed in V (its weight is 0 in every row, but 0 times a NaN would not be).
+// The decode over selected pages runs on the same kernels, without masks.
+//
+// The e4m3 form of these kernels runs both products in fp8, with fewer rounding
+// steps than the one above:
+//   scores  sigma_r is a power of two, so q / sigma_r keeps its 8 bits and two
+//           e4m3 parts of 4 bits hold them exactly (below 2^-11 of the row's
+//           maximum, where e4m3 runs out of exponents, to 2^-19 of it).  Two parts with their
+//           RoPE dims fit in TMEM beside both S buffers, so that no score MMA
+//           reads Q from shared memory.
+//   values  the weights w_j = p_j c_j times a power of two per row (chosen by the largest
+//           weight, lowered lazily like the running maximum, carried by O and
+//           divided out at the end) are split into two e4m3 parts as well, and the V codes
+//           are MN-major operands as they land: nothing is widened, a stage is
+//           32 KB and four are in flight.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
@@ -111,6 +125,7 @@ constexpr bool kPairGather = kSparse && MLA_SPARSE_MULTICAST != 0;
 #endif
 constexpr bool kTree = MLA_SPLIT_TREE != 0;      // the last rows of a sequence are a draft tree's nodes
 constexpr bool kMask = kSparse || kTree;         // pages carry a 64-bit mask of their visible rows
+constexpr bool kE8 = kFp8 && kTree;              // fp8 products on both sides, Q in two exact parts (see the header)
 static_assert(!(kSparse && kTree), "a sparse list has no tree");
 static_assert(!(kSparse && kFp8) && (!kSparse || MLA_SPLIT_D == 576), "sparse decode: 576-wide bf16 rows");
 constexpr bool kRing = kFp8 || kSparse;          // a per-step side ring (e4m3: token scales; sparse: key masks)
@@ -132,7 +147,7 @@ constexpr int kStepPages = (kFp8 || kSparse) ? 1 : 2;
 // so that each SM's gather engine moves about half of a page's rows.
 constexpr int kKSlots = kFp8 ? 4 : (kSparse ? 2 : 10);
 constexpr int kRingSlots = kKSlots / kScoreIssuers;  // slots per score-MMA issuer's ring
-constexpr int kVStages = 2;                    // value CTA ring: whole pages (dims 0..511)
+constexpr int kVStages = kE8 ? 4 : 2;          // value CTA ring: whole pages (dims 0..511)
 constexpr int kSBufs = 2;                      // S buffers in TMEM (score CTA), one per step
 constexpr int kPBufs = 2;                      // P buffers (staging in the score CTA, landing in the value CTA)
 constexpr int kKChunks = kD / 64;              // 9 (or 8) chunks of 64 dims (128 B rows)
@@ -141,7 +156,9 @@ constexpr int kLatChunks = kDv / 64;           // 8 latent chunks: the Q part ke
 constexpr uint32_t kChunkBytes = kPage * 128;  // 64 tokens x 128 B = 8 KB
 constexpr uint32_t kE4ChunkBytes = kPage * 64;             // one 64-code chunk of one e4m3 page: 4 KB
 constexpr uint32_t kSlotBytes = kFp8 ? kKChunks * kE4ChunkBytes : 2 * kChunkBytes;  // 36 KB / 16 KB
-constexpr uint32_t kVStageBytes = (kSparse ? kKChunks : kVChunks) * kChunkBytes;  // 64 KB (sparse: 72 KB page buffers)
+// 64 KB (sparse: 72 KB page buffers; fp8 P V: 32 KB, four chunks of 64 tokens x 128 codes)
+constexpr int kVTiles = kE8 ? kDv / 128 : kVChunks;   // 8 KB chunks of a stage's value dims
+constexpr uint32_t kVStageBytes = (kSparse ? kKChunks : kVTiles) * kChunkBytes;
 constexpr uint32_t kPBytes = kTileRows * 128;             // 16 KB: 128 rows x 64 bf16, 128B-swizzled
 constexpr uint32_t kFacOff = kPBytes;                      // then fac[128] (fp32)
 constexpr uint32_t kInvLOff = kPBytes + kTileRows * 4;     // then inv_l[128] (fp32)
@@ -150,8 +167,9 @@ constexpr uint32_t kPMsgBytes = kPBytes + 2 * kTileRows * 4;  // 17 KB, a multip
 // (sigma_r = max |q_r| / 448), each contracted with the codes in fp8 on the
 // tensor cores; the latent dims of the three parts sit in TMEM (four codes
 // per column), their RoPE dims in 64-byte-swizzled shared tiles
-constexpr int kQParts = kFp8 ? 3 : 1;
-constexpr uint32_t kQPartCols = kDv / 4;                   // e4m3: one part's 512 latent codes = 128 columns
+constexpr int kQParts = kE8 ? 2 : kFp8 ? 3 : 1;
+constexpr bool kQRopeSmem = kHasRope && !kE8;              // Q's RoPE dims in shared memory, or with the rest in TMEM
+constexpr uint32_t kQPartCols = (kE8 ? kD : kDv) / 4;      // e4m3: one part's codes, four per column
 constexpr uint32_t kQCols = kFp8 ? kQParts * kQPartCols : kDv / 2;  // bf16: 256 columns of bf16 pairs
 constexpr uint32_t kSCol0 = kQCols;                        // S buffers follow Q
 constexpr uint32_t kSCols = kStepPages * kPage;            // an S buffer holds the scores of one step
@@ -179,7 +197,7 @@ static_assert(kE4PageBytes % 16 == 0 && kE4ScaleOff % 16 == 0, "TMA and bulk-cop
 constexpr uint32_t kKRingOff = 0;
 constexpr uint32_t kQRopeOff = kKRingOff + (kSparse ? kVStages * kVStageBytes : kKSlots * kSlotBytes);
 constexpr uint32_t kQRopePartBytes = kTileRows * (kFp8 ? 64 : 128);  // one part's [128 rows] RoPE tile
-constexpr uint32_t kStageOff = kQRopeOff + (kHasRope ? kQParts * kQRopePartBytes : 0);
+constexpr uint32_t kStageOff = kQRopeOff + (kQRopeSmem ? kQParts * kQRopePartBytes : 0);
 constexpr uint32_t kScaleOff = kStageOff + kPBufs * kPMsgBytes;   // the side ring of the steps in flight
 constexpr uint32_t kScoreEnd = kScaleOff + (kRing ? kScSlots * kScBytes : 0);
 // value CTA: [V ring 2 x 64 KB (sparse: the page buffers)][P landing 2 x 17 KB][epilogue staging 34 KB]
@@ -238,6 +256,10 @@ __device__ __forceinline__ int tree_nodes(const DecodeParams &p, int b) {
         return n < 0 ? 0 : p.s_q;
     }
     return n;
+}
+// position of a sequence's first node; past every page when the call has no masks
+__device__ __forceinline__ int tree_start(const DecodeParams &p, int T, int nodes) {
+    return p.tree_mask ? T - nodes : 0x7fffffff;
 }
 __device__ __forceinline__ int work_entries(const DecodeParams &p) { return kTree ? p.batch * p.tiles : p.batch; }
 // rows of one work entry: what a workspace slot holds
@@ -717,7 +739,11 @@ __device__ void value_producer(const DecodeParams &p, const Ctx &c, const CUtens
             }
             const int blk = safe_block(p, s.b, pg);
             uint8_t *dst = c.base + kVRingOff + st * kVStageBytes;
-            if constexpr (kFp8) {
+            if constexpr (kE8) {
+                mbar_arrive_expect_tx(c.bar(B_VFULL + st), kVStageBytes);
+                for (int ch = 0; ch < kVTiles; ++ch)
+                    tma_load_3d(dst + ch * kChunkBytes, map, c.bar(B_VFULL + st), 128 * ch, 0, blk);
+            } else if constexpr (kFp8) {
                 mbar_arrive_expect_tx(c.bar(B_VLAND + st), kVChunks * kE4ChunkBytes);
                 for (int ch = 0; ch < kVChunks; ++ch)
                     tma_load_3d(dst + kVLandOff + ch * kE4ChunkBytes, map, c.bar(B_VLAND + st), 64 * ch, 0, blk);
@@ -728,7 +754,7 @@ __device__ void value_producer(const DecodeParams &p, const Ctx &c, const CUtens
             }
         }
     }
-    constexpr int land = kFp8 ? B_VLAND : B_VFULL;  // the barrier the loads complete on
+    constexpr int land = kFp8 && !kE8 ? B_VLAND : B_VFULL;  // the barrier the loads complete on
     for (uint32_t k = it > (uint32_t)kVStages ? it - kVStages : 0; k < it; ++k)
         mbar_wait(c.bar(land + (int)(k % kVStages)), (k / kVStages) & 1, c.status);
 }
@@ -783,7 +809,7 @@ __device__ void score_mma(const DecodeParams &p, const Ctx &c, uint32_t tmem, in
                     const uint32_t b = slot + ch * kE4ChunkBytes;
 #pragma unroll
                     for (int t = 0; t < kQParts; ++t) {
-                        if (ch < kLatChunks) {
+                        if (!kQRopeSmem || ch < kLatChunks) {
                             const uint32_t a = tmem + t * kQPartCols + ch * 16;
                             mma_ts_f8(d, a, desc_sw64(b), id8, (ch | t) ? 1u : 0u);
                             mma_ts_f8(d, a + 8, desc_sw64(b + 32), id8, 1u);
@@ -879,6 +905,19 @@ __device__ void value_mma(const DecodeParams &p, const Ctx &c, uint32_t tmem, in
             tc_fence_after();
             const uint32_t vtile = smem_u32(c.base + kVRingOff + st * kVStageBytes);
             const uint32_t ptile = smem_u32(c.base + kPBufOff + pb * kPMsgBytes);
+            if constexpr (kE8) {
+                // P's two e4m3 parts (codes 0..63 and 64..127 of a row) times the
+                // codes as they landed, 32 tokens per MMA
+                constexpr uint32_t id8 = idesc_e4m3(kTileRows, 256, true);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint64_t ad = desc_sw128(ptile + k * 32, 16, 1024);
+                        const uint64_t bd = desc_sw128(vtile + h * 2 * kChunkBytes + (k & 1) * 4096, kChunkBytes, 1024);
+                        mma_ss_f8(tmem + h * 256, ad, bd, id8, (pg > s.p0 || k > 0) ? 1u : 0u);
+                    }
+            } else
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -919,7 +958,7 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
             row_ok = gr < p.rows;
             qi = row_ok ? gr / p.h_q : 0;
             const int nodes = tree_nodes(p, s.b);
-            tree_base = s.T - nodes;
+            tree_base = tree_start(p, s.T, nodes);
             if (qi >= nodes) T_row = 0;  // a row behind the tree sees nothing
         }
         // both MMA issuers have seen the previous segment's Q (and, having
@@ -950,6 +989,9 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
                     }
                 }
                 qsig = amax > 0.f ? amax / kE4Max : 1.f;
+                // fp8 on both sides: the next power of two, so that q / qsig keeps
+                // its 8 bits and two parts of 4 bits hold them all
+                if constexpr (kE8) qsig = __uint_as_float((__float_as_uint(qsig) + 0x7fffffu) & 0x7f800000u);
                 const float inv = 1.f / qsig;
                 // one 64-dim chunk: three parts of 16 words (four codes each)
                 auto split = [&](const uint4 (&x)[8], uint32_t (&ph)[16], uint32_t (&pm)[16], uint32_t (&pl)[16]) {
@@ -964,12 +1006,12 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
                                 v[2 * e] = __uint_as_float(w4[2 * hw + e] << 16) * inv;
                                 v[2 * e + 1] = __uint_as_float(w4[2 * hw + e] & 0xffff0000u) * inv;
                             }
-                            uint32_t code[3];
+                            uint32_t code[3] = {0u, 0u, 0u};
 #pragma unroll
-                            for (int t = 0; t < 3; ++t) {
+                            for (int t = 0; t < kQParts; ++t) {
                                 const uint32_t c01 = pack_e4m3x2(v[0], v[1]), c23 = pack_e4m3x2(v[2], v[3]);
                                 code[t] = c01 | (c23 << 16);
-                                if (t < 2) {
+                                if (t < kQParts - 1) {
                                     float d0, d1, d2, d3;
                                     f16x2_to_f32(e4m3x2_to_f16x2(c01), d0, d1);
                                     f16x2_to_f32(e4m3x2_to_f16x2(c23), d2, d3);
@@ -999,10 +1041,10 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
                     }
                     uint32_t ph[16], pm[16], pl[16];
                     split(x, ph, pm, pl);
-                    if (ch < kLatChunks) {
+                    if (!kQRopeSmem || ch < kLatChunks) {
                         tmem_st16(tmem + lane_base + 0 * kQPartCols + ch * 16, ph);
                         tmem_st16(tmem + lane_base + 1 * kQPartCols + ch * 16, pm);
-                        tmem_st16(tmem + lane_base + 2 * kQPartCols + ch * 16, pl);
+                        if constexpr (kQParts > 2) tmem_st16(tmem + lane_base + 2 * kQPartCols + ch * 16, pl);
                     } else {
                         // 64 B per row; 16-byte piece q of row r at q ^ ((r >> 1) & 3)
                         const uint32_t rope = smem_u32(c.base + kQRopeOff) + (uint32_t)r * 64u;
@@ -1060,6 +1102,7 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
         mbar_arrive(c.bar(B_QFULL));
 
         float m = -CUDART_INF_F, l = 0.f;
+        float ko = 0.f;  // fp8 P V: the power of two that O and P carry (0: every weight so far is 0)
         for (int pg = s.p0; pg < s.p1; ++pg, ++it) {
             const int pb = it % kPBufs;
             const int q2 = (pg - s.p0) % kStepPages;  // position of this page in its step
@@ -1181,7 +1224,14 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
                     f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[2 * j]), __uint_as_float(sr[2 * j + 1])), sc2, nm2), xa, xb);
                     const float a = ex2(xa), b = ex2(xb);
                     sum2[j & 3] = f2_add(sum2[j & 3], f2_pack(a, b));
-                    if constexpr (kFp8) {
+                    if constexpr (kE8) {
+                        // P of key j times its token's scale, kept in fp32
+                        // (in the score registers, which are read no more)
+                        float pa, pb2;
+                        f2_unpack(f2_fma(f2_pack(a, b), f2_pack(cs[2 * j], cs[2 * j + 1]), f2_pack(0.f, 0.f)), pa, pb2);
+                        sr[2 * j] = __float_as_uint(pa);
+                        sr[2 * j + 1] = __float_as_uint(pb2);
+                    } else if constexpr (kFp8) {
                         // P of key j times its token's scale: the dequantized value row
                         float pa, pb2;
                         f2_unpack(f2_fma(f2_pack(a, b), f2_pack(cs[2 * j], cs[2 * j + 1]), f2_pack(0.f, 0.f)), pa,
@@ -1196,6 +1246,42 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
             f2_unpack(f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3])), sum_lo, sum_hi);
             const float sum = sum_lo + sum_hi;
             l = l * fac + sum;
+            if constexpr (kE8) {
+                // The weights w = P c as e4m3 need their place in its range: a
+                // power of two ko per row puts the largest at 56..112 when it is
+                // set, and only shrinks (with O, through fac) when a page's
+                // largest would pass 448.  w ko is split into two e4m3 parts (4 bits each,
+                // subtracted in f16, exactly): off by at most 2^-8 of itself, or
+                // 2^-10 where the largest is at least 56.
+                if (m != -CUDART_INF_F) {
+                    float wx[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        wx[j & 3] = max3f(wx[j & 3], fabsf(__uint_as_float(sr[2 * j])), fabsf(__uint_as_float(sr[2 * j + 1])));
+                    const float wmax = fmaxf(fmaxf(wx[0], wx[1]), fmaxf(wx[2], wx[3]));
+                    if (wmax * ko > kE4Max || (ko == 0.f && wmax > 0.f)) {
+                        const float kn = __uint_as_float(__float_as_uint(fminf(kE4Max / 4.f / wmax, 0x1p100f)) & 0x7f800000u);
+                        if (ko != 0.f) fac *= kn / ko;
+                        ko = kn;
+                    }
+                    const uint64_t ko2 = f2_pack(ko, ko), zero2 = f2_pack(0.f, 0.f);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {  // keys 4 j .. 4 j + 3
+                        uint32_t hi[2], lo[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float wa, wb;
+                            f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[4 * j + 2 * e]), __uint_as_float(sr[4 * j + 2 * e + 1])),
+                                             ko2, zero2), wa, wb);
+                            const uint32_t w16 = pack_f16(wa, wb);
+                            hi[e] = pack_e4m3x2_f16(w16);
+                            lo[e] = pack_e4m3x2_f16(f16x2_sub(w16, e4m3x2_to_f16x2(hi[e])));
+                        }
+                        pk[j] = hi[0] | (hi[1] << 16);
+                        pk[16 + j] = lo[0] | (lo[1] << 16);
+                    }
+                }
+            }
 
             // staging pb is free once the value CTA's MMA of page it - 2 is
             // done: that MMA consumed the bulk copy made from it
@@ -1206,7 +1292,10 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
             for (int j = 0; j < 8; ++j)
                 sts128(stage_s + r * 128 + 16 * (j ^ (r & 7)), pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
             sts32(stage_s + kFacOff + 4 * r, __float_as_uint(fac));
-            if (pg == s.p1 - 1) sts32(stage_s + kInvLOff + 4 * r, __float_as_uint(l > 0.f ? 1.f / l : 0.f));
+            if (pg == s.p1 - 1) {
+                const float div = kE8 ? l * ko : l;  // O carries ko
+                sts32(stage_s + kInvLOff + 4 * r, __float_as_uint(div > 0.f ? 1.f / div : 0.f));
+            }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
@@ -1258,7 +1347,7 @@ __device__ void value_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
         if constexpr (kTree) {
             tile = s.tile;
             nodes = tree_nodes(p, s.b);
-            tree_base = s.T - nodes;
+            tree_base = tree_start(p, s.T, nodes);
         }
         for (int pg = s.p0; pg < s.p1; ++pg, ++it) {
             const int pb = it % kPBufs, st = it % kVStages;
@@ -1267,7 +1356,7 @@ __device__ void value_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
             if constexpr (kTree) {
                 if ((pg + 1) * kPage > tree_base) tmask = tree_tile_mask(p, s.b, tile, nodes, tree_base, pg);
             }
-            if constexpr (kFp8) {
+            if constexpr (kFp8 && !kE8) {
                 // widen the page's V codes in place as soon as they land (rows
                 // past the sequence's end become zeros); the 128 threads' reads
                 // all come before any write through B_VREAD, a bounded barrier
@@ -1292,7 +1381,7 @@ __device__ void value_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
             // rows past the sequence's end in its last page: zero them in V so
             // that garbage (even NaN) times a zero weight stays zero
             const int tail = s.T - pg * kPage;
-            if (!kFp8 && (tail < kPage || (kTree && tmask != ~0ull))) {
+            if ((!kFp8 || kE8) && (tail < kPage || (kTree && tmask != ~0ull))) {
                 if constexpr (kSparse) {
                     for (int ch = 0; ch < kVChunks; ++ch)
                         if (!warp_wait(c, B_CHUNK + st * kKChunks + ch, (it / kVStages) & 1)) return;
@@ -1306,7 +1395,7 @@ __device__ void value_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
                 for (int rr = (kTree ? 0 : (tail > 0 ? tail : 0)) + (tid >> 3); rr < kPage; rr += 16)
                     if (!kTree || rr >= tail || ((tmask >> rr) & 1ull) == 0)
 #pragma unroll
-                    for (int ch = 0; ch < kVChunks; ++ch) sts128(vt + ch * kChunkBytes + rr * 128, 0u, 0u, 0u, 0u);
+                    for (int ch = 0; ch < kVTiles; ++ch) sts128(vt + ch * kChunkBytes + rr * 128, 0u, 0u, 0u, 0u);
                 fence_proxy_async_smem();
             }
             // lazy rescale of this row of O before the next accumulation
@@ -1449,7 +1538,7 @@ split_kv_tc_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_cons
             mbar_init(c.bar(B_KEMPTY + i), 1);
         }
         for (int i = 0; i < kVStages; ++i) {
-            mbar_init(c.bar(B_VFULL + i), kFp8 ? 128 : 1);  // e4m3: the 128 row threads that widened the page
+            mbar_init(c.bar(B_VFULL + i), kFp8 && !kE8 ? 128 : 1);  // e4m3: the 128 row threads that widened the page
             mbar_init(c.bar(B_VEMPTY + i), 1);
         }
         if constexpr (kSparse) {
@@ -1582,12 +1671,13 @@ bool make_kv_map(CUtensorMap *m, CUtensorMap *m2, const void *kcache, int64_t nu
         cuuint64_t dims[3] = {(cuuint64_t)kD, (cuuint64_t)kPage, (cuuint64_t)num_blocks};
         cuuint64_t strides[2] = {(cuuint64_t)kD, (cuuint64_t)kE4PageBytes};
         cuuint32_t box[3] = {64, (cuuint32_t)kPage, 1};
+        cuuint32_t box2[3] = {128, (cuuint32_t)kPage, 1};  // fp8 P V: V's MN-major operand chunks
         cuuint32_t es[3] = {1, 1, 1};
         return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(kcache), dims, strides, box, es,
                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS &&
-               enc(m2, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(kcache), dims, strides, box, es,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               enc(m2, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(kcache), dims, strides, kE8 ? box2 : box, es,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, kE8 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
     }
     *m2 = *m;

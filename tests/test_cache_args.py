@@ -81,14 +81,14 @@ def blocks(lib, fp8=False, **over):
     (dict(scale=0.0), BAD), (dict(scale=-0.1), BAD), (dict(scale=float("nan")), BAD),
     (dict(q=264), BAD), (dict(keys=264), BAD), (dict(o=264), BAD), (dict(ws=272), BAD), (dict(mb=1 << 25), BAD),
     (dict(dv=256), UNSUP), (dict(hkv=2), UNSUP), (dict(d=448), UNSUP), (dict(b=65536), UNSUP), (dict(b=8192, s=8), UNSUP),
-    (dict(h=65537), UNSUP), (dict(topk=1 << 25), UNSUP), (dict(bytes=4096), WS)])
+    (dict(h=16385), UNSUP), (dict(topk=1 << 25), UNSUP), (dict(bytes=4096), WS)])
 def test_blocks(lib, fp8, over, code):
     assert blocks(lib, fp8, **over) == code
 
 
 def test_blocks_workspace(lib):
     n = lib.mla_blocks_workspace_bytes(4, 2, 128, 1, 512, 100, 16, 76)
-    decode = lib.mla_workspace_bytes(8, 1, 128, 1, 512, 76)
+    decode = lib.mla_tree_workspace_bytes(8, 1, 128, 1, 512, 76)
     assert n % 256 == 0 and n >= decode + 4 * 8 * 100 + 4 * 8 * 16 + 4 * 8 + 32 * 76 + 4 * 9
     for bad in ((0, 2, 128, 1, 512, 100, 16, 76), (4, 0, 128, 1, 512, 100, 16, 76), (4, 2, 0, 1, 512, 100, 16, 76),
                 (4, 2, 128, 2, 512, 100, 16, 76), (4, 2, 128, 1, 576, 100, 16, 76), (4, 2, 128, 1, 512, 0, 16, 76),
