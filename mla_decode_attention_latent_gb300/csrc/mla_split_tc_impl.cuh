@@ -1249,18 +1249,21 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
             if constexpr (kE8) {
                 // The weights w = P c as e4m3 need their place in its range: a
                 // power of two ko per row puts the largest at 56..112 when it is
-                // set, and only shrinks (with O, through fac) when a page's
-                // largest would pass 448.  w ko is split into two e4m3 parts (4 bits each,
-                // subtracted in f16, exactly): off by at most 2^-8 of itself, or
-                // 2^-10 where the largest is at least 56.
+                // set; it is set anew when a page's largest would pass 448, and
+                // with every new running maximum (which shrinks P itself), never
+                // so that what O holds would grow.  w ko is split into two e4m3
+                // parts (4 bits each, subtracted in f16, exactly): off by at most
+                // about 2^-8 of itself, or 2^-10 where the largest so far is at least 56.
                 if (m != -CUDART_INF_F) {
                     float wx[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
                         wx[j & 3] = max3f(wx[j & 3], fabsf(__uint_as_float(sr[2 * j])), fabsf(__uint_as_float(sr[2 * j + 1])));
                     const float wmax = fmaxf(fmaxf(wx[0], wx[1]), fmaxf(wx[2], wx[3]));
-                    if (wmax * ko > kE4Max || (ko == 0.f && wmax > 0.f)) {
-                        const float kn = __uint_as_float(__float_as_uint(fminf(kE4Max / 4.f / wmax, 0x1p100f)) & 0x7f800000u);
+                    if (wmax > 0.f && (wmax * ko > kE4Max || fac != 1.f || ko == 0.f)) {
+                        float kn = fminf(kE4Max / 4.f / wmax, 0x1p100f);
+                        if (ko != 0.f) kn = fminf(kn, ko / fac);  // fac kn / ko <= 1 (fac = 0: no limit)
+                        kn = __uint_as_float(__float_as_uint(kn) & 0x7f800000u);
                         if (ko != 0.f) fac *= kn / ko;
                         ko = kn;
                     }

@@ -296,3 +296,37 @@ def test_partition_over_row_tiles(dev):
                                             None if given is None else torch.tensor(nodes, dtype=torch.int32, device=dev),
                                             num_parts=parts)
             assert np.array_equal(got[0].cpu().numpy(), want[0]) and np.array_equal(got[1].cpu().numpy(), want[1])
+
+
+@pytest.mark.parametrize("d,fp8,max_exp", [(576, False, 40.0), (512, False, 40.0), (576, True, 10.0)])
+@pytest.mark.parametrize("jump,starts", [(11.0, [0, 4, 9, 14]), (5.0, [0, 2, 4, 6, 8, 10, 12, 14]), (7.5, [0, 1, 2, 3, 11, 12, 13])])
+@pytest.mark.parametrize("num_parts", [1, 3])
+def test_scores_that_climb(dev, d, fp8, max_exp, jump, starts, num_parts):
+    """The running maximum rises again and again, by more and by less than the lazy rescale lets pass, and what
+    older rows lose in weight their values make up for."""
+    from mla_decode_attention_latent_gb300 import workloads as W
+    lens, s_q, h = [1000, 700], 3, 64
+    c = W.Case("climb", batch=2, s_q=s_q, h_q=h, seqlens=tuple(lens), seed=300, d=d, fp8=fp8)
+    x = W.staircase(W.make_inputs(c, "cpu"), starts, jump_log2=jump, max_exp=max_exp)
+    sees = np.stack([R.ancestors([-1, 0, 0])] * 2)
+    check(dev, x.q, x.kcache, x.block_table, lens, sees, num_parts=num_parts)
+
+
+@pytest.mark.parametrize("num_parts", [1, 3])
+@pytest.mark.parametrize("order", ["up", "down", "mixed"])
+def test_scales_of_many_sizes(dev, order, num_parts):
+    """e4m3 rows whose scales span 2^20, rising, falling and mixed along the sequence, with nearly even weights: the
+    range that the weights take in the fp8 product follows the largest, and small rows must not disturb it."""
+    from mla_decode_attention_latent_gb300 import workloads as W
+    g = torch.Generator().manual_seed(7)
+    lens, s_q, h = [900, 500], 2, 64
+    table, used = R.random_table(g, lens)
+    rows = torch.randn((used, 64, 576), generator=g)
+    for b, T in enumerate(lens):
+        e = torch.linspace(-14, 6, T) if order == "up" else torch.linspace(6, -14, T) if order == "down" else \
+            torch.rand((T,), generator=g) * 20 - 14
+        for t in range(T):
+            rows[R.place(table, b, t)] *= 2.0 ** float(e[t])
+    q = (torch.randn((2, s_q, h, 576), generator=g) * 2.0 ** -9).to(torch.bfloat16)
+    cache = W.pack_e4m3_pages(rows)
+    check(dev, q, cache, table, lens, np.stack([R.ancestors([-1, 0])] * 2), num_parts=num_parts)
