@@ -130,7 +130,10 @@ static_assert(!(kSparse && kTree), "a sparse list has no tree");
 static_assert(!(kSparse && kFp8) && (!kSparse || MLA_SPLIT_D == 576), "sparse decode: 576-wide bf16 rows");
 constexpr bool kRing = kFp8 || kSparse;          // a per-step side ring (e4m3: token scales; sparse: key masks)
 
-constexpr int kThreads = 256;                  // 8 warps: TMA, MMA, 4 row warps, second score MMA issuer and TMA producer
+// 8 warps: TMA, MMA, 4 row warps, second score MMA issuer and TMA producer; fp8
+// products: 4 more row warps in the score CTA, the two groups alternating pages
+constexpr int kThreads = kE8 ? 384 : 256;
+constexpr int kGroups = kE8 ? 2 : 1;           // row-warp groups of the score CTA
 constexpr int kTileRows = 128;                 // query rows per tile = TMEM lanes
 constexpr int kScoreIssuers = 2;               // score-CTA MMA issuers (and TMA producers), alternating steps
 // Pages per score step: two for bf16 rows (one tcgen05 MMA with N = 128
@@ -199,7 +202,10 @@ constexpr uint32_t kQRopeOff = kKRingOff + (kSparse ? kVStages * kVStageBytes : 
 constexpr uint32_t kQRopePartBytes = kTileRows * (kFp8 ? 64 : 128);  // one part's [128 rows] RoPE tile
 constexpr uint32_t kStageOff = kQRopeOff + (kQRopeSmem ? kQParts * kQRopePartBytes : 0);
 constexpr uint32_t kScaleOff = kStageOff + kPBufs * kPMsgBytes;   // the side ring of the steps in flight
-constexpr uint32_t kScoreEnd = kScaleOff + (kRing ? kScSlots * kScBytes : 0);
+// two groups: the running state that one leaves for the other's next page,
+// [maximum 2 x 128][row sum 2 x 128][weight scale 2 x 128] fp32
+constexpr uint32_t kChainOff = kScaleOff + (kRing ? kScSlots * kScBytes : 0);
+constexpr uint32_t kScoreEnd = kChainOff + (kGroups > 1 ? 6 * kTileRows * 4 : 0);
 // value CTA: [V ring 2 x 64 KB (sparse: the page buffers)][P landing 2 x 17 KB][epilogue staging 34 KB]
 constexpr uint32_t kVRingOff = 0;
 constexpr uint32_t kPBufOff = kVRingOff + kVStages * kVStageBytes;
@@ -230,7 +236,11 @@ constexpr int B_VLAND = B_BASE_COUNT, B_SCFULL = B_VLAND + kVStages, B_SCEMPTY =
 // offset in both CTAs, so that the score MMAs can start on a page's first
 // chunks while the rest are still being gathered
 constexpr int B_CHUNK = B_VREAD + 1;
-constexpr int B_COUNT = kSparse ? B_CHUNK + kVStages * kKChunks : (kRing ? B_VREAD + 1 : B_BASE_COUNT);
+// two groups: [group][warp of the group] x {maximum, sum and scale} left for the
+// other group's warp of the same rows (32 arrivals each)
+constexpr int B_CHAIN = B_VREAD + 1;
+constexpr int B_COUNT = kSparse ? B_CHUNK + kVStages * kKChunks
+                                : (kGroups > 1 ? B_CHAIN + 16 : (kRing ? B_VREAD + 1 : B_BASE_COUNT));
 constexpr uint32_t kTmemSlotOff = kBarOff + B_COUNT * 8;
 constexpr uint32_t kAbortOff = kTmemSlotOff + 4;
 constexpr uint32_t kSmemUsed = kAbortOff + 4;
@@ -941,6 +951,10 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = 32 * (warp & 3) + lane;                // tile row = TMEM lane
     const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
+    // two groups: this thread's takes pages it of parity `grp`; both keep count of all
+    const int grp = kGroups > 1 && warp >= 8 ? 1 : 0;
+    const int chain_own = B_CHAIN + 8 * grp + 2 * (warp & 3), chain_peer = B_CHAIN + 8 * (grp ^ 1) + 2 * (warp & 3);
+    const uint32_t chain_s = smem_u32(c.base + kChainOff) + 4u * (uint32_t)r;
     int gr = tile * kTileRows + r;                       // row within the sequence's rows
     bool row_ok = gr < p.rows;
     int qi = row_ok ? gr / p.h_q : 0;                    // query token index
@@ -1028,7 +1042,7 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
                     }
                 };
 #pragma unroll 1
-                for (int ch = 0; ch < kKChunks; ++ch) {
+                for (int ch = grp; ch < kKChunks; ch += kGroups) {
                     // three chunks' loads per round (the first pass brought the row into L1)
                     uint4 x[8];
 #pragma unroll
@@ -1104,6 +1118,12 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
         float m = -CUDART_INF_F, l = 0.f;
         float ko = 0.f;  // fp8 P V: the power of two that O and P carry (0: every weight so far is 0)
         for (int pg = s.p0; pg < s.p1; ++pg, ++it) {
+            if (kGroups > 1 && (int)(it % kGroups) != grp) {  // the other group's page
+                ++step;
+                // Q may be replaced only when the segment's last MMAs are done
+                if (pg == s.p1 - 1 && !warp_wait(c, B_SFULL + (int)((step - 1) % kSBufs), ((step - 1) / kSBufs) & 1)) return;
+                continue;
+            }
             const int pb = it % kPBufs;
             const int q2 = (pg - s.p0) % kStepPages;  // position of this page in its step
             const int sb = step % kSBufs;
@@ -1146,8 +1166,12 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
             }
             // e4m3 cache: the page's per-token scales (those of keys past the
             // visible ones, whatever the page holds there, read as 0)
-            float cs[kFp8 ? kPage : 1];
-            if constexpr (kFp8) {
+            // (two groups: the row threads have fewer registers, and take the
+            // scales from shared memory where they are used)
+            constexpr bool kHoldScales = kFp8 && kGroups == 1;
+            const uint32_t cs_s = smem_u32(c.base + kScaleOff) + (uint32_t)scs * kScBytes;
+            float cs[kHoldScales ? kPage : 1];
+            if constexpr (kHoldScales) {
                 const uint32_t sc_s =
                     smem_u32(c.base + kScaleOff) + (uint32_t)scs * kScBytes + (uint32_t)q2 * kPage * 4;
 #pragma unroll
@@ -1168,10 +1192,25 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
             if (q2 == kStepPages - 1 || pg == s.p1 - 1) {  // last page of the step: release its S buffer
                 tc_fence_before();
                 mbar_arrive(c.bar(B_SEMPTY + sb));
-                if constexpr (kRing) mbar_arrive(c.bar(B_SCEMPTY + scs));  // the scales / masks are in registers
+                if constexpr (kRing && (!kFp8 || kHoldScales)) mbar_arrive(c.bar(B_SCEMPTY + scs));  // the scales / masks are in registers
                 ++step;
             }
-            if constexpr (kFp8) {
+            if constexpr (kFp8 && !kHoldScales) {
+                const uint64_t zero2 = f2_pack(0.f, 0.f);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const uint4 c4 = lds128(cs_s + 16 * j);
+                    float xa, xb;
+                    f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[4 * j]), __uint_as_float(sr[4 * j + 1])),
+                                     f2_pack(__uint_as_float(c4.x), __uint_as_float(c4.y)), zero2), xa, xb);
+                    sr[4 * j] = __float_as_uint(xa);
+                    sr[4 * j + 1] = __float_as_uint(xb);
+                    f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[4 * j + 2]), __uint_as_float(sr[4 * j + 3])),
+                                     f2_pack(__uint_as_float(c4.z), __uint_as_float(c4.w)), zero2), xa, xb);
+                    sr[4 * j + 2] = __float_as_uint(xa);
+                    sr[4 * j + 3] = __float_as_uint(xb);
+                }
+            } else if constexpr (kFp8) {
                 // score of key j times its token's scale: the dequantized key
                 const uint64_t zero2 = f2_pack(0.f, 0.f);
 #pragma unroll
@@ -1205,17 +1244,29 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
             for (int j = 0; j < 32; ++j)
                 mx4[j & 3] = max3f(mx4[j & 3], __uint_as_float(sr[2 * j]), __uint_as_float(sr[2 * j + 1]));
             const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * fsc;
+            if constexpr (kGroups > 1) {
+                // the running maximum after the page before, the other group's
+                if (it > 0 && !warp_wait(c, chain_peer, ((it - 1) / kGroups) & 1)) return;
+                m = pg == s.p0 ? -CUDART_INF_F : __uint_as_float(lds32(chain_s + (grp ^ 1) * kTileRows * 4));
+            }
             float fac = 1.f;
             if (mx > m + kRescaleLog2 || (m == -CUDART_INF_F && mx > -CUDART_INF_F)) {
                 fac = ex2(m - mx);  // 0 when m was -inf
                 m = mx;
+            }
+            if constexpr (kGroups > 1) {
+                sts32(chain_s + grp * kTileRows * 4, __float_as_uint(m));
+                mbar_arrive(c.bar(chain_own));
             }
             // exponent inputs and the row sum two lanes per instruction
             uint64_t sum2[4] = {0ull, 0ull, 0ull, 0ull};
             uint32_t pk[32];
             if (m == -CUDART_INF_F) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j) pk[j] = 0u;
+                for (int j = 0; j < 32; ++j) {
+                    pk[j] = 0u;
+                    if constexpr (kE8) sr[2 * j] = sr[2 * j + 1] = 0u;  // the weights
+                }
             } else {
                 const uint64_t sc2 = f2_pack(fsc, fsc), nm2 = f2_pack(-m, -m);
 #pragma unroll
@@ -1225,10 +1276,11 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
                     const float a = ex2(xa), b = ex2(xb);
                     sum2[j & 3] = f2_add(sum2[j & 3], f2_pack(a, b));
                     if constexpr (kE8) {
-                        // P of key j times its token's scale, kept in fp32
-                        // (in the score registers, which are read no more)
-                        float pa, pb2;
-                        f2_unpack(f2_fma(f2_pack(a, b), f2_pack(cs[2 * j], cs[2 * j + 1]), f2_pack(0.f, 0.f)), pa, pb2);
+                        // P of key j times its token's scale, kept in fp32 (in
+                        // the score registers, which are read no more)
+                        float ca, cb, pa, pb2;
+                        lds64f(cs_s + 8 * j, ca, cb);
+                        f2_unpack(f2_fma(f2_pack(a, b), f2_pack(ca, cb), f2_pack(0.f, 0.f)), pa, pb2);
                         sr[2 * j] = __float_as_uint(pa);
                         sr[2 * j + 1] = __float_as_uint(pb2);
                     } else if constexpr (kFp8) {
@@ -1245,7 +1297,17 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
             float sum_lo, sum_hi;
             f2_unpack(f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3])), sum_lo, sum_hi);
             const float sum = sum_lo + sum_hi;
+            if constexpr (kRing && kFp8 && !kHoldScales) mbar_arrive(c.bar(B_SCEMPTY + scs));  // the scales are in the weights
+            if constexpr (kGroups > 1) {
+                if (it > 0 && !warp_wait(c, chain_peer + 1, ((it - 1) / kGroups) & 1)) return;
+                l = pg == s.p0 ? 0.f : __uint_as_float(lds32(chain_s + (2 + (grp ^ 1)) * kTileRows * 4));
+                ko = pg == s.p0 ? 0.f : __uint_as_float(lds32(chain_s + (4 + (grp ^ 1)) * kTileRows * 4));
+            }
             l = l * fac + sum;
+            if (kE8 && vmask != ~0ull) {  // the scale of an invisible key may be anything, its weight is 0
+#pragma unroll
+                for (int j = 0; j < kPage; ++j) sr[j] = ((vmask >> j) & 1ull) ? sr[j] : 0u;
+            }
             if constexpr (kE8) {
                 // The weights w = P c as e4m3 need their place in its range: a
                 // power of two ko per row puts the largest at 56..112 when it is
@@ -1254,7 +1316,7 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
                 // so that what O holds would grow.  w ko is split into two e4m3
                 // parts (4 bits each, subtracted in f16, exactly): off by at most
                 // about 2^-8 of itself, or 2^-10 where the largest so far is at least 56.
-                if (m != -CUDART_INF_F) {
+                {
                     float wx[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
@@ -1267,6 +1329,9 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
                         if (ko != 0.f) fac *= kn / ko;
                         ko = kn;
                     }
+                    sts32(chain_s + (2 + grp) * kTileRows * 4, __float_as_uint(l));
+                    sts32(chain_s + (4 + grp) * kTileRows * 4, __float_as_uint(ko));
+                    mbar_arrive(c.bar(chain_own + 1));
                     const uint64_t ko2 = f2_pack(ko, ko), zero2 = f2_pack(0.f, 0.f);
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {  // keys 4 j .. 4 j + 3
@@ -1276,9 +1341,12 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
                             float wa, wb;
                             f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[4 * j + 2 * e]), __uint_as_float(sr[4 * j + 2 * e + 1])),
                                              ko2, zero2), wa, wb);
+                            // the upper 4 bits of w by w (2^7 + 1) - (w (2^7 + 1) - w)
                             const uint32_t w16 = pack_f16(wa, wb);
-                            hi[e] = pack_e4m3x2_f16(w16);
-                            lo[e] = pack_e4m3x2_f16(f16x2_sub(w16, e4m3x2_to_f16x2(hi[e])));
+                            const uint32_t t16 = f16x2_mul(w16, 0x58085808u);  // 129
+                            const uint32_t h16 = f16x2_sub(t16, f16x2_sub(t16, w16));
+                            hi[e] = pack_e4m3x2_f16(h16);
+                            lo[e] = pack_e4m3x2_f16(f16x2_sub(w16, h16));
                         }
                         pk[j] = hi[0] | (hi[1] << 16);
                         pk[16 + j] = lo[0] | (lo[1] << 16);
@@ -1314,8 +1382,9 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
                 if (last) bulk_copy_to_peer(dst + kInvLOff + fac_off, stage + kInvLOff + fac_off, 32 * 4, bar);
             }
         }
-        // LSE of this row over the segment (natural log)
-        if (row_ok) {
+        // LSE of this row over the segment (natural log), from the thread that had
+        // its last page
+        if (row_ok && (kGroups == 1 || (s.p1 > s.p0 ? (int)((it - 1) % kGroups) == grp : grp == 0))) {
             const float lse_row = l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : -CUDART_INF_F;
             if (s.n_split <= 1) {
                 p.lse[(size_t)s.b * p.rows + gr] = lse_row;
@@ -1558,12 +1627,14 @@ split_kv_tc_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_cons
                 mbar_init(c.bar(B_SCEMPTY + i), 128);
             }
             mbar_init(c.bar(B_VREAD), 128);
+            if constexpr (kGroups > 1)
+                for (int i = 0; i < 16; ++i) mbar_init(c.bar(B_CHAIN + i), 32);
         }
         for (int i = 0; i < kSBufs; ++i) {
             mbar_init(c.bar(B_SFULL + i), 1);
             mbar_init(c.bar(B_SEMPTY + i), 128);
         }
-        mbar_init(c.bar(B_QFULL), 128);
+        mbar_init(c.bar(B_QFULL), 128 * kGroups);
         mbar_init(c.bar(B_QACK), kScoreIssuers);  // every score-MMA issuer has seen a segment's Q
         for (int i = 0; i < kPBufs; ++i) {
             mbar_init(c.bar(B_PFREE + i), 1);
@@ -1619,7 +1690,7 @@ split_kv_tc_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_cons
         __syncwarp();
     } else {
         if (is_score) score_rows(p, c, tmem, part, tile);
-        else value_rows(p, c, tmem, part, tile);
+        else if (warp < 8) value_rows(p, c, tmem, part, tile);
     }
 
     tc_fence_before();
