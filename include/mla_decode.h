@@ -538,7 +538,9 @@ MLA_API size_t mla_tree_workspace_bytes(int batch, int s_q, int h_q, int h_kv, i
  *   tree_lens  device int32 [batch], 0 <= n_b <= s_q, or NULL: s_q everywhere.
  *              A value outside sets MLA_DEVERR_SEQLEN and is clamped
  *   tile_scheduler_metadata, num_splits, num_parts
- *              from mla_get_metadata_tree with the same lengths and tree lengths
+ *              from mla_get_metadata_tree with the same lengths and tree lengths;
+ *              both NULL: computed by this call, in the workspace, for num_parts
+ *              parts
  *   workspace  at least mla_tree_workspace_bytes(...) bytes, 256-byte aligned
  *   everything else as for mla_decode_kvcache (d = 576 or 512; no causal
  *   argument: a chain's mask is the causal one).  T_b < n_b drops the nodes that

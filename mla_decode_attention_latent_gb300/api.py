@@ -316,8 +316,32 @@ def mla_decode_kvcache_noalloc(q: torch.Tensor, kcache: torch.Tensor, block_tabl
     check("mla_decode_kvcache_noalloc", st)
 
 
+# Serving loops make the calls below once per layer and token, so the host's
+# share of a small call counts: the library's functions are looked up once, and
+# the device is switched only when it is not the current one.
+def _call(name: str, dev: torch.device, *args) -> None:
+    """Run a library call on ``dev`` and its current stream; raise on a bad status."""
+    fn = getattr(load(), name)
+    index = dev.index
+    if index == torch.cuda.current_device():
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if st != _lib.MLA_OK:
+        check(name, st)
+
+
+def _on(dev: torch.device, of: str, name: str, t: torch.Tensor, dtype: torch.dtype) -> int:
+    """Check a contiguous CUDA tensor on ``dev``; returns its address."""
+    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.device == dev and t.is_contiguous()):
+        _need_cuda(name, t, dtype)
+        _same_device(dev, of, **{name: t})
+    return t.data_ptr()
+
+
 # ---------------------------------------------------------------- cache rows
-def _need_rows(name: str, t: torch.Tensor, cols: int, written: bool) -> int:
+def _need_rows(name: str, t: torch.Tensor, cols: int, n: int, dev: torch.device, written: bool) -> int:
     """bf16 [n, cols] with unit inner stride, 16-byte aligned rows; returns the row stride in elements."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -325,80 +349,78 @@ def _need_rows(name: str, t: torch.Tensor, cols: int, written: bool) -> int:
         raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if t.dim() != 2 or t.shape[1] != cols or t.stride(1) != 1:
-        raise ValueError(f"{name} must be [rows, {cols}] with contiguous rows")
-    if t.shape[0] <= 1:
+    if t.device != dev:
+        _same_device(dev, "cache", **{name: t})
+    if t.dim() != 2 or t.shape[0] != n or t.shape[1] != cols:
+        raise ValueError(f"{name} must be [{n}, {cols}]")
+    stride, inner = t.stride()
+    if n <= 1:
         stride = cols
-    else:
-        stride = t.stride(0)
-        if stride % 8 or (written and stride < cols):
-            raise ValueError(f"{name}: the row stride must be a multiple of 8 elements"
-                             + (" and rows must not overlap" if written else ""))
+    if inner != 1 or stride % 8 or (written and stride < cols):
+        raise ValueError(f"{name}: rows must be contiguous, the row stride a multiple of 8 elements"
+                         + (" and rows must not overlap" if written else ""))
     if t.data_ptr() % 16:
         raise ValueError(f"{name} must be 16-byte aligned")
     return stride
 
 
 def _paged_args(cache, block_table, fp8):
-    """Check a paged cache and its table; returns (num_blocks, d)."""
-    _need_cuda("block_table", block_table, torch.int32)
-    if block_table.dim() != 2 or block_table.shape[0] < 1 or block_table.shape[1] < 1:
-        raise ValueError("block_table must be [b, max_blocks], neither of them 0")
+    """Check a paged cache and its table; returns (num_blocks, d, b, max_blocks, device, address of the table)."""
     if fp8:
         _need_cuda("kv_pages", cache, torch.uint8)
         d = _lib.MLA_HEAD_DIM
-        if cache.dim() != 2 or cache.shape[1] != _lib.MLA_FP8_PAGE_BYTES(d):
-            raise ValueError(f"kv_pages must be [num_blocks, {_lib.MLA_FP8_PAGE_BYTES(d)}]")
+        if cache.dim() != 2 or cache.shape[1] != _FP8_PAGE:
+            raise ValueError(f"kv_pages must be [num_blocks, {_FP8_PAGE}]")
+        num_blocks = cache.shape[0]
     else:
         _need_cuda("kcache", cache, torch.bfloat16)
-        if cache.dim() != 4 or cache.shape[1] != _lib.MLA_PAGE_SIZE or cache.shape[2] != 1:
+        if cache.dim() != 4:
             raise ValueError("kcache must be [num_blocks, 64, 1, d]")
-        d = cache.shape[3]
-    return cache.shape[0], d
+        num_blocks, page, h_kv, d = cache.shape
+        if page != _lib.MLA_PAGE_SIZE or h_kv != 1:
+            raise ValueError("kcache must be [num_blocks, 64, 1, d]")
+    dev = cache.device
+    table = _on(dev, "cache", "block_table", block_table, torch.int32)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [b, max_blocks]")
+    b, max_blocks = block_table.shape
+    if b < 1 or max_blocks < 1:
+        raise ValueError("block_table must be [b, max_blocks], neither of them 0")
+    return num_blocks, d, b, max_blocks, dev, table
 
 
-def _need_vector(name: str, t: torch.Tensor, n: int) -> None:
-    _need_cuda(name, t, torch.int32)
+_FP8_PAGE = _lib.MLA_FP8_PAGE_BYTES(_lib.MLA_HEAD_DIM)
+
+
+def _vector(dev: torch.device, of: str, name: str, t: torch.Tensor, n: int) -> int:
+    """Check an int32 [n] on ``dev``; returns its address."""
+    ptr = _on(dev, of, name, t, torch.int32)
     if t.dim() != 1 or t.shape[0] != n:
         raise ValueError(f"{name} must be [{n}]")
+    return ptr
 
 
 def _cache_rows(call, cache, block_table, starts, num_rows, cu_rows, latent, k_rope, fp8, write):
-    num_blocks, d = _paged_args(cache, block_table, fp8)
-    b, max_blocks = block_table.shape
-    dev = cache.device
-    _need_vector("starts", starts, b)
+    num_blocks, d, b, max_blocks, dev, table = _paged_args(cache, block_table, fp8)
+    st_ptr = _vector(dev, "cache", "starts", starts, b)
+    cu_ptr = None
     if cu_rows is not None:
-        _need_vector("cu_rows", cu_rows, b + 1)
+        cu_ptr = _vector(dev, "cache", "cu_rows", cu_rows, b + 1)
     elif num_rows % b:
         raise ValueError("without cu_rows every sequence has the same number of rows: b must divide them")
-    ls = _need_rows("latent", latent, MLA_V_DIM, not write)
-    if latent.shape[0] != num_rows:
-        raise ValueError(f"latent must have {num_rows} rows")
-    rope_dims = d - MLA_V_DIM
+    ls = _need_rows("latent", latent, MLA_V_DIM, num_rows, dev, not write)
     rs, rope_ptr = 0, None
-    if rope_dims > 0:
-        rs = _need_rows("k_rope", k_rope, rope_dims, not write)
-        if k_rope.shape[0] != num_rows:
-            raise ValueError(f"k_rope must have {num_rows} rows")
+    if d > MLA_V_DIM:
+        rs = _need_rows("k_rope", k_rope, d - MLA_V_DIM, num_rows, dev, not write)
         rope_ptr = k_rope.data_ptr()
-        _same_device(dev, "cache", k_rope=k_rope)
     elif k_rope is not None:
         raise ValueError("a cache of 512-wide rows has no RoPE part: k_rope must be None")
-    _same_device(dev, "cache", block_table=block_table, starts=starts, latent=latent)
-    if cu_rows is not None:
-        _same_device(dev, "cache", cu_rows=cu_rows)
-    cu_ptr = None if cu_rows is None else cu_rows.data_ptr()
-    with torch.cuda.device(dev):
-        if write:
-            st = getattr(load(), call)(latent.data_ptr(), ls, rope_ptr, rs, num_rows, cu_ptr, starts.data_ptr(), b,
-                                       cache.data_ptr(), num_blocks, block_table.data_ptr(), max_blocks, d,
-                                       _stream_handle(dev))
-        else:
-            st = getattr(load(), call)(cache.data_ptr(), num_blocks, block_table.data_ptr(), max_blocks,
-                                       starts.data_ptr(), cu_ptr, b, num_rows, latent.data_ptr(), ls, rope_ptr, rs, d,
-                                       _stream_handle(dev))
-    check(call, st)
+    if write:
+        _call(call, dev, latent.data_ptr(), ls, rope_ptr, rs, num_rows, cu_ptr, st_ptr, b, cache.data_ptr(), num_blocks,
+              table, max_blocks, d)
+    else:
+        _call(call, dev, cache.data_ptr(), num_blocks, table, max_blocks, st_ptr, cu_ptr, b, num_rows,
+              latent.data_ptr(), ls, rope_ptr, rs, d)
 
 
 def mla_cache_write(latent: torch.Tensor, k_rope: Optional[torch.Tensor], kcache: torch.Tensor,
@@ -422,10 +444,10 @@ def mla_cache_write_fp8(latent: torch.Tensor, k_rope: torch.Tensor, kv_pages: to
 
 
 def _cache_read(call, cache, block_table, starts, num_rows, cu_rows, latent, k_rope, fp8):
-    _, d = _paged_args(cache, block_table, fp8)
     num_rows = int(num_rows)
     if num_rows < 0:
         raise ValueError("num_rows must not be negative")
+    d = _paged_args(cache, block_table, fp8)[1] if latent is None or k_rope is None else 0
     if latent is None:
         latent = torch.empty((num_rows, MLA_V_DIM), dtype=torch.bfloat16, device=cache.device)
     if k_rope is None and d > MLA_V_DIM:
@@ -455,29 +477,21 @@ def mla_cache_read_fp8(kv_pages: torch.Tensor, block_table: torch.Tensor, starts
 
 
 # ---------------------------------------------------------------- page keys and page selection
-def _page_key_args(cache, num_blocks, d, page_keys, page_scales):
-    _need_cuda("page_keys", page_keys, torch.int8)
-    _need_cuda("page_scales", page_scales, torch.float32)
-    if tuple(page_keys.shape) != (num_blocks, d) or tuple(page_scales.shape) != (num_blocks,):
+def _page_key_args(dev, num_blocks, d, page_keys, page_scales):
+    """Check the page keys of a cache; returns their addresses."""
+    keys = _on(dev, "cache", "page_keys", page_keys, torch.int8)
+    scales = _on(dev, "cache", "page_scales", page_scales, torch.float32)
+    if page_keys.shape != (num_blocks, d) or page_scales.shape != (num_blocks,):
         raise ValueError(f"page_keys must be [{num_blocks}, {d}] and page_scales [{num_blocks}]")
-    _same_device(cache.device, "cache", page_keys=page_keys, page_scales=page_scales)
+    return keys, scales
 
 
 def _update_page_keys(call, cache, block_table, cache_seqlens, page_keys, page_scales, starts, fp8):
-    num_blocks, d = _paged_args(cache, block_table, fp8)
-    b, max_blocks = block_table.shape
-    dev = cache.device
-    _need_vector("cache_seqlens", cache_seqlens, b)
-    _page_key_args(cache, num_blocks, d, page_keys, page_scales)
-    _same_device(dev, "cache", block_table=block_table, cache_seqlens=cache_seqlens)
-    if starts is not None:
-        _need_vector("starts", starts, b)
-        _same_device(dev, "cache", starts=starts)
-    with torch.cuda.device(dev):
-        st = getattr(load(), call)(cache.data_ptr(), num_blocks, block_table.data_ptr(), max_blocks,
-                                   cache_seqlens.data_ptr(), None if starts is None else starts.data_ptr(), b, d,
-                                   page_keys.data_ptr(), page_scales.data_ptr(), _stream_handle(dev))
-    check(call, st)
+    num_blocks, d, b, max_blocks, dev, table = _paged_args(cache, block_table, fp8)
+    lens = _vector(dev, "cache", "cache_seqlens", cache_seqlens, b)
+    keys, scales = _page_key_args(dev, num_blocks, d, page_keys, page_scales)
+    st_ptr = None if starts is None else _vector(dev, "cache", "starts", starts, b)
+    _call(call, dev, cache.data_ptr(), num_blocks, table, max_blocks, lens, st_ptr, b, d, keys, scales)
 
 
 def mla_update_page_keys(kcache: torch.Tensor, block_table: torch.Tensor, cache_seqlens: torch.Tensor,
@@ -507,60 +521,52 @@ def mla_blocks_workspace_bytes(batch: int, s_q: int, h_q: int, h_kv: int, dv: in
 
 
 def _outputs(b, s_q, h_q, dv, dev, out, lse):
+    """The outputs of a decode, created where missing, and their addresses."""
     if out is None:
         out = torch.empty((b, s_q, h_q, dv), dtype=torch.bfloat16, device=dev)
+    elif out.shape != (b, s_q, h_q, dv):
+        raise ValueError("out must be [b, s_q, h_q, dv]")
     if lse is None:
         lse = torch.empty((b, s_q, h_q), dtype=torch.float32, device=dev)
-    _need_cuda("out", out, torch.bfloat16)
-    _need_cuda("lse", lse, torch.float32)
-    if tuple(out.shape) != (b, s_q, h_q, dv) or tuple(lse.shape) != (b, s_q, h_q):
-        raise ValueError("out must be [b, s_q, h_q, dv] and lse [b, s_q, h_q]")
-    return out, lse
+    elif lse.shape != (b, s_q, h_q):
+        raise ValueError("lse must be [b, s_q, h_q]")
+    return out, lse, _on(dev, "q", "out", out, torch.bfloat16), _on(dev, "q", "lse", lse, torch.float32)
 
 
 def _query_args(q, cache, block_table, cache_seqlens, fp8):
-    """Check the query against a paged cache; returns (b, s_q, h_q, d, num_blocks, max_blocks)."""
-    num_blocks, d = _paged_args(cache, block_table, fp8)
-    _need_cuda("q", q, torch.bfloat16)
-    if q.dim() != 4 or q.shape[3] != d:
-        raise ValueError(f"q must be [b, s_q, h_q, {d}]")
-    b, s_q, h_q, _ = q.shape
-    if block_table.shape[0] != b:
-        raise ValueError("batch size differs between q and block_table")
-    _need_vector("cache_seqlens", cache_seqlens, b)
-    return b, s_q, h_q, d, num_blocks, block_table.shape[1]
+    """Check the query against a paged cache; returns (b, s_q, h_q, d, num_blocks, max_blocks, device, addresses of
+    q, the table and the lengths)."""
+    num_blocks, d, b, max_blocks, dev, table = _paged_args(cache, block_table, fp8)
+    q_ptr = _on(dev, "the cache", "q", q, torch.bfloat16)
+    if q.dim() != 4 or q.shape[0] != b or q.shape[3] != d or q.shape[1] < 1 or q.shape[2] < 1:
+        raise ValueError(f"q must be [{b}, s_q, h_q, {d}]")
+    lens = _vector(dev, "q", "cache_seqlens", cache_seqlens, b)
+    return b, q.shape[1], q.shape[2], d, num_blocks, max_blocks, dev, q_ptr, table, lens
 
 
 def _decode_blocks(call, q, cache, block_table, cache_seqlens, page_keys, page_scales, topk_pages, dv, sink_pages,
                    local_pages, softmax_scale, causal, out, lse, pages, workspace, fp8):
-    b, s_q, h_q, d, num_blocks, max_blocks = _query_args(q, cache, block_table, cache_seqlens, fp8)
-    dev = q.device
-    _page_key_args(cache, num_blocks, d, page_keys, page_scales)
+    b, s_q, h_q, d, num_blocks, max_blocks, dev, q_ptr, table, lens = _query_args(q, cache, block_table, cache_seqlens, fp8)
+    keys, scales = _page_key_args(dev, num_blocks, d, page_keys, page_scales)
     topk_pages, sink_pages, local_pages = int(topk_pages), int(sink_pages), int(local_pages)
     if sink_pages < 0 or local_pages < 1 or topk_pages < sink_pages + local_pages:
         raise ValueError("topk_pages must cover sink_pages (>= 0) and local_pages (>= 1)")
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(d)
     num_parts = mla_num_sm_parts(1, 1, dev)
-    ws_need = mla_blocks_workspace_bytes(b, s_q, h_q, 1, dv, max_blocks, topk_pages, num_parts)
-    out, lse = _outputs(b, s_q, h_q, dv, dev, out, lse)
+    out, lse, o_ptr, lse_ptr = _outputs(b, s_q, h_q, dv, dev, out, lse)
     if pages is None:
         pages = torch.empty((b, s_q, topk_pages), dtype=torch.int32, device=dev)
-    _need_cuda("pages", pages, torch.int32)
-    if tuple(pages.shape) != (b, s_q, topk_pages):
+    elif pages.shape != (b, s_q, topk_pages):
         raise ValueError("pages must be [b, s_q, topk_pages]")
+    pages_ptr = _on(dev, "q", "pages", pages, torch.int32)
     if workspace is None:
-        workspace = torch.empty((ws_need,), dtype=torch.uint8, device=dev)
-    _need_cuda("workspace", workspace, torch.uint8)
-    _same_device(dev, cache=cache, block_table=block_table, cache_seqlens=cache_seqlens, out=out, lse=lse, pages=pages,
-                 workspace=workspace)
-    with torch.cuda.device(dev):
-        st = getattr(load(), call)(
-            q.data_ptr(), cache.data_ptr(), num_blocks, block_table.data_ptr(), max_blocks, cache_seqlens.data_ptr(),
-            page_keys.data_ptr(), page_scales.data_ptr(), topk_pages, sink_pages, local_pages, b, s_q, h_q, 1, d, dv,
-            num_parts, float(softmax_scale), int(bool(causal)), out.data_ptr(), lse.data_ptr(), pages.data_ptr(),
-            workspace.data_ptr(), workspace.numel(), _stream_handle(dev))
-    check(call, st)
+        need = mla_blocks_workspace_bytes(b, s_q, h_q, 1, dv, max_blocks, topk_pages, num_parts)
+        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+    ws_ptr = _on(dev, "q", "workspace", workspace, torch.uint8)
+    _call(call, dev, q_ptr, cache.data_ptr(), num_blocks, table, max_blocks, lens, keys, scales, topk_pages, sink_pages,
+          local_pages, b, s_q, h_q, 1, d, dv, num_parts, float(softmax_scale), int(bool(causal)), o_ptr, lse_ptr, pages_ptr,
+          ws_ptr, workspace.numel())
     return out, lse, pages
 
 
@@ -603,9 +609,7 @@ def mla_tree_mask(parents: torch.Tensor) -> torch.Tensor:
     b, s_q = parents.shape
     dev = parents.device
     mask = torch.empty((b, s_q, (s_q + 31) // 32), dtype=torch.int32, device=dev)
-    with torch.cuda.device(dev):
-        st = load().mla_tree_mask(parents.data_ptr(), b, s_q, mask.data_ptr(), _stream_handle(dev))
-    check("mla_tree_mask", st)
+    _call("mla_tree_mask", dev, parents.data_ptr(), b, s_q, mask.data_ptr())
     return mask
 
 
@@ -624,17 +628,13 @@ def mla_get_metadata_tree(cache_seqlens: torch.Tensor, s_q: int, h_q: int, tree_
     s_q, h_q = int(s_q), int(h_q)
     if b < 1 or s_q < 1 or h_q < 1:
         raise ValueError("cache_seqlens, s_q and h_q must not be empty or 0")
-    if tree_lens is not None:
-        _need_vector("tree_lens", tree_lens, b)
-        _same_device(dev, "cache_seqlens", tree_lens=tree_lens)
+    nodes = None if tree_lens is None else _vector(dev, "cache_seqlens", "tree_lens", tree_lens, b)
     if num_parts is None:
         num_parts = mla_num_sm_parts(1, 1, dev)
     md = torch.empty((num_parts, MLA_METADATA_INTS), dtype=torch.int32, device=dev)
     ns = torch.empty((b * _row_tiles(s_q, h_q) + 1,), dtype=torch.int32, device=dev)
-    with torch.cuda.device(dev):
-        st = load().mla_get_metadata_tree(cache_seqlens.data_ptr(), None if tree_lens is None else tree_lens.data_ptr(), b,
-                                          s_q, h_q, 1, int(num_parts), md.data_ptr(), ns.data_ptr(), _stream_handle(dev))
-    check("mla_get_metadata_tree", st)
+    _call("mla_get_metadata_tree", dev, cache_seqlens.data_ptr(), nodes, b, s_q, h_q, 1, int(num_parts), md.data_ptr(),
+          ns.data_ptr())
     return md, ns
 
 
@@ -647,40 +647,31 @@ def mla_tree_workspace_bytes(batch: int, s_q: int, h_q: int, h_kv: int, dv: int,
 
 def _decode_tree(call, q, cache, block_table, cache_seqlens, tree_mask, dv, tile_scheduler_metadata, num_splits,
                  tree_lens, softmax_scale, out, lse, workspace, fp8):
-    b, s_q, h_q, d, num_blocks, max_blocks = _query_args(q, cache, block_table, cache_seqlens, fp8)
-    dev = q.device
-    _need_cuda("tree_mask", tree_mask, torch.int32)
-    if tuple(tree_mask.shape) != (b, s_q, (s_q + 31) // 32):
+    b, s_q, h_q, d, num_blocks, max_blocks, dev, q_ptr, table, lens = _query_args(q, cache, block_table, cache_seqlens, fp8)
+    mask = _on(dev, "q", "tree_mask", tree_mask, torch.int32)
+    if tree_mask.shape != (b, s_q, (s_q + 31) // 32):
         raise ValueError("tree_mask must be [b, s_q, ceil(s_q / 32)]")
-    if tree_lens is not None:
-        _need_vector("tree_lens", tree_lens, b)
-        _same_device(dev, tree_lens=tree_lens)
+    nodes = None if tree_lens is None else _vector(dev, "q", "tree_lens", tree_lens, b)
+    md = ns = None
     if (tile_scheduler_metadata is None) != (num_splits is None):
         raise ValueError("tile_scheduler_metadata and num_splits come together")
     if tile_scheduler_metadata is None:
-        tile_scheduler_metadata, num_splits = mla_get_metadata_tree(cache_seqlens, s_q, h_q, tree_lens)
-    _need_cuda("tile_scheduler_metadata", tile_scheduler_metadata, torch.int32)
-    _need_vector("num_splits", num_splits, b * _row_tiles(s_q, h_q) + 1)
-    if tile_scheduler_metadata.dim() != 2 or tile_scheduler_metadata.shape[1] != MLA_METADATA_INTS:
-        raise ValueError("tile_scheduler_metadata must be [num_parts, 8]")
-    num_parts = tile_scheduler_metadata.shape[0]
+        num_parts = mla_num_sm_parts(1, 1, dev)
+    else:
+        md = _on(dev, "q", "tile_scheduler_metadata", tile_scheduler_metadata, torch.int32)
+        ns = _vector(dev, "q", "num_splits", num_splits, b * _row_tiles(s_q, h_q) + 1)
+        if tile_scheduler_metadata.dim() != 2 or tile_scheduler_metadata.shape[1] != MLA_METADATA_INTS:
+            raise ValueError("tile_scheduler_metadata must be [num_parts, 8]")
+        num_parts = tile_scheduler_metadata.shape[0]
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(d)
-    ws_need = mla_tree_workspace_bytes(b, s_q, h_q, 1, dv, num_parts)
-    out, lse = _outputs(b, s_q, h_q, dv, dev, out, lse)
+    out, lse, o_ptr, lse_ptr = _outputs(b, s_q, h_q, dv, dev, out, lse)
     if workspace is None:
-        workspace = torch.empty((ws_need,), dtype=torch.uint8, device=dev)
-    _need_cuda("workspace", workspace, torch.uint8)
-    _same_device(dev, cache=cache, block_table=block_table, cache_seqlens=cache_seqlens, tree_mask=tree_mask,
-                 tile_scheduler_metadata=tile_scheduler_metadata, num_splits=num_splits, out=out, lse=lse,
-                 workspace=workspace)
-    with torch.cuda.device(dev):
-        st = getattr(load(), call)(
-            q.data_ptr(), cache.data_ptr(), num_blocks, block_table.data_ptr(), max_blocks, cache_seqlens.data_ptr(),
-            tree_mask.data_ptr(), None if tree_lens is None else tree_lens.data_ptr(), b, s_q, h_q, 1, d, dv,
-            tile_scheduler_metadata.data_ptr(), num_splits.data_ptr(), num_parts, float(softmax_scale), out.data_ptr(),
-            lse.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream_handle(dev))
-    check(call, st)
+        need = mla_tree_workspace_bytes(b, s_q, h_q, 1, dv, num_parts)
+        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+    ws_ptr = _on(dev, "q", "workspace", workspace, torch.uint8)
+    _call(call, dev, q_ptr, cache.data_ptr(), num_blocks, table, max_blocks, lens, mask, nodes, b, s_q, h_q, 1, d, dv, md, ns,
+          num_parts, float(softmax_scale), o_ptr, lse_ptr, ws_ptr, workspace.numel())
     return out, lse
 
 

@@ -146,6 +146,19 @@ size_t mla_workspace_bytes(int batch, int s_q, int h_q, int h_kv, int dv, int nu
 
 namespace {
 
+// workspace of a draft-tree decode: the split-KV scratch, then room for the
+// partition when the caller brings none
+struct TreeLayout {
+    size_t metadata, splits, total;
+};
+TreeLayout tree_layout(int entries, int num_parts) {
+    TreeLayout l;
+    l.metadata = workspace_bytes(entries, kRowsPerTile, num_parts);
+    l.splits = l.metadata + align_up((size_t)num_parts * kMdInts * sizeof(int32_t));
+    l.total = l.splits + align_up(((size_t)entries + 1) * sizeof(int32_t));
+    return l;
+}
+
 enum class Kind { kBf16, kE4m3, kSparse };
 
 // Index lists of the sparse decode (unused otherwise).
@@ -250,6 +263,43 @@ int decode(const void *q, const void *kcache, Kind kind, int64_t num_blocks, con
 }  // namespace
 
 namespace mla {
+// A draft-tree call; without metadata the partition is computed here, in the
+// workspace.
+static int decode_tree(const void *q, const void *cache, Kind kind, int64_t num_blocks, const int32_t *block_table,
+                       int max_blocks, const int32_t *cache_seqlens, const int32_t *tree_mask, const int32_t *tree_lens,
+                       int batch, int s_q, int h_q, int h_kv, int d, int dv, const int32_t *metadata,
+                       const int32_t *num_splits, int num_parts, float softmax_scale, void *o, float *lse, void *workspace,
+                       size_t ws_bytes, struct CUstream_st *stream) {
+    if (!tree_mask || (metadata == nullptr) != (num_splits == nullptr)) return MLA_ERR_INVALID_ARG;
+    if (!metadata) {
+        // everything that the decode would refuse is refused before the partition is launched
+        if (!q || !cache || !block_table || !cache_seqlens || !o || !lse || !workspace) return MLA_ERR_INVALID_ARG;
+        if (batch < 1 || batch > 65535 || s_q < 1 || h_q < 1 || h_kv < 1 || num_blocks < 1 || max_blocks < 1 ||
+            num_parts < 1 || d < 1 || dv < 1 || !(softmax_scale == softmax_scale))
+            return MLA_ERR_INVALID_ARG;
+        if ((d != kDqk && (d != kDv || kind == Kind::kE4m3)) || dv != kDv || h_kv != 1) return MLA_ERR_UNSUPPORTED;
+        if ((long long)s_q * h_q > kMaxRows) return MLA_ERR_UNSUPPORTED;
+        if ((long long)max_blocks * kPage > 0x7fffffffLL) return MLA_ERR_INVALID_ARG;
+        if (!aligned16(q) || !aligned16(cache) || !aligned16(o) || !aligned16(workspace)) return MLA_ERR_INVALID_ARG;
+        const int tiles = (s_q * h_q + kRowsPerTile - 1) / kRowsPerTile;
+        if ((long long)batch * tiles > kMaxTreeEntries) return MLA_ERR_UNSUPPORTED;
+        const TreeLayout l = tree_layout(batch * tiles, num_parts);
+        if (ws_bytes < l.total) return MLA_ERR_WORKSPACE;
+        int32_t *md = reinterpret_cast<int32_t *>(static_cast<char *>(workspace) + l.metadata);
+        int32_t *ns = reinterpret_cast<int32_t *>(static_cast<char *>(workspace) + l.splits);
+        const int st = mla_get_metadata_tree(cache_seqlens, tree_lens, batch, s_q, h_q, h_kv, num_parts, md, ns, stream);
+        if (st != MLA_OK) return st;
+        metadata = md;
+        num_splits = ns;
+    }
+    Tree tree;
+    tree.tiled = true;
+    tree.mask = reinterpret_cast<const uint32_t *>(tree_mask);
+    tree.lens = tree_lens;
+    return decode(q, cache, kind, num_blocks, block_table, max_blocks, cache_seqlens, batch, s_q, h_q, h_kv, d, dv, metadata,
+                  num_splits, num_parts, softmax_scale, 0, o, lse, workspace, ws_bytes, stream, Lists(), tree);
+}
+
 int decode_tiled(const void *q, const void *cache, bool e4m3, int64_t num_blocks, const int32_t *block_table, int max_blocks,
                  const int32_t *seqlens, int batch, int h_q, int d, const int32_t *metadata, const int32_t *num_splits,
                  int num_parts, float softmax_scale, void *o, float *lse, void *workspace, size_t ws_bytes,
@@ -321,7 +371,7 @@ size_t mla_tree_workspace_bytes(int batch, int s_q, int h_q, int h_kv, int dv, i
     if ((long long)s_q * h_q > kMaxRows) return 0;
     const int tiles = (s_q * h_q + kRowsPerTile - 1) / kRowsPerTile;
     if ((long long)batch * tiles > kMaxTreeEntries) return 0;
-    return workspace_bytes(batch * tiles, kRowsPerTile, num_parts);
+    return tree_layout(batch * tiles, num_parts).total;
 }
 
 int mla_tree_mask(const int32_t *parents, int batch, int s_q, int32_t *tree_mask, struct CUstream_st *stream) {
@@ -341,14 +391,9 @@ int mla_decode_kvcache_tree(const void *q, const void *kcache, int64_t num_block
                             const int32_t *tile_scheduler_metadata, const int32_t *num_splits, int num_parts,
                             float softmax_scale, void *o, float *lse, void *workspace, size_t ws_bytes,
                             struct CUstream_st *stream) {
-    if (!tree_mask) return MLA_ERR_INVALID_ARG;
-    Tree tree;
-    tree.tiled = true;
-    tree.mask = reinterpret_cast<const uint32_t *>(tree_mask);
-    tree.lens = tree_lens;
-    return decode(q, kcache, Kind::kBf16, num_blocks, block_table, max_blocks_per_seq, cache_seqlens, batch, s_q, h_q,
-                  h_kv, d, dv, tile_scheduler_metadata, num_splits, num_parts, softmax_scale, 0, o, lse, workspace,
-                  ws_bytes, stream, Lists(), tree);
+    return decode_tree(q, kcache, Kind::kBf16, num_blocks, block_table, max_blocks_per_seq, cache_seqlens, tree_mask, tree_lens,
+                       batch, s_q, h_q, h_kv, d, dv, tile_scheduler_metadata, num_splits, num_parts, softmax_scale, o, lse,
+                       workspace, ws_bytes, stream);
 }
 
 int mla_decode_kvcache_tree_fp8(const void *q, const void *kv_pages, int64_t num_blocks, const int32_t *block_table,
@@ -357,14 +402,9 @@ int mla_decode_kvcache_tree_fp8(const void *q, const void *kv_pages, int64_t num
                                 const int32_t *tile_scheduler_metadata, const int32_t *num_splits, int num_parts,
                                 float softmax_scale, void *o, float *lse, void *workspace, size_t ws_bytes,
                                 struct CUstream_st *stream) {
-    if (!tree_mask) return MLA_ERR_INVALID_ARG;
-    Tree tree;
-    tree.tiled = true;
-    tree.mask = reinterpret_cast<const uint32_t *>(tree_mask);
-    tree.lens = tree_lens;
-    return decode(q, kv_pages, Kind::kE4m3, num_blocks, block_table, max_blocks_per_seq, cache_seqlens, batch, s_q, h_q,
-                  h_kv, d, dv, tile_scheduler_metadata, num_splits, num_parts, softmax_scale, 0, o, lse, workspace,
-                  ws_bytes, stream, Lists(), tree);
+    return decode_tree(q, kv_pages, Kind::kE4m3, num_blocks, block_table, max_blocks_per_seq, cache_seqlens, tree_mask, tree_lens,
+                       batch, s_q, h_q, h_kv, d, dv, tile_scheduler_metadata, num_splits, num_parts, softmax_scale, o, lse,
+                       workspace, ws_bytes, stream);
 }
 
 int mla_device_status(int *status, int clear) {

@@ -88,7 +88,7 @@ def test_blocks(lib, fp8, over, code):
 
 def test_blocks_workspace(lib):
     n = lib.mla_blocks_workspace_bytes(4, 2, 128, 1, 512, 100, 16, 76)
-    decode = lib.mla_tree_workspace_bytes(8, 1, 128, 1, 512, 76)
+    decode = (8 + 76) * 128 * 513 * 4
     assert n % 256 == 0 and n >= decode + 4 * 8 * 100 + 4 * 8 * 16 + 4 * 8 + 32 * 76 + 4 * 9
     for bad in ((0, 2, 128, 1, 512, 100, 16, 76), (4, 0, 128, 1, 512, 100, 16, 76), (4, 2, 0, 1, 512, 100, 16, 76),
                 (4, 2, 128, 2, 512, 100, 16, 76), (4, 2, 128, 1, 576, 100, 16, 76), (4, 2, 128, 1, 512, 0, 16, 76),
@@ -110,6 +110,12 @@ def tree(lib, fp8=False, **over):
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("over,code", [
     *[({k: None}, BAD) for k in ("q", "cache", "bt", "sl", "mask", "md", "ns", "o", "lse", "ws")],
+    # without a partition (the call makes its own) the same are refused, before it is launched
+    *[({k: None, "md": None, "ns": None}, BAD) for k in ("q", "cache", "bt", "sl", "mask", "o", "lse", "ws")],
+    *[({k: 0, "md": None, "ns": None}, BAD) for k in ("nblk", "mb", "b", "s", "h", "hkv", "d", "dv", "parts")],
+    *[({**v, "md": None, "ns": None}, c) for v, c in ((dict(scale=float("nan")), BAD), (dict(q=264), BAD), (dict(dv=256), UNSUP),
+                                                       (dict(hkv=2), UNSUP), (dict(d=448), UNSUP), (dict(s=8192, h=16), UNSUP),
+                                                       (dict(mb=1 << 25), BAD), (dict(b=65536), BAD), (dict(bytes=4096), WS))],
     *[({k: 0}, BAD) for k in ("nblk", "mb", "b", "s", "h", "hkv", "d", "dv", "parts")],
     (dict(scale=float("nan")), BAD), (dict(q=264), BAD), (dict(dv=256), UNSUP), (dict(hkv=2), UNSUP), (dict(d=448), UNSUP),
     (dict(s=8192, h=16), UNSUP), (dict(bytes=4096), WS)])
@@ -175,9 +181,9 @@ def test_tree_partition(lib):
         assert lib.mla_get_metadata_tree(*args, None) == code
     # a slot holds one 128-row tile: 3 tiles of 2 sequences, 5 parts
     n = lib.mla_tree_workspace_bytes(2, 3, 100, 1, 512, 5)
-    assert n % 256 == 0 and n >= (2 * 3 + 5) * 128 * 513 * 4 > n - 512
+    assert n % 256 == 0 and n >= (2 * 3 + 5) * 128 * 513 * 4 + 5 * 32 + 7 * 4 > n - 1024
     for bad in ((0, 3, 100, 1, 512, 5), (2, 0, 100, 1, 512, 5), (2, 3, 0, 1, 512, 5), (2, 3, 100, 2, 512, 5),
                 (2, 3, 100, 1, 576, 5), (2, 3, 100, 1, 512, 0), (2, 8192, 16, 1, 512, 5), (65535, 512, 128, 1, 512, 5)):
         assert lib.mla_tree_workspace_bytes(*bad) == 0
-    assert tree(lib, b=2, s=3, h=100, parts=5, bytes=n - 1) == WS
+    assert tree(lib, b=2, s=3, h=100, parts=5, md=None, ns=None, bytes=n - 1) == WS
     assert tree(lib, b=65535, s=512, h=128) == UNSUP
