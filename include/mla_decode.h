@@ -473,8 +473,8 @@ MLA_API size_t mla_blocks_workspace_bytes(int batch, int s_q, int h_q, int h_kv,
  *                  pages of each token (logical, ascending), -1 behind them
  *   workspace      device scratch of at least mla_blocks_workspace_bytes(...)
  *                  bytes, 256-byte aligned
- * Five kernels are enqueued on `stream` (scores, selection, partition, split-KV,
- * combine).  Stream order, graph capture, status bits and errors: as for
+ * Five kernels are enqueued on `stream` (query codes, scores, selection with the
+ * partition, split-KV, combine).  Stream order, graph capture, status bits and errors: as for
  * mla_decode_kvcache.
  */
 MLA_API int mla_decode_kvcache_blocks(const void *q, const void *kcache, int64_t num_blocks,

@@ -86,7 +86,7 @@ int update_page_keys(const void *cache, int64_t num_blocks, const int32_t *block
 
 // workspace of a page-selecting decode: the selection's arrays, then the decode's
 struct BlocksLayout {
-    size_t scores, table, lens, metadata, splits, decode, total;
+    size_t codes, units, scores, table, lens, metadata, splits, decode, total;
 };
 
 BlocksLayout blocks_layout(int tokens, int h_q, int max_blocks, int topk, int num_parts) {
@@ -97,6 +97,8 @@ BlocksLayout blocks_layout(int tokens, int h_q, int max_blocks, int topk, int nu
         at += align_up(bytes);
         return here;
     };
+    l.codes = take((size_t)tokens * h_q * kDqk);
+    l.units = take((size_t)tokens * h_q * sizeof(float));
     l.scores = take((size_t)tokens * max_blocks * sizeof(float));
     l.table = take((size_t)tokens * topk * sizeof(int32_t));
     l.lens = take((size_t)tokens * sizeof(int32_t));
@@ -146,18 +148,23 @@ int decode_blocks(const void *q, const void *cache, int64_t num_blocks, const in
     p.sink = sink;
     p.local = local;
     p.causal = causal != 0;
+    p.q_codes = reinterpret_cast<int8_t *>(ws + l.codes);
+    p.q_units = reinterpret_cast<float *>(ws + l.units);
     p.scores = reinterpret_cast<float *>(ws + l.scores);
     p.sel_table = reinterpret_cast<int32_t *>(ws + l.table);
     p.sel_lens = reinterpret_cast<int32_t *>(ws + l.lens);
     p.pages = pages;
+    p.num_parts = num_parts;
+    p.metadata = reinterpret_cast<int32_t *>(ws + l.metadata);
+    p.num_splits = reinterpret_cast<int32_t *>(ws + l.splits);
     if (status_address(&p.status) != MLA_OK) return MLA_ERR_CUDA;
-    if (launch_select_pages(p, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return MLA_ERR_CUDA;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    // without more pages than topk there is nothing to score
+    if (max_blocks > topk && launch_page_scores(p, s) != cudaSuccess) return MLA_ERR_CUDA;
+    if (launch_select_pages(p, s) != cudaSuccess) return MLA_ERR_CUDA;
     // one "sequence" per query token over its own block table
-    int32_t *md = reinterpret_cast<int32_t *>(ws + l.metadata), *ns = reinterpret_cast<int32_t *>(ws + l.splits);
-    st = mla_get_metadata_tree(p.sel_lens, nullptr, tokens, 1, h_q, 1, num_parts, md, ns, stream);
-    if (st != MLA_OK) return st;
-    return decode_tiled(q, cache, e4m3, num_blocks, p.sel_table, topk, p.sel_lens, tokens, h_q, d, md, ns, num_parts,
-                        softmax_scale, o, lse, ws + l.decode, ws_bytes - l.decode, stream);
+    return decode_tiled(q, cache, e4m3, num_blocks, p.sel_table, topk, p.sel_lens, tokens, h_q, d, p.metadata, p.num_splits,
+                        num_parts, softmax_scale, o, lse, ws + l.decode, ws_bytes - l.decode, stream);
 }
 
 }  // namespace

@@ -81,7 +81,8 @@ struct PageKeysParams {
     unsigned int *status;
 };
 
-// One call that scores the pages of each query token and selects topk of them.
+// One call that scores the pages of each query token, selects topk of them and
+// partitions the decode over the selection.
 struct SelectParams {
     const uint16_t *q;            // [batch][s_q][h_q][d] bf16
     const int8_t *keys;           // [num_blocks][d]
@@ -93,10 +94,15 @@ struct SelectParams {
     int batch, s_q, h_q, d;
     int topk, sink, local;
     int causal;
+    int8_t *q_codes;              // workspace [batch * s_q][h_q][d]: the heads, quantised
+    float *q_units;               // workspace [batch * s_q][h_q]: their scales
     float *scores;                // workspace [batch * s_q][max_blocks]
     int32_t *sel_table;           // workspace [batch * s_q][topk]: physical pages, the block table of the decode
     int32_t *sel_lens;            // workspace [batch * s_q]: lengths over the selected pages
     int32_t *pages;               // [batch][s_q][topk], out: logical pages, ascending, -1 behind them
+    int num_parts;                // of the decode's work partition
+    int32_t *metadata;            // workspace [num_parts][8]
+    int32_t *num_splits;          // workspace [batch * s_q * row tiles + 1]
     unsigned int *status;
 };
 
@@ -132,6 +138,7 @@ cudaError_t launch_split_kv_tc_tree(const DecodeParams &p, cudaStream_t stream);
 
 cudaError_t launch_cache_rows(const CacheRowsParams &p, int d, bool e4m3, bool write, cudaStream_t stream);
 cudaError_t launch_page_keys(const PageKeysParams &p, int d, bool e4m3, cudaStream_t stream);
+cudaError_t launch_page_scores(const SelectParams &p, cudaStream_t stream);
 cudaError_t launch_select_pages(const SelectParams &p, cudaStream_t stream);
 cudaError_t launch_tree_mask(const int32_t *parents, int batch, int s_q, uint32_t *mask, unsigned int *status,
                              cudaStream_t stream);
