@@ -31,12 +31,13 @@ namespace {
 
 using namespace sm103;
 
-constexpr int kScoreThreads = 256;
+constexpr int kScoreThreads = 256;            // 8 warps that stage keys and read products
+constexpr int kCtaThreads = kScoreThreads + 32;  // and one that issues the MMAs
 constexpr int kTilePages = 128;               // rows of an MMA = TMEM lanes
 constexpr int kHeadChunk = 128;               // heads of an MMA
 constexpr int kStages = 4;
 constexpr uint32_t kTileBytes = 128 * 128;    // 128 rows of 64 f16
-constexpr uint32_t kTmemCols = 128;
+constexpr uint32_t kTmemCols = 256;           // two accumulators
 
 template <int D>
 struct ScoreSmem {
@@ -45,12 +46,12 @@ struct ScoreSmem {
     static constexpr uint32_t a = q + kChunks * kTileBytes;           // [stage][page][64] f16
     static constexpr uint32_t unit = a + kStages * kTileBytes;        // [head] u_h
     static constexpr uint32_t best = unit + kHeadChunk * 4;           // [page] maximum of the upper heads
-    static constexpr uint32_t bars = best + kTilePages * 4;           // stage barriers, done barrier
-    static constexpr uint32_t tmem = bars + (kStages + 1) * 8;
+    static constexpr uint32_t bars = best + kTilePages * 4;           // B_* below
+    static constexpr uint32_t tmem = bars + (2 * kStages + 4) * 8;
     static constexpr uint32_t bad = tmem + 4;                         // the token holds a NaN or an infinity
     static constexpr uint32_t first = bad + 4;                        // the CTA's first unit: {sequence, unit in it}
     static constexpr uint32_t scan = (first + 8 + 15) & ~15u;         // [9] long long
-    static constexpr uint32_t total = scan + 9 * 8;
+    static constexpr uint32_t total = scan + (kCtaThreads / 32) * 8;
 };
 
 // int8 codes (four per word) to f16 values: a byte b + 128 in the low bits of
@@ -110,8 +111,44 @@ __global__ void __launch_bounds__(kQuantWarps * 32) quantise_heads_kernel(const 
     if (lane == 0) p.q_units[row] = u;
 }
 
+// barriers: stage staged (256 arrivals) / free (commit), accumulator finished
+// (commit) / read (256 arrivals)
+enum { B_FULL = 0, B_EMPTY = kStages, B_DONE = 2 * kStages, B_READ = 2 * kStages + 2, B_ALL = 2 * kStages + 4 };
+
+// The MMA issuer (one thread): for every job, the chunks in order.  A wait
+// that gave up leaves `ok` false; the loops go on without waiting or issuing, so
+// that every thread reaches the kernel's end.
 template <int D>
-__global__ void __launch_bounds__(kScoreThreads, 1) page_scores_kernel(const SelectParams p) {
+__device__ void score_issuer(const SelectParams &p, uint32_t base_s, uint64_t *bars, uint32_t tmem, long long jobs) {
+    using S = ScoreSmem<D>;
+    uint32_t fill = 0;
+    bool ok = true;
+    const int passes = (p.h_q + kHeadChunk - 1) / kHeadChunk;
+    for (long long j = 0; j < jobs; ++j) {
+        const int heads = min(kHeadChunk, p.h_q - (int)(j % passes) * kHeadChunk);
+        const uint32_t idesc = idesc_f16(kTilePages, (heads + 15) & ~15, false, false);
+        const uint32_t buf = (uint32_t)(j & 1), d = tmem + buf * 128;
+        if (ok) ok = mbar_wait(bars + B_READ + buf, (uint32_t)((j >> 1) & 1) ^ 1u, p.status);
+        tc_fence_after();
+        for (int c = 0; c < S::kChunks; ++c, ++fill) {
+            const uint32_t st = fill % kStages;
+            if (ok) ok = mbar_wait(bars + B_FULL + st, (fill / kStages) & 1, p.status);
+            if (!ok) continue;
+            const uint64_t ad = desc_sw128(base_s + S::a + st * kTileBytes, 16, 1024);
+            const uint64_t bd = desc_sw128(base_s + S::q + c * kTileBytes, 16, 1024);
+#pragma unroll
+            for (int s = 0; s < 4; ++s) mma_ss(d, ad + 2 * s, bd + 2 * s, idesc, c > 0 || s > 0);
+            mma_commit(bars + B_EMPTY + st);
+            if (c == S::kChunks - 1) mma_commit(bars + B_DONE + buf);
+        }
+    }
+    // everything issued has finished before the tensor memory goes (after a wait
+    // that gave up, long ago: MMAs take microseconds, the limit is seconds)
+    if (ok && jobs > 0) mbar_wait(bars + B_DONE + (uint32_t)((jobs - 1) & 1), (uint32_t)(((jobs - 1) >> 1) & 1), p.status);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kCtaThreads, 1) page_scores_kernel(const SelectParams p) {
     using S = ScoreSmem<D>;
     constexpr int kChunks = S::kChunks;
     extern __shared__ uint8_t smem_raw[];
@@ -121,11 +158,12 @@ __global__ void __launch_bounds__(kScoreThreads, 1) page_scores_kernel(const Sel
     float *s_unit = reinterpret_cast<float *>(base + S::unit), *s_best = reinterpret_cast<float *>(base + S::best);
     volatile int *s_bad = reinterpret_cast<volatile int *>(base + S::bad);
     int *s_first = reinterpret_cast<int *>(base + S::first);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int row = tid & 127, half = tid >> 7;  // the thread's page, and its half of every 64 dims and of the heads
+    const int tid = threadIdx.x, warp = tid >> 5;
+    const int row = tid & 127, half = (tid >> 7) & 1;  // the thread's page, and its half of the heads
 
     if (tid == 0) {
-        for (int i = 0; i <= kStages; ++i) mbar_init(bars + i, 1);
+        for (int i = 0; i < B_ALL; ++i)
+            mbar_init(bars + i, (i >= B_EMPTY && i < B_READ) ? 1 : kScoreThreads);
         fence_mbar_init();
     }
     if (warp == 0) {
@@ -147,11 +185,11 @@ __global__ void __launch_bounds__(kScoreThreads, 1) page_scores_kernel(const Sel
         return n > p.topk ? (long long)p.s_q * ((n + kTilePages - 1) / kTilePages) : 0;
     };
     // this CTA's range of all units, and where it starts
-    const int chunk = (p.batch + kScoreThreads - 1) / kScoreThreads;
+    const int chunk = (p.batch + kCtaThreads - 1) / kCtaThreads;
     const int i0 = min(tid * chunk, p.batch), i1 = min(i0 + chunk, p.batch);
     long long mine = 0, total;
     for (int i = i0; i < i1; ++i) mine += units(i);
-    long long at = block_exclusive_scan<kScoreThreads>(mine, reinterpret_cast<long long *>(base + S::scan), &total);
+    long long at = block_exclusive_scan<kCtaThreads>(mine, reinterpret_cast<long long *>(base + S::scan), &total);
     const long long share = (total + gridDim.x - 1) / gridDim.x;
     const long long u0 = share * blockIdx.x, u1 = min(u0 + share, total);
     if (u0 >= at && u0 < at + mine) {
@@ -188,164 +226,202 @@ __global__ void __launch_bounds__(kScoreThreads, 1) page_scores_kernel(const Sel
         }
         set_token(u);
     };
-    // the thread's part of its page's key, 32 bytes of every 64 dims, and the scale
+    // The thread's part of the unit's keys: of every 64 dims, 16 bytes of rows
+    // srow and srow + 64 (four neighbouring lanes read 64 contiguous bytes); and
+    // the scale of its own page.  A page that is not there reads block 0's key
+    // (its score goes nowhere, or, for a bad block id, is any number).  The block
+    // ids are looked up a unit ahead of the keys, and the keys a unit ahead of
+    // their use, so that no load waits for another.
+    const int srow = (tid & 255) >> 2, quarter = tid & 3;
     uint4 key[kChunks][2];
     float scale = 0.f;
-    auto load_keys = [&](const UnitAt &u) {
-        const int page = u.tile * kTilePages + row;
+    struct Blocks {
+        int s0, s1, own;
+    };
+    auto block_of = [&](const UnitAt &u, int r) {
+        const int page = u.tile * kTilePages + r;
+        return page < u.n ? __ldg(p.block_table + (size_t)u.b * p.max_blocks + page) : 0;
+    };
+    auto look_up = [&](const UnitAt &u) { return Blocks{block_of(u, srow), block_of(u, srow + 64), block_of(u, row)}; };
+    auto load_keys = [&](Blocks b) {
+        if (b.own < 0 || (int64_t)b.own >= p.num_blocks) atomicOr(p.status, MLA_DEVERR_BLOCK_ID);
+        auto safe = [&](int blk) { return blk < 0 || (int64_t)blk >= p.num_blocks ? 0 : blk; };
+        const uint4 *s0 = reinterpret_cast<const uint4 *>(p.keys + (size_t)safe(b.s0) * D) + quarter;
+        const uint4 *s1 = reinterpret_cast<const uint4 *>(p.keys + (size_t)safe(b.s1) * D) + quarter;
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c) key[c][0] = key[c][1] = make_uint4(0, 0, 0, 0);
-        scale = 0.f;
-        if (page < u.n) {
-            const int blk = p.block_table[(size_t)u.b * p.max_blocks + page];
-            if (blk < 0 || (int64_t)blk >= p.num_blocks) {
-                atomicOr(p.status, MLA_DEVERR_BLOCK_ID);
-            } else {
-                const uint4 *src = reinterpret_cast<const uint4 *>(p.keys + (size_t)blk * D) + 2 * half;
-#pragma unroll
-                for (int c = 0; c < kChunks; ++c) {
-                    key[c][0] = __ldg(src + 4 * c);
-                    key[c][1] = __ldg(src + 4 * c + 1);
-                }
-                scale = __ldg(p.scales + blk);
-            }
+        for (int c = 0; c < kChunks; ++c) {
+            key[c][0] = __ldg(s0 + 4 * c);
+            key[c][1] = __ldg(s1 + 4 * c);
         }
+        scale = __ldg(p.scales + safe(b.own));
     };
     // codes of heads h0 .. h0 + heads - 1 of a token, widened into shared memory
     auto load_heads = [&](const UnitAt &u, int h0, int heads) {
         constexpr int kPieces = D / 16;  // 16-code pieces of a row
-        constexpr int kItems = 128 * kPieces / kScoreThreads;
+        constexpr int kItems = 128 * kPieces / kScoreThreads, kBatch = kItems / 2;  // loads in flight: half of them
+        static_assert(kItems % 2 == 0, "two batches");
         const size_t first = ((size_t)u.b * p.s_q + u.tok) * p.h_q + h0;
         if (tid == 0 && h0 == 0) *s_bad = 0;
-        uint4 x[kItems];
-#pragma unroll
-        for (int i = 0; i < kItems; ++i) {
-            const int item = tid + i * kScoreThreads;
-            x[i] = item < heads * kPieces ? reinterpret_cast<const uint4 *>(p.q_codes + first * D)[item] : make_uint4(0, 0, 0, 0);
-        }
         const float un = tid < heads ? p.q_units[first + tid] : 1.f;
-        __syncthreads();
-        if (tid < heads) {
-            s_unit[tid] = un;
+        named_bar_sync(1, kScoreThreads);  // s_bad is cleared, and what the heads before left is read
+        if (tid < kHeadChunk) {
+            // a product with NaN never is the maximum: the columns behind the heads drop out
+            s_unit[tid] = tid < heads ? un : __uint_as_float(0x7fffffffu);
             if (un != un) *s_bad = 1;
         }
+#pragma unroll 1
+        for (int i0 = 0; i0 < kItems; i0 += kBatch) {
+            uint4 x[kBatch];
 #pragma unroll
-        for (int i = 0; i < kItems; ++i) {
-            const int item = tid + i * kScoreThreads, h = item / kPieces, piece = 2 * (item - h * kPieces);
-            uint32_t w[8];
-            widen4(x[i].x, w[0], w[1]);
-            widen4(x[i].y, w[2], w[3]);
-            widen4(x[i].z, w[4], w[5]);
-            widen4(x[i].w, w[6], w[7]);
-            const uint32_t dst = base_s + S::q + (uint32_t)(piece >> 3) * kTileBytes + 128u * (uint32_t)h;
-            sts128(dst + 16u * (uint32_t)((piece & 7) ^ (h & 7)), w[0], w[1], w[2], w[3]);
-            sts128(dst + 16u * (uint32_t)(((piece & 7) + 1) ^ (h & 7)), w[4], w[5], w[6], w[7]);
+            for (int i = 0; i < kBatch; ++i) {
+                const int item = tid + (i0 + i) * kScoreThreads;
+                x[i] = item < heads * kPieces ? reinterpret_cast<const uint4 *>(p.q_codes + first * D)[item]
+                                              : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int item = tid + (i0 + i) * kScoreThreads, h = item / kPieces, piece = 2 * (item - h * kPieces);
+                uint32_t w[8];
+                widen4(x[i].x, w[0], w[1]);
+                widen4(x[i].y, w[2], w[3]);
+                widen4(x[i].z, w[4], w[5]);
+                widen4(x[i].w, w[6], w[7]);
+                const uint32_t dst = base_s + S::q + (uint32_t)(piece >> 3) * kTileBytes + 128u * (uint32_t)h;
+                sts128(dst + 16u * (uint32_t)((piece & 7) ^ (h & 7)), w[0], w[1], w[2], w[3]);
+                sts128(dst + 16u * (uint32_t)(((piece & 7) + 1) ^ (h & 7)), w[4], w[5], w[6], w[7]);
+            }
         }
     };
 
-    UnitAt u{};
-    if (todo > 0) {
-        u.b = s_first[0];
-        load_seq(u);
-        u.tok = s_first[1] / u.tiles;
-        u.tile = s_first[1] - u.tok * u.tiles;
-        set_token(u);
-        load_keys(u);
-    }
-    griddep_wait();  // the heads' codes; writes to memory start behind it too
-    int held_b = -1, held_tok = -1, held_h = -1;  // whose heads are in shared memory
-    uint32_t fill = 0, done = 0;                  // chunks staged, products finished
-    bool ok = true;
-    for (int k = 0; k < todo && ok; ++k) {
-        float best = -__uint_as_float(0x7f800000u);
-        const float my_scale = scale;
+    const int passes = (p.h_q + kHeadChunk - 1) / kHeadChunk;  // jobs of a unit: its heads, 128 at a time
+    if (warp == kScoreThreads / 32) {
+        if (elect_one_lane()) score_issuer<D>(p, base_s, bars, tmem, (long long)todo * passes);
+    } else {
+        UnitAt u{};
+        if (todo > 0) {
+            u.b = s_first[0];
+            load_seq(u);
+            u.tok = s_first[1] / u.tiles;
+            u.tile = s_first[1] - u.tok * u.tiles;
+            set_token(u);
+            load_keys(look_up(u));
+        }
+        // the unit after this one, and its block ids
         UnitAt next = u;
-        if (k + 1 < todo) advance(next);
-        for (int h0 = 0; h0 < p.h_q && ok; h0 += kHeadChunk) {
-            const int heads = min(kHeadChunk, p.h_q - h0);
-            if (held_b != u.b || held_tok != u.tok || held_h != h0) {
-                load_heads(u, h0, heads);  // (the products of the heads before are finished)
-                held_b = u.b;
-                held_tok = u.tok;
-                held_h = h0;
-            }
-            const uint32_t idesc = idesc_f16(kTilePages, (heads + 15) & ~15, false, false);
-#pragma unroll
-            for (int c = 0; c < kChunks; ++c) {
-                const uint32_t st = fill % kStages;
-                if (ok) ok = mbar_wait(bars + st, ((fill / kStages) & 1) ^ 1, p.status);
-                const uint32_t dst = base_s + S::a + st * kTileBytes + 128u * (uint32_t)row;
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const uint4 x = key[c][j];
-                    uint32_t w[8];
-                    widen4(x.x, w[0], w[1]);
-                    widen4(x.y, w[2], w[3]);
-                    widen4(x.z, w[4], w[5]);
-                    widen4(x.w, w[6], w[7]);
-                    const uint32_t piece = 4u * (uint32_t)half + 2u * (uint32_t)j;
-                    sts128(dst + 16u * (piece ^ (uint32_t)(row & 7)), w[0], w[1], w[2], w[3]);
-                    sts128(dst + 16u * ((piece + 1) ^ (uint32_t)(row & 7)), w[4], w[5], w[6], w[7]);
-                }
-                fence_proxy_async_smem();
-                ok = __syncthreads_and(ok) != 0;
-                if (tid == 0 && ok) {
-                    tc_fence_after();
-                    const uint64_t ad = desc_sw128(base_s + S::a + st * kTileBytes, 16, 1024);
-                    const uint64_t bd = desc_sw128(base_s + S::q + c * kTileBytes, 16, 1024);
-#pragma unroll
-                    for (int s = 0; s < 4; ++s) mma_ss(tmem, ad + 2 * s, bd + 2 * s, idesc, c > 0 || s > 0);
-                    mma_commit(bars + st);
-                    if (c == kChunks - 1) mma_commit(bars + kStages);
-                }
-                ++fill;
-            }
-            // the next unit's keys travel while the products finish and are read
-            if (k + 1 < todo && h0 + kHeadChunk >= p.h_q) load_keys(next);
-            if (ok) ok = mbar_wait(bars + kStages, done & 1, p.status);
-            ok = __syncthreads_and(ok) != 0;
-            if (!ok) break;
-            ++done;
+        Blocks next_blocks{0, 0, 0};
+        if (todo > 1) {
+            advance(next);
+            next_blocks = look_up(next);
+        }
+        griddep_wait();  // the heads' codes; the scores are written behind it too
+        bool ok = true;
+        float best = -__uint_as_float(0x7f800000u);
+        // The products of job j are read after job j + 1 is staged, or before the
+        // heads are replaced: `late` is what that needs.
+        struct Late {
+            int heads = 0;        // 0: nothing to read
+            bool last = false;    // the unit's last heads: its scores are complete
+            long long job = 0;
+            float scale = 0.f;
+            float *out = nullptr;
+        } late;
+        auto read_products = [&] {
+            if (late.heads == 0) return;
+            const uint32_t buf = (uint32_t)(late.job & 1);
+            if (ok) ok = mbar_wait(bars + B_DONE + buf, (uint32_t)((late.job >> 1) & 1), p.status);
             tc_fence_after();
-            const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+            const uint32_t lanes = tmem + buf * 128 + ((uint32_t)(32 * (warp & 3)) << 16);
 #pragma unroll
             for (int c0 = 0; c0 < 64; c0 += 32) {
                 const int col = 64 * half + c0;
-                if (col < heads) {
+                if (col < late.heads) {
                     uint32_t v[32];
                     tmem_ld32(lanes + (uint32_t)col, v);
                     tmem_wait_ld();
-                    if (col + 32 <= heads) {
+                    const uint32_t un = base_s + S::unit + 4u * (uint32_t)col;
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) best = fmaxf(best, __fmul_rn(s_unit[col + j], __uint_as_float(v[j])));
-                    } else {
+                    for (int j = 0; j < 32; j += 4) {
+                        const uint4 w = lds128(un + 4 * j);
+                        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (col + j < heads) best = fmaxf(best, __fmul_rn(s_unit[col + j], __uint_as_float(v[j])));
+                        for (int e = 0; e < 4; ++e)
+                            best = fmaxf(best, __fmul_rn(__uint_as_float(ws[e]), __uint_as_float(v[j + e])));
                     }
                 }
             }
             tc_fence_before();
-            __syncthreads();  // the accumulator and the heads may be replaced
-            tc_fence_after();
+            mbar_arrive(bars + B_READ + buf);
+            if (late.last) {
+                if (half) s_best[row] = best;
+                const bool bad = *s_bad != 0;
+                named_bar_sync(1, kScoreThreads);
+                if (!half && late.out) {
+                    best = fmaxf(best, s_best[row]);
+                    *late.out = bad ? __uint_as_float(0x7fffffffu) : __fmul_rn(best, late.scale);
+                }
+                named_bar_sync(1, kScoreThreads);  // s_best may be written again
+                best = -__uint_as_float(0x7f800000u);
+            }
+            late.heads = 0;
+        };
+        int held_b = -1, held_tok = -1, held_h = -1;  // whose heads are in shared memory
+        uint32_t fill = 0;
+        long long job = 0;
+        for (int k = 0; k < todo; ++k) {
+            const int page = u.tile * kTilePages + row;
+            const float my_scale = scale;
+            UnitAt after = next;
+            Blocks after_blocks{0, 0, 0};
+            for (int h0 = 0; h0 < p.h_q; h0 += kHeadChunk, ++job) {
+                const int heads = min(kHeadChunk, p.h_q - h0);
+                if (held_b != u.b || held_tok != u.tok || held_h != h0) {
+                    read_products();  // waits for the products that use the heads in place
+                    load_heads(u, h0, heads);
+                    held_b = u.b;
+                    held_tok = u.tok;
+                    held_h = h0;
+                }
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c, ++fill) {
+                    const uint32_t st = fill % kStages;
+                    if (ok) ok = mbar_wait(bars + B_EMPTY + st, ((fill / kStages) & 1) ^ 1, p.status);
+                    const uint32_t dst = base_s + S::a + st * kTileBytes + 128u * (uint32_t)srow;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const uint4 x = key[c][j];
+                        uint32_t w[8];
+                        widen4(x.x, w[0], w[1]);
+                        widen4(x.y, w[2], w[3]);
+                        widen4(x.z, w[4], w[5]);
+                        widen4(x.w, w[6], w[7]);
+                        const uint32_t piece = 2u * (uint32_t)quarter, at = dst + 64u * 128u * (uint32_t)j;
+                        sts128(at + 16u * (piece ^ (uint32_t)(srow & 7)), w[0], w[1], w[2], w[3]);
+                        sts128(at + 16u * ((piece + 1) ^ (uint32_t)(srow & 7)), w[4], w[5], w[6], w[7]);
+                    }
+                    fence_proxy_async_smem();  // these and the heads, before the MMAs that the arrival lets go
+                    mbar_arrive(bars + B_FULL + st);
+                }
+                // the next unit's keys travel while products finish and are read
+                if (h0 + kHeadChunk >= p.h_q && k + 1 < todo) {
+                    load_keys(next_blocks);
+                    if (k + 2 < todo) {
+                        advance(after);
+                        after_blocks = look_up(after);
+                    }
+                }
+                read_products();
+                late.heads = heads;
+                late.last = h0 + kHeadChunk >= p.h_q;
+                late.job = job;
+                late.scale = my_scale;
+                late.out = page < u.n ? p.scores + ((size_t)u.b * p.s_q + u.tok) * p.max_blocks + page : nullptr;
+            }
+            u = next;
+            next = after;
+            next_blocks = after_blocks;
         }
-        if (!ok) break;
-        if (half) s_best[row] = best;
-        const bool bad = *s_bad != 0;
-        __syncthreads();
-        const int page = u.tile * kTilePages + row;
-        if (!half && page < u.n) {
-            best = fmaxf(best, s_best[row]);
-            p.scores[((size_t)u.b * p.s_q + u.tok) * p.max_blocks + page] =
-                bad ? __uint_as_float(0x7fffffffu) : __fmul_rn(best, my_scale);
-        }
-        u = next;
+        read_products();
     }
-    // the last products have finished (they were waited for); a wait that gave up
-    // leaves at most what this CTA staged, which its own barriers still count
-    if (!ok && tid == 0)
-        for (uint32_t f = fill > (uint32_t)kStages ? fill - kStages : 0; f < fill; ++f)
-            mbar_wait(bars + f % kStages, (f / kStages) & 1, p.status);
     tc_fence_before();
     __syncthreads();
     if (warp == 0) {
@@ -387,8 +463,8 @@ cudaError_t launch_page_scores(const SelectParams &p, cudaStream_t stream) {
     e = p.d == kDqk ? launch_after(quantise_heads_kernel<kDqk>, qgrid, qblock, 0, stream, p)
                     : launch_after(quantise_heads_kernel<kDv>, qgrid, qblock, 0, stream, p);
     if (e != cudaSuccess) return e;
-    return p.d == kDqk ? launch_after(page_scores_kernel<kDqk>, dim3(grid), dim3(kScoreThreads), score_smem<kDqk>(), stream, p)
-                       : launch_after(page_scores_kernel<kDv>, dim3(grid), dim3(kScoreThreads), score_smem<kDv>(), stream, p);
+    return p.d == kDqk ? launch_after(page_scores_kernel<kDqk>, dim3(grid), dim3(kCtaThreads), score_smem<kDqk>(), stream, p)
+                       : launch_after(page_scores_kernel<kDv>, dim3(grid), dim3(kCtaThreads), score_smem<kDv>(), stream, p);
 }
 
 }  // namespace mla
