@@ -372,7 +372,8 @@ MLA_API int mla_cache_write(const void *latent, int64_t latent_stride, const voi
  * mla_cache_write_fp8 — the same into packed e4m3 pages, quantised per token
  * (d = 576 only; the page layout of mla_decode_kvcache_fp8):
  *   c_j = max |x| / 448 over the row (1 for a row of zeros), code = e4m3(x / c_j)
- * with both quotients in fp32 (IEEE) and round to nearest even.  A row whose
+ * with both quotients in fp32 (IEEE) and round to nearest even; a zero's code is
+ * +0.  A row whose
  * scale reaches MLA_FP8_SCALE_LIMIT, or that holds a NaN or an infinity (its
  * scale becomes NaN), sets MLA_DEVERR_SCALE: the decode would report it too.
  */

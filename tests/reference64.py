@@ -32,7 +32,8 @@ def quantised_row(x: torch.Tensor):
     """(codes uint8 [d], scale fp32) of one row of bf16 values."""
     amax = x.float().abs().max()
     c = amax / torch.tensor(448.0) if amax > 0 else torch.tensor(1.0)
-    return (x.float() / c).to(torch.float8_e4m3fn).view(torch.uint8), c
+    code = (x.float() / c).to(torch.float8_e4m3fn).view(torch.uint8)
+    return torch.where(x == 0, torch.zeros_like(code), code), c  # a zero's code is +0
 
 
 def page_key(rows: torch.Tensor):

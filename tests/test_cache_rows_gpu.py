@@ -325,3 +325,29 @@ def test_page_keys_report_bad_lengths_and_blocks(dev):
         mla.mla_update_page_keys(cache, tb.to(dev), i32(lens, dev), keys, scales)
         assert mla.mla_device_status() == status
         assert float(scales[int(table[0, 0])]) > 0
+
+
+@pytest.mark.parametrize("exponent", [40, 120, 127, 134, 140])
+def test_codes_of_every_value(dev, exponent):
+    """Every significand of the row's largest value with every bf16 value of the 12 octaves below it, among them all
+    quotients that lie on or next to a rounding border: the codes are those of the division."""
+    amax = torch.tensor([(exponent << 7) | m for m in range(128)], dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+    values = torch.arange((exponent - 12) << 7, (exponent + 1) << 7, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+    rows = []
+    for m in range(128):
+        v = values[values.float() <= amax[m].float()]
+        v = torch.cat([v, -v])
+        v = torch.cat([v, v[:(-v.numel()) % 575]]).view(-1, 575)
+        rows.append(torch.cat([amax[m].expand(v.shape[0], 1), v], 1))
+    x = torch.cat(rows)
+    blocks = (x.shape[0] + 63) // 64
+    cache = torch.zeros((blocks, _lib.MLA_FP8_PAGE_BYTES(576)), dtype=torch.uint8, device=dev)
+    xd = x.to(dev)
+    mla.mla_cache_write_fp8(xd[:, :512], xd[:, 512:], cache, torch.arange(blocks, dtype=torch.int32, device=dev)[None],
+                            i32([0], dev))
+    scale = x[:, 0].float() / torch.tensor(448.0)
+    want = (x.float() / scale[:, None]).to(torch.float8_e4m3fn).view(torch.uint8)
+    got = cache.cpu()
+    assert torch.equal(got[:, 64 * 576:].contiguous().view(torch.float32).view(-1)[:x.shape[0]], scale)
+    assert torch.equal(got[:, :64 * 576].reshape(-1, 576)[:x.shape[0]], want)
+    assert mla.mla_device_status() in (0, _lib.MLA_DEVERR_SCALE)
