@@ -131,9 +131,9 @@ static_assert(!(kSparse && kFp8) && (!kSparse || MLA_SPLIT_D == 576), "sparse de
 constexpr bool kRing = kFp8 || kSparse;          // a per-step side ring (e4m3: token scales; sparse: key masks)
 
 // 8 warps: TMA, MMA, 4 row warps, second score MMA issuer and TMA producer; fp8
-// products: 4 more row warps in the score CTA, the two groups alternating pages
-constexpr int kThreads = kE8 ? 384 : 256;
-constexpr int kGroups = kE8 ? 2 : 1;           // row-warp groups of the score CTA
+// products: 8 more row warps in the score CTA, the three groups taking turns
+constexpr int kThreads = kE8 ? 512 : 256;
+constexpr int kGroups = kE8 ? 3 : 1;           // row-warp groups of the score CTA
 constexpr int kTileRows = 128;                 // query rows per tile = TMEM lanes
 constexpr int kScoreIssuers = 2;               // score-CTA MMA issuers (and TMA producers), alternating steps
 // Pages per score step: two for bf16 rows (one tcgen05 MMA with N = 128
@@ -151,8 +151,8 @@ constexpr int kStepPages = (kFp8 || kSparse) ? 1 : 2;
 constexpr int kKSlots = kFp8 ? 4 : (kSparse ? 2 : 10);
 constexpr int kRingSlots = kKSlots / kScoreIssuers;  // slots per score-MMA issuer's ring
 constexpr int kVStages = kE8 ? 4 : 2;          // value CTA ring: whole pages (dims 0..511)
-constexpr int kSBufs = 2;                      // S buffers in TMEM (score CTA), one per step
-constexpr int kPBufs = 2;                      // P buffers (staging in the score CTA, landing in the value CTA)
+constexpr int kSBufs = kE8 ? 3 : 2;            // S buffers in TMEM (score CTA), one per step
+constexpr int kPBufs = kE8 ? 3 : 2;                      // P buffers (staging in the score CTA, landing in the value CTA)
 constexpr int kKChunks = kD / 64;              // 9 (or 8) chunks of 64 dims (128 B rows)
 constexpr int kVChunks = kDv / 64;             // 8
 constexpr int kLatChunks = kDv / 64;           // 8 latent chunks: the Q part kept in TMEM
@@ -202,10 +202,10 @@ constexpr uint32_t kQRopeOff = kKRingOff + (kSparse ? kVStages * kVStageBytes : 
 constexpr uint32_t kQRopePartBytes = kTileRows * (kFp8 ? 64 : 128);  // one part's [128 rows] RoPE tile
 constexpr uint32_t kStageOff = kQRopeOff + (kQRopeSmem ? kQParts * kQRopePartBytes : 0);
 constexpr uint32_t kScaleOff = kStageOff + kPBufs * kPMsgBytes;   // the side ring of the steps in flight
-// two groups: the running state that one leaves for the other's next page,
-// [maximum 2 x 128][row sum 2 x 128][weight scale 2 x 128] fp32
+// several groups: the running state that each leaves for the next page's,
+// [group][maximum, row sum, weight scale][128 rows] fp32
 constexpr uint32_t kChainOff = kScaleOff + (kRing ? kScSlots * kScBytes : 0);
-constexpr uint32_t kScoreEnd = kChainOff + (kGroups > 1 ? 6 * kTileRows * 4 : 0);
+constexpr uint32_t kScoreEnd = kChainOff + (kGroups > 1 ? kGroups * 3 * kTileRows * 4 : 0);
 // value CTA: [V ring 2 x 64 KB (sparse: the page buffers)][P landing 2 x 17 KB][epilogue staging 34 KB]
 constexpr uint32_t kVRingOff = 0;
 constexpr uint32_t kPBufOff = kVRingOff + kVStages * kVStageBytes;
@@ -217,13 +217,17 @@ static_assert(kQRopeOff % 1024 == 0 && kStageOff % 1024 == 0 && kPBufOff % 1024 
                   kSlotBytes % 1024 == 0,
               "swizzled tiles need 1 KB alignment");
 
+// P V done: one barrier, or with more than two P buffers one per buffer (a row
+// warp that has page it's P knows that the P V of page it - kPBufs is done; the
+// parity it waits for must not be that of a phase before)
+constexpr int kPVBars = kPBufs > 2 ? kPBufs : 1;
 enum Bar {
     // score CTA
     B_KFULL = 0, B_KEMPTY = B_KFULL + kKSlots, B_SFULL = B_KEMPTY + kKSlots, B_SEMPTY = B_SFULL + kSBufs,
     B_QFULL = B_SEMPTY + kSBufs, B_QACK = B_QFULL + 1, B_PFREE = B_QACK + 1,
     // value CTA
     B_VFULL = B_PFREE + kPBufs, B_VEMPTY = B_VFULL + kVStages, B_PFULL = B_VEMPTY + kVStages,
-    B_PREADY = B_PFULL + kPBufs, B_PVDONE = B_PREADY + kPBufs, B_ODONE = B_PVDONE + 1, B_OEMPTY = B_ODONE + 1,
+    B_PREADY = B_PFULL + kPBufs, B_PVDONE = B_PREADY + kPBufs, B_ODONE = B_PVDONE + kPVBars, B_OEMPTY = B_ODONE + 1,
     // both
     B_FINAL = B_OEMPTY + 1, B_BASE_COUNT = B_FINAL + 1
 };
@@ -236,17 +240,17 @@ constexpr int B_VLAND = B_BASE_COUNT, B_SCFULL = B_VLAND + kVStages, B_SCEMPTY =
 // offset in both CTAs, so that the score MMAs can start on a page's first
 // chunks while the rest are still being gathered
 constexpr int B_CHUNK = B_VREAD + 1;
-// two groups: [group][warp of the group] x {maximum, sum and scale} left for the
-// other group's warp of the same rows (32 arrivals each)
+// several groups: [group][warp of the group] state left for the next group's warp
+// of the same rows (32 arrivals)
 constexpr int B_CHAIN = B_VREAD + 1;
 constexpr int B_COUNT = kSparse ? B_CHUNK + kVStages * kKChunks
-                                : (kGroups > 1 ? B_CHAIN + 16 : (kRing ? B_VREAD + 1 : B_BASE_COUNT));
+                                : (kGroups > 1 ? B_CHAIN + 4 * kGroups : (kRing ? B_VREAD + 1 : B_BASE_COUNT));
 constexpr uint32_t kTmemSlotOff = kBarOff + B_COUNT * 8;
 constexpr uint32_t kAbortOff = kTmemSlotOff + 4;
 constexpr uint32_t kSmemUsed = kAbortOff + 4;
 constexpr size_t kSmemBytes = kSmemUsed + 1024;  // + alignment slack of the dynamic base
 static_assert(kSmemBytes <= 232448, "shared memory per CTA");
-static_assert(kRingSlots * kScoreIssuers == kKSlots && kSBufs % kScoreIssuers == 0, "one K ring per score-MMA issuer");
+static_assert(kRingSlots * kScoreIssuers == kKSlots && (kE8 || kSBufs % kScoreIssuers == 0), "one K ring per score-MMA issuer");
 
 // -------------------------------------------------------------- work walk
 struct Segment {
@@ -937,7 +941,7 @@ __device__ void value_mma(const DecodeParams &p, const Ctx &c, uint32_t tmem, in
                     mma_ss(tmem + h * 256, ad, bd, idesc, (pg > s.p0 || k > 0) ? 1u : 0u);
                 }
             mma_commit(c.bar(B_VEMPTY + st));
-            mma_commit(c.bar(B_PVDONE));
+            mma_commit(c.bar(B_PVDONE + (kPVBars > 1 ? pb : 0)));
             if (pg == s.p1 - 1) mma_commit(c.bar(B_ODONE));  // O of the segment is complete
             mma_commit_multicast(c.bar(B_PFREE + pb), (uint16_t)(1u << c.peer));
         }
@@ -951,10 +955,6 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = 32 * (warp & 3) + lane;                // tile row = TMEM lane
     const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
-    // two groups: this thread's takes pages it of parity `grp`; both keep count of all
-    const int grp = kGroups > 1 && warp >= 8 ? 1 : 0;
-    const int chain_own = B_CHAIN + 8 * grp + 2 * (warp & 3), chain_peer = B_CHAIN + 8 * (grp ^ 1) + 2 * (warp & 3);
-    const uint32_t chain_s = smem_u32(c.base + kChainOff) + 4u * (uint32_t)r;
     int gr = tile * kTileRows + r;                       // row within the sequence's rows
     bool row_ok = gr < p.rows;
     int qi = row_ok ? gr / p.h_q : 0;                    // query token index
@@ -1003,9 +1003,6 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
                     }
                 }
                 qsig = amax > 0.f ? amax / kE4Max : 1.f;
-                // fp8 on both sides: the next power of two, so that q / qsig keeps
-                // its 8 bits and two parts of 4 bits hold them all
-                if constexpr (kE8) qsig = __uint_as_float((__float_as_uint(qsig) + 0x7fffffu) & 0x7f800000u);
                 const float inv = 1.f / qsig;
                 // one 64-dim chunk: three parts of 16 words (four codes each)
                 auto split = [&](const uint4 (&x)[8], uint32_t (&ph)[16], uint32_t (&pm)[16], uint32_t (&pl)[16]) {
@@ -1020,12 +1017,12 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
                                 v[2 * e] = __uint_as_float(w4[2 * hw + e] << 16) * inv;
                                 v[2 * e + 1] = __uint_as_float(w4[2 * hw + e] & 0xffff0000u) * inv;
                             }
-                            uint32_t code[3] = {0u, 0u, 0u};
+                            uint32_t code[3];
 #pragma unroll
-                            for (int t = 0; t < kQParts; ++t) {
+                            for (int t = 0; t < 3; ++t) {
                                 const uint32_t c01 = pack_e4m3x2(v[0], v[1]), c23 = pack_e4m3x2(v[2], v[3]);
                                 code[t] = c01 | (c23 << 16);
-                                if (t < kQParts - 1) {
+                                if (t < 2) {
                                     float d0, d1, d2, d3;
                                     f16x2_to_f32(e4m3x2_to_f16x2(c01), d0, d1);
                                     f16x2_to_f32(e4m3x2_to_f16x2(c23), d2, d3);
@@ -1042,7 +1039,7 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
                     }
                 };
 #pragma unroll 1
-                for (int ch = grp; ch < kKChunks; ch += kGroups) {
+                for (int ch = 0; ch < kKChunks; ++ch) {
                     // three chunks' loads per round (the first pass brought the row into L1)
                     uint4 x[8];
 #pragma unroll
@@ -1055,10 +1052,10 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
                     }
                     uint32_t ph[16], pm[16], pl[16];
                     split(x, ph, pm, pl);
-                    if (!kQRopeSmem || ch < kLatChunks) {
+                    if (ch < kLatChunks) {
                         tmem_st16(tmem + lane_base + 0 * kQPartCols + ch * 16, ph);
                         tmem_st16(tmem + lane_base + 1 * kQPartCols + ch * 16, pm);
-                        if constexpr (kQParts > 2) tmem_st16(tmem + lane_base + 2 * kQPartCols + ch * 16, pl);
+                        tmem_st16(tmem + lane_base + 2 * kQPartCols + ch * 16, pl);
                     } else {
                         // 64 B per row; 16-byte piece q of row r at q ^ ((r >> 1) & 3)
                         const uint32_t rope = smem_u32(c.base + kQRopeOff) + (uint32_t)r * 64u;
@@ -1116,14 +1113,7 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
         mbar_arrive(c.bar(B_QFULL));
 
         float m = -CUDART_INF_F, l = 0.f;
-        float ko = 0.f;  // fp8 P V: the power of two that O and P carry (0: every weight so far is 0)
         for (int pg = s.p0; pg < s.p1; ++pg, ++it) {
-            if (kGroups > 1 && (int)(it % kGroups) != grp) {  // the other group's page
-                ++step;
-                // Q may be replaced only when the segment's last MMAs are done
-                if (pg == s.p1 - 1 && !warp_wait(c, B_SFULL + (int)((step - 1) % kSBufs), ((step - 1) / kSBufs) & 1)) return;
-                continue;
-            }
             const int pb = it % kPBufs;
             const int q2 = (pg - s.p0) % kStepPages;  // position of this page in its step
             const int sb = step % kSBufs;
@@ -1166,12 +1156,8 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
             }
             // e4m3 cache: the page's per-token scales (those of keys past the
             // visible ones, whatever the page holds there, read as 0)
-            // (two groups: the row threads have fewer registers, and take the
-            // scales from shared memory where they are used)
-            constexpr bool kHoldScales = kFp8 && kGroups == 1;
-            const uint32_t cs_s = smem_u32(c.base + kScaleOff) + (uint32_t)scs * kScBytes;
-            float cs[kHoldScales ? kPage : 1];
-            if constexpr (kHoldScales) {
+            float cs[kFp8 ? kPage : 1];
+            if constexpr (kFp8) {
                 const uint32_t sc_s =
                     smem_u32(c.base + kScaleOff) + (uint32_t)scs * kScBytes + (uint32_t)q2 * kPage * 4;
 #pragma unroll
@@ -1182,35 +1168,19 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
                     cs[4 * j + 2] = __uint_as_float(c4.z);
                     cs[4 * j + 3] = __uint_as_float(c4.w);
                 }
-                if (kTree ? vmask != ~0ull : nvalid < kPage) {
+                if (nvalid < kPage) {
 #pragma unroll
-                    for (int j = 0; j < kPage; ++j)
-                        cs[j] = (kTree ? ((vmask >> j) & 1ull) != 0 : j < nvalid) ? cs[j] : 0.f;
+                    for (int j = 0; j < kPage; ++j) cs[j] = j < nvalid ? cs[j] : 0.f;
                 }
             }
             tmem_wait_ld();
             if (q2 == kStepPages - 1 || pg == s.p1 - 1) {  // last page of the step: release its S buffer
                 tc_fence_before();
                 mbar_arrive(c.bar(B_SEMPTY + sb));
-                if constexpr (kRing && (!kFp8 || kHoldScales)) mbar_arrive(c.bar(B_SCEMPTY + scs));  // the scales / masks are in registers
+                if constexpr (kRing) mbar_arrive(c.bar(B_SCEMPTY + scs));  // the scales / masks are in registers
                 ++step;
             }
-            if constexpr (kFp8 && !kHoldScales) {
-                const uint64_t zero2 = f2_pack(0.f, 0.f);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const uint4 c4 = lds128(cs_s + 16 * j);
-                    float xa, xb;
-                    f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[4 * j]), __uint_as_float(sr[4 * j + 1])),
-                                     f2_pack(__uint_as_float(c4.x), __uint_as_float(c4.y)), zero2), xa, xb);
-                    sr[4 * j] = __float_as_uint(xa);
-                    sr[4 * j + 1] = __float_as_uint(xb);
-                    f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[4 * j + 2]), __uint_as_float(sr[4 * j + 3])),
-                                     f2_pack(__uint_as_float(c4.z), __uint_as_float(c4.w)), zero2), xa, xb);
-                    sr[4 * j + 2] = __float_as_uint(xa);
-                    sr[4 * j + 3] = __float_as_uint(xb);
-                }
-            } else if constexpr (kFp8) {
+            if constexpr (kFp8) {
                 // score of key j times its token's scale: the dequantized key
                 const uint64_t zero2 = f2_pack(0.f, 0.f);
 #pragma unroll
@@ -1244,29 +1214,17 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
             for (int j = 0; j < 32; ++j)
                 mx4[j & 3] = max3f(mx4[j & 3], __uint_as_float(sr[2 * j]), __uint_as_float(sr[2 * j + 1]));
             const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * fsc;
-            if constexpr (kGroups > 1) {
-                // the running maximum after the page before, the other group's
-                if (it > 0 && !warp_wait(c, chain_peer, ((it - 1) / kGroups) & 1)) return;
-                m = pg == s.p0 ? -CUDART_INF_F : __uint_as_float(lds32(chain_s + (grp ^ 1) * kTileRows * 4));
-            }
             float fac = 1.f;
             if (mx > m + kRescaleLog2 || (m == -CUDART_INF_F && mx > -CUDART_INF_F)) {
                 fac = ex2(m - mx);  // 0 when m was -inf
                 m = mx;
-            }
-            if constexpr (kGroups > 1) {
-                sts32(chain_s + grp * kTileRows * 4, __float_as_uint(m));
-                mbar_arrive(c.bar(chain_own));
             }
             // exponent inputs and the row sum two lanes per instruction
             uint64_t sum2[4] = {0ull, 0ull, 0ull, 0ull};
             uint32_t pk[32];
             if (m == -CUDART_INF_F) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    pk[j] = 0u;
-                    if constexpr (kE8) sr[2 * j] = sr[2 * j + 1] = 0u;  // the weights
-                }
+                for (int j = 0; j < 32; ++j) pk[j] = 0u;
             } else {
                 const uint64_t sc2 = f2_pack(fsc, fsc), nm2 = f2_pack(-m, -m);
 #pragma unroll
@@ -1275,15 +1233,7 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
                     f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[2 * j]), __uint_as_float(sr[2 * j + 1])), sc2, nm2), xa, xb);
                     const float a = ex2(xa), b = ex2(xb);
                     sum2[j & 3] = f2_add(sum2[j & 3], f2_pack(a, b));
-                    if constexpr (kE8) {
-                        // P of key j times its token's scale, kept in fp32 (in
-                        // the score registers, which are read no more)
-                        float ca, cb, pa, pb2;
-                        lds64f(cs_s + 8 * j, ca, cb);
-                        f2_unpack(f2_fma(f2_pack(a, b), f2_pack(ca, cb), f2_pack(0.f, 0.f)), pa, pb2);
-                        sr[2 * j] = __float_as_uint(pa);
-                        sr[2 * j + 1] = __float_as_uint(pb2);
-                    } else if constexpr (kFp8) {
+                    if constexpr (kFp8) {
                         // P of key j times its token's scale: the dequantized value row
                         float pa, pb2;
                         f2_unpack(f2_fma(f2_pack(a, b), f2_pack(cs[2 * j], cs[2 * j + 1]), f2_pack(0.f, 0.f)), pa,
@@ -1297,62 +1247,7 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
             float sum_lo, sum_hi;
             f2_unpack(f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3])), sum_lo, sum_hi);
             const float sum = sum_lo + sum_hi;
-            if constexpr (kRing && kFp8 && !kHoldScales) mbar_arrive(c.bar(B_SCEMPTY + scs));  // the scales are in the weights
-            if constexpr (kGroups > 1) {
-                if (it > 0 && !warp_wait(c, chain_peer + 1, ((it - 1) / kGroups) & 1)) return;
-                l = pg == s.p0 ? 0.f : __uint_as_float(lds32(chain_s + (2 + (grp ^ 1)) * kTileRows * 4));
-                ko = pg == s.p0 ? 0.f : __uint_as_float(lds32(chain_s + (4 + (grp ^ 1)) * kTileRows * 4));
-            }
             l = l * fac + sum;
-            if (kE8 && vmask != ~0ull) {  // the scale of an invisible key may be anything, its weight is 0
-#pragma unroll
-                for (int j = 0; j < kPage; ++j) sr[j] = ((vmask >> j) & 1ull) ? sr[j] : 0u;
-            }
-            if constexpr (kE8) {
-                // The weights w = P c as e4m3 need their place in its range: a
-                // power of two ko per row puts the largest at 56..112 when it is
-                // set; it is set anew when a page's largest would pass 448, and
-                // with every new running maximum (which shrinks P itself), never
-                // so that what O holds would grow.  w ko is split into two e4m3
-                // parts (4 bits each, subtracted in f16, exactly): off by at most
-                // about 2^-8 of itself, or 2^-10 where the largest so far is at least 56.
-                {
-                    float wx[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        wx[j & 3] = max3f(wx[j & 3], fabsf(__uint_as_float(sr[2 * j])), fabsf(__uint_as_float(sr[2 * j + 1])));
-                    const float wmax = fmaxf(fmaxf(wx[0], wx[1]), fmaxf(wx[2], wx[3]));
-                    if (wmax > 0.f && (wmax * ko > kE4Max || fac != 1.f || ko == 0.f)) {
-                        float kn = fminf(kE4Max / 4.f / wmax, 0x1p100f);
-                        if (ko != 0.f) kn = fminf(kn, ko / fac);  // fac kn / ko <= 1 (fac = 0: no limit)
-                        kn = __uint_as_float(__float_as_uint(kn) & 0x7f800000u);
-                        if (ko != 0.f) fac *= kn / ko;
-                        ko = kn;
-                    }
-                    sts32(chain_s + (2 + grp) * kTileRows * 4, __float_as_uint(l));
-                    sts32(chain_s + (4 + grp) * kTileRows * 4, __float_as_uint(ko));
-                    mbar_arrive(c.bar(chain_own + 1));
-                    const uint64_t ko2 = f2_pack(ko, ko), zero2 = f2_pack(0.f, 0.f);
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {  // keys 4 j .. 4 j + 3
-                        uint32_t hi[2], lo[2];
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float wa, wb;
-                            f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[4 * j + 2 * e]), __uint_as_float(sr[4 * j + 2 * e + 1])),
-                                             ko2, zero2), wa, wb);
-                            // the upper 4 bits of w by w (2^7 + 1) - (w (2^7 + 1) - w)
-                            const uint32_t w16 = pack_f16(wa, wb);
-                            const uint32_t t16 = f16x2_mul(w16, 0x58085808u);  // 129
-                            const uint32_t h16 = f16x2_sub(t16, f16x2_sub(t16, w16));
-                            hi[e] = pack_e4m3x2_f16(h16);
-                            lo[e] = pack_e4m3x2_f16(f16x2_sub(w16, h16));
-                        }
-                        pk[j] = hi[0] | (hi[1] << 16);
-                        pk[16 + j] = lo[0] | (lo[1] << 16);
-                    }
-                }
-            }
 
             // staging pb is free once the value CTA's MMA of page it - 2 is
             // done: that MMA consumed the bulk copy made from it
@@ -1363,10 +1258,7 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
             for (int j = 0; j < 8; ++j)
                 sts128(stage_s + r * 128 + 16 * (j ^ (r & 7)), pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
             sts32(stage_s + kFacOff + 4 * r, __float_as_uint(fac));
-            if (pg == s.p1 - 1) {
-                const float div = kE8 ? l * ko : l;  // O carries ko
-                sts32(stage_s + kInvLOff + 4 * r, __float_as_uint(div > 0.f ? 1.f / div : 0.f));
-            }
+            if (pg == s.p1 - 1) sts32(stage_s + kInvLOff + 4 * r, __float_as_uint(l > 0.f ? 1.f / l : 0.f));
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
@@ -1382,9 +1274,8 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
                 if (last) bulk_copy_to_peer(dst + kInvLOff + fac_off, stage + kInvLOff + fac_off, 32 * 4, bar);
             }
         }
-        // LSE of this row over the segment (natural log), from the thread that had
-        // its last page
-        if (row_ok && (kGroups == 1 || (s.p1 > s.p0 ? (int)((it - 1) % kGroups) == grp : grp == 0))) {
+        // LSE of this row over the segment (natural log)
+        if (row_ok) {
             const float lse_row = l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : -CUDART_INF_F;
             if (s.n_split <= 1) {
                 p.lse[(size_t)s.b * p.rows + gr] = lse_row;
@@ -1400,6 +1291,312 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
     for (uint32_t k = it > (uint32_t)kPBufs ? it - kPBufs : 0; k < it; ++k)
         if (!warp_wait<true>(c, B_PFREE + (int)(k % kPBufs), (k / kPBufs) & 1)) return;
 }
+
+// Score-CTA row warps of the fp8 products, three groups of four warps that
+// take every third page: with one group the chain of a page (TMEM loads,
+// exponents, splitting, staging, hand-off) took 4000 cycles, far above what its
+// instructions need, and with all 64 keys of a row unrolled the code missed the instruction
+// cache.  Here a page is one rolled pass over four chunks of 16 keys that goes
+// straight from TMEM to the staged codes, and the page's state (running maximum
+// m, weight scale ko, sum L in units of ko 2^-m) travels from group to group:
+//   pass: x_j = s_j c_j sc - (m - log2 ko), p_j = 2^x_j, w_j = p_j c_j -> two e4m3 parts
+// A page is run on the state that its group knew last, three pages ago, and is
+// good if the state has not changed since and the page changes nothing in it:
+// its maximum within 2^8 of m, its largest weight within the e4m3 range.  Only
+// otherwise (a segment's first page, and the few where a maximum rises) it is run
+// again: for the maximum, for the largest weight, and for the codes.
+//   ko    a power of two that puts the largest weight at 28..56 when it is set (so
+//         that weights may grow eightfold before it has to change: with 56..112
+//         every seventh page of 16,384 N(0, 1) tokens ran again); set anew when a
+//         weight would pass 448 and with every new maximum, never so that what O
+//         holds would grow (negative: no weight so far)
+//   parts h = the upper 4 bits of w by w (2^7 + 1) - (w (2^7 + 1) - w) in f16, l = w - h
+//         (exact): off by about 2^-8 of w, or 2^-9 where the largest is at least 28
+#if MLA_SPLIT_FP8 && MLA_SPLIT_TREE
+__device__ void score_rows_e8(const DecodeParams &p, const Ctx &c, uint32_t tmem, int part) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int r = 32 * (warp & 3) + lane;                // tile row = TMEM lane
+    const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
+    const int grp = warp < 6 ? 0 : (warp - 4) >> 2;      // warps 2..5, 8..11, 12..15
+    const int before = (grp + kGroups - 1) % kGroups;    // the group of the page before
+    const int chain_own = B_CHAIN + 4 * grp + (warp & 3), chain_prev = B_CHAIN + 4 * before + (warp & 3);
+    const uint32_t own_s = smem_u32(c.base + kChainOff) + 4u * (uint32_t)(3 * kTileRows * grp + r);
+    const uint32_t prev_s = smem_u32(c.base + kChainOff) + 4u * (uint32_t)(3 * kTileRows * before + r);
+    const uint32_t peer_buf = mapa(smem_u32(c.base + kPBufOff), c.peer);
+    const uint32_t peer_pfull = mapa(smem_u32(c.bar(B_PFULL)), c.peer);
+    const uint64_t zero2 = f2_pack(0.f, 0.f);
+    PartWalk walk;
+    walk.init(p, part);
+    Segment s;
+    uint32_t it = 0, seg = 0;
+    while (walk.next(p, s)) {
+        const int gr = s.tile * kTileRows + r;           // row within the sequence's rows
+        const bool row_ok = gr < p.rows;
+        const int qi = row_ok ? gr / p.h_q : 0;          // query token index
+        const int nodes = tree_nodes(p, s.b);
+        const int tree_base = tree_start(p, s.T, nodes);
+        const int T_row = qi < nodes ? s.T : 0;          // a row behind the tree sees nothing
+        // both MMA issuers have seen the previous segment's Q (and, with all its
+        // scores waited for, the MMAs reading it are done)
+        if (seg > 0 && !warp_wait(c, B_QACK, (seg - 1) & 1)) return;
+        ++seg;
+        float qsig = 1.f;  // this row's Q scale (q = qsig * (h + l))
+        if (s.p1 > s.p0) {
+            // Q row r as two e4m3 parts of q / qsig, qsig the power of two at or
+            // above max |q| / 448: q / qsig keeps its 8 bits, and h = e4m3(x),
+            // l = e4m3(x - h) hold them.  Part t of dim d at TMEM column
+            // 144 t + d / 4 of lane r.  The groups share the nine 64-dim chunks.
+            const uint4 *qrow = reinterpret_cast<const uint4 *>(p.q + ((size_t)s.b * p.rows + (row_ok ? gr : 0)) * kD);
+            uint32_t top = 0;
+#pragma unroll 1
+            for (int j0 = 0; j0 < kD / 8; j0 += 12) {
+                uint4 x[12];
+#pragma unroll
+                for (int j = 0; j < 12; ++j) x[j] = row_ok ? __ldg(qrow + j0 + j) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int j = 0; j < 12; ++j)
+                    top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[j].x & 0x7fff7fffu, x[j].y & 0x7fff7fffu),
+                                                 __vmaxu2(x[j].z & 0x7fff7fffu, x[j].w & 0x7fff7fffu)));
+            }
+            const float amax = __uint_as_float(max(top >> 16, top & 0xffffu) << 16);
+            if (amax > 0.f) qsig = __uint_as_float((__float_as_uint(amax / kE4Max) + 0x7fffffu) & 0x7f800000u);
+            const float inv = 1.f / qsig;
+#pragma unroll 1
+            for (int ch = grp; ch < kKChunks; ch += kGroups) {
+                uint32_t ph[16], pl[16];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint4 x = row_ok ? __ldg(qrow + ch * 8 + j) : make_uint4(0, 0, 0, 0);
+                    const uint32_t w4[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int hw = 0; hw < 2; ++hw) {
+                        uint32_t code[2][2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float a = __uint_as_float(w4[2 * hw + e] << 16) * inv;
+                            const float b = __uint_as_float(w4[2 * hw + e] & 0xffff0000u) * inv;
+                            code[0][e] = pack_e4m3x2(a, b);
+                            float ha, hb;
+                            f16x2_to_f32(e4m3x2_to_f16x2(code[0][e]), ha, hb);
+                            code[1][e] = pack_e4m3x2(a - ha, b - hb);
+                        }
+                        ph[2 * j + hw] = code[0][0] | (code[0][1] << 16);
+                        pl[2 * j + hw] = code[1][0] | (code[1][1] << 16);
+                    }
+                }
+                tmem_st16(tmem + lane_base + ch * 16, ph);
+                tmem_st16(tmem + lane_base + kQPartCols + ch * 16, pl);
+            }
+            tmem_wait_st();
+        }
+        tc_fence_before();
+        mbar_arrive(c.bar(B_QFULL));
+
+        const float sc = p.scale_log2 * qsig;  // the row's Q scale folded in
+        const uint64_t sc2 = f2_pack(sc, sc);
+        // a new weight scale for a page's largest weight w > 0 (in units of 2^-m);
+        // returns the factor of O: fac, the maximum's, times the scale's change
+        auto new_scale = [](float w, float fac, float &ko) {
+            float kn = fminf(kE4Max / 8.f / w, 0x1p100f);
+            if (ko > 0.f) kn = fminf(kn, ko / fac);  // fac kn / ko <= 1 (fac = 0: no limit)
+            kn = __uint_as_float(__float_as_uint(kn) & 0x7f800000u);
+            fac *= kn / fabsf(ko);
+            ko = kn;
+            return fac;
+        };
+        // what this group knows of the row: state after some page of the segment
+        float m = -CUDART_INF_F, L = 0.f, ko = -1.f;
+        for (int pg = s.p0; pg < s.p1; ++pg, ++it) {
+            const int sb = (int)(it % kSBufs);
+            if ((int)(it % kGroups) != grp) {  // another group's page
+                // Q may be replaced only when the segment's last MMAs are done
+                if (pg >= s.p1 - kScoreIssuers && !warp_wait(c, B_SFULL + sb, (it / kSBufs) & 1)) return;
+                continue;
+            }
+            const int pb = (int)(it % kPBufs), scs = (int)(it % kScSlots);
+            const uint32_t cs_s = smem_u32(c.base + kScaleOff) + (uint32_t)scs * kScBytes;
+            if (!warp_wait(c, B_SCFULL + scs, (it / kScSlots) & 1)) return;
+            if ((warp & 3) == 0) {
+                // one warp of the group checks the scales of the sequence's tokens
+                // on this page against the limit (a NaN scale fails too)
+                const int nseq = min(kPage, s.T - pg * kPage);
+                const float a = lane < nseq ? fabsf(__uint_as_float(lds32(cs_s + 4 * lane))) : 0.f;
+                const float b = lane + 32 < nseq ? fabsf(__uint_as_float(lds32(cs_s + 4 * (lane + 32)))) : 0.f;
+                if (__any_sync(0xffffffffu, !(a < kE4ScaleLimit) || !(b < kE4ScaleLimit)) && lane == 0)
+                    atomicOr(p.status, MLA_DEVERR_SCALE);
+            }
+            // the rows of the page that this row sees
+            int nvalid = row_ok ? T_row - pg * kPage : 0;
+            nvalid = nvalid < 0 ? 0 : (nvalid > kPage ? kPage : nvalid);
+            uint64_t vmask = ~0ull;
+            if ((pg + 1) * kPage > tree_base && nvalid > 0) vmask = tree_page_mask(p, s.b, qi, tree_base, pg);
+            if (nvalid < kPage) vmask &= nvalid > 0 ? (~0ull >> (kPage - nvalid)) : 0ull;
+            // staging pb is free once the value CTA's MMA of page it - kPBufs is
+            // done: that MMA consumed the bulk copy made from it
+            if (!warp_wait<true>(c, B_PFREE + pb, ((it / kPBufs) & 1) ^ 1)) return;
+            uint8_t *stage = c.base + kStageOff + pb * kPMsgBytes;
+            const uint32_t stage_s = smem_u32(stage);
+            if (!warp_wait(c, B_SFULL + sb, (it / kSBufs) & 1)) return;
+            tc_fence_after();
+
+            // a segment's first pages run on the state after the page before
+            bool chained = pg - s.p0 < kGroups;
+            if (chained) {
+                if (it > 0 && !warp_wait(c, chain_prev, ((it - 1) / kGroups) & 1)) return;
+                if (pg > s.p0) {
+                    m = __uint_as_float(lds32(prev_s));
+                    L = __uint_as_float(lds32(prev_s + kTileRows * 4));
+                    ko = __uint_as_float(lds32(prev_s + 2 * kTileRows * 4));
+                }
+            }
+            float fac = 1.f;
+            enum { kTry, kMaximum, kLargest, kCodes };
+            int phase = pg == s.p0 ? kMaximum : kTry;
+            while (true) {
+                const float lk = (float)((int)(__float_as_uint(fabsf(ko)) >> 23) - 127);
+                const float ref = phase == kMaximum || m == -CUDART_INF_F ? 0.f : phase == kLargest ? m : m - lk;
+                const uint64_t nref2 = f2_pack(-ref, -ref);
+                const bool write = phase == kTry || phase == kCodes;
+                float xa4[2] = {-CUDART_INF_F, -CUDART_INF_F}, wa4[2] = {0.f, 0.f};
+                uint64_t sum2[2] = {0ull, 0ull};
+#pragma unroll 1
+                for (int ch = 0; ch < kPage / 16; ++ch) {
+                    uint32_t v[16];
+                    tmem_ld16(tmem + lane_base + kSCol0 + sb * kSCols + ch * 16, v);
+                    uint64_t cs2[8];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint4 c4 = lds128(cs_s + 64 * ch + 16 * j);
+                        cs2[2 * j] = f2_pack(__uint_as_float(c4.x), __uint_as_float(c4.y));
+                        cs2[2 * j + 1] = f2_pack(__uint_as_float(c4.z), __uint_as_float(c4.w));
+                    }
+                    tmem_wait_ld();
+                    float x[16];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        f2_unpack(f2_fma(f2_fma(f2_pack(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), cs2[j], zero2),
+                                         sc2, nref2), x[2 * j], x[2 * j + 1]);
+                    const uint32_t vis = (uint32_t)(vmask >> (16 * ch)) & 0xffffu;
+                    if (vis != 0xffffu) {  // neither the score nor the scale of an invisible key counts
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) x[j] = (vis >> j) & 1u ? x[j] : -CUDART_INF_F;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            float ca, cb;
+                            f2_unpack(cs2[j], ca, cb);
+                            cs2[j] = f2_pack((vis >> (2 * j)) & 1u ? ca : 0.f, (vis >> (2 * j + 1)) & 1u ? cb : 0.f);
+                        }
+                    }
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t h16[2], l16[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int j = 2 * q + e;
+                            xa4[e] = max3f(xa4[e], x[2 * j], x[2 * j + 1]);
+                            const uint64_t p2 = f2_pack(ex2(x[2 * j]), ex2(x[2 * j + 1]));
+                            sum2[e] = f2_add(sum2[e], p2);
+                            float wa, wb;
+                            f2_unpack(f2_fma(p2, cs2[j], zero2), wa, wb);
+                            wa4[e] = max3f(wa4[e], fabsf(wa), fabsf(wb));
+                            const uint32_t w16 = pack_f16(wa, wb), t16 = f16x2_mul(w16, 0x58085808u);  // 129
+                            h16[e] = f16x2_sub(t16, f16x2_sub(t16, w16));
+                            l16[e] = f16x2_sub(w16, h16[e]);
+                        }
+                        hi[q] = pack_e4m3x4_f16(h16[0], h16[1]);
+                        lo[q] = pack_e4m3x4_f16(l16[0], l16[1]);
+                    }
+                    if (write) {  // 16 codes of the upper parts, and of the lower ones 64 bytes behind
+                        sts128(stage_s + r * 128 + 16 * (ch ^ (r & 7)), hi[0], hi[1], hi[2], hi[3]);
+                        sts128(stage_s + r * 128 + 16 * ((ch + 4) ^ (r & 7)), lo[0], lo[1], lo[2], lo[3]);
+                    }
+                }
+                const float xmax = fmaxf(xa4[0], xa4[1]), wmax = fmaxf(wa4[0], wa4[1]);
+                float sum_lo, sum_hi;
+                f2_unpack(f2_add(sum2[0], sum2[1]), sum_lo, sum_hi);
+                const float sum = sum_lo + sum_hi;
+                if (phase == kTry) {
+                    bool same = true;
+                    if (!chained) {
+                        if (!warp_wait(c, chain_prev, ((it - 1) / kGroups) & 1)) return;
+                        const float m1 = __uint_as_float(lds32(prev_s)), ko1 = __uint_as_float(lds32(prev_s + 2 * kTileRows * 4));
+                        same = m1 == m && ko1 == ko;
+                        m = m1;
+                        ko = ko1;
+                        L = __uint_as_float(lds32(prev_s + kTileRows * 4));
+                        chained = true;
+                    }
+                    if (!__all_sync(0xffffffffu, same)) continue;  // once more, on the state that is
+                    const bool low = m == -CUDART_INF_F ? xmax == -CUDART_INF_F : xmax <= kRescaleLog2 + lk;
+                    const bool fits = wmax <= kE4Max && !(ko < 0.f && wmax > 0.f);
+                    if (!__all_sync(0xffffffffu, low)) {
+                        phase = kMaximum;
+                    } else if (!__all_sync(0xffffffffu, fits)) {
+                        if (!fits) fac = new_scale(wmax / fabsf(ko), fac, ko);
+                        phase = kCodes;
+                    } else {
+                        L += sum;
+                        break;
+                    }
+                } else if (phase == kMaximum) {
+                    if (xmax > m + kRescaleLog2 || (m == -CUDART_INF_F && xmax > -CUDART_INF_F)) {
+                        fac = ex2(m - xmax);  // 0 when m was -inf
+                        m = xmax;
+                    }
+                    phase = kLargest;
+                } else if (phase == kLargest) {
+                    if (wmax > 0.f && (ko < 0.f || wmax * ko > kE4Max || fac != 1.f)) fac = new_scale(wmax, fac, ko);
+                    phase = kCodes;
+                } else {
+                    L = L * fac + sum;
+                    break;
+                }
+            }
+            tc_fence_before();
+            mbar_arrive(c.bar(B_SEMPTY + sb));
+            mbar_arrive(c.bar(B_SCEMPTY + scs));
+            sts32(own_s, __float_as_uint(m));
+            sts32(own_s + kTileRows * 4, __float_as_uint(L));
+            sts32(own_s + 2 * kTileRows * 4, __float_as_uint(ko));
+            mbar_arrive(c.bar(chain_own));
+
+            const bool last = pg == s.p1 - 1;
+            sts32(stage_s + kFacOff + 4 * r, __float_as_uint(fac));
+            if (last) sts32(stage_s + kInvLOff + 4 * r, __float_as_uint(L > 0.f ? 1.f / L : 0.f));
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                // this warp's 32 rows of P and of the row factors, as in score_rows
+                const uint32_t bar = peer_pfull + pb * 8;
+                const uint32_t rows_off = (uint32_t)(32 * (warp & 3)) * 128, fac_off = (uint32_t)(32 * (warp & 3)) * 4;
+                const uint32_t dst = peer_buf + pb * kPMsgBytes;
+                mbar_arrive_expect_tx_remote_relaxed(bar, 32 * 128 + (last ? 2 : 1) * 32 * 4);
+                bulk_copy_to_peer(dst + rows_off, stage + rows_off, 32 * 128, bar);
+                bulk_copy_to_peer(dst + kFacOff + fac_off, stage + kFacOff + fac_off, 32 * 4, bar);
+                if (last) bulk_copy_to_peer(dst + kInvLOff + fac_off, stage + kInvLOff + fac_off, 32 * 4, bar);
+            }
+        }
+        // LSE of this row over the segment (natural log), from the thread that had
+        // its last page; L counts in units of |ko| 2^-m
+        if (row_ok && (s.p1 > s.p0 ? (int)((it - 1) % kGroups) == grp : grp == 0)) {
+            const float lk = (float)((int)(__float_as_uint(fabsf(ko)) >> 23) - 127);
+            const float lse_row = L > 0.f ? (m - lk + __log2f(L)) * 0.69314718055994531f : -CUDART_INF_F;
+            if (s.n_split <= 1) {
+                p.lse[(size_t)s.b * p.rows + gr] = lse_row;
+            } else {
+                const int slot = p.num_splits[s.entry] + s.split;
+                if (slot >= 0 && slot < p.max_splits) p.lse_accum[(size_t)slot * slot_rows(p) + r] = lse_row;
+                else atomicOr(p.status, MLA_DEVERR_SEQLEN);
+            }
+        }
+    }
+    // the peer's last commits arrive on our P-free barriers: let them land
+    // before this CTA can leave (this also covers the last bulk copies)
+    for (uint32_t k = it > (uint32_t)kPBufs ? it - kPBufs : 0; k < it; ++k)
+        if (!warp_wait<true>(c, B_PFREE + (int)(k % kPBufs), (k / kPBufs) & 1)) return;
+}
+#endif
 
 // Value-CTA row warps: V tail zeroing (e4m3 cache: widening of each V page),
 // lazy O rescale, epilogue.
@@ -1473,7 +1670,8 @@ __device__ void value_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
             // lazy rescale of this row of O before the next accumulation
             const bool need = (pg > s.p0) && (fac != 1.f);
             if (__any_sync(0xffffffffu, need)) {
-                if (!warp_wait(c, B_PVDONE, (it - 1) & 1)) return;  // every earlier P V has landed
+                // every earlier P V has landed
+                if (!warp_wait(c, B_PVDONE + (int)((it - 1) % kPVBars), ((it - 1) / kPVBars) & 1)) return;
                 tc_fence_after();
 #pragma unroll 1
                 for (int ch = 0; ch < 16; ++ch) {
@@ -1628,7 +1826,7 @@ split_kv_tc_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_cons
             }
             mbar_init(c.bar(B_VREAD), 128);
             if constexpr (kGroups > 1)
-                for (int i = 0; i < 16; ++i) mbar_init(c.bar(B_CHAIN + i), 32);
+                for (int i = 0; i < 4 * kGroups; ++i) mbar_init(c.bar(B_CHAIN + i), 32);
         }
         for (int i = 0; i < kSBufs; ++i) {
             mbar_init(c.bar(B_SFULL + i), 1);
@@ -1641,7 +1839,7 @@ split_kv_tc_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_cons
             mbar_init(c.bar(B_PFULL + i), 4);  // one arrival per row warp of the score CTA
             mbar_init(c.bar(B_PREADY + i), 128);
         }
-        mbar_init(c.bar(B_PVDONE), 1);
+        for (int i = 0; i < kPVBars; ++i) mbar_init(c.bar(B_PVDONE + i), 1);
         mbar_init(c.bar(B_ODONE), 1);
         mbar_init(c.bar(B_OEMPTY), 128);
         mbar_init(c.bar(B_FINAL), is_score ? kScoreIssuers : 1);  // one commit per MMA issuer
@@ -1689,7 +1887,11 @@ split_kv_tc_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_cons
         }
         __syncwarp();
     } else {
+#if MLA_SPLIT_FP8 && MLA_SPLIT_TREE
+        if (is_score) score_rows_e8(p, c, tmem, part);
+#else
         if (is_score) score_rows(p, c, tmem, part, tile);
+#endif
         else if (warp < 8) value_rows(p, c, tmem, part, tile);
     }
 
