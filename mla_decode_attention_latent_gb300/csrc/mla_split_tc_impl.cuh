@@ -205,7 +205,9 @@ constexpr uint32_t kScaleOff = kStageOff + kPBufs * kPMsgBytes;   // the side ri
 // several groups: the running state that each leaves for the next page's,
 // [group][maximum, row sum, weight scale][128 rows] fp32
 constexpr uint32_t kChainOff = kScaleOff + (kRing ? kScSlots * kScBytes : 0);
-constexpr uint32_t kScoreEnd = kChainOff + (kGroups > 1 ? kGroups * 3 * kTileRows * 4 : 0);
+// and each group's part of the maxima of Q's rows, [group][128 rows]
+constexpr uint32_t kQMaxOff = kChainOff + (kGroups > 1 ? kGroups * 3 * kTileRows * 4 : 0);
+constexpr uint32_t kScoreEnd = kQMaxOff + (kGroups > 1 ? kGroups * kTileRows * 4 : 0);
 // value CTA: [V ring 2 x 64 KB (sparse: the page buffers)][P landing 2 x 17 KB][epilogue staging 34 KB]
 constexpr uint32_t kVRingOff = 0;
 constexpr uint32_t kPBufOff = kVRingOff + kVStages * kVStageBytes;
@@ -243,8 +245,9 @@ constexpr int B_CHUNK = B_VREAD + 1;
 // several groups: [group][warp of the group] state left for the next group's warp
 // of the same rows (32 arrivals)
 constexpr int B_CHAIN = B_VREAD + 1;
+constexpr int B_QMAX = B_CHAIN + 4 * kGroups;  // [warp of a group] the groups' maxima of Q (32 arrivals per group)
 constexpr int B_COUNT = kSparse ? B_CHUNK + kVStages * kKChunks
-                                : (kGroups > 1 ? B_CHAIN + 4 * kGroups : (kRing ? B_VREAD + 1 : B_BASE_COUNT));
+                                : (kGroups > 1 ? B_QMAX + 4 : (kRing ? B_VREAD + 1 : B_BASE_COUNT));
 constexpr uint32_t kTmemSlotOff = kBarOff + B_COUNT * 8;
 constexpr uint32_t kAbortOff = kTmemSlotOff + 4;
 constexpr uint32_t kSmemUsed = kAbortOff + 4;
@@ -324,11 +327,34 @@ struct Ctx {
     __device__ uint64_t *bar(int i) const { return bars + i; }
 };
 
+// fp8 products: the waiting itself out of line, since the row code of three groups
+// competes for the instruction cache (1.40 -> 1.35 us a page; the bf16 kernels
+// measured 5-7 % slower with it)
+template <bool kCluster>
+__device__ __noinline__ bool wait_out_of_line(uint32_t bar, uint32_t parity, uint32_t abort_flag, uint32_t peer,
+                                              unsigned int *status) {
+    const uint64_t t0 = global_timer_ns();
+    while (true) {
+        for (int i = 0; i < 32; ++i)
+            if (kCluster ? mbar_test_cluster(bar, parity) : mbar_test(bar, parity)) return true;
+        if (lds32(abort_flag)) return false;
+        if (global_timer_ns() - t0 > kWaitLimitNs) {
+            atomicOr(status, MLA_DEVERR_TIMEOUT);
+            sts32(abort_flag, 1u);
+            // tell the peer CTA to stop waiting on us
+            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa(abort_flag, peer)), "r"(1) : "memory");
+            return false;
+        }
+    }
+}
+
 // bounded wait that also gives up when this CTA was told to abort
 template <bool kCluster = false>
 __device__ __forceinline__ bool wait(const Ctx &c, int bar_idx, uint32_t parity) {
     const uint32_t a = smem_u32(c.bar(bar_idx));
     if (kCluster ? mbar_test_cluster(a, parity) : mbar_test(a, parity)) return true;
+    if constexpr (kE8)
+        return wait_out_of_line<kCluster>(a, parity, smem_u32((const void *)c.abort_flag), c.peer, c.status);
     const uint64_t t0 = global_timer_ns();
     while (true) {
         for (int i = 0; i < 32; ++i)
@@ -1328,7 +1354,7 @@ __device__ void score_rows_e8(const DecodeParams &p, const Ctx &c, uint32_t tmem
     PartWalk walk;
     walk.init(p, part);
     Segment s;
-    uint32_t it = 0, seg = 0;
+    uint32_t it = 0, seg = 0, qseg = 0;
     while (walk.next(p, s)) {
         const int gr = s.tile * kTileRows + r;           // row within the sequence's rows
         const bool row_ok = gr < p.rows;
@@ -1345,29 +1371,45 @@ __device__ void score_rows_e8(const DecodeParams &p, const Ctx &c, uint32_t tmem
             // Q row r as two e4m3 parts of q / qsig, qsig the power of two at or
             // above max |q| / 448: q / qsig keeps its 8 bits, and h = e4m3(x),
             // l = e4m3(x - h) hold them.  Part t of dim d at TMEM column
-            // 144 t + d / 4 of lane r.  The groups share the nine 64-dim chunks.
+            // 144 t + d / 4 of lane r.  The groups share the nine 64-dim chunks, and
+            // put the maximum of the row together in shared memory.
             const uint4 *qrow = reinterpret_cast<const uint4 *>(p.q + ((size_t)s.b * p.rows + (row_ok ? gr : 0)) * kD);
+            constexpr int kOwn = kKChunks / kGroups;
+            static_assert(kOwn * kGroups == kKChunks, "chunks of Q per group");
             uint32_t top = 0;
 #pragma unroll 1
-            for (int j0 = 0; j0 < kD / 8; j0 += 12) {
+            for (int k0 = 0; k0 < kOwn * 8; k0 += 12) {  // (and into L1, for the round below)
                 uint4 x[12];
 #pragma unroll
-                for (int j = 0; j < 12; ++j) x[j] = row_ok ? __ldg(qrow + j0 + j) : make_uint4(0, 0, 0, 0);
+                for (int i = 0; i < 12; ++i) {
+                    const int k = k0 + i;
+                    x[i] = row_ok ? __ldg(qrow + (grp + kGroups * (k >> 3)) * 8 + (k & 7)) : make_uint4(0, 0, 0, 0);
+                }
 #pragma unroll
-                for (int j = 0; j < 12; ++j)
-                    top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[j].x & 0x7fff7fffu, x[j].y & 0x7fff7fffu),
-                                                 __vmaxu2(x[j].z & 0x7fff7fffu, x[j].w & 0x7fff7fffu)));
+                for (int i = 0; i < 12; ++i)
+                    top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
+                                                 __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu)));
             }
-            const float amax = __uint_as_float(max(top >> 16, top & 0xffffu) << 16);
+            top = max(top >> 16, top & 0xffffu) << 16;
+            const uint32_t tops = smem_u32(c.base + kQMaxOff) + 4u * (uint32_t)r;
+            sts32(tops + grp * kTileRows * 4, top);
+            mbar_arrive(c.bar(B_QMAX + (warp & 3)));
+            if (!warp_wait(c, B_QMAX + (warp & 3), qseg & 1)) return;
+            ++qseg;
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) top = max(top, lds32(tops + g * kTileRows * 4));
+            const float amax = __uint_as_float(top);
             if (amax > 0.f) qsig = __uint_as_float((__float_as_uint(amax / kE4Max) + 0x7fffffu) & 0x7f800000u);
             const float inv = 1.f / qsig;
 #pragma unroll 1
-            for (int ch = grp; ch < kKChunks; ch += kGroups) {
+            for (int k = 0; k < kOwn; ++k) {
                 uint32_t ph[16], pl[16];
+                uint4 x[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = row_ok ? __ldg(qrow + (grp + kGroups * k) * 8 + j) : make_uint4(0, 0, 0, 0);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const uint4 x = row_ok ? __ldg(qrow + ch * 8 + j) : make_uint4(0, 0, 0, 0);
-                    const uint32_t w4[4] = {x.x, x.y, x.z, x.w};
+                    const uint32_t w4[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
 #pragma unroll
                     for (int hw = 0; hw < 2; ++hw) {
                         uint32_t code[2][2];
@@ -1384,6 +1426,7 @@ __device__ void score_rows_e8(const DecodeParams &p, const Ctx &c, uint32_t tmem
                         pl[2 * j + hw] = code[1][0] | (code[1][1] << 16);
                     }
                 }
+                const int ch = grp + kGroups * k;
                 tmem_st16(tmem + lane_base + ch * 16, ph);
                 tmem_st16(tmem + lane_base + kQPartCols + ch * 16, pl);
             }
@@ -1450,13 +1493,14 @@ __device__ void score_rows_e8(const DecodeParams &p, const Ctx &c, uint32_t tmem
                 }
             }
             float fac = 1.f;
-            enum { kTry, kMaximum, kLargest, kCodes };
+            enum { kTry, kMaximum, kFirst, kLargest, kCodes };
             int phase = pg == s.p0 ? kMaximum : kTry;
             while (true) {
                 const float lk = (float)((int)(__float_as_uint(fabsf(ko)) >> 23) - 127);
                 const float ref = phase == kMaximum || m == -CUDART_INF_F ? 0.f : phase == kLargest ? m : m - lk;
                 const uint64_t nref2 = f2_pack(-ref, -ref);
-                const bool write = phase == kTry || phase == kCodes;
+                const bool write = phase == kTry || phase == kFirst || phase == kCodes;
+                float ca4[2] = {0.f, 0.f};  // kMaximum: the largest scale of a visible key
                 float xa4[2] = {-CUDART_INF_F, -CUDART_INF_F}, wa4[2] = {0.f, 0.f};
                 uint64_t sum2[2] = {0ull, 0ull};
 #pragma unroll 1
@@ -1485,6 +1529,14 @@ __device__ void score_rows_e8(const DecodeParams &p, const Ctx &c, uint32_t tmem
                             float ca, cb;
                             f2_unpack(cs2[j], ca, cb);
                             cs2[j] = f2_pack((vis >> (2 * j)) & 1u ? ca : 0.f, (vis >> (2 * j + 1)) & 1u ? cb : 0.f);
+                        }
+                    }
+                    if (phase == kMaximum) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            float ca, cb;
+                            f2_unpack(cs2[j], ca, cb);
+                            ca4[j & 1] = max3f(ca4[j & 1], fabsf(ca), fabsf(cb));
                         }
                     }
                     uint32_t hi[4], lo[4];
@@ -1544,7 +1596,32 @@ __device__ void score_rows_e8(const DecodeParams &p, const Ctx &c, uint32_t tmem
                         fac = ex2(m - xmax);  // 0 when m was -inf
                         m = xmax;
                     }
-                    phase = kLargest;
+                    // a first page's weights are at most its largest scale
+                    const float cmax = fmaxf(ca4[0], ca4[1]);
+                    if (pg == s.p0) {
+                        if (cmax > 0.f && m > -CUDART_INF_F) fac = new_scale(cmax, fac, ko);
+                        phase = kFirst;
+                    } else {
+                        phase = kLargest;
+                    }
+                } else if (phase == kFirst) {
+                    // good enough unless the heavy keys have small scales
+                    if (__all_sync(0xffffffffu, wmax >= kE4Max / 64.f || wmax == 0.f)) {
+                        L = sum;
+                        if (wmax == 0.f && ko > 0.f) {  // no weight yet
+                            L /= ko;
+                            ko = -1.f;
+                        }
+                        break;
+                    }
+                    if (wmax > 0.f) {
+                        const float w = wmax / ko;
+                        ko = -1.f;
+                        new_scale(w, 0.f, ko);
+                    } else {
+                        ko = -1.f;
+                    }
+                    phase = kCodes;
                 } else if (phase == kLargest) {
                     if (wmax > 0.f && (ko < 0.f || wmax * ko > kE4Max || fac != 1.f)) fac = new_scale(wmax, fac, ko);
                     phase = kCodes;
@@ -1825,8 +1902,10 @@ split_kv_tc_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_cons
                 mbar_init(c.bar(B_SCEMPTY + i), 128);
             }
             mbar_init(c.bar(B_VREAD), 128);
-            if constexpr (kGroups > 1)
+            if constexpr (kGroups > 1) {
                 for (int i = 0; i < 4 * kGroups; ++i) mbar_init(c.bar(B_CHAIN + i), 32);
+                for (int i = 0; i < 4; ++i) mbar_init(c.bar(B_QMAX + i), 32 * kGroups);
+            }
         }
         for (int i = 0; i < kSBufs; ++i) {
             mbar_init(c.bar(B_SFULL + i), 1);
