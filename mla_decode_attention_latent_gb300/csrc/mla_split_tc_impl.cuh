@@ -1331,13 +1331,15 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
 // its maximum within 2^8 of m, its largest weight within the e4m3 range.  Only
 // otherwise (a segment's first page, and the few where a maximum rises) it is run
 // again: for the maximum, for the largest weight, and for the codes.
-//   ko    a power of two that puts the largest weight at 28..56 when it is set (so
-//         that weights may grow eightfold before it has to change: with 56..112
-//         every seventh page of 16,384 N(0, 1) tokens ran again); set anew when a
-//         weight would pass 448 and with every new maximum, never so that what O
-//         holds would grow (negative: no weight so far)
+//   ko    a power of two that puts a segment's first page's largest weight at
+//         3.5..7 (so that later ones may be 64 times as large before it has to
+//         change: with a factor of 4 every seventh page of 16,384 N(0, 1) tokens
+//         ran again; 24 ragged trees took 282 us with 8, 252 with 32, 235 with 64, 229
+//         with 128, where the error of o grew from 0.0017 to 0.0018); set anew, the largest then at 28..56, when a weight would pass
+//         448 and with every new maximum, never so that what O holds would grow
+//         (negative: no weight so far)
 //   parts h = the upper 4 bits of w by w (2^7 + 1) - (w (2^7 + 1) - w) in f16, l = w - h
-//         (exact): off by about 2^-8 of w, or 2^-9 where the largest is at least 28
+//         (exact): off by about 2^-8 of w, or by 2^-9 where the largest is at least 3.5
 #if MLA_SPLIT_FP8 && MLA_SPLIT_TREE
 __device__ void score_rows_e8(const DecodeParams &p, const Ctx &c, uint32_t tmem, int part) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1437,10 +1439,12 @@ __device__ void score_rows_e8(const DecodeParams &p, const Ctx &c, uint32_t tmem
 
         const float sc = p.scale_log2 * qsig;  // the row's Q scale folded in
         const uint64_t sc2 = f2_pack(sc, sc);
-        // a new weight scale for a page's largest weight w > 0 (in units of 2^-m);
-        // returns the factor of O: fac, the maximum's, times the scale's change
-        auto new_scale = [](float w, float fac, float &ko) {
-            float kn = fminf(kE4Max / 8.f / w, 0x1p100f);
+        // a new weight scale that puts w > 0, a page's largest weight (in units of
+        // 2^-m), next below `at`; returns the factor of O: fac, the maximum's,
+        // times the scale's change
+        constexpr float kAtFirst = kE4Max / 64.f, kAtLater = kE4Max / 8.f;
+        auto new_scale = [](float w, float at, float fac, float &ko) {
+            float kn = fminf(at / w, 0x1p100f);
             if (ko > 0.f) kn = fminf(kn, ko / fac);  // fac kn / ko <= 1 (fac = 0: no limit)
             kn = __uint_as_float(__float_as_uint(kn) & 0x7f800000u);
             fac *= kn / fabsf(ko);
@@ -1585,7 +1589,7 @@ __device__ void score_rows_e8(const DecodeParams &p, const Ctx &c, uint32_t tmem
                     if (!__all_sync(0xffffffffu, low)) {
                         phase = kMaximum;
                     } else if (!__all_sync(0xffffffffu, fits)) {
-                        if (!fits) fac = new_scale(wmax / fabsf(ko), fac, ko);
+                        if (!fits) fac = new_scale(wmax / fabsf(ko), kAtLater, fac, ko);
                         phase = kCodes;
                     } else {
                         L += sum;
@@ -1599,14 +1603,14 @@ __device__ void score_rows_e8(const DecodeParams &p, const Ctx &c, uint32_t tmem
                     // a first page's weights are at most its largest scale
                     const float cmax = fmaxf(ca4[0], ca4[1]);
                     if (pg == s.p0) {
-                        if (cmax > 0.f && m > -CUDART_INF_F) fac = new_scale(cmax, fac, ko);
+                        if (cmax > 0.f && m > -CUDART_INF_F) fac = new_scale(cmax, kAtFirst, fac, ko);
                         phase = kFirst;
                     } else {
                         phase = kLargest;
                     }
                 } else if (phase == kFirst) {
                     // good enough unless the heavy keys have small scales
-                    if (__all_sync(0xffffffffu, wmax >= kE4Max / 64.f || wmax == 0.f)) {
+                    if (__all_sync(0xffffffffu, wmax >= kAtFirst / 8.f || wmax == 0.f)) {
                         L = sum;
                         if (wmax == 0.f && ko > 0.f) {  // no weight yet
                             L /= ko;
@@ -1617,13 +1621,13 @@ __device__ void score_rows_e8(const DecodeParams &p, const Ctx &c, uint32_t tmem
                     if (wmax > 0.f) {
                         const float w = wmax / ko;
                         ko = -1.f;
-                        new_scale(w, 0.f, ko);
+                        new_scale(w, kAtFirst, 0.f, ko);
                     } else {
                         ko = -1.f;
                     }
                     phase = kCodes;
                 } else if (phase == kLargest) {
-                    if (wmax > 0.f && (ko < 0.f || wmax * ko > kE4Max || fac != 1.f)) fac = new_scale(wmax, fac, ko);
+                    if (wmax > 0.f && (ko < 0.f || wmax * ko > kE4Max || fac != 1.f)) fac = new_scale(wmax, kAtLater, fac, ko);
                     phase = kCodes;
                 } else {
                     L = L * fac + sum;
