@@ -562,7 +562,7 @@ MLA_API int mla_decode_kvcache_tree(const void *q, const void *kcache, int64_t n
  * Scales as for mla_decode_kvcache_fp8.  Precision: both products run on the fp8
  * tensor cores.  q is held exactly, but for elements below 2^-11 of their row's
  * largest (to 2^-19 of it); a softmax weight times its token's scale is held to
- * about 2^-8 of itself, or to 2^-10 of the row's largest in the first page where that
+ * about 2^-8 of itself, or to 2^-11 of the row's largest in the first page where that
  * is more.
  */
 MLA_API int mla_decode_kvcache_tree_fp8(const void *q, const void *kv_pages, int64_t num_blocks,

@@ -16,6 +16,7 @@ and passes raw pointers and the current stream.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 from typing import Optional, Tuple
 
@@ -317,11 +318,12 @@ def mla_decode_kvcache_noalloc(q: torch.Tensor, kcache: torch.Tensor, block_tabl
 
 
 # Serving loops make the calls below once per layer and token, so the host's
-# share of a small call counts: the library's functions are looked up once, and
-# the device is switched only when it is not the current one.
+# share of a small call counts: what depends on the device or on shapes alone is
+# asked of the library once, and the device is switched only when it is not the
+# current one.
 def _call(name: str, dev: torch.device, *args) -> None:
     """Run a library call on ``dev`` and its current stream; raise on a bad status."""
-    fn = getattr(load(), name)
+    fn = getattr(_lib._lib or load(), name)
     index = dev.index
     if index == torch.cuda.current_device():
         st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
@@ -338,6 +340,12 @@ def _on(dev: torch.device, of: str, name: str, t: torch.Tensor, dtype: torch.dty
         _need_cuda(name, t, dtype)
         _same_device(dev, of, **{name: t})
     return t.data_ptr()
+
+
+@functools.lru_cache(maxsize=None)
+def _pairs(index: int) -> int:
+    """CTA pairs of a device: the split-KV parts of a decode over row tiles."""
+    return mla_num_sm_parts(1, 1, torch.device("cuda", index))
 
 
 # ---------------------------------------------------------------- cache rows
@@ -512,6 +520,7 @@ def mla_update_page_keys_fp8(kv_pages: torch.Tensor, block_table: torch.Tensor, 
                       starts, True)
 
 
+@functools.lru_cache(maxsize=256)
 def mla_blocks_workspace_bytes(batch: int, s_q: int, h_q: int, h_kv: int, dv: int, max_blocks: int, topk_pages: int,
                                num_parts: int) -> int:
     n = load().mla_blocks_workspace_bytes(batch, s_q, h_q, h_kv, dv, max_blocks, topk_pages, num_parts)
@@ -520,10 +529,10 @@ def mla_blocks_workspace_bytes(batch: int, s_q: int, h_q: int, h_kv: int, dv: in
     return int(n)
 
 
-def _outputs(b, s_q, h_q, dv, dev, out, lse):
+def _outputs(q, b, s_q, h_q, dv, dev, out, lse):
     """The outputs of a decode, created where missing, and their addresses."""
     if out is None:
-        out = torch.empty((b, s_q, h_q, dv), dtype=torch.bfloat16, device=dev)
+        out = q.new_empty((b, s_q, h_q, dv))
     elif out.shape != (b, s_q, h_q, dv):
         raise ValueError("out must be [b, s_q, h_q, dv]")
     if lse is None:
@@ -553,10 +562,10 @@ def _decode_blocks(call, q, cache, block_table, cache_seqlens, page_keys, page_s
         raise ValueError("topk_pages must cover sink_pages (>= 0) and local_pages (>= 1)")
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(d)
-    num_parts = mla_num_sm_parts(1, 1, dev)
-    out, lse, o_ptr, lse_ptr = _outputs(b, s_q, h_q, dv, dev, out, lse)
+    num_parts = _pairs(dev.index)
+    out, lse, o_ptr, lse_ptr = _outputs(q, b, s_q, h_q, dv, dev, out, lse)
     if pages is None:
-        pages = torch.empty((b, s_q, topk_pages), dtype=torch.int32, device=dev)
+        pages = block_table.new_empty((b, s_q, topk_pages))
     elif pages.shape != (b, s_q, topk_pages):
         raise ValueError("pages must be [b, s_q, topk_pages]")
     pages_ptr = _on(dev, "q", "pages", pages, torch.int32)
@@ -630,7 +639,7 @@ def mla_get_metadata_tree(cache_seqlens: torch.Tensor, s_q: int, h_q: int, tree_
         raise ValueError("cache_seqlens, s_q and h_q must not be empty or 0")
     nodes = None if tree_lens is None else _vector(dev, "cache_seqlens", "tree_lens", tree_lens, b)
     if num_parts is None:
-        num_parts = mla_num_sm_parts(1, 1, dev)
+        num_parts = _pairs(dev.index)
     md = torch.empty((num_parts, MLA_METADATA_INTS), dtype=torch.int32, device=dev)
     ns = torch.empty((b * _row_tiles(s_q, h_q) + 1,), dtype=torch.int32, device=dev)
     _call("mla_get_metadata_tree", dev, cache_seqlens.data_ptr(), nodes, b, s_q, h_q, 1, int(num_parts), md.data_ptr(),
@@ -638,6 +647,7 @@ def mla_get_metadata_tree(cache_seqlens: torch.Tensor, s_q: int, h_q: int, tree_
     return md, ns
 
 
+@functools.lru_cache(maxsize=256)
 def mla_tree_workspace_bytes(batch: int, s_q: int, h_q: int, h_kv: int, dv: int, num_parts: int) -> int:
     n = load().mla_tree_workspace_bytes(batch, s_q, h_q, h_kv, dv, num_parts)
     if n == 0:
@@ -656,7 +666,7 @@ def _decode_tree(call, q, cache, block_table, cache_seqlens, tree_mask, dv, tile
     if (tile_scheduler_metadata is None) != (num_splits is None):
         raise ValueError("tile_scheduler_metadata and num_splits come together")
     if tile_scheduler_metadata is None:
-        num_parts = mla_num_sm_parts(1, 1, dev)
+        num_parts = _pairs(dev.index)
     else:
         md = _on(dev, "q", "tile_scheduler_metadata", tile_scheduler_metadata, torch.int32)
         ns = _vector(dev, "q", "num_splits", num_splits, b * _row_tiles(s_q, h_q) + 1)
@@ -665,7 +675,7 @@ def _decode_tree(call, q, cache, block_table, cache_seqlens, tree_mask, dv, tile
         num_parts = tile_scheduler_metadata.shape[0]
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(d)
-    out, lse, o_ptr, lse_ptr = _outputs(b, s_q, h_q, dv, dev, out, lse)
+    out, lse, o_ptr, lse_ptr = _outputs(q, b, s_q, h_q, dv, dev, out, lse)
     if workspace is None:
         need = mla_tree_workspace_bytes(b, s_q, h_q, 1, dv, num_parts)
         workspace = torch.empty((need,), dtype=torch.uint8, device=dev)

@@ -48,6 +48,7 @@ struct ScheduleShared {
     long long start[kSchedThreads + 1];  // first unit of every chunk; [kSchedThreads] = total
     long long warp64[kSchedThreads / 32];
     int warp32[kSchedThreads / 32];
+    int pages[kSchedThreads];            // with one entry per thread: its pages, so that none is looked up again
 };
 
 template <int kSchedThreads, typename Entries>
@@ -64,7 +65,9 @@ __device__ void schedule_body(ScheduleShared<kSchedThreads> &sh, const Entries &
         const int t = seqlens[i];
         bad |= t < 0;
         cost += pages_of(t) + fixed_cost;
+        if (chunk == 1) sh.pages[i] = pages_of(t);
     }
+    auto entry_pages = [&](int i) { return chunk == 1 ? sh.pages[i] : pages_of(seqlens[i]); };
     if (bad) atomicOr(status, MLA_DEVERR_SEQLEN);
     long long total;
     const long long first_unit = block_exclusive_scan<kSchedThreads>(cost, s_warp64, &total);
@@ -75,17 +78,22 @@ __device__ void schedule_body(ScheduleShared<kSchedThreads> &sh, const Entries &
     // batch is smaller and that is estimated to finish sooner.  A candidate
     // with quota q costs q, plus F + C when a part would start strictly
     // inside some sequence's pages (a multiple of q in (S_b + F, S_{b+1})).
+    // (quotients of a line below 2^31 units, which 64-bit division is five times slower at)
+    const bool narrow = total < 0x7fffffffll - num_parts - fixed_cost;
+    auto div = [&](long long a, long long b) {
+        return narrow ? (long long)((unsigned)a / (unsigned)b) : a / b;
+    };
     const long long q_all = (total + num_parts - 1) / num_parts;  // total >= batch * F > 0
     const long long q_seq = (total + batch - 1) / batch;
     bool cut_all = false, cut_seq = false;
     if (batch < num_parts) {
         long long u = first_unit;
         for (int i = i0; i < i1; ++i) {
-            const int n = pages_of(seqlens[i]);
+            const int n = entry_pages(i);
             const long long next = u + n + fixed_cost;
             if (n > 0) {
-                cut_all |= (next - 1) / q_all > (u + fixed_cost) / q_all;
-                cut_seq |= (next - 1) / q_seq > (u + fixed_cost) / q_seq;
+                cut_all |= div(next - 1, q_all) > div(u + fixed_cost, q_all);
+                cut_seq |= div(next - 1, q_seq) > div(u + fixed_cost, q_seq);
             }
             u = next;
         }
@@ -113,7 +121,7 @@ __device__ void schedule_body(ScheduleShared<kSchedThreads> &sh, const Entries &
         long long u = s_start[lo];
         int i = lo * chunk;
         while (true) {
-            const long long c = pages_of(seqlens[i]) + fixed_cost;
+            const long long c = entry_pages(i) + fixed_cost;
             if (x < u + c) break;
             u += c;
             ++i;
@@ -131,7 +139,7 @@ __device__ void schedule_body(ScheduleShared<kSchedThreads> &sh, const Entries &
         if (p + 1 < num_parts) cursor((long long)(p + 1) * quota, b1, pg1, s1);
         // parts touching b0 before p: the one holding its page 0, then every
         // part that started inside its pages (the first at floor((S + F) / Q) + 1)
-        const int split0 = pg0 > 0 ? (int)(p - (s0 + fixed_cost) / quota) : 0;
+        const int split0 = pg0 > 0 ? (int)(p - div(s0 + fixed_cost, quota)) : 0;
         int32_t *row = metadata + (size_t)p * kMdInts;  // 4-byte alignment is all the caller promises
         row[0] = b0;
         row[1] = pg0;
@@ -148,9 +156,9 @@ __device__ void schedule_body(ScheduleShared<kSchedThreads> &sh, const Entries &
     {
         long long u = first_unit;
         for (int i = i0; i < i1; ++i) {
-            const int n = pages_of(seqlens[i]);
+            const int n = entry_pages(i);
             const long long next = u + n + fixed_cost;
-            segs += 1 + (n > 0 ? (int)((next - 1) / quota - (u + fixed_cost) / quota) : 0);
+            segs += 1 + (n > 0 ? (int)(div(next - 1, quota) - div(u + fixed_cost, quota)) : 0);
             u = next;
         }
     }
@@ -159,9 +167,9 @@ __device__ void schedule_body(ScheduleShared<kSchedThreads> &sh, const Entries &
     {
         long long u = first_unit;
         for (int i = i0; i < i1; ++i) {
-            const int n = pages_of(seqlens[i]);
+            const int n = entry_pages(i);
             const long long next = u + n + fixed_cost;
-            run += 1 + (n > 0 ? (int)((next - 1) / quota - (u + fixed_cost) / quota) : 0);
+            run += 1 + (n > 0 ? (int)(div(next - 1, quota) - div(u + fixed_cost, quota)) : 0);
             num_splits[i + 1] = run;
             u = next;
         }

@@ -64,6 +64,8 @@ __global__ void __launch_bounds__(kSelectThreads) select_pages_kernel(const Sele
     __shared__ int s_pick[2];
     sm103::griddep_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    // (letting the split-KV launch start its prologue meanwhile measured 4-5 us
+    // slower on 64 tokens: its CTAs take the SMs before the selection's last ones)
     if (blockIdx.x == 0) {
         const int tiles = (p.h_q + MLA_TILE_ROWS - 1) / MLA_TILE_ROWS;
         schedule_body(s_sched, SelectedLengths{p, tiles}, p.batch * p.s_q * tiles, p.num_parts, kFixedCost, kCombineCost,

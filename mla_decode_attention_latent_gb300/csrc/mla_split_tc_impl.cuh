@@ -1338,8 +1338,8 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
 //         with 128, where the error of o grew from 0.0017 to 0.0018); set anew, the largest then at 28..56, when a weight would pass
 //         448 and with every new maximum, never so that what O holds would grow
 //         (negative: no weight so far)
-//   parts h = the upper 4 bits of w by w (2^7 + 1) - (w (2^7 + 1) - w) in f16, l = w - h
-//         (exact): off by about 2^-8 of w, or by 2^-9 where the largest is at least 3.5
+//   parts h = e4m3(w), l = e4m3(w - h), the difference exact in f16: off by about
+//         2^-8 of w, or by 2^-10 where the first page's largest is at least 3.5
 #if MLA_SPLIT_FP8 && MLA_SPLIT_TREE
 __device__ void score_rows_e8(const DecodeParams &p, const Ctx &c, uint32_t tmem, int part) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1546,7 +1546,7 @@ __device__ void score_rows_e8(const DecodeParams &p, const Ctx &c, uint32_t tmem
                     uint32_t hi[4], lo[4];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        uint32_t h16[2], l16[2];
+                        uint32_t w16[2], l16[2];
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             const int j = 2 * q + e;
@@ -1556,11 +1556,11 @@ __device__ void score_rows_e8(const DecodeParams &p, const Ctx &c, uint32_t tmem
                             float wa, wb;
                             f2_unpack(f2_fma(p2, cs2[j], zero2), wa, wb);
                             wa4[e] = max3f(wa4[e], fabsf(wa), fabsf(wb));
-                            const uint32_t w16 = pack_f16(wa, wb), t16 = f16x2_mul(w16, 0x58085808u);  // 129
-                            h16[e] = f16x2_sub(t16, f16x2_sub(t16, w16));
-                            l16[e] = f16x2_sub(w16, h16[e]);
+                            w16[e] = pack_f16(wa, wb);
                         }
-                        hi[q] = pack_e4m3x4_f16(h16[0], h16[1]);
+                        hi[q] = pack_e4m3x4_f16(w16[0], w16[1]);
+                        l16[0] = f16x2_sub(w16[0], e4m3x2_to_f16x2(hi[q]));
+                        l16[1] = f16x2_sub(w16[1], e4m3x2_to_f16x2(hi[q] >> 16));
                         lo[q] = pack_e4m3x4_f16(l16[0], l16[1]);
                     }
                     if (write) {  // 16 codes of the upper parts, and of the lower ones 64 bytes behind

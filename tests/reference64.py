@@ -77,8 +77,9 @@ def select(score, n: int, topk: int, sink: int, local: int):
     return sorted(list(range(sink)) + mid + list(range(n - local, n)))
 
 
-def attend(q: torch.Tensor, rows: torch.Tensor, scale: float):
-    """(o [h, 512], lse [h], a [h, 512]) of q [h, d] over rows [t, d]; a = sum of weight * |value|."""
+def attend(q: torch.Tensor, rows: torch.Tensor, scale: float, fp8: bool = False):
+    """(o [h, 512], lse [h], a [h, 512]) of q [h, d] over rows [t, d]; a = sum of weight * |value|, for an e4m3
+    cache with the further term of assert_attention."""
     h = q.shape[0]
     if rows.shape[0] == 0:
         return torch.zeros((h, DV), dtype=torch.float64), torch.full((h,), -math.inf, dtype=torch.float64), \
@@ -86,17 +87,24 @@ def attend(q: torch.Tensor, rows: torch.Tensor, scale: float):
     z = q.double() @ rows.T * scale
     lse = torch.logsumexp(z, 1)
     p = torch.exp(z - lse[:, None])
-    return p @ rows[:, :DV], lse, p @ rows[:, :DV].abs()
+    a = p @ rows[:, :DV].abs()
+    if fp8:
+        c = rows.abs().amax(1) / 448  # the row's scale (1 for a row of zeros, whose values are 0)
+        c = torch.where(c > 0, c, torch.ones_like(c))
+        a = a + (p * c).amax(1, keepdim=True) / 8 * (rows[:, :DV].abs() / c[:, None]).sum(0)
+    return p @ rows[:, :DV], lse, a
 
 
 def assert_attention(o, lse, o_ref, lse_ref, a_ref, fp8: bool, what=""):
     """o and lse against 64 bits.
 
-    Rounding o to bf16 is off by at most 2^-8 |o|.  The weights are rounded to bf16 (2^-8 each; f16 in the
-    e4m3 kernel, 2^-11, where instead the three-part query is off by up to 2^-12 per element and the scores
-    with it), and a score's fp32 accumulation adds less than 2^-11 of its weight, so the sum over the values
-    is off by at most (2^-8 + 2^-11) * sum of weight * |value| (e4m3: the score error dominates, bounded
-    here by the same amount).  LSE: 2e-3, the library's bound for both caches."""
+    Rounding o to bf16 is off by at most 2^-8 |o|.  The weights are rounded to bf16 (2^-8 each), and a score's
+    fp32 accumulation adds less than 2^-11 of its weight, so the sum over the values is off by at most
+    (2^-8 + 2^-11) * a, a = sum of weight * |value|.  e4m3: a weight times its token's scale, w_j = p_j c_j, is held
+    in two e4m3 parts, each off by half a step: 2^-4 * 2^-4 of w_j, or half the smallest step, 2^-10, where the
+    largest weight of the segment's first page is at least 3.5; 2^-10 / 3.5 < 2^-11 of the largest w, which adds
+    2^-11 max w * sum |code| = 2^-8 * (max w / 8) * sum |value| / c to the bound: the term that attend adds to a.
+    LSE: 2e-3, the library's bound for both caches."""
     o, lse = o.double().cpu(), lse.double().cpu()
     inf = torch.isneginf(lse_ref)
     assert torch.equal(torch.isneginf(lse), inf), f"{what}: pattern of empty rows"

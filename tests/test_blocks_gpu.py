@@ -45,7 +45,7 @@ def reference(q, cache, table, lens, keys, scales, topk, sink, local, causal, sc
             pages[i, j, :len(pick)] = torch.tensor(pick, dtype=torch.int32)
             k = [rows[int(table[i, p])][:min(64, L - 64 * p)] for p in pick]
             k = torch.cat(k) if k else torch.zeros((0, d), dtype=torch.float64)
-            o[i, j], lse[i, j], a[i, j] = R.attend(q[i, j], k, scale)
+            o[i, j], lse[i, j], a[i, j] = R.attend(q[i, j], k, scale, cache.dtype != torch.bfloat16)
     return o, lse, a, pages
 
 

@@ -49,7 +49,7 @@ def reference(q, cache, table, lens, sees, nodes, scale):
         flat = torch.cat([rows[int(table[i, p])] for p in range((T + 63) // 64)] + [torch.zeros((0, d), dtype=torch.float64)])[:T]
         for j in range(n):
             see = [p for p in range(T) if p < T - n or sees[i][j, p - (T - n)]]
-            o[i, j], lse[i, j], a[i, j] = R.attend(q[i, j], flat[see], scale)
+            o[i, j], lse[i, j], a[i, j] = R.attend(q[i, j], flat[see], scale, cache.dtype != torch.bfloat16)
     return o, lse, a
 
 
@@ -114,7 +114,7 @@ def test_sequence_shorter_than_its_tree(dev, fp8):
         flat = torch.cat([rows[int(table[i, p])] for p in range((T + 63) // 64)])[:T]
         for j in range(80):
             see = [p for p in range(T) if sees[i][j, p - (T - 80)]]
-            r = R.attend(q[i, j], flat[see], 576 ** -0.5)
+            r = R.attend(q[i, j], flat[see], 576 ** -0.5, fp8)
             R.assert_attention(o[i, j], lse[i, j], *r, fp8, f"{i} {j}")
 
 
