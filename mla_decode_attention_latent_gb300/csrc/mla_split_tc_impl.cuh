@@ -200,7 +200,10 @@ static_assert(kE4PageBytes % 16 == 0 && kE4ScaleOff % 16 == 0, "TMA and bulk-cop
 constexpr uint32_t kKRingOff = 0;
 constexpr uint32_t kQRopeOff = kKRingOff + (kSparse ? kVStages * kVStageBytes : kKSlots * kSlotBytes);
 constexpr uint32_t kQRopePartBytes = kTileRows * (kFp8 ? 64 : 128);  // one part's [128 rows] RoPE tile
-constexpr uint32_t kStageOff = kQRopeOff + (kQRopeSmem ? kQParts * kQRopePartBytes : 0);
+// (draft trees, bf16: Q's rows are turned through the RoPE tile, or a tile of its size)
+constexpr bool kTurnQ = kTree && !kFp8;
+constexpr uint32_t kStageOff =
+    kQRopeOff + (kQRopeSmem ? kQParts * kQRopePartBytes : kTurnQ ? (uint32_t)kTileRows * 128u : 0u);
 constexpr uint32_t kScaleOff = kStageOff + kPBufs * kPMsgBytes;   // the side ring of the steps in flight
 // several groups: the running state that each leaves for the next page's,
 // [group][maximum, row sum, weight scale][128 rows] fp32
@@ -1095,6 +1098,60 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
                         }
                         fence_proxy_async_smem();
                     }
+                }
+                tmem_wait_st();
+            } else if constexpr (kTurnQ) {
+                // Q row r into TMEM lane r (columns 0..255, bf16 pairs) and row r of
+                // the RoPE tile.  A thread that reads its own row touches 32 lines
+                // with every warp load (5.6 us a tile, a third of a one-page
+                // decode); here eight lanes read 128 contiguous bytes of a row, and
+                // the rows turn through the RoPE tile, 64 dims of the warp's own 32
+                // rows at a time, the RoPE chunk last.
+                const int row0 = 32 * (warp & 3), sub = lane & 7, first = gr - lane;  // first: row 0 of the warp
+                const uint32_t tile_s = smem_u32(c.base + kQRopeOff) + (uint32_t)row0 * 128u;
+                const uint4 *src = reinterpret_cast<const uint4 *>(p.q + ((size_t)s.b * p.rows + first) * kD);
+                auto load8 = [&](uint4 (&x)[8], int ch) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int row = 4 * i + (lane >> 3);
+                        x[i] = first + row < p.rows ? __ldg(src + (size_t)row * (kD / 8) + ch * 8 + sub) : make_uint4(0, 0, 0, 0);
+                    }
+                };
+                auto put8 = [&](const uint4 (&x)[8]) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int row = 4 * i + (lane >> 3);
+                        sts128(tile_s + (uint32_t)row * 128u + 16u * (uint32_t)(sub ^ (row & 7)), x[i].x, x[i].y, x[i].z, x[i].w);
+                    }
+                };
+#pragma unroll 1
+                for (int ch0 = 0; ch0 < kLatChunks; ch0 += 4) {
+                    uint4 x[4][8];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) load8(x[k], ch0 + k);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        __syncwarp();  // the chunk before has been read
+                        put8(x[k]);
+                        __syncwarp();
+                        uint32_t v[32];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const uint4 y = lds128(tile_s + (uint32_t)lane * 128u + 16u * (uint32_t)(j ^ (lane & 7)));
+                            v[4 * j] = y.x;
+                            v[4 * j + 1] = y.y;
+                            v[4 * j + 2] = y.z;
+                            v[4 * j + 3] = y.w;
+                        }
+                        tmem_st32(tmem + lane_base + (ch0 + k) * 32, v);
+                    }
+                }
+                if constexpr (kHasRope) {
+                    uint4 x[8];
+                    load8(x, kLatChunks);
+                    __syncwarp();
+                    put8(x);
+                    fence_proxy_async_smem();
                 }
                 tmem_wait_st();
             } else {
