@@ -547,8 +547,10 @@ MLA_API size_t mla_tree_workspace_bytes(int batch, int s_q, int h_q, int h_kv, i
  *   argument: a chain's mask is the causal one).  T_b < n_b drops the nodes that
  *   would lie before the sequence.
  * A cached row that some query token of its sequence sees must be finite (a
- * non-finite one makes that token's output NaN, and may make that of the tokens
+ * non-finite one makes that token's o and lse NaN, and may make those of the tokens
  * of the same 128-row tile); a node's row that no token sees may hold any bits.
+ * A query row that is not finite and sees something gets o = lse = NaN, and leaves
+ * the other rows as they are.
  */
 MLA_API int mla_decode_kvcache_tree(const void *q, const void *kcache, int64_t num_blocks, const int32_t *block_table,
                                     int max_blocks_per_seq, const int32_t *cache_seqlens, const int32_t *tree_mask,

@@ -372,6 +372,14 @@ def _need_rows(name: str, t: torch.Tensor, cols: int, n: int, dev: torch.device,
     return stride
 
 
+def _row_count(latent) -> int:
+    if not isinstance(latent, torch.Tensor):
+        raise TypeError("latent must be a torch.Tensor")
+    if latent.dim() != 2:
+        raise ValueError(f"latent must be [n, {MLA_V_DIM}]")
+    return latent.shape[0]
+
+
 def _paged_args(cache, block_table, fp8):
     """Check a paged cache and its table; returns (num_blocks, d, b, max_blocks, device, address of the table)."""
     if fp8:
@@ -440,14 +448,14 @@ def mla_cache_write(latent: torch.Tensor, k_rope: Optional[torch.Tensor], kcache
     ``starts[b], starts[b] + 1, ...`` of sequence b; without ``cu_rows`` every
     sequence has n / b rows.  Rows behind ``cu_rows[b]`` are ignored.  The
     inputs may be slices of wider rows (strides of a multiple of 8 elements)."""
-    _cache_rows("mla_cache_write", kcache, block_table, starts, latent.shape[0], cu_rows, latent, k_rope, False, True)
+    _cache_rows("mla_cache_write", kcache, block_table, starts, _row_count(latent), cu_rows, latent, k_rope, False, True)
 
 
 def mla_cache_write_fp8(latent: torch.Tensor, k_rope: torch.Tensor, kv_pages: torch.Tensor,
                         block_table: torch.Tensor, starts: torch.Tensor, cu_rows: Optional[torch.Tensor] = None) -> None:
     """``mla_cache_write`` into packed e4m3 pages (uint8 [num_blocks, MLA_FP8_PAGE_BYTES(576)]): each row is
     quantised as it is written, with its own scale max |x| / 448."""
-    _cache_rows("mla_cache_write_fp8", kv_pages, block_table, starts, latent.shape[0], cu_rows, latent, k_rope, True,
+    _cache_rows("mla_cache_write_fp8", kv_pages, block_table, starts, _row_count(latent), cu_rows, latent, k_rope, True,
                 True)
 
 
@@ -560,6 +568,8 @@ def _decode_blocks(call, q, cache, block_table, cache_seqlens, page_keys, page_s
     topk_pages, sink_pages, local_pages = int(topk_pages), int(sink_pages), int(local_pages)
     if sink_pages < 0 or local_pages < 1 or topk_pages < sink_pages + local_pages:
         raise ValueError("topk_pages must cover sink_pages (>= 0) and local_pages (>= 1)")
+    if topk_pages * _lib.MLA_PAGE_SIZE > 0x7fffffff:
+        raise ValueError("topk_pages is too large")
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(d)
     num_parts = _pairs(dev.index)

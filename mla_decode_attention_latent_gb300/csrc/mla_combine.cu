@@ -57,7 +57,13 @@ combine_kernel(const float *__restrict__ o_accum, const float *__restrict__ lse_
     // lane s keeps L_s of partial s (partials past 32 are read again below)
     const float l_own = lane < n ? lse_accum[(size_t)(first + lane) * rows + row] : -CUDART_INF_F;
     float m = l_own;
-    for (int s = lane + 32; s < n; s += 32) m = fmaxf(m, lse_accum[(size_t)(first + s) * rows + row]);
+    bool spoilt = kTiles && l_own != l_own;  // a partial that is no number: so is the result
+    for (int s = lane + 32; s < n; s += 32) {
+        const float l = lse_accum[(size_t)(first + s) * rows + row];
+        m = fmaxf(m, l);
+        spoilt |= kTiles && l != l;
+    }
+    if (kTiles) spoilt = __any_sync(0xffffffffu, spoilt);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
 
@@ -66,7 +72,7 @@ combine_kernel(const float *__restrict__ o_accum, const float *__restrict__ lse_
 #pragma unroll
     for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
     float total_lse = -CUDART_INF_F;
-    if (m != -CUDART_INF_F) {
+    if (m != -CUDART_INF_F || spoilt) {
         float sum = lane < n ? __expf(l_own - m) : 0.f;
         for (int s = lane + 32; s < n; s += 32) sum += __expf(lse_accum[(size_t)(first + s) * rows + row] - m);
 #pragma unroll

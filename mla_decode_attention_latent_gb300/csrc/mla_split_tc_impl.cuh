@@ -977,6 +977,11 @@ __device__ void value_mma(const DecodeParams &p, const Ctx &c, uint32_t tmem, in
     }
 }
 
+// A row's sum l of weights: its inverse, and its LSE where l is not positive.  0:
+// the row saw nothing.  Draft trees: a NaN (a score was no number) makes the row NaN.
+__device__ __forceinline__ float inverse_sum(float l) { return l > 0.f ? 1.f / l : kTree && l != 0.f ? l : 0.f; }
+__device__ __forceinline__ float no_lse(float l) { return kTree && l != 0.f ? l : -CUDART_INF_F; }
+
 // Score-CTA row warps: Q -> TMEM and smem, masked online softmax, P and row
 // factors -> staging -> bulk copies into the value CTA, each warp sending its
 // own 32 rows as soon as they are staged.
@@ -1295,8 +1300,10 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
             }
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-                mx4[j & 3] = max3f(mx4[j & 3], __uint_as_float(sr[2 * j]), __uint_as_float(sr[2 * j + 1]));
-            const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * fsc;
+                mx4[j & 3] = kTree ? max3f_nan(mx4[j & 3], __uint_as_float(sr[2 * j]), __uint_as_float(sr[2 * j + 1]))
+                                   : max3f(mx4[j & 3], __uint_as_float(sr[2 * j]), __uint_as_float(sr[2 * j + 1]));
+            const float mx = (kTree ? max3f_nan(max3f_nan(mx4[0], mx4[1], mx4[2]), mx4[3], mx4[3])
+                                    : fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]))) * fsc;
             float fac = 1.f;
             if (mx > m + kRescaleLog2 || (m == -CUDART_INF_F && mx > -CUDART_INF_F)) {
                 fac = ex2(m - mx);  // 0 when m was -inf
@@ -1308,6 +1315,8 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
             if (m == -CUDART_INF_F) {
 #pragma unroll
                 for (int j = 0; j < 32; ++j) pk[j] = 0u;
+                // nothing visible so far, or a score that is no number: the sum keeps that
+                if constexpr (kTree) sum2[0] = f2_pack(mx == -CUDART_INF_F ? 0.f : mx, 0.f);
             } else {
                 const uint64_t sc2 = f2_pack(fsc, fsc), nm2 = f2_pack(-m, -m);
 #pragma unroll
@@ -1341,7 +1350,7 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
             for (int j = 0; j < 8; ++j)
                 sts128(stage_s + r * 128 + 16 * (j ^ (r & 7)), pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
             sts32(stage_s + kFacOff + 4 * r, __float_as_uint(fac));
-            if (pg == s.p1 - 1) sts32(stage_s + kInvLOff + 4 * r, __float_as_uint(l > 0.f ? 1.f / l : 0.f));
+            if (pg == s.p1 - 1) sts32(stage_s + kInvLOff + 4 * r, __float_as_uint(inverse_sum(l)));
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
@@ -1359,7 +1368,7 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
         }
         // LSE of this row over the segment (natural log)
         if (row_ok) {
-            const float lse_row = l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : -CUDART_INF_F;
+            const float lse_row = l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : no_lse(l);
             if (s.n_split <= 1) {
                 p.lse[(size_t)s.b * p.rows + gr] = lse_row;
             } else {
@@ -1738,7 +1747,7 @@ __device__ void score_rows_e8(const DecodeParams &p, const Ctx &c, uint32_t tmem
 
             const bool last = pg == s.p1 - 1;
             sts32(stage_s + kFacOff + 4 * r, __float_as_uint(fac));
-            if (last) sts32(stage_s + kInvLOff + 4 * r, __float_as_uint(L > 0.f ? 1.f / L : 0.f));
+            if (last) sts32(stage_s + kInvLOff + 4 * r, __float_as_uint(inverse_sum(L)));
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
@@ -1756,7 +1765,7 @@ __device__ void score_rows_e8(const DecodeParams &p, const Ctx &c, uint32_t tmem
         // its last page; L counts in units of |ko| 2^-m
         if (row_ok && (s.p1 > s.p0 ? (int)((it - 1) % kGroups) == grp : grp == 0)) {
             const float lk = (float)((int)(__float_as_uint(fabsf(ko)) >> 23) - 127);
-            const float lse_row = L > 0.f ? (m - lk + __log2f(L)) * 0.69314718055994531f : -CUDART_INF_F;
+            const float lse_row = L > 0.f ? (m - lk + __log2f(L)) * 0.69314718055994531f : no_lse(L);
             if (s.n_split <= 1) {
                 p.lse[(size_t)s.b * p.rows + gr] = lse_row;
             } else {

@@ -210,3 +210,42 @@ def test_two_streams_and_a_graph(dev):
         assert torch.equal(out[2].cpu(), want[i][3])
         R.assert_attention(out[0], out[1], *want[i][:3], False)
     assert mla.mla_device_status() == 0
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_pages_far_into_a_large_pool(dev, fp8):
+    """Pages whose offsets pass 2^32, and their keys, give the results of the same ones at the pool's start."""
+    lens = [900, 300]
+    q, cache, table, keys, scales = make(lens, 2, 48, 576, fp8, seed=21)
+    want = decode(dev, q, cache, table, lens, keys, scales, 4)
+    n = cache.shape[0]
+    nblk = 2 ** 32 // (64 * 576) + 64
+    pool = torch.empty((nblk, *cache.shape[1:]), dtype=cache.dtype, device=dev)
+    pool[-n:] = cache.to(dev)
+    far_keys = torch.empty((nblk, 576), dtype=torch.int8, device=dev)
+    far_scales = torch.empty((nblk,), device=dev)
+    far_keys[-n:], far_scales[-n:] = keys.to(dev), scales.to(dev)
+    got = decode(dev, q, pool, table + (nblk - n), lens, far_keys, far_scales, 4)
+    assert mla.mla_device_status() == 0
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def test_a_workspace_and_outputs_of_the_caller(dev):
+    """A workspace full of NaN that a second call of other lengths reuses; outputs that held something else."""
+    lens = [900, 300, 64]
+    q, cache, table, keys, scales = make(lens, 2, 48, 576, seed=22)
+    need = mla.mla_blocks_workspace_bytes(3, 2, 48, 1, 512, table.shape[1], 4, mla.mla_num_sm_parts(1, 1, dev))
+    ws = torch.full((need,), 0xff, dtype=torch.uint8, device=dev)
+    out = torch.full((3, 2, 48, 512), 7.0, dtype=torch.bfloat16, device=dev)
+    lse = torch.full((3, 2, 48), 7.0, device=dev)
+    pages = torch.full((3, 2, 4), 7, dtype=torch.int32, device=dev)
+    for now in (lens, [0, 70, 64], [500, 1, 3]):
+        ref = reference(q, cache, table, now, keys, scales, 4, 1, 1, True, 576 ** -0.5)
+        got = decode(dev, q, cache, table, now, keys, scales, 4, causal=True, out=out, lse=lse, pages=pages, workspace=ws)
+        assert mla.mla_device_status() == 0 and got[0] is out and got[2] is pages
+        assert torch.equal(pages.cpu(), ref[3])
+        R.assert_attention(out, lse, *ref[:3], False)
+    with pytest.raises(RuntimeError, match="workspace"):
+        decode(dev, q, cache, table, lens, keys, scales, 4, workspace=ws[:need - 256])
+    with pytest.raises(ValueError, match="too large"):
+        decode(dev, q, cache, table, lens, keys, scales, 1 << 26)

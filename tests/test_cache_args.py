@@ -148,6 +148,16 @@ def test_tensors_of_the_host_are_refused():
             call()
 
 
+def test_rows_that_are_not_a_matrix_are_refused():
+    cache, table = torch.zeros((2, 64, 1, 576), dtype=torch.bfloat16), torch.zeros((1, 2), dtype=torch.int32)
+    for call in (mla.mla_cache_write, mla.mla_cache_write_fp8):
+        with pytest.raises(TypeError, match="torch.Tensor"):
+            call([[0.0] * 512], None, cache, table, table[:, 0])
+        for shape in ((), (512,), (1, 1, 512)):
+            with pytest.raises(ValueError, match="latent must be"):
+                call(torch.zeros(shape, dtype=torch.bfloat16), None, cache, table, table[:, 0])
+
+
 # ---------------------------------------------------------------- the tests' own restatements
 def test_page_key_of_known_pages():
     rows = torch.zeros((2, 4), dtype=torch.float64)

@@ -330,3 +330,71 @@ def test_scales_of_many_sizes(dev, order, num_parts):
     q = (torch.randn((2, s_q, h, 576), generator=g) * 2.0 ** -9).to(torch.bfloat16)
     cache = W.pack_e4m3_pages(rows)
     check(dev, q, cache, table, lens, np.stack([R.ancestors([-1, 0])] * 2), num_parts=num_parts)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("num_parts", [1, 5])
+def test_a_query_that_is_not_finite_spoils_its_own_row_only(dev, fp8, bad, num_parts):
+    """The heads of a token share a tile, and their maxima one decision: the other rows keep their bits."""
+    lens = [700, 90]
+    q, cache, table, sees = make(lens, 4, 24, 576, fp8, seed=11)
+    o, lse = decode(dev, q, cache, table, lens, sees, num_parts=num_parts)
+    spoilt = q.clone()
+    spoilt[0, 1, 5, 100] = bad
+    o2, lse2 = decode(dev, spoilt, cache, table, lens, sees, num_parts=num_parts)
+    assert mla.mla_device_status() == 0
+    keep = torch.ones(o.shape[:3], dtype=torch.bool)
+    keep[0, 1, 5] = False
+    assert torch.equal(o[keep], o2[keep]) and torch.equal(lse[keep], lse2[keep])
+    assert bool(torch.isnan(o2[0, 1, 5]).all()) and bool(torch.isnan(lse2[0, 1, 5]))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_pages_far_into_a_large_pool(dev, fp8):
+    """Pages whose byte and element offsets pass 2^32 give the results of the same pages at the pool's start."""
+    lens, s_q, h = [300, 130], 5, 32
+    q, cache, table, sees = make(lens, s_q, h, 576, fp8, seed=12)
+    want = decode(dev, q, cache, table, lens, sees)
+    n = cache.shape[0]
+    nblk = 2 ** 32 // (64 * 576) + 64
+    pool = torch.empty((nblk, *cache.shape[1:]), dtype=cache.dtype, device=dev)
+    pool[-n:] = cache.to(dev)
+    got = decode(dev, q, pool, table + (nblk - n), lens, sees)
+    assert mla.mla_device_status() == 0
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_a_workspace_and_outputs_of_the_caller(dev, fp8):
+    """A workspace full of NaN, reused by a second call of other lengths; outputs that held something else."""
+    lens, s_q, h = [1000, 64, 333], 6, 40
+    q, cache, table, sees = make(lens, s_q, h, 576, fp8, seed=13)
+    need = mla.mla_tree_workspace_bytes(3, s_q, h, 1, 512, mla.mla_num_sm_parts(1, 1, dev))
+    ws = torch.full((need,), 0xff, dtype=torch.uint8, device=dev)
+    out = torch.full((3, s_q, h, 512), 7.0, dtype=torch.bfloat16, device=dev)
+    lse = torch.full((3, s_q, h), 7.0, device=dev)
+    check(dev, q, cache, table, lens, sees, out=out, lse=lse, workspace=ws)
+    short = [70, 6, 65]
+    o, l2 = check(dev, q, cache, table, short, sees, out=out, lse=lse, workspace=ws)
+    assert o is out and l2 is lse
+    with pytest.raises(RuntimeError, match="workspace"):
+        decode(dev, q, cache, table, lens, sees, workspace=ws[:need - 256])
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("num_parts", [1, 5])
+def test_a_visible_key_that_is_not_finite_shows(dev, fp8, num_parts):
+    """In one part of a cut sequence, or in the only one: o and lse of the tokens that see it are NaN."""
+    lens, s_q, h = [700, 90], 1, 128
+    q, cache, table, sees = make(lens, s_q, h, 576, fp8, seed=14)
+    want = decode(dev, q, cache, table, lens, sees, num_parts=num_parts)
+    blk, off = R.place(table, 0, 130)
+    if fp8:
+        cache[blk, off * 576:(off + 1) * 576] = 0x7f
+    else:
+        cache[blk, off] = float("nan")
+    o, lse = decode(dev, q, cache, table, lens, sees, num_parts=num_parts)
+    assert mla.mla_device_status() == 0
+    assert bool(torch.isnan(o[0]).all()) and bool(torch.isnan(lse[0]).all())
+    assert torch.equal(o[1], want[0][1]) and torch.equal(lse[1], want[1][1])
