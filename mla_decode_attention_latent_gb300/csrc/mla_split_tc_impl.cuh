@@ -83,7 +83,7 @@
 //           weight, lowered lazily like the running maximum, carried by O and
 //           divided out at the end) are split into two e4m3 parts as well, and the V codes
 //           are MN-major operands as they land: nothing is widened, a stage is
-//           32 KB and four are in flight.
+//           32 KB and three are in flight.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
@@ -150,9 +150,12 @@ constexpr int kStepPages = (kFp8 || kSparse) ? 1 : 2;
 // so that each SM's gather engine moves about half of a page's rows.
 constexpr int kKSlots = kFp8 ? 4 : (kSparse ? 2 : 10);
 constexpr int kRingSlots = kKSlots / kScoreIssuers;  // slots per score-MMA issuer's ring
-constexpr int kVStages = kE8 ? 4 : 2;          // value CTA ring: whole pages (dims 0..511)
+constexpr int kVStages = kE8 ? 3 : 2;          // value CTA ring: whole pages (dims 0..511)
 constexpr int kSBufs = kE8 ? 3 : 2;            // S buffers in TMEM (score CTA), one per step
-constexpr int kPBufs = kE8 ? 3 : 2;                      // P buffers (staging in the score CTA, landing in the value CTA)
+// P buffers (staging in the score CTA, landing in the value CTA).  fp8 products: a
+// group holds one from before its pass until P V has used it, so that with one per
+// group they bound the pace (1.08 us a page; four, and three V stages: 1.04)
+constexpr int kPBufs = kE8 ? 4 : 2;
 constexpr int kKChunks = kD / 64;              // 9 (or 8) chunks of 64 dims (128 B rows)
 constexpr int kVChunks = kDv / 64;             // 8
 constexpr int kLatChunks = kDv / 64;           // 8 latent chunks: the Q part kept in TMEM
@@ -1442,12 +1445,11 @@ __device__ void score_rows_e8(const DecodeParams &p, const Ctx &c, uint32_t tmem
             // 144 t + d / 4 of lane r.  The groups share the nine 64-dim chunks, and
             // put the maximum of the row together in shared memory.
             // As in score_rows, eight lanes read 128 contiguous bytes of a row, and the
-            // rows turn through the group's own P staging (a thread that read its own row
+            // rows turn through a P staging buffer (a thread that read its own row
             // touched 32 lines with every load: a one-page decode took 23.1 us, now 17.2,
             // and 64 x 128 rows of 1536 tokens 49.9, now 44.2).
             constexpr int kOwn = kKChunks / kGroups;
             static_assert(kOwn == 3 && kOwn * kGroups == kKChunks, "chunks of Q per group");
-            static_assert(kPBufs == kGroups, "a group's pages share one P buffer");
             const int sub = lane & 7, first = gr - lane;  // first: row 0 of the warp
             const uint4 *src = reinterpret_cast<const uint4 *>(p.q + ((size_t)s.b * p.rows + first) * kD) + grp * 8 + sub;
             auto load8 = [&](uint4 (&x)[8], int k) {
@@ -1488,8 +1490,9 @@ __device__ void score_rows_e8(const DecodeParams &p, const Ctx &c, uint32_t tmem
             const int row0 = 32 * (warp & 3);
             sts32(tops + 4u * (uint32_t)(grp * kTileRows + row0 + 4 * sub + (lane >> 3)), max(t8[0] >> 16, t8[0] & 0xffffu) << 16);
             mbar_arrive(c.bar(B_QMAX + (warp & 3)));
-            // the group's P staging: the bulk copy of its last page has been consumed
-            const uint32_t turn = it + (uint32_t)((grp + kGroups - (int)(it % kGroups)) % kGroups);  // its next page
+            // P buffer grp is the group's to turn its rows in: what it held has been
+            // consumed, and its next page's P comes after every group's Q
+            const uint32_t turn = it + (uint32_t)((grp + kPBufs - (int)(it % kPBufs)) % kPBufs);
             if (!warp_wait<true>(c, B_PFREE + grp, ((turn / kPBufs) & 1) ^ 1)) return;
             if (!warp_wait(c, B_QMAX + (warp & 3), qseg & 1)) return;
             ++qseg;
@@ -1686,17 +1689,18 @@ __device__ void score_rows_e8(const DecodeParams &p, const Ctx &c, uint32_t tmem
                         L = __uint_as_float(lds32(prev_s + kTileRows * 4));
                         chained = true;
                     }
-                    if (!__all_sync(0xffffffffu, same)) continue;  // once more, on the state that is
                     const bool low = m == -CUDART_INF_F ? xmax == -CUDART_INF_F : xmax <= kRescaleLog2 + lk;
                     const bool fits = wmax <= kE4Max && !(ko < 0.f && wmax > 0.f);
-                    if (!__all_sync(0xffffffffu, low)) {
-                        phase = kMaximum;
-                    } else if (!__all_sync(0xffffffffu, fits)) {
-                        if (!fits) fac = new_scale(wmax / fabsf(ko), kAtLater, fac, ko);
-                        phase = kCodes;
-                    } else {
+                    if (__all_sync(0xffffffffu, same && low && fits)) {
                         L += sum;
                         break;
+                    }
+                    if (!__all_sync(0xffffffffu, same)) continue;  // once more, on the state that is
+                    if (!__all_sync(0xffffffffu, low)) {
+                        phase = kMaximum;
+                    } else {
+                        if (!fits) fac = new_scale(wmax / fabsf(ko), kAtLater, fac, ko);
+                        phase = kCodes;
                     }
                 } else if (phase == kMaximum) {
                     if (xmax > m + kRescaleLog2 || (m == -CUDART_INF_F && xmax > -CUDART_INF_F)) {
