@@ -243,17 +243,11 @@ __global__ void __launch_bounds__(kCtaThreads, 1) page_scores_kernel(const Selec
         return page < u.n ? __ldg(p.block_table + (size_t)u.b * p.max_blocks + page) : 0;
     };
     auto look_up = [&](const UnitAt &u) { return Blocks{block_of(u, srow), block_of(u, srow + 64), block_of(u, row)}; };
-    auto load_keys = [&](Blocks b) {
-        if (b.own < 0 || (int64_t)b.own >= p.num_blocks) atomicOr(p.status, MLA_DEVERR_BLOCK_ID);
-        auto safe = [&](int blk) { return blk < 0 || (int64_t)blk >= p.num_blocks ? 0 : blk; };
-        const uint4 *s0 = reinterpret_cast<const uint4 *>(p.keys + (size_t)safe(b.s0) * D) + quarter;
-        const uint4 *s1 = reinterpret_cast<const uint4 *>(p.keys + (size_t)safe(b.s1) * D) + quarter;
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-            key[c][0] = __ldg(s0 + 4 * c);
-            key[c][1] = __ldg(s1 + 4 * c);
-        }
-        scale = __ldg(p.scales + safe(b.own));
+    auto safe = [&](int blk) { return blk < 0 || (int64_t)blk >= p.num_blocks ? 0 : blk; };
+    auto key_row = [&](int blk) { return reinterpret_cast<const uint4 *>(p.keys + (size_t)safe(blk) * D) + quarter; };
+    auto load_scale = [&](int own) {
+        if (own < 0 || (int64_t)own >= p.num_blocks) atomicOr(p.status, MLA_DEVERR_BLOCK_ID);
+        scale = __ldg(p.scales + safe(own));
     };
     // codes of heads h0 .. h0 + heads - 1 of a token, widened into shared memory
     auto load_heads = [&](const UnitAt &u, int h0, int heads) {
@@ -304,7 +298,14 @@ __global__ void __launch_bounds__(kCtaThreads, 1) page_scores_kernel(const Selec
             u.tok = s_first[1] / u.tiles;
             u.tile = s_first[1] - u.tok * u.tiles;
             set_token(u);
-            load_keys(look_up(u));
+            const Blocks b = look_up(u);
+            const uint4 *s0 = key_row(b.s0), *s1 = key_row(b.s1);
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+                key[c][0] = __ldg(s0 + 4 * c);
+                key[c][1] = __ldg(s1 + 4 * c);
+            }
+            load_scale(b.own);
         }
         // the unit after this one, and its block ids
         UnitAt next = u;
@@ -381,6 +382,11 @@ __global__ void __launch_bounds__(kCtaThreads, 1) page_scores_kernel(const Selec
                     held_tok = u.tok;
                     held_h = h0;
                 }
+                // with a unit's last heads the next unit's keys replace its own piece by
+                // piece: their loads spread over the staging (all at once behind it
+                // they queue up: 36.5 us for 64 tokens of 1024 pages and 128 heads, now MEASURED)
+                const bool ahead = h0 + kHeadChunk >= p.h_q && k + 1 < todo;
+                const uint4 *s0 = key_row(next_blocks.s0), *s1 = key_row(next_blocks.s1);
 #pragma unroll
                 for (int c = 0; c < kChunks; ++c, ++fill) {
                     const uint32_t st = fill % kStages;
@@ -400,10 +406,13 @@ __global__ void __launch_bounds__(kCtaThreads, 1) page_scores_kernel(const Selec
                     }
                     fence_proxy_async_smem();  // these and the heads, before the MMAs that the arrival lets go
                     mbar_arrive(bars + B_FULL + st);
+                    if (ahead) {
+                        key[c][0] = __ldg(s0 + 4 * c);
+                        key[c][1] = __ldg(s1 + 4 * c);
+                    }
                 }
-                // the next unit's keys travel while products finish and are read
-                if (h0 + kHeadChunk >= p.h_q && k + 1 < todo) {
-                    load_keys(next_blocks);
+                if (ahead) {
+                    load_scale(next_blocks.own);
                     if (k + 2 < todo) {
                         advance(after);
                         after_blocks = look_up(after);
