@@ -11,12 +11,20 @@
 // while consecutive units share the token).  Pages are the rows of D, so a
 // thread reads the products of its page out of its TMEM lane and the maximum
 // over the heads needs no exchange but between the two threads that share a
-// page's heads.  The keys arrive as int8 (580 bytes a page: reading them is
-// the bound for 128 heads) and are widened to f16 on their way into the
-// swizzled operand: all of a unit's loads are in registers one unit ahead, 64 dims
-// at a time go through four 16 KB stages that the MMAs free.  The heads' codes
-// come from a small kernel in front.
+// page's heads.  The keys arrive as int8 (580 bytes a page) through asynchronous
+// copies that run up to six chunks of 64 dims ahead, and are widened to f16 on
+// their way into tensor memory, where A is read from: through shared memory the
+// staging, the MMAs' reads of both operands and the copies share its bandwidth.
+// The heads' codes come from a small kernel in front.
 // Work is cut into contiguous ranges of units, one per CTA.
+//
+// Measured on GB300, 64 tokens x 1024 pages x 128 heads (38 MB of keys and 9.7 GFLOP: 6
+// us for either): 155 us on one issuing thread among the staging ones, 36.6 with
+// its own warp and products read late, 30.8 with the next unit's loads spread over
+// the staging, 26.5 by asynchronous copies, 24.2 with A in tensor memory.  What is left
+// per CTA: 6 us until the first keys and heads are there, four units of 3.5 us, of
+// which the widening threads' own work is 2.5.  A second issuer (each with half the
+// dims) changed nothing.
 #include <cuda_runtime.h>
 
 #include <mutex>
@@ -35,18 +43,21 @@ constexpr int kScoreThreads = 256;            // 8 warps that stage keys and rea
 constexpr int kCtaThreads = kScoreThreads + 32;  // and one that issues the MMAs
 constexpr int kTilePages = 128;               // rows of an MMA = TMEM lanes
 constexpr int kHeadChunk = 128;               // heads of an MMA
-constexpr int kStages = 4;
+constexpr int kStages = 4;                    // widened chunks of 64 dims (in tensor memory), and
+constexpr int kRaw = 3;                       // chunks of codes on their way, of each half of the warps
 constexpr uint32_t kTileBytes = 128 * 128;    // 128 rows of 64 f16
-constexpr uint32_t kTmemCols = 256;           // two accumulators
+constexpr uint32_t kRawBytes = 128 * 64;
+constexpr uint32_t kTmemCols = 512;           // two accumulators of 128 columns, then (kStageCol) the stages of 32
+constexpr uint32_t kStageCol = 256;
 
 template <int D>
 struct ScoreSmem {
     static constexpr int kChunks = D / 64;
     static constexpr uint32_t q = 0;                                  // [chunk][head][64] f16, 128-byte swizzle
-    static constexpr uint32_t a = q + kChunks * kTileBytes;           // [stage][page][64] f16
-    static constexpr uint32_t unit = a + kStages * kTileBytes;        // [head] u_h
-    static constexpr uint32_t best = unit + kHeadChunk * 4;           // [page] maximum of the upper heads
-    static constexpr uint32_t bars = best + kTilePages * 4;           // B_* below
+    static constexpr uint32_t raw = q + kChunks * kTileBytes;         // [warp][slot][page of the warp] 64 codes
+    static constexpr uint32_t unit = raw + 2 * kRaw * kRawBytes;          // [head] u_h
+    static constexpr uint32_t best = unit + kHeadChunk * 4;           // [unit parity][page] maximum of the upper heads
+    static constexpr uint32_t bars = best + 2 * kTilePages * 4;           // B_* below
     static constexpr uint32_t tmem = bars + (2 * kStages + 4) * 8;
     static constexpr uint32_t bad = tmem + 4;                         // the token holds a NaN or an infinity
     static constexpr uint32_t first = bad + 4;                        // the CTA's first unit: {sequence, unit in it}
@@ -111,7 +122,7 @@ __global__ void __launch_bounds__(kQuantWarps * 32) quantise_heads_kernel(const 
     if (lane == 0) p.q_units[row] = u;
 }
 
-// barriers: stage staged (256 arrivals) / free (commit), accumulator finished
+// barriers: stage staged (128 arrivals) / free (commit), accumulator finished
 // (commit) / read (256 arrivals)
 enum { B_FULL = 0, B_EMPTY = kStages, B_DONE = 2 * kStages, B_READ = 2 * kStages + 2, B_ALL = 2 * kStages + 4 };
 
@@ -134,10 +145,10 @@ __device__ void score_issuer(const SelectParams &p, uint32_t base_s, uint64_t *b
             const uint32_t st = fill % kStages;
             if (ok) ok = mbar_wait(bars + B_FULL + st, (fill / kStages) & 1, p.status);
             if (!ok) continue;
-            const uint64_t ad = desc_sw128(base_s + S::a + st * kTileBytes, 16, 1024);
+            tc_fence_after();
             const uint64_t bd = desc_sw128(base_s + S::q + c * kTileBytes, 16, 1024);
 #pragma unroll
-            for (int s = 0; s < 4; ++s) mma_ss(d, ad + 2 * s, bd + 2 * s, idesc, c > 0 || s > 0);
+            for (int s = 0; s < 4; ++s) mma_ts(d, tmem + kStageCol + 32 * st + 8 * s, bd + 2 * s, idesc, c > 0 || s > 0);
             mma_commit(bars + B_EMPTY + st);
             if (c == S::kChunks - 1) mma_commit(bars + B_DONE + buf);
         }
@@ -163,7 +174,7 @@ __global__ void __launch_bounds__(kCtaThreads, 1) page_scores_kernel(const Selec
 
     if (tid == 0) {
         for (int i = 0; i < B_ALL; ++i)
-            mbar_init(bars + i, (i >= B_EMPTY && i < B_READ) ? 1 : kScoreThreads);
+            mbar_init(bars + i, i < B_EMPTY ? kScoreThreads / 2 : i < B_READ ? 1 : kScoreThreads);
         fence_mbar_init();
     }
     if (warp == 0) {
@@ -226,28 +237,65 @@ __global__ void __launch_bounds__(kCtaThreads, 1) page_scores_kernel(const Selec
         }
         set_token(u);
     };
-    // The thread's part of the unit's keys: of every 64 dims, 16 bytes of rows
-    // srow and srow + 64 (four neighbouring lanes read 64 contiguous bytes); and
-    // the scale of its own page.  A page that is not there reads block 0's key
-    // (its score goes nowhere, or, for a bad block id, is any number).  The block
-    // ids are looked up a unit ahead of the keys, and the keys a unit ahead of
-    // their use, so that no load waits for another.
-    const int srow = (tid & 255) >> 2, quarter = tid & 3;
-    uint4 key[kChunks][2];
-    float scale = 0.f;
+    // The two halves of the warps widen every other chunk: a warp 64 dims of its 32
+    // pages, a page per lane.  It copies them kRaw of its chunks ahead and across
+    // units, so that the loads never wait for one another and no warp for another's.
+    // Four neighbouring lanes copy one page's 64 bytes, pages first + lane / 4 and 8, 16
+    // and 24 behind it.  A page that is not there reads block 0's key (its score goes
+    // nowhere, or, for a bad block id, is any number).  The block ids are looked up a
+    // unit ahead of the copies.
+    const int lane = tid & 31, srow = (row & ~31) + (lane >> 2);
+    const int passes = (p.h_q + kHeadChunk - 1) / kHeadChunk;  // jobs of a unit: its heads, 128 at a time
     struct Blocks {
-        int s0, s1, own;
+        int s[4], own;
     };
     auto block_of = [&](const UnitAt &u, int r) {
         const int page = u.tile * kTilePages + r;
         return page < u.n ? __ldg(p.block_table + (size_t)u.b * p.max_blocks + page) : 0;
     };
-    auto look_up = [&](const UnitAt &u) { return Blocks{block_of(u, srow), block_of(u, srow + 64), block_of(u, row)}; };
+    auto look_up = [&](const UnitAt &u) { return Blocks{{block_of(u, srow), block_of(u, srow + 8), block_of(u, srow + 16), block_of(u, srow + 24)}, block_of(u, row)}; };
     auto safe = [&](int blk) { return blk < 0 || (int64_t)blk >= p.num_blocks ? 0 : blk; };
-    auto key_row = [&](int blk) { return reinterpret_cast<const uint4 *>(p.keys + (size_t)safe(blk) * D) + quarter; };
-    auto load_scale = [&](int own) {
-        if (own < 0 || (int64_t)own >= p.num_blocks) atomicOr(p.status, MLA_DEVERR_BLOCK_ID);
-        scale = __ldg(p.scales + safe(own));
+    auto key_row = [&](int blk) { return reinterpret_cast<const uint4 *>(p.keys + (size_t)safe(blk) * D) + (lane & 3); };
+    const uint32_t raw_s = base_s + S::raw + (uint32_t)(warp & 7) * (kRaw * 2048u);  // (16-byte piece q of page r at q ^ (r / 2 & 3))
+    struct Feed {
+        int left = 0;               // units to come, this one included
+        UnitAt u{}, next{};         // and the one behind it, whose block ids are known
+        Blocks blocks{};
+        const uint4 *s[4] = {};
+        float scale = 0.f;          // of the thread's own page of u
+        int pass = 0, c = 0;
+        uint32_t slot = 0;
+    } feed;
+    auto feed_unit = [&](const Blocks &b) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) feed.s[i] = key_row(b.s[i]);
+        if (b.own < 0 || (int64_t)b.own >= p.num_blocks) atomicOr(p.status, MLA_DEVERR_BLOCK_ID);
+        feed.scale = __ldg(p.scales + safe(b.own));
+        feed.next = feed.u;
+        if (feed.left > 1) {
+            advance(feed.next);
+            feed.blocks = look_up(feed.next);
+        }
+    };
+    // one chunk (an empty group behind the last, which keeps the count)
+    auto feed_chunk = [&] {
+        if (feed.left > 0) {
+            const uint32_t dst = raw_s + feed.slot * 2048u + 64u * (uint32_t)(lane >> 2) + 16u * (uint32_t)((lane ^ (lane >> 3)) & 3);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) cp_async16(dst + 512u * i, feed.s[i] + 4 * feed.c);
+            if (++feed.slot == kRaw) feed.slot = 0;
+            if ((feed.c += 2) >= kChunks) {
+                feed.c -= kChunks;
+                if (++feed.pass == passes) {
+                    feed.pass = 0;
+                    if (--feed.left > 0) {
+                        feed.u = feed.next;
+                        feed_unit(feed.blocks);
+                    }
+                }
+            }
+        }
+        cp_async_commit();
     };
     // codes of heads h0 .. h0 + heads - 1 of a token, widened into shared memory
     auto load_heads = [&](const UnitAt &u, int h0, int heads) {
@@ -285,35 +333,27 @@ __global__ void __launch_bounds__(kCtaThreads, 1) page_scores_kernel(const Selec
                 sts128(dst + 16u * (uint32_t)(((piece & 7) + 1) ^ (h & 7)), w[4], w[5], w[6], w[7]);
             }
         }
+        fence_proxy_async_smem();
+        named_bar_sync(1, kScoreThreads);  // all of it, before the MMAs that the next arrivals let go
     };
 
-    const int passes = (p.h_q + kHeadChunk - 1) / kHeadChunk;  // jobs of a unit: its heads, 128 at a time
     if (warp == kScoreThreads / 32) {
         if (elect_one_lane()) score_issuer<D>(p, base_s, bars, tmem, (long long)todo * passes);
     } else {
-        UnitAt u{};
         if (todo > 0) {
+            UnitAt u{};
             u.b = s_first[0];
             load_seq(u);
             u.tok = s_first[1] / u.tiles;
             u.tile = s_first[1] - u.tok * u.tiles;
             set_token(u);
-            const Blocks b = look_up(u);
-            const uint4 *s0 = key_row(b.s0), *s1 = key_row(b.s1);
-#pragma unroll
-            for (int c = 0; c < kChunks; ++c) {
-                key[c][0] = __ldg(s0 + 4 * c);
-                key[c][1] = __ldg(s1 + 4 * c);
-            }
-            load_scale(b.own);
+            feed.left = todo;
+            feed.c = half;
+            feed.u = u;
+            feed_unit(look_up(u));
         }
-        // the unit after this one, and its block ids
-        UnitAt next = u;
-        Blocks next_blocks{0, 0, 0};
-        if (todo > 1) {
-            advance(next);
-            next_blocks = look_up(next);
-        }
+#pragma unroll 1
+        for (int i = 0; i < kRaw; ++i) feed_chunk();
         griddep_wait();  // the heads' codes; the scores are written behind it too
         bool ok = true;
         float best = -__uint_as_float(0x7f800000u);
@@ -326,10 +366,12 @@ __global__ void __launch_bounds__(kCtaThreads, 1) page_scores_kernel(const Selec
             float scale = 0.f;
             float *out = nullptr;
         } late;
+        int units_read = 0;
         auto read_products = [&] {
             if (late.heads == 0) return;
             const uint32_t buf = (uint32_t)(late.job & 1);
             if (ok) ok = mbar_wait(bars + B_DONE + buf, (uint32_t)((late.job >> 1) & 1), p.status);
+            __syncwarp();
             tc_fence_after();
             const uint32_t lanes = tmem + buf * 128 + ((uint32_t)(32 * (warp & 3)) << 16);
 #pragma unroll
@@ -353,26 +395,26 @@ __global__ void __launch_bounds__(kCtaThreads, 1) page_scores_kernel(const Selec
             tc_fence_before();
             mbar_arrive(bars + B_READ + buf);
             if (late.last) {
-                if (half) s_best[row] = best;
+                float *other = s_best + (units_read++ & 1) * kTilePages + row;  // (its last reader met a barrier since)
+                if (half) *other = best;
                 const bool bad = *s_bad != 0;
                 named_bar_sync(1, kScoreThreads);
                 if (!half && late.out) {
-                    best = fmaxf(best, s_best[row]);
+                    best = fmaxf(best, *other);
                     *late.out = bad ? __uint_as_float(0x7fffffffu) : __fmul_rn(best, late.scale);
                 }
-                named_bar_sync(1, kScoreThreads);  // s_best may be written again
                 best = -__uint_as_float(0x7f800000u);
             }
             late.heads = 0;
         };
         int held_b = -1, held_tok = -1, held_h = -1;  // whose heads are in shared memory
-        uint32_t fill = 0;
+        uint32_t fill = 0, slot = 0;
         long long job = 0;
         for (int k = 0; k < todo; ++k) {
+            static_assert(2 * kRaw < kChunks && kStages % 2 == 0, "the feed is less than a unit ahead");
+            const UnitAt u = feed.u;
             const int page = u.tile * kTilePages + row;
-            const float my_scale = scale;
-            UnitAt after = next;
-            Blocks after_blocks{0, 0, 0};
+            const float my_scale = feed.scale;
             for (int h0 = 0; h0 < p.h_q; h0 += kHeadChunk, ++job) {
                 const int heads = min(kHeadChunk, p.h_q - h0);
                 if (held_b != u.b || held_tok != u.tok || held_h != h0) {
@@ -382,41 +424,31 @@ __global__ void __launch_bounds__(kCtaThreads, 1) page_scores_kernel(const Selec
                     held_tok = u.tok;
                     held_h = h0;
                 }
-                // with a unit's last heads the next unit's keys replace its own piece by
-                // piece: their loads spread over the staging (all at once behind it
-                // they queue up: 36.5 us for 64 tokens of 1024 pages and 128 heads, now MEASURED)
-                const bool ahead = h0 + kHeadChunk >= p.h_q && k + 1 < todo;
-                const uint4 *s0 = key_row(next_blocks.s0), *s1 = key_row(next_blocks.s1);
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < kChunks; ++c, ++fill) {
+                    if ((int)(fill & 1) != half) continue;  // the other half's chunk
                     const uint32_t st = fill % kStages;
-                    if (ok) ok = mbar_wait(bars + B_EMPTY + st, ((fill / kStages) & 1) ^ 1, p.status);
-                    const uint32_t dst = base_s + S::a + st * kTileBytes + 128u * (uint32_t)srow;
+                    cp_async_wait<kRaw - 1>();
+                    __syncwarp();  // every lane's copies
+                    const uint32_t src = raw_s + slot * 2048u + 64u * (uint32_t)lane;
+                    uint32_t w[32];
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const uint4 x = key[c][j];
-                        uint32_t w[8];
-                        widen4(x.x, w[0], w[1]);
-                        widen4(x.y, w[2], w[3]);
-                        widen4(x.z, w[4], w[5]);
-                        widen4(x.w, w[6], w[7]);
-                        const uint32_t piece = 2u * (uint32_t)quarter, at = dst + 64u * 128u * (uint32_t)j;
-                        sts128(at + 16u * (piece ^ (uint32_t)(srow & 7)), w[0], w[1], w[2], w[3]);
-                        sts128(at + 16u * ((piece + 1) ^ (uint32_t)(srow & 7)), w[4], w[5], w[6], w[7]);
+                    for (int j = 0; j < 4; ++j) {
+                        const uint4 x = lds128(src + 16u * (uint32_t)(j ^ ((lane >> 1) & 3)));
+                        widen4(x.x, w[8 * j], w[8 * j + 1]);
+                        widen4(x.y, w[8 * j + 2], w[8 * j + 3]);
+                        widen4(x.z, w[8 * j + 4], w[8 * j + 5]);
+                        widen4(x.w, w[8 * j + 6], w[8 * j + 7]);
                     }
-                    fence_proxy_async_smem();  // these and the heads, before the MMAs that the arrival lets go
+                    if (++slot == kRaw) slot = 0;
+                    if (ok) ok = mbar_wait(bars + B_EMPTY + st, ((fill / kStages) & 1) ^ 1, p.status);
+                    __syncwarp();
+                    tc_fence_after();
+                    tmem_st32(tmem + kStageCol + 32 * st + ((uint32_t)(32 * (warp & 3)) << 16), w);
+                    tmem_wait_st();
+                    tc_fence_before();
                     mbar_arrive(bars + B_FULL + st);
-                    if (ahead) {
-                        key[c][0] = __ldg(s0 + 4 * c);
-                        key[c][1] = __ldg(s1 + 4 * c);
-                    }
-                }
-                if (ahead) {
-                    load_scale(next_blocks.own);
-                    if (k + 2 < todo) {
-                        advance(after);
-                        after_blocks = look_up(after);
-                    }
+                    feed_chunk();  // into the slot that the warp has just read
                 }
                 read_products();
                 late.heads = heads;
@@ -425,9 +457,6 @@ __global__ void __launch_bounds__(kCtaThreads, 1) page_scores_kernel(const Selec
                 late.scale = my_scale;
                 late.out = page < u.n ? p.scores + ((size_t)u.b * p.s_q + u.tok) * p.max_blocks + page : nullptr;
             }
-            u = next;
-            next = after;
-            next_blocks = after_blocks;
         }
         read_products();
     }
