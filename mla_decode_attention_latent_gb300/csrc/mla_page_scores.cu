@@ -23,8 +23,8 @@
 // its own warp and products read late, 30.8 with the next unit's loads spread over
 // the staging, 26.5 by asynchronous copies, 24.2 with A in tensor memory.  What is left
 // per CTA: 6 us until the first keys and heads are there, four units of 3.5 us, of
-// which the widening threads' own work is 2.5.  A second issuer (each with half the
-// dims) changed nothing.
+// which the widening threads' own work is 2.5.  A second issuer, each with half the
+// dims, changed nothing while A was in shared memory; now there is no room for its sums.
 #include <cuda_runtime.h>
 
 #include <mutex>
@@ -55,9 +55,9 @@ struct ScoreSmem {
     static constexpr int kChunks = D / 64;
     static constexpr uint32_t q = 0;                                  // [chunk][head][64] f16, 128-byte swizzle
     static constexpr uint32_t raw = q + kChunks * kTileBytes;         // [warp][slot][page of the warp] 64 codes
-    static constexpr uint32_t unit = raw + 2 * kRaw * kRawBytes;          // [head] u_h
+    static constexpr uint32_t unit = raw + 2 * kRaw * kRawBytes;      // [head] u_h
     static constexpr uint32_t best = unit + kHeadChunk * 4;           // [unit parity][page] maximum of the upper heads
-    static constexpr uint32_t bars = best + 2 * kTilePages * 4;           // B_* below
+    static constexpr uint32_t bars = best + 2 * kTilePages * 4;       // B_* below
     static constexpr uint32_t tmem = bars + (2 * kStages + 4) * 8;
     static constexpr uint32_t bad = tmem + 4;                         // the token holds a NaN or an infinity
     static constexpr uint32_t first = bad + 4;                        // the CTA's first unit: {sequence, unit in it}
