@@ -49,7 +49,7 @@ schedule_kernel(const Entries seqlens, int batch, int num_parts, int fixed_cost,
     // the split-KV launch that follows may start its prologue now; it waits
     // for this grid to complete before it reads the partition
     if (threadIdx.x == 0) sm103::griddep_launch_dependents();
-    schedule_body(shared, seqlens, batch, num_parts, fixed_cost, combine_cost, metadata, num_splits, status);
+    schedule_body<false>(shared, seqlens, batch, num_parts, fixed_cost, combine_cost, metadata, num_splits, status);
 }
 
 }  // namespace

@@ -42,7 +42,10 @@ __device__ T block_exclusive_scan(T v, T *s_warp, T *total) {
 // [t * chunk, (t + 1) * chunk); a scan of the chunk costs gives every chunk's
 // first unit, so a unit is located by a binary search over the chunks and a
 // short walk inside one.
-// `seqlens[i]` is the length of entry i.
+// `seqlens[i]` is the length of entry i.  kWhole: a batch of at most one entry
+// per part may also get one part each, whole, where that is estimated no slower:
+// the line's grid cuts entries whose lengths differ a little, and each cut costs a
+// segment and the combine.
 template <int kSchedThreads>
 struct ScheduleShared {
     long long start[kSchedThreads + 1];  // first unit of every chunk; [kSchedThreads] = total
@@ -51,7 +54,7 @@ struct ScheduleShared {
     int pages[kSchedThreads];            // with one entry per thread: its pages, so that none is looked up again
 };
 
-template <int kSchedThreads, typename Entries>
+template <bool kWhole, int kSchedThreads, typename Entries>
 __device__ void schedule_body(ScheduleShared<kSchedThreads> &sh, const Entries &seqlens, int batch, int num_parts,
                               int fixed_cost, int combine_cost, int32_t *__restrict__ metadata,
                               int32_t *__restrict__ num_splits, unsigned int *status) {
@@ -103,6 +106,29 @@ __device__ void schedule_body(ScheduleShared<kSchedThreads> &sh, const Entries &
     const long long est_all = q_all + (cut_all ? fixed_cost + combine_cost : 0);
     const long long est_seq = q_seq + (cut_seq ? fixed_cost + combine_cost : 0);
     const long long quota = (batch < num_parts && est_seq < est_all) ? q_seq : q_all;
+
+    if constexpr (kWhole) {
+        if (batch <= num_parts) {
+            int longest = 0;
+            for (int i = i0; i < i1; ++i) longest = max(longest, entry_pages(i));
+            longest = __reduce_max_sync(0xffffffffu, longest);
+            if ((threadIdx.x & 31) == 0) s_warp32[threadIdx.x >> 5] = longest;
+            __syncthreads();
+            for (int w = 0; w < kSchedThreads / 32; ++w) longest = max(longest, s_warp32[w]);
+            if (longest + fixed_cost <= (est_seq < est_all ? est_seq : est_all)) {
+                for (int p = threadIdx.x; p < num_parts; p += kSchedThreads) {
+                    const int b = min(p, batch), next = min(p + 1, batch);
+                    int32_t *row = metadata + (size_t)p * kMdInts;
+                    row[0] = b;
+                    row[2] = next;
+                    row[1] = row[3] = row[4] = row[5] = row[6] = row[7] = 0;
+                }
+                for (int i = threadIdx.x; i <= batch; i += kSchedThreads) num_splits[i] = i;
+                return;
+            }
+            __syncthreads();  // s_warp32 is used again
+        }
+    }
 
     // cursor of unit x: sequence b, page, and S_b
     auto cursor = [&](long long x, int &b, int &pg, long long &sb) {

@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_pages_kernel(const Sele
     // slower on 64 tokens: its CTAs take the SMs before the selection's last ones)
     if (blockIdx.x == 0) {
         const int tiles = (p.h_q + MLA_TILE_ROWS - 1) / MLA_TILE_ROWS;
-        schedule_body(s_sched, SelectedLengths{p, tiles}, p.batch * p.s_q * tiles, p.num_parts, kFixedCost, kCombineCost,
+        schedule_body<true>(s_sched, SelectedLengths{p, tiles}, p.batch * p.s_q * tiles, p.num_parts, kFixedCost, kCombineCost,
                       p.metadata, p.num_splits, p.status);
         return;
     }
