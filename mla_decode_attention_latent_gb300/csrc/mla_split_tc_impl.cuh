@@ -544,6 +544,10 @@ __device__ void score_producer_e4m3(const DecodeParams &p, const Ctx &c, const C
     uint32_t ring_it = 0, step = 0, own = 0;
     bool ok = true;
     while (ok && walk.next(p, s)) {
+        if (kTree && r == 0 && s.p1 > s.p0) {  // the segment's Q rows into L2, as in score_producer
+            const int rows = min(kTileRows, p.rows - s.tile * kTileRows);
+            if (rows > 0) prefetch_l2(p.q + ((size_t)s.b * p.rows + (size_t)s.tile * kTileRows) * kD, (uint32_t)rows * kD * 2);
+        }
         for (int pg = s.p0; ok && pg < s.p1; ++pg, ++step) {
             if ((int)(step % kScoreIssuers) != r) continue;  // the other ring's step
             const int blk = safe_block(p, s.b, pg);
