@@ -1408,11 +1408,17 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
 //         3.5..7 (so that later ones may be 64 times as large before it has to
 //         change: with a factor of 4 every seventh page of 16,384 N(0, 1) tokens
 //         ran again; 24 ragged trees took 282 us with 8, 252 with 32, 235 with 64, 229
-//         with 128, where the error of o grew from 0.0017 to 0.0018); set anew, the largest then at 28..56, when a weight would pass
-//         448 and with every new maximum, never so that what O holds would grow
-//         (negative: no weight so far)
+//         with 128, where the error of o grew from 0.0017 to 0.0018); set anew, the
+//         largest then at 28..56, when a weight would pass 448 and with every new
+//         maximum, never so that what O holds would grow (negative: no weight so far)
 //   parts h = e4m3(w), l = e4m3(w - h), the difference exact in f16: off by about
 //         2^-8 of w, or by 2^-10 where the first page's largest is at least 3.5
+// Measured on GB300: 1.04 us a page (76 sequences of 16,384 tokens, one tile each:
+// 287 us) and about 14 us a further segment.  An S buffer is held for 3500 cycles by
+// its page's 36 MMAs (two issuers share the pipe) and 2700 by the pass, which with
+// three buffers is 2100 cycles a page, at 2.03 GHz the time measured; a fourth does
+// not fit beside Q.  (With half the MMAs a page takes 0.99 us: P's buffers close
+// next.  Without the TMEM loads or the staging stores it takes as long as with them.)
 #if MLA_SPLIT_FP8 && MLA_SPLIT_TREE
 __device__ void score_rows_e8(const DecodeParams &p, const Ctx &c, uint32_t tmem, int part) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
