@@ -49,6 +49,7 @@ schedule_kernel(const Entries seqlens, int batch, int num_parts, int fixed_cost,
     // the split-KV launch that follows may start its prologue now; it waits
     // for this grid to complete before it reads the partition
     if (threadIdx.x == 0) sm103::griddep_launch_dependents();
+    sm103::griddep_wait();  // a draft tree's partition is a dependent launch itself
     schedule_body<false>(shared, seqlens, batch, num_parts, fixed_cost, combine_cost, metadata, num_splits, status);
 }
 
@@ -66,9 +67,8 @@ cudaError_t launch_schedule_tree(const int32_t *seqlens, const int32_t *tree_len
                                  int h_q, int num_parts, int32_t *metadata, int32_t *num_splits, unsigned int *status,
                                  cudaStream_t stream) {
     const Entries entries{seqlens, tiles, tile_rows, h_q, tree_lens};
-    schedule_kernel<<<1, kSchedThreads, 0, stream>>>(entries, batch * tiles, num_parts, kFixedCost, kCombineCost, metadata,
-                                                     num_splits, status);
-    return cudaGetLastError();
+    return launch_after(schedule_kernel, dim3(1), dim3(kSchedThreads), 0, stream, entries, batch * tiles, num_parts, kFixedCost,
+                        kCombineCost, metadata, num_splits, status);
 }
 
 }  // namespace mla
