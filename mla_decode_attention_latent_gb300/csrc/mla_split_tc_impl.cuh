@@ -1511,7 +1511,7 @@ __device__ void score_rows_e8(const DecodeParams &p, const Ctx &c, uint32_t tmem
             for (int g = 0; g < kGroups; ++g) top = max(top, lds32(tops + 4u * (uint32_t)(g * kTileRows + r)));
             const float amax = __uint_as_float(top);
             if (amax > 0.f) qsig = __uint_as_float((__float_as_uint(amax / kE4Max) + 0x7fffffu) & 0x7f800000u);
-            const float inv = 1.f / qsig;
+            const uint64_t inv2 = f2_pack(1.f / qsig, 1.f / qsig);
             const uint32_t tile_s = smem_u32(c.base + kStageOff + grp * kPMsgBytes) + (uint32_t)row0 * 128u;
 #pragma unroll 1
             for (int k = 0; k < kOwn; ++k) {
@@ -1527,20 +1527,19 @@ __device__ void score_rows_e8(const DecodeParams &p, const Ctx &c, uint32_t tmem
                 for (int j = 0; j < 8; ++j) {
                     const uint4 y = lds128(tile_s + (uint32_t)lane * 128u + 16u * (uint32_t)(j ^ (lane & 7)));
                     const uint32_t w4[4] = {y.x, y.y, y.z, y.w};
+                    uint32_t x16[4];  // (x / qsig has 8 bits, at most 448: exact in f16 down to 2^-17)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float a, b;
+                        f2_unpack(f2_fma(f2_pack(__uint_as_float(w4[e] << 16), __uint_as_float(w4[e] & 0xffff0000u)), inv2, zero2), a, b);
+                        x16[e] = pack_f16(a, b);
+                    }
 #pragma unroll
                     for (int hw = 0; hw < 2; ++hw) {
-                        uint32_t code[2][2];
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const float a = __uint_as_float(w4[2 * hw + e] << 16) * inv;
-                            const float b = __uint_as_float(w4[2 * hw + e] & 0xffff0000u) * inv;
-                            code[0][e] = pack_e4m3x2(a, b);
-                            float ha, hb;
-                            f16x2_to_f32(e4m3x2_to_f16x2(code[0][e]), ha, hb);
-                            code[1][e] = pack_e4m3x2(a - ha, b - hb);
-                        }
-                        ph[2 * j + hw] = code[0][0] | (code[0][1] << 16);
-                        pl[2 * j + hw] = code[1][0] | (code[1][1] << 16);
+                        const uint32_t hi = pack_e4m3x4_f16(x16[2 * hw], x16[2 * hw + 1]);
+                        ph[2 * j + hw] = hi;
+                        pl[2 * j + hw] = pack_e4m3x4_f16(f16x2_sub(x16[2 * hw], e4m3x2_to_f16x2(hi)),
+                                                         f16x2_sub(x16[2 * hw + 1], e4m3x2_to_f16x2(hi >> 16)));
                     }
                 }
                 const int ch = grp + kGroups * k;
@@ -1616,11 +1615,42 @@ __device__ void score_rows_e8(const DecodeParams &p, const Ctx &c, uint32_t tmem
             enum { kTry, kMaximum, kFirst, kLargest, kCodes };
             int phase = pg == s.p0 ? kMaximum : kTry;
             while (true) {
+                if (phase == kMaximum) {  // (a loop of its own: the pass below for it too took 203 us, now 191, on 24 ragged trees)
+                    float xm = -CUDART_INF_F, cm = 0.f;  // the largest score, and the largest scale of a visible key
+#pragma unroll 1
+                    for (int ch = 0; ch < kPage / 16; ++ch) {
+                        uint32_t v[16];
+                        tmem_ld16(tmem + lane_base + kSCol0 + sb * kSCols + ch * 16, v);
+                        const uint32_t vis = (uint32_t)(vmask >> (16 * ch)) & 0xffffu;
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint4 c4 = lds128(cs_s + 64 * ch + 16 * j);
+                            const uint32_t cw[4] = {c4.x, c4.y, c4.z, c4.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float cs = __uint_as_float(cw[e]), x = __uint_as_float(v[4 * j + e]) * cs * sc;
+                                const bool on = (vis >> (4 * j + e)) & 1u;
+                                xm = fmaxf(xm, on ? x : -CUDART_INF_F);
+                                cm = fmaxf(cm, on ? fabsf(cs) : 0.f);
+                            }
+                        }
+                    }
+                    if (xm > m + kRescaleLog2 || (m == -CUDART_INF_F && xm > -CUDART_INF_F)) {
+                        fac = ex2(m - xm);  // 0 when m was -inf
+                        m = xm;
+                    }
+                    if (pg == s.p0) {  // a first page's weights are at most its largest scale
+                        if (cm > 0.f && m > -CUDART_INF_F) fac = new_scale(cm, kAtFirst, fac, ko);
+                        phase = kFirst;
+                    } else {
+                        phase = kLargest;
+                    }
+                }
                 const float lk = (float)((int)(__float_as_uint(fabsf(ko)) >> 23) - 127);
-                const float ref = phase == kMaximum || m == -CUDART_INF_F ? 0.f : phase == kLargest ? m : m - lk;
+                const float ref = m == -CUDART_INF_F ? 0.f : phase == kLargest ? m : m - lk;
                 const uint64_t nref2 = f2_pack(-ref, -ref);
-                const bool write = phase == kTry || phase == kFirst || phase == kCodes;
-                float ca4[2] = {0.f, 0.f};  // kMaximum: the largest scale of a visible key
+                const bool write = phase != kLargest;
                 float xa4[2] = {-CUDART_INF_F, -CUDART_INF_F}, wa4[2] = {0.f, 0.f};
                 uint64_t sum2[2] = {0ull, 0ull};
 #pragma unroll 1
@@ -1649,14 +1679,6 @@ __device__ void score_rows_e8(const DecodeParams &p, const Ctx &c, uint32_t tmem
                             float ca, cb;
                             f2_unpack(cs2[j], ca, cb);
                             cs2[j] = f2_pack((vis >> (2 * j)) & 1u ? ca : 0.f, (vis >> (2 * j + 1)) & 1u ? cb : 0.f);
-                        }
-                    }
-                    if (phase == kMaximum) {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            float ca, cb;
-                            f2_unpack(cs2[j], ca, cb);
-                            ca4[j & 1] = max3f(ca4[j & 1], fabsf(ca), fabsf(cb));
                         }
                     }
                     uint32_t hi[4], lo[4];
@@ -1711,19 +1733,6 @@ __device__ void score_rows_e8(const DecodeParams &p, const Ctx &c, uint32_t tmem
                     } else {
                         if (!fits) fac = new_scale(wmax / fabsf(ko), kAtLater, fac, ko);
                         phase = kCodes;
-                    }
-                } else if (phase == kMaximum) {
-                    if (xmax > m + kRescaleLog2 || (m == -CUDART_INF_F && xmax > -CUDART_INF_F)) {
-                        fac = ex2(m - xmax);  // 0 when m was -inf
-                        m = xmax;
-                    }
-                    // a first page's weights are at most its largest scale
-                    const float cmax = fmaxf(ca4[0], ca4[1]);
-                    if (pg == s.p0) {
-                        if (cmax > 0.f && m > -CUDART_INF_F) fac = new_scale(cmax, kAtFirst, fac, ko);
-                        phase = kFirst;
-                    } else {
-                        phase = kLargest;
                     }
                 } else if (phase == kFirst) {
                     // good enough unless the heavy keys have small scales
