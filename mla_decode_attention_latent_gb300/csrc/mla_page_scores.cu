@@ -80,7 +80,8 @@ struct UnitAt {
 // Query heads to codes: u_h = max |q| / 127 (NaN for a head that is not finite,
 // whose codes are 0), qi = rint(q / u_h).  One warp per head, so that the tokens'
 // heads are quantised once, on all SMs, and not again by every CTA that scores
-// pages for the token (which cost 7 us per token and CTA).
+// pages for the token (which cost 7 us per token and CTA).  64 x 128 heads: 8.6 us
+// with divisions, 6.4 without.
 constexpr int kQuantWarps = 8;
 template <int D>
 __global__ void __launch_bounds__(kQuantWarps * 32) quantise_heads_kernel(const SelectParams p) {
@@ -106,6 +107,12 @@ __global__ void __launch_bounds__(kQuantWarps * 32) quantise_heads_kernel(const 
     top = __reduce_max_sync(0xffffffffu, top);
     const bool finite = top < 0x7f800000u;
     const float u = !finite ? __uint_as_float(0x7fffffffu) : top ? __uint_as_float(top) / 127.f : 1.f;
+    // x / u without the division: with inv = 1 / u correctly rounded, q = x inv and
+    // the fused remainder r = x - q u, q + r inv is the correctly rounded quotient
+    // (Markstein's theorem; u = m / 127 for an 8-bit m never has the all-ones
+    // significand that it excludes: m is 127 times a power of two, or 1/254 of it off)
+    const float inv = 1.f / u;
+    const uint64_t inv2 = f2_pack(inv, inv), minus_u2 = f2_pack(-u, -u);
     uint2 *dst = reinterpret_cast<uint2 *>(p.q_codes + row * D);
 #pragma unroll
     for (int j = 0; j < 3; ++j) {
@@ -114,8 +121,16 @@ __global__ void __launch_bounds__(kQuantWarps * 32) quantise_heads_kernel(const 
         uint32_t c[8];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            c[2 * e] = finite ? (uint32_t)__float2int_rn(__uint_as_float(w[e] << 16) / u) & 255u : 0u;
-            c[2 * e + 1] = finite ? (uint32_t)__float2int_rn(__uint_as_float(w[e] & 0xffff0000u) / u) & 255u : 0u;
+            float a = __uint_as_float(w[e] << 16), b = __uint_as_float(w[e] & 0xffff0000u);
+            if (u < 0x1p-100f) {  // the remainder and the reciprocal would leave the normal range
+                a /= u;
+                b /= u;
+            } else {
+                const uint64_t x2 = f2_pack(a, b), q2 = f2_fma(x2, inv2, f2_pack(0.f, 0.f));
+                f2_unpack(f2_fma(f2_fma(q2, minus_u2, x2), inv2, q2), a, b);
+            }
+            c[2 * e] = finite ? (uint32_t)__float2int_rn(a) & 255u : 0u;
+            c[2 * e + 1] = finite ? (uint32_t)__float2int_rn(b) & 255u : 0u;
         }
         dst[lane + 32 * j] = make_uint2(c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24, c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24);
     }

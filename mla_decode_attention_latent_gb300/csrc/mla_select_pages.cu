@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_pages_kernel(const Sele
     }
     // `want` pages of rank `prefix` are taken, the first ones in order
     const bool by_score = p.topk > p.sink + p.local;
-    int done = 0, ties = 0;  // pages taken and ties seen before this round
+    int done = 0, ties = 0;  // pages taken and ties seen so far
     for (int i0 = 0; i0 < n; i0 += kSelectThreads) {
         const int i = i0 + tid;
         bool take = false, tie = false;
