@@ -249,3 +249,16 @@ def test_a_workspace_and_outputs_of_the_caller(dev):
         decode(dev, q, cache, table, lens, keys, scales, 4, workspace=ws[:need - 256])
     with pytest.raises(ValueError, match="too large"):
         decode(dev, q, cache, table, lens, keys, scales, 1 << 26)
+
+
+@pytest.mark.parametrize("exponent", [-122, -108, -101, -93, 90])
+def test_heads_of_every_magnitude(dev, exponent):
+    """The heads' codes are the quotients' also where a reciprocal or a remainder would be subnormal."""
+    lens = [900, 650]
+    q, cache, table, keys, scales = make(lens, 2, 24, 576, seed=23)
+    spread = torch.arange(24).view(1, 1, 24, 1) % 8
+    q = (q.float() * 2.0 ** exponent * 2.0 ** spread).to(torch.bfloat16)
+    ref = reference(q, cache, table, lens, keys, scales, 5, 1, 1, False, 1.0)
+    got = decode(dev, q, cache, table, lens, keys, scales, 5, softmax_scale=1.0)
+    assert mla.mla_device_status() == 0
+    assert torch.equal(got[2].cpu(), ref[3])
