@@ -2137,7 +2137,8 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 // page stride; a box (64 codes x 64 tokens) lands unswizzled, 64 B per token.
 // The tensor maps of the cache.  bf16 rows: `m` only.  e4m3 pages: `m` lands
 // each 64-code box with the 64-byte swizzle of the fp8 MMA operands (score
-// CTA), `m2` unswizzled, 64 B per token, for the value CTA's widening.
+// CTA), `m2` unswizzled, 64 B per token, for the value CTA's widening, or, where
+// V's codes are MMA operands as they land, 128-code boxes with the 128-byte swizzle.
 bool make_kv_map(CUtensorMap *m, CUtensorMap *m2, const void *kcache, int64_t num_blocks) {
     auto enc = encode_fn();
     if (!enc) return false;
