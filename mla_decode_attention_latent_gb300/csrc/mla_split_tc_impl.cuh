@@ -76,14 +76,14 @@
 // steps than the one above:
 //   scores  sigma_r is a power of two, so q / sigma_r keeps its 8 bits and two
 //           e4m3 parts of 4 bits hold them exactly (below 2^-11 of the row's
-//           maximum, where e4m3 runs out of exponents, to 2^-19 of it).  Two parts with their
-//           RoPE dims fit in TMEM beside both S buffers, so that no score MMA
-//           reads Q from shared memory.
-//   values  the weights w_j = p_j c_j times a power of two per row (chosen by the largest
-//           weight, lowered lazily like the running maximum, carried by O and
-//           divided out at the end) are split into two e4m3 parts as well, and the V codes
-//           are MN-major operands as they land: nothing is widened, a stage is
-//           32 KB and three are in flight.
+//           maximum, where e4m3 runs out of exponents, to 2^-19 of it).  Two parts
+//           with their RoPE dims fit in TMEM beside three S buffers of a page, so
+//           that no score MMA reads Q from shared memory.
+//   values  the weights w_j = p_j c_j times a power of two per row (chosen by the
+//           largest weight, lowered lazily like the running maximum, carried by O
+//           and divided out at the end) are split into two e4m3 parts as well, and
+//           the V codes are MN-major operands as they land: nothing is widened, a
+//           stage is 32 KB and three are in flight.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
