@@ -262,3 +262,29 @@ def test_heads_of_every_magnitude(dev, exponent):
     got = decode(dev, q, cache, table, lens, keys, scales, 5, softmax_scale=1.0)
     assert mla.mla_device_status() == 0
     assert torch.equal(got[2].cpu(), ref[3])
+
+
+def test_calls_from_several_threads_at_once(dev):
+    """Threads with a stream each, both formats, small and full tiles: every call gives the bits it gives alone."""
+    import threading
+    lens = [1500, 300, 576]
+    cases = [make(lens, 2, h, 576, fp8, seed=24) for h, fp8 in ((128, False), (128, True), (32, False), (32, True))]
+    cases = [[t.to(dev) for t in c] for c in cases]
+    run = lambda c: decode(dev, c[0], c[1], c[2], lens, c[3], c[4], 6)
+    want = [run(c) for c in cases]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        stream = torch.cuda.Stream(dev)
+        with torch.cuda.stream(stream):
+            got = [run(cases[i]) for _ in range(20)]
+            stream.synchronize()
+            wrong.extend(i for g in got if not all(torch.equal(a, b) for a, b in zip(want[i], g)))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(cases))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong and mla.mla_device_status() == 0
