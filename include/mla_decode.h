@@ -563,9 +563,9 @@ MLA_API int mla_decode_kvcache_tree(const void *q, const void *kcache, int64_t n
  *
  * Scales as for mla_decode_kvcache_fp8.  Precision: both products run on the fp8
  * tensor cores.  q is held exactly, but for elements below 2^-11 of their row's
- * largest (to 2^-19 of it); a softmax weight times its token's scale is held to
- * about 2^-8 of itself, or to 2^-11 of the row's largest in the first page where that
- * is more.
+ * largest (to 2^-19 of it).  A softmax weight times its token's scale, w, is held to
+ * 2^-8 of itself; what weights too small for that lose is kept below 2^-9 of the
+ * row's sum of w, whatever their number (a heavy key before thousands of light ones).
  */
 MLA_API int mla_decode_kvcache_tree_fp8(const void *q, const void *kv_pages, int64_t num_blocks,
                                         const int32_t *block_table, int max_blocks_per_seq,

@@ -233,9 +233,9 @@ __device__ __forceinline__ uint64_t desc_sw64(uint32_t smem_addr) {
            (4ull << 61);
 }
 
-// instruction descriptor: kind::f8f6f4 with e4m3 A and B (format fields 0), fp32 accumulator
-__host__ __device__ constexpr uint32_t idesc_e4m3(int m, int n, bool b_mn_major = false) {
-    return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+// instruction descriptor: kind::f8f6f4 with e4m3 B and A (format fields 0) or e5m2 A (1), fp32 accumulator
+__host__ __device__ constexpr uint32_t idesc_e4m3(int m, int n, bool b_mn_major = false, bool a_e5m2 = false) {
+    return (1u << 4) | ((a_e5m2 ? 1u : 0u) << 7) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
 // instruction descriptor: kind::f16 with f16 A and B (format field 0), fp32 accumulator
@@ -490,6 +490,16 @@ __device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
 __device__ __forceinline__ uint32_t pack_e4m3x4_f16(uint32_t x01, uint32_t x23) {
     uint32_t r;
     asm("{\n\t.reg .b16 a, b;\n\tcvt.rn.satfinite.e4m3x2.f16x2 a, %1;\n\tcvt.rn.satfinite.e4m3x2.f16x2 b, %2;\n\t"
+        "mov.b32 %0, {a, b};\n\t}"
+        : "=r"(r)
+        : "r"(x01), "r"(x23));
+    return r;
+}
+
+// four f16 values -> four e5m2 codes, the first in the low byte
+__device__ __forceinline__ uint32_t pack_e5m2x4_f16(uint32_t x01, uint32_t x23) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 a, b;\n\tcvt.rn.satfinite.e5m2x2.f16x2 a, %1;\n\tcvt.rn.satfinite.e5m2x2.f16x2 b, %2;\n\t"
         "mov.b32 %0, {a, b};\n\t}"
         : "=r"(r)
         : "r"(x01), "r"(x23));

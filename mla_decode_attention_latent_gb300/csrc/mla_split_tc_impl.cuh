@@ -79,9 +79,9 @@
 //           maximum, where e4m3 runs out of exponents, to 2^-19 of it).  Two parts
 //           with their RoPE dims fit in TMEM beside three S buffers of a page, so
 //           that no score MMA reads Q from shared memory.
-//   values  the weights w_j = p_j c_j times a power of two per row (chosen by the
-//           largest weight, lowered lazily like the running maximum, carried by O
-//           and divided out at the end) are split into two e4m3 parts as well, and
+//   values  the weights w_j = p_j c_j times a power of two per row (lowered when a weight
+//           would pass the range, raised when what light ones lose would count, carried
+//           by O and divided out at the end) are split into an e4m3 and an e5m2 part, and
 //           the V codes are MN-major operands as they land: nothing is widened, a
 //           stage is 32 KB and three are in flight.
 #include <cuda.h>
@@ -209,10 +209,10 @@ constexpr uint32_t kStageOff =
     kQRopeOff + (kQRopeSmem ? kQParts * kQRopePartBytes : kTurnQ ? (uint32_t)kTileRows * 128u : 0u);
 constexpr uint32_t kScaleOff = kStageOff + kPBufs * kPMsgBytes;   // the side ring of the steps in flight
 // several groups: the running state that each leaves for the next page's,
-// [group][maximum, row sum, weight scale][128 rows] fp32
+// [group][maximum, row sum, weight scale, allowance][128 rows] fp32
 constexpr uint32_t kChainOff = kScaleOff + (kRing ? kScSlots * kScBytes : 0);
 // and each group's part of the maxima of Q's rows, [group][128 rows]
-constexpr uint32_t kQMaxOff = kChainOff + (kGroups > 1 ? kGroups * 3 * kTileRows * 4 : 0);
+constexpr uint32_t kQMaxOff = kChainOff + (kGroups > 1 ? kGroups * 4 * kTileRows * 4 : 0);
 constexpr uint32_t kScoreEnd = kQMaxOff + (kGroups > 1 ? kGroups * kTileRows * 4 : 0);
 // value CTA: [V ring 2 x 64 KB (sparse: the page buffers)][P landing 2 x 17 KB][epilogue staging 34 KB]
 constexpr uint32_t kVRingOff = 0;
@@ -956,16 +956,16 @@ __device__ void value_mma(const DecodeParams &p, const Ctx &c, uint32_t tmem, in
             const uint32_t vtile = smem_u32(c.base + kVRingOff + st * kVStageBytes);
             const uint32_t ptile = smem_u32(c.base + kPBufOff + pb * kPMsgBytes);
             if constexpr (kE8) {
-                // P's two e4m3 parts (codes 0..63 and 64..127 of a row) times the
-                // codes as they landed, 32 tokens per MMA
-                constexpr uint32_t id8 = idesc_e4m3(kTileRows, 256, true);
+                // P's upper (e4m3) and lower (e5m2) parts, codes 0..63 and 64..127 of a
+                // row, times the codes as they landed, 32 tokens per MMA
+                constexpr uint32_t id8 = idesc_e4m3(kTileRows, 256, true), id8lo = idesc_e4m3(kTileRows, 256, true, true);
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const uint64_t ad = desc_sw128(ptile + k * 32, 16, 1024);
                         const uint64_t bd = desc_sw128(vtile + h * 2 * kChunkBytes + (k & 1) * 4096, kChunkBytes, 1024);
-                        mma_ss_f8(tmem + h * 256, ad, bd, id8, (pg > s.p0 || k > 0) ? 1u : 0u);
+                        mma_ss_f8(tmem + h * 256, ad, bd, k < 2 ? id8 : id8lo, (pg > s.p0 || k > 0) ? 1u : 0u);
                     }
             } else
 #pragma unroll
@@ -1398,21 +1398,33 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
 // cache.  Here a page is one rolled pass over four chunks of 16 keys that goes
 // straight from TMEM to the staged codes, and the page's state (running maximum
 // m, weight scale ko, sum L in units of ko 2^-m) travels from group to group:
-//   pass: x_j = s_j c_j sc - (m - log2 ko), p_j = 2^x_j, w_j = p_j c_j -> two e4m3 parts
+//   pass: x_j = s_j c_j sc - (m - log2 ko), p_j = 2^x_j, w_j = p_j c_j -> two parts
 // A page is run on the state that its group knew last, three pages ago, and is
 // good if the state has not changed since and the page changes nothing in it:
-// its maximum within 2^8 of m, its largest weight within the e4m3 range.  Only
-// otherwise (a segment's first page, and the few where a maximum rises) it is run
-// again: for the maximum, for the largest weight, and for the codes.
-//   ko    a power of two that puts a segment's first page's largest weight at
-//         3.5..7 (so that later ones may be 64 times as large before it has to
-//         change: with a factor of 4 every seventh page of 16,384 N(0, 1) tokens
-//         ran again; 24 ragged trees took 282 us with 8, 252 with 32, 235 with 64, 229
-//         with 128, where the error of o grew from 0.0017 to 0.0018); set anew, the
-//         largest then at 28..56, when a weight would pass 448 and with every new
-//         maximum, never so that what O holds would grow (negative: no weight so far)
-//   parts h = e4m3(w), l = e4m3(w - h), the difference exact in f16: off by about
-//         2^-8 of w, or by 2^-10 where the first page's largest is at least 3.5
+// its maximum within 2^8 of m, its largest weight within the e4m3 range, its light
+// weights within the allowance.  Only otherwise (a segment's first page, and the few
+// where a maximum rises) it is run again: for the maximum, for the largest weight,
+// and for the codes.
+//   parts h = e4m3(w), l = e5m2(w - h), the difference exact in f16: off by at most
+//         2^-8 of w from 2^-6 up (as a bf16 weight), and by at most 2^-14 below, where
+//         h has one step.  (l as e4m3 is off by 2^-9 of w, but by 2^-10 below: what a
+//         tail loses then has to be watched 16 times more closely, and 24 ragged trees
+//         took 225 us, now 202.)
+//   allowance  L counts every p in full, so what the parts lose is missing from o, and
+//         behind one heavy key thousands of light ones may hold most of the mass.  Per
+//         row, B = 2^-9 sum S - sum E over the pages, in the units of O, never
+//         falls below 0: S is a lower bound of a page's sum of w (its largest w, or its
+//         smallest scale times its sum of p), E an upper bound of its loss (2^-14 for
+//         each visible key, or all of it).  So the loss stays below 2^-9 of the sum of
+//         all w, however many keys there are
+//   ko    a power of two that puts the largest scale of a segment's first page at
+//         3.5..7 (so that later weights may be 64 times as large before it has to
+//         change: a factor of 32 is 1 % slower on N(0, 2) scores).  When a weight would
+//         pass 448, and with every new maximum, it is set anew, the largest weight then
+//         at 28..56, and O shrinks with it or stays; when B would fall below 0 it is
+//         raised, S then at 8..16, and O grows with it (negative: no weight so far)
+// What it costs, with the state that it carries: 1.5-3 % on scores of up to 1.5 nats'
+// spread, where nearly no page is run again, up to 25 % on scores that spread by 3 to 5.
 // Measured on GB300: 1.04 us a page (76 sequences of 16,384 tokens, one tile each:
 // 287 us) and about 14 us a further segment.  An S buffer is held for 3500 cycles by
 // its page's 36 MMAs (two issuers share the pipe) and 2700 by the pass, which with
@@ -1427,8 +1439,8 @@ __device__ void score_rows_e8(const DecodeParams &p, const Ctx &c, uint32_t tmem
     const int grp = warp < 6 ? 0 : (warp - 4) >> 2;      // warps 2..5, 8..11, 12..15
     const int before = (grp + kGroups - 1) % kGroups;    // the group of the page before
     const int chain_own = B_CHAIN + 4 * grp + (warp & 3), chain_prev = B_CHAIN + 4 * before + (warp & 3);
-    const uint32_t own_s = smem_u32(c.base + kChainOff) + 4u * (uint32_t)(3 * kTileRows * grp + r);
-    const uint32_t prev_s = smem_u32(c.base + kChainOff) + 4u * (uint32_t)(3 * kTileRows * before + r);
+    const uint32_t own_s = smem_u32(c.base + kChainOff) + 4u * (uint32_t)(4 * kTileRows * grp + r);
+    const uint32_t prev_s = smem_u32(c.base + kChainOff) + 4u * (uint32_t)(4 * kTileRows * before + r);
     const uint32_t peer_buf = mapa(smem_u32(c.base + kPBufOff), c.peer);
     const uint32_t peer_pfull = mapa(smem_u32(c.bar(B_PFULL)), c.peer);
     const uint64_t zero2 = f2_pack(0.f, 0.f);
@@ -1566,6 +1578,16 @@ __device__ void score_rows_e8(const DecodeParams &p, const Ctx &c, uint32_t tmem
             ko = kn;
             return fac;
         };
+        // the allowance (above), and the scale raised so that a page's S is at 8..16: four
+        // times what keeps B from falling.  O grows with the scale (returns its factor); sums
+        // stay finite, since p is below 2^9, a scale below 2^8 and ko at most 2^70
+        constexpr float kShare = 0x1p-9f, kLostEach = 0x1p-14f, kAtRaised = 16.f, kRaiseLimit = 0x1p70f;
+        auto raise = [](float S, float fac, float &ko) {
+            const float g = __uint_as_float(__float_as_uint(fminf(kAtRaised / S, kRaiseLimit / ko)) & 0x7f800000u);
+            if (!(g > 1.f)) return fac;
+            ko *= g;
+            return fac * g;
+        };
         // what this group knows of the row: state after some page of the segment
         float m = -CUDART_INF_F, L = 0.f, ko = -1.f;
         for (int pg = s.p0; pg < s.p1; ++pg, ++it) {
@@ -1578,14 +1600,17 @@ __device__ void score_rows_e8(const DecodeParams &p, const Ctx &c, uint32_t tmem
             const int pb = (int)(it % kPBufs), scs = (int)(it % kScSlots);
             const uint32_t cs_s = smem_u32(c.base + kScaleOff) + (uint32_t)scs * kScBytes;
             if (!warp_wait(c, B_SCFULL + scs, (it / kScSlots) & 1)) return;
-            if ((warp & 3) == 0) {
-                // one warp of the group checks the scales of the sequence's tokens
-                // on this page against the limit (a NaN scale fails too)
+            // the smallest and largest |scale| of the sequence's tokens on this page (magnitude
+            // bits order as magnitudes do, NaN on top); one warp of the group checks them
+            float cs_least, cs_most;
+            {
                 const int nseq = min(kPage, s.T - pg * kPage);
-                const float a = lane < nseq ? fabsf(__uint_as_float(lds32(cs_s + 4 * lane))) : 0.f;
-                const float b = lane + 32 < nseq ? fabsf(__uint_as_float(lds32(cs_s + 4 * (lane + 32)))) : 0.f;
-                if (__any_sync(0xffffffffu, !(a < kE4ScaleLimit) || !(b < kE4ScaleLimit)) && lane == 0)
-                    atomicOr(p.status, MLA_DEVERR_SCALE);
+                const uint32_t a = lds32(cs_s + 4 * lane) & 0x7fffffffu, b = lds32(cs_s + 4 * (lane + 32)) & 0x7fffffffu;
+                const uint32_t lo = min(lane < nseq ? a : ~0u, lane + 32 < nseq ? b : ~0u);
+                const uint32_t hi = max(lane < nseq ? a : 0u, lane + 32 < nseq ? b : 0u);
+                cs_least = __uint_as_float(__reduce_min_sync(0xffffffffu, lo));
+                cs_most = __uint_as_float(__reduce_max_sync(0xffffffffu, hi));
+                if ((warp & 3) == 0 && lane == 0 && !(cs_most < kE4ScaleLimit)) atomicOr(p.status, MLA_DEVERR_SCALE);
             }
             // the rows of the page that this row sees
             int nvalid = row_ok ? T_row - pg * kPage : 0;
@@ -1593,6 +1618,11 @@ __device__ void score_rows_e8(const DecodeParams &p, const Ctx &c, uint32_t tmem
             uint64_t vmask = ~0ull;
             if ((pg + 1) * kPage > tree_base && nvalid > 0) vmask = tree_page_mask(p, s.b, qi, tree_base, pg);
             if (nvalid < kPage) vmask &= nvalid > 0 ? (~0ull >> (kPage - nvalid)) : 0ull;
+            // what the page adds to the allowance, from its largest weight and its sum of p ko
+            auto earned = [&](float wmax, float sum, float &S) {
+                S = fmaxf(wmax, sum * cs_least);
+                return wmax > 0.f ? kShare * S - fminf(sum * cs_most, (float)__popcll(vmask) * kLostEach) : 0.f;
+            };
             // staging pb is free once the value CTA's MMA of page it - kPBufs is
             // done: that MMA consumed the bulk copy made from it
             if (!warp_wait<true>(c, B_PFREE + pb, ((it / kPBufs) & 1) ^ 1)) return;
@@ -1611,7 +1641,7 @@ __device__ void score_rows_e8(const DecodeParams &p, const Ctx &c, uint32_t tmem
                     ko = __uint_as_float(lds32(prev_s + 2 * kTileRows * 4));
                 }
             }
-            float fac = 1.f;
+            float fac = 1.f, allowance;
             enum { kTry, kMaximum, kFirst, kLargest, kCodes };
             int phase = pg == s.p0 ? kMaximum : kTry;
             while (true) {
@@ -1699,7 +1729,7 @@ __device__ void score_rows_e8(const DecodeParams &p, const Ctx &c, uint32_t tmem
                         hi[q] = pack_e4m3x4_f16(w16[0], w16[1]);
                         l16[0] = f16x2_sub(w16[0], e4m3x2_to_f16x2(hi[q]));
                         l16[1] = f16x2_sub(w16[1], e4m3x2_to_f16x2(hi[q] >> 16));
-                        lo[q] = pack_e4m3x4_f16(l16[0], l16[1]);
+                        lo[q] = pack_e5m2x4_f16(l16[0], l16[1]);
                     }
                     if (write) {  // 16 codes of the upper parts, and of the lower ones 64 bytes behind
                         sts128(stage_s + r * 128 + 16 * (ch ^ (r & 7)), hi[0], hi[1], hi[2], hi[3]);
@@ -1712,6 +1742,8 @@ __device__ void score_rows_e8(const DecodeParams &p, const Ctx &c, uint32_t tmem
                 const float sum = sum_lo + sum_hi;
                 if (phase == kTry) {
                     bool same = true;
+                    float S;
+                    allowance = earned(wmax, sum, S);
                     if (!chained) {
                         if (!warp_wait(c, chain_prev, ((it - 1) / kGroups) & 1)) return;
                         const float m1 = __uint_as_float(lds32(prev_s)), ko1 = __uint_as_float(lds32(prev_s + 2 * kTileRows * 4));
@@ -1722,8 +1754,10 @@ __device__ void score_rows_e8(const DecodeParams &p, const Ctx &c, uint32_t tmem
                         chained = true;
                     }
                     const bool low = m == -CUDART_INF_F ? xmax == -CUDART_INF_F : xmax <= kRescaleLog2 + lk;
-                    const bool fits = wmax <= kE4Max && !(ko < 0.f && wmax > 0.f);
-                    if (__all_sync(0xffffffffu, same && low && fits)) {
+                    const bool over = wmax > kE4Max || (ko < 0.f && wmax > 0.f);
+                    allowance += __uint_as_float(lds32(prev_s + 3 * kTileRows * 4));
+                    const bool lost = wmax > 0.f && allowance < 0.f && ko < kRaiseLimit;
+                    if (__all_sync(0xffffffffu, same && low && !over && !lost)) {
                         L += sum;
                         break;
                     }
@@ -1731,12 +1765,15 @@ __device__ void score_rows_e8(const DecodeParams &p, const Ctx &c, uint32_t tmem
                     if (!__all_sync(0xffffffffu, low)) {
                         phase = kMaximum;
                     } else {
-                        if (!fits) fac = new_scale(wmax / fabsf(ko), kAtLater, fac, ko);
+                        if (over) fac = new_scale(wmax / fabsf(ko), kAtLater, fac, ko);
+                        else if (lost) fac = raise(S, fac, ko);
                         phase = kCodes;
                     }
                 } else if (phase == kFirst) {
-                    // good enough unless the heavy keys have small scales
-                    if (__all_sync(0xffffffffu, wmax >= kAtFirst / 8.f || wmax == 0.f)) {
+                    float S;
+                    allowance = earned(wmax, sum, S);
+                    const bool lost = wmax > 0.f && allowance < 0.f;
+                    if (!__any_sync(0xffffffffu, lost)) {
                         L = sum;
                         if (wmax == 0.f && ko > 0.f) {  // no weight yet
                             L /= ko;
@@ -1744,19 +1781,21 @@ __device__ void score_rows_e8(const DecodeParams &p, const Ctx &c, uint32_t tmem
                         }
                         break;
                     }
-                    if (wmax > 0.f) {
-                        const float w = wmax / ko;
-                        ko = -1.f;
-                        new_scale(w, kAtFirst, 0.f, ko);
-                    } else {
-                        ko = -1.f;
-                    }
+                    if (lost) raise(S, 0.f, ko);
+                    else if (wmax == 0.f) ko = -1.f;
                     phase = kCodes;
                 } else if (phase == kLargest) {
                     if (wmax > 0.f && (ko < 0.f || wmax * ko > kE4Max || fac != 1.f)) fac = new_scale(wmax, kAtLater, fac, ko);
+                    if (wmax > 0.f) {
+                        float S;
+                        const float left = __uint_as_float(lds32(prev_s + 3 * kTileRows * 4)) * fac + earned(wmax * ko, sum * ko, S);
+                        if (left < 0.f) fac = raise(S, fac, ko);
+                    }
                     phase = kCodes;
                 } else {
+                    float S;
                     L = L * fac + sum;
+                    allowance = (pg > s.p0 ? __uint_as_float(lds32(prev_s + 3 * kTileRows * 4)) * fac : 0.f) + earned(wmax, sum, S);
                     break;
                 }
             }
@@ -1766,6 +1805,7 @@ __device__ void score_rows_e8(const DecodeParams &p, const Ctx &c, uint32_t tmem
             sts32(own_s, __float_as_uint(m));
             sts32(own_s + kTileRows * 4, __float_as_uint(L));
             sts32(own_s + 2 * kTileRows * 4, __float_as_uint(ko));
+            sts32(own_s + 3 * kTileRows * 4, __float_as_uint(allowance));
             mbar_arrive(c.bar(chain_own));
 
             const bool last = pg == s.p1 - 1;
