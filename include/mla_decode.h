@@ -561,7 +561,8 @@ MLA_API int mla_decode_kvcache_tree(const void *q, const void *kcache, int64_t n
 /*
  * mla_decode_kvcache_tree_fp8 — the same over packed e4m3 pages (d = 576).
  *
- * Scales as for mla_decode_kvcache_fp8.  Precision: both products run on the fp8
+ * Scales as for mla_decode_kvcache_fp8 (that of a node that no token sees may be
+ * anything, like its row).  Precision: both products run on the fp8
  * tensor cores.  q is held exactly, but for elements below 2^-11 of their row's
  * largest (to 2^-19 of it).  A softmax weight times its token's scale, w, is held to
  * 2^-8 of itself; what weights too small for that lose is kept below 2^-9 of the

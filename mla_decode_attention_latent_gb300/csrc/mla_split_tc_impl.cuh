@@ -1601,7 +1601,8 @@ __device__ void score_rows_e8(const DecodeParams &p, const Ctx &c, uint32_t tmem
             const uint32_t cs_s = smem_u32(c.base + kScaleOff) + (uint32_t)scs * kScBytes;
             if (!warp_wait(c, B_SCFULL + scs, (it / kScSlots) & 1)) return;
             // the smallest and largest |scale| of the sequence's tokens on this page (magnitude
-            // bits order as magnitudes do, NaN on top); one warp of the group checks them
+            // bits order as magnitudes do, NaN on top); one warp of the group reports those
+            // past the limit that some row of the tile sees
             float cs_least, cs_most;
             {
                 const int nseq = min(kPage, s.T - pg * kPage);
@@ -1610,7 +1611,13 @@ __device__ void score_rows_e8(const DecodeParams &p, const Ctx &c, uint32_t tmem
                 const uint32_t hi = max(lane < nseq ? a : 0u, lane + 32 < nseq ? b : 0u);
                 cs_least = __uint_as_float(__reduce_min_sync(0xffffffffu, lo));
                 cs_most = __uint_as_float(__reduce_max_sync(0xffffffffu, hi));
-                if ((warp & 3) == 0 && lane == 0 && !(cs_most < kE4ScaleLimit)) atomicOr(p.status, MLA_DEVERR_SCALE);
+                if ((warp & 3) == 0 && !(cs_most < kE4ScaleLimit)) {
+                    const uint64_t seen =
+                        (pg + 1) * kPage > tree_base ? tree_tile_mask(p, s.b, s.tile, nodes, tree_base, pg) : ~0ull;
+                    const bool bad_a = lane < nseq && ((seen >> lane) & 1ull) && !(__uint_as_float(a) < kE4ScaleLimit);
+                    const bool bad_b = lane + 32 < nseq && ((seen >> (lane + 32)) & 1ull) && !(__uint_as_float(b) < kE4ScaleLimit);
+                    if (bad_a || bad_b) atomicOr(p.status, MLA_DEVERR_SCALE);
+                }
             }
             // the rows of the page that this row sees
             int nvalid = row_ok ? T_row - pg * kPage : 0;

@@ -175,3 +175,35 @@ def test_random_scores_of_many_spreads(dev):
     assert mla.mla_device_status() == 0
     for b, T in enumerate(lens):
         compare(o[b, 0], lse[b, 0], reference(q[b, 0], rows_of(cache, table[b:b + 1], T)), f"{T} keys")
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf"), 1e30, 255.0])
+@pytest.mark.parametrize("h", [16, 128])
+def test_the_scale_of_a_node_that_nothing_sees(dev, bad, h):
+    """It is neither used nor reported; with 128 heads (one token per tile) one that token 6 sees is reported."""
+    from mla_decode_attention_latent_gb300 import _lib
+    g = torch.Generator().manual_seed(6)
+    lens, s_q = [200, 70], 10
+    table, used = R.random_table(g, lens)
+    cache = R.random_cache(g, used, 576, True)
+    q = torch.randn((2, s_q, h, 576), generator=g).to(torch.bfloat16)
+    sees = R.ancestors([-1, 0, 0, 1, 2, 3, 0, 1, 1, 0])
+    sees[:, 4] = False
+    mask = torch.stack([R.mask_words(sees)] * 2).to(dev)
+    sl = torch.tensor(lens, dtype=torch.int32, device=dev)
+
+    def decode():
+        o, lse = mla.mla_decode_kvcache_tree_fp8(q.to(dev), cache.to(dev), table.to(dev), sl, mask, 512)
+        return o, lse, mla.mla_device_status()
+
+    def spoil(node):
+        for i, T in enumerate(lens):
+            blk, off = R.place(table, i, T - s_q + node)
+            cache[blk, 64 * 576 + 4 * off:64 * 576 + 4 * off + 4] = torch.tensor([bad]).view(torch.uint8)
+    want = decode()
+    spoil(4)
+    got = decode()
+    assert want[2] == got[2] == 0
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+    spoil(6)
+    assert decode()[2] == _lib.MLA_DEVERR_SCALE
