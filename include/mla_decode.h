@@ -415,7 +415,8 @@ MLA_API int mla_cache_read_fp8(const void *kv_pages, int64_t num_blocks, const i
  *   mean  = (sum of its n rows) / n   in fp32, summed as a balanced tree over the
  *           64 rows (neighbours first, absent rows 0)
  *   scale = max |mean| / 127 (1 for a mean of zeros),  key = rint(mean / scale)
- * (IEEE fp32 quotients).  A mean that is not finite gives key 0 and scale NaN.
+ * (IEEE fp32 quotients; a subnormal scale is at least 2^-149, and a key that it
+ * would round past 127 is 127).  A mean that is not finite gives key 0 and scale NaN.
  *   cache_seqlens  device int32 [batch], as for mla_decode_kvcache
  *   starts         device int32 [batch] (e.g. the lengths before the last write),
  *                  or NULL: every page of every sequence

@@ -4,8 +4,9 @@
 // For a page with n rows inside its sequence:
 //   mean[c] = (sum over its rows of k[c]) / n        fp32, absent rows as 0,
 //             summed as a balanced tree over the row index (neighbours first)
-//   scale   = max_c |mean[c]| / 127                  (1 for a mean of zeros)
-//   key[c]  = rint(mean[c] / scale)                  -127 .. 127
+//   scale   = max_c |mean[c]| / 127                  (1 for a mean of zeros, else 2^-149 at least)
+//   key[c]  = rint(mean[c] / scale)                  -127 .. 127: limited, since a subnormal
+//             scale has few bits and the quotient may round to 128
 // The order of the sums and the roundings (IEEE fp32 throughout) are part of
 // the definition, so a page's key has one value however it is computed.  A page
 // whose mean is not finite gets zero codes and a NaN scale (its score is then
@@ -166,10 +167,11 @@ __global__ void __launch_bounds__(kKeyThreads, key_ctas(E4M3)) page_keys_kernel(
 #pragma unroll
         for (int i = 0; i < kKeyThreads / 32; ++i) top = max(top, __float_as_uint(s_max[i]));
         const bool finite = top < 0x7f800000u;
-        const float scale = !finite ? __uint_as_float(0x7fffffffu) : top ? __uint_as_float(top) / 127.f : 1.f;
+        const float scale = !finite ? __uint_as_float(0x7fffffffu) : top ? fmaxf(__uint_as_float(top) / 127.f, 0x1p-149f) : 1.f;
         if (blk >= 0 && 2 * tid < D) {
             char2 k = make_char2(0, 0);
-            if (finite) k = make_char2((signed char)__float2int_rn(m0 / scale), (signed char)__float2int_rn(m1 / scale));
+            const auto code = [&](float m) { return (signed char)__float2int_rn(fminf(fmaxf(m / scale, -127.f), 127.f)); };
+            if (finite) k = make_char2(code(m0), code(m1));
             reinterpret_cast<char2 *>(p.keys + (size_t)blk * D)[tid] = k;
         }
         if (blk >= 0 && tid == 0) p.scales[blk] = scale;
