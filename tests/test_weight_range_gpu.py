@@ -207,3 +207,34 @@ def test_the_scale_of_a_node_that_nothing_sees(dev, bad, h):
     assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
     spoil(6)
     assert decode()[2] == _lib.MLA_DEVERR_SCALE
+
+
+@pytest.mark.parametrize("s_q,h,lens,num_parts", [
+    (1, 16, [1, 64, 65], None), (8, 16, [500, 8, 71], None), (7, 30, [64, 130, 9], 3), (33, 4, [33, 100, 128], None),
+    (5, 128, [70, 200], 5), (3, 160, [65, 700, 129], None), (66, 8, [400, 75, 66, 129], 7), (1, 100, [3000, 5000], None)])
+def test_trees_of_many_shapes(dev, s_q, h, lens, num_parts):
+    """N(0, 1) rows and random trees under the bound above, which does not grow with the number of keys."""
+    from tests import test_tree_gpu as trees
+    q, cache, table, sees = trees.make(lens, s_q, h, 576, True, seed=s_q)
+    o, lse = trees.decode(dev, q, cache, table, lens, sees, num_parts=num_parts)
+    assert mla.mla_device_status() == 0
+    for b, T in enumerate(lens):
+        rows = rows_of(cache, table[b:b + 1], T)
+        for i in range(s_q):
+            see = [t for t in range(T) if t < T - s_q or sees[b][i, t - (T - s_q)]]
+            compare(o[b, i], lse[b, i], reference(q[b, i], rows[see]), f"sequence {b} token {i}")
+
+
+@pytest.mark.parametrize("s_q,h,lens,topk,causal", [
+    (1, 16, [1000, 1, 64, 65, 700], 5, False), (3, 32, [400, 66, 130, 321], 4, True), (1, 160, [900, 64], 8, False),
+    (4, 128, [1500, 300, 576], 6, True)])
+def test_selected_pages_of_many_shapes(dev, s_q, h, lens, topk, causal):
+    from tests import test_blocks_gpu as blocks
+    q, cache, table, keys, scales = blocks.make(lens, s_q, h, 576, True, seed=h)
+    o, lse, pages = blocks.decode(dev, q, cache, table, lens, keys, scales, topk, causal=causal)
+    assert mla.mla_device_status() == 0
+    for b, T in enumerate(lens):
+        for i in range(s_q):
+            n = R.token_len(T, s_q, i, causal)
+            pick = [p for p in pages[b, i].tolist() if p >= 0]
+            compare(o[b, i], lse[b, i], reference(q[b, i], rows_of(cache, table[b:b + 1], n, pick)), f"{b} {i}")
