@@ -1888,7 +1888,7 @@ __device__ void value_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
                 const int keep = min(s.T - pg * kPage, kPage);
                 const bool ok = widen_e4m3<16, 128>(
                     stage, stage + kVLandOff, tid,
-                    [&](int row) { return row < keep && (!kTree || ((tmask >> row) & 1ull) != 0); },
+                    [&](int row) { return row < keep; },
                     [&] {
                         mbar_arrive(c.bar(B_VREAD));
                         return warp_wait(c, B_VREAD, it & 1);
