@@ -1600,9 +1600,15 @@ __device__ void score_rows_e8(const DecodeParams &p, const Ctx &c, uint32_t tmem
             const int pb = (int)(it % kPBufs), scs = (int)(it % kScSlots);
             const uint32_t cs_s = smem_u32(c.base + kScaleOff) + (uint32_t)scs * kScBytes;
             if (!warp_wait(c, B_SCFULL + scs, (it / kScSlots) & 1)) return;
+            // the rows of the page that this row sees
+            int nvalid = row_ok ? T_row - pg * kPage : 0;
+            nvalid = nvalid < 0 ? 0 : (nvalid > kPage ? kPage : nvalid);
+            uint64_t vmask = ~0ull;
+            if ((pg + 1) * kPage > tree_base && nvalid > 0) vmask = tree_page_mask(p, s.b, qi, tree_base, pg);
+            if (nvalid < kPage) vmask &= nvalid > 0 ? (~0ull >> (kPage - nvalid)) : 0ull;
             // the smallest and largest |scale| of the sequence's tokens on this page (magnitude
-            // bits order as magnitudes do, NaN on top); one warp of the group reports those
-            // past the limit that some row of the tile sees
+            // bits order as magnitudes do, NaN on top); one past the limit is reported where a
+            // row sees it
             float cs_least, cs_most;
             {
                 const int nseq = min(kPage, s.T - pg * kPage);
@@ -1611,20 +1617,12 @@ __device__ void score_rows_e8(const DecodeParams &p, const Ctx &c, uint32_t tmem
                 const uint32_t hi = max(lane < nseq ? a : 0u, lane + 32 < nseq ? b : 0u);
                 cs_least = __uint_as_float(__reduce_min_sync(0xffffffffu, lo));
                 cs_most = __uint_as_float(__reduce_max_sync(0xffffffffu, hi));
-                if ((warp & 3) == 0 && !(cs_most < kE4ScaleLimit)) {
-                    const uint64_t seen =
-                        (pg + 1) * kPage > tree_base ? tree_tile_mask(p, s.b, s.tile, nodes, tree_base, pg) : ~0ull;
-                    const bool bad_a = lane < nseq && ((seen >> lane) & 1ull) && !(__uint_as_float(a) < kE4ScaleLimit);
-                    const bool bad_b = lane + 32 < nseq && ((seen >> (lane + 32)) & 1ull) && !(__uint_as_float(b) < kE4ScaleLimit);
-                    if (bad_a || bad_b) atomicOr(p.status, MLA_DEVERR_SCALE);
+                if (!(cs_most < kE4ScaleLimit)) {
+                    const uint32_t bad_a = __ballot_sync(0xffffffffu, !(__uint_as_float(a) < kE4ScaleLimit));
+                    const uint32_t bad_b = __ballot_sync(0xffffffffu, !(__uint_as_float(b) < kE4ScaleLimit));
+                    if (vmask & ((uint64_t)bad_b << 32 | bad_a)) atomicOr(p.status, MLA_DEVERR_SCALE);
                 }
             }
-            // the rows of the page that this row sees
-            int nvalid = row_ok ? T_row - pg * kPage : 0;
-            nvalid = nvalid < 0 ? 0 : (nvalid > kPage ? kPage : nvalid);
-            uint64_t vmask = ~0ull;
-            if ((pg + 1) * kPage > tree_base && nvalid > 0) vmask = tree_page_mask(p, s.b, qi, tree_base, pg);
-            if (nvalid < kPage) vmask &= nvalid > 0 ? (~0ull >> (kPage - nvalid)) : 0ull;
             // what the page adds to the allowance, from its largest weight and its sum of p ko
             auto earned = [&](float wmax, float sum, float &S) {
                 S = fmaxf(wmax, sum * cs_least);
