@@ -154,7 +154,7 @@ constexpr int kVStages = kE8 ? 3 : 2;          // value CTA ring: whole pages (d
 constexpr int kSBufs = kE8 ? 3 : 2;            // S buffers in TMEM (score CTA), one per step
 // P buffers (staging in the score CTA, landing in the value CTA).  fp8 products: a
 // group holds one from before its pass until P V has used it, so that with one per
-// group they bound the pace (1.08 us a page; four, and three V stages: 1.04)
+// group they bound the pace (four, and three V stages: 4 % less a page)
 constexpr int kPBufs = kE8 ? 4 : 2;
 constexpr int kKChunks = kD / 64;              // 9 (or 8) chunks of 64 dims (128 B rows)
 constexpr int kVChunks = kDv / 64;             // 8
@@ -1423,14 +1423,15 @@ __device__ void score_rows(const DecodeParams &p, const Ctx &c, uint32_t tmem, i
 //         pass 448, and with every new maximum, it is set anew, the largest weight then
 //         at 28..56, and O shrinks with it or stays; when B would fall below 0 it is
 //         raised, S then at 8..16, and O grows with it (negative: no weight so far)
-// What it costs, with the state that it carries: 1.5-3 % on scores of up to 1.5 nats'
-// spread, where nearly no page is run again, up to 25 % on scores that spread by 3 to 5.
-// Measured on GB300: 1.04 us a page (76 sequences of 16,384 tokens, one tile each:
-// 287 us) and about 14 us a further segment.  An S buffer is held for 3500 cycles by
-// its page's 36 MMAs (two issuers share the pipe) and 2700 by the pass, which with
-// three buffers is 2100 cycles a page, at 2.03 GHz the time measured; a fourth does
-// not fit beside Q.  (With half the MMAs a page takes 0.99 us: P's buffers close
-// next.  Without the TMEM loads or the staging stores it takes as long as with them.)
+// Keeping the allowance costs 3 % where scores spread by up to 1.5 nats and nearly no
+// page is run again (288 -> 298 us for 76 sequences of 16,384 tokens), and 10-25 % where
+// they spread by 3 to 5, since scales that are raised are lowered again.
+// Measured on GB300: 1.06 us a page (76 sequences of 16,384 tokens, one tile each:
+// 298 us) and about 14 us a further segment.  An S buffer is held for 3500 cycles by
+// its page's 36 MMAs (two issuers share the pipe) and about 2900 by the pass and the
+// state's chain, which with three buffers is 2150 cycles a page, at 2.03 GHz the time
+// measured; a fourth does not fit beside Q.  (With half the MMAs a page took 5 % less:
+// P's buffers close next.  Without the TMEM loads or the staging stores it took as long.)
 #if MLA_SPLIT_FP8 && MLA_SPLIT_TREE
 __device__ void score_rows_e8(const DecodeParams &p, const Ctx &c, uint32_t tmem, int part) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
