@@ -238,3 +238,30 @@ def test_selected_pages_of_many_shapes(dev, s_q, h, lens, topk, causal):
             n = R.token_len(T, s_q, i, causal)
             pick = [p for p in pages[b, i].tolist() if p >= 0]
             compare(o[b, i], lse[b, i], reference(q[b, i], rows_of(cache, table[b:b + 1], n, pick)), f"{b} {i}")
+
+
+@pytest.mark.parametrize("softmax_scale", [576 ** -0.5, -576 ** -0.5, 0.0])
+def test_scales_of_both_signs(dev, softmax_scale):
+    """Rows may be held as negative scales times negated codes, and the softmax scale may have any sign."""
+    T = 3000
+    q, cache, table = make(heavy_at(T, 0))
+    want_rows = rows_of(cache, table, T)
+    turned = torch.rand((cache.shape[0], 64), generator=torch.Generator().manual_seed(3)) < 0.5
+    codes, scales = cache[:, :64 * 576].view(-1, 64, 576), cache[:, 64 * 576:].view(torch.float32)
+    codes[turned] ^= 0x80
+    scales[turned] *= -1
+    rows = rows_of(cache, table, T)
+    assert torch.equal(rows, want_rows)
+    lens = torch.tensor([T], dtype=torch.int32, device=dev)
+    o, lse = mla.mla_decode_kvcache_tree_fp8(q.to(dev), cache.to(dev), table.to(dev), lens,
+                                             R.mask_words(R.ancestors([-1, 0]))[None].to(dev), 512,
+                                             softmax_scale=softmax_scale)
+    assert mla.mla_device_status() == 0
+    for i, n in ((0, T - 1), (1, T)):
+        compare(o[0, i], lse[0, i], reference(q[0, i].double() * (softmax_scale * 24), rows[:n]), f"token {i}")
+
+
+def test_a_long_sequence_behind_a_sink(dev):
+    T = 65536 + 77
+    check_tree(dev, *make(heavy_at(T, 0)), T, 76)
+    check_blocks(dev, *make(heavy_at(T, 0)), T, 512)
