@@ -578,6 +578,137 @@ MLA_API int mla_decode_kvcache_tree_fp8(const void *q, const void *kv_pages, int
                                         size_t workspace_bytes, struct CUstream_st *stream);
 
 /*
+ * mla_assign_pages — block tables, positions and slots of a step's new rows,
+ * pages taken from a free list on the device.
+ *
+ * Sequence b holds len_b = cache_seqlens[b] rows and gets n_b = cu_rows[b + 1] -
+ * cu_rows[b] more (one of a decoding step, a whole prompt), so it needs
+ * need_b = ceil((len_b + n_b) / 64) - ceil(len_b / 64) new pages.  The free
+ * list is a stack: of num_free pages, page k of the call is
+ * free_pages[num_free - 1 - k].  Sequences are taken in order; b is served when
+ * need_b = 0 or need_0 + .. + need_b <= num_free (the needs of all before it,
+ * served or not, so that nobody overtakes), and then
+ *   block_table[b][ceil(len_b / 64) ..]   its new pages, in order
+ *   new_seqlens[b]   len_b + n_b
+ *   positions[r]     len_b + r - cu_rows[b] for its rows r
+ *   slots[r]         64 * page + position % 64
+ * A sequence that is not served keeps its entries, new_seqlens[b] = len_b, and
+ * its rows get position 0 and slot -1 (as rows of no sequence do), which
+ * mla_norm_rope_cache_write skips.
+ *   cache_seqlens  device int32 [batch]
+ *   cu_rows        device int32 [batch + 1], ascending, at most num_rows
+ *   num_rows       rows of positions and slots, >= cu_rows[batch]
+ *   block_table    device int32 [batch][max_blocks_per_seq], in/out
+ *   free_pages     device int32 [max_free]; num_free  device int32 [1]
+ *   num_free_out   device int32 [1], out; may be num_free (the step is taken) or
+ *                  another word (the step is planned: free_pages is only read)
+ *   new_seqlens    device int32 [batch], out; may be cache_seqlens
+ *   positions, slots  device int32 / int64 [num_rows], out, or NULL
+ * A sequence whose bounds or lengths make no sense, or that would pass its table,
+ * is not served and needs nothing, and sets MLA_DEVERR_SEQLEN; a table entry that is
+ * no page where a row lands gives slot -1 and sets MLA_DEVERR_BLOCK_ID.
+ * One kernel, no workspace.  Errors: MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED
+ * (2^31 rows or pages), MLA_ERR_CUDA.
+ */
+MLA_API int mla_assign_pages(const int32_t *cache_seqlens, const int32_t *cu_rows, int batch, int64_t num_rows,
+                             int32_t *block_table, int max_blocks_per_seq, const int32_t *free_pages, int64_t max_free,
+                             const int32_t *num_free, int32_t *num_free_out, int32_t *new_seqlens, int32_t *positions,
+                             int64_t *slots, struct CUstream_st *stream);
+
+/*
+ * mla_release_pages — the pages of finished sequences back onto the free list.
+ *
+ * For every b with finished[b] != 0, in order: its ceil(cache_seqlens[b] / 64)
+ * table entries are pushed in order and set to -1, and its length becomes 0.
+ *   cache_seqlens  device int32 [batch], in/out;  finished  device int32 [batch]
+ *   num_blocks     pages of the pool
+ *   free_pages, max_free, num_free   as for mla_assign_pages, all in/out
+ * An entry outside [0, num_blocks) is not pushed (MLA_DEVERR_BLOCK_ID); pages past
+ * max_free are dropped (MLA_DEVERR_SEQLEN).  Errors: as mla_assign_pages.
+ */
+MLA_API int mla_release_pages(int32_t *cache_seqlens, const int32_t *finished, int batch, int32_t *block_table,
+                              int max_blocks_per_seq, int64_t num_blocks, int32_t *free_pages, int64_t max_free,
+                              int32_t *num_free, struct CUstream_st *stream);
+
+/*
+ * mla_rope_turns — rotation frequencies as turns per position, in units of 2^-64
+ * (host memory in, host memory out; the calls below take a device copy).
+ *
+ *   f_i = base^(-2 i / rope_dim) radians per position, i < rope_dim / 2
+ * For contexts `factor` times longer: f_i / factor, or, with original_positions
+ * > 0, f_i (1 - r_i) + f_i / factor * r_i, where the ramp r goes from 0 at the pair
+ * that makes fast_turns turns in original_positions to 1 at the one that makes
+ * slow_turns:
+ *   pair(t) = rope_dim ln(original_positions / (2 pi t)) / (2 ln base)
+ *   lo = max(0, floor(pair(fast_turns))), hi = min(rope_dim - 1, ceil(pair(slow_turns)))
+ *   r_i = clamp((i - lo) / max(hi - lo, 0.001), 0, 1)
+ *   rope_dim  even, > 0;  base > 1;  factor >= 1;  turns  int64 [rope_dim / 2], out
+ * Returns MLA_OK or MLA_ERR_INVALID_ARG.
+ */
+MLA_API int mla_rope_turns(int rope_dim, double base, double factor, int original_positions, double fast_turns,
+                           double slow_turns, int64_t *turns);
+
+/*
+ * mla_norm_rope — norm of every head and rotation of its last rope_dim values,
+ * in one pass, fp32 inside, rounded to bf16 once.
+ *
+ *   y = x / sqrt(mean(x^2) + eps) * weight          (weight NULL: y = x)
+ *   (a, b) = (a cos t - b sin t, b cos t + a sin t) * rope_scale
+ * for the pairs of the last rope_dim values, t = positions[token] * turns[i] (whole
+ * turns drop out exactly, at any position): pair i is (i, i + rope_dim / 2) of
+ * them, or (2 i, 2 i + 1) with `interleaved`.
+ *   x       device bf16 [num_tokens][heads][d], read with the two strides (elements,
+ *           multiples of 8); 16-byte aligned
+ *   d       a multiple of 8, at most 576
+ *   weight  device bf16 [d], 16-byte aligned, or NULL
+ *   positions  device int32 [num_tokens];  turns  device int64 [rope_dim / 2]
+ *   rope_dim   a multiple of 16, at most min(d, 256); 0: no rotation
+ *   out     device bf16, as x with its own strides, heads not overlapping; x
+ *           itself (same strides) for a call in place, which without a weight
+ *           touches the rotated values only.  No other overlap with x
+ * Errors: MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED, MLA_ERR_CUDA.
+ */
+MLA_API int mla_norm_rope(const void *x, int64_t x_token_stride, int64_t x_head_stride, int64_t num_tokens, int heads,
+                          int d, const void *weight, float eps, const int32_t *positions, const int64_t *turns,
+                          int rope_dim, int interleaved, float rope_scale, void *out, int64_t out_token_stride,
+                          int64_t out_head_stride, struct CUstream_st *stream);
+
+/*
+ * mla_norm_rope_cache_write — new rows from a projection's output into the cache
+ * in one pass: the 512 latent dims normalised, the 64 RoPE dims rotated (as
+ * mla_norm_rope), and the row stored at slots[r] = 64 * block + row of the page.
+ *   latent, k_rope  as for mla_cache_write (slices of one buffer, strides in
+ *                   elements, multiples of 8); k_rope, positions and turns are
+ *                   not read for d = 512
+ *   weight      device bf16 [512], 16-byte aligned, or NULL: latent as it is
+ *   positions   device int32 [num_rows];  turns  device int64 [32]
+ *   slots       device int64 [num_rows] (mla_assign_pages); negative: the row goes
+ *               nowhere; past the pool: the same, and MLA_DEVERR_BLOCK_ID
+ *   latent_out, k_rope_out   device bf16, out, or NULL: the rows as bf16 as well
+ *               (what the prompt path up-projects), for every row, slot or not
+ * Two rows of one call must not have the same slot.
+ * Errors: MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED (row width), MLA_ERR_CUDA.
+ */
+MLA_API int mla_norm_rope_cache_write(const void *latent, int64_t latent_stride, const void *k_rope, int64_t k_rope_stride,
+                                      int64_t num_rows, const void *weight, float eps, const int32_t *positions,
+                                      const int64_t *turns, int interleaved, float rope_scale, const int64_t *slots,
+                                      void *kcache, int64_t num_blocks, int d, void *latent_out, int64_t latent_out_stride,
+                                      void *k_rope_out, int64_t k_rope_out_stride, struct CUstream_st *stream);
+
+/*
+ * mla_norm_rope_cache_write_fp8 — the same into packed e4m3 pages (d = 576): a
+ * row's scale is max |y| / 448 (1 for zeros) of its fp32 values y, its codes
+ * e4m3(y / scale), rounded once.  A row that is not finite, or whose scale reaches
+ * the limit of the e4m3 decode, sets MLA_DEVERR_SCALE as in mla_cache_write_fp8.
+ */
+MLA_API int mla_norm_rope_cache_write_fp8(const void *latent, int64_t latent_stride, const void *k_rope,
+                                          int64_t k_rope_stride, int64_t num_rows, const void *weight, float eps,
+                                          const int32_t *positions, const int64_t *turns, int interleaved, float rope_scale,
+                                          const int64_t *slots, void *kv_pages, int64_t num_blocks, int d, void *latent_out,
+                                          int64_t latent_out_stride, void *k_rope_out, int64_t k_rope_out_stride,
+                                          struct CUstream_st *stream);
+
+/*
  * mla_device_status — read the device status word of the current device.
  *
  * Synchronizes the device, stores the OR of the MLA_DEVERR_* bits raised by

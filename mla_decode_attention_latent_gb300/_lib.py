@@ -41,7 +41,8 @@ MLA_DEVERR_SEQLEN = 0x4
 MLA_DEVERR_SCALE = 0x8
 
 # every call the C header declares, with its ctypes signature
-_P, _I, _I64, _SZ, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
+_P, _I, _I64, _SZ, _F, _D = (ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float,
+                             ctypes.c_double)
 SIGNATURES = {
     "mla_num_sm_parts": (_I, [_I, _I, _I, ctypes.POINTER(ctypes.c_int)]),
     "mla_get_metadata": (_I, [_P, _I, _I, _I, _I, _P, _P, _P]),
@@ -73,6 +74,14 @@ SIGNATURES = {
                                      _P, _P, _SZ, _P]),
     "mla_decode_kvcache_tree_fp8": (_I, [_P, _P, _I64, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _I, _F,
                                          _P, _P, _P, _SZ, _P]),
+    "mla_assign_pages": (_I, [_P, _P, _I, _I64, _P, _I, _P, _I64, _P, _P, _P, _P, _P, _P]),
+    "mla_release_pages": (_I, [_P, _P, _I, _P, _I, _I64, _P, _I64, _P, _P]),
+    "mla_rope_turns": (_I, [_I, _D, _D, _I, _D, _D, _P]),
+    "mla_norm_rope": (_I, [_P, _I64, _I64, _I64, _I, _I, _P, _F, _P, _P, _I, _I, _F, _P, _I64, _I64, _P]),
+    "mla_norm_rope_cache_write": (_I, [_P, _I64, _P, _I64, _I64, _P, _F, _P, _P, _I, _F, _P, _P, _I64, _I, _P, _I64, _P,
+                                       _I64, _P]),
+    "mla_norm_rope_cache_write_fp8": (_I, [_P, _I64, _P, _I64, _I64, _P, _F, _P, _P, _I, _F, _P, _P, _I64, _I, _P, _I64,
+                                           _P, _I64, _P]),
     "mla_device_status": (_I, [ctypes.POINTER(ctypes.c_int), _I]),
     "mla_set_timing_events": (_I, [_P, _P]),
     "mla_set_cluster_multicast": (_I, [_I]),

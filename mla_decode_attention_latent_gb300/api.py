@@ -723,6 +723,222 @@ def mla_decode_kvcache_tree_fp8(q: torch.Tensor, kv_pages: torch.Tensor, block_t
                         tile_scheduler_metadata, num_splits, tree_lens, softmax_scale, out, lse, workspace, True)
 
 
+# ---------------------------------------------------------------- pages of requests
+def mla_assign_pages(cache_seqlens: torch.Tensor, cu_rows: torch.Tensor, block_table: torch.Tensor,
+                     free_pages: torch.Tensor, num_free: torch.Tensor, num_rows: int,
+                     num_free_out: Optional[torch.Tensor] = None, new_seqlens: Optional[torch.Tensor] = None,
+                     positions: Optional[torch.Tensor] = None, slots: Optional[torch.Tensor] = None
+                     ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Pages for a step's new rows, on the GPU: rows ``cu_rows[b] .. cu_rows[b + 1]`` of ``num_rows`` come behind
+    the ``cache_seqlens[b]`` rows of sequence b.  New pages are popped off the stack ``free_pages`` int32 [max_free]
+    (``num_free`` int32 [1], updated in place unless ``num_free_out`` is given) into ``block_table``, in place.
+
+    Returns (new_seqlens int32 [b], positions int32 [num_rows], slots int64 [num_rows]: 64 * page + row of the page).
+    A sequence for which the pages no longer suffice keeps its length, and its rows, like rows of no sequence, get
+    position 0 and slot -1; see ``include/mla_decode.h``.  ``new_seqlens`` may be ``cache_seqlens``."""
+    _need_cuda("block_table", block_table, torch.int32)
+    if block_table.dim() != 2 or block_table.shape[0] < 1 or block_table.shape[1] < 1:
+        raise ValueError("block_table must be [b, max_blocks], neither of them 0")
+    b, max_blocks = block_table.shape
+    dev = block_table.device
+    num_rows = int(num_rows)
+    if num_rows < 0:
+        raise ValueError("num_rows must not be negative")
+    lens = _vector(dev, "block_table", "cache_seqlens", cache_seqlens, b)
+    cu = _vector(dev, "block_table", "cu_rows", cu_rows, b + 1)
+    free, left = _free_list(dev, free_pages, num_free)
+    left_out = left if num_free_out is None else _vector(dev, "block_table", "num_free_out", num_free_out, 1)
+    if new_seqlens is None:
+        new_seqlens = torch.empty_like(cache_seqlens)
+    if positions is None:
+        positions = torch.empty((num_rows,), dtype=torch.int32, device=dev)
+    if slots is None:
+        slots = torch.empty((num_rows,), dtype=torch.int64, device=dev)
+    new = _vector(dev, "block_table", "new_seqlens", new_seqlens, b)
+    pos = _vector(dev, "block_table", "positions", positions, num_rows)
+    _call("mla_assign_pages", dev, lens, cu, b, num_rows, block_table.data_ptr(), max_blocks, free, free_pages.shape[0], left,
+          left_out, new, pos, _slots(dev, "block_table", slots, num_rows))
+    return new_seqlens, positions, slots
+
+
+def mla_release_pages(cache_seqlens: torch.Tensor, finished: torch.Tensor, block_table: torch.Tensor, num_blocks: int,
+                      free_pages: torch.Tensor, num_free: torch.Tensor) -> None:
+    """Push the pages of every sequence with ``finished[b] != 0`` (int32 [b]) back onto the free list, in place: its
+    table entries become -1 and its length 0.  ``num_blocks``: pages of the pool."""
+    _need_cuda("block_table", block_table, torch.int32)
+    if block_table.dim() != 2 or block_table.shape[0] < 1 or block_table.shape[1] < 1:
+        raise ValueError("block_table must be [b, max_blocks], neither of them 0")
+    b, max_blocks = block_table.shape
+    dev = block_table.device
+    lens = _vector(dev, "block_table", "cache_seqlens", cache_seqlens, b)
+    done = _vector(dev, "block_table", "finished", finished, b)
+    free, left = _free_list(dev, free_pages, num_free)
+    _call("mla_release_pages", dev, lens, done, b, block_table.data_ptr(), max_blocks, int(num_blocks), free,
+          free_pages.shape[0], left)
+
+
+def _free_list(dev, free_pages, num_free):
+    """Check a free list; returns the addresses of its pages and of their count."""
+    free = _on(dev, "block_table", "free_pages", free_pages, torch.int32)
+    if free_pages.dim() != 1 or free_pages.shape[0] < 1:
+        raise ValueError("free_pages must be [max_free], not empty")
+    return free, _vector(dev, "block_table", "num_free", num_free, 1)
+
+
+def _slots(dev, of, slots, n):
+    """Check an int64 [n] of slots; returns its address."""
+    ptr = _on(dev, of, "slots", slots, torch.int64)
+    if slots.dim() != 1 or slots.shape[0] != n:
+        raise ValueError(f"slots must be [{n}]")
+    return ptr
+
+
+# ---------------------------------------------------------------- norms and rotations
+def mla_rope_turns(rope_dim: int, base: float = 10000.0, factor: float = 1.0, original_positions: int = 0,
+                   fast_turns: float = 32.0, slow_turns: float = 1.0,
+                   device: Optional[torch.device] = None) -> torch.Tensor:
+    """Rotation frequencies for the calls below, int64 [rope_dim / 2] on ``device``: turns per position in units of
+    2^-64.  Contexts ``factor`` times longer divide every frequency by ``factor``, or, with ``original_positions``,
+    those of the slow pairs only, over a ramp (``include/mla_decode.h``).  Computed once per model."""
+    rope_dim = int(rope_dim)
+    if rope_dim < 2:
+        raise ValueError("rope_dim must be even and positive")
+    host = torch.empty((rope_dim // 2,), dtype=torch.int64)
+    check("mla_rope_turns", load().mla_rope_turns(rope_dim, float(base), float(factor), int(original_positions),
+                                                  float(fast_turns), float(slow_turns), host.data_ptr()))
+    return host.to(device if device is not None else torch.device("cuda", torch.cuda.current_device()))
+
+
+def _weight(dev, of, weight, d):
+    """Check a norm's weight (bf16 [d]) or None; returns its address."""
+    if weight is None:
+        return None
+    ptr = _on(dev, of, "weight", weight, torch.bfloat16)
+    if weight.dim() != 1 or weight.shape[0] != d:
+        raise ValueError(f"weight must be [{d}]")
+    if ptr % 16:
+        raise ValueError("weight must be 16-byte aligned")
+    return ptr
+
+
+def _heads(name: str, t: torch.Tensor, dev: Optional[torch.device], of: str) -> Tuple[int, int]:
+    """bf16 [n, heads, d] with unit inner stride, 16-byte aligned heads; returns the strides of a token and a head."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if dev is not None and t.device != dev:
+        _same_device(dev, of, **{name: t})
+    if t.dim() != 3 or t.shape[1] < 1 or t.shape[2] < 1:
+        raise ValueError(f"{name} must be [n, heads, d]")
+    n, h, d = t.shape
+    token, head, inner = t.stride()
+    if h == 1:
+        head = -(-d // 8) * 8
+    if n <= 1:
+        token = max(token, (h - 1) * head + -(-d // 8) * 8)
+    if (inner != 1 and d > 1) or token % 8 or head % 8 or t.data_ptr() % 16:
+        raise ValueError(f"{name}: heads must be contiguous and 16-byte aligned, the strides multiples of 8 elements")
+    return token, head
+
+
+def mla_norm_rope(x: torch.Tensor, positions: Optional[torch.Tensor], turns: Optional[torch.Tensor],
+                  weight: Optional[torch.Tensor] = None, eps: float = 1e-6, interleaved: bool = False,
+                  rope_scale: float = 1.0, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Norm of every head of ``x`` bf16 [n, heads, d] (with ``weight`` bf16 [d]; None: no norm) and rotation of its
+    last ``2 * len(turns)`` values by ``positions`` int32 [n] (``turns`` from ``mla_rope_turns``; both None: no rotation),
+    in one pass.  Pairs are (i, i + half) of the rotated values, or neighbours with ``interleaved``; the rotated
+    values are multiplied by ``rope_scale``.
+
+    ``x`` and ``out`` may be slices of wider heads (strides of a multiple of 8 elements).  ``out`` may be ``x``: the call
+    is then in place and, without a norm, touches the rotated values only.  Returns ``out``."""
+    x_token, x_head = _heads("x", x, None, "x")
+    n, h, d = x.shape
+    dev = x.device
+    rope_dim, pos, trn = 0, None, None
+    if (positions is None) != (turns is None):
+        raise ValueError("positions and turns come together")
+    if turns is not None:
+        trn = _on(dev, "x", "turns", turns, torch.int64)
+        if turns.dim() != 1 or turns.shape[0] < 1:
+            raise ValueError("turns must be [rope_dim / 2]")
+        rope_dim = 2 * turns.shape[0]
+        pos = _vector(dev, "x", "positions", positions, n)
+    w = _weight(dev, "x", weight, d)
+    if out is None:
+        out = torch.empty((n, h, d), dtype=torch.bfloat16, device=dev)
+    o_token, o_head = _heads("out", out, dev, "x")
+    if out.shape != x.shape:
+        raise ValueError("out must have the shape of x")
+    if out.data_ptr() == x.data_ptr() and (x_token, x_head) != (o_token, o_head):
+        raise ValueError("a call in place needs the same strides on both sides")
+    _call("mla_norm_rope", dev, x.data_ptr(), x_token, x_head, n, h, d, w, float(eps), pos, trn, rope_dim,
+          int(bool(interleaved)), float(rope_scale), out.data_ptr(), o_token, o_head)
+    return out
+
+
+def _place_rows(call, latent, k_rope, positions, turns, slots, cache, weight, eps, interleaved, rope_scale, latent_out,
+                k_rope_out, fp8):
+    if fp8:
+        _need_cuda("kv_pages", cache, torch.uint8)
+        d = _lib.MLA_HEAD_DIM
+        if cache.dim() != 2 or cache.shape[1] != _FP8_PAGE:
+            raise ValueError(f"kv_pages must be [num_blocks, {_FP8_PAGE}]")
+    else:
+        _need_cuda("kcache", cache, torch.bfloat16)
+        if cache.dim() != 4 or cache.shape[1] != _lib.MLA_PAGE_SIZE or cache.shape[2] != 1:
+            raise ValueError("kcache must be [num_blocks, 64, 1, d]")
+        d = cache.shape[3]
+    dev = cache.device
+    n, rope = _row_count(latent), d - MLA_V_DIM
+    ls = _need_rows("latent", latent, MLA_V_DIM, n, dev, False)
+    rs, rope_ptr, pos, trn = 0, None, None, None
+    if rope > 0:
+        rs, rope_ptr = _need_rows("k_rope", k_rope, rope, n, dev, False), k_rope.data_ptr()
+        pos = _vector(dev, "cache", "positions", positions, n)
+        trn = _on(dev, "cache", "turns", turns, torch.int64)
+        if turns.dim() != 1 or 2 * turns.shape[0] != rope:
+            raise ValueError(f"turns must be [{rope // 2}]")
+    elif k_rope is not None or positions is not None or turns is not None or k_rope_out is not None:
+        raise ValueError("a cache of 512-wide rows has no RoPE part: k_rope, positions, turns and k_rope_out must be None")
+    at = _slots(dev, "cache", slots, n)
+    w = _weight(dev, "cache", weight, MLA_V_DIM)
+    lo, los, ro, ros = None, 0, None, 0
+    if latent_out is not None:
+        los, lo = _need_rows("latent_out", latent_out, MLA_V_DIM, n, dev, True), latent_out.data_ptr()
+    if k_rope_out is not None:
+        ros, ro = _need_rows("k_rope_out", k_rope_out, rope, n, dev, True), k_rope_out.data_ptr()
+    _call(call, dev, latent.data_ptr(), ls, rope_ptr, rs, n, w, float(eps), pos, trn, int(bool(interleaved)), float(rope_scale), at,
+          cache.data_ptr(), cache.shape[0], d, lo, los, ro, ros)
+
+
+def mla_norm_rope_cache_write(latent: torch.Tensor, k_rope: Optional[torch.Tensor], positions: Optional[torch.Tensor],
+                              turns: Optional[torch.Tensor], slots: torch.Tensor, kcache: torch.Tensor,
+                              weight: Optional[torch.Tensor] = None, eps: float = 1e-6, interleaved: bool = False,
+                              rope_scale: float = 1.0, latent_out: Optional[torch.Tensor] = None,
+                              k_rope_out: Optional[torch.Tensor] = None) -> None:
+    """New rows from a projection's output into the bf16 cache, in place and in one pass: ``latent`` bf16 [n, 512]
+    normalised with ``weight`` bf16 [512] (None: as it is), ``k_rope`` bf16 [n, 64] rotated by ``positions`` int32 [n],
+    the row stored at ``slots`` int64 [n] (``mla_assign_pages``; a negative slot: nowhere).  A cache of 512-wide
+    rows takes None for ``k_rope``, ``positions`` and ``turns``.  ``latent_out`` / ``k_rope_out`` get the same rows as
+    bf16, for the prompt path's up-projection.  Inputs and outputs may be slices of wider rows."""
+    _place_rows("mla_norm_rope_cache_write", latent, k_rope, positions, turns, slots, kcache, weight, eps, interleaved,
+                rope_scale, latent_out, k_rope_out, False)
+
+
+def mla_norm_rope_cache_write_fp8(latent: torch.Tensor, k_rope: torch.Tensor, positions: torch.Tensor,
+                                  turns: torch.Tensor, slots: torch.Tensor, kv_pages: torch.Tensor,
+                                  weight: Optional[torch.Tensor] = None, eps: float = 1e-6, interleaved: bool = False,
+                                  rope_scale: float = 1.0, latent_out: Optional[torch.Tensor] = None,
+                                  k_rope_out: Optional[torch.Tensor] = None) -> None:
+    """``mla_norm_rope_cache_write`` into packed e4m3 pages, each row quantised from its fp32 values with its own
+    scale max |y| / 448."""
+    _place_rows("mla_norm_rope_cache_write_fp8", latent, k_rope, positions, turns, slots, kv_pages, weight, eps,
+                interleaved, rope_scale, latent_out, k_rope_out, True)
+
+
 def mla_device_status(clear: bool = True) -> int:
     """Synchronize and return the OR of the MLA_DEVERR_* bits kernels raised."""
     v = ctypes.c_int(0)

@@ -106,6 +106,81 @@ struct SelectParams {
     unsigned int *status;
 };
 
+// One call that takes the pages of a step's new rows from the free list.
+struct AssignPagesParams {
+    const int32_t *seqlens;       // [batch] rows before the step
+    const int32_t *cu_rows;       // [batch + 1]
+    int batch;
+    int64_t num_rows;
+    int32_t *block_table;         // [batch][max_blocks]
+    int max_blocks;
+    const int32_t *free_pages;    // [max_free], the first num_free of them free
+    int64_t max_free;
+    const int32_t *num_free;
+    int32_t *num_free_out;        // may be num_free
+    int32_t *new_seqlens;         // [batch], may be seqlens
+    int32_t *positions;           // [num_rows] or null
+    int64_t *slots;               // [num_rows] or null
+    unsigned int *status;
+};
+
+// One call that returns the pages of finished sequences.
+struct ReleasePagesParams {
+    int32_t *seqlens;             // [batch], 0 afterwards where finished
+    const int32_t *finished;      // [batch]
+    int batch;
+    int32_t *block_table;         // [batch][max_blocks]
+    int max_blocks;
+    int64_t num_blocks;
+    int32_t *free_pages;          // [max_free]
+    int64_t max_free;
+    int32_t *num_free;
+    unsigned int *status;
+};
+
+// Rotation of a row's last rope_dim values.
+struct RopeParams {
+    const int32_t *positions;     // [num_rows], or null: no rotation
+    const int64_t *turns;         // [rope_dim / 2] turns per position, units of 2^-64
+    int rope_dim;
+    int interleaved;              // pairs (2 i, 2 i + 1), otherwise (i, i + rope_dim / 2)
+    float scale;                  // of the rotated values
+};
+
+// One call that normalises and rotates heads.
+struct NormRopeParams {
+    const uint16_t *x;            // [tokens][heads][d] bf16
+    int64_t x_token, x_head;      // strides in elements
+    uint16_t *out;
+    int64_t out_token, out_head;
+    const uint16_t *weight;       // [d] bf16, or null: no norm
+    float eps;
+    int64_t tokens;
+    int heads, d;
+    int first;                    // first value that the call writes: 0, or d - rope_dim (rotation in place)
+    RopeParams rope;
+};
+
+// One call that normalises latent rows, rotates their RoPE keys and places both.
+struct PlaceRowsParams {
+    const uint16_t *latent;       // [num_rows] rows of 512 bf16
+    int64_t latent_stride;
+    const uint16_t *k_rope;       // [num_rows] rows of 64 bf16 (d = 576)
+    int64_t k_rope_stride;
+    int64_t num_rows;
+    const uint16_t *weight;       // [512] bf16, or null: no norm
+    float eps;
+    RopeParams rope;
+    const int64_t *slots;         // [num_rows]: block * 64 + row of the page, negative: nowhere
+    void *cache;
+    int64_t num_blocks;
+    uint16_t *latent_out;         // rows of 512, or null
+    int64_t latent_out_stride;
+    uint16_t *k_rope_out;         // rows of 64, or null
+    int64_t k_rope_out_stride;
+    unsigned int *status;
+};
+
 // Workspace carve-up shared by the API, the split kernel and the combine.
 size_t workspace_bytes(int batch, int rows, int num_parts);
 void carve_workspace(void *ws, int batch, int rows, int num_parts, float **o_accum, float **lse_accum);
@@ -142,6 +217,11 @@ cudaError_t launch_page_scores(const SelectParams &p, cudaStream_t stream);
 cudaError_t launch_select_pages(const SelectParams &p, cudaStream_t stream);
 cudaError_t launch_tree_mask(const int32_t *parents, int batch, int s_q, uint32_t *mask, unsigned int *status,
                              cudaStream_t stream);
+
+cudaError_t launch_assign_pages(const AssignPagesParams &p, cudaStream_t stream);
+cudaError_t launch_release_pages(const ReleasePagesParams &p, cudaStream_t stream);
+cudaError_t launch_norm_rope(const NormRopeParams &p, cudaStream_t stream);
+cudaError_t launch_place_rows(const PlaceRowsParams &p, int d, bool e4m3, cudaStream_t stream);
 
 // decode of one query token per sequence on the tree kernels, without masks:
 // work entries are row tiles (partition: launch_schedule_tree)

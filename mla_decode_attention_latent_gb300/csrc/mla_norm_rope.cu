@@ -1,0 +1,332 @@
+// Norm and rotation of rows in one pass: query or key heads, and latent rows on
+// their way into the paged cache.
+//
+//   y = x / sqrt(mean(x^2) + eps) * w        (heads, or the 512 latent dims of a row; optional)
+//   (a, b) -> (a cos t - b sin t, b cos t + a sin t), each times `scale`, for the
+//   pairs of the last rope_dim values, t = position * frequency
+// in fp32 from bf16 values, rounded once when a value is stored.
+//
+// Angles.  A frequency is a whole number of 2^-64 turns per position, so the
+// phase of a position is one 64-bit product that drops whole turns by itself: exact
+// but for the frequency's own 2^-65, at any position, where an angle in radians
+// loses a bit for every doubling.  Its distance to the nearest whole turn goes to
+// sincospif as a float, so a small angle keeps its 24 bits.
+//
+// Heads: a group of 8 lanes per head, lane l taking the 16-byte pieces l, l + 8, ...
+// (128 contiguous bytes per load and group; a head of 192 keeps every lane busy,
+// where a warp per head would idle a quarter of them).  A CTA takes a run of
+// consecutive heads of consecutive tokens and computes the tokens' sines once, in
+// shared memory, for all of their heads.  Everything is loaded once and stays in
+// registers; the partner of a value in the half layout is loaded again by the lane
+// that needs it (from L1), before anything is stored, so that a call may be in place.
+// Bound by HBM on prompts and by the launch on single tokens.
+//
+// Rows: a warp per cached row, the 512 latent dims as 64 pieces over its lanes and
+// the RoPE key as 8 more; each lane computes one of the row's 32 angles.
+#include <cuda_runtime.h>
+
+#include "mla_internal.h"
+#include "mla_sm103.cuh"
+
+namespace mla {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kGroup = 8;                       // lanes of a head
+constexpr int kGroups = kThreads / kGroup;
+constexpr int kMaxPieces = 9;                   // 16-byte pieces of a lane: heads of up to 576 values
+constexpr int kMaxAngles = 4096;                // of a CTA: 32 KB
+
+// cosine and sine of position * turns, times scale
+__device__ __forceinline__ float2 angle(int position, int64_t turns, float scale) {
+    const int64_t phase = (int64_t)((uint64_t)turns * (uint64_t)(int64_t)position);  // turns to the nearest whole one, units of 2^-64
+    float s, c;
+    sincospif((float)phase * 0x1p-63f, &s, &c);
+    return make_float2(c * scale, s * scale);
+}
+
+__device__ __forceinline__ void widen8(uint4 x, float (&f)[8]) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+
+__device__ __forceinline__ uint4 round8(const float (&f)[8]) {
+    return make_uint4(sm103::pack_bf16(f[0], f[1]), sm103::pack_bf16(f[2], f[3]), sm103::pack_bf16(f[4], f[5]),
+                      sm103::pack_bf16(f[6], f[7]));
+}
+
+// sum of the squares of 8 values, each times k
+__device__ __forceinline__ float squares(uint4 x, float k = 1.f) {
+    float f[8], s = 0.f;
+    widen8(x, f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s = fmaf(f[i] * k, f[i] * k, s);
+    return s;
+}
+
+// 1 / sqrt(mean of x^2 + eps) for a row whose sum of squares of k x is sum(k), the
+// same in all of its lanes.  Values near the ends of the type, whose squares leave
+// fp32, are scaled by a power of two first; the whole warp takes that way together.
+template <typename Sum>
+__device__ __forceinline__ float inverse_rms(Sum sum, int d, float eps) {
+    float s = sum(1.f);
+    float inv = 1.f / sqrtf(s / (float)d + eps);
+    const bool large = !(s < 0x1p120f), small = s < 0x1p-90f && eps < 0x1p-60f;
+    if (__any_sync(0xffffffffu, large || small)) {
+        const float k = large ? 0x1p-70f : 0x1p70f;
+        s = sum(k);
+        if (large || small) inv = k / sqrtf(s / (float)d + eps * k * k);
+    }
+    return inv;
+}
+
+__device__ __forceinline__ void scale8(float (&f)[8], uint4 w, float r) {
+    float g[8];
+    widen8(w, g);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = f[i] * r * g[i];  // (x r first: at most sqrt(d))
+}
+
+// 8 values of the rotated part turned by the angles of their pairs.  Interleaved:
+// four pairs.  Halves: the values of the first (low) or second half, `other` their partners.
+template <bool kInterleaved>
+__device__ __forceinline__ void rotate8(float (&f)[8], const float (&other)[8], const float2 (&cs)[8], bool low) {
+    if constexpr (kInterleaved) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float a = f[2 * k], b = f[2 * k + 1];
+            f[2 * k] = a * cs[k].x - b * cs[k].y;
+            f[2 * k + 1] = b * cs[k].x + a * cs[k].y;
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] = low ? f[k] * cs[k].x - other[k] * cs[k].y : f[k] * cs[k].x + other[k] * cs[k].y;
+    }
+}
+
+// kPieces: 16-byte pieces of a lane
+template <int kPieces, bool kNorm, bool kInterleaved>
+__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeParams p, int rows_per_cta) {
+    extern __shared__ float2 s_angle[];  // [tokens of the CTA][rope_dim / 2]
+    sm103::griddep_wait();
+    const int group = threadIdx.x / kGroup, lane = threadIdx.x % kGroup;
+    const int64_t rows = p.tokens * p.heads, row0 = (int64_t)blockIdx.x * rows_per_cta;
+    const int64_t row1 = min(row0 + rows_per_cta, rows);
+    const int64_t token0 = row0 / p.heads;
+    const int pairs = p.rope.positions ? p.rope.rope_dim / 2 : 0;
+    if (pairs) {
+        const int tokens = (int)((row1 - 1) / p.heads - token0) + 1;
+        for (int i = threadIdx.x; i < tokens * pairs; i += kThreads) {
+            const int t = i / pairs, k = i - t * pairs;
+            s_angle[i] = angle(p.rope.positions[token0 + t], p.rope.turns[k], p.rope.scale);
+        }
+        __syncthreads();
+    }
+    const int piece0 = p.first / 8, pieces = p.d / 8, rope0 = pieces - pairs / 4, half = pairs / 8;
+    uint4 w[kPieces], wo[kPieces];
+    if constexpr (kNorm) {
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) {
+            const int i = piece0 + lane + kGroup * j;
+            if (i < pieces) w[j] = reinterpret_cast<const uint4 *>(p.weight)[i];
+            if (!kInterleaved && i >= rope0 && i < pieces)
+                wo[j] = reinterpret_cast<const uint4 *>(p.weight)[i - rope0 < half ? i + half : i - half];
+        }
+    }
+    // every group makes the same number of turns, for the shuffles
+    for (int64_t r = row0 + group; r - group < row1; r += kGroups) {
+        const bool on = r < row1;
+        const int64_t row = on ? r : row1 - 1, token = row / p.heads;
+        const int head = (int)(row - token * p.heads);
+        const uint4 *src = reinterpret_cast<const uint4 *>(p.x + token * p.x_token + head * p.x_head);
+        uint4 *dst = reinterpret_cast<uint4 *>(p.out + token * p.out_token + head * p.out_head);
+        uint4 x[kPieces], o[kPieces];
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) {
+            const int i = piece0 + lane + kGroup * j;
+            x[j] = o[j] = make_uint4(0, 0, 0, 0);
+            if (i < pieces) x[j] = src[i];
+            if (!kInterleaved && i >= rope0 && i < pieces) o[j] = src[i - rope0 < half ? i + half : i - half];
+        }
+        float inv = 1.f;
+        if constexpr (kNorm) {
+            inv = inverse_rms([&](float k) {
+                float s = 0.f;
+#pragma unroll
+                for (int j = 0; j < kPieces; ++j) s += squares(x[j], k);
+#pragma unroll
+                for (int off = 1; off < kGroup; off <<= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+                return s;
+            }, p.d, p.eps);
+        }
+        __syncwarp();  // in place: every load of the warp's heads comes before a store
+        if (!on) continue;
+        const float2 *cs = s_angle + (int)(token - token0) * pairs;
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) {
+            const int i = piece0 + lane + kGroup * j;
+            if (i >= pieces) continue;
+            uint4 y = x[j];
+            if (kNorm || i >= rope0) {
+                float f[8], g[8];
+                widen8(x[j], f);
+                if constexpr (kNorm) scale8(f, w[j], inv);
+                if (i >= rope0) {
+                    if constexpr (!kInterleaved) {
+                        widen8(o[j], g);
+                        if constexpr (kNorm) scale8(g, wo[j], inv);
+                    }
+                    const int part = i - rope0;
+                    const bool low = part < half;
+                    float2 t[8];
+#pragma unroll
+                    for (int k = 0; k < (kInterleaved ? 4 : 8); ++k) t[k] = cs[kInterleaved ? 4 * part + k : 8 * (low ? part : part - half) + k];
+                    rotate8<kInterleaved>(f, g, t, low);
+                }
+                y = round8(f);
+            }
+            dst[i] = y;
+        }
+    }
+}
+
+template <int kPieces>
+cudaError_t launch_heads(const NormRopeParams &p, cudaStream_t stream) {
+    const int pairs = p.rope.positions ? p.rope.rope_dim / 2 : 0;
+    const int64_t rows = p.tokens * p.heads;
+    int sms = 0;
+    cudaError_t e = device_sm_count(&sms);
+    if (e != cudaSuccess) return e;
+    // a turn of the CTA's groups each while that gives every SM several CTAs, four at most
+    int per_cta = kGroups * (int)max((int64_t)1, min((int64_t)4, rows / (kGroups * 8 * (int64_t)sms)));
+    if (pairs) {
+        // the tokens that a run of heads touches have their angles in shared memory
+        const int tokens = kMaxAngles / pairs;
+        while (per_cta > 1 && (per_cta - 1) / p.heads + 2 > tokens) per_cta /= 2;
+    }
+    const size_t smem = pairs ? ((size_t)(per_cta - 1) / p.heads + 2) * pairs * sizeof(float2) : 0;
+    const int64_t ctas = (rows + per_cta - 1) / per_cta;
+    if (ctas > 0x7fffffffll) return cudaErrorInvalidValue;
+    const bool il = p.rope.interleaved != 0;
+    void (*kernel)(NormRopeParams, int) = p.weight ? (il ? norm_rope_kernel<kPieces, true, true> : norm_rope_kernel<kPieces, true, false>)
+                                                   : (il ? norm_rope_kernel<kPieces, false, true> : norm_rope_kernel<kPieces, false, false>);
+    return launch_after(kernel, dim3((unsigned)ctas), dim3(kThreads), smem, stream, p, per_cta);
+}
+
+// ---------------------------------------------------------------- rows into the cache
+constexpr int kRowWarps = 8;
+constexpr int kRopeDims = kDqk - kDv;
+
+template <int D, bool kE4m3>
+__global__ void __launch_bounds__(kRowWarps * 32) place_rows_kernel(const PlaceRowsParams p) {
+    constexpr bool kRope = D > kDv;
+    sm103::griddep_wait();
+    const int lane = threadIdx.x & 31;
+    const int64_t r = (int64_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
+    if (r >= p.num_rows) return;
+    const uint4 *src = reinterpret_cast<const uint4 *>(p.latent + r * p.latent_stride);
+    const uint4 raw[2] = {src[lane], src[lane + 32]};
+    uint4 key = make_uint4(0, 0, 0, 0), other = make_uint4(0, 0, 0, 0);
+    const int half = kRopeDims / 16;
+    if constexpr (kRope) {
+        const uint4 *at = reinterpret_cast<const uint4 *>(p.k_rope + r * p.k_rope_stride);
+        key = at[lane & 7];
+        if (!p.rope.interleaved) other = at[(lane & 7) ^ half];
+    }
+    const int64_t slot = p.slots[r];
+    float f[3][8];
+    widen8(raw[0], f[0]);
+    widen8(raw[1], f[1]);
+    if (p.weight) {
+        const float inv = inverse_rms([&](float k) {
+            float s = squares(raw[0], k) + squares(raw[1], k);
+#pragma unroll
+            for (int off = 16; off; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+            return s;
+        }, kDv, p.eps);
+        const uint4 *w = reinterpret_cast<const uint4 *>(p.weight);
+        scale8(f[0], w[lane], inv);
+        scale8(f[1], w[lane + 32], inv);
+    }
+    if constexpr (kRope) {
+        // lane i turns pair i; eight lanes (four groups of them, alike) need 8 or 4 pairs each
+        const float2 mine = angle(p.rope.positions[r], p.rope.turns[lane], p.rope.scale);
+        float g[8];
+        widen8(key, f[2]);
+        widen8(other, g);
+        const int i = lane & 7;
+        float2 cs[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int from = p.rope.interleaved ? 4 * i + (k & 3) : 8 * (i & 3) + k;
+            cs[k].x = __shfl_sync(0xffffffffu, mine.x, from);
+            cs[k].y = __shfl_sync(0xffffffffu, mine.y, from);
+        }
+        if (p.rope.interleaved) rotate8<true>(f[2], g, cs, true);
+        else rotate8<false>(f[2], g, cs, i < half);
+    }
+    if (p.latent_out) {
+        uint4 *out = reinterpret_cast<uint4 *>(p.latent_out + r * p.latent_out_stride);
+        out[lane] = round8(f[0]);
+        out[lane + 32] = round8(f[1]);
+    }
+    if (kRope && p.k_rope_out && lane < 8) reinterpret_cast<uint4 *>(p.k_rope_out + r * p.k_rope_out_stride)[lane] = round8(f[2]);
+    if (slot < 0) return;
+    if (slot >= p.num_blocks * kPage) {
+        if (lane == 0) atomicOr(p.status, MLA_DEVERR_BLOCK_ID);
+        return;
+    }
+    if constexpr (!kE4m3) {
+        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.cache) + slot * D);
+        dst[lane] = round8(f[0]);
+        dst[lane + 32] = round8(f[1]);
+        if (kRope && lane < 8) dst[64 + lane] = round8(f[2]);
+    } else {
+        // the row's largest magnitude, by its bits: infinities and NaN on top
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < 3; ++j)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(f[j][k]) & 0x7fffffffu);
+        top = __reduce_max_sync(0xffffffffu, top);
+        const float c = top >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : top ? fmaxf(__uint_as_float(top) / 448.f, 0x1p-149f) : 1.f;
+        uint8_t *page = static_cast<uint8_t *>(p.cache) + (slot / kPage) * (int64_t)MLA_FP8_PAGE_BYTES(kDqk);
+        const int off = (int)(slot % kPage);
+        if (lane == 0) {
+            if (!(c < (float)MLA_FP8_SCALE_LIMIT)) atomicOr(p.status, MLA_DEVERR_SCALE);
+            reinterpret_cast<float *>(page + kPage * kDqk)[off] = c;
+        }
+        uint2 *dst = reinterpret_cast<uint2 *>(page + off * kDqk);
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {
+            uint32_t code[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) code[k] = sm103::pack_e4m3x2(f[j][2 * k] / c + 0.f, f[j][2 * k + 1] / c + 0.f);
+            if (j < 2 || lane < 8) dst[lane + 32 * j] = make_uint2(code[0] | (code[1] << 16), code[2] | (code[3] << 16));
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_norm_rope(const NormRopeParams &p, cudaStream_t stream) {
+    switch (((p.d - p.first) / 8 + kGroup - 1) / kGroup) {
+        case 1: return launch_heads<1>(p, stream);
+        case 2: return launch_heads<2>(p, stream);
+        case 3: return launch_heads<3>(p, stream);
+        case 4: return launch_heads<4>(p, stream);
+        default: return launch_heads<kMaxPieces>(p, stream);
+    }
+}
+
+cudaError_t launch_place_rows(const PlaceRowsParams &p, int d, bool e4m3, cudaStream_t stream) {
+    const unsigned grid = (unsigned)((p.num_rows + kRowWarps - 1) / kRowWarps);
+    void (*kernel)(PlaceRowsParams) = e4m3 ? place_rows_kernel<kDqk, true> : d == kDqk ? place_rows_kernel<kDqk, false> : place_rows_kernel<kDv, false>;
+    return launch_after(kernel, dim3(grid), dim3(kRowWarps * 32), 0, stream, p);
+}
+
+}  // namespace mla

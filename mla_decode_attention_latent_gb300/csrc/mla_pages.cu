@@ -1,0 +1,233 @@
+// Pages of requests: block tables, positions and slots of a step's new rows, and
+// the pages of finished requests back to the free list.
+//
+// Sequence b holds len_b rows in have_b = ceil(len_b / 64) pages and gets n_b =
+// cu_rows[b + 1] - cu_rows[b] more, so it needs
+//   need_b = ceil((len_b + n_b) / 64) - have_b
+// new pages.  The free list is a stack of num_free pages; page k of the step is
+// free_pages[num_free - 1 - k].  Sequences are taken in order: b is served when
+// need_b = 0 or need_0 + .. + need_b <= num_free, and its pages are the ones
+// behind the need of those before it.  (A sequence that needs pages and is served
+// has only served ones before it among those that need any, so the pages of a step
+// are the top of the stack without gaps.)  Row r of sequence b is at position
+// p = len_b + r - cu_rows[b], in slot 64 * page + p % 64.
+//
+// Everything follows from prefix sums of the need, which every CTA computes for
+// itself, so nothing is exchanged between CTAs: the page of a position is an
+// entry of the table as it was (have_b and below) or an entry of the free list.
+// One cluster of up to 8 CTAs runs the call: the words that are read by all and
+// may be updated in place (the lengths, the count of free pages) are written
+// behind a cluster barrier, so one launch does it and no workspace is kept.
+// Bound by latency: a chunk's lengths and bounds, its scan, one page id per row.
+#include <cuda_runtime.h>
+
+#include "mla_internal.h"
+#include "mla_schedule.cuh"
+#include "mla_sm103.cuh"
+
+namespace mla {
+namespace {
+
+constexpr int kThreads = 1024;  // also the sequences of a chunk
+constexpr int kMaxCtas = 8;     // portable cluster size
+constexpr int kRowsInFlight = 4;
+
+struct AssignShared {
+    long long warp[kThreads / 32];
+    int cu[kThreads + 1];
+    int len[kThreads];        // rows before the step; -1: not served
+    long long first[kThreads];  // pages that earlier sequences need
+};
+
+__global__ void __launch_bounds__(kThreads) assign_pages_kernel(const AssignPagesParams p) {
+    __shared__ AssignShared sh;
+    sm103::griddep_wait();
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int cta = blockIdx.x, ctas = gridDim.x;  // one cluster
+    int left = *p.num_free;
+    if (left < 0 || left > p.max_free) {
+        if (tid == 0) atomicOr(p.status, MLA_DEVERR_SEQLEN);
+        left = left < 0 ? 0 : (int)p.max_free;
+    }
+    const long long cap = (long long)p.max_blocks * kPage;
+    long long before = 0, taken = 0;  // pages needed, pages taken, by the chunks so far
+    for (int c0 = 0; c0 < p.batch; c0 += kThreads) {
+        const int n = min(kThreads, p.batch - c0), b = c0 + tid;
+        int len = 0, count = 0, need = 0;
+        bool bad = false;
+        if (tid < n) {
+            const int lo = p.cu_rows[b], hi = p.cu_rows[b + 1];
+            sh.cu[tid] = lo;
+            if (tid == n - 1) sh.cu[n] = hi;
+            len = p.seqlens[b];
+            count = hi - lo;
+            bad = lo < 0 || hi < lo || hi > p.num_rows || len < 0 || (long long)len + count > cap;
+            if (bad) atomicOr(p.status, MLA_DEVERR_SEQLEN);
+            else need = pages_of(len + count) - pages_of(len);
+        }
+        long long total;
+        const long long first = before + block_exclusive_scan<kThreads>((long long)need, sh.warp, &total);
+        const bool served = tid < n && !bad && (need == 0 || first + need <= left);
+        if (tid < n) {
+            sh.len[tid] = served ? len : -1;
+            sh.first[tid] = first;
+        }
+        long long used;
+        block_exclusive_scan<kThreads>((long long)(served ? need : 0), sh.warp, &used);  // its barriers publish the chunk
+        // every CTA has the chunk's lengths before one of them changes them
+        sm103::cluster_arrive();
+        // new table entries: a warp per sequence
+        for (int i = cta * (kThreads / 32) + (tid >> 5); i < n; i += ctas * (kThreads / 32)) {
+            const int l = sh.len[i];
+            if (l < 0) continue;
+            const int have = pages_of(l), end = pages_of(l + sh.cu[i + 1] - sh.cu[i]);
+            for (int c = have + lane; c < end; c += 32)
+                p.block_table[(size_t)(c0 + i) * p.max_blocks + c] = p.free_pages[left - 1 - (sh.first[i] + c - have)];
+        }
+        // the chunk's rows (and those before the first sequence and behind the last)
+        const long long r0 = c0 == 0 ? 0 : max(0, sh.cu[0]), r1 = c0 + n == p.batch ? p.num_rows : min((long long)sh.cu[n], (long long)p.num_rows);
+        const long long stride = (long long)ctas * kThreads;
+        for (long long r = r0 + (long long)cta * kThreads + tid; r < r1; r += stride * kRowsInFlight) {
+            int pos[kRowsInFlight], page[kRowsInFlight];
+            bool live[kRowsInFlight];
+#pragma unroll
+            for (int k = 0; k < kRowsInFlight; ++k) {
+                const long long row = r + k * stride;
+                int lo = 0, hi = n;  // the last i with cu[i] <= row
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (sh.cu[mid] <= row) lo = mid;
+                    else hi = mid;
+                }
+                const int l = sh.len[lo];
+                live[k] = row < r1 && l >= 0 && row >= sh.cu[lo] && row < sh.cu[lo + 1];
+                pos[k] = live[k] ? l + (int)(row - sh.cu[lo]) : 0;
+                page[k] = 0;
+                if (live[k]) {
+                    const int c = pos[k] / kPage, have = pages_of(l);
+                    page[k] = c < have ? p.block_table[(size_t)(c0 + lo) * p.max_blocks + c]
+                                       : p.free_pages[left - 1 - (sh.first[lo] + c - have)];
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kRowsInFlight; ++k) {
+                const long long row = r + k * stride;
+                if (row >= r1) continue;
+                if (live[k] && page[k] < 0) atomicOr(p.status, MLA_DEVERR_BLOCK_ID);
+                if (p.positions) p.positions[row] = pos[k];
+                if (p.slots) p.slots[row] = live[k] && page[k] >= 0 ? (int64_t)page[k] * kPage + pos[k] % kPage : -1;
+            }
+        }
+        sm103::cluster_wait();
+        if (cta == 0 && tid < n) p.new_seqlens[b] = served ? len + count : (len < 0 ? 0 : len);
+        before += total;
+        taken += used;
+        __syncthreads();  // the chunk in shared memory is used up
+    }
+    // behind the last chunk's barrier every CTA has read the count
+    if (cta == 0 && tid == 0) *p.num_free_out = (int)(left - taken);
+}
+
+// Pages of finished sequences onto the stack, in the order of the sequences and
+// of their pages; one CTA.  An entry that is no page is reported and not pushed.
+struct ReleaseShared {
+    long long warp[kThreads / 32];
+    int count[kThreads];
+    long long first[kThreads];
+};
+
+__global__ void __launch_bounds__(kThreads) release_pages_kernel(const ReleasePagesParams p) {
+    __shared__ ReleaseShared sh;
+    sm103::griddep_wait();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int left = *p.num_free;
+    if (left < 0 || left > p.max_free) {
+        if (tid == 0) atomicOr(p.status, MLA_DEVERR_SEQLEN);
+        left = left < 0 ? 0 : (int)p.max_free;
+    }
+    long long top = left;
+    for (int c0 = 0; c0 < p.batch; c0 += kThreads) {
+        const int n = min(kThreads, p.batch - c0);
+        // entries to push of each sequence
+        for (int i = warp; i < n; i += kThreads / 32) {
+            const int b = c0 + i;
+            int count = 0;
+            if (p.finished[b] != 0) {
+                int len = p.seqlens[b];
+                const long long cap = (long long)p.max_blocks * kPage;
+                if (len < 0 || len > cap) {
+                    if (lane == 0) atomicOr(p.status, MLA_DEVERR_SEQLEN);
+                    len = len < 0 ? 0 : (int)cap;
+                }
+                const int pages = pages_of(len);
+                for (int c = 0; c < pages; c += 32) {
+                    const bool in = c + lane < pages;
+                    const int id = in ? p.block_table[(size_t)b * p.max_blocks + c + lane] : 0;
+                    const bool good = in && id >= 0 && id < p.num_blocks;
+                    if (in && !good) atomicOr(p.status, MLA_DEVERR_BLOCK_ID);
+                    count += __popc(__ballot_sync(0xffffffffu, good));
+                }
+            }
+            if (lane == 0) sh.count[i] = count;
+        }
+        __syncthreads();
+        long long total;
+        const long long first = block_exclusive_scan<kThreads>((long long)(tid < n ? sh.count[tid] : 0), sh.warp, &total);
+        if (tid < n) sh.first[tid] = top + first;
+        __syncthreads();
+        for (int i = warp; i < n; i += kThreads / 32) {
+            const int b = c0 + i;
+            if (p.finished[b] == 0) continue;
+            const int len = p.seqlens[b];
+            const long long cap = (long long)p.max_blocks * kPage;
+            const int pages = pages_of(len < 0 ? 0 : len > cap ? (int)cap : len);
+            long long at = sh.first[i];
+            for (int c = 0; c < pages; c += 32) {
+                const bool in = c + lane < pages;
+                int32_t *entry = p.block_table + (size_t)b * p.max_blocks + c + lane;
+                const int id = in ? *entry : 0;
+                const bool good = in && id >= 0 && id < p.num_blocks;
+                const unsigned mask = __ballot_sync(0xffffffffu, good);
+                const long long to = at + __popc(mask & ((1u << lane) - 1u));
+                if (good) {
+                    if (to < p.max_free) p.free_pages[to] = id;
+                    else atomicOr(p.status, MLA_DEVERR_SEQLEN);
+                }
+                if (in) *entry = -1;
+                at += __popc(mask);
+            }
+            __syncwarp();
+            if (lane == 0) p.seqlens[b] = 0;
+        }
+        top += total;
+        __syncthreads();
+    }
+    if (tid == 0) *p.num_free = (int)min(top, (long long)p.max_free);
+}
+
+}  // namespace
+
+cudaError_t launch_assign_pages(const AssignPagesParams &p, cudaStream_t stream) {
+    // few rows and table entries: one CTA
+    const int ctas = p.num_rows <= 2 * kThreads && p.batch <= 128 ? 1 : kMaxCtas;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, assign_pages_kernel, p);
+}
+
+cudaError_t launch_release_pages(const ReleasePagesParams &p, cudaStream_t stream) {
+    return launch_after(release_pages_kernel, dim3(1), dim3(kThreads), 0, stream, p);
+}
+
+}  // namespace mla
