@@ -81,6 +81,7 @@ struct CUstream_st;
 #define MLA_V_DIM 512
 #define MLA_METADATA_INTS 8
 #define MLA_TILE_ROWS 128  /* query rows of one tensor-core tile */
+#define MLA_PREFILL_HEAD_DIM 128  /* dims of a prompt's heads, RoPE dims apart */
 /* fixed cost of one split-KV segment, in pages, used by the work partition */
 #define MLA_SCHED_FIXED_COST_PAGES 8
 /* cost, in pages, that the partition charges for needing the combine pass */
@@ -707,6 +708,68 @@ MLA_API int mla_norm_rope_cache_write_fp8(const void *latent, int64_t latent_str
                                           const int64_t *slots, void *kv_pages, int64_t num_blocks, int d, void *latent_out,
                                           int64_t latent_out_stride, void *k_rope_out, int64_t k_rope_out_stride,
                                           struct CUstream_st *stream);
+
+/*
+ * mla_prefill_metadata_ints, mla_prefill_workspace_bytes — int32 words of the work
+ * partition, and device scratch, of a prompt attention on the current device.  0 on
+ * invalid arguments.
+ */
+MLA_API int64_t mla_prefill_metadata_ints(int batch, int64_t num_q, int h_q, int h_kv);
+MLA_API size_t mla_prefill_workspace_bytes(int batch, int64_t num_q, int h_q, int h_kv);
+
+/*
+ * mla_get_metadata_prefill — work partition of a prompt attention: blocks of query
+ * tokens, the longest first, cut along their keys where that fills the GPU.
+ *
+ * It depends on the bounds and shapes only: one call serves every layer.
+ *   cu_q, cu_k, batch, num_q, num_k, h_q, h_kv, causal   as for mla_prefill
+ *   metadata   device int32 [mla_prefill_metadata_ints(...)], out
+ * Errors: MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED, MLA_ERR_CUDA.
+ */
+MLA_API int mla_get_metadata_prefill(const int32_t *cu_q, const int32_t *cu_k, int batch, int64_t num_q, int64_t num_k,
+                                     int h_q, int h_kv, int causal, int32_t *metadata, struct CUstream_st *stream);
+
+/*
+ * mla_prefill — attention of packed prompts, or of chunks of new tokens behind a
+ * context that was read back (mla_cache_read) and up-projected.
+ *
+ * Query rows cu_q[b] .. cu_q[b + 1] attend to key rows cu_k[b] .. cu_k[b + 1] of the
+ * same sequence; query head h uses key head h / (h_q / h_kv).  With `causal`, row
+ * i of n_q sees the first n_k - n_q + i + 1 of the n_k keys (the last row sees all of
+ * them).  A row that sees nothing gets o = 0 and lse = -inf.
+ *   q        device bf16 [num_q][h_q][d_qk], d_qk = 128, or 192 with k_rope
+ *   k        device bf16 [num_k][h_kv][128]: the dims of a key without RoPE
+ *   v        device bf16 [num_k][h_kv][128] (d_v = 128)
+ *   k_rope   device bf16 [num_k][64], the RoPE dims of a key, shared by all heads
+ *            (the last 64 of d_qk), or NULL
+ *            each with strides in elements, multiples of 8, 16-byte aligned,
+ *            heads not overlapping (slices of wider rows)
+ *   cu_q, cu_k   device int32 [batch + 1], ascending, at most num_q / num_k.
+ *            Sequences whose bounds make no sense are skipped, with
+ *            MLA_DEVERR_SEQLEN
+ *   h_q      a multiple of h_kv, at most 128 h_kv
+ *   softmax_scale  > 0
+ *   metadata from mla_get_metadata_prefill with the same bounds and shapes, or NULL:
+ *            computed by this call, in the workspace
+ *   out      device bf16 [num_q][h_q][128], out;  lse  device fp32 [num_q][h_q], out:
+ *            natural log of the sum of exp(softmax_scale q . k), for joining with other
+ *            keys' results.  Rows of no sequence are left as they were
+ *   workspace  at least mla_prefill_workspace_bytes(...) bytes, 256-byte aligned; calls
+ *            that may overlap need workspaces of their own
+ * Keys and values that some row of their sequence sees must be finite (one that is not
+ * makes the rows that see it NaN, and may make those of the same 128-row tile); other
+ * rows of k, k_rope and v may hold any bits.  A query row that is not finite leaves the
+ * other rows as they are.
+ * Up to three kernels are enqueued (partition, attention, combine of cut blocks).  Stream
+ * order and graph capture: as for mla_decode_kvcache.  Errors: MLA_ERR_INVALID_ARG,
+ * MLA_ERR_UNSUPPORTED (widths, 2^30 rows), MLA_ERR_WORKSPACE, MLA_ERR_CUDA.
+ */
+MLA_API int mla_prefill(const void *q, int64_t q_token_stride, int64_t q_head_stride, const void *k, int64_t k_token_stride,
+                        int64_t k_head_stride, const void *v, int64_t v_token_stride, int64_t v_head_stride,
+                        const void *k_rope, int64_t k_rope_token_stride, const int32_t *cu_q, const int32_t *cu_k, int batch,
+                        int64_t num_q, int64_t num_k, int h_q, int h_kv, int d_qk, int d_v, float softmax_scale, int causal,
+                        const int32_t *metadata, void *out, float *lse, void *workspace, size_t workspace_bytes,
+                        struct CUstream_st *stream);
 
 /*
  * mla_device_status — read the device status word of the current device.

@@ -17,7 +17,8 @@ from .api import (flash_mla_with_kvcache, get_mla_metadata, mla_assign_pages, ml
                   mla_decode_kvcache_noalloc, mla_decode_kvcache_sparse, mla_decode_kvcache_tree,
                   mla_decode_kvcache_tree_fp8, mla_device_status, mla_get_metadata, mla_get_metadata_sparse,
                   mla_get_metadata_tree, mla_norm_rope, mla_norm_rope_cache_write, mla_norm_rope_cache_write_fp8,
-                  mla_num_sm_parts, mla_release_pages, mla_rope_turns, mla_set_cluster_multicast, mla_set_timing_events, mla_tree_mask,
+                  mla_get_metadata_prefill, mla_num_sm_parts, mla_prefill, mla_prefill_workspace_bytes,
+                  mla_release_pages, mla_rope_turns, mla_set_cluster_multicast, mla_set_timing_events, mla_tree_mask,
                   mla_tree_workspace_bytes,
                   mla_update_page_keys, mla_update_page_keys_fp8, mla_workspace_bytes)
 
@@ -29,6 +30,7 @@ __all__ = ["mla_get_metadata", "mla_get_metadata_sparse", "mla_decode_kvcache", 
            "mla_tree_mask", "mla_get_metadata_tree", "mla_tree_workspace_bytes", "mla_decode_kvcache_tree", "mla_decode_kvcache_tree_fp8",
            "mla_assign_pages", "mla_release_pages", "mla_rope_turns", "mla_norm_rope", "mla_norm_rope_cache_write",
            "mla_norm_rope_cache_write_fp8",
+           "mla_get_metadata_prefill", "mla_prefill_workspace_bytes", "mla_prefill",
            "mla_num_sm_parts", "mla_workspace_bytes", "mla_device_status", "mla_set_timing_events",
            "mla_set_cluster_multicast",
            "get_mla_metadata", "flash_mla_with_kvcache"]

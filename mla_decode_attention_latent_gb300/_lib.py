@@ -25,6 +25,7 @@ MLA_HEAD_DIM = 576
 MLA_V_DIM = 512
 MLA_METADATA_INTS = 8
 MLA_TILE_ROWS = 128
+MLA_PREFILL_HEAD_DIM = 128
 
 MLA_FP8_SCALE_LIMIT = 255
 
@@ -82,6 +83,11 @@ SIGNATURES = {
                                        _I64, _P]),
     "mla_norm_rope_cache_write_fp8": (_I, [_P, _I64, _P, _I64, _I64, _P, _F, _P, _P, _I, _F, _P, _P, _I64, _I, _P, _I64,
                                            _P, _I64, _P]),
+    "mla_prefill_metadata_ints": (_I64, [_I, _I64, _I, _I]),
+    "mla_prefill_workspace_bytes": (_SZ, [_I, _I64, _I, _I]),
+    "mla_get_metadata_prefill": (_I, [_P, _P, _I, _I64, _I64, _I, _I, _I, _P, _P]),
+    "mla_prefill": (_I, [_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _P, _P, _I, _I64, _I64, _I, _I, _I, _I, _F, _I,
+                         _P, _P, _P, _P, _SZ, _P]),
     "mla_device_status": (_I, [ctypes.POINTER(ctypes.c_int), _I]),
     "mla_set_timing_events": (_I, [_P, _P]),
     "mla_set_cluster_multicast": (_I, [_I]),

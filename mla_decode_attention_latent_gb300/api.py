@@ -939,6 +939,94 @@ def mla_norm_rope_cache_write_fp8(latent: torch.Tensor, k_rope: torch.Tensor, po
                 interleaved, rope_scale, latent_out, k_rope_out, True)
 
 
+# ---------------------------------------------------------------- prompt attention
+_HEAD = _lib.MLA_PREFILL_HEAD_DIM
+
+
+@functools.lru_cache(maxsize=256)
+def _prefill_sizes(index: int, batch: int, num_q: int, h_q: int, h_kv: int) -> Tuple[int, int]:
+    """(int32 words of the partition, workspace bytes) of a prompt attention on a device."""
+    with torch.cuda.device(index):
+        words = load().mla_prefill_metadata_ints(batch, num_q, h_q, h_kv)
+        size = load().mla_prefill_workspace_bytes(batch, num_q, h_q, h_kv)
+    if words == 0 or size == 0:
+        raise ValueError("invalid shape for a prompt attention: h_q must be a multiple of h_kv, at most 128 of it")
+    return int(words), int(size)
+
+
+def mla_prefill_workspace_bytes(batch: int, num_q: int, h_q: int, h_kv: int, device: Optional[torch.device] = None) -> int:
+    dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+    index = torch.cuda.current_device() if dev.index is None else dev.index
+    return _prefill_sizes(index, int(batch), int(num_q), int(h_q), int(h_kv))[1]
+
+
+def mla_get_metadata_prefill(cu_q: torch.Tensor, cu_k: torch.Tensor, num_q: int, num_k: int, h_q: int, h_kv: int,
+                             causal: bool = True) -> torch.Tensor:
+    """The work partition of a prompt attention over ``num_q`` query and ``num_k`` key rows (those of the tensors),
+    int32.  It depends on the bounds and shapes only: one call serves every layer of a step."""
+    _need_cuda("cu_q", cu_q, torch.int32)
+    dev = cu_q.device
+    b = cu_q.numel() - 1
+    if b < 1:
+        raise ValueError("cu_q must be [b + 1], b at least 1")
+    num_q, num_k, h_q, h_kv = int(num_q), int(num_k), int(h_q), int(h_kv)
+    q, k = _vector(dev, "cu_q", "cu_q", cu_q, b + 1), _vector(dev, "cu_q", "cu_k", cu_k, b + 1)
+    md = torch.empty((_prefill_sizes(dev.index, b, num_q, h_q, h_kv)[0],), dtype=torch.int32, device=dev)
+    _call("mla_get_metadata_prefill", dev, q, k, b, num_q, num_k, h_q, h_kv, int(bool(causal)), md.data_ptr())
+    return md
+
+
+def mla_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor, cu_k: torch.Tensor,
+                k_rope: Optional[torch.Tensor] = None, softmax_scale: Optional[float] = None, causal: bool = True,
+                metadata: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None
+                ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Attention of packed prompts, or of chunks of new tokens behind up-projected contexts: query rows
+    ``cu_q[b] .. cu_q[b + 1]`` of ``q`` bf16 [num_q, h_q, 128 (+ 64)] over key rows ``cu_k[b] .. cu_k[b + 1]`` of ``k`` and
+    ``v`` bf16 [num_k, h_kv, 128], with ``k_rope`` bf16 [num_k, 64] the last 64 dims of every head's key (None: none).
+    With ``causal``, row i of n_q sees the first n_k - n_q + i + 1 of n_k keys.  All may be slices of wider rows.
+
+    Returns (out bf16 [num_q, h_q, 128], lse fp32 [num_q, h_q]); rows that see nothing get 0 and -inf, rows of no
+    sequence are left as they were (unset in outputs that the call allocates).  ``metadata`` from
+    ``mla_get_metadata_prefill`` (computed when not given)."""
+    q_token, q_head = _heads("q", q, None, "q")
+    dev = q.device
+    k_token, k_head = _heads("k", k, dev, "q")
+    v_token, v_head = _heads("v", v, dev, "q")
+    num_q, h_q, d_qk = q.shape
+    num_k, h_kv, d_k = k.shape
+    rope = 0 if k_rope is None else _lib.MLA_HEAD_DIM - MLA_V_DIM
+    if d_k != _HEAD or d_qk != _HEAD + rope or v.shape != (num_k, h_kv, _HEAD) or h_q % h_kv:
+        raise ValueError(f"q must be [num_q, h_q, {_HEAD + rope}], k and v [num_k, h_kv, {_HEAD}], h_q a multiple of h_kv")
+    rope_ptr, rope_stride = None, 0
+    if k_rope is not None:
+        rope_stride, rope_ptr = _need_rows("k_rope", k_rope, rope, num_k, dev, True), k_rope.data_ptr()
+    if not (isinstance(cu_q, torch.Tensor) and cu_q.numel() > 1):
+        raise ValueError("cu_q must be [b + 1], b at least 1")
+    b = cu_q.numel() - 1
+    cq, ck = _vector(dev, "q", "cu_q", cu_q, b + 1), _vector(dev, "q", "cu_k", cu_k, b + 1)
+    words, need = _prefill_sizes(dev.index, b, num_q, h_q, h_kv)
+    md = None if metadata is None else _vector(dev, "q", "metadata", metadata, words)
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(d_qk)
+    if out is None:
+        out = torch.empty((num_q, h_q, _HEAD), dtype=torch.bfloat16, device=dev)
+    elif out.shape != (num_q, h_q, _HEAD):
+        raise ValueError(f"out must be [num_q, h_q, {_HEAD}]")
+    if lse is None:
+        lse = torch.empty((num_q, h_q), dtype=torch.float32, device=dev)
+    elif lse.shape != (num_q, h_q):
+        raise ValueError("lse must be [num_q, h_q]")
+    o_ptr, lse_ptr = _on(dev, "q", "out", out, torch.bfloat16), _on(dev, "q", "lse", lse, torch.float32)
+    if workspace is None:
+        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+    ws_ptr = _on(dev, "q", "workspace", workspace, torch.uint8)
+    _call("mla_prefill", dev, q.data_ptr(), q_token, q_head, k.data_ptr(), k_token, k_head, v.data_ptr(), v_token, v_head,
+          rope_ptr, rope_stride, cq, ck, b, num_q, num_k, h_q, h_kv, d_qk, _HEAD, float(softmax_scale), int(bool(causal)), md, o_ptr,
+          lse_ptr, ws_ptr, workspace.numel())
+    return out, lse
+
+
 def mla_device_status(clear: bool = True) -> int:
     """Synchronize and return the OR of the MLA_DEVERR_* bits kernels raised."""
     v = ctypes.c_int(0)

@@ -181,6 +181,35 @@ struct PlaceRowsParams {
     unsigned int *status;
 };
 
+// One prompt attention: packed sequences, d_qk = 128 or 128 + 64, d_v = 128.
+struct PrefillParams {
+    const uint16_t *q;            // [num_q][h_q][128 or 192] bf16, strides in elements
+    int64_t q_token, q_head;
+    const uint16_t *k;            // [num_k][h_kv][128]
+    int64_t k_token, k_head;
+    const uint16_t *v;            // [num_k][h_kv][128]
+    int64_t v_token, v_head;
+    const uint16_t *k_rope;       // [num_k][64], one for all heads (rope only)
+    int64_t k_rope_token;
+    int rope;                     // d_qk = 192
+    const int32_t *cu_q, *cu_k;   // [batch + 1]
+    int batch;
+    int64_t num_q, num_k;
+    int h_q, h_kv, group;         // group = h_q / h_kv
+    int causal;
+    float scale, scale_log2;      // softmax scale, and times log2(e)
+    uint16_t *out;                // [num_q][h_q][128]
+    float *lse;                   // [num_q][h_q]
+    int32_t *metadata;            // header, segments, cut blocks (mla_prefill.cuh)
+    int64_t max_segments;
+    int max_slots;
+    float *o_part;                // [max_slots][h_kv][256][128] fp32
+    float *lse_part;              // [max_slots][h_kv][256]
+    int sms;
+    int head_chunk;               // key heads that run side by side
+    unsigned int *status;
+};
+
 // Workspace carve-up shared by the API, the split kernel and the combine.
 size_t workspace_bytes(int batch, int rows, int num_parts);
 void carve_workspace(void *ws, int batch, int rows, int num_parts, float **o_accum, float **lse_accum);
@@ -222,6 +251,10 @@ cudaError_t launch_assign_pages(const AssignPagesParams &p, cudaStream_t stream)
 cudaError_t launch_release_pages(const ReleasePagesParams &p, cudaStream_t stream);
 cudaError_t launch_norm_rope(const NormRopeParams &p, cudaStream_t stream);
 cudaError_t launch_place_rows(const PlaceRowsParams &p, int d, bool e4m3, cudaStream_t stream);
+
+// prompt attention: the partition, then the kernel and the combine of cut blocks
+cudaError_t launch_prefill_schedule(const PrefillParams &p, cudaStream_t stream);
+cudaError_t launch_prefill(const PrefillParams &p, cudaStream_t stream);
 
 // decode of one query token per sequence on the tree kernels, without masks:
 // work entries are row tiles (partition: launch_schedule_tree)

@@ -6,6 +6,7 @@
 #include <cmath>
 
 #include "mla_internal.h"
+#include "mla_prefill.cuh"
 
 namespace mla {
 namespace {
@@ -62,6 +63,38 @@ int place_rows(const void *latent, int64_t latent_stride, const void *k_rope, in
     p.k_rope_out_stride = k_rope_out_stride;
     if (status_address(&p.status) != MLA_OK) return MLA_ERR_CUDA;
     return result(launch_place_rows(p, d, e4m3, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+constexpr size_t kAlign = 256;
+size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+
+// shapes that a prompt attention takes
+int prefill_shape(int batch, int64_t num_q, int h_q, int h_kv) {
+    if (batch < 1 || num_q < 0 || h_q < 1 || h_kv < 1 || h_q % h_kv) return MLA_ERR_INVALID_ARG;
+    if (h_q / h_kv > kPreTile || h_q > 16384 || num_q > 0x7fffffffLL / 2) return MLA_ERR_UNSUPPORTED;
+    return MLA_OK;
+}
+
+// words of the partition, and the workspace: the partial results of cut blocks, then
+// room for the partition when the caller brings none
+struct PrefillLayout {
+    int64_t max_segments;
+    int max_slots;
+    size_t words, o_part, lse_part, metadata, total;
+};
+
+PrefillLayout prefill_layout(int batch, int64_t num_q, int h_q, int h_kv, int sms) {
+    PrefillLayout l;
+    const int rows = kPreTiles * kPreTile;
+    l.max_slots = pre_max_slots(sms, h_kv);
+    l.max_segments = pre_max_segments(num_q, batch, h_q / h_kv, sms, h_kv);
+    l.words = (sizeof(PreHeader) + l.max_segments * sizeof(PreSegment) + l.max_slots * sizeof(PreCut)) / sizeof(int32_t);
+    const size_t parts = (size_t)l.max_slots * h_kv * rows;
+    l.o_part = 0;
+    l.lse_part = align_up(parts * kPreHead * sizeof(float));
+    l.metadata = l.lse_part + align_up(parts * sizeof(float));
+    l.total = l.metadata + align_up(l.words * sizeof(int32_t));
+    return l;
 }
 
 }  // namespace
@@ -194,6 +227,121 @@ int mla_norm_rope_cache_write_fp8(const void *latent, int64_t latent_stride, con
                                   int64_t k_rope_out_stride, struct CUstream_st *stream) {
     return place_rows(latent, latent_stride, k_rope, k_rope_stride, num_rows, weight, eps, positions, turns, interleaved, rope_scale,
                       slots, kv_pages, num_blocks, d, latent_out, latent_out_stride, k_rope_out, k_rope_out_stride, true, stream);
+}
+
+int64_t mla_prefill_metadata_ints(int batch, int64_t num_q, int h_q, int h_kv) {
+    int sms = 0;
+    if (prefill_shape(batch, num_q, h_q, h_kv) != MLA_OK || device_sm_count(&sms) != cudaSuccess) return 0;
+    return (int64_t)prefill_layout(batch, num_q, h_q, h_kv, sms).words;
+}
+
+size_t mla_prefill_workspace_bytes(int batch, int64_t num_q, int h_q, int h_kv) {
+    int sms = 0;
+    if (prefill_shape(batch, num_q, h_q, h_kv) != MLA_OK || device_sm_count(&sms) != cudaSuccess) return 0;
+    return prefill_layout(batch, num_q, h_q, h_kv, sms).total;
+}
+
+int mla_get_metadata_prefill(const int32_t *cu_q, const int32_t *cu_k, int batch, int64_t num_q, int64_t num_k, int h_q, int h_kv,
+                             int causal, int32_t *metadata, struct CUstream_st *stream) {
+    const int st = prefill_shape(batch, num_q, h_q, h_kv);
+    if (st != MLA_OK) return st;
+    if (!cu_q || !cu_k || !metadata || num_k < 0) return MLA_ERR_INVALID_ARG;
+    if (num_k > 0x7fffffffLL / 2) return MLA_ERR_UNSUPPORTED;
+    Range range("mla_get_metadata_prefill");
+    PrefillParams p{};
+    if (device_sm_count(&p.sms) != cudaSuccess) return MLA_ERR_CUDA;
+    const PrefillLayout l = prefill_layout(batch, num_q, h_q, h_kv, p.sms);
+    p.cu_q = cu_q;
+    p.cu_k = cu_k;
+    p.batch = batch;
+    p.num_q = num_q;
+    p.num_k = num_k;
+    p.h_q = h_q;
+    p.h_kv = h_kv;
+    p.group = h_q / h_kv;
+    p.causal = causal != 0;
+    p.metadata = metadata;
+    p.max_segments = l.max_segments;
+    p.max_slots = l.max_slots;
+    if (status_address(&p.status) != MLA_OK) return MLA_ERR_CUDA;
+    return result(launch_prefill_schedule(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int mla_prefill(const void *q, int64_t q_token_stride, int64_t q_head_stride, const void *k, int64_t k_token_stride,
+                int64_t k_head_stride, const void *v, int64_t v_token_stride, int64_t v_head_stride, const void *k_rope,
+                int64_t k_rope_token_stride, const int32_t *cu_q, const int32_t *cu_k, int batch, int64_t num_q, int64_t num_k,
+                int h_q, int h_kv, int d_qk, int d_v, float softmax_scale, int causal, const int32_t *metadata, void *out, float *lse,
+                void *workspace, size_t workspace_bytes, struct CUstream_st *stream) {
+    int st = prefill_shape(batch, num_q, h_q, h_kv);
+    if (st != MLA_OK) return st;
+    if (!cu_q || !cu_k || num_k < 0 || d_qk < 1 || d_v < 1) return MLA_ERR_INVALID_ARG;
+    if (num_q > 0 && (!q || !out || !lse || !workspace)) return MLA_ERR_INVALID_ARG;
+    if (num_q > 0 && num_k > 0 && (!k || !v)) return MLA_ERR_INVALID_ARG;
+    if (num_k > 0x7fffffffLL / 2) return MLA_ERR_UNSUPPORTED;
+    if (d_v != kPreHead || (d_qk != kPreHead && d_qk != kPreHead + kPreRope)) return MLA_ERR_UNSUPPORTED;
+    const bool rope = d_qk > kPreHead;
+    if (num_q > 0 && num_k > 0 && rope != (k_rope != nullptr)) return MLA_ERR_INVALID_ARG;  // empty tensors may be null
+    // rows are ranked by raw scores, which is the order of the scaled ones for a positive scale only
+    if (!(softmax_scale > 0.f) || !real(softmax_scale)) return MLA_ERR_INVALID_ARG;
+    auto heads = [](const void *ptr, int64_t token, int64_t head, int64_t n, int64_t h, int64_t d) {
+        // 16-byte aligned heads that do not overlap, strides that a tensor map holds
+        if (!aligned16(ptr) || token % 8 || head % 8 || token >= (1LL << 38) || head >= (1LL << 38)) return false;
+        return (head >= d && token >= (h - 1) * head + d) || (token >= d && head >= (n - 1) * token + d);
+    };
+    if (num_q > 0 && !heads(q, q_token_stride, q_head_stride, num_q, h_q, d_qk)) return MLA_ERR_INVALID_ARG;
+    if (num_q > 0 && num_k > 0) {
+        if (!heads(k, k_token_stride, k_head_stride, num_k, h_kv, kPreHead)) return MLA_ERR_INVALID_ARG;
+        if (!heads(v, v_token_stride, v_head_stride, num_k, h_kv, kPreHead)) return MLA_ERR_INVALID_ARG;
+        if (rope && !heads(k_rope, k_rope_token_stride, kPreRope, num_k, 1, kPreRope)) return MLA_ERR_INVALID_ARG;
+    }
+    if (!aligned16(out) || (reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1))) return MLA_ERR_INVALID_ARG;
+    if (num_q == 0) return MLA_OK;
+    PrefillParams p{};
+    if (device_sm_count(&p.sms) != cudaSuccess) return MLA_ERR_CUDA;
+    const PrefillLayout l = prefill_layout(batch, num_q, h_q, h_kv, p.sms);
+    if (workspace_bytes < l.total) return MLA_ERR_WORKSPACE;
+    Range range("mla_prefill");
+    char *ws = static_cast<char *>(workspace);
+    p.metadata = metadata ? const_cast<int32_t *>(metadata) : reinterpret_cast<int32_t *>(ws + l.metadata);
+    if (!metadata) {
+        st = mla_get_metadata_prefill(cu_q, cu_k, batch, num_q, num_k, h_q, h_kv, causal, p.metadata, stream);
+        if (st != MLA_OK) return st;
+    }
+    p.q = static_cast<const uint16_t *>(q);
+    p.q_token = q_token_stride;
+    p.q_head = q_head_stride;
+    p.k = static_cast<const uint16_t *>(k);
+    p.k_token = k_token_stride;
+    p.k_head = k_head_stride;
+    p.v = static_cast<const uint16_t *>(v);
+    p.v_token = v_token_stride;
+    p.v_head = v_head_stride;
+    p.k_rope = static_cast<const uint16_t *>(k_rope);
+    p.k_rope_token = k_rope_token_stride;
+    p.rope = rope;
+    p.cu_q = cu_q;
+    p.cu_k = cu_k;
+    p.batch = batch;
+    p.num_q = num_q;
+    p.num_k = num_k;
+    p.h_q = h_q;
+    p.h_kv = h_kv;
+    p.group = h_q / h_kv;
+    p.causal = causal != 0;
+    p.scale = softmax_scale;
+    p.scale_log2 = softmax_scale * 1.4426950408889634f;
+    p.out = static_cast<uint16_t *>(out);
+    p.lse = lse;
+    p.max_segments = l.max_segments;
+    p.max_slots = l.max_slots;
+    p.o_part = reinterpret_cast<float *>(ws + l.o_part);
+    p.lse_part = reinterpret_cast<float *>(ws + l.lse_part);
+    // key heads side by side: as many as keep their keys and values in half of L2
+    const int64_t head_bytes = (num_k > 0 ? num_k : 1) * 4 * kPreHead;
+    const int64_t side = (64LL << 20) / head_bytes;
+    p.head_chunk = (int)(side < 1 ? 1 : side > h_kv ? h_kv : side);
+    if (status_address(&p.status) != MLA_OK) return MLA_ERR_CUDA;
+    return result(launch_prefill(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"
