@@ -41,8 +41,8 @@ using namespace sm103;
 
 constexpr int kThreads = 384;
 // registers of a thread: 168 at launch, then a thread of the rows keeps its 128 scores and
-// gets some of the others' (256 x 208 + 128 x 88 = 384 x 168)
-constexpr int kRowRegs = 208, kOtherRegs = 88;
+// gets some of the others' (256 x 200 + 128 x 104 = 384 x 168)
+constexpr int kRowRegs = 200, kOtherRegs = 104;
 static_assert(256 * kRowRegs + 128 * kOtherRegs <= kThreads * 168, "a split of what the CTA was launched with");
 constexpr int kLoadWarp = 8, kMmaWarp = 9, kZeroWarp = 10;
 constexpr int kRows = kPreTiles * kPreTile;
@@ -97,10 +97,13 @@ struct Walk {
     int count;
     __device__ bool next(const PrefillParams &p, PreSegment &s, int &head) {
         if (at >= items) return false;
+        // every other round of the CTAs runs backwards: over lengths that fall, each CTA gets its share
+        const int64_t round = at / gridDim.x, last = min((long long)items - 1, (long long)(round + 1) * gridDim.x - 1);
+        const int64_t i = round & 1 ? last - (at - round * gridDim.x) : at;
         const int64_t per = (int64_t)count * chunk;
-        const int c = (int)(at / per);
+        const int c = (int)(i / per);
         const int heads = min(chunk, h_kv - c * chunk);
-        const int64_t in = at - c * per;
+        const int64_t in = i - c * per;
         s = segments[in / heads];
         head = c * chunk + (int)(in % heads);
         at += gridDim.x;
@@ -135,6 +138,16 @@ struct Tile {
     }
 };
 
+// One lane of a converged warp, the same one every time.  The load and MMA warps run
+// their role as whole warps and only issue in the elected lane: where one lane runs the
+// role alone, the compiler cannot tell that an operand is the same for the warp, and
+// an MMA costs its issuer 200 cycles instead of the 64 that it takes.
+__device__ __forceinline__ bool elected() {
+    uint32_t yes;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n}" : "=r"(yes));
+    return yes != 0;
+}
+
 // ---------------------------------------------------------------- loads
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, uint64_t *bar, int x, int head, int token) {
     asm volatile(
@@ -162,34 +175,40 @@ __device__ void load_role(const PrefillParams &p, const Ctx &c, const CUtensorMa
 #pragma unroll
                 for (int t = 0; t < kPreTiles; ++t) {
                     if (!ok || (t ? b.steps : a.steps) == 0) continue;
-                    ok = c.wait(B_QEMPTY + t, (qn[t] & 1) ^ 1);
+                    ok = __all_sync(0xffffffffu, c.wait(B_QEMPTY + t, (qn[t] & 1) ^ 1));
                     if (!ok) continue;
                     ++qn[t];
-                    mbar_arrive_expect_tx(c.bar(B_QFULL + t), L::kChunks * q_bytes);
-                    for (int ch = 0; ch < L::kChunks; ++ch)
-                        tma_load(smem_u32(c.base + (t * L::kChunks + ch) * kSlotBytes), mq, c.bar(B_QFULL + t), 64 * ch, head * p.group,
-                                 s.q0 + t * pre_tile_tokens(p.group));
+                    if (elected()) {
+                        mbar_arrive_expect_tx(c.bar(B_QFULL + t), L::kChunks * q_bytes);
+                        for (int ch = 0; ch < L::kChunks; ++ch)
+                            tma_load(smem_u32(c.base + (t * L::kChunks + ch) * kSlotBytes), mq, c.bar(B_QFULL + t), 64 * ch, head * p.group,
+                                     s.q0 + t * pre_tile_tokens(p.group));
+                    }
+                    __syncwarp();
                 }
                 continue;
             }
             const int k0 = s.k0 + (s.step0 + j) * kPreTile;
             for (int ch = 0; ch < L::kStepSlots && ok; ++ch, ++it) {
                 const int slot = it % L::kSlots;
-                ok = c.wait(B_EMPTY + slot, ((it / L::kSlots) & 1) ^ 1);
+                ok = __all_sync(0xffffffffu, c.wait(B_EMPTY + slot, ((it / L::kSlots) & 1) ^ 1));
                 if (!ok) break;
                 uint64_t *bar = c.bar(B_FULL + slot);
                 const uint32_t dst = smem_u32(c.base + L::kRing + slot * kSlotBytes);
-                mbar_arrive_expect_tx(bar, kSlotBytes);
-                if (ch < 2) {
-                    tma_load(dst, mk, bar, 64 * ch, head, k0);
-                } else if (kRope && ch == 2) {
-                    tma_load(dst, mr, bar, 0, 0, k0);
-                } else {
-                    const int keys = k0 + 64 * (ch - L::kChunks);
-                    tma_load(dst, mv, bar, 0, head, keys);
-                    tma_load(dst + kSlotBytes / 2, mv, bar, 64, head, keys);
-                    if (ch == L::kStepSlots - 1 && tail_step(s, j)) mbar_arrive(c.bar(B_TAIL + (it - 1) % L::kSlots));
+                if (elected()) {
+                    mbar_arrive_expect_tx(bar, kSlotBytes);
+                    if (ch < 2) {
+                        tma_load(dst, mk, bar, 64 * ch, head, k0);
+                    } else if (kRope && ch == 2) {
+                        tma_load(dst, mr, bar, 0, 0, k0);
+                    } else {
+                        const int keys = k0 + 64 * (ch - L::kChunks);
+                        tma_load(dst, mv, bar, 0, head, keys);
+                        tma_load(dst + kSlotBytes / 2, mv, bar, 64, head, keys);
+                        if (ch == L::kStepSlots - 1 && tail_step(s, j)) mbar_arrive(c.bar(B_TAIL + (it - 1) % L::kSlots));
+                    }
                 }
+                __syncwarp();
             }
         }
     }
@@ -214,6 +233,7 @@ __device__ void mma_role(const PrefillParams &p, const Ctx &c, uint32_t tmem) {
     int head;
     uint32_t it = 0, qn[kPreTiles] = {0, 0}, steps[kPreTiles] = {0, 0}, zeroed = 0;  // zeroed: a bit per slot, the phase of its B_ZERO
     const uint32_t ring = smem_u32(c.base + L::kRing), qbase = smem_u32(c.base);
+    auto wait = [&](int bar, uint32_t parity) { return __all_sync(0xffffffffu, c.wait(bar, parity)) != 0; };
     while (walk.next(p, s, head)) {
         const Tile tile[kPreTiles] = {Tile(p, s, 0), Tile(p, s, 1)};
         const int n = max(tile[0].steps, tile[1].steps);
@@ -230,14 +250,20 @@ __device__ void mma_role(const PrefillParams &p, const Ctx &c, uint32_t tmem) {
 #pragma unroll
             for (int ch = 0; ch < L::kChunks; ++ch) {
                 const uint32_t slot = (k + ch) % L::kSlots;
-                if (first_user(t, j) && !c.wait(B_FULL + slot, ((k + ch) / L::kSlots) & 1)) return false;
+                if (first_user(t, j) && !wait(B_FULL + slot, ((k + ch) / L::kSlots) & 1)) return false;
                 const uint64_t ad = desc_sw128(qbase + (t * L::kChunks + ch) * kSlotBytes, 16, 1024), bd = desc_sw128(ring + slot * kSlotBytes, 16, 1024);
+                if (elected()) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) mma_ss(tmem + t * 128, ad + 2 * i, bd + 2 * i, idesc, ch + i > 0);  // +32 B along the dims
+                    for (int i = 0; i < 4; ++i) mma_ss(tmem + t * 128, ad + 2 * i, bd + 2 * i, idesc, ch + i > 0);  // +32 B along the dims
+                }
+                __syncwarp();
             }
-            mma_commit(c.bar(B_S + t));
-            if (j == tile[t].steps - 1) mma_commit(c.bar(B_QEMPTY + t));
-            if (last_user(t, j)) free_slots(k, L::kChunks);
+            if (elected()) {
+                mma_commit(c.bar(B_S + t));
+                if (j == tile[t].steps - 1) mma_commit(c.bar(B_QEMPTY + t));
+                if (last_user(t, j)) free_slots(k, L::kChunks);
+            }
+            __syncwarp();
             return true;
         };
         // O_t (+)= P_t V(j)
@@ -246,34 +272,39 @@ __device__ void mma_role(const PrefillParams &p, const Ctx &c, uint32_t tmem) {
             const int base = (s.step0 + j) * kPreTile, parts = keys16(tile[t].seen - base) / 16;
             if (first_user(t, j)) {
                 for (int i = 0; i < 2; ++i)
-                    if (!c.wait(B_FULL + (v + i) % L::kSlots, ((v + i) / L::kSlots) & 1)) return false;
+                    if (!wait(B_FULL + (v + i) % L::kSlots, ((v + i) / L::kSlots) & 1)) return false;
                 if (tail_step(s, j)) {
                     const uint32_t slot = v % L::kSlots;
-                    if (!c.wait(B_ZERO + slot, (zeroed >> slot) & 1)) return false;
+                    if (!wait(B_ZERO + slot, (zeroed >> slot) & 1)) return false;
                     zeroed ^= 1u << slot;
                 }
             }
-            for (int i = 0; i < parts; ++i) {
-                const uint32_t slot = (v + i / 4) % L::kSlots;
-                const uint64_t bd = desc_sw128(ring + slot * kSlotBytes + (i & 3) * 2048, kSlotBytes / 2, 1024);
-                mma_ts(tmem + 256 + t * 128, tmem + t * 128 + 8 * i, bd, kPvDesc, j + i > 0);
+            if (elected()) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint64_t bd = desc_sw128(ring + (v + h) % L::kSlots * kSlotBytes, kSlotBytes / 2, 1024);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)  // 16 keys: 2048 B
+                        if (4 * h + i < parts) mma_ts(tmem + 256 + t * 128, tmem + t * 128 + 8 * (4 * h + i), bd + 128 * i, kPvDesc, j + h + i > 0);
+                }
+                mma_commit(c.bar(B_PV + t));
+                if (last_user(t, j)) free_slots(v, 2);
             }
-            mma_commit(c.bar(B_PV + t));
-            if (last_user(t, j)) free_slots(v, 2);
+            __syncwarp();
             return true;
         };
 #pragma unroll
         for (int t = 0; t < kPreTiles; ++t) {
             if (tile[t].steps == 0) continue;
-            if (!c.wait(B_QFULL + t, qn[t] & 1)) return;
+            if (!wait(B_QFULL + t, qn[t] & 1)) return;
             if (!scores(t, 0)) return;
         }
         for (int j = 0; j < n; ++j)
 #pragma unroll
             for (int t = 0; t < kPreTiles; ++t) {
                 if (j >= tile[t].steps) continue;
-                if (j == 0 && !c.wait(B_OFREE + t, (qn[t] & 1) ^ 1)) return;  // O of the segment before is read
-                if (!c.wait(B_P + t, (steps[t] + j) & 1)) return;
+                if (j == 0 && !wait(B_OFREE + t, (qn[t] & 1) ^ 1)) return;  // O of the segment before is read
+                if (!wait(B_P + t, (steps[t] + j) & 1)) return;
                 tc_fence_after();
                 if (!values(t, j)) return;
                 if (j + 1 < tile[t].steps && !scores(t, j + 1)) return;
@@ -471,7 +502,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     c.base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     c.bars = reinterpret_cast<uint64_t *>(c.base + L::kBars);
     c.status = p.status;
-    const int warp = threadIdx.x >> 5;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
     if (threadIdx.x == 0) {
         for (int i = 0; i < L::kSlots; ++i) {
             mbar_init(c.bar(B_FULL + i), 1);
@@ -511,15 +542,12 @@ prefill_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == kLoadWarp) {
-            if (elect_one_lane()) load_role<kRope>(p, c, &mq, &mk, &mr, &mv);
-            __syncwarp();
+            load_role<kRope>(p, c, &mq, &mk, &mr, &mv);
         } else if (warp == kMmaWarp) {
-            if (elect_one_lane()) {
-                mma_role<kRope>(p, c, tmem);
-                mma_commit(c.bar(B_FINAL));  // every MMA of this thread is done before tensor memory is released
-                c.wait(B_FINAL, 0);
-            }
+            mma_role<kRope>(p, c, tmem);
+            if (elected()) mma_commit(c.bar(B_FINAL));  // every MMA of this thread is done before tensor memory is released
             __syncwarp();
+            c.wait(B_FINAL, 0);
         } else if (warp == kZeroWarp) {
             zero_role<kRope>(p, c);
         }
