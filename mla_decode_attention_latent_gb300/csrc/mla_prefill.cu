@@ -10,15 +10,16 @@
 // key head), walking steps of 128 keys together, so that every key and value
 // that lands in shared memory serves 256 rows.  Tensor memory is full: S_A, S_B, O_A,
 // O_B take 128 of the 512 columns each, and a tile's weights P overwrite its scores
-// as bf16 operands.  The roles, of 12 warps (the last idles):
+// as bf16 operands.  The roles, of 12 warps:
 //   0-3, 4-7  rows of A and of B, a thread per row: S from tensor memory, mask, running
 //             maximum and sum in fp32, P back; O read and written at the end.  O is only
 //             rescaled when a maximum grows by more than 2^8 over the one in use
-//   8         loads: Q of a segment, then chunks of 16 KB through one ring (a step's
-//             keys are 64-dim chunks of 128 keys, its values 128-dim chunks of 64)
-//   9         MMAs, in the order PV_A(j) QK_A(j+1) PV_B(j) QK_B(j+1): while the rows of one
-//             tile take their maximum and exponents, the other tile's products run
-//   10        zeroes the value rows behind a sequence's last key, which belong to
+//   8         loads: Q of a segment, then keys and values of each step in turn, as chunks
+//             of 16 KB through one ring (64 dims of 128 keys, 128 dims of 64 values)
+//   9, 10     MMAs of A and of B, in turns of PV(j) QK(j+1): while the rows of one tile take
+//             their maximum and exponents, the other tile's products run.  PV starts on
+//             the first half of the weights
+//   11        zeroes the value rows behind a sequence's last key, which belong to
 //             another sequence (weight 0 times an infinity would be NaN)
 // Products stop at multiples of 16 keys behind the last one that a tile sees.
 //
@@ -44,7 +45,7 @@ constexpr int kThreads = 384;
 // gets some of the others' (256 x 200 + 128 x 104 = 384 x 168)
 constexpr int kRowRegs = 200, kOtherRegs = 104;
 static_assert(256 * kRowRegs + 128 * kOtherRegs <= kThreads * 168, "a split of what the CTA was launched with");
-constexpr int kLoadWarp = 8, kMmaWarp = 9, kZeroWarp = 10;
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kZeroWarp = 11;  // MMAs: a warp per tile
 constexpr int kRows = kPreTiles * kPreTile;
 constexpr uint32_t kSlotBytes = 16384;
 constexpr uint32_t kTmemCols = 512;
@@ -55,18 +56,22 @@ template <bool kRope>
 struct Layout {
     static constexpr int kChunks = kRope ? 3 : 2;         // 64-dim chunks of a query or key
     static constexpr int kStepSlots = kChunks + 2;        // ring slots of a step: keys, then values
-    static constexpr int kSlots = kRope ? 8 : 10;
+    static constexpr int kSlots = kRope ? 8 : 10;         // 1.6 or 2.5 steps
     static constexpr uint32_t kRing = kPreTiles * kChunks * kSlotBytes;
     static constexpr uint32_t kBars = kRing + kSlots * kSlotBytes;
     static constexpr uint32_t kBytes = kBars + 512 + 1024;  // 1024: room to align the base
 };
 static_assert(Layout<true>::kBytes <= 232448 && Layout<false>::kBytes <= 232448, "shared memory of a CTA");
 
-// barriers
-constexpr int kMaxSlots = 10;
-enum { B_FULL = 0, B_EMPTY = B_FULL + kMaxSlots, B_QFULL = B_EMPTY + kMaxSlots, B_QEMPTY = B_QFULL + 2, B_S = B_QEMPTY + 2, B_P = B_S + 2,
-       B_PV = B_P + 2, B_OFREE = B_PV + 2, B_TAIL = B_OFREE + 2, B_ZERO = B_TAIL + kMaxSlots, B_FINAL = B_ZERO + kMaxSlots, kNumBars };
+// Barriers.  The keys of a step are one load group, its values the next: group g has
+// the barriers g % kGroups, whose next use, g + kGroups, is loaded into slots of g, so
+// after g is used up.
+constexpr int kGroups = 6;
+enum { B_FULL = 0, B_EMPTY = B_FULL + kGroups, B_TAIL = B_EMPTY + kGroups, B_ZERO = B_TAIL + kGroups, B_QFULL = B_ZERO + kGroups,
+       B_QEMPTY = B_QFULL + 2, B_S = B_QEMPTY + 2, B_P = B_S + 2, B_PV = B_P + 4, B_OFREE = B_PV + 2, B_TURN = B_OFREE + 2, B_FINAL = B_TURN + 2, kNumBars = B_FINAL + 2 };
 static_assert(kNumBars * 8 <= 512, "room for the barriers");
+static_assert(Layout<true>::kSlots < kGroups / 2 * Layout<true>::kStepSlots && Layout<false>::kSlots < kGroups / 2 * Layout<false>::kStepSlots,
+              "the ring holds fewer than kGroups groups");
 
 struct Ctx {
     char *base;
@@ -120,10 +125,9 @@ struct Walk {
 
 // Whether step j of a segment has value rows behind the sequence's last key that a
 // product reaches: zeroed, in the slots of the step's values.  The load role says when
-// such a step has been issued (B_TAIL of the values' first slot: only then are the
-// slots' barriers in the phase that the zeroing waits for), the zero role when it is
-// done (B_ZERO).  A slot's next use comes after both, so each barrier is at most one
-// phase ahead of who waits for it.
+// such a group has been issued (B_TAIL: only then is the group's B_FULL in the phase
+// that the zeroing waits for), the zero role when it is done (B_ZERO).  The group's
+// barriers are used again after both, so none is more than a phase ahead of who waits.
 __device__ __forceinline__ bool tail_step(const PreSegment &s, int j) {
     return s.keys - (s.step0 + j) * kPreTile < kPreTile && s.keys % 16 != 0;
 }
@@ -163,57 +167,80 @@ __device__ void load_role(const PrefillParams &p, const Ctx &c, const CUtensorMa
     Walk walk(p);
     PreSegment s;
     int head;
-    uint32_t it = 0, qn[kPreTiles] = {0, 0};
+    uint32_t slot = 0, group = 0, freed = 0, held = 0;  // groups issued and given back, slots that the others hold
+    uint32_t qn[kPreTiles] = {0, 0};
     const uint32_t q_bytes = (uint32_t)(pre_tile_tokens(p.group) * p.group) * 128u;
+    auto wait = [&](int bar, uint32_t parity) { return __all_sync(0xffffffffu, c.wait(bar, parity)) != 0; };
+    // room for a group of n slots: groups come back in order, keys and values in turn
+    auto room = [&](uint32_t n) {
+        while (held + n > L::kSlots) {
+            if (!wait(B_EMPTY + freed % kGroups, (freed / kGroups) & 1)) return false;
+            held -= freed & 1 ? 2 : L::kChunks;
+            ++freed;
+        }
+        held += n;
+        return true;
+    };
+    auto next_slot = [&] {
+        const uint32_t at = smem_u32(c.base + L::kRing) + slot * kSlotBytes;
+        slot = slot + 1 == L::kSlots ? 0 : slot + 1;
+        return at;
+    };
     bool ok = true;
     while (ok && walk.next(p, s, head)) {
         const Tile a(p, s, 0), b(p, s, 1);
         const int n = max(a.steps, b.steps);
-        for (int j = -1; ok && j < n; ++j) {
-            if (j < 0) {
-                // Q of the tiles that walk, each before the first keys are needed
+        // Q of the tiles that walk
 #pragma unroll
-                for (int t = 0; t < kPreTiles; ++t) {
-                    if (!ok || (t ? b.steps : a.steps) == 0) continue;
-                    ok = __all_sync(0xffffffffu, c.wait(B_QEMPTY + t, (qn[t] & 1) ^ 1));
-                    if (!ok) continue;
-                    ++qn[t];
-                    if (elected()) {
-                        mbar_arrive_expect_tx(c.bar(B_QFULL + t), L::kChunks * q_bytes);
-                        for (int ch = 0; ch < L::kChunks; ++ch)
-                            tma_load(smem_u32(c.base + (t * L::kChunks + ch) * kSlotBytes), mq, c.bar(B_QFULL + t), 64 * ch, head * p.group,
-                                     s.q0 + t * pre_tile_tokens(p.group));
-                    }
-                    __syncwarp();
-                }
-                continue;
+        for (int t = 0; t < kPreTiles; ++t) {
+            if (!ok || (t ? b.steps : a.steps) == 0) continue;
+            ok = wait(B_QEMPTY + t, (qn[t] & 1) ^ 1);
+            if (!ok) continue;
+            ++qn[t];
+            if (elected()) {
+                mbar_arrive_expect_tx(c.bar(B_QFULL + t), L::kChunks * q_bytes);
+                for (int ch = 0; ch < L::kChunks; ++ch)
+                    tma_load(smem_u32(c.base + (t * L::kChunks + ch) * kSlotBytes), mq, c.bar(B_QFULL + t), 64 * ch, head * p.group,
+                             s.q0 + t * pre_tile_tokens(p.group));
             }
+            __syncwarp();
+        }
+        for (int j = 0; ok && j < n; ++j) {
             const int k0 = s.k0 + (s.step0 + j) * kPreTile;
-            for (int ch = 0; ch < L::kStepSlots && ok; ++ch, ++it) {
-                const int slot = it % L::kSlots;
-                ok = __all_sync(0xffffffffu, c.wait(B_EMPTY + slot, ((it / L::kSlots) & 1) ^ 1));
-                if (!ok) break;
-                uint64_t *bar = c.bar(B_FULL + slot);
-                const uint32_t dst = smem_u32(c.base + L::kRing + slot * kSlotBytes);
+            if (!(ok = room(L::kChunks))) break;
+            uint64_t *bar = c.bar(B_FULL + group % kGroups);
+            ++group;
+            if (elected()) mbar_arrive_expect_tx(bar, L::kChunks * kSlotBytes);
+            __syncwarp();
+#pragma unroll
+            for (int ch = 0; ch < L::kChunks; ++ch) {
+                const uint32_t dst = next_slot();
                 if (elected()) {
-                    mbar_arrive_expect_tx(bar, kSlotBytes);
-                    if (ch < 2) {
-                        tma_load(dst, mk, bar, 64 * ch, head, k0);
-                    } else if (kRope && ch == 2) {
-                        tma_load(dst, mr, bar, 0, 0, k0);
-                    } else {
-                        const int keys = k0 + 64 * (ch - L::kChunks);
-                        tma_load(dst, mv, bar, 0, head, keys);
-                        tma_load(dst + kSlotBytes / 2, mv, bar, 64, head, keys);
-                        if (ch == L::kStepSlots - 1 && tail_step(s, j)) mbar_arrive(c.bar(B_TAIL + (it - 1) % L::kSlots));
-                    }
+                    if (ch < 2) tma_load(dst, mk, bar, 64 * ch, head, k0);
+                    else tma_load(dst, mr, bar, 0, 0, k0);
+                }
+                __syncwarp();
+            }
+            if (!(ok = room(2))) break;
+            bar = c.bar(B_FULL + group % kGroups);
+            const uint32_t tail = group % kGroups;
+            ++group;
+            if (elected()) mbar_arrive_expect_tx(bar, 2 * kSlotBytes);
+            __syncwarp();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t dst = next_slot();
+                if (elected()) {
+                    tma_load(dst, mv, bar, 0, head, k0 + 64 * h);
+                    tma_load(dst + kSlotBytes / 2, mv, bar, 64, head, k0 + 64 * h);
+                    if (h == 1 && tail_step(s, j)) mbar_arrive(c.bar(B_TAIL + tail));
                 }
                 __syncwarp();
             }
         }
     }
     // nothing may be in flight when the CTA ends (after a wait that gave up, too)
-    for (uint32_t i = it > L::kSlots ? it - L::kSlots : 0; i < it; ++i) c.wait(B_FULL + i % L::kSlots, (i / L::kSlots) & 1);
+    for (uint32_t g = freed; g < group; ++g) c.wait(B_FULL + g % kGroups, (g / kGroups) & 1);
 #pragma unroll
     for (int t = 0; t < kPreTiles; ++t)
         if (qn[t]) c.wait(B_QFULL + t, (qn[t] - 1) & 1);
@@ -224,96 +251,108 @@ __device__ void load_role(const PrefillParams &p, const Ctx &c, const CUtensorMa
 __device__ __forceinline__ uint32_t idesc_keys(int keys) { return idesc_bf16(kPreTile, 0, false, false) | ((uint32_t)(keys >> 3) << 17); }
 __device__ __forceinline__ int keys16(int keys) { return keys >= kPreTile ? kPreTile : (keys + 15) & ~15; }
 
+// The MMAs of tile t.  An MMA holds its issuer for about its own duration, so a wait
+// of one issuer would idle the pipe: the two tiles have a warp each, and one waits
+// while the other issues.  Left alone they fall into step (both tiles' products at
+// once, then both tiles' exponents), so they take turns: a turn is PV(j) QK(j+1), and is
+// handed over a few MMAs before its end.
 template <bool kRope>
-__device__ void mma_role(const PrefillParams &p, const Ctx &c, uint32_t tmem) {
+__device__ void mma_role(const PrefillParams &p, const Ctx &c, uint32_t tmem, int t) {
     using L = Layout<kRope>;
     constexpr uint32_t kPvDesc = idesc_bf16(kPreTile, kPreHead, false, true);
     Walk walk(p);
     PreSegment s;
     int head;
-    uint32_t it = 0, qn[kPreTiles] = {0, 0}, steps[kPreTiles] = {0, 0}, zeroed = 0;  // zeroed: a bit per slot, the phase of its B_ZERO
-    const uint32_t ring = smem_u32(c.base + L::kRing), qbase = smem_u32(c.base);
+    uint32_t slot = 0, group = 0, qn = 0, done = 0, turn = 0;
+    uint32_t zeroed = 0;  // a bit per group barrier, the phase of its B_ZERO
+    const uint32_t ring = smem_u32(c.base + L::kRing);
+    const uint32_t s_col = tmem + t * 128, o_col = tmem + 256 + t * 128;
+    const uint64_t q_desc = desc_sw128(smem_u32(c.base) + t * L::kChunks * kSlotBytes, 16, 1024), k_desc = desc_sw128(ring, 16, 1024),
+                   v_desc = desc_sw128(ring, kSlotBytes / 2, 1024);
     auto wait = [&](int bar, uint32_t parity) { return __all_sync(0xffffffffu, c.wait(bar, parity)) != 0; };
+    auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+    auto after = [](uint32_t at, uint32_t n) { return at + n >= L::kSlots ? at + n - L::kSlots : at + n; };
     while (walk.next(p, s, head)) {
-        const Tile tile[kPreTiles] = {Tile(p, s, 0), Tile(p, s, 1)};
-        const int n = max(tile[0].steps, tile[1].steps);
-        if (n == 0) continue;
-        auto last_user = [&](int t, int j) { return t == 1 || tile[1].steps <= j; };  // of step j's keys or values
-        auto first_user = [&](int t, int j) { return t == 0 || tile[0].steps <= j; };
-        auto free_slots = [&](uint32_t first, int count) {
-            for (int i = 0; i < count; ++i) mma_commit(c.bar(B_EMPTY + (first + i) % L::kSlots));
-        };
-        // S_t = Q_t K(j)^T
-        auto scores = [&](int t, int j) {
-            const uint32_t k = it + j * L::kStepSlots;
-            const uint32_t idesc = idesc_keys(keys16(tile[t].seen - (s.step0 + j) * kPreTile));
+        const Tile mine(p, s, t), other(p, s, 1 - t);
+        const int steps = uniform(mine.steps), n = uniform(max(mine.steps, other.steps)), seen = uniform(mine.seen - s.step0 * kPreTile);
+        // S = Q K(j)^T, the keys (group g) at slot `at`; `hand_over`: the turn ends here
+        auto scores = [&](int j, uint32_t at, uint32_t g, bool hand_over) {
+            const uint32_t idesc = idesc_keys(keys16(seen - j * kPreTile));
+            uint64_t bd[L::kChunks];
 #pragma unroll
-            for (int ch = 0; ch < L::kChunks; ++ch) {
-                const uint32_t slot = (k + ch) % L::kSlots;
-                if (first_user(t, j) && !wait(B_FULL + slot, ((k + ch) / L::kSlots) & 1)) return false;
-                const uint64_t ad = desc_sw128(qbase + (t * L::kChunks + ch) * kSlotBytes, 16, 1024), bd = desc_sw128(ring + slot * kSlotBytes, 16, 1024);
-                if (elected()) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) mma_ss(tmem + t * 128, ad + 2 * i, bd + 2 * i, idesc, ch + i > 0);  // +32 B along the dims
-                }
-                __syncwarp();
-            }
+            for (int ch = 0; ch < L::kChunks; ++ch) bd[ch] = k_desc + after(at, ch) * (kSlotBytes / 16);
             if (elected()) {
+#pragma unroll
+                for (int ch = 0; ch < L::kChunks; ++ch) {
+                    if (ch == L::kChunks - 1 && hand_over) mbar_arrive(c.bar(B_TURN + 1 - t));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)  // 16 dims: 32 B
+                        mma_ss(s_col, q_desc + ch * (kSlotBytes / 16) + 2 * i, bd[ch] + 2 * i, idesc, ch + i > 0);
+                }
                 mma_commit(c.bar(B_S + t));
-                if (j == tile[t].steps - 1) mma_commit(c.bar(B_QEMPTY + t));
-                if (last_user(t, j)) free_slots(k, L::kChunks);
+                mma_commit(c.bar(B_EMPTY + g % kGroups));
+                if (j == steps - 1) mma_commit(c.bar(B_QEMPTY + t));
             }
+            __syncwarp();
+        };
+        // a group that the other tile alone uses (its keys lie behind this tile's rows)
+        auto pass = [&](uint32_t g) {
+            if (!wait(B_FULL + g % kGroups, (g / kGroups) & 1)) return false;
+            if (elected()) mbar_arrive(c.bar(B_EMPTY + g % kGroups));
             __syncwarp();
             return true;
         };
-        // O_t (+)= P_t V(j)
-        auto values = [&](int t, int j) {
-            const uint32_t v = it + j * L::kStepSlots + L::kChunks;
-            const int base = (s.step0 + j) * kPreTile, parts = keys16(tile[t].seen - base) / 16;
-            if (first_user(t, j)) {
-                for (int i = 0; i < 2; ++i)
-                    if (!wait(B_FULL + (v + i) % L::kSlots, ((v + i) / L::kSlots) & 1)) return false;
-                if (tail_step(s, j)) {
-                    const uint32_t slot = v % L::kSlots;
-                    if (!wait(B_ZERO + slot, (zeroed >> slot) & 1)) return false;
-                    zeroed ^= 1u << slot;
-                }
-            }
-            if (elected()) {
+        if (n == 0) continue;
+        if (steps > 0) {
+            if (!wait(B_QFULL + t, qn & 1) || !wait(B_FULL + group % kGroups, (group / kGroups) & 1)) return;
+            ++qn;
+            scores(0, slot, group, false);
+        } else if (!pass(group)) {
+            return;
+        }
+        ++group;
+        slot = after(slot, L::kChunks);
+        for (int j = 0; j < n; ++j, ++turn) {
+            // the values of step j, then the keys of step j + 1
+            const uint32_t vg = group % kGroups, kg = group + 1, k_at = after(slot, 2);
+            const bool tail = tail_step(s, j), more = j + 1 < n, scores_too = j + 1 < steps;
+            if (j < steps) {
+                const uint64_t bd[2] = {v_desc + slot * (kSlotBytes / 16), v_desc + after(slot, 1) * (kSlotBytes / 16)};
+                const int parts = keys16(seen - j * kPreTile) / 16;
+                if (!wait(B_FULL + vg, (group / kGroups) & 1)) return;
+                if (tail && !wait(B_ZERO + vg, (zeroed >> vg) & 1)) return;
+                if (j == 0 && !wait(B_OFREE + t, qn & 1)) return;  // O of the segment before is read
+                if (scores_too && !wait(B_FULL + kg % kGroups, (kg / kGroups) & 1)) return;
+                if (!wait(B_P + 2 * t, done & 1)) return;
+                if (!wait(B_TURN + t, t == 0 ? (turn & 1) ^ 1 : turn & 1)) return;
+                // O (+)= P V(j), the weights in two halves
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const uint64_t bd = desc_sw128(ring + (v + h) % L::kSlots * kSlotBytes, kSlotBytes / 2, 1024);
+                    if (h && !wait(B_P + 2 * t + 1, done & 1)) return;
+                    tc_fence_after();
+                    if (elected()) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)  // 16 keys: 2048 B
-                        if (4 * h + i < parts) mma_ts(tmem + 256 + t * 128, tmem + t * 128 + 8 * (4 * h + i), bd + 128 * i, kPvDesc, j + h + i > 0);
+                        for (int i = 0; i < 4; ++i)  // 16 keys: 2048 B
+                            if (4 * h + i < parts) mma_ts(o_col, s_col + 8 * (4 * h + i), bd[h] + 128 * i, kPvDesc, j + h + i > 0);
+                        if (h == 1) {
+                            mma_commit(c.bar(B_PV + t));
+                            mma_commit(c.bar(B_EMPTY + vg));
+                            if (!scores_too) mbar_arrive(c.bar(B_TURN + 1 - t));
+                        }
+                    }
+                    __syncwarp();
                 }
-                mma_commit(c.bar(B_PV + t));
-                if (last_user(t, j)) free_slots(v, 2);
+                ++done;
+                if (scores_too) scores(j + 1, k_at, kg, true);
+            } else {
+                if (!pass(group) || !wait(B_TURN + t, t == 0 ? (turn & 1) ^ 1 : turn & 1)) return;
+                if (elected()) mbar_arrive(c.bar(B_TURN + 1 - t));
+                __syncwarp();
             }
-            __syncwarp();
-            return true;
-        };
-#pragma unroll
-        for (int t = 0; t < kPreTiles; ++t) {
-            if (tile[t].steps == 0) continue;
-            if (!wait(B_QFULL + t, qn[t] & 1)) return;
-            if (!scores(t, 0)) return;
-        }
-        for (int j = 0; j < n; ++j)
-#pragma unroll
-            for (int t = 0; t < kPreTiles; ++t) {
-                if (j >= tile[t].steps) continue;
-                if (j == 0 && !wait(B_OFREE + t, (qn[t] & 1) ^ 1)) return;  // O of the segment before is read
-                if (!wait(B_P + t, (steps[t] + j) & 1)) return;
-                tc_fence_after();
-                if (!values(t, j)) return;
-                if (j + 1 < tile[t].steps && !scores(t, j + 1)) return;
-            }
-        it += n * L::kStepSlots;
-#pragma unroll
-        for (int t = 0; t < kPreTiles; ++t) {
-            if (tile[t].steps) ++qn[t];
-            steps[t] += tile[t].steps;
+            if (tail) zeroed ^= 1u << vg;
+            if (more && !scores_too && !pass(kg)) return;
+            group += more ? 2 : 1;
+            slot = more ? after(k_at, L::kChunks) : k_at;
         }
     }
 }
@@ -325,29 +364,31 @@ __device__ void zero_role(const PrefillParams &p, const Ctx &c) {
     Walk walk(p);
     PreSegment s;
     int head;
-    uint32_t it = 0, tails = 0;  // tails: a bit per slot, the phase of its B_TAIL
+    uint32_t slot = 0, group = 0, tails = 0;  // tails: a bit per group barrier, the phase of its B_TAIL
     const int lane = threadIdx.x & 31;
     while (walk.next(p, s, head)) {
         const Tile a(p, s, 0), b(p, s, 1);
         const int n = max(a.steps, b.steps);
-        if (n > 0 && tail_step(s, n - 1)) {
+        if (n == 0) continue;
+        if (tail_step(s, n - 1)) {
             const int valid = s.keys - (s.step0 + n - 1) * kPreTile;  // keys of the last step
-            const uint32_t v = it + (n - 1) * L::kStepSlots + L::kChunks, first = v % L::kSlots;
-            if (!__all_sync(0xffffffffu, c.wait(B_TAIL + first, (tails >> first) & 1))) return;
-            tails ^= 1u << first;
-            for (int i = 0; i < 2; ++i)
-                if (!__all_sync(0xffffffffu, c.wait(B_FULL + (v + i) % L::kSlots, ((v + i) / L::kSlots) & 1))) return;
+            const uint32_t last = group + 2 * n - 1, g = last % kGroups;
+            const uint32_t first = (uint32_t)((slot + (uint64_t)n * L::kStepSlots - 2) % L::kSlots);
+            if (!__all_sync(0xffffffffu, c.wait(B_TAIL + g, (tails >> g) & 1))) return;
+            tails ^= 1u << g;
+            if (!__all_sync(0xffffffffu, c.wait(B_FULL + g, (last / kGroups) & 1))) return;
             // rows valid .. of the 16 that the products reach, all 256 bytes of each
             for (int i = lane; i < (16 - valid % 16) * 16; i += 32) {
                 const int row = valid + i / 16, piece = i % 16;
-                const uint32_t slot = (v + row / 64) % L::kSlots;
-                sts128(smem_u32(c.base + L::kRing + slot * kSlotBytes) + (piece / 8) * (kSlotBytes / 2) + (row % 64) * 128 + (piece % 8) * 16, 0, 0, 0, 0);
+                const uint32_t at = (first + row / 64) % L::kSlots;
+                sts128(smem_u32(c.base + L::kRing + at * kSlotBytes) + (piece / 8) * (kSlotBytes / 2) + (row % 64) * 128 + (piece % 8) * 16, 0, 0, 0, 0);
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(c.bar(B_ZERO + first));
+            if (lane == 0) mbar_arrive(c.bar(B_ZERO + g));
         }
-        it += n * L::kStepSlots;
+        group += 2 * n;
+        slot = (uint32_t)((slot + (uint64_t)n * L::kStepSlots) % L::kSlots);
     }
 }
 
@@ -391,13 +432,17 @@ __device__ void row_role(const PrefillParams &p, const Ctx &c, uint32_t tmem, in
 #pragma unroll
                 for (int i = 0; i < 128; ++i) x[i] = i < left ? x[i] : -INFINITY;
             }
-            float mx[4] = {x[0], x[1], x[2], x[3]};
+            float mx[8];
 #pragma unroll
-            for (int i = 4; i < 124; i += 8) {
+            for (int k = 0; k < 8; ++k) mx[k] = x[k];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) mx[k] = max3f(mx[k], x[i + 2 * k], x[i + 2 * k + 1]);
+            for (int i = 8; i < 120; i += 16) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) mx[k] = max3f(mx[k], x[i + 2 * k], x[i + 2 * k + 1]);
             }
-            float top = max3f(max3f(mx[0], mx[1], mx[2]), max3f(mx[3], x[124], x[125]), fmaxf(x[126], x[127]));
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mx[k] = max3f(mx[k], mx[k + 4], fmaxf(x[120 + 2 * k], x[121 + 2 * k]));
+            const float top = fmaxf(max3f(mx[0], mx[1], mx[2]), mx[3]);
             const bool grow = top > m + lazy;  // (m = -inf: the first score of the row)
             const float m_new = grow ? top : m;
             if (j > 0 && __any_sync(0xffffffffu, grow)) {
@@ -434,15 +479,13 @@ __device__ void row_role(const PrefillParams &p, const Ctx &c, uint32_t tmem, in
                     w[i] = pack_bf16(a, b);
                 }
                 tmem_st32(s_col + 32 * h, w);
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(c.bar(B_P + 2 * t + h));
             }
-            {
-                float a, b;
-                f2_unpack(f2_add(sum[0], sum[1]), a, b);
-                l += a + b;
-            }
-            tmem_wait_st();
-            tc_fence_before();
-            mbar_arrive(c.bar(B_P + t));
+            float a, b;
+            f2_unpack(f2_add(sum[0], sum[1]), a, b);
+            l += a + b;
         }
         // epilogue: o = O / l, lse
         float lse = l == 0.f ? -INFINITY : m * p.scale + logf(l);
@@ -504,9 +547,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     c.status = p.status;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
     if (threadIdx.x == 0) {
-        for (int i = 0; i < L::kSlots; ++i) {
+        for (int i = 0; i < kGroups; ++i) {
             mbar_init(c.bar(B_FULL + i), 1);
-            mbar_init(c.bar(B_EMPTY + i), 1);
+            mbar_init(c.bar(B_EMPTY + i), kPreTiles);
             mbar_init(c.bar(B_TAIL + i), 1);
             mbar_init(c.bar(B_ZERO + i), 1);
         }
@@ -514,11 +557,13 @@ prefill_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             mbar_init(c.bar(B_QFULL + t), 1);
             mbar_init(c.bar(B_QEMPTY + t), 1);
             mbar_init(c.bar(B_S + t), 1);
-            mbar_init(c.bar(B_P + t), kPreTile);
+            mbar_init(c.bar(B_P + 2 * t), kPreTile);
+            mbar_init(c.bar(B_P + 2 * t + 1), kPreTile);
             mbar_init(c.bar(B_PV + t), 1);
             mbar_init(c.bar(B_OFREE + t), kPreTile);
+            mbar_init(c.bar(B_TURN + t), 1);
+            mbar_init(c.bar(B_FINAL + t), 1);
         }
-        mbar_init(c.bar(B_FINAL), 1);
         fence_mbar_init();
     }
     if (warp == kLoadWarp && elect_one_lane()) {
@@ -534,7 +579,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = s_tmem;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
     griddep_wait();
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRowRegs));
@@ -543,12 +588,13 @@ prefill_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == kLoadWarp) {
             load_role<kRope>(p, c, &mq, &mk, &mr, &mv);
-        } else if (warp == kMmaWarp) {
-            mma_role<kRope>(p, c, tmem);
-            if (elected()) mma_commit(c.bar(B_FINAL));  // every MMA of this thread is done before tensor memory is released
+        } else if (warp < kZeroWarp) {
+            const int t = warp - kMmaWarp;
+            mma_role<kRope>(p, c, tmem, t);
+            if (elected()) mma_commit(c.bar(B_FINAL + t));  // every MMA of this thread is done before tensor memory is released
             __syncwarp();
-            c.wait(B_FINAL, 0);
-        } else if (warp == kZeroWarp) {
+            c.wait(B_FINAL + t, 0);
+        } else {
             zero_role<kRope>(p, c);
         }
     }
