@@ -11,9 +11,8 @@
 // that lands in shared memory serves 256 rows.  Tensor memory is full: S_A, S_B, O_A,
 // O_B take 128 of the 512 columns each, and a tile's weights P overwrite its scores
 // as bf16 operands.  The roles, of 12 warps:
-//   0-3, 4-7  rows of A and of B, a thread per row: S from tensor memory, mask, running
-//             maximum and sum in fp32, P back; O read and written at the end.  O is only
-//             rescaled when a maximum grows by more than 2^8 over the one in use
+//   0-3, 4-7  rows of A and of B, a thread per row: S from tensor memory, mask, weights and
+//             their sum in fp32, P back in two halves; O read and written at the end
 //   8         loads: Q of a segment, then keys and values of each step in turn, as chunks
 //             of 16 KB through one ring (64 dims of 128 keys, 128 dims of 64 values)
 //   9, 10     MMAs of A and of B, in turns of PV(j) QK(j+1): while the rows of one tile take
@@ -49,7 +48,7 @@ constexpr int kLoadWarp = 8, kMmaWarp = 9, kZeroWarp = 11;  // MMAs: a warp per 
 constexpr int kRows = kPreTiles * kPreTile;
 constexpr uint32_t kSlotBytes = 16384;
 constexpr uint32_t kTmemCols = 512;
-constexpr float kLazy = 8.f;  // log2: how far a maximum may pass the one in use
+constexpr float kMostWeight = 0x1p20f;  // that a row's 64 weights may add up to before their reference is raised
 
 // shared memory: Q of both tiles, the ring, barriers
 template <bool kRope>
@@ -68,7 +67,7 @@ static_assert(Layout<true>::kBytes <= 232448 && Layout<false>::kBytes <= 232448,
 // after g is used up.
 constexpr int kGroups = 6;
 enum { B_FULL = 0, B_EMPTY = B_FULL + kGroups, B_TAIL = B_EMPTY + kGroups, B_ZERO = B_TAIL + kGroups, B_QFULL = B_ZERO + kGroups,
-       B_QEMPTY = B_QFULL + 2, B_S = B_QEMPTY + 2, B_P = B_S + 2, B_PV = B_P + 4, B_OFREE = B_PV + 2, B_TURN = B_OFREE + 2, B_FINAL = B_TURN + 2, kNumBars = B_FINAL + 2 };
+       B_QEMPTY = B_QFULL + 2, B_S = B_QEMPTY + 2, B_P = B_S + 2, B_PV0 = B_P + 4, B_PV = B_PV0 + 2, B_OFREE = B_PV + 2, B_TURN = B_OFREE + 2, B_FINAL = B_TURN + 2, kNumBars = B_FINAL + 2 };
 static_assert(kNumBars * 8 <= 512, "room for the barriers");
 static_assert(Layout<true>::kSlots < kGroups / 2 * Layout<true>::kStepSlots && Layout<false>::kSlots < kGroups / 2 * Layout<false>::kStepSlots,
               "the ring holds fewer than kGroups groups");
@@ -322,7 +321,6 @@ __device__ void mma_role(const PrefillParams &p, const Ctx &c, uint32_t tmem, in
                 if (!wait(B_FULL + vg, (group / kGroups) & 1)) return;
                 if (tail && !wait(B_ZERO + vg, (zeroed >> vg) & 1)) return;
                 if (j == 0 && !wait(B_OFREE + t, qn & 1)) return;  // O of the segment before is read
-                if (scores_too && !wait(B_FULL + kg % kGroups, (kg / kGroups) & 1)) return;
                 if (!wait(B_P + 2 * t, done & 1)) return;
                 if (!wait(B_TURN + t, t == 0 ? (turn & 1) ^ 1 : turn & 1)) return;
                 // O (+)= P V(j), the weights in two halves
@@ -334,7 +332,9 @@ __device__ void mma_role(const PrefillParams &p, const Ctx &c, uint32_t tmem, in
 #pragma unroll
                         for (int i = 0; i < 4; ++i)  // 16 keys: 2048 B
                             if (4 * h + i < parts) mma_ts(o_col, s_col + 8 * (4 * h + i), bd[h] + 128 * i, kPvDesc, j + h + i > 0);
-                        if (h == 1) {
+                        if (h == 0) {
+                            mma_commit(c.bar(B_PV0 + t));
+                        } else {
                             mma_commit(c.bar(B_PV + t));
                             mma_commit(c.bar(B_EMPTY + vg));
                             if (!scores_too) mbar_arrive(c.bar(B_TURN + 1 - t));
@@ -343,7 +343,10 @@ __device__ void mma_role(const PrefillParams &p, const Ctx &c, uint32_t tmem, in
                     __syncwarp();
                 }
                 ++done;
-                if (scores_too) scores(j + 1, k_at, kg, true);
+                if (scores_too) {
+                    if (!wait(B_FULL + kg % kGroups, (kg / kGroups) & 1)) return;
+                    scores(j + 1, k_at, kg, true);
+                }
             } else {
                 if (!pass(group) || !wait(B_TURN + t, t == 0 ? (turn & 1) ^ 1 : turn & 1)) return;
                 if (elected()) mbar_arrive(c.bar(B_TURN + 1 - t));
@@ -399,12 +402,56 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
+// 32 columns of tensor memory that are complete behind arrived()
+__device__ __forceinline__ void arrived(uint32_t (&a)[32], uint32_t (&b)[32]) {
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(a[i]), "+r"(b[i]));  // no use moves before the wait
+}
+
+// A row's weights are exp2(score * scale - reference).  The reference need not be the
+// running maximum: bf16 and fp32 hold a weight as exactly at 2^20 as at 1.  So it is the
+// largest of the row's first 64 scores, and is raised only when 64 weights add up to
+// more than kMostWeight, which their sum tells without a maximum; then their
+// maximum becomes the reference, O and the sum are scaled, and they are computed again.
+__device__ __forceinline__ float largest(const uint32_t (&a)[32], const uint32_t (&b)[32]) {
+    float mx[4] = {__uint_as_float(a[0]), __uint_as_float(a[1]), __uint_as_float(b[0]), __uint_as_float(b[1])};
+#pragma unroll
+    for (int i = 2; i < 30; i += 4) {
+        mx[0] = max3f(mx[0], __uint_as_float(a[i]), __uint_as_float(a[i + 1]));
+        mx[1] = max3f(mx[1], __uint_as_float(a[i + 2]), __uint_as_float(a[i + 3]));
+        mx[2] = max3f(mx[2], __uint_as_float(b[i]), __uint_as_float(b[i + 1]));
+        mx[3] = max3f(mx[3], __uint_as_float(b[i + 2]), __uint_as_float(b[i + 3]));
+    }
+    const float c = max3f(mx[0], mx[1], fmaxf(__uint_as_float(a[30]), __uint_as_float(a[31])));
+    return max3f(c, max3f(mx[2], mx[3], __uint_as_float(b[30])), __uint_as_float(b[31]));
+}
+
+// 64 weights as bf16 pairs, and their sum
+__device__ __forceinline__ float weigh(const uint32_t (&a)[32], const uint32_t (&b)[32], float m, float scale_log2, uint32_t (&w)[32]) {
+    const float shift = m == -INFINITY ? 0.f : -m * scale_log2;
+    const uint64_t scale2 = f2_pack(scale_log2, scale_log2), shift2 = f2_pack(shift, shift);
+    uint64_t sum[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        const uint32_t *x = i < 16 ? a + 2 * i : b + 2 * (i - 16);
+        float lo, hi;
+        f2_unpack(f2_fma(f2_pack(__uint_as_float(x[0]), __uint_as_float(x[1])), scale2, shift2), lo, hi);
+        lo = exp2_fast(lo);
+        hi = exp2_fast(hi);
+        sum[i & 1] = f2_add(sum[i & 1], f2_pack(lo, hi));
+        w[i] = pack_bf16(lo, hi);
+    }
+    float lo, hi;
+    f2_unpack(f2_add(sum[0], sum[1]), lo, hi);
+    return lo + hi;
+}
+
 __device__ void row_role(const PrefillParams &p, const Ctx &c, uint32_t tmem, int t) {
     const int warp = threadIdx.x >> 5, r = threadIdx.x & (kPreTile - 1);
     const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t s_col = tmem + lane_base + t * 128, o_col = tmem + lane_base + 256 + t * 128;
     const int per = pre_tile_tokens(p.group), in_tile = r / p.group, hh = r - in_tile * p.group;
-    const float lazy = kLazy / p.scale_log2;  // in units of the raw scores
     Walk walk(p);
     PreSegment s;
     int head;
@@ -414,78 +461,61 @@ __device__ void row_role(const PrefillParams &p, const Ctx &c, uint32_t tmem, in
         const int token = t * per + in_tile;
         const bool on = in_tile < per && token < s.tokens;
         const int seen = !on ? 0 : p.causal ? pre_seen(s, token) : s.keys;
-        float m = -INFINITY, l = 0.f;  // maximum in use (raw scores), sum of the weights
+        float m = -INFINITY, l = 0.f;  // reference (a raw score), sum of the weights
         for (int j = 0; j < tile.steps; ++j, ++phase) {
             if (!__all_sync(0xffffffffu, c.wait(B_S + t, phase & 1))) return;
             tc_fence_after();
-            float x[128];
-            {
-                uint32_t u[4][32];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) tmem_ld32(s_col + 32 * i, u[i]);
-                tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 128; ++i) x[i] = __uint_as_float(u[i / 32][i % 32]);
-            }
-            const int left = seen - (s.step0 + j) * kPreTile;
-            if (left < kPreTile) {
-#pragma unroll
-                for (int i = 0; i < 128; ++i) x[i] = i < left ? x[i] : -INFINITY;
-            }
-            float mx[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) mx[k] = x[k];
-#pragma unroll
-            for (int i = 8; i < 120; i += 16) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) mx[k] = max3f(mx[k], x[i + 2 * k], x[i + 2 * k + 1]);
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) mx[k] = max3f(mx[k], mx[k + 4], fmaxf(x[120 + 2 * k], x[121 + 2 * k]));
-            const float top = fmaxf(max3f(mx[0], mx[1], mx[2]), mx[3]);
-            const bool grow = top > m + lazy;  // (m = -inf: the first score of the row)
-            const float m_new = grow ? top : m;
-            if (j > 0 && __any_sync(0xffffffffu, grow)) {
-                // O is in units of the old maximum, or of none
-                if (!__all_sync(0xffffffffu, c.wait(B_PV + t, (phase - 1) & 1))) return;
-                tc_fence_after();
-                const float f = grow ? (m == -INFINITY ? 0.f : exp2_fast((m - m_new) * p.scale_log2)) : 1.f;
-                l *= f;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t o[32];
-                    tmem_ld32(o_col + 32 * i, o);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                    tmem_st32(o_col + 32 * i, o);
-                }
-                tmem_wait_st();
-            }
-            m = m_new;
-            const float shift = m == -INFINITY ? 0.f : -m * p.scale_log2;
-            const uint64_t scale2 = f2_pack(p.scale_log2, p.scale_log2), shift2 = f2_pack(shift, shift);
-            uint64_t sum[2] = {0, 0};
+            uint32_t x[4][32];
+            tmem_ld32(s_col, x[0]);
+            tmem_ld32(s_col + 32, x[1]);
+            arrived(x[0], x[1]);
+            tmem_ld32(s_col + 64, x[2]);  // the second half lands behind the first one's work
+            tmem_ld32(s_col + 96, x[3]);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                uint32_t w[32];
+                uint32_t(&a)[32] = x[2 * h];
+                uint32_t(&b)[32] = x[2 * h + 1];
+                if (h) arrived(a, b);
+                const int left = seen - (s.step0 + j) * kPreTile - 64 * h;
+                if (left < 64) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    float a, b;
-                    f2_unpack(f2_fma(f2_pack(x[64 * h + 2 * i], x[64 * h + 2 * i + 1]), scale2, shift2), a, b);
-                    a = exp2_fast(a);
-                    b = exp2_fast(b);
-                    sum[i & 1] = f2_add(sum[i & 1], f2_pack(a, b));
-                    w[i] = pack_bf16(a, b);
+                    for (int i = 0; i < 32; ++i) {
+                        a[i] = i < left ? a[i] : 0xff800000u;
+                        b[i] = i + 32 < left ? b[i] : 0xff800000u;
+                    }
                 }
+                if (j == 0 && h == 0) m = largest(a, b);
+                uint32_t w[32];
+                float sum = weigh(a, b, m, p.scale_log2, w);
+                const bool raise = !(sum <= kMostWeight) || (m == -INFINITY && left > 0);
+                if (__any_sync(0xffffffffu, raise)) {
+                    const float top = fmaxf(m, largest(a, b)), m_new = raise ? top : m;
+                    const float f = !raise ? 1.f : m == -INFINITY ? 0.f : exp2_fast((m - m_new) * p.scale_log2);
+                    if (j + h > 0) {
+                        // every product so far is in O: the step before's, or this step's first half
+                        if (!__all_sync(0xffffffffu, h ? c.wait(B_PV0 + t, phase & 1) : c.wait(B_PV + t, (phase - 1) & 1))) return;
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int i = 0; i < 8; ++i) {
+                            uint32_t o[16];
+                            tmem_ld16(o_col + 16 * i, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                            tmem_st16(o_col + 16 * i, o);
+                        }
+                        tmem_wait_st();
+                    }
+                    l *= f;
+                    m = m_new;
+                    sum = weigh(a, b, m, p.scale_log2, w);
+                }
+                l += sum;
                 tmem_st32(s_col + 32 * h, w);
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(c.bar(B_P + 2 * t + h));
             }
-            float a, b;
-            f2_unpack(f2_add(sum[0], sum[1]), a, b);
-            l += a + b;
         }
         // epilogue: o = O / l, lse
         float lse = l == 0.f ? -INFINITY : m * p.scale + logf(l);
@@ -559,6 +589,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             mbar_init(c.bar(B_S + t), 1);
             mbar_init(c.bar(B_P + 2 * t), kPreTile);
             mbar_init(c.bar(B_P + 2 * t + 1), kPreTile);
+            mbar_init(c.bar(B_PV0 + t), 1);
             mbar_init(c.bar(B_PV + t), 1);
             mbar_init(c.bar(B_OFREE + t), kPreTile);
             mbar_init(c.bar(B_TURN + t), 1);
