@@ -40,10 +40,6 @@ namespace {
 using namespace sm103;
 
 constexpr int kThreads = 384;
-// registers of a thread: 168 at launch, then a thread of the rows keeps its 128 scores and
-// gets some of the others' (256 x 200 + 128 x 104 = 384 x 168)
-constexpr int kRowRegs = 200, kOtherRegs = 104;
-static_assert(256 * kRowRegs + 128 * kOtherRegs <= kThreads * 168, "a split of what the CTA was launched with");
 constexpr int kLoadWarp = 8, kMmaWarp = 9, kZeroWarp = 11;  // MMAs: a warp per tile
 constexpr int kRows = kPreTiles * kPreTile;
 constexpr uint32_t kSlotBytes = 16384;
@@ -283,11 +279,12 @@ __device__ void mma_role(const PrefillParams &p, const Ctx &c, uint32_t tmem, in
             if (elected()) {
 #pragma unroll
                 for (int ch = 0; ch < L::kChunks; ++ch) {
-                    if (ch == L::kChunks - 1 && hand_over) mbar_arrive(c.bar(B_TURN + 1 - t));
+                    
 #pragma unroll
                     for (int i = 0; i < 4; ++i)  // 16 dims: 32 B
                         mma_ss(s_col, q_desc + ch * (kSlotBytes / 16) + 2 * i, bd[ch] + 2 * i, idesc, ch + i > 0);
                 }
+                if (hand_over) mbar_arrive(c.bar(B_TURN + 1 - t));
                 mma_commit(c.bar(B_S + t));
                 mma_commit(c.bar(B_EMPTY + g % kGroups));
                 if (j == steps - 1) mma_commit(c.bar(B_QEMPTY + t));
@@ -447,6 +444,63 @@ __device__ __forceinline__ float weigh(const uint32_t (&a)[32], const uint32_t (
     return lo + hi;
 }
 
+// 64 scores of a row, and what its weights refer to
+struct Half {
+    uint32_t s_col, o_col;  // tensor memory: the scores (the weights go to `p_col`), the tile's O
+    uint32_t p_col;
+    int left;               // scores in sight, from the first on
+    float m, l;             // reference (a raw score), sum of the weights so far
+    bool first;             // no reference yet
+};
+struct State {
+    float m, l;
+    int ok;
+};
+
+// The half that a warp meets now and then: some row's first scores, scores out of
+// sight, or weights far above the reference.  Out of line, so that the loop over ordinary
+// halves stays within the instruction cache.
+__device__ __noinline__ State careful_half(const Half x, float scale_log2, uint64_t *products, uint32_t parity, unsigned int *status) {
+    uint32_t a[32], b[32], w[32];
+    tmem_ld32(x.s_col, a);
+    tmem_ld32(x.s_col + 32, b);
+    arrived(a, b);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        a[i] = i < x.left ? a[i] : 0xff800000u;
+        b[i] = i + 32 < x.left ? b[i] : 0xff800000u;
+    }
+    const float top = largest(a, b);
+    float m = x.first ? top : x.m, l = x.l, sum = 0.f;
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+        sum = weigh(a, b, m, scale_log2, w);
+        const bool raise = !(sum <= kMostWeight) || (m == -INFINITY && x.left > 0);
+        if (pass || !__any_sync(0xffffffffu, raise)) break;
+        const float m_new = raise ? fmaxf(m, top) : m;
+        const float f = !raise ? 1.f : m == -INFINITY ? 0.f : exp2_fast((m - m_new) * scale_log2);
+        if (products) {
+            // every product so far is in O
+            if (!__all_sync(0xffffffffu, mbar_wait(products, parity, status))) return {m, l, 0};
+            tc_fence_after();
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i) {
+                uint32_t o[16];
+                tmem_ld16(x.o_col + 16 * i, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                tmem_st16(x.o_col + 16 * i, o);
+            }
+            tmem_wait_st();
+        }
+        l *= f;
+        m = m_new;
+    }
+    tmem_st32(x.p_col, w);
+    return {m, l + sum, 1};
+}
+
 __device__ void row_role(const PrefillParams &p, const Ctx &c, uint32_t tmem, int t) {
     const int warp = threadIdx.x >> 5, r = threadIdx.x & (kPreTile - 1);
     const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
@@ -465,53 +519,31 @@ __device__ void row_role(const PrefillParams &p, const Ctx &c, uint32_t tmem, in
         for (int j = 0; j < tile.steps; ++j, ++phase) {
             if (!__all_sync(0xffffffffu, c.wait(B_S + t, phase & 1))) return;
             tc_fence_after();
-            uint32_t x[4][32];
-            tmem_ld32(s_col, x[0]);
-            tmem_ld32(s_col + 32, x[1]);
-            arrived(x[0], x[1]);
-            tmem_ld32(s_col + 64, x[2]);  // the second half lands behind the first one's work
-            tmem_ld32(s_col + 96, x[3]);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t(&a)[32] = x[2 * h];
-                uint32_t(&b)[32] = x[2 * h + 1];
-                if (h) arrived(a, b);
-                const int left = seen - (s.step0 + j) * kPreTile - 64 * h;
-                if (left < 64) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        a[i] = i < left ? a[i] : 0xff800000u;
-                        b[i] = i + 32 < left ? b[i] : 0xff800000u;
-                    }
-                }
-                if (j == 0 && h == 0) m = largest(a, b);
-                uint32_t w[32];
-                float sum = weigh(a, b, m, p.scale_log2, w);
-                const bool raise = !(sum <= kMostWeight) || (m == -INFINITY && left > 0);
-                if (__any_sync(0xffffffffu, raise)) {
-                    const float top = fmaxf(m, largest(a, b)), m_new = raise ? top : m;
-                    const float f = !raise ? 1.f : m == -INFINITY ? 0.f : exp2_fast((m - m_new) * p.scale_log2);
-                    if (j + h > 0) {
-                        // every product so far is in O: the step before's, or this step's first half
-                        if (!__all_sync(0xffffffffu, h ? c.wait(B_PV0 + t, phase & 1) : c.wait(B_PV + t, (phase - 1) & 1))) return;
-                        tc_fence_after();
 #pragma unroll 1
-                        for (int i = 0; i < 8; ++i) {
-                            uint32_t o[16];
-                            tmem_ld16(o_col + 16 * i, o);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                            tmem_st16(o_col + 16 * i, o);
-                        }
-                        tmem_wait_st();
-                    }
-                    l *= f;
-                    m = m_new;
+            for (int h = 0; h < 2; ++h) {
+                const int left = seen - (s.step0 + j) * kPreTile - 64 * h;
+                bool careful = j + h == 0 || left < 64;
+                uint32_t w[32];
+                float sum = 0.f;
+                if (!__any_sync(0xffffffffu, careful)) {
+                    uint32_t a[32], b[32];
+                    tmem_ld32(s_col + 64 * h, a);
+                    tmem_ld32(s_col + 64 * h + 32, b);
+                    arrived(a, b);
                     sum = weigh(a, b, m, p.scale_log2, w);
+                    careful = !(sum <= kMostWeight) || m == -INFINITY;
                 }
-                l += sum;
-                tmem_st32(s_col + 32 * h, w);
+                if (!__any_sync(0xffffffffu, careful)) {
+                    l += sum;
+                    tmem_st32(s_col + 32 * h, w);
+                } else {
+                    // products so far: the step before's, or this step's first half
+                    const Half x = {s_col + 64 * h, o_col, s_col + 32 * h, left, m, l, j + h == 0};
+                    const State y = careful_half(x, p.scale_log2, j + h == 0 ? nullptr : c.bar((h ? B_PV0 : B_PV) + t), (h ? phase : phase - 1) & 1, c.status);
+                    if (!y.ok) return;
+                    m = y.m;
+                    l = y.l;
+                }
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(c.bar(B_P + 2 * t + h));
@@ -613,10 +645,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
     griddep_wait();
     if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRowRegs));
         row_role(p, c, tmem, warp >> 2);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == kLoadWarp) {
             load_role<kRope>(p, c, &mq, &mk, &mr, &mv);
         } else if (warp < kZeroWarp) {
