@@ -200,12 +200,11 @@ struct PrefillParams {
     float scale, scale_log2;      // softmax scale, and times log2(e)
     uint16_t *out;                // [num_q][h_q][128]
     float *lse;                   // [num_q][h_q]
-    int32_t *metadata;            // header, segments, cut blocks (mla_prefill.cuh)
-    int64_t max_segments;
-    int max_slots;
-    float *o_part;                // [max_slots][h_kv][256][128] fp32
-    float *lse_part;              // [max_slots][h_kv][256]
-    int sms;
+    int32_t *metadata;            // the partition (mla_prefill.cuh)
+    int64_t max_blocks;
+    float *o_part;                // [2 sms][256][128] fp32: a CTA's first and last item may be cut
+    float *lse_part;              // [2 sms][256]
+    int sms;                      // CTAs
     int head_chunk;               // key heads that run side by side
     unsigned int *status;
 };

@@ -4,8 +4,8 @@
 // over the keys j that query row i sees, d_qk = 128 or 128 + 64 (the 64 RoPE dims
 // of a key shared by all heads, read from their own tensor), d_v = 128.
 //
-// A CTA takes one segment of the partition (mla_prefill_schedule.cu) for one
-// key head at a time: two tiles A and B of 128 query rows (row r of a tile is
+// A CTA takes one segment at a time, steps of a block of the partition
+// (mla_prefill_schedule.cu) for one key head: two tiles A and B of 128 query rows (row r of a tile is
 // head r % group of token r / group, so that grouped heads share the loads of their
 // key head), walking steps of 128 keys together, so that every key and value
 // that lands in shared memory serves 256 rows.  Tensor memory is full: S_A, S_B, O_A,
@@ -41,7 +41,6 @@ using namespace sm103;
 
 constexpr int kThreads = 384;
 constexpr int kLoadWarp = 8, kMmaWarp = 9, kZeroWarp = 11;  // MMAs: a warp per tile
-constexpr int kRows = kPreTiles * kPreTile;
 constexpr uint32_t kSlotBytes = 16384;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kMostWeight = 0x1p20f;  // that a row's 64 weights may add up to before their reference is raised
@@ -76,43 +75,56 @@ struct Ctx {
     __device__ bool wait(int i, uint32_t parity) const { return mbar_wait(bars + i, parity, status); }
 };
 
-// Items of a CTA: (segment, key head).  Heads go in chunks, a chunk's segments longest
-// first with its heads side by side, so that the CTAs of a moment share few
-// heads' keys (in L2) and the last items are short ones.
+// A part of an item: steps step0 .. step1 of a block, for one key head.
+struct Segment : PreBlock {
+    int step0, step1;
+    int slot;           // of the partial results; -1: the whole item
+};
+
+// The segments of a CTA: its items of every round, or its share of the line
+// (mla_prefill_schedule.cu).
 struct Walk {
-    const PreHeader *header;
-    const PreSegment *segments;
-    int64_t at, items;
-    int h_kv, chunk;
-    __device__ Walk(const PrefillParams &p) {
-        header = reinterpret_cast<const PreHeader *>(p.metadata);
-        segments = reinterpret_cast<const PreSegment *>(header + 1);
-        const int n = (int)min((long long)max(0, header->segments), (long long)p.max_segments);
-        items = (int64_t)n * p.h_kv;
-        h_kv = p.h_kv;
-        chunk = p.head_chunk;
-        at = blockIdx.x;
-        count = n;
+    PreWork work;
+    int blocks, round = 0;
+    bool line;
+    PrePlace at, end;
+    __device__ Walk(const PrefillParams &p) : work(p.metadata, p.max_blocks, p.sms) {
+        blocks = (int)min((long long)max(0, work.header->blocks), (long long)p.max_blocks);
+        line = work.header->line != 0;
+        if (line) {
+            at = work.places[blockIdx.x];
+            end = work.places[blockIdx.x + 1];
+        }
     }
-    int count;
-    __device__ bool next(const PrefillParams &p, PreSegment &s, int &head) {
-        if (at >= items) return false;
-        // every other round of the CTAs runs backwards: over lengths that fall, each CTA gets its share
-        const int64_t round = at / gridDim.x, last = min((long long)items - 1, (long long)(round + 1) * gridDim.x - 1);
-        const int64_t i = round & 1 ? last - (at - round * gridDim.x) : at;
-        const int64_t per = (int64_t)count * chunk;
-        const int c = (int)(i / per);
-        const int heads = min(chunk, h_kv - c * chunk);
-        const int64_t in = i - c * per;
-        s = segments[in / heads];
-        head = c * chunk + (int)(in % heads);
-        at += gridDim.x;
+    __device__ bool next(const PrefillParams &p, Segment &s, int &head) {
+        int block, step0 = 0, step1 = 0x7fffffff;
+        if (line) {
+            block = at.block, head = at.head, step0 = at.step;
+            const bool last = block == end.block && head == end.head;
+            if (block >= end.block && (block > end.block || head > end.head || (last && step0 >= end.step))) return false;
+            if (block < 0 || block >= blocks || head < 0 || head >= p.h_kv) return false;
+            if (last) {
+                step1 = end.step;
+                at = end;
+            } else {
+                at = {block + (head + 1 == p.h_kv), head + 1 == p.h_kv ? 0 : head + 1, 0, 0};
+            }
+        } else if (!pre_round_item(round, blockIdx.x, gridDim.x, blocks, p.h_kv, p.head_chunk, block, head)) {
+            return false;
+        }
+        static_cast<PreBlock &>(s) = work.blocks[block];
+        s.step0 = step0;
+        s.step1 = min(step1, s.steps);
+        // the first of a line's segments and the last may be parts
+        s.slot = s.step0 > 0 || s.step1 < s.steps ? 2 * (int)blockIdx.x + (round > 0) : -1;
+        ++round;
         // a partition of other lengths must not make the kernel leave its tensors
         const int most = kPreTiles * pre_tile_tokens(p.group);
-        if (s.q0 < 0 || s.tokens < 0 || s.tokens > most || (int64_t)s.q0 + s.tokens > p.num_q || s.slot >= p.max_slots ||
-            s.keys < 0 || s.k0 < 0 || (int64_t)s.k0 + s.keys > p.num_k || s.step0 < 0 || s.step1 > pre_steps(s.keys)) {
+        if (s.q0 < 0 || s.tokens < 0 || s.tokens > most || (int64_t)s.q0 + s.tokens > p.num_q || s.keys < 0 || s.k0 < 0 ||
+            (int64_t)s.k0 + s.keys > p.num_k || s.step0 < 0 || s.step1 > pre_steps(s.keys)) {
             if ((threadIdx.x & 31) == 0) atomicOr(p.status, MLA_DEVERR_SEQLEN);
             s.tokens = s.step0 = s.step1 = 0;
+            s.slot = -1;
         }
         return true;
     }
@@ -123,14 +135,14 @@ struct Walk {
 // such a group has been issued (B_TAIL: only then is the group's B_FULL in the phase
 // that the zeroing waits for), the zero role when it is done (B_ZERO).  The group's
 // barriers are used again after both, so none is more than a phase ahead of who waits.
-__device__ __forceinline__ bool tail_step(const PreSegment &s, int j) {
+__device__ __forceinline__ bool tail_step(const Segment &s, int j) {
     return s.keys - (s.step0 + j) * kPreTile < kPreTile && s.keys % 16 != 0;
 }
 
 // what a tile of a segment does: keys that its last token sees, and its steps
 struct Tile {
     int seen, steps;
-    __device__ Tile(const PrefillParams &p, const PreSegment &s, int t) {
+    __device__ Tile(const PrefillParams &p, const Segment &s, int t) {
         const int per = pre_tile_tokens(p.group), last = min(s.tokens, (t + 1) * per) - 1;
         seen = last < t * per ? 0 : p.causal ? pre_seen(s, last) : s.keys;
         steps = max(0, min(pre_steps(seen), s.step1) - s.step0);
@@ -160,7 +172,7 @@ __device__ void load_role(const PrefillParams &p, const Ctx &c, const CUtensorMa
                           const CUtensorMap *mv) {
     using L = Layout<kRope>;
     Walk walk(p);
-    PreSegment s;
+    Segment s;
     int head;
     uint32_t slot = 0, group = 0, freed = 0, held = 0;  // groups issued and given back, slots that the others hold
     uint32_t qn[kPreTiles] = {0, 0};
@@ -256,7 +268,7 @@ __device__ void mma_role(const PrefillParams &p, const Ctx &c, uint32_t tmem, in
     using L = Layout<kRope>;
     constexpr uint32_t kPvDesc = idesc_bf16(kPreTile, kPreHead, false, true);
     Walk walk(p);
-    PreSegment s;
+    Segment s;
     int head;
     uint32_t slot = 0, group = 0, qn = 0, done = 0, turn = 0;
     uint32_t zeroed = 0;  // a bit per group barrier, the phase of its B_ZERO
@@ -362,7 +374,7 @@ template <bool kRope>
 __device__ void zero_role(const PrefillParams &p, const Ctx &c) {
     using L = Layout<kRope>;
     Walk walk(p);
-    PreSegment s;
+    Segment s;
     int head;
     uint32_t slot = 0, group = 0, tails = 0;  // tails: a bit per group barrier, the phase of its B_TAIL
     const int lane = threadIdx.x & 31;
@@ -507,7 +519,7 @@ __device__ void row_role(const PrefillParams &p, const Ctx &c, uint32_t tmem, in
     const uint32_t s_col = tmem + lane_base + t * 128, o_col = tmem + lane_base + 256 + t * 128;
     const int per = pre_tile_tokens(p.group), in_tile = r / p.group, hh = r - in_tile * p.group;
     Walk walk(p);
-    PreSegment s;
+    Segment s;
     int head;
     uint32_t phase = 0;  // steps of this tile so far
     while (walk.next(p, s, head)) {
@@ -553,7 +565,7 @@ __device__ void row_role(const PrefillParams &p, const Ctx &c, uint32_t tmem, in
         float lse = l == 0.f ? -INFINITY : m * p.scale + logf(l);
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const int64_t row = (int64_t)(s.q0 + token) * p.h_q + head * p.group + hh;
-        const int64_t part = ((int64_t)s.slot * p.h_kv + head) * kRows + t * kPreTile + r;
+        const int64_t part = (int64_t)s.slot * kPreRows + t * kPreTile + r;
         if (on) {
             if (s.slot < 0) p.lse[row] = lse;
             else p.lse_part[part] = lse;
@@ -668,33 +680,34 @@ prefill_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
 }
 
 // ---------------------------------------------------------------- combine of cut blocks
-// A warp per (block, head, row): o = sum_s w_s o_s, w_s = exp(lse_s - lse); a part in
+// A warp per (item, row): o = sum_s w_s o_s, w_s = exp(lse_s - lse); a part in
 // which the row saw nothing (lse -inf) was not written and is not read.
 constexpr int kCombineWarps = 8;
 
 __global__ void __launch_bounds__(kCombineWarps * 32) prefill_combine_kernel(const __grid_constant__ PrefillParams p) {
     griddep_wait();
-    const PreHeader *header = reinterpret_cast<const PreHeader *>(p.metadata);
-    const PreCut *cuts = reinterpret_cast<const PreCut *>(reinterpret_cast<const PreSegment *>(header + 1) + p.max_segments);
+    const PreWork work(p.metadata, p.max_blocks, p.sms);
     const int lane = threadIdx.x & 31, per = pre_tile_tokens(p.group);
-    const int n = min(header->cuts, p.max_slots);
-    const int64_t total = (int64_t)n * p.h_kv * kRows, stride = (int64_t)gridDim.x * kCombineWarps;
-    for (int64_t i = (int64_t)blockIdx.x * kCombineWarps + (threadIdx.x >> 5); i < total; i += stride) {
-        const int r = (int)(i % kRows), head = (int)(i / kRows % p.h_kv);
-        const PreCut cut = cuts[i / kRows / p.h_kv];
+    const int n = work.header->line ? min(work.header->cuts, p.sms) : 0;
+    const int total = n * kPreRows, stride = gridDim.x * kCombineWarps;
+    for (int i = blockIdx.x * kCombineWarps + (threadIdx.x >> 5); i < total; i += stride) {
+        const int r = i % kPreRows;
+        const PreCut cut = work.cuts[i / kPreRows];
+        if (cut.block < 0 || cut.block >= p.max_blocks || cut.slot0 < 0 || cut.cta < 1 || cut.cta + cut.count - 1 > p.sms) continue;
+        const PreBlock block = work.blocks[cut.block];
         const int t = r / kPreTile, in_tile = (r % kPreTile) / p.group, hh = (r % kPreTile) - in_tile * p.group, token = t * per + in_tile;
-        if (in_tile >= per || token >= cut.tokens || cut.slot0 < 0 || cut.slot0 + cut.count > p.max_slots || (int64_t)cut.q0 + token >= p.num_q) continue;
-        const int64_t step = (int64_t)p.h_kv * kRows, first = ((int64_t)cut.slot0 * p.h_kv + head) * kRows + r;
+        if (in_tile >= per || token >= block.tokens || block.q0 < 0 || (int64_t)block.q0 + token >= p.num_q) continue;
+        auto part = [&](int k) { return (int64_t)(k ? 2 * (cut.cta + k - 1) : cut.slot0) * kPreRows + r; };
         float top = -INFINITY;
-        for (int k = 0; k < cut.count; ++k) top = fmaxf(top, p.lse_part[first + k * step]);
+        for (int k = 0; k < cut.count; ++k) top = fmaxf(top, p.lse_part[part(k)]);
         const float base = top == -INFINITY ? 0.f : top;
         float sum = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int k = 0; k < cut.count; ++k) {
-            const float lse = p.lse_part[first + k * step];
+            const float lse = p.lse_part[part(k)];
             if (lse == -INFINITY) continue;
             const float w = exp2_fast((lse - base) * 1.4426950408889634f);
-            const float4 x = reinterpret_cast<const float4 *>(p.o_part + (first + k * step) * kPreHead)[lane];
+            const float4 x = reinterpret_cast<const float4 *>(p.o_part + part(k) * kPreHead)[lane];
             sum += w;
             o.x = fmaf(w, x.x, o.x);
             o.y = fmaf(w, x.y, o.y);
@@ -702,7 +715,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) prefill_combine_kernel(con
             o.w = fmaf(w, x.w, o.w);
         }
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const int64_t row = (int64_t)(cut.q0 + token) * p.h_q + head * p.group + hh;
+        const int64_t row = (int64_t)(block.q0 + token) * p.h_q + cut.head * p.group + hh;
         reinterpret_cast<uint2 *>(p.out + row * kPreHead)[lane] = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
         if (lane == 0) p.lse[row] = sum == 0.f ? -INFINITY : base + logf(sum);
     }
@@ -764,10 +777,9 @@ cudaError_t launch(const PrefillParams &p, cudaStream_t stream) {
         mr = mk;
         if (kRope && !make_map(&mr, p.k_rope, kPreRope, 1, p.num_k, kPreRope, p.k_rope_token, 1, kPreTile)) return cudaErrorInvalidValue;
     }
-    const int64_t items = p.max_segments * p.h_kv;
-    const unsigned grid = (unsigned)(items < p.sms ? items : p.sms);
-    e = launch_after(prefill_kernel<kRope>, dim3(grid), dim3(kThreads), Layout<kRope>::kBytes, stream, mq, mk, mr, mv, p);
-    if (e != cudaSuccess || p.max_slots == 0) return e;
+    // (a CTA per SM: the line counts on them; in rounds the last may have no item)
+    e = launch_after(prefill_kernel<kRope>, dim3(p.sms), dim3(kThreads), Layout<kRope>::kBytes, stream, mq, mk, mr, mv, p);
+    if (e != cudaSuccess) return e;
     return launch_after(prefill_combine_kernel, dim3(2 * p.sms), dim3(kCombineWarps * 32), 0, stream, p);
 }
 

@@ -75,26 +75,29 @@ int prefill_shape(int batch, int64_t num_q, int h_q, int h_kv) {
     return MLA_OK;
 }
 
-// words of the partition, and the workspace: the partial results of cut blocks, then
+// words of the partition, and the workspace: the partial results of cut items, then
 // room for the partition when the caller brings none
 struct PrefillLayout {
-    int64_t max_segments;
-    int max_slots;
+    int64_t max_blocks;
     size_t words, o_part, lse_part, metadata, total;
 };
 
-PrefillLayout prefill_layout(int batch, int64_t num_q, int h_q, int h_kv, int sms) {
+PrefillLayout prefill_layout(int batch, int64_t num_q, int group, int sms) {
     PrefillLayout l;
-    const int rows = kPreTiles * kPreTile;
-    l.max_slots = pre_max_slots(sms, h_kv);
-    l.max_segments = pre_max_segments(num_q, batch, h_q / h_kv, sms, h_kv);
-    l.words = (sizeof(PreHeader) + l.max_segments * sizeof(PreSegment) + l.max_slots * sizeof(PreCut)) / sizeof(int32_t);
-    const size_t parts = (size_t)l.max_slots * h_kv * rows;
+    l.max_blocks = pre_max_blocks(num_q, batch, group);
+    l.words = pre_words(l.max_blocks, sms);
+    const size_t rows = (size_t)pre_slots(sms) * kPreRows;
     l.o_part = 0;
-    l.lse_part = align_up(parts * kPreHead * sizeof(float));
-    l.metadata = l.lse_part + align_up(parts * sizeof(float));
+    l.lse_part = align_up(rows * kPreHead * sizeof(float));
+    l.metadata = l.lse_part + align_up(rows * sizeof(float));
     l.total = l.metadata + align_up(l.words * sizeof(int32_t));
     return l;
+}
+
+// key heads side by side: as many as keep their keys and values in half of L2
+int prefill_head_chunk(int64_t num_k, int h_kv) {
+    const int64_t side = (64LL << 20) / ((num_k > 0 ? num_k : 1) * 4 * kPreHead);
+    return (int)(side < 1 ? 1 : side > h_kv ? h_kv : side);
 }
 
 }  // namespace
@@ -232,13 +235,13 @@ int mla_norm_rope_cache_write_fp8(const void *latent, int64_t latent_stride, con
 int64_t mla_prefill_metadata_ints(int batch, int64_t num_q, int h_q, int h_kv) {
     int sms = 0;
     if (prefill_shape(batch, num_q, h_q, h_kv) != MLA_OK || device_sm_count(&sms) != cudaSuccess) return 0;
-    return (int64_t)prefill_layout(batch, num_q, h_q, h_kv, sms).words;
+    return (int64_t)prefill_layout(batch, num_q, h_q / h_kv, sms).words;
 }
 
 size_t mla_prefill_workspace_bytes(int batch, int64_t num_q, int h_q, int h_kv) {
     int sms = 0;
     if (prefill_shape(batch, num_q, h_q, h_kv) != MLA_OK || device_sm_count(&sms) != cudaSuccess) return 0;
-    return prefill_layout(batch, num_q, h_q, h_kv, sms).total;
+    return prefill_layout(batch, num_q, h_q / h_kv, sms).total;
 }
 
 int mla_get_metadata_prefill(const int32_t *cu_q, const int32_t *cu_k, int batch, int64_t num_q, int64_t num_k, int h_q, int h_kv,
@@ -250,7 +253,6 @@ int mla_get_metadata_prefill(const int32_t *cu_q, const int32_t *cu_k, int batch
     Range range("mla_get_metadata_prefill");
     PrefillParams p{};
     if (device_sm_count(&p.sms) != cudaSuccess) return MLA_ERR_CUDA;
-    const PrefillLayout l = prefill_layout(batch, num_q, h_q, h_kv, p.sms);
     p.cu_q = cu_q;
     p.cu_k = cu_k;
     p.batch = batch;
@@ -261,8 +263,8 @@ int mla_get_metadata_prefill(const int32_t *cu_q, const int32_t *cu_k, int batch
     p.group = h_q / h_kv;
     p.causal = causal != 0;
     p.metadata = metadata;
-    p.max_segments = l.max_segments;
-    p.max_slots = l.max_slots;
+    p.max_blocks = pre_max_blocks(num_q, batch, p.group);
+    p.head_chunk = prefill_head_chunk(num_k, h_kv);
     if (status_address(&p.status) != MLA_OK) return MLA_ERR_CUDA;
     return result(launch_prefill_schedule(p, reinterpret_cast<cudaStream_t>(stream)));
 }
@@ -298,7 +300,7 @@ int mla_prefill(const void *q, int64_t q_token_stride, int64_t q_head_stride, co
     if (num_q == 0) return MLA_OK;
     PrefillParams p{};
     if (device_sm_count(&p.sms) != cudaSuccess) return MLA_ERR_CUDA;
-    const PrefillLayout l = prefill_layout(batch, num_q, h_q, h_kv, p.sms);
+    const PrefillLayout l = prefill_layout(batch, num_q, h_q / h_kv, p.sms);
     if (workspace_bytes < l.total) return MLA_ERR_WORKSPACE;
     Range range("mla_prefill");
     char *ws = static_cast<char *>(workspace);
@@ -332,14 +334,10 @@ int mla_prefill(const void *q, int64_t q_token_stride, int64_t q_head_stride, co
     p.scale_log2 = softmax_scale * 1.4426950408889634f;
     p.out = static_cast<uint16_t *>(out);
     p.lse = lse;
-    p.max_segments = l.max_segments;
-    p.max_slots = l.max_slots;
+    p.max_blocks = l.max_blocks;
     p.o_part = reinterpret_cast<float *>(ws + l.o_part);
     p.lse_part = reinterpret_cast<float *>(ws + l.lse_part);
-    // key heads side by side: as many as keep their keys and values in half of L2
-    const int64_t head_bytes = (num_k > 0 ? num_k : 1) * 4 * kPreHead;
-    const int64_t side = (64LL << 20) / head_bytes;
-    p.head_chunk = (int)(side < 1 ? 1 : side > h_kv ? h_kv : side);
+    p.head_chunk = prefill_head_chunk(num_k, h_kv);
     if (status_address(&p.status) != MLA_OK) return MLA_ERR_CUDA;
     return result(launch_prefill(p, reinterpret_cast<cudaStream_t>(stream)));
 }

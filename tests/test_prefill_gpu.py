@@ -236,12 +236,13 @@ def test_the_partition_serves_every_layer_and_a_graph(dev):
 
 
 def test_the_same_bits_every_time(dev):
-    lq, lk = [900, 5, 130], [900, 9000, 2000]
-    q, k, v, kr = make(dev, lq, lk, 16, 4, True)
-    first = mla.mla_prefill(q, k, v, cu_of(lq, dev), cu_of(lk, dev), k_rope=kr)
-    for _ in range(5):
-        again = mla.mla_prefill(q, k, v, cu_of(lq, dev), cu_of(lk, dev), k_rope=kr)
-        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+    # the last: many items of one length, of which some are cut
+    for lq, lk, hq, hkv in (([900, 5, 130], [900, 9000, 2000], 16, 4), ([64] * 37, [5000] * 37, 8, 8)):
+        q, k, v, kr = make(dev, lq, lk, hq, hkv, True)
+        first = mla.mla_prefill(q, k, v, cu_of(lq, dev), cu_of(lk, dev), k_rope=kr)
+        for _ in range(5):
+            again = mla.mla_prefill(q, k, v, cu_of(lq, dev), cu_of(lk, dev), k_rope=kr)
+            assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
 
 
 def test_streams_and_threads(dev):
