@@ -40,6 +40,11 @@ namespace {
 using namespace sm103;
 
 constexpr int kThreads = 384;
+// registers of a thread: 168 at launch; the rows' threads, which keep what they know of the
+// next item beside a half's scores and weights, get some of the others'
+// (256 x 200 + 128 x 104 = 384 x 168)
+constexpr int kRowRegs = 200, kOtherRegs = 104;
+static_assert(256 * kRowRegs + 128 * kOtherRegs <= kThreads * 168, "a split of what the CTA was launched with");
 constexpr int kLoadWarp = 8, kMmaWarp = 9, kZeroWarp = 11;  // MMAs: a warp per tile
 constexpr uint32_t kSlotBytes = 16384;
 constexpr uint32_t kTmemCols = 512;
@@ -83,11 +88,14 @@ struct Segment : PreBlock {
 
 // The segments of a CTA: its items of every round, or its share of the line
 // (mla_prefill_schedule.cu).
+// The block of the next one is fetched while the current one runs.
 struct Walk {
     PreWork work;
     int blocks, round = 0;
-    bool line;
+    bool line, more;
     PrePlace at, end;
+    Segment ahead;
+    int ahead_head;
     __device__ Walk(const PrefillParams &p) : work(p.metadata, p.max_blocks, p.sms) {
         blocks = (int)min((long long)max(0, work.header->blocks), (long long)p.max_blocks);
         line = work.header->line != 0;
@@ -95,29 +103,41 @@ struct Walk {
             at = work.places[blockIdx.x];
             end = work.places[blockIdx.x + 1];
         }
+        fetch(p);
     }
-    __device__ bool next(const PrefillParams &p, Segment &s, int &head) {
-        int block, step0 = 0, step1 = 0x7fffffff;
+    __device__ __forceinline__ void fetch(const PrefillParams &p) {
+        int block, step1 = 0x7fffffff;
+        ahead.step0 = 0;
+        more = false;
         if (line) {
-            block = at.block, head = at.head, step0 = at.step;
-            const bool last = block == end.block && head == end.head;
-            if (block >= end.block && (block > end.block || head > end.head || (last && step0 >= end.step))) return false;
-            if (block < 0 || block >= blocks || head < 0 || head >= p.h_kv) return false;
+            block = at.block, ahead_head = at.head, ahead.step0 = at.step;
+            const bool last = block == end.block && ahead_head == end.head;
+            if (block > end.block || (block == end.block && (ahead_head > end.head || (last && at.step >= end.step)))) return;
+            if (block < 0 || block >= blocks || ahead_head < 0 || ahead_head >= p.h_kv) return;
             if (last) {
                 step1 = end.step;
                 at = end;
             } else {
-                at = {block + (head + 1 == p.h_kv), head + 1 == p.h_kv ? 0 : head + 1, 0, 0};
+                at = {block + (ahead_head + 1 == p.h_kv), ahead_head + 1 == p.h_kv ? 0 : ahead_head + 1, 0, 0};
             }
-        } else if (!pre_round_item(round, blockIdx.x, gridDim.x, blocks, p.h_kv, p.head_chunk, block, head)) {
-            return false;
+        } else if (!pre_round_item(round, blockIdx.x, gridDim.x, blocks, p.h_kv, p.head_chunk, block, ahead_head)) {
+            return;
         }
-        static_cast<PreBlock &>(s) = work.blocks[block];
-        s.step0 = step0;
-        s.step1 = min(step1, s.steps);
-        // the first of a line's segments and the last may be parts
-        s.slot = s.step0 > 0 || s.step1 < s.steps ? 2 * (int)blockIdx.x + (round > 0) : -1;
+        more = true;
+        const int4 *src = reinterpret_cast<const int4 *>(work.blocks + block);
+        const int4 u = src[0], v = src[1];
+        ahead.q0 = u.x, ahead.tokens = u.y, ahead.k0 = u.z, ahead.keys = u.w, ahead.seen = v.x, ahead.steps = v.y;
+        ahead.step1 = step1;
         ++round;
+    }
+    __device__ __forceinline__ bool next(const PrefillParams &p, Segment &s, int &head) {
+        if (!more) return false;
+        s = ahead;
+        head = ahead_head;
+        s.step1 = min(s.step1, s.steps);
+        // the first of a line's segments and the last may be parts
+        s.slot = s.step0 > 0 || s.step1 < s.steps ? 2 * (int)blockIdx.x + (round > 1) : -1;
+        fetch(p);
         // a partition of other lengths must not make the kernel leave its tensors
         const int most = kPreTiles * pre_tile_tokens(p.group);
         if (s.q0 < 0 || s.tokens < 0 || s.tokens > most || (int64_t)s.q0 + s.tokens > p.num_q || s.keys < 0 || s.k0 < 0 ||
@@ -197,21 +217,22 @@ __device__ void load_role(const PrefillParams &p, const Ctx &c, const CUtensorMa
     while (ok && walk.next(p, s, head)) {
         const Tile a(p, s, 0), b(p, s, 1);
         const int n = max(a.steps, b.steps);
-        // Q of the tiles that walk
+        // Q of the tiles that walk, behind the first keys: its place is free only when the
+            // products of the segment before have read it
 #pragma unroll
-        for (int t = 0; t < kPreTiles; ++t) {
-            if (!ok || (t ? b.steps : a.steps) == 0) continue;
-            ok = wait(B_QEMPTY + t, (qn[t] & 1) ^ 1);
-            if (!ok) continue;
-            ++qn[t];
-            if (elected()) {
-                mbar_arrive_expect_tx(c.bar(B_QFULL + t), L::kChunks * q_bytes);
-                for (int ch = 0; ch < L::kChunks; ++ch)
-                    tma_load(smem_u32(c.base + (t * L::kChunks + ch) * kSlotBytes), mq, c.bar(B_QFULL + t), 64 * ch, head * p.group,
-                             s.q0 + t * pre_tile_tokens(p.group));
+            for (int t = 0; t < kPreTiles; ++t) {
+                if (!ok || (t ? b.steps : a.steps) == 0) continue;
+                ok = wait(B_QEMPTY + t, (qn[t] & 1) ^ 1);
+                if (!ok) continue;
+                ++qn[t];
+                if (elected()) {
+                    mbar_arrive_expect_tx(c.bar(B_QFULL + t), L::kChunks * q_bytes);
+                    for (int ch = 0; ch < L::kChunks; ++ch)
+                        tma_load(smem_u32(c.base + (t * L::kChunks + ch) * kSlotBytes), mq, c.bar(B_QFULL + t), 64 * ch, head * p.group,
+                                 s.q0 + t * pre_tile_tokens(p.group));
+                }
+                __syncwarp();
             }
-            __syncwarp();
-        }
         for (int j = 0; ok && j < n; ++j) {
             const int k0 = s.k0 + (s.step0 + j) * kPreTile;
             if (!(ok = room(L::kChunks))) break;
@@ -228,7 +249,7 @@ __device__ void load_role(const PrefillParams &p, const Ctx &c, const CUtensorMa
                 }
                 __syncwarp();
             }
-            if (!(ok = room(2))) break;
+            if (!ok || !(ok = room(2))) break;
             bar = c.bar(B_FULL + group % kGroups);
             const uint32_t tail = group % kGroups;
             ++group;
@@ -513,6 +534,9 @@ __device__ __noinline__ State careful_half(const Half x, float scale_log2, uint6
     return {m, l + sum, 1};
 }
 
+// A partial result's 4 dims 4 c .. of a row: rows side by side, as the rows' threads write them
+__device__ __forceinline__ int64_t part_at(int64_t slot, int c, int row) { return (slot * (kPreHead / 4) + c) * kPreRows + row; }
+
 __device__ void row_role(const PrefillParams &p, const Ctx &c, uint32_t tmem, int t) {
     const int warp = threadIdx.x >> 5, r = threadIdx.x & (kPreTile - 1);
     const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
@@ -565,10 +589,9 @@ __device__ void row_role(const PrefillParams &p, const Ctx &c, uint32_t tmem, in
         float lse = l == 0.f ? -INFINITY : m * p.scale + logf(l);
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const int64_t row = (int64_t)(s.q0 + token) * p.h_q + head * p.group + hh;
-        const int64_t part = (int64_t)s.slot * kPreRows + t * kPreTile + r;
         if (on) {
             if (s.slot < 0) p.lse[row] = lse;
-            else p.lse_part[part] = lse;
+            else p.lse_part[(int64_t)s.slot * kPreRows + t * kPreTile + r] = lse;
         }
         if (tile.steps == 0) {
             if (on && s.slot < 0)
@@ -588,6 +611,8 @@ __device__ void row_role(const PrefillParams &p, const Ctx &c, uint32_t tmem, in
             }
             if (!on) continue;
             if (s.slot < 0) {
+                // (a lane writes its own row: turned among four lanes, so that a store touches 8 lines
+                // instead of 32, prompts of 300 rows took 95.6 us for 87.8)
                 uint4 *dst = reinterpret_cast<uint4 *>(p.out + row * kPreHead + 32 * i);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
@@ -598,11 +623,11 @@ __device__ void row_role(const PrefillParams &p, const Ctx &c, uint32_t tmem, in
                     dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
                 }
             } else {
-                float4 *dst = reinterpret_cast<float4 *>(p.o_part + part * kPreHead + 32 * i);
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                    dst[k] = make_float4(__uint_as_float(o[4 * k]) * inv, __uint_as_float(o[4 * k + 1]) * inv, __uint_as_float(o[4 * k + 2]) * inv,
-                                         __uint_as_float(o[4 * k + 3]) * inv);
+                    reinterpret_cast<float4 *>(p.o_part)[part_at(s.slot, 8 * i + k, t * kPreTile + r)] =
+                        make_float4(__uint_as_float(o[4 * k]) * inv, __uint_as_float(o[4 * k + 1]) * inv, __uint_as_float(o[4 * k + 2]) * inv,
+                                    __uint_as_float(o[4 * k + 3]) * inv);
             }
         }
     }
@@ -657,8 +682,10 @@ prefill_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
     griddep_wait();
     if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRowRegs));
         row_role(p, c, tmem, warp >> 2);
     } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == kLoadWarp) {
             load_role<kRope>(p, c, &mq, &mk, &mr, &mv);
         } else if (warp < kZeroWarp) {
@@ -679,45 +706,56 @@ prefill_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     }
 }
 
-// ---------------------------------------------------------------- combine of cut blocks
-// A warp per (item, row): o = sum_s w_s o_s, w_s = exp(lse_s - lse); a part in
-// which the row saw nothing (lse -inf) was not written and is not read.
-constexpr int kCombineWarps = 8;
+// ---------------------------------------------------------------- combine of cut items
+// A warp per 32 rows of an item and 16 of the dims, a lane per row (the partial results'
+// order): o = sum_s w_s o_s, w_s = exp(lse_s - lse).  A part in which the row saw
+// nothing (lse -inf) was not written and is not read.
+constexpr int kCombineWarps = 8, kCombineDims = 16;
 
 __global__ void __launch_bounds__(kCombineWarps * 32) prefill_combine_kernel(const __grid_constant__ PrefillParams p) {
     griddep_wait();
     const PreWork work(p.metadata, p.max_blocks, p.sms);
     const int lane = threadIdx.x & 31, per = pre_tile_tokens(p.group);
+    constexpr int kUnits = kPreRows / 32 * (kPreHead / kCombineDims);  // of an item
     const int n = work.header->line ? min(work.header->cuts, p.sms) : 0;
-    const int total = n * kPreRows, stride = gridDim.x * kCombineWarps;
+    const int total = n * kUnits, stride = gridDim.x * kCombineWarps;
     for (int i = blockIdx.x * kCombineWarps + (threadIdx.x >> 5); i < total; i += stride) {
-        const int r = i % kPreRows;
-        const PreCut cut = work.cuts[i / kPreRows];
-        if (cut.block < 0 || cut.block >= p.max_blocks || cut.slot0 < 0 || cut.cta < 1 || cut.cta + cut.count - 1 > p.sms) continue;
+        const PreCut cut = work.cuts[i / kUnits];
+        if (cut.block < 0 || cut.block >= p.max_blocks || cut.slot0 < 0 || cut.slot0 >= pre_slots(p.sms) || cut.cta < 1 ||
+            cut.count < 1 || cut.cta + cut.count - 1 > p.sms)
+            continue;
         const PreBlock block = work.blocks[cut.block];
+        const int unit = i % kUnits, r = unit % (kPreRows / 32) * 32 + lane, c0 = unit / (kPreRows / 32) * (kCombineDims / 4);
         const int t = r / kPreTile, in_tile = (r % kPreTile) / p.group, hh = (r % kPreTile) - in_tile * p.group, token = t * per + in_tile;
         if (in_tile >= per || token >= block.tokens || block.q0 < 0 || (int64_t)block.q0 + token >= p.num_q) continue;
-        auto part = [&](int k) { return (int64_t)(k ? 2 * (cut.cta + k - 1) : cut.slot0) * kPreRows + r; };
+        auto slot = [&](int k) { return k ? 2 * (cut.cta + k - 1) : cut.slot0; };
         float top = -INFINITY;
-        for (int k = 0; k < cut.count; ++k) top = fmaxf(top, p.lse_part[part(k)]);
+        for (int k = 0; k < cut.count; ++k) top = fmaxf(top, p.lse_part[(int64_t)slot(k) * kPreRows + r]);
         const float base = top == -INFINITY ? 0.f : top;
-        float sum = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        float sum = 0.f, o[kCombineDims] = {};
         for (int k = 0; k < cut.count; ++k) {
-            const float lse = p.lse_part[part(k)];
+            const float lse = p.lse_part[(int64_t)slot(k) * kPreRows + r];
             if (lse == -INFINITY) continue;
             const float w = exp2_fast((lse - base) * 1.4426950408889634f);
-            const float4 x = reinterpret_cast<const float4 *>(p.o_part + part(k) * kPreHead)[lane];
             sum += w;
-            o.x = fmaf(w, x.x, o.x);
-            o.y = fmaf(w, x.y, o.y);
-            o.z = fmaf(w, x.z, o.z);
-            o.w = fmaf(w, x.w, o.w);
+#pragma unroll
+            for (int c = 0; c < kCombineDims / 4; ++c) {
+                const float4 x = reinterpret_cast<const float4 *>(p.o_part)[part_at(slot(k), c0 + c, r)];
+                o[4 * c] = fmaf(w, x.x, o[4 * c]);
+                o[4 * c + 1] = fmaf(w, x.y, o[4 * c + 1]);
+                o[4 * c + 2] = fmaf(w, x.z, o[4 * c + 2]);
+                o[4 * c + 3] = fmaf(w, x.w, o[4 * c + 3]);
+            }
         }
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
         const int64_t row = (int64_t)(block.q0 + token) * p.h_q + cut.head * p.group + hh;
-        reinterpret_cast<uint2 *>(p.out + row * kPreHead)[lane] = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-        if (lane == 0) p.lse[row] = sum == 0.f ? -INFINITY : base + logf(sum);
+        uint32_t w[kCombineDims / 2];
+#pragma unroll
+        for (int k = 0; k < kCombineDims / 2; ++k) w[k] = pack_bf16(o[2 * k] * inv, o[2 * k + 1] * inv);
+        uint4 *dst = reinterpret_cast<uint4 *>(p.out + row * kPreHead + 4 * c0);
+        dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        if (c0 == 0) p.lse[row] = sum == 0.f ? -INFINITY : base + logf(sum);
     }
 }
 
@@ -780,6 +818,7 @@ cudaError_t launch(const PrefillParams &p, cudaStream_t stream) {
     // (a CTA per SM: the line counts on them; in rounds the last may have no item)
     e = launch_after(prefill_kernel<kRope>, dim3(p.sms), dim3(kThreads), Layout<kRope>::kBytes, stream, mq, mk, mr, mv, p);
     if (e != cudaSuccess) return e;
+    if (!pre_line(p.max_blocks, p.h_kv, p.sms)) return cudaSuccess;
     return launch_after(prefill_combine_kernel, dim3(2 * p.sms), dim3(kCombineWarps * 32), 0, stream, p);
 }
 

@@ -42,6 +42,11 @@ __host__ __device__ inline int64_t pre_max_blocks(int64_t num_q, int batch, int 
     const int64_t t = kPreTiles * pre_tile_tokens(group);
     return num_q / t + (num_q < batch ? num_q : batch);
 }
+// More rounds of whole items than this are even enough: the line is not considered.  By
+// the most blocks that a call can have, which the host knows: it then leaves out the
+// combine.
+constexpr int kPreRounds = 8;
+__host__ __device__ inline bool pre_line(int64_t max_blocks, int h_kv, int ctas) { return max_blocks * h_kv <= (int64_t)kPreRounds * ctas; }
 // slots of partial results: a CTA's first and last item may be cut
 __host__ __device__ constexpr int pre_slots(int ctas) { return 2 * ctas; }
 // keys that token i of a block sees
@@ -77,9 +82,12 @@ __host__ __device__ inline bool pre_round_item(int64_t round, int cta, int ctas,
     const int64_t last = items - 1 < first + ctas - 1 ? items - 1 : first + ctas - 1;
     const int64_t i = round & 1 ? last - cta : first + cta;
     const int64_t per = (int64_t)blocks * chunk;
-    const int c = (int)(i / per), heads = chunk < h_kv - c * chunk ? chunk : h_kv - c * chunk;
-    block = (int)((i - c * per) / heads);
-    head = c * chunk + (int)((i - c * per) % heads);
+    int c = 0;
+    if (i >= per) c = items <= 0x7fffffff ? (int)((uint32_t)i / (uint32_t)per) : (int)(i / per);
+    const int heads = chunk < h_kv - c * chunk ? chunk : h_kv - c * chunk;
+    const int64_t in = i - c * per;
+    block = in <= 0x7fffffff ? (int)((uint32_t)in / (uint32_t)heads) : (int)(in / heads);
+    head = c * chunk + (int)(in - (int64_t)block * heads);
     return true;
 }
 

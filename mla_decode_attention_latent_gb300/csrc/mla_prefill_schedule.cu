@@ -32,9 +32,8 @@ constexpr int kThreads = 1024;
 constexpr int kFixed = 2;        // units of an item beside its steps
 constexpr int kCombine = 3;      // units of the combine
 constexpr int kLeastShare = 6;   // units of a share on the line
-constexpr int kRounds = 8;       // more rounds than this are even enough
 constexpr int kLengths = 1024;   // lengths that the sort tells apart
-constexpr int kStable = 1280;    // blocks that are sorted stably, and more than a line has
+constexpr int kStable = 1280;    // blocks that are sorted stably: as many as a line can have, and more
 
 struct Shared {
     long long warp[kThreads / 32];
@@ -100,6 +99,7 @@ __device__ void each_block(const PrefillParams &p, Shared &sh, bool report, F f)
 
 __global__ void __launch_bounds__(kThreads) prefill_schedule_kernel(const PrefillParams p) {
     __shared__ Shared sh;
+    static_assert(kStable >= kPreRounds * 160 && kThreads / 4 >= 160, "multiprocessors");
     if (threadIdx.x == 0) sm103::griddep_launch_dependents();
     sm103::griddep_wait();
     const PreWork work(p.metadata, p.max_blocks, p.sms);
@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kThreads) prefill_schedule_kernel(const Prefil
     const long long items = (long long)blocks * p.h_kv, units = (all + (long long)kFixed * blocks) * p.h_kv;
     const long long share = max((units + p.sms - 1) / p.sms, (long long)kLeastShare);
     bool line = false;
-    if (stable && items > 0 && items <= (long long)kRounds * p.sms && p.sms <= kThreads / 4) {
+    if (items > 0 && pre_line(p.max_blocks, p.h_kv, p.sms)) {
         if ((int)threadIdx.x < p.sms) {
             long long mine = 0;
             int block, head;
