@@ -12,13 +12,14 @@
 // loses a bit for every doubling.  Its distance to the nearest whole turn goes to
 // sincospif as a float, so a small angle keeps its 24 bits.
 //
-// Heads: a group of 8 lanes per head, lane l taking the 16-byte pieces l, l + 8, ...
+// Heads: a group of 8 lanes per head (32 above 256 values), lane l taking the 16-byte pieces l, l + 8, ...
 // (128 contiguous bytes per load and group; a head of 192 keeps every lane busy,
 // where a warp per head would idle a quarter of them).  A CTA takes a run of
 // consecutive heads of consecutive tokens and computes the tokens' sines once, in
 // shared memory, for all of their heads.  Everything is loaded once and stays in
-// registers; the partner of a value in the half layout is loaded again by the lane
-// that needs it (from L1), before anything is stored, so that a call may be in place.
+// registers, the next head on its way while one is computed; the partner of a value in
+// the half layout comes from the lane that has it, or is loaded again where heads are cut
+// oddly, in both cases before anything of its head is stored, so that a call may be in place.
 // Bound by HBM on prompts and by the launch on single tokens.
 //
 // Rows: a warp per cached row, the 512 latent dims as 64 pieces over its lanes and
@@ -32,9 +33,7 @@ namespace mla {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kGroup = 8;                       // lanes of a head
-constexpr int kGroups = kThreads / kGroup;
-constexpr int kMaxPieces = 9;                   // 16-byte pieces of a lane: heads of up to 576 values
+constexpr int kNarrow = 8, kWide = 32;          // lanes of a head of up to 256 values, and of a wider one
 constexpr int kMaxAngles = 4096;                // of a CTA: 32 KB
 
 // cosine and sine of position * turns, times scale
@@ -108,94 +107,152 @@ __device__ __forceinline__ void rotate8(float (&f)[8], const float (&other)[8], 
     }
 }
 
-// kPieces: 16-byte pieces of a lane
-template <int kPieces, bool kNorm, bool kInterleaved>
+// Where the partner of a rotated value is.
+enum Pairs {
+    kNeighbours,  // interleaved: in the same piece
+    kOwn,         // halves of as many pieces as lanes, from the first lane on: the lane's piece before or behind
+    kOther,       // halves of a power of two of pieces, both inside the lanes: the lane `half` away
+    kReload,      // any other place: loaded again
+};
+
+// kGroup: lanes of a head, kPieces: 16-byte pieces of a lane
+template <int kGroup, int kPieces, bool kNorm, Pairs kPairs>
 __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeParams p, int rows_per_cta) {
+    constexpr int kGroups = kThreads / kGroup;
     extern __shared__ float2 s_angle[];  // [tokens of the CTA][rope_dim / 2]
     sm103::griddep_wait();
     const int group = threadIdx.x / kGroup, lane = threadIdx.x % kGroup;
     const int64_t rows = p.tokens * p.heads, row0 = (int64_t)blockIdx.x * rows_per_cta;
-    const int64_t row1 = min(row0 + rows_per_cta, rows);
+    const int64_t row1 = min((long long)row0 + rows_per_cta, (long long)rows);
     const int64_t token0 = row0 / p.heads;
+    const int head0 = (int)(row0 - token0 * p.heads), count = (int)(row1 - row0);
     const int pairs = p.rope.positions ? p.rope.rope_dim / 2 : 0;
+    const int piece0 = p.first / 8 + lane, pieces = p.d / 8, rope0 = pieces - pairs / 4, half = pairs / 8;
+    constexpr int kAgain = kPairs == kReload ? kPieces : 1;
+    // one row's pieces (and, loaded again, the partners of its rotated ones)
+    struct Pieces {
+        uint4 x[kPieces], again[kAgain];
+    };
+    auto place = [&](int i, int &token, int &head) {
+        const unsigned at = (unsigned)(head0 + i);
+        token = (int)(at / (unsigned)p.heads);
+        head = (int)(at - (unsigned)token * (unsigned)p.heads);
+    };
+    auto load = [&](int i, Pieces &v) {
+        int token, head;
+        place(min(i, count - 1), token, head);
+        const uint4 *src = reinterpret_cast<const uint4 *>(p.x + (token0 + token) * p.x_token + head * p.x_head);
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) {
+            const int at = piece0 + kGroup * j;
+            v.x[j] = at < pieces ? src[at] : make_uint4(0, 0, 0, 0);
+            if constexpr (kPairs == kReload) v.again[j] = at >= rope0 && at < pieces ? src[at - rope0 < half ? at + half : at - half] : make_uint4(0, 0, 0, 0);
+        }
+    };
+    Pieces next;
+    load(group, next);  // under way while the angles are computed
     if (pairs) {
-        const int tokens = (int)((row1 - 1) / p.heads - token0) + 1;
+        const int tokens = (head0 + count - 1) / p.heads + 1;
         for (int i = threadIdx.x; i < tokens * pairs; i += kThreads) {
             const int t = i / pairs, k = i - t * pairs;
             s_angle[i] = angle(p.rope.positions[token0 + t], p.rope.turns[k], p.rope.scale);
         }
-        __syncthreads();
     }
-    const int piece0 = p.first / 8, pieces = p.d / 8, rope0 = pieces - pairs / 4, half = pairs / 8;
-    uint4 w[kPieces], wo[kPieces];
+    uint4 w[kPieces], wo[kAgain];  // wo: weights of the partners
     if constexpr (kNorm) {
+        const uint4 *src = reinterpret_cast<const uint4 *>(p.weight);
 #pragma unroll
         for (int j = 0; j < kPieces; ++j) {
-            const int i = piece0 + lane + kGroup * j;
-            if (i < pieces) w[j] = reinterpret_cast<const uint4 *>(p.weight)[i];
-            if (!kInterleaved && i >= rope0 && i < pieces)
-                wo[j] = reinterpret_cast<const uint4 *>(p.weight)[i - rope0 < half ? i + half : i - half];
+            const int at = piece0 + kGroup * j;
+            w[j] = at < pieces ? src[at] : make_uint4(0, 0, 0, 0);
+            if constexpr (kPairs == kReload) wo[j] = at >= rope0 && at < pieces ? src[at - rope0 < half ? at + half : at - half] : make_uint4(0, 0, 0, 0);
+            if constexpr (kPairs == kOther)  // (a lane has one rotated piece)
+                if (at >= rope0 && at < pieces) wo[0] = src[at - rope0 < half ? at + half : at - half];
         }
     }
+    if (pairs) __syncthreads();
     // every group makes the same number of turns, for the shuffles
-    for (int64_t r = row0 + group; r - group < row1; r += kGroups) {
-        const bool on = r < row1;
-        const int64_t row = on ? r : row1 - 1, token = row / p.heads;
-        const int head = (int)(row - token * p.heads);
-        const uint4 *src = reinterpret_cast<const uint4 *>(p.x + token * p.x_token + head * p.x_head);
-        uint4 *dst = reinterpret_cast<uint4 *>(p.out + token * p.out_token + head * p.out_head);
-        uint4 x[kPieces], o[kPieces];
-#pragma unroll
-        for (int j = 0; j < kPieces; ++j) {
-            const int i = piece0 + lane + kGroup * j;
-            x[j] = o[j] = make_uint4(0, 0, 0, 0);
-            if (i < pieces) x[j] = src[i];
-            if (!kInterleaved && i >= rope0 && i < pieces) o[j] = src[i - rope0 < half ? i + half : i - half];
-        }
+    for (int r = group; r - group < count; r += kGroups) {
+        const Pieces v = next;
+        if (r - group + kGroups < count) load(r + kGroups, next);
+        if constexpr (kPairs == kReload) __syncwarp();  // in place: no lane stores a head before all have loaded it
+        int token, head;
+        place(min(r, count - 1), token, head);
+        uint4 *dst = reinterpret_cast<uint4 *>(p.out + (token0 + token) * p.out_token + head * p.out_head);
         float inv = 1.f;
         if constexpr (kNorm) {
             inv = inverse_rms([&](float k) {
                 float s = 0.f;
 #pragma unroll
-                for (int j = 0; j < kPieces; ++j) s += squares(x[j], k);
+                for (int j = 0; j < kPieces; ++j) s += squares(v.x[j], k);
 #pragma unroll
                 for (int off = 1; off < kGroup; off <<= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
                 return s;
             }, p.d, p.eps);
         }
-        __syncwarp();  // in place: every load of the warp's heads comes before a store
-        if (!on) continue;
-        const float2 *cs = s_angle + (int)(token - token0) * pairs;
+        const float2 *cs = s_angle + token * pairs;
 #pragma unroll
         for (int j = 0; j < kPieces; ++j) {
-            const int i = piece0 + lane + kGroup * j;
-            if (i >= pieces) continue;
-            uint4 y = x[j];
-            if (kNorm || i >= rope0) {
+            const int at = piece0 + kGroup * j, part = at - rope0;
+            const bool turned = part >= 0 && at < pieces, low = part < half;
+            uint4 other = make_uint4(0, 0, 0, 0), other_w = make_uint4(0, 0, 0, 0);
+            if constexpr (kPairs == kOwn) {
+                other = low ? v.x[j + 1 < kPieces ? j + 1 : j] : v.x[j > 0 ? j - 1 : 0];
+                if constexpr (kNorm) other_w = low ? w[j + 1 < kPieces ? j + 1 : j] : w[j > 0 ? j - 1 : 0];
+            } else if constexpr (kPairs == kOther) {
+                if (__any_sync(0xffffffffu, turned)) {
+                    other.x = __shfl_xor_sync(0xffffffffu, v.x[j].x, half);
+                    other.y = __shfl_xor_sync(0xffffffffu, v.x[j].y, half);
+                    other.z = __shfl_xor_sync(0xffffffffu, v.x[j].z, half);
+                    other.w = __shfl_xor_sync(0xffffffffu, v.x[j].w, half);
+                }
+                if constexpr (kNorm) other_w = wo[0];
+            } else if constexpr (kPairs == kReload) {
+                other = v.again[j];
+                if constexpr (kNorm) other_w = wo[j];
+            }
+            if (r >= count || at >= pieces) continue;
+            uint4 y = v.x[j];
+            if (kNorm || turned) {
                 float f[8], g[8];
-                widen8(x[j], f);
+                widen8(v.x[j], f);
                 if constexpr (kNorm) scale8(f, w[j], inv);
-                if (i >= rope0) {
-                    if constexpr (!kInterleaved) {
-                        widen8(o[j], g);
-                        if constexpr (kNorm) scale8(g, wo[j], inv);
-                    }
-                    const int part = i - rope0;
-                    const bool low = part < half;
+                if (turned) {
                     float2 t[8];
+                    // two angles a load
+                    const float4 *from = reinterpret_cast<const float4 *>(cs + (kPairs == kNeighbours ? 4 * part : 8 * (low ? part : part - half)));
 #pragma unroll
-                    for (int k = 0; k < (kInterleaved ? 4 : 8); ++k) t[k] = cs[kInterleaved ? 4 * part + k : 8 * (low ? part : part - half) + k];
-                    rotate8<kInterleaved>(f, g, t, low);
+                    for (int k = 0; k < (kPairs == kNeighbours ? 2 : 4); ++k) {
+                        const float4 two = from[k];
+                        t[2 * k] = make_float2(two.x, two.y);
+                        t[2 * k + 1] = make_float2(two.z, two.w);
+                    }
+                    if constexpr (kPairs != kNeighbours) {
+                        widen8(other, g);
+                        if constexpr (kNorm) scale8(g, other_w, inv);
+                    }
+                    rotate8<kPairs == kNeighbours>(f, g, t, low);
                 }
                 y = round8(f);
             }
-            dst[i] = y;
+            dst[at] = y;
         }
     }
 }
 
-template <int kPieces>
+template <int kGroup, int kPieces, bool kNorm>
+void (*heads_kernel(Pairs pairs))(NormRopeParams, int) {
+    switch (pairs) {
+        case kNeighbours: return norm_rope_kernel<kGroup, kPieces, kNorm, kNeighbours>;
+        case kOwn: return norm_rope_kernel<kGroup, kPieces, kNorm, kOwn>;
+        case kOther: return norm_rope_kernel<kGroup, kPieces, kNorm, kOther>;
+        default: return norm_rope_kernel<kGroup, kPieces, kNorm, kReload>;
+    }
+}
+
+template <int kGroup, int kPieces>
 cudaError_t launch_heads(const NormRopeParams &p, cudaStream_t stream) {
+    constexpr int kGroups = kThreads / kGroup;
     const int pairs = p.rope.positions ? p.rope.rope_dim / 2 : 0;
     const int64_t rows = p.tokens * p.heads;
     int sms = 0;
@@ -211,10 +268,11 @@ cudaError_t launch_heads(const NormRopeParams &p, cudaStream_t stream) {
     const size_t smem = pairs ? ((size_t)(per_cta - 1) / p.heads + 2) * pairs * sizeof(float2) : 0;
     const int64_t ctas = (rows + per_cta - 1) / per_cta;
     if (ctas > 0x7fffffffll) return cudaErrorInvalidValue;
-    const bool il = p.rope.interleaved != 0;
-    void (*kernel)(NormRopeParams, int) = p.weight ? (il ? norm_rope_kernel<kPieces, true, true> : norm_rope_kernel<kPieces, true, false>)
-                                                   : (il ? norm_rope_kernel<kPieces, false, true> : norm_rope_kernel<kPieces, false, false>);
-    return launch_after(kernel, dim3((unsigned)ctas), dim3(kThreads), smem, stream, p, per_cta);
+    const int half = pairs / 8, rel = (p.d - p.first) / 8 - pairs / 4;  // pieces of a half, and before the first
+    const Pairs where = p.rope.interleaved || !pairs ? kNeighbours : half == kGroup && rel % kGroup == 0 ? kOwn
+                        : 2 * half <= kGroup && (half & (half - 1)) == 0 && rel % (2 * half) == 0 ? kOther : kReload;
+    return launch_after(p.weight ? heads_kernel<kGroup, kPieces, true>(where) : heads_kernel<kGroup, kPieces, false>(where), dim3((unsigned)ctas),
+                        dim3(kThreads), smem, stream, p, per_cta);
 }
 
 // ---------------------------------------------------------------- rows into the cache
@@ -314,12 +372,13 @@ __global__ void __launch_bounds__(kRowWarps * 32) place_rows_kernel(const PlaceR
 }  // namespace
 
 cudaError_t launch_norm_rope(const NormRopeParams &p, cudaStream_t stream) {
-    switch (((p.d - p.first) / 8 + kGroup - 1) / kGroup) {
-        case 1: return launch_heads<1>(p, stream);
-        case 2: return launch_heads<2>(p, stream);
-        case 3: return launch_heads<3>(p, stream);
-        case 4: return launch_heads<4>(p, stream);
-        default: return launch_heads<kMaxPieces>(p, stream);
+    const int pieces = (p.d - p.first) / 8;
+    if (pieces > 4 * kNarrow) return launch_heads<kWide, 3>(p, stream);
+    switch ((pieces + kNarrow - 1) / kNarrow) {
+        case 1: return launch_heads<kNarrow, 1>(p, stream);
+        case 2: return launch_heads<kNarrow, 2>(p, stream);
+        case 3: return launch_heads<kNarrow, 3>(p, stream);
+        default: return launch_heads<kNarrow, 4>(p, stream);
     }
 }
 
