@@ -117,9 +117,10 @@ enum Pairs {
 
 // kGroup: lanes of a head, kPieces: 16-byte pieces of a lane
 template <int kGroup, int kPieces, bool kNorm, Pairs kPairs>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeParams p, int rows_per_cta) {
+__global__ void __launch_bounds__(kThreads, kPairs == kReload ? 2 : kPieces <= 3 ? 4 : 3) norm_rope_kernel(const NormRopeParams p, int rows_per_cta) {
     constexpr int kGroups = kThreads / kGroup;
     extern __shared__ float2 s_angle[];  // [tokens of the CTA][rope_dim / 2]
+    __shared__ uint4 s_weight[kGroup * kPieces];
     sm103::griddep_wait();
     const int group = threadIdx.x / kGroup, lane = threadIdx.x % kGroup;
     const int64_t rows = p.tokens * p.heads, row0 = (int64_t)blockIdx.x * rows_per_cta;
@@ -158,19 +159,11 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeParam
             s_angle[i] = angle(p.rope.positions[token0 + t], p.rope.turns[k], p.rope.scale);
         }
     }
-    uint4 w[kPieces], wo[kAgain];  // wo: weights of the partners
+    // the weights, in shared memory: in registers they would cost a CTA per SM
     if constexpr (kNorm) {
-        const uint4 *src = reinterpret_cast<const uint4 *>(p.weight);
-#pragma unroll
-        for (int j = 0; j < kPieces; ++j) {
-            const int at = piece0 + kGroup * j;
-            w[j] = at < pieces ? src[at] : make_uint4(0, 0, 0, 0);
-            if constexpr (kPairs == kReload) wo[j] = at >= rope0 && at < pieces ? src[at - rope0 < half ? at + half : at - half] : make_uint4(0, 0, 0, 0);
-            if constexpr (kPairs == kOther)  // (a lane has one rotated piece)
-                if (at >= rope0 && at < pieces) wo[0] = src[at - rope0 < half ? at + half : at - half];
-        }
+        if (threadIdx.x < pieces - p.first / 8) s_weight[threadIdx.x] = reinterpret_cast<const uint4 *>(p.weight)[threadIdx.x];
     }
-    if (pairs) __syncthreads();
+    if (pairs || kNorm) __syncthreads();
     // every group makes the same number of turns, for the shuffles
     for (int r = group; r - group < count; r += kGroups) {
         const Pieces v = next;
@@ -195,10 +188,9 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeParam
         for (int j = 0; j < kPieces; ++j) {
             const int at = piece0 + kGroup * j, part = at - rope0;
             const bool turned = part >= 0 && at < pieces, low = part < half;
-            uint4 other = make_uint4(0, 0, 0, 0), other_w = make_uint4(0, 0, 0, 0);
+            uint4 other = make_uint4(0, 0, 0, 0);
             if constexpr (kPairs == kOwn) {
                 other = low ? v.x[j + 1 < kPieces ? j + 1 : j] : v.x[j > 0 ? j - 1 : 0];
-                if constexpr (kNorm) other_w = low ? w[j + 1 < kPieces ? j + 1 : j] : w[j > 0 ? j - 1 : 0];
             } else if constexpr (kPairs == kOther) {
                 if (__any_sync(0xffffffffu, turned)) {
                     other.x = __shfl_xor_sync(0xffffffffu, v.x[j].x, half);
@@ -206,17 +198,15 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeParam
                     other.z = __shfl_xor_sync(0xffffffffu, v.x[j].z, half);
                     other.w = __shfl_xor_sync(0xffffffffu, v.x[j].w, half);
                 }
-                if constexpr (kNorm) other_w = wo[0];
             } else if constexpr (kPairs == kReload) {
                 other = v.again[j];
-                if constexpr (kNorm) other_w = wo[j];
             }
             if (r >= count || at >= pieces) continue;
             uint4 y = v.x[j];
             if (kNorm || turned) {
                 float f[8], g[8];
                 widen8(v.x[j], f);
-                if constexpr (kNorm) scale8(f, w[j], inv);
+                if constexpr (kNorm) scale8(f, s_weight[at], inv);
                 if (turned) {
                     float2 t[8];
                     // two angles a load
@@ -229,7 +219,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeParam
                     }
                     if constexpr (kPairs != kNeighbours) {
                         widen8(other, g);
-                        if constexpr (kNorm) scale8(g, other_w, inv);
+                        if constexpr (kNorm) scale8(g, s_weight[low ? at + half : at - half], inv);
                     }
                     rotate8<kPairs == kNeighbours>(f, g, t, low);
                 }
@@ -258,8 +248,12 @@ cudaError_t launch_heads(const NormRopeParams &p, cudaStream_t stream) {
     int sms = 0;
     cudaError_t e = device_sm_count(&sms);
     if (e != cudaSuccess) return e;
-    // a turn of the CTA's groups each while that gives every SM several CTAs, four at most
-    int per_cta = kGroups * (int)max((int64_t)1, min((int64_t)4, rows / (kGroups * 8 * (int64_t)sms)));
+    // as many turns of the groups as leave about kCtas CTAs per SM, at most kTurns: they share
+    // the tokens' angles (1777 tokens of 40 heads of 128: 1 / 4 / 8 turns 13.6 / 12.7 / 11.8 us;
+    // 4096 tokens of 128 heads of 192: 115 / 80.8 / 80.7, 32 turns 99.7 with the last CTAs alone)
+    constexpr int64_t kCtas = 3, kTurns = 8;
+    const int64_t turns = (rows + kGroups * kCtas * sms - 1) / (kGroups * kCtas * sms);
+    int per_cta = kGroups * (int)(turns < kTurns ? turns : kTurns);
     if (pairs) {
         // the tokens that a run of heads touches have their angles in shared memory
         const int tokens = kMaxAngles / pairs;
@@ -278,6 +272,28 @@ cudaError_t launch_heads(const NormRopeParams &p, cudaStream_t stream) {
 // ---------------------------------------------------------------- rows into the cache
 constexpr int kRowWarps = 8;
 constexpr int kRopeDims = kDqk - kDv;
+
+// e4m3(y / c) of 8 values.  With inv the rounded reciprocal of c, q = y inv, the remainder
+// y - q c is exact in one fused operation, and q + (y - q c) inv is the quotient to
+// within its last bit.  Two values per instruction.  A zero's code is +0.
+__device__ __forceinline__ uint2 quantise8(const float (&y)[8], float c, float inv) {
+    uint32_t code[4];
+    if (c < 0x1p-100f) {  // the remainder and the reciprocal leave the normal range
+#pragma unroll
+        for (int k = 0; k < 4; ++k) code[k] = sm103::pack_e4m3x2(y[2 * k] / c + 0.f, y[2 * k + 1] / c + 0.f);
+    } else {
+        const uint64_t inv2 = sm103::f2_pack(inv, inv), minus_c2 = sm103::f2_pack(-c, -c), zero2 = sm103::f2_pack(0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint64_t v = sm103::f2_pack(y[2 * k], y[2 * k + 1]);
+            const uint64_t q = sm103::f2_fma(v, inv2, zero2), r = sm103::f2_fma(q, minus_c2, v);
+            float a, b;
+            sm103::f2_unpack(sm103::f2_fma(r, inv2, q), a, b);
+            code[k] = sm103::pack_e4m3x2(a, b);
+        }
+    }
+    return make_uint2(code[0] | (code[1] << 16), code[2] | (code[3] << 16));
+}
 
 template <int D, bool kE4m3>
 __global__ void __launch_bounds__(kRowWarps * 32) place_rows_kernel(const PlaceRowsParams p) {
@@ -359,13 +375,10 @@ __global__ void __launch_bounds__(kRowWarps * 32) place_rows_kernel(const PlaceR
             reinterpret_cast<float *>(page + kPage * kDqk)[off] = c;
         }
         uint2 *dst = reinterpret_cast<uint2 *>(page + off * kDqk);
+        const float inv = 1.f / c;
 #pragma unroll
-        for (int j = 0; j < 3; ++j) {
-            uint32_t code[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) code[k] = sm103::pack_e4m3x2(f[j][2 * k] / c + 0.f, f[j][2 * k + 1] / c + 0.f);
-            if (j < 2 || lane < 8) dst[lane + 32 * j] = make_uint2(code[0] | (code[1] << 16), code[2] | (code[3] << 16));
-        }
+        for (int j = 0; j < 3; ++j)
+            if (j < 2 || lane < 8) dst[lane + 32 * j] = quantise8(f[j], c, inv);
     }
 }
 
