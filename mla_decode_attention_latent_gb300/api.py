@@ -325,7 +325,7 @@ def _call(name: str, dev: torch.device, *args) -> None:
     """Run a library call on ``dev`` and its current stream; raise on a bad status."""
     fn = getattr(_lib._lib or load(), name)
     index = dev.index
-    if index == torch.cuda.current_device():
+    if index == torch._C._cuda_getDevice():  # (the device is initialised: it has the caller's tensors)
         st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(dev):
@@ -810,9 +810,7 @@ def mla_rope_turns(rope_dim: int, base: float = 10000.0, factor: float = 1.0, or
 
 
 def _weight(dev, of, weight, d):
-    """Check a norm's weight (bf16 [d]) or None; returns its address."""
-    if weight is None:
-        return None
+    """Check a norm's weight (bf16 [d]); returns its address."""
     ptr = _on(dev, of, "weight", weight, torch.bfloat16)
     if weight.dim() != 1 or weight.shape[0] != d:
         raise ValueError(f"weight must be [{d}]")
@@ -821,27 +819,31 @@ def _weight(dev, of, weight, d):
     return ptr
 
 
-def _heads(name: str, t: torch.Tensor, dev: Optional[torch.device], of: str) -> Tuple[int, int]:
-    """bf16 [n, heads, d] with unit inner stride, 16-byte aligned heads; returns the strides of a token and a head."""
+def _heads(name: str, t: torch.Tensor, dev: Optional[torch.device], of: str) -> Tuple[int, int, int]:
+    """bf16 [n, heads, d] with unit inner stride, 16-byte aligned heads; returns the strides of a token and a head,
+    and the address."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if dev is not None and t.device != dev:
-        _same_device(dev, of, **{name: t})
-    if t.dim() != 3 or t.shape[1] < 1 or t.shape[2] < 1:
+    if t.device != dev:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+        if dev is not None:
+            _same_device(dev, of, **{name: t})
+    shape = t.shape
+    if len(shape) != 3 or shape[1] < 1 or shape[2] < 1:
         raise ValueError(f"{name} must be [n, heads, d]")
-    n, h, d = t.shape
+    n, h, d = shape
     token, head, inner = t.stride()
     if h == 1:
         head = -(-d // 8) * 8
     if n <= 1:
         token = max(token, (h - 1) * head + -(-d // 8) * 8)
-    if (inner != 1 and d > 1) or token % 8 or head % 8 or t.data_ptr() % 16:
+    ptr = t.data_ptr()
+    if (inner != 1 and d > 1) or token % 8 or head % 8 or ptr % 16:
         raise ValueError(f"{name}: heads must be contiguous and 16-byte aligned, the strides multiples of 8 elements")
-    return token, head
+    return token, head, ptr
 
 
 def mla_norm_rope(x: torch.Tensor, positions: Optional[torch.Tensor], turns: Optional[torch.Tensor],
@@ -854,8 +856,9 @@ def mla_norm_rope(x: torch.Tensor, positions: Optional[torch.Tensor], turns: Opt
 
     ``x`` and ``out`` may be slices of wider heads (strides of a multiple of 8 elements).  ``out`` may be ``x``: the call
     is then in place and, without a norm, touches the rotated values only.  Returns ``out``."""
-    x_token, x_head = _heads("x", x, None, "x")
-    n, h, d = x.shape
+    x_token, x_head, x_ptr = _heads("x", x, None, "x")
+    shape = x.shape
+    n, h, d = shape
     dev = x.device
     rope_dim, pos, trn = 0, None, None
     if (positions is None) != (turns is None):
@@ -866,16 +869,16 @@ def mla_norm_rope(x: torch.Tensor, positions: Optional[torch.Tensor], turns: Opt
             raise ValueError("turns must be [rope_dim / 2]")
         rope_dim = 2 * turns.shape[0]
         pos = _vector(dev, "x", "positions", positions, n)
-    w = _weight(dev, "x", weight, d)
+    w = None if weight is None else _weight(dev, "x", weight, d)
     if out is None:
         out = torch.empty((n, h, d), dtype=torch.bfloat16, device=dev)
-    o_token, o_head = _heads("out", out, dev, "x")
-    if out.shape != x.shape:
+    o_token, o_head, o_ptr = _heads("out", out, dev, "x")
+    if out.shape != shape:
         raise ValueError("out must have the shape of x")
-    if out.data_ptr() == x.data_ptr() and (x_token, x_head) != (o_token, o_head):
+    if o_ptr == x_ptr and (x_token, x_head) != (o_token, o_head):
         raise ValueError("a call in place needs the same strides on both sides")
-    _call("mla_norm_rope", dev, x.data_ptr(), x_token, x_head, n, h, d, w, float(eps), pos, trn, rope_dim,
-          int(bool(interleaved)), float(rope_scale), out.data_ptr(), o_token, o_head)
+    _call("mla_norm_rope", dev, x_ptr, x_token, x_head, n, h, d, w, eps, pos, trn, rope_dim, 1 if interleaved else 0, rope_scale, o_ptr,
+          o_token, o_head)
     return out
 
 
@@ -904,14 +907,14 @@ def _place_rows(call, latent, k_rope, positions, turns, slots, cache, weight, ep
     elif k_rope is not None or positions is not None or turns is not None or k_rope_out is not None:
         raise ValueError("a cache of 512-wide rows has no RoPE part: k_rope, positions, turns and k_rope_out must be None")
     at = _slots(dev, "cache", slots, n)
-    w = _weight(dev, "cache", weight, MLA_V_DIM)
+    w = None if weight is None else _weight(dev, "cache", weight, MLA_V_DIM)
     lo, los, ro, ros = None, 0, None, 0
     if latent_out is not None:
         los, lo = _need_rows("latent_out", latent_out, MLA_V_DIM, n, dev, True), latent_out.data_ptr()
     if k_rope_out is not None:
         ros, ro = _need_rows("k_rope_out", k_rope_out, rope, n, dev, True), k_rope_out.data_ptr()
-    _call(call, dev, latent.data_ptr(), ls, rope_ptr, rs, n, w, float(eps), pos, trn, int(bool(interleaved)), float(rope_scale), at,
-          cache.data_ptr(), cache.shape[0], d, lo, los, ro, ros)
+    _call(call, dev, latent.data_ptr(), ls, rope_ptr, rs, n, w, eps, pos, trn, 1 if interleaved else 0, rope_scale, at, cache.data_ptr(),
+          cache.shape[0], d, lo, los, ro, ros)
 
 
 def mla_norm_rope_cache_write(latent: torch.Tensor, k_rope: Optional[torch.Tensor], positions: Optional[torch.Tensor],
@@ -989,10 +992,10 @@ def mla_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.T
     Returns (out bf16 [num_q, h_q, 128], lse fp32 [num_q, h_q]); rows that see nothing get 0 and -inf, rows of no
     sequence are left as they were (unset in outputs that the call allocates).  ``metadata`` from
     ``mla_get_metadata_prefill`` (computed when not given)."""
-    q_token, q_head = _heads("q", q, None, "q")
+    q_token, q_head, q_ptr = _heads("q", q, None, "q")
     dev = q.device
-    k_token, k_head = _heads("k", k, dev, "q")
-    v_token, v_head = _heads("v", v, dev, "q")
+    k_token, k_head, k_ptr = _heads("k", k, dev, "q")
+    v_token, v_head, v_ptr = _heads("v", v, dev, "q")
     num_q, h_q, d_qk = q.shape
     num_k, h_kv, d_k = k.shape
     rope = 0 if k_rope is None else _lib.MLA_HEAD_DIM - MLA_V_DIM
@@ -1001,10 +1004,11 @@ def mla_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.T
     rope_ptr, rope_stride = None, 0
     if k_rope is not None:
         rope_stride, rope_ptr = _need_rows("k_rope", k_rope, rope, num_k, dev, True), k_rope.data_ptr()
-    if not (isinstance(cu_q, torch.Tensor) and cu_q.numel() > 1):
-        raise ValueError("cu_q must be [b + 1], b at least 1")
+    cq = _on(dev, "q", "cu_q", cu_q, torch.int32)
     b = cu_q.numel() - 1
-    cq, ck = _vector(dev, "q", "cu_q", cu_q, b + 1), _vector(dev, "q", "cu_k", cu_k, b + 1)
+    if b < 1 or cu_q.dim() != 1:
+        raise ValueError("cu_q must be [b + 1], b at least 1")
+    ck = _vector(dev, "q", "cu_k", cu_k, b + 1)
     words, need = _prefill_sizes(dev.index, b, num_q, h_q, h_kv)
     md = None if metadata is None else _vector(dev, "q", "metadata", metadata, words)
     if softmax_scale is None:
@@ -1021,9 +1025,8 @@ def mla_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.T
     if workspace is None:
         workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
     ws_ptr = _on(dev, "q", "workspace", workspace, torch.uint8)
-    _call("mla_prefill", dev, q.data_ptr(), q_token, q_head, k.data_ptr(), k_token, k_head, v.data_ptr(), v_token, v_head,
-          rope_ptr, rope_stride, cq, ck, b, num_q, num_k, h_q, h_kv, d_qk, _HEAD, float(softmax_scale), int(bool(causal)), md, o_ptr,
-          lse_ptr, ws_ptr, workspace.numel())
+    _call("mla_prefill", dev, q_ptr, q_token, q_head, k_ptr, k_token, k_head, v_ptr, v_token, v_head, rope_ptr, rope_stride, cq, ck, b,
+          num_q, num_k, h_q, h_kv, d_qk, _HEAD, softmax_scale, 1 if causal else 0, md, o_ptr, lse_ptr, ws_ptr, workspace.numel())
     return out, lse
 
 

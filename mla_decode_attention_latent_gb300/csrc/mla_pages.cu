@@ -29,18 +29,23 @@ namespace mla {
 namespace {
 
 constexpr int kThreads = 1024;  // also the sequences of a chunk
+constexpr int kFewThreads = 128;  // of a call with few sequences and rows, whose barriers cost less
 constexpr int kMaxCtas = 8;     // portable cluster size
-constexpr int kRowsInFlight = 4;
+constexpr int kRun = 4;         // consecutive rows of a thread: one search, and mostly one page
+constexpr int kRunsInFlight = 2;
 
+template <int kThreads>
 struct AssignShared {
     long long warp[kThreads / 32];
     int cu[kThreads + 1];
     int len[kThreads];        // rows before the step; -1: not served
     long long first[kThreads];  // pages that earlier sequences need
+    int taken;                // pages taken so far
 };
 
-__global__ void __launch_bounds__(kThreads) assign_pages_kernel(const AssignPagesParams p) {
-    __shared__ AssignShared sh;
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads) assign_pages_kernel(const AssignPagesParams p, bool wide) {
+    __shared__ AssignShared<kThreads> sh;
     sm103::griddep_wait();
     const int tid = threadIdx.x, lane = tid & 31;
     const int cta = blockIdx.x, ctas = gridDim.x;  // one cluster
@@ -50,7 +55,8 @@ __global__ void __launch_bounds__(kThreads) assign_pages_kernel(const AssignPage
         left = left < 0 ? 0 : (int)p.max_free;
     }
     const long long cap = (long long)p.max_blocks * kPage;
-    long long before = 0, taken = 0;  // pages needed, pages taken, by the chunks so far
+    long long before = 0;  // pages needed by the chunks so far
+    if (tid == 0) sh.taken = 0;
     for (int c0 = 0; c0 < p.batch; c0 += kThreads) {
         const int n = min(kThreads, p.batch - c0), b = c0 + tid;
         int len = 0, count = 0, need = 0;
@@ -72,60 +78,97 @@ __global__ void __launch_bounds__(kThreads) assign_pages_kernel(const AssignPage
             sh.len[tid] = served ? len : -1;
             sh.first[tid] = first;
         }
-        long long used;
-        block_exclusive_scan<kThreads>((long long)(served ? need : 0), sh.warp, &used);  // its barriers publish the chunk
+        // those that are served of those that need any are the first ones: the last one's end
+        if (served && need > 0) atomicMax(&sh.taken, (int)(first + need));
+        __syncthreads();
         // every CTA has the chunk's lengths before one of them changes them
         sm103::cluster_arrive();
-        // new table entries: a warp per sequence
-        for (int i = cta * (kThreads / 32) + (tid >> 5); i < n; i += ctas * (kThreads / 32)) {
-            const int l = sh.len[i];
-            if (l < 0) continue;
-            const int have = pages_of(l), end = pages_of(l + sh.cu[i + 1] - sh.cu[i]);
-            for (int c = have + lane; c < end; c += 32)
-                p.block_table[(size_t)(c0 + i) * p.max_blocks + c] = p.free_pages[left - 1 - (sh.first[i] + c - have)];
+        // new table entries: a thread per page of the chunk's need
+        const long long most = min(before + total, (long long)left);
+        for (long long k = before + (long long)cta * kThreads + tid; k < most; k += (long long)ctas * kThreads) {
+            int i = 0, hi = n;  // the last i with first[i] <= k: the one that needs page k
+            while (hi - i > 1) {
+                const int mid = (i + hi) >> 1;
+                if (sh.first[mid] <= k) i = mid;
+                else hi = mid;
+            }
+            if (sh.len[i] >= 0) p.block_table[(size_t)(c0 + i) * p.max_blocks + pages_of(sh.len[i]) + (k - sh.first[i])] = p.free_pages[left - 1 - k];
         }
         // the chunk's rows (and those before the first sequence and behind the last)
         const long long r0 = c0 == 0 ? 0 : max(0, sh.cu[0]), r1 = c0 + n == p.batch ? p.num_rows : min((long long)sh.cu[n], (long long)p.num_rows);
-        const long long stride = (long long)ctas * kThreads;
-        for (long long r = r0 + (long long)cta * kThreads + tid; r < r1; r += stride * kRowsInFlight) {
-            int pos[kRowsInFlight], page[kRowsInFlight];
-            bool live[kRowsInFlight];
+        const long long stride = (long long)ctas * kThreads * kRun;
+        for (long long r = (r0 & ~(long long)(kRun - 1)) + ((long long)cta * kThreads + tid) * kRun; r < r1; r += stride * kRunsInFlight) {
+            int pos[kRunsInFlight][kRun], page[kRunsInFlight][kRun];
+            bool live[kRunsInFlight][kRun];
 #pragma unroll
-            for (int k = 0; k < kRowsInFlight; ++k) {
-                const long long row = r + k * stride;
-                int lo = 0, hi = n;  // the last i with cu[i] <= row
-                while (hi - lo > 1) {
-                    const int mid = (lo + hi) >> 1;
-                    if (sh.cu[mid] <= row) lo = mid;
+            for (int k = 0; k < kRunsInFlight; ++k) {
+                const long long row0 = r + k * stride;
+                int i = 0, hi = n;  // the last i with cu[i] <= the run's first row
+                while (hi - i > 1) {
+                    const int mid = (i + hi) >> 1;
+                    if (sh.cu[mid] <= row0) i = mid;
                     else hi = mid;
                 }
-                const int l = sh.len[lo];
-                live[k] = row < r1 && l >= 0 && row >= sh.cu[lo] && row < sh.cu[lo + 1];
-                pos[k] = live[k] ? l + (int)(row - sh.cu[lo]) : 0;
-                page[k] = 0;
-                if (live[k]) {
-                    const int c = pos[k] / kPage, have = pages_of(l);
-                    page[k] = c < have ? p.block_table[(size_t)(c0 + lo) * p.max_blocks + c]
-                                       : p.free_pages[left - 1 - (sh.first[lo] + c - have)];
+                auto page_of = [&](int at) {
+                    const int c = at / kPage, have = pages_of(sh.len[i]);
+                    return c < have ? p.block_table[(size_t)(c0 + i) * p.max_blocks + c] : p.free_pages[left - 1 - (sh.first[i] + c - have)];
+                };
+                const int first = sh.len[i] + (int)(row0 - sh.cu[i]);
+                if (sh.len[i] >= 0 && row0 >= r0 && row0 >= sh.cu[i] && row0 + kRun <= min((long long)sh.cu[i + 1], r1) && first % kPage <= kPage - kRun) {
+                    const int id = page_of(first);  // the whole run on one page of one sequence
+#pragma unroll
+                    for (int e = 0; e < kRun; ++e) {
+                        live[k][e] = true;
+                        pos[k][e] = first + e;
+                        page[k][e] = id;
+                    }
+                    continue;
+                }
+#pragma unroll
+                for (int e = 0; e < kRun; ++e) {
+                    const long long row = row0 + e;
+                    while (i + 1 < n && sh.cu[i + 1] <= row) ++i;
+                    const int l = sh.len[i];
+                    live[k][e] = row >= r0 && row < r1 && l >= 0 && row >= sh.cu[i] && row < sh.cu[i + 1];
+                    pos[k][e] = live[k][e] ? l + (int)(row - sh.cu[i]) : 0;
+                    page[k][e] = live[k][e] ? page_of(pos[k][e]) : 0;
                 }
             }
 #pragma unroll
-            for (int k = 0; k < kRowsInFlight; ++k) {
-                const long long row = r + k * stride;
-                if (row >= r1) continue;
-                if (live[k] && page[k] < 0) atomicOr(p.status, MLA_DEVERR_BLOCK_ID);
-                if (p.positions) p.positions[row] = pos[k];
-                if (p.slots) p.slots[row] = live[k] && page[k] >= 0 ? (int64_t)page[k] * kPage + pos[k] % kPage : -1;
+            for (int k = 0; k < kRunsInFlight; ++k) {
+                const long long row0 = r + k * stride;
+                if (row0 >= r1) continue;
+                int64_t slot[kRun];
+#pragma unroll
+                for (int e = 0; e < kRun; ++e) {
+                    if (live[k][e] && page[k][e] < 0) atomicOr(p.status, MLA_DEVERR_BLOCK_ID);
+                    slot[e] = live[k][e] && page[k][e] >= 0 ? (int64_t)page[k][e] * kPage + pos[k][e] % kPage : -1;
+                }
+                if (wide && row0 >= r0 && row0 + kRun <= r1) {
+                    if (p.positions) *reinterpret_cast<int4 *>(p.positions + row0) = make_int4(pos[k][0], pos[k][1], pos[k][2], pos[k][3]);
+                    if (p.slots) {
+                        longlong2 *dst = reinterpret_cast<longlong2 *>(p.slots + row0);
+                        dst[0] = make_longlong2(slot[0], slot[1]);
+                        dst[1] = make_longlong2(slot[2], slot[3]);
+                    }
+                    continue;
+                }
+#pragma unroll
+                for (int e = 0; e < kRun; ++e) {
+                    const long long row = row0 + e;
+                    if (row < r0 || row >= r1) continue;
+                    if (p.positions) p.positions[row] = pos[k][e];
+                    if (p.slots) p.slots[row] = slot[e];
+                }
             }
         }
         sm103::cluster_wait();
         if (cta == 0 && tid < n) p.new_seqlens[b] = served ? len + count : (len < 0 ? 0 : len);
         before += total;
-        taken += used;
         __syncthreads();  // the chunk in shared memory is used up
     }
     // behind the last chunk's barrier every CTA has read the count
-    if (cta == 0 && tid == 0) *p.num_free_out = (int)(left - taken);
+    if (cta == 0 && tid == 0) *p.num_free_out = left - sh.taken;
 }
 
 // Pages of finished sequences onto the stack, in the order of the sequences and
@@ -208,11 +251,13 @@ __global__ void __launch_bounds__(kThreads) release_pages_kernel(const ReleasePa
 }  // namespace
 
 cudaError_t launch_assign_pages(const AssignPagesParams &p, cudaStream_t stream) {
-    // few rows and table entries: one CTA
-    const int ctas = p.num_rows <= 2 * kThreads && p.batch <= 128 ? 1 : kMaxCtas;
+    const bool few = p.num_rows <= 4 * kFewThreads * kRun && p.batch <= kFewThreads;
+    const int ctas = few || p.num_rows <= kThreads * kRun ? 1 : kMaxCtas;
+    // whole runs are stored at once where the outputs allow it
+    const bool wide = ((reinterpret_cast<uintptr_t>(p.positions) | reinterpret_cast<uintptr_t>(p.slots)) & 15) == 0;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(few ? kFewThreads : kThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -223,7 +268,7 @@ cudaError_t launch_assign_pages(const AssignPagesParams &p, cudaStream_t stream)
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, assign_pages_kernel, p);
+    return few ? cudaLaunchKernelEx(&cfg, assign_pages_kernel<kFewThreads>, p, wide) : cudaLaunchKernelEx(&cfg, assign_pages_kernel<kThreads>, p, wide);
 }
 
 cudaError_t launch_release_pages(const ReleasePagesParams &p, cudaStream_t stream) {
