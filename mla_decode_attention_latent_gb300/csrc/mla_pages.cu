@@ -109,21 +109,7 @@ __global__ void __launch_bounds__(kThreads) assign_pages_kernel(const AssignPage
                     if (sh.cu[mid] <= row0) i = mid;
                     else hi = mid;
                 }
-                auto page_of = [&](int at) {
-                    const int c = at / kPage, have = pages_of(sh.len[i]);
-                    return c < have ? p.block_table[(size_t)(c0 + i) * p.max_blocks + c] : p.free_pages[left - 1 - (sh.first[i] + c - have)];
-                };
-                const int first = sh.len[i] + (int)(row0 - sh.cu[i]);
-                if (sh.len[i] >= 0 && row0 >= r0 && row0 >= sh.cu[i] && row0 + kRun <= min((long long)sh.cu[i + 1], r1) && first % kPage <= kPage - kRun) {
-                    const int id = page_of(first);  // the whole run on one page of one sequence
-#pragma unroll
-                    for (int e = 0; e < kRun; ++e) {
-                        live[k][e] = true;
-                        pos[k][e] = first + e;
-                        page[k][e] = id;
-                    }
-                    continue;
-                }
+                const int32_t *from[kRun];
 #pragma unroll
                 for (int e = 0; e < kRun; ++e) {
                     const long long row = row0 + e;
@@ -131,8 +117,12 @@ __global__ void __launch_bounds__(kThreads) assign_pages_kernel(const AssignPage
                     const int l = sh.len[i];
                     live[k][e] = row >= r0 && row < r1 && l >= 0 && row >= sh.cu[i] && row < sh.cu[i + 1];
                     pos[k][e] = live[k][e] ? l + (int)(row - sh.cu[i]) : 0;
-                    page[k][e] = live[k][e] ? page_of(pos[k][e]) : 0;
+                    const int c = pos[k][e] / kPage, have = pages_of(l);
+                    from[e] = !live[k][e] ? p.num_free  // (any word that can be read)
+                              : c < have ? p.block_table + (size_t)(c0 + i) * p.max_blocks + c : p.free_pages + (left - 1 - (sh.first[i] + c - have));
                 }
+#pragma unroll
+                for (int e = 0; e < kRun; ++e) page[k][e] = *from[e];  // together under way
             }
 #pragma unroll
             for (int k = 0; k < kRunsInFlight; ++k) {
