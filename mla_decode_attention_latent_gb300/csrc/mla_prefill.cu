@@ -495,6 +495,12 @@ struct State {
 // halves stays within the instruction cache.
 __device__ __noinline__ State careful_half(const Half x, float scale_log2, uint64_t *products, uint32_t parity, unsigned int *status) {
     uint32_t a[32], b[32], w[32];
+    if (!x.first && !__any_sync(0xffffffffu, x.left > 0)) {  // nothing in sight of the warp's rows
+#pragma unroll
+        for (int i = 0; i < 32; ++i) w[i] = 0;
+        tmem_st32(x.p_col, w);
+        return {x.m, x.l, 1};
+    }
     tmem_ld32(x.s_col, a);
     tmem_ld32(x.s_col + 32, b);
     arrived(a, b);
@@ -503,14 +509,13 @@ __device__ __noinline__ State careful_half(const Half x, float scale_log2, uint6
         a[i] = i < x.left ? a[i] : 0xff800000u;
         b[i] = i + 32 < x.left ? b[i] : 0xff800000u;
     }
-    const float top = largest(a, b);
-    float m = x.first ? top : x.m, l = x.l, sum = 0.f;
+    float m = x.first ? largest(a, b) : x.m, l = x.l, sum = 0.f;
 #pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
         sum = weigh(a, b, m, scale_log2, w);
         const bool raise = !(sum <= kMostWeight) || (m == -INFINITY && x.left > 0);
         if (pass || !__any_sync(0xffffffffu, raise)) break;
-        const float m_new = raise ? fmaxf(m, top) : m;
+        const float m_new = raise ? fmaxf(m, largest(a, b)) : m;
         const float f = !raise ? 1.f : m == -INFINITY ? 0.f : exp2_fast((m - m_new) * scale_log2);
         if (products) {
             // every product so far is in O
@@ -601,33 +606,37 @@ __device__ void row_role(const PrefillParams &p, const Ctx &c, uint32_t tmem, in
         if (!__all_sync(0xffffffffu, c.wait(B_PV + t, (phase - 1) & 1))) return;
         tc_fence_after();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t o[32];
-            tmem_ld32(o_col + 32 * i, o);
-            tmem_wait_ld();
-            if (i == 3) {
+        for (int i2 = 0; i2 < 2; ++i2) {
+            uint32_t both[2][32];
+            tmem_ld32(o_col + 64 * i2, both[0]);
+            tmem_ld32(o_col + 64 * i2 + 32, both[1]);
+            arrived(both[0], both[1]);
+            if (i2 == 1) {
                 tc_fence_before();
                 mbar_arrive(c.bar(B_OFREE + t));
             }
             if (!on) continue;
-            if (s.slot < 0) {
-                // (a lane writes its own row: turned among four lanes, so that a store touches 8 lines
-                // instead of 32, prompts of 300 rows took 95.6 us for 87.8)
-                uint4 *dst = reinterpret_cast<uint4 *>(p.out + row * kPreHead + 32 * i);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    uint32_t w[4];
+            for (int i1 = 0; i1 < 2; ++i1) {
+                const int i = 2 * i2 + i1;
+                uint32_t (&o)[32] = both[i1];
+                if (s.slot < 0) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(p.out + row * kPreHead + 32 * i);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        w[e] = pack_bf16(__uint_as_float(o[8 * k + 2 * e]) * inv, __uint_as_float(o[8 * k + 2 * e + 1]) * inv);
-                    dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            w[e] = pack_bf16(__uint_as_float(o[8 * k + 2 * e]) * inv, __uint_as_float(o[8 * k + 2 * e + 1]) * inv);
+                        dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        reinterpret_cast<float4 *>(p.o_part)[part_at(s.slot, 8 * i + k, t * kPreTile + r)] =
+                            make_float4(__uint_as_float(o[4 * k]) * inv, __uint_as_float(o[4 * k + 1]) * inv, __uint_as_float(o[4 * k + 2]) * inv,
+                                        __uint_as_float(o[4 * k + 3]) * inv);
                 }
-            } else {
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    reinterpret_cast<float4 *>(p.o_part)[part_at(s.slot, 8 * i + k, t * kPreTile + r)] =
-                        make_float4(__uint_as_float(o[4 * k]) * inv, __uint_as_float(o[4 * k + 1]) * inv, __uint_as_float(o[4 * k + 2]) * inv,
-                                    __uint_as_float(o[4 * k + 3]) * inv);
             }
         }
     }
