@@ -202,7 +202,7 @@ struct PrefillParams {
     float *lse;                   // [num_q][h_q]
     int32_t *metadata;            // the partition (mla_prefill.cuh)
     int64_t max_blocks;
-    float *o_part;                // [2 sms][256][128] fp32: a CTA's first and last item may be cut
+    float *o_part;                // [2 sms] slots of 128 x 256 rows, fp32: partial results of cut blocks
     float *lse_part;              // [2 sms][256]
     int sms;                      // CTAs
     int head_chunk;               // key heads that run side by side

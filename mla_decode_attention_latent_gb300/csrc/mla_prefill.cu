@@ -80,71 +80,42 @@ struct Ctx {
     __device__ bool wait(int i, uint32_t parity) const { return mbar_wait(bars + i, parity, status); }
 };
 
-// A part of an item: steps step0 .. step1 of a block, for one key head.
-struct Segment : PreBlock {
-    int step0, step1;
-    int slot;           // of the partial results; -1: the whole item
-};
+// The items (segment, key head) of a CTA.  The segment of the next one is fetched while the
+// current one runs.
+using Segment = PreSegment;
 
-// The segments of a CTA: its items of every round, or its share of the line
-// (mla_prefill_schedule.cu).
-// The block of the next one is fetched while the current one runs.
 struct Walk {
     PreWork work;
-    int blocks, round = 0;
-    bool line, more;
-    PrePlace at, end;
+    int segments, round = 0;
+    bool more;
     Segment ahead;
     int ahead_head;
     __device__ Walk(const PrefillParams &p) : work(p.metadata, p.max_blocks, p.sms) {
-        blocks = (int)min((long long)max(0, work.header->blocks), (long long)p.max_blocks);
-        line = work.header->line != 0;
-        if (line) {
-            at = work.places[blockIdx.x];
-            end = work.places[blockIdx.x + 1];
-        }
+        segments = (int)min((long long)max(0, work.header->segments), (long long)pre_max_segments(p.max_blocks, p.sms));
         fetch(p);
     }
     __device__ __forceinline__ void fetch(const PrefillParams &p) {
-        int block, step1 = 0x7fffffff;
-        ahead.step0 = 0;
-        more = false;
-        if (line) {
-            block = at.block, ahead_head = at.head, ahead.step0 = at.step;
-            const bool last = block == end.block && ahead_head == end.head;
-            if (block > end.block || (block == end.block && (ahead_head > end.head || (last && at.step >= end.step)))) return;
-            if (block < 0 || block >= blocks || ahead_head < 0 || ahead_head >= p.h_kv) return;
-            if (last) {
-                step1 = end.step;
-                at = end;
-            } else {
-                at = {block + (ahead_head + 1 == p.h_kv), ahead_head + 1 == p.h_kv ? 0 : ahead_head + 1, 0, 0};
-            }
-        } else if (!pre_round_item(round, blockIdx.x, gridDim.x, blocks, p.h_kv, p.head_chunk, block, ahead_head)) {
-            return;
-        }
-        more = true;
-        const int4 *src = reinterpret_cast<const int4 *>(work.blocks + block);
+        int segment;
+        more = pre_round_item(round, blockIdx.x, gridDim.x, segments, p.h_kv, p.head_chunk, segment, ahead_head);
+        if (!more) return;
+        const int4 *src = reinterpret_cast<const int4 *>(work.segments + segment);
         const int4 u = src[0], v = src[1];
-        ahead.q0 = u.x, ahead.tokens = u.y, ahead.k0 = u.z, ahead.keys = u.w, ahead.seen = v.x, ahead.steps = v.y;
-        ahead.step1 = step1;
+        ahead = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
         ++round;
     }
     __device__ __forceinline__ bool next(const PrefillParams &p, Segment &s, int &head) {
         if (!more) return false;
         s = ahead;
         head = ahead_head;
-        s.step1 = min(s.step1, s.steps);
-        // the first of a line's segments and the last may be parts
-        s.slot = s.step0 > 0 || s.step1 < s.steps ? 2 * (int)blockIdx.x + (round > 1) : -1;
         fetch(p);
         // a partition of other lengths must not make the kernel leave its tensors
         const int most = kPreTiles * pre_tile_tokens(p.group);
         if (s.q0 < 0 || s.tokens < 0 || s.tokens > most || (int64_t)s.q0 + s.tokens > p.num_q || s.keys < 0 || s.k0 < 0 ||
-            (int64_t)s.k0 + s.keys > p.num_k || s.step0 < 0 || s.step1 > pre_steps(s.keys)) {
+            (int64_t)s.k0 + s.keys > p.num_k || s.step0 < 0 || s.step1 > pre_steps(s.keys) ||
+            (s.part >= 0 && ((int64_t)s.part + 1) * p.h_kv > pre_slots(p.sms))) {
             if ((threadIdx.x & 31) == 0) atomicOr(p.status, MLA_DEVERR_SEQLEN);
             s.tokens = s.step0 = s.step1 = 0;
-            s.slot = -1;
+            s.part = -1;
         }
         return true;
     }
@@ -594,12 +565,13 @@ __device__ void row_role(const PrefillParams &p, const Ctx &c, uint32_t tmem, in
         float lse = l == 0.f ? -INFINITY : m * p.scale + logf(l);
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const int64_t row = (int64_t)(s.q0 + token) * p.h_q + head * p.group + hh;
+        const int64_t slot = (int64_t)s.part * p.h_kv + head;
         if (on) {
-            if (s.slot < 0) p.lse[row] = lse;
-            else p.lse_part[(int64_t)s.slot * kPreRows + t * kPreTile + r] = lse;
+            if (s.part < 0) p.lse[row] = lse;
+            else p.lse_part[slot * kPreRows + t * kPreTile + r] = lse;
         }
         if (tile.steps == 0) {
-            if (on && s.slot < 0)
+            if (on && s.part < 0)
                 for (int i = 0; i < kPreHead / 8; ++i) reinterpret_cast<uint4 *>(p.out + row * kPreHead)[i] = make_uint4(0, 0, 0, 0);
             continue;
         }
@@ -620,7 +592,7 @@ __device__ void row_role(const PrefillParams &p, const Ctx &c, uint32_t tmem, in
             for (int i1 = 0; i1 < 2; ++i1) {
                 const int i = 2 * i2 + i1;
                 uint32_t (&o)[32] = both[i1];
-                if (s.slot < 0) {
+                if (s.part < 0) {
                     uint4 *dst = reinterpret_cast<uint4 *>(p.out + row * kPreHead + 32 * i);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
@@ -633,7 +605,7 @@ __device__ void row_role(const PrefillParams &p, const Ctx &c, uint32_t tmem, in
                 } else {
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        reinterpret_cast<float4 *>(p.o_part)[part_at(s.slot, 8 * i + k, t * kPreTile + r)] =
+                        reinterpret_cast<float4 *>(p.o_part)[part_at(slot, 8 * i + k, t * kPreTile + r)] =
                             make_float4(__uint_as_float(o[4 * k]) * inv, __uint_as_float(o[4 * k + 1]) * inv, __uint_as_float(o[4 * k + 2]) * inv,
                                         __uint_as_float(o[4 * k + 3]) * inv);
                 }
@@ -718,46 +690,47 @@ prefill_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
 // ---------------------------------------------------------------- combine of cut items
 // A warp per 32 rows of an item and 16 of the dims, a lane per row (the partial results'
 // order): o = sum_s w_s o_s, w_s = exp(lse_s - lse).  A part in which the row saw
-// nothing (lse -inf) was not written and is not read.
-constexpr int kCombineWarps = 8, kCombineDims = 16;
+// nothing (lse -inf) was not written and does not count.
+constexpr int kCombineWarps = 4, kCombineDims = 16;
 
 __global__ void __launch_bounds__(kCombineWarps * 32) prefill_combine_kernel(const __grid_constant__ PrefillParams p) {
     griddep_wait();
     const PreWork work(p.metadata, p.max_blocks, p.sms);
     const int lane = threadIdx.x & 31, per = pre_tile_tokens(p.group);
     constexpr int kUnits = kPreRows / 32 * (kPreHead / kCombineDims);  // of an item
-    const int n = work.header->line ? min(work.header->cuts, p.sms) : 0;
-    const int total = n * kUnits, stride = gridDim.x * kCombineWarps;
-    for (int i = blockIdx.x * kCombineWarps + (threadIdx.x >> 5); i < total; i += stride) {
-        const PreCut cut = work.cuts[i / kUnits];
-        if (cut.block < 0 || cut.block >= p.max_blocks || cut.slot0 < 0 || cut.slot0 >= pre_slots(p.sms) || cut.cta < 1 ||
-            cut.count < 1 || cut.cta + cut.count - 1 > p.sms)
-            continue;
-        const PreBlock block = work.blocks[cut.block];
-        const int unit = i % kUnits, r = unit % (kPreRows / 32) * 32 + lane, c0 = unit / (kPreRows / 32) * (kCombineDims / 4);
+    const int n = max(0, min(work.header->cuts, pre_slots(p.sms)));
+    const int64_t total = (int64_t)n * p.h_kv * kUnits, stride = gridDim.x * kCombineWarps;
+    for (int64_t i = (int64_t)blockIdx.x * kCombineWarps + (threadIdx.x >> 5); i < total; i += stride) {
+        const int unit = (int)(i % kUnits), head = (int)(i / kUnits % p.h_kv);
+        const PreCut cut = work.cuts[i / kUnits / p.h_kv];
+        if (cut.part < 0 || cut.count < 1 || ((int64_t)cut.part + cut.count) * p.h_kv > pre_slots(p.sms)) continue;
+        const int r = unit % (kPreRows / 32) * 32 + lane, c0 = unit / (kPreRows / 32) * (kCombineDims / 4);
         const int t = r / kPreTile, in_tile = (r % kPreTile) / p.group, hh = (r % kPreTile) - in_tile * p.group, token = t * per + in_tile;
-        if (in_tile >= per || token >= block.tokens || block.q0 < 0 || (int64_t)block.q0 + token >= p.num_q) continue;
-        auto slot = [&](int k) { return k ? 2 * (cut.cta + k - 1) : cut.slot0; };
+        if (in_tile >= per || token >= cut.tokens || cut.q0 < 0 || (int64_t)cut.q0 + token >= p.num_q) continue;
+        const int64_t slot0 = (int64_t)cut.part * p.h_kv + head;
         float top = -INFINITY;
-        for (int k = 0; k < cut.count; ++k) top = fmaxf(top, p.lse_part[(int64_t)slot(k) * kPreRows + r]);
+#pragma unroll 4
+        for (int k = 0; k < cut.count; ++k) top = fmaxf(top, p.lse_part[(slot0 + (int64_t)k * p.h_kv) * kPreRows + r]);
         const float base = top == -INFINITY ? 0.f : top;
         float sum = 0.f, o[kCombineDims] = {};
+#pragma unroll 2
         for (int k = 0; k < cut.count; ++k) {
-            const float lse = p.lse_part[(int64_t)slot(k) * kPreRows + r];
-            if (lse == -INFINITY) continue;
+            const int64_t slot = slot0 + (int64_t)k * p.h_kv;
+            const float lse = p.lse_part[slot * kPreRows + r];
             const float w = exp2_fast((lse - base) * 1.4426950408889634f);
+            const bool none = lse == -INFINITY;
             sum += w;
 #pragma unroll
             for (int c = 0; c < kCombineDims / 4; ++c) {
-                const float4 x = reinterpret_cast<const float4 *>(p.o_part)[part_at(slot(k), c0 + c, r)];
-                o[4 * c] = fmaf(w, x.x, o[4 * c]);
-                o[4 * c + 1] = fmaf(w, x.y, o[4 * c + 1]);
-                o[4 * c + 2] = fmaf(w, x.z, o[4 * c + 2]);
-                o[4 * c + 3] = fmaf(w, x.w, o[4 * c + 3]);
+                const float4 x = reinterpret_cast<const float4 *>(p.o_part)[part_at(slot, c0 + c, r)];
+                o[4 * c] = none ? o[4 * c] : fmaf(w, x.x, o[4 * c]);
+                o[4 * c + 1] = none ? o[4 * c + 1] : fmaf(w, x.y, o[4 * c + 1]);
+                o[4 * c + 2] = none ? o[4 * c + 2] : fmaf(w, x.z, o[4 * c + 2]);
+                o[4 * c + 3] = none ? o[4 * c + 3] : fmaf(w, x.w, o[4 * c + 3]);
             }
         }
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const int64_t row = (int64_t)(block.q0 + token) * p.h_q + cut.head * p.group + hh;
+        const int64_t row = (int64_t)(cut.q0 + token) * p.h_q + head * p.group + hh;
         uint32_t w[kCombineDims / 2];
 #pragma unroll
         for (int k = 0; k < kCombineDims / 2; ++k) w[k] = pack_bf16(o[2 * k] * inv, o[2 * k + 1] * inv);
@@ -824,11 +797,10 @@ cudaError_t launch(const PrefillParams &p, cudaStream_t stream) {
         mr = mk;
         if (kRope && !make_map(&mr, p.k_rope, kPreRope, 1, p.num_k, kPreRope, p.k_rope_token, 1, kPreTile)) return cudaErrorInvalidValue;
     }
-    // (a CTA per SM: the line counts on them; in rounds the last may have no item)
     e = launch_after(prefill_kernel<kRope>, dim3(p.sms), dim3(kThreads), Layout<kRope>::kBytes, stream, mq, mk, mr, mv, p);
     if (e != cudaSuccess) return e;
-    if (!pre_line(p.max_blocks, p.h_kv, p.sms)) return cudaSuccess;
-    return launch_after(prefill_combine_kernel, dim3(2 * p.sms), dim3(kCombineWarps * 32), 0, stream, p);
+    if (!pre_may_cut(p.max_blocks, p.h_kv, p.sms)) return cudaSuccess;
+    return launch_after(prefill_combine_kernel, dim3(4 * p.sms), dim3(kCombineWarps * 32), 0, stream, p);
 }
 
 }  // namespace

@@ -1,25 +1,32 @@
 // Partition of a prompt attention: packed sequences into blocks of query tokens,
-// longest first, and the items (block, key head) onto the CTAs.
+// longest first, and some of them into parts.
 //
 // A block is up to 256 query rows of one sequence and one key head: t =
 // floor(128 / group) tokens per 128-row tile, with `group` query heads each, and
 // two tiles.  It walks ceil(seen / 128) steps of 128 keys, `seen` being what its
-// last token sees.  Two ways to share the items, of which the one is taken that is
-// estimated to end first (the line where it gains an eighth: 512 equal items of 152 CTAs
-// lose 7 % on it):
-//   rounds  whole items, in rounds over the CTAs (pre_round_item)
-//   line    the items one behind the other, each taking F + steps units (F: its fixed
-//           cost), cut into equal shares; a unit inside an item's first F moves to its
-//           start.  Items that a share ends in are cut along their keys, and the
-//           combine (cost C) joins the partial results
-// Rounds suit many items: nothing is cut and the heads of a moment are few.  The line
-// suits few rows over many keys, and counts that leave most CTAs idle in a last round.
+// last token sees.
 //
-// One CTA.  The bounds of up to 1024 sequences sit in shared memory, and the blocks
-// are gone through twice (how many have each length; their places, a counting sort).
-// Where the line may be taken the sort is stable, so that the same call always cuts the
-// same items; in rounds the order of equal blocks has no influence on a result.
+// The items (segment, key head) go to the CTAs in rounds, longest first
+// (pre_round_item).  A segment is a block, or a part of one: blocks of more than c
+// steps are cut into ceil(steps / c) equal parts, whose partial results the combine
+// joins.  32 values of c around an even share of the work are tried, and none: with n
+// items of F + steps units each (F: an item's fixed cost), the last CTA is estimated to
+// end at the larger of an even share of all units and, for the ceil(n / ctas) rounds,
+// the longest item and a shortest one for every further round; a cut costs C for the
+// combine, and has to gain an eighth.  So few rows over many keys fill the GPU, and a
+// batch of prompts with many heads is not cut at all.  All heads of a part are
+// side by side, over the same keys: cut apart from each other (a line of all items in
+// equal shares), heads whose keys are neighbours in memory read them at different
+// times, and a step of three chunks behind long contexts took 3.2 us instead of 2.0.
+//
+// One CTA.  Up to 1280 blocks, as many as there are where any is cut, are kept in shared
+// memory and sorted by counting, for each segment, those before it, which is stable: the
+// same call always cuts the same blocks.  More blocks are gone through twice (how many
+// have each length; their places), in an order of equal ones that has no influence on
+// a result.
 #include <cuda_runtime.h>
+
+#include <mutex>
 
 #include "mla_prefill.cuh"
 #include "mla_schedule.cuh"
@@ -28,40 +35,43 @@
 namespace mla {
 namespace {
 
-constexpr int kThreads = 1024;
-constexpr int kFixed = 2;        // units of an item beside its steps
+constexpr int kFixed = 8;        // units of an item beside its steps (2 / 4 / 8: three chunks 86 / 86 / 83 us)
 constexpr int kCombine = 3;      // units of the combine
-constexpr int kLeastShare = 6;   // units of a share on the line
-constexpr int kLengths = 1024;   // lengths that the sort tells apart
-constexpr int kStable = 1280;    // blocks that are sorted stably: as many as a line can have, and more
+constexpr int kLeastPart = 4;    // steps of a part
+constexpr int kLengths = 1024;   // lengths that the counting sort tells apart
+constexpr int kStable = 1280;    // blocks or segments that are sorted stably: as many as there are where any is cut
+constexpr int kMany = 1024, kFew = 256;  // threads; few: for as many sequences and blocks, whose barriers cost less
 
+template <int kThreads>
 struct Shared {
     long long warp[kThreads / 32];
     long long end[kThreads];     // blocks up to and with each sequence of the chunk
     int q[kThreads], lq[kThreads], k[kThreads], lk[kThreads];
-    int count[kLengths];         // blocks of each length; then their first place
+    int count[kThreads == kMany ? kLengths : 1];  // blocks of each length; then their first place
     int scan[kThreads / 32];
-    int longest, cuts;
-    PrePlace place[kThreads / 4 + 1];
-    short bucket[kStable];       // of each block
-    long long units[kStable + 1];  // on the line before each block
+    unsigned long long steps;    // of all blocks
+    int cost[32];                // estimates of the values of c
+    int cuts, parts;
+    PreSegment block[kStable];
+    int first[kStable];          // segments before each block
+    int length[kStable];         // of each segment
 };
 
-// f(block, its index) for every block, the threads sharing the blocks of 1024 sequences at a time
-template <typename F>
-__device__ void each_block(const PrefillParams &p, Shared &sh, bool report, F f) {
+// f(block, its index) for every block, the threads sharing the blocks of kThreads sequences at a time; their number
+template <int kThreads, typename F>
+__device__ long long each_block(const PrefillParams &p, Shared<kThreads> &sh, bool again, F f) {
     const int per = kPreTiles * pre_tile_tokens(p.group);
     long long base = 0;
     for (int c0 = 0; c0 < p.batch; c0 += kThreads) {
         const int n = min(kThreads, p.batch - c0), b = c0 + threadIdx.x;
         // the bounds stay in shared memory where one chunk holds all sequences
-        if (report || p.batch > kThreads) {
+        if (!again || p.batch > kThreads) {
             int q = 0, lq = 0, k = 0, lk = 0;
             if ((int)threadIdx.x < n) {
                 q = p.cu_q[b], k = p.cu_k[b];
                 const int q1 = p.cu_q[b + 1], k1 = p.cu_k[b + 1];
                 if (q < 0 || q1 < q || q1 > p.num_q || k < 0 || k1 < k || k1 > p.num_k) {
-                    if (report) atomicOr(p.status, MLA_DEVERR_SEQLEN);
+                    if (!again) atomicOr(p.status, MLA_DEVERR_SEQLEN);
                     q = k = 0;
                 } else {
                     lq = q1 - q, lk = k1 - k;
@@ -82,132 +92,185 @@ __device__ void each_block(const PrefillParams &p, Shared &sh, bool report, F f)
                 else lo = mid + 1;
             }
             const int first = (int)(i - (lo ? sh.end[lo - 1] : 0)) * per;
-            PreBlock x;
+            PreSegment x;
             x.q0 = sh.q[lo] + first;
             x.tokens = min(per, sh.lq[lo] - first);
             x.k0 = sh.k[lo];
             x.keys = sh.lk[lo];
             x.seen = p.causal ? sh.lk[lo] - sh.lq[lo] + first + 1 : sh.lk[lo];
-            x.steps = pre_steps(pre_seen(x, x.tokens - 1));
-            x.pad[0] = x.pad[1] = 0;
+            x.step0 = 0;
+            x.step1 = pre_steps(pre_seen(x, x.tokens - 1));
+            x.part = -1;
             f(x, base + i);
         }
         base += sh.end[n - 1];
         __syncthreads();
     }
+    return base;
 }
 
+// parts of a block of `steps` for c = most; the first `longer` of them have one step more than the others
+__device__ __forceinline__ int cut(int steps, int most, int &shorter, int &longer) {
+    const int n = steps > most ? (int)(((unsigned)steps + most - 1) / (unsigned)most) : 1;
+    shorter = (int)((unsigned)steps / (unsigned)n);
+    longer = steps - shorter * n;
+    return n;
+}
+
+template <int kThreads>
 __global__ void __launch_bounds__(kThreads) prefill_schedule_kernel(const PrefillParams p) {
-    __shared__ Shared sh;
-    static_assert(kStable >= kPreRounds * 160 && kThreads / 4 >= 160, "multiprocessors");
+    extern __shared__ __align__(16) char raw[];
+    Shared<kThreads> &sh = *reinterpret_cast<Shared<kThreads> *>(raw);
     if (threadIdx.x == 0) sm103::griddep_launch_dependents();
     sm103::griddep_wait();
     const PreWork work(p.metadata, p.max_blocks, p.sms);
-    for (int i = threadIdx.x; i < kLengths; i += kThreads) sh.count[i] = 0;
-    if (threadIdx.x == 0) sh.longest = sh.cuts = 0;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if constexpr (kThreads == kMany) sh.count[threadIdx.x] = 0;
+    if (threadIdx.x == 0) {
+        sh.cuts = sh.parts = 0;
+        sh.steps = 0;
+    }
     __syncthreads();
     // most steps first: bucket 0 holds the longest
     auto bucket = [](int steps) { return kLengths - 1 - min(steps, kLengths - 1); };
-    long long steps = 0;
-    each_block(p, sh, true, [&](const PreBlock &x, long long i) {
-        atomicAdd(&sh.count[bucket(x.steps)], 1);
-        if (i < kStable) sh.bucket[i] = (short)bucket(x.steps);
-        steps += x.steps;
+    unsigned long long steps = 0;
+    const long long found = each_block(p, sh, false, [&](const PreSegment &x, long long i) {
+        if (i < kStable) sh.block[i] = x;
+        if constexpr (kThreads == kMany) atomicAdd(&sh.count[bucket(x.step1)], 1);
+        steps += x.step1;
     });
-    int blocks;
-    {
+    const int blocks = (int)min(found, (long long)p.max_blocks);
+    if (kThreads == kMany && blocks > kStable) {
+        int total;
         const int here = sh.count[threadIdx.x];
-        const int first = block_exclusive_scan<kThreads>(here, sh.scan, &blocks);
-        sh.count[threadIdx.x] = first;
-        blocks = (int)min((long long)blocks, (long long)p.max_blocks);
-    }
-    long long all;
-    block_exclusive_scan<kThreads>(steps, sh.warp, &all);  // its barriers publish the places
-    const bool stable = blocks <= kStable;
-    each_block(p, sh, false, [&](const PreBlock &x, long long i) {
-        const int mine = bucket(x.steps);
-        int at;
-        if (stable) {
-            at = sh.count[mine];
-            for (int k = 0; k < i; ++k) at += sh.bucket[k] == mine;
-        } else {
-            at = atomicAdd(&sh.count[mine], 1);
+        sh.count[threadIdx.x] = block_exclusive_scan<kThreads>(here, sh.scan, &total);
+        __syncthreads();
+        each_block(p, sh, true, [&](const PreSegment &x, long long i) {
+            const int at = atomicAdd(&sh.count[bucket(x.step1)], 1);
+            if (at < blocks) work.segments[at] = x;
+        });
+        if (threadIdx.x == 0) {
+            work.header->segments = blocks;
+            work.header->cuts = 0;
         }
-        if (at < blocks) work.blocks[at] = x;
-    });
-    __syncthreads();
-    // when the last CTA ends, in units
-    const long long items = (long long)blocks * p.h_kv, units = (all + (long long)kFixed * blocks) * p.h_kv;
-    const long long share = max((units + p.sms - 1) / p.sms, (long long)kLeastShare);
-    bool line = false;
-    if (items > 0 && pre_line(p.max_blocks, p.h_kv, p.sms)) {
-        if ((int)threadIdx.x < p.sms) {
-            long long mine = 0;
-            int block, head;
-            for (int round = 0; pre_round_item(round, threadIdx.x, p.sms, blocks, p.h_kv, p.head_chunk, block, head); ++round)
-                mine += kFixed + work.blocks[block].steps;
-            atomicMax(&sh.longest, (int)min(mine, 0x7fffffffll));
+        return;
+    }
+    int most = 0x7fffffff;  // c
+    if (blocks > 0 && pre_may_cut(p.max_blocks, p.h_kv, p.sms) && kPreRounds * p.sms <= kStable) {
+        if (steps) atomicAdd(&sh.steps, steps);
+        __syncthreads();
+        // values of c, one per warp at a time: the last none, the others from a quarter to four times an even share
+        const float share = (float)sh.steps * p.h_kv / p.sms;
+        auto value = [&](int w) { return w == 31 ? 0x7fffffff : max(kLeastPart, (int)ceilf(fminf(share * exp2f((float)w * (4.f / 30.f) - 2.f), 1e9f))); };
+        for (int w = warp; w < 32; w += kThreads / 32) {
+            const int c = value(w);
+            int n = 0, parts = 0, longest = 0, shortest = 0x7fffffff;
+            float units = 0.f;
+            for (int i = lane; i < blocks; i += 32) {
+                int shorter, longer;
+                const int all = sh.block[i].step1, mine = cut(all, c, shorter, longer);
+                n += mine;
+                parts += mine > 1 ? mine : 0;
+                units += (float)all;
+                longest = max(longest, shorter + (longer > 0));
+                shortest = min(shortest, shorter);
+            }
+#pragma unroll
+            for (int off = 16; off; off >>= 1) units += __shfl_xor_sync(0xffffffffu, units, off);
+            n = __reduce_add_sync(0xffffffffu, n);  // (at most 1280 blocks of 2^23 steps, in parts of 4 or more: below 2^31)
+            parts = __reduce_add_sync(0xffffffffu, parts);
+            longest = __reduce_max_sync(0xffffffffu, longest);
+            shortest = __reduce_min_sync(0xffffffffu, shortest);
+            const long long items = (long long)n * p.h_kv;
+            const bool fits = items <= (long long)kPreRounds * p.sms && (long long)parts * p.h_kv <= pre_slots(p.sms);
+            const float rounds = fits || c == 0x7fffffff ? ceilf((float)items / p.sms) : 0.f;
+            const float even = (units + (float)kFixed * n) * p.h_kv / p.sms;
+            const float end = fmaxf(even, longest + kFixed + (rounds - 1.f) * (shortest + kFixed)) + (parts ? kCombine : 0);
+            if (lane == 0) sh.cost[w] = fits || c == 0x7fffffff ? (int)fminf(end, 5e7f) : 60000000;
         }
         __syncthreads();
-        line = (share + kFixed + kCombine) * 8 < (long long)sh.longest * 7;
+        // the least of them, and whether it gains an eighth on not cutting
+        const unsigned mine = (unsigned)sh.cost[lane] * 32 + lane, least = __reduce_min_sync(0xffffffffu, mine);
+        if ((long long)(least / 32) * 8 < (long long)sh.cost[31] * 7) most = value(least % 32);
+    }
+    // segments: where each block's begin, and their lengths
+    int segments = 0;
+    for (int c0 = 0; c0 < blocks; c0 += kThreads) {
+        const int i = c0 + threadIdx.x;
+        int shorter = 0, longer = 0, n = 0;
+        if (i < blocks) n = cut(sh.block[i].step1, most, shorter, longer);
+        int total;
+        const int first = segments + block_exclusive_scan<kThreads>(n, sh.scan, &total);
+        if (i < blocks) sh.first[i] = first;
+        if (n == 1) sh.length[first] = shorter;
+        if (n > 1) {
+            const int part = atomicAdd(&sh.parts, n);  // (which slots a block has makes no difference)
+            sh.block[i].part = part;
+            work.cuts[atomicAdd(&sh.cuts, 1)] = {sh.block[i].q0, sh.block[i].tokens, part, n};
+        }
+        segments += total;
+    }
+    __syncthreads();
+    // a thread per segment: its block, its part of it, its place among all by length
+    for (int at = threadIdx.x; at < segments; at += kThreads) {
+        int i = 0, hi = blocks;  // first[i] <= at < first[i + 1]
+        while (hi - i > 1) {
+            const int mid = (i + hi) >> 1;
+            if (sh.first[mid] <= at) i = mid;
+            else hi = mid;
+        }
+        int shorter, longer;
+        cut(sh.block[i].step1, most, shorter, longer);
+        sh.length[at] = shorter + (at - sh.first[i] < longer);
+    }
+    __syncthreads();
+    for (int at = threadIdx.x; at < segments; at += kThreads) {
+        int i = 0, hi = blocks;
+        while (hi - i > 1) {
+            const int mid = (i + hi) >> 1;
+            if (sh.first[mid] <= at) i = mid;
+            else hi = mid;
+        }
+        int shorter, longer;
+        const int n = cut(sh.block[i].step1, most, shorter, longer), k = at - sh.first[i], mine = sh.length[at];
+        int rank = 0;
+        for (int other = 0; other < segments; ++other) rank += sh.length[other] + (other < at) > mine;
+        PreSegment x = sh.block[i];
+        x.step0 = k * shorter + min(k, longer);
+        x.step1 = x.step0 + mine;
+        x.part = n > 1 ? x.part + k : -1;
+        work.segments[rank] = x;
     }
     if (threadIdx.x == 0) {
-        work.header->blocks = blocks;
-        work.header->line = line;
-        work.header->cuts = 0;
+        work.header->segments = segments;
+        work.header->cuts = sh.cuts;
     }
-    if (!line) return;
-    // where every CTA begins
-    long long before = 0;
-    for (int c0 = 0; c0 < blocks; c0 += kThreads) {
-        const int b = c0 + threadIdx.x;
-        const long long each = b < blocks ? (long long)(kFixed + work.blocks[b].steps) * p.h_kv : 0;
-        long long total;
-        const long long first = before + block_exclusive_scan<kThreads>(each, sh.warp, &total);
-        if (b < blocks) sh.units[b] = first;
-        before += total;
-    }
-    if (threadIdx.x == 0) sh.units[blocks] = before;
-    __syncthreads();
-    const int cta = threadIdx.x;
-    if (cta <= p.sms) {
-        PrePlace place = {blocks, 0, 0, 0};
-        const long long unit = cta * share;
-        if (cta < p.sms && unit < before) {
-            int lo = 0, hi = blocks;  // units[lo] <= unit < units[hi]
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (sh.units[mid] <= unit) lo = mid;
-                else hi = mid;
-            }
-            const long long each = (sh.units[lo + 1] - sh.units[lo]) / p.h_kv, in = unit - sh.units[lo];
-            place.block = lo;
-            place.head = (int)(in / each);
-            place.step = (int)max(0ll, in - place.head * each - kFixed);
-        }
-        sh.place[cta] = work.places[cta] = place;
-    }
-    __syncthreads();
-    // a cut item: the first CTA that begins inside it
-    if (cta > 0 && cta < p.sms && sh.place[cta].step > 0) {
-        const PrePlace here = sh.place[cta], left = sh.place[cta - 1];
-        const bool same = left.block == here.block && left.head == here.head;
-        if (!(same && left.step > 0)) {
-            int n = 2;
-            for (int next = cta + 1; next < p.sms && sh.place[next].block == here.block && sh.place[next].head == here.head && sh.place[next].step > 0; ++next) ++n;
-            // the part before it is the last item of the CTA on its left, or all that one has
-            const int at = atomicAdd(&sh.cuts, 1);
-            work.cuts[at] = {here.block, here.head, 2 * (cta - 1) + (same ? 0 : 1), cta, n, {0, 0, 0}};
+}
+
+template <int kThreads>
+cudaError_t launch(const PrefillParams &p, cudaStream_t stream) {
+    constexpr int kMaxDevices = 64;
+    static std::mutex mutex;
+    static bool ready[kMaxDevices] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    {
+        std::lock_guard<std::mutex> lock(mutex);
+        if (!ready[dev]) {
+            e = cudaFuncSetAttribute(prefill_schedule_kernel<kThreads>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Shared<kThreads>));
+            if (e != cudaSuccess) return e;
+            ready[dev] = true;
         }
     }
-    __syncthreads();
-    if (threadIdx.x == 0) work.header->cuts = sh.cuts;
+    return launch_after(prefill_schedule_kernel<kThreads>, dim3(1), dim3(kThreads), sizeof(Shared<kThreads>), stream, p);
 }
 
 }  // namespace
 
 cudaError_t launch_prefill_schedule(const PrefillParams &p, cudaStream_t stream) {
-    return launch_after(prefill_schedule_kernel, dim3(1), dim3(kThreads), 0, stream, p);
+    return p.batch <= kFew && p.max_blocks <= kFew ? launch<kFew>(p, stream) : launch<kMany>(p, stream);
 }
 
 }  // namespace mla
