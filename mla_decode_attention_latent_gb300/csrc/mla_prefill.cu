@@ -799,7 +799,7 @@ cudaError_t launch(const PrefillParams &p, cudaStream_t stream) {
     }
     e = launch_after(prefill_kernel<kRope>, dim3(p.sms), dim3(kThreads), Layout<kRope>::kBytes, stream, mq, mk, mr, mv, p);
     if (e != cudaSuccess) return e;
-    if (!pre_may_cut(p.max_blocks, p.h_kv, p.sms)) return cudaSuccess;
+    if (!pre_may_cut(p.max_blocks, p.num_k, p.h_kv, p.sms)) return cudaSuccess;
     return launch_after(prefill_combine_kernel, dim3(4 * p.sms), dim3(kCombineWarps * 32), 0, stream, p);
 }
 

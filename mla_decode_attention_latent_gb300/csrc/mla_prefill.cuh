@@ -38,10 +38,13 @@ __host__ __device__ inline int64_t pre_max_blocks(int64_t num_q, int batch, int 
     return num_q / t + (num_q < batch ? num_q : batch);
 }
 // Blocks are cut only where at most this many items (segment, key head) come to a CTA: more
-// are even enough.  By the most blocks that a call can have, which the host knows: it
-// then leaves out the combine.
+// are even enough.  By the most blocks and steps that a call can have, which the host
+// knows: it then leaves out the combine.
 constexpr int kPreRounds = 8;
-__host__ __device__ inline bool pre_may_cut(int64_t max_blocks, int h_kv, int ctas) { return max_blocks * h_kv <= (int64_t)kPreRounds * ctas; }
+constexpr int kPreWhole = 9;  // steps that are never worth a cut (by the costs in mla_prefill_schedule.cu)
+__host__ __device__ inline bool pre_may_cut(int64_t max_blocks, int64_t num_k, int h_kv, int ctas) {
+    return max_blocks * h_kv <= (int64_t)kPreRounds * ctas && num_k > kPreWhole * kPreTile;
+}
 __host__ __device__ inline int64_t pre_max_segments(int64_t max_blocks, int ctas) {
     return max_blocks > kPreRounds * ctas ? max_blocks : kPreRounds * ctas;
 }

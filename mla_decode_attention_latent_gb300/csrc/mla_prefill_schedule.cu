@@ -14,10 +14,10 @@
 // end at the larger of an even share of all units and, for the ceil(n / ctas) rounds,
 // the longest item and a shortest one for every further round; a cut costs C for the
 // combine, and has to gain an eighth.  So few rows over many keys fill the GPU, and a
-// batch of prompts with many heads is not cut at all.  All heads of a part are
-// side by side, over the same keys: cut apart from each other (a line of all items in
-// equal shares), heads whose keys are neighbours in memory read them at different
-// times, and a step of three chunks behind long contexts took 3.2 us instead of 2.0.
+// batch of prompts with many heads is not cut at all.  (Equal shares of a line of all
+// items instead, each CTA beginning inside an item, kept three chunks behind long
+// contexts as busy, 80 against 82 us, but 512 equal items took 258 us for 231: the heads
+// of a moment then share no keys in L2.)
 //
 // One CTA.  Up to 1280 blocks, as many as there are where any is cut, are kept in shared
 // memory and sorted by counting, for each segment, those before it, which is stable: the
@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(kThreads) prefill_schedule_kernel(const Prefil
         return;
     }
     int most = 0x7fffffff;  // c
-    if (blocks > 0 && pre_may_cut(p.max_blocks, p.h_kv, p.sms) && kPreRounds * p.sms <= kStable) {
+    if (blocks > 0 && pre_may_cut(p.max_blocks, p.num_k, p.h_kv, p.sms) && kPreRounds * p.sms <= kStable) {
         if (steps) atomicAdd(&sh.steps, steps);
         __syncthreads();
         // values of c, one per warp at a time: the last none, the others from a quarter to four times an even share
