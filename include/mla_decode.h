@@ -751,7 +751,8 @@ MLA_API int mla_get_metadata_prefill(const int32_t *cu_q, const int32_t *cu_k, i
  *   softmax_scale  > 0
  *   metadata from mla_get_metadata_prefill with the same bounds and shapes, or NULL:
  *            computed by this call, in the workspace
- *   out      device bf16 [num_q][h_q][128], out;  lse  device fp32 [num_q][h_q], out:
+ *   out      device bf16 [num_q][h_q][128], out, 32-byte aligned;  lse  device fp32
+ *            [num_q][h_q], out:
  *            natural log of the sum of exp(softmax_scale q . k), for joining with other
  *            keys' results.  Rows of no sequence are left as they were
  *   workspace  at least mla_prefill_workspace_bytes(...) bytes, 256-byte aligned; calls

@@ -196,6 +196,7 @@ struct PrefillParams {
     int batch;
     int64_t num_q, num_k;
     int h_q, h_kv, group;         // group = h_q / h_kv
+    int tile_tokens;              // of a query tile: floor(128 / group)
     int causal;
     float scale, scale_log2;      // softmax scale, and times log2(e)
     uint16_t *out;                // [num_q][h_q][128]

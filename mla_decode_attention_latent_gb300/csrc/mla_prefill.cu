@@ -58,7 +58,8 @@ struct Layout {
     static constexpr int kSlots = kRope ? 8 : 10;         // 1.6 or 2.5 steps
     static constexpr uint32_t kRing = kPreTiles * kChunks * kSlotBytes;
     static constexpr uint32_t kBars = kRing + kSlots * kSlotBytes;
-    static constexpr uint32_t kBytes = kBars + 512 + 1024;  // 1024: room to align the base
+    static constexpr uint32_t kItems = kBars + 512;       // descriptions of items
+    static constexpr uint32_t kBytes = kItems + 256 + 1024;  // 1024: room to align the base
 };
 static_assert(Layout<true>::kBytes <= 232448 && Layout<false>::kBytes <= 232448, "shared memory of a CTA");
 
@@ -67,7 +68,8 @@ static_assert(Layout<true>::kBytes <= 232448 && Layout<false>::kBytes <= 232448,
 // after g is used up.
 constexpr int kGroups = 6;
 enum { B_FULL = 0, B_EMPTY = B_FULL + kGroups, B_TAIL = B_EMPTY + kGroups, B_ZERO = B_TAIL + kGroups, B_QFULL = B_ZERO + kGroups,
-       B_QEMPTY = B_QFULL + 2, B_S = B_QEMPTY + 2, B_P = B_S + 2, B_PV0 = B_P + 4, B_PV = B_PV0 + 2, B_OFREE = B_PV + 2, B_TURN = B_OFREE + 2, B_FINAL = B_TURN + 2, kNumBars = B_FINAL + 2 };
+       B_QEMPTY = B_QFULL + 2, B_S = B_QEMPTY + 2, B_P = B_S + 2, B_PV0 = B_P + 4, B_PV = B_PV0 + 2, B_OFREE = B_PV + 2, B_TURN = B_OFREE + 2, B_FINAL = B_TURN + 2, B_ITEM = B_FINAL + 2, B_READ = B_ITEM + 4,
+       kNumBars = B_READ + 4 };
 static_assert(kNumBars * 8 <= 512, "room for the barriers");
 static_assert(Layout<true>::kSlots < kGroups / 2 * Layout<true>::kStepSlots && Layout<false>::kSlots < kGroups / 2 * Layout<false>::kStepSlots,
               "the ring holds fewer than kGroups groups");
@@ -80,15 +82,13 @@ struct Ctx {
     __device__ bool wait(int i, uint32_t parity) const { return mbar_wait(bars + i, parity, status); }
 };
 
-// The items (segment, key head) of a CTA.  The segment of the next one is fetched while the
-// current one runs.
-using Segment = PreSegment;
-
+// The items (segment, key head) of a CTA, as the load warp goes through them.  The segment
+// of the next one is fetched while the current one is loaded.
 struct Walk {
     PreWork work;
     int segments, round = 0;
     bool more;
-    Segment ahead;
+    PreSegment ahead;
     int ahead_head;
     __device__ Walk(const PrefillParams &p) : work(p.metadata, p.max_blocks, p.sms) {
         segments = (int)min((long long)max(0, work.header->segments), (long long)pre_max_segments(p.max_blocks, p.sms));
@@ -103,21 +103,72 @@ struct Walk {
         ahead = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
         ++round;
     }
-    __device__ __forceinline__ bool next(const PrefillParams &p, Segment &s, int &head) {
-        if (!more) return false;
-        s = ahead;
-        head = ahead_head;
-        fetch(p);
-        // a partition of other lengths must not make the kernel leave its tensors
-        const int most = kPreTiles * pre_tile_tokens(p.group);
-        if (s.q0 < 0 || s.tokens < 0 || s.tokens > most || (int64_t)s.q0 + s.tokens > p.num_q || s.keys < 0 || s.k0 < 0 ||
-            (int64_t)s.k0 + s.keys > p.num_k || s.step0 < 0 || s.step1 > pre_steps(s.keys) ||
-            (s.part >= 0 && ((int64_t)s.part + 1) * p.h_kv > pre_slots(p.sms))) {
-            if ((threadIdx.x & 31) == 0) atomicOr(p.status, MLA_DEVERR_SEQLEN);
-            s.tokens = s.step0 = s.step1 = 0;
-            s.part = -1;
+};
+
+// An item as all roles see it.
+struct Item : PreSegment {
+    int head;
+    int seen_of[kPreTiles], steps_of[kPreTiles];  // of each tile: keys that its last token sees, steps of them in the segment
+};
+static_assert(sizeof(PreSegment) == 32, "an item is written as three 16-byte words");
+
+__device__ Item make_item(const PrefillParams &p, PreSegment s, int head) {
+    const int per = p.tile_tokens;
+    // a partition of other lengths must not make the kernel leave its tensors
+    if (s.q0 < 0 || s.tokens < 0 || s.tokens > kPreTiles * per || (int64_t)s.q0 + s.tokens > p.num_q || s.keys < 0 || s.k0 < 0 ||
+        (int64_t)s.k0 + s.keys > p.num_k || s.step0 < 0 || s.step1 > pre_steps(s.keys) ||
+        (s.part >= 0 && ((int64_t)s.part + 1) * p.h_kv > pre_slots(p.sms))) {
+        if ((threadIdx.x & 31) == 0) atomicOr(p.status, MLA_DEVERR_SEQLEN);
+        s.q0 = s.tokens = s.step0 = s.step1 = 0;
+        s.part = -1;
+    }
+    Item x;
+    static_cast<PreSegment &>(x) = s;
+    x.head = head;
+#pragma unroll
+    for (int t = 0; t < kPreTiles; ++t) {
+        const int last = min(s.tokens, (t + 1) * per) - 1;
+        x.seen_of[t] = last < t * per ? 0 : p.causal ? pre_seen(s, last) : s.keys;
+        x.steps_of[t] = max(0, min(pre_steps(x.seen_of[t]), s.step1) - s.step0);
+    }
+    return x;
+}
+
+// The items on their way from the load warp to the others, four at most, so that no role
+// works an item out for itself between two others (which took 2 us of each): written
+// an item ahead, read by a warp at once.  An item of q0 < 0 is the end.
+constexpr int kItems = 4, kReaders = 11;
+
+struct Items {
+    uint32_t base, n = 0;
+    __device__ Items(uint32_t at) : base(at) {}
+    __device__ bool put(const Ctx &c, const Item &x) {
+        const uint32_t i = n % kItems;
+        if (!__all_sync(0xffffffffu, c.wait(B_READ + i, ((n / kItems) & 1) ^ 1))) return false;
+        if (elect_one_lane()) {
+            const uint32_t at = base + i * 64;
+            sts128(at, x.q0, x.tokens, x.k0, x.keys);
+            sts128(at + 16, x.seen, x.step0, x.step1, x.part);
+            sts128(at + 32, x.seen_of[0], x.seen_of[1], x.steps_of[0], x.steps_of[1]);
+            sts32(at + 48, x.head);
+            mbar_arrive(c.bar(B_ITEM + i));
         }
+        __syncwarp();
+        ++n;
         return true;
+    }
+    // a warp's next item; false at the end (or when it does not come)
+    __device__ __forceinline__ bool get(const Ctx &c, Item &x) {
+        const uint32_t i = n % kItems, at = base + i * 64;
+        if (!__all_sync(0xffffffffu, c.wait(B_ITEM + i, (n / kItems) & 1))) return false;
+        const uint4 u = lds128(at), v = lds128(at + 16), w = lds128(at + 32);
+        x.head = (int)lds32(at + 48);
+        x.q0 = u.x, x.tokens = u.y, x.k0 = u.z, x.keys = u.w, x.seen = v.x, x.step0 = v.y, x.step1 = v.z, x.part = v.w;
+        x.seen_of[0] = w.x, x.seen_of[1] = w.y, x.steps_of[0] = w.z, x.steps_of[1] = w.w;
+        __syncwarp();
+        if (elect_one_lane()) mbar_arrive(c.bar(B_READ + i));
+        ++n;
+        return x.q0 >= 0;
     }
 };
 
@@ -126,19 +177,9 @@ struct Walk {
 // such a group has been issued (B_TAIL: only then is the group's B_FULL in the phase
 // that the zeroing waits for), the zero role when it is done (B_ZERO).  The group's
 // barriers are used again after both, so none is more than a phase ahead of who waits.
-__device__ __forceinline__ bool tail_step(const Segment &s, int j) {
+__device__ __forceinline__ bool tail_step(const PreSegment &s, int j) {
     return s.keys - (s.step0 + j) * kPreTile < kPreTile && s.keys % 16 != 0;
 }
-
-// what a tile of a segment does: keys that its last token sees, and its steps
-struct Tile {
-    int seen, steps;
-    __device__ Tile(const PrefillParams &p, const Segment &s, int t) {
-        const int per = pre_tile_tokens(p.group), last = min(s.tokens, (t + 1) * per) - 1;
-        seen = last < t * per ? 0 : p.causal ? pre_seen(s, last) : s.keys;
-        steps = max(0, min(pre_steps(seen), s.step1) - s.step0);
-    }
-};
 
 // One lane of a converged warp, the same one every time.  The load and MMA warps run
 // their role as whole warps and only issue in the elected lane: where one lane runs the
@@ -159,15 +200,13 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, u
 }
 
 template <bool kRope>
-__device__ void load_role(const PrefillParams &p, const Ctx &c, const CUtensorMap *mq, const CUtensorMap *mk, const CUtensorMap *mr,
+__device__ void load_role(const PrefillParams &p, const Ctx &c, Items items, const CUtensorMap *mq, const CUtensorMap *mk, const CUtensorMap *mr,
                           const CUtensorMap *mv) {
     using L = Layout<kRope>;
     Walk walk(p);
-    Segment s;
-    int head;
     uint32_t slot = 0, group = 0, freed = 0, held = 0;  // groups issued and given back, slots that the others hold
     uint32_t qn[kPreTiles] = {0, 0};
-    const uint32_t q_bytes = (uint32_t)(pre_tile_tokens(p.group) * p.group) * 128u;
+    const uint32_t q_bytes = (uint32_t)(p.tile_tokens * p.group) * 128u;
     auto wait = [&](int bar, uint32_t parity) { return __all_sync(0xffffffffu, c.wait(bar, parity)) != 0; };
     // room for a group of n slots: groups come back in order, keys and values in turn
     auto room = [&](uint32_t n) {
@@ -185,14 +224,29 @@ __device__ void load_role(const PrefillParams &p, const Ctx &c, const CUtensorMa
         return at;
     };
     bool ok = true;
-    while (ok && walk.next(p, s, head)) {
-        const Tile a(p, s, 0), b(p, s, 1);
-        const int n = max(a.steps, b.steps);
+    Item next;
+    // the next item, or the end, worked out and told to the others
+    auto look_ahead = [&] {
+        if (walk.more) {
+            const PreSegment segment = walk.ahead;
+            const int head = walk.ahead_head;
+            walk.fetch(p);
+            next = make_item(p, segment, head);
+        } else {
+            next.q0 = -1;
+        }
+        return items.put(c, next);
+    };
+    ok = look_ahead();
+    while (ok && next.q0 >= 0) {
+        const Item s = next;
+        const int head = s.head, n = max(s.steps_of[0], s.steps_of[1]);
+        if (!(ok = look_ahead())) break;
         // Q of the tiles that walk, behind the first keys: its place is free only when the
             // products of the segment before have read it
 #pragma unroll
             for (int t = 0; t < kPreTiles; ++t) {
-                if (!ok || (t ? b.steps : a.steps) == 0) continue;
+                if (!ok || s.steps_of[t] == 0) continue;
                 ok = wait(B_QEMPTY + t, (qn[t] & 1) ^ 1);
                 if (!ok) continue;
                 ++qn[t];
@@ -200,7 +254,7 @@ __device__ void load_role(const PrefillParams &p, const Ctx &c, const CUtensorMa
                     mbar_arrive_expect_tx(c.bar(B_QFULL + t), L::kChunks * q_bytes);
                     for (int ch = 0; ch < L::kChunks; ++ch)
                         tma_load(smem_u32(c.base + (t * L::kChunks + ch) * kSlotBytes), mq, c.bar(B_QFULL + t), 64 * ch, head * p.group,
-                                 s.q0 + t * pre_tile_tokens(p.group));
+                                 s.q0 + t * p.tile_tokens);
                 }
                 __syncwarp();
             }
@@ -256,12 +310,10 @@ __device__ __forceinline__ int keys16(int keys) { return keys >= kPreTile ? kPre
 // once, then both tiles' exponents), so they take turns: a turn is PV(j) QK(j+1), and is
 // handed over a few MMAs before its end.
 template <bool kRope>
-__device__ void mma_role(const PrefillParams &p, const Ctx &c, uint32_t tmem, int t) {
+__device__ void mma_role(const Ctx &c, Items items, uint32_t tmem, int t) {
     using L = Layout<kRope>;
     constexpr uint32_t kPvDesc = idesc_bf16(kPreTile, kPreHead, false, true);
-    Walk walk(p);
-    Segment s;
-    int head;
+    Item s;
     uint32_t slot = 0, group = 0, qn = 0, done = 0, turn = 0;
     uint32_t zeroed = 0;  // a bit per group barrier, the phase of its B_ZERO
     const uint32_t ring = smem_u32(c.base + L::kRing);
@@ -271,9 +323,9 @@ __device__ void mma_role(const PrefillParams &p, const Ctx &c, uint32_t tmem, in
     auto wait = [&](int bar, uint32_t parity) { return __all_sync(0xffffffffu, c.wait(bar, parity)) != 0; };
     auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
     auto after = [](uint32_t at, uint32_t n) { return at + n >= L::kSlots ? at + n - L::kSlots : at + n; };
-    while (walk.next(p, s, head)) {
-        const Tile mine(p, s, t), other(p, s, 1 - t);
-        const int steps = uniform(mine.steps), n = uniform(max(mine.steps, other.steps)), seen = uniform(mine.seen - s.step0 * kPreTile);
+    while (items.get(c, s)) {
+        const int steps = uniform(t ? s.steps_of[1] : s.steps_of[0]), n = uniform(max(s.steps_of[0], s.steps_of[1])),
+                  seen = uniform((t ? s.seen_of[1] : s.seen_of[0]) - s.step0 * kPreTile);
         // S = Q K(j)^T, the keys (group g) at slot `at`; `hand_over`: the turn ends here
         auto scores = [&](int j, uint32_t at, uint32_t g, bool hand_over) {
             const uint32_t idesc = idesc_keys(keys16(seen - j * kPreTile));
@@ -363,16 +415,13 @@ __device__ void mma_role(const PrefillParams &p, const Ctx &c, uint32_t tmem, in
 
 // ---------------------------------------------------------------- value rows behind a sequence
 template <bool kRope>
-__device__ void zero_role(const PrefillParams &p, const Ctx &c) {
+__device__ void zero_role(const Ctx &c, Items items) {
     using L = Layout<kRope>;
-    Walk walk(p);
-    Segment s;
-    int head;
+    Item s;
     uint32_t slot = 0, group = 0, tails = 0;  // tails: a bit per group barrier, the phase of its B_TAIL
     const int lane = threadIdx.x & 31;
-    while (walk.next(p, s, head)) {
-        const Tile a(p, s, 0), b(p, s, 1);
-        const int n = max(a.steps, b.steps);
+    while (items.get(c, s)) {
+        const int n = max(s.steps_of[0], s.steps_of[1]);
         if (n == 0) continue;
         if (tail_step(s, n - 1)) {
             const int valid = s.keys - (s.step0 + n - 1) * kPreTile;  // keys of the last step
@@ -513,22 +562,28 @@ __device__ __noinline__ State careful_half(const Half x, float scale_log2, uint6
 // A partial result's 4 dims 4 c .. of a row: rows side by side, as the rows' threads write them
 __device__ __forceinline__ int64_t part_at(int64_t slot, int c, int row) { return (slot * (kPreHead / 4) + c) * kPreRows + row; }
 
-__device__ void row_role(const PrefillParams &p, const Ctx &c, uint32_t tmem, int t) {
+// 32 bytes at once: a lane writes its own row, and a store instruction takes a cycle for each
+// of the 32 lines that it touches
+__device__ __forceinline__ void store32(void *dst, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]),
+                 "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+__device__ void row_role(const PrefillParams &p, const Ctx &c, Items items, uint32_t tmem, int t) {
     const int warp = threadIdx.x >> 5, r = threadIdx.x & (kPreTile - 1);
     const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t s_col = tmem + lane_base + t * 128, o_col = tmem + lane_base + 256 + t * 128;
-    const int per = pre_tile_tokens(p.group), in_tile = r / p.group, hh = r - in_tile * p.group;
-    Walk walk(p);
-    Segment s;
-    int head;
+    const int per = p.tile_tokens, in_tile = r / p.group, hh = r - in_tile * p.group;
+    Item s;
     uint32_t phase = 0;  // steps of this tile so far
-    while (walk.next(p, s, head)) {
-        const Tile tile(p, s, t);
+    while (items.get(c, s)) {
+        const int head = s.head, steps = t ? s.steps_of[1] : s.steps_of[0];
         const int token = t * per + in_tile;
         const bool on = in_tile < per && token < s.tokens;
         const int seen = !on ? 0 : p.causal ? pre_seen(s, token) : s.keys;
         float m = -INFINITY, l = 0.f;  // reference (a raw score), sum of the weights
-        for (int j = 0; j < tile.steps; ++j, ++phase) {
+        for (int j = 0; j < steps; ++j, ++phase) {
             if (!__all_sync(0xffffffffu, c.wait(B_S + t, phase & 1))) return;
             tc_fence_after();
 #pragma unroll 1
@@ -570,7 +625,7 @@ __device__ void row_role(const PrefillParams &p, const Ctx &c, uint32_t tmem, in
             if (s.part < 0) p.lse[row] = lse;
             else p.lse_part[slot * kPreRows + t * kPreTile + r] = lse;
         }
-        if (tile.steps == 0) {
+        if (steps == 0) {
             if (on && s.part < 0)
                 for (int i = 0; i < kPreHead / 8; ++i) reinterpret_cast<uint4 *>(p.out + row * kPreHead)[i] = make_uint4(0, 0, 0, 0);
             continue;
@@ -593,14 +648,13 @@ __device__ void row_role(const PrefillParams &p, const Ctx &c, uint32_t tmem, in
                 const int i = 2 * i2 + i1;
                 uint32_t (&o)[32] = both[i1];
                 if (s.part < 0) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(p.out + row * kPreHead + 32 * i);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        uint32_t w[4];
+                    for (int k = 0; k < 2; ++k) {
+                        uint32_t w[8];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            w[e] = pack_bf16(__uint_as_float(o[8 * k + 2 * e]) * inv, __uint_as_float(o[8 * k + 2 * e + 1]) * inv);
-                        dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
+                        for (int e = 0; e < 8; ++e)
+                            w[e] = pack_bf16(__uint_as_float(o[16 * k + 2 * e]) * inv, __uint_as_float(o[16 * k + 2 * e + 1]) * inv);
+                        store32(p.out + row * kPreHead + 32 * i + 16 * k, w);
                     }
                 } else {
 #pragma unroll
@@ -645,6 +699,10 @@ prefill_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             mbar_init(c.bar(B_TURN + t), 1);
             mbar_init(c.bar(B_FINAL + t), 1);
         }
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(c.bar(B_ITEM + i), 1);
+            mbar_init(c.bar(B_READ + i), kReaders);
+        }
         fence_mbar_init();
     }
     if (warp == kLoadWarp && elect_one_lane()) {
@@ -662,21 +720,22 @@ prefill_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
     griddep_wait();
+    const Items items(smem_u32(c.base + L::kItems));
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRowRegs));
-        row_role(p, c, tmem, warp >> 2);
+        row_role(p, c, items, tmem, warp >> 2);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == kLoadWarp) {
-            load_role<kRope>(p, c, &mq, &mk, &mr, &mv);
+            load_role<kRope>(p, c, items, &mq, &mk, &mr, &mv);
         } else if (warp < kZeroWarp) {
             const int t = warp - kMmaWarp;
-            mma_role<kRope>(p, c, tmem, t);
+            mma_role<kRope>(c, items, tmem, t);
             if (elected()) mma_commit(c.bar(B_FINAL + t));  // every MMA of this thread is done before tensor memory is released
             __syncwarp();
             c.wait(B_FINAL + t, 0);
         } else {
-            zero_role<kRope>(p, c);
+            zero_role<kRope>(c, items);
         }
     }
     tc_fence_before();

@@ -261,6 +261,7 @@ int mla_get_metadata_prefill(const int32_t *cu_q, const int32_t *cu_k, int batch
     p.h_q = h_q;
     p.h_kv = h_kv;
     p.group = h_q / h_kv;
+    p.tile_tokens = pre_tile_tokens(p.group);
     p.causal = causal != 0;
     p.metadata = metadata;
     p.max_blocks = pre_max_blocks(num_q, batch, p.group);
@@ -296,7 +297,7 @@ int mla_prefill(const void *q, int64_t q_token_stride, int64_t q_head_stride, co
         if (!heads(v, v_token_stride, v_head_stride, num_k, h_kv, kPreHead)) return MLA_ERR_INVALID_ARG;
         if (rope && !heads(k_rope, k_rope_token_stride, kPreRope, num_k, 1, kPreRope)) return MLA_ERR_INVALID_ARG;
     }
-    if (!aligned16(out) || (reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1))) return MLA_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(out) & 31) || (reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1))) return MLA_ERR_INVALID_ARG;
     if (num_q == 0) return MLA_OK;
     PrefillParams p{};
     if (device_sm_count(&p.sms) != cudaSuccess) return MLA_ERR_CUDA;
@@ -329,6 +330,7 @@ int mla_prefill(const void *q, int64_t q_token_stride, int64_t q_head_stride, co
     p.h_q = h_q;
     p.h_kv = h_kv;
     p.group = h_q / h_kv;
+    p.tile_tokens = pre_tile_tokens(p.group);
     p.causal = causal != 0;
     p.scale = softmax_scale;
     p.scale_log2 = softmax_scale * 1.4426950408889634f;
