@@ -719,13 +719,22 @@ prefill_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
-    griddep_wait();
     const Items items(smem_u32(c.base + L::kItems));
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRowRegs));
+        {
+            // Before the kernel in front has ended: the code for a first half into the instruction
+            // cache, run on what the tile's O happens to hold (the first PV overwrites it)
+            const uint32_t at = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 256 + 128 * (warp >> 2);
+            const Half none = {at, at + 64, at, 64, 0.f, 0.f, true};
+            careful_half(none, 1.f, nullptr, 0, c.status);
+            tmem_wait_st();
+        }
+        griddep_wait();
         row_role(p, c, items, tmem, warp >> 2);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        griddep_wait();
         if (warp == kLoadWarp) {
             load_role<kRope>(p, c, items, &mq, &mk, &mr, &mv);
         } else if (warp < kZeroWarp) {
