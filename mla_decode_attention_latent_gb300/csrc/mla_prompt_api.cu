@@ -285,7 +285,7 @@ int mla_prefill(const void *q, int64_t q_token_stride, int64_t q_head_stride, co
     const bool rope = d_qk > kPreHead;
     if (num_q > 0 && num_k > 0 && rope != (k_rope != nullptr)) return MLA_ERR_INVALID_ARG;  // empty tensors may be null
     // rows are ranked by raw scores, which is the order of the scaled ones for a positive scale only
-    if (!(softmax_scale > 0.f) || !real(softmax_scale)) return MLA_ERR_INVALID_ARG;
+    if (!(softmax_scale > 0.f) || !real(softmax_scale * 1.4426950408889634f)) return MLA_ERR_INVALID_ARG;
     auto heads = [](const void *ptr, int64_t token, int64_t head, int64_t n, int64_t h, int64_t d) {
         // 16-byte aligned heads that do not overlap, strides that a tensor map holds
         if (!aligned16(ptr) || token % 8 || head % 8 || token >= (1LL << 38) || head >= (1LL << 38)) return false;

@@ -85,3 +85,63 @@ def test_rows_of_one_format_only(lib):
     assert call(lib.mla_norm_rope_cache_write_fp8, ROWS, dict(d=512)) == UNSUP
     assert call(lib.mla_norm_rope_cache_write, ROWS, dict(d=512, ro=256, ros=64)) == BAD  # no RoPE part to write
     assert call(lib.mla_norm_rope_cache_write, ROWS, dict(d=512, n=0)) == OK
+
+
+PREFILL = dict(q=256, qt=16 * 192, qh=192, k=256, kt=4 * 256, kh=256, v=512, vt=4 * 256, vh=256, kr=256, krt=64, cq=256, ck=256, b=2, nq=9, nk=11, hq=16, hkv=4, dqk=192,
+               dv=128, scale=0.07, causal=1, md=256, out=512, lse=256, ws=256, bytes=1 << 40)
+
+
+@pytest.mark.parametrize("over,code", [
+    *[({k: None}, BAD) for k in ("q", "k", "v", "kr", "cq", "ck", "out", "lse", "ws")],
+    *[({k: 0}, BAD) for k in ("b", "hq", "hkv", "dqk", "dv")], (dict(nq=-1), BAD), (dict(nk=-1), BAD), (dict(hq=18), BAD),
+    (dict(hq=129 * 4), UNSUP), (dict(hq=4096 * 8, hkv=4096), UNSUP), (dict(nq=1 << 30), UNSUP), (dict(nk=1 << 30), UNSUP),
+    (dict(dqk=160), UNSUP), (dict(dqk=576), UNSUP), (dict(dv=64), UNSUP), (dict(dqk=128), BAD),  # a RoPE key with heads that have no room for it
+    (dict(scale=0.0), BAD), (dict(scale=-1.0), BAD), (dict(scale=NAN), BAD), (dict(scale=INF), BAD), (dict(scale=3.4e38), BAD),
+    (dict(q=264), BAD), (dict(k=264), BAD), (dict(v=264), BAD), (dict(kr=264), BAD), (dict(out=528), BAD), (dict(ws=384), BAD),
+    (dict(qt=3076), BAD), (dict(qh=190), BAD), (dict(kt=8), BAD), (dict(kh=120), BAD), (dict(vh=0), BAD), (dict(krt=56), BAD), (dict(krt=68), BAD),
+    (dict(kt=1 << 40), BAD), (dict(nq=0), OK), (dict(nq=0, q=None, out=None, lse=None, ws=None), OK)])
+def test_prefill(lib, over, code):
+    assert call(lib.mla_prefill, PREFILL, over) == code
+
+
+@pytest.mark.parametrize("over,code", [
+    *[({k: None}, BAD) for k in ("cq", "ck", "md")], *[({k: 0}, BAD) for k in ("b", "hq", "hkv")], (dict(nq=-1), BAD), (dict(nk=-1), BAD), (dict(hq=18), BAD),
+    (dict(hq=129 * 4), UNSUP), (dict(nq=1 << 30), UNSUP), (dict(nk=1 << 30), UNSUP)])
+def test_prefill_partition(lib, over, code):
+    assert call(lib.mla_get_metadata_prefill, dict(cq=256, ck=256, b=2, nq=9, nk=11, hq=16, hkv=4, causal=1, md=256), over) == code
+
+
+def test_prefill_sizes_of_impossible_shapes(lib):
+    for shape in ((0, 9, 16, 4), (2, -1, 16, 4), (2, 9, 18, 4), (2, 9, 0, 4), (2, 9, 516, 4), (2, 1 << 30, 16, 4)):
+        assert lib.mla_prefill_metadata_ints(*shape) == 0 and lib.mla_prefill_workspace_bytes(*shape) == 0
+
+
+def test_the_binding_refuses_host_tensors_and_wrong_kinds():
+    import torch
+
+    import mla_decode_attention_latent_gb300 as mla
+    i, f, h, l = (torch.zeros((4,), dtype=t) for t in (torch.int32, torch.float32, torch.bfloat16, torch.int64))
+    heads = torch.zeros((4, 2, 64), dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        mla.mla_norm_rope(heads, None, None, weight=h)
+    with pytest.raises(TypeError):
+        mla.mla_norm_rope(heads.float(), None, None)
+    with pytest.raises(TypeError):
+        mla.mla_norm_rope([1], None, None)
+    with pytest.raises(ValueError):
+        mla.mla_assign_pages(i, i, torch.zeros((3, 2), dtype=torch.int32), i, i[:1], 4)
+    with pytest.raises(ValueError):
+        mla.mla_release_pages(i, i, torch.zeros((4, 2), dtype=torch.int32), 9, i, i[:1])
+    with pytest.raises(ValueError):
+        mla.mla_norm_rope_cache_write(torch.zeros((4, 512), dtype=torch.bfloat16), torch.zeros((4, 64), dtype=torch.bfloat16), i, l, l,
+                                      torch.zeros((2, 64, 1, 576), dtype=torch.bfloat16))
+    with pytest.raises(ValueError):
+        mla.mla_prefill(heads, heads, heads, i, i)
+    with pytest.raises(ValueError):
+        mla.mla_get_metadata_prefill(i, i, 4, 4, 2, 2)
+    for dims in (0, -2, 7):
+        with pytest.raises((ValueError, RuntimeError)):
+            mla.mla_rope_turns(dims, device="cpu")
+    with pytest.raises(RuntimeError):
+        mla.mla_rope_turns(64, base=0.5, device="cpu")
+    assert f.dtype == torch.float32
