@@ -243,21 +243,21 @@ __device__ void load_role(const PrefillParams &p, const Ctx &c, Items items, con
         const int head = s.head, n = max(s.steps_of[0], s.steps_of[1]);
         if (!(ok = look_ahead())) break;
         // Q of the tiles that walk, behind the first keys: its place is free only when the
-            // products of the segment before have read it
+        // products of the segment before have read it
 #pragma unroll
-            for (int t = 0; t < kPreTiles; ++t) {
-                if (!ok || s.steps_of[t] == 0) continue;
-                ok = wait(B_QEMPTY + t, (qn[t] & 1) ^ 1);
-                if (!ok) continue;
-                ++qn[t];
-                if (elected()) {
-                    mbar_arrive_expect_tx(c.bar(B_QFULL + t), L::kChunks * q_bytes);
-                    for (int ch = 0; ch < L::kChunks; ++ch)
-                        tma_load(smem_u32(c.base + (t * L::kChunks + ch) * kSlotBytes), mq, c.bar(B_QFULL + t), 64 * ch, head * p.group,
-                                 s.q0 + t * p.tile_tokens);
-                }
-                __syncwarp();
+        for (int t = 0; t < kPreTiles; ++t) {
+            if (!ok || s.steps_of[t] == 0) continue;
+            ok = wait(B_QEMPTY + t, (qn[t] & 1) ^ 1);
+            if (!ok) continue;
+            ++qn[t];
+            if (elected()) {
+                mbar_arrive_expect_tx(c.bar(B_QFULL + t), L::kChunks * q_bytes);
+                for (int ch = 0; ch < L::kChunks; ++ch)
+                    tma_load(smem_u32(c.base + (t * L::kChunks + ch) * kSlotBytes), mq, c.bar(B_QFULL + t), 64 * ch, head * p.group,
+                             s.q0 + t * p.tile_tokens);
             }
+            __syncwarp();
+        }
         for (int j = 0; ok && j < n; ++j) {
             const int k0 = s.k0 + (s.step0 + j) * kPreTile;
             if (!(ok = room(L::kChunks))) break;
@@ -335,7 +335,6 @@ __device__ void mma_role(const Ctx &c, Items items, uint32_t tmem, int t) {
             if (elected()) {
 #pragma unroll
                 for (int ch = 0; ch < L::kChunks; ++ch) {
-                    
 #pragma unroll
                     for (int i = 0; i < 4; ++i)  // 16 dims: 32 B
                         mma_ss(s_col, q_desc + ch * (kSlotBytes / 16) + 2 * i, bd[ch] + 2 * i, idesc, ch + i > 0);
@@ -781,7 +780,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) prefill_combine_kernel(con
         for (int k = 0; k < cut.count; ++k) top = fmaxf(top, p.lse_part[(slot0 + (int64_t)k * p.h_kv) * kPreRows + r]);
         const float base = top == -INFINITY ? 0.f : top;
         float sum = 0.f, o[kCombineDims] = {};
-#pragma unroll 2
+#pragma unroll 4
         for (int k = 0; k < cut.count; ++k) {
             const int64_t slot = slot0 + (int64_t)k * p.h_kv;
             const float lse = p.lse_part[slot * kPreRows + r];
@@ -868,7 +867,7 @@ cudaError_t launch(const PrefillParams &p, cudaStream_t stream) {
     e = launch_after(prefill_kernel<kRope>, dim3(p.sms), dim3(kThreads), Layout<kRope>::kBytes, stream, mq, mk, mr, mv, p);
     if (e != cudaSuccess) return e;
     if (!pre_may_cut(p.max_blocks, p.num_k, p.h_kv, p.sms)) return cudaSuccess;
-    return launch_after(prefill_combine_kernel, dim3(4 * p.sms), dim3(kCombineWarps * 32), 0, stream, p);
+    return launch_after(prefill_combine_kernel, dim3(8 * p.sms), dim3(kCombineWarps * 32), 0, stream, p);
 }
 
 }  // namespace
