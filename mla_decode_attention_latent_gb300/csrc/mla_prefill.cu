@@ -458,6 +458,12 @@ __device__ __forceinline__ void arrived(uint32_t (&a)[32], uint32_t (&b)[32]) {
     for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(a[i]), "+r"(b[i]));  // no use moves before the wait
 }
 
+__device__ __forceinline__ void arrived(uint32_t (&a)[32]) {
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(a[i]));
+}
+
 // A row's weights are exp2(score * scale - reference).  The reference need not be the
 // running maximum: bf16 and fp32 hold a weight as exactly at 2^20 as at 1.  So it is the
 // largest of the row's first 64 scores, and is raised only when 64 weights add up to
@@ -476,25 +482,31 @@ __device__ __forceinline__ float largest(const uint32_t (&a)[32], const uint32_t
     return max3f(c, max3f(mx[2], mx[3], __uint_as_float(b[30])), __uint_as_float(b[31]));
 }
 
-// 64 weights as bf16 pairs, and their sum
-__device__ __forceinline__ float weigh(const uint32_t (&a)[32], const uint32_t (&b)[32], float m, float scale_log2, uint32_t (&w)[32]) {
-    const float shift = m == -INFINITY ? 0.f : -m * scale_log2;
-    const uint64_t scale2 = f2_pack(scale_log2, scale_log2), shift2 = f2_pack(shift, shift);
-    uint64_t sum[2] = {0, 0};
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        const uint32_t *x = i < 16 ? a + 2 * i : b + 2 * (i - 16);
-        float lo, hi;
-        f2_unpack(f2_fma(f2_pack(__uint_as_float(x[0]), __uint_as_float(x[1])), scale2, shift2), lo, hi);
-        lo = exp2_fast(lo);
-        hi = exp2_fast(hi);
-        sum[i & 1] = f2_add(sum[i & 1], f2_pack(lo, hi));
-        w[i] = pack_bf16(lo, hi);
+// 32 weights as bf16 pairs, added up in `sum`
+struct Weigh {
+    uint64_t scale2, shift2, sum[2];
+    __device__ __forceinline__ Weigh(float m, float scale_log2) {
+        const float shift = m == -INFINITY ? 0.f : -m * scale_log2;
+        scale2 = f2_pack(scale_log2, scale_log2), shift2 = f2_pack(shift, shift);
+        sum[0] = sum[1] = 0;
     }
-    float lo, hi;
-    f2_unpack(f2_add(sum[0], sum[1]), lo, hi);
-    return lo + hi;
-}
+    __device__ __forceinline__ void operator()(const uint32_t (&x)[32], uint32_t *w) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float lo, hi;
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), scale2, shift2), lo, hi);
+            lo = exp2_fast(lo);
+            hi = exp2_fast(hi);
+            sum[i & 1] = f2_add(sum[i & 1], f2_pack(lo, hi));
+            w[i] = pack_bf16(lo, hi);
+        }
+    }
+    __device__ __forceinline__ float total() const {
+        float lo, hi;
+        f2_unpack(f2_add(sum[0], sum[1]), lo, hi);
+        return lo + hi;
+    }
+};
 
 // 64 scores of a row, and what its weights refer to
 struct Half {
@@ -523,36 +535,44 @@ __device__ __noinline__ State careful_half(const Half x, float scale_log2, uint6
     tmem_ld32(x.s_col, a);
     tmem_ld32(x.s_col + 32, b);
     arrived(a, b);
+    if (__any_sync(0xffffffffu, x.left < 64)) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        a[i] = i < x.left ? a[i] : 0xff800000u;
-        b[i] = i + 32 < x.left ? b[i] : 0xff800000u;
+        for (int i = 0; i < 32; ++i) {
+            a[i] = i < x.left ? a[i] : 0xff800000u;
+            b[i] = i + 32 < x.left ? b[i] : 0xff800000u;
+        }
     }
-    float m = x.first ? largest(a, b) : x.m, l = x.l, sum = 0.f;
+    float m = x.m, l = x.l, sum = 0.f;
+    bool raise = x.first;
 #pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
-        sum = weigh(a, b, m, scale_log2, w);
-        const bool raise = !(sum <= kMostWeight) || (m == -INFINITY && x.left > 0);
-        if (pass || !__any_sync(0xffffffffu, raise)) break;
-        const float m_new = raise ? fmaxf(m, largest(a, b)) : m;
-        const float f = !raise ? 1.f : m == -INFINITY ? 0.f : exp2_fast((m - m_new) * scale_log2);
-        if (products) {
-            // every product so far is in O
-            if (!__all_sync(0xffffffffu, mbar_wait(products, parity, status))) return {m, l, 0};
-            tc_fence_after();
+        if (__any_sync(0xffffffffu, raise)) {
+            const float m_new = raise ? fmaxf(m, largest(a, b)) : m;
+            const float f = !raise ? 1.f : m == -INFINITY ? 0.f : exp2_fast((m - m_new) * scale_log2);
+            if (products) {
+                // every product so far is in O
+                if (!__all_sync(0xffffffffu, mbar_wait(products, parity, status))) return {m, l, 0};
+                tc_fence_after();
 #pragma unroll 1
-            for (int i = 0; i < 8; ++i) {
-                uint32_t o[16];
-                tmem_ld16(x.o_col + 16 * i, o);
-                tmem_wait_ld();
+                for (int i = 0; i < 8; ++i) {
+                    uint32_t o[16];
+                    tmem_ld16(x.o_col + 16 * i, o);
+                    tmem_wait_ld();
 #pragma unroll
-                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                tmem_st16(x.o_col + 16 * i, o);
+                    for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                    tmem_st16(x.o_col + 16 * i, o);
+                }
+                tmem_wait_st();
             }
-            tmem_wait_st();
+            l *= f;
+            m = m_new;
         }
-        l *= f;
-        m = m_new;
+        Weigh weigh(m, scale_log2);
+        weigh(a, w);
+        weigh(b, w + 16);
+        sum = weigh.total();
+        raise = !(sum <= kMostWeight) || (m == -INFINITY && x.left > 0);
+        if (!__any_sync(0xffffffffu, raise)) break;
     }
     tmem_st32(x.p_col, w);
     return {m, l + sum, 1};
@@ -585,31 +605,52 @@ __device__ void row_role(const PrefillParams &p, const Ctx &c, Items items, uint
         for (int j = 0; j < steps; ++j, ++phase) {
             if (!__all_sync(0xffffffffu, c.wait(B_S + t, phase & 1))) return;
             tc_fence_after();
+            const int ahead = seen - (s.step0 + j) * kPreTile;
+            int h = 0;
+            if (!__any_sync(0xffffffffu, j == 0 || ahead < kPreTile || m == -INFINITY)) {
+                // the ordinary step: 32 scores are on their way while 32 are weighed
+                uint32_t x0[32], x1[32], w[32];
+                Weigh first(m, p.scale_log2), second(m, p.scale_log2);
+                tmem_ld32(s_col, x0);
+                arrived(x0);
+                tmem_ld32(s_col + 32, x1);
+                first(x0, w);
+                arrived(x1);
+                tmem_ld32(s_col + 64, x0);
+                first(x1, w + 16);
+                const float sum0 = first.total();
+                const bool good = __all_sync(0xffffffffu, sum0 <= kMostWeight);
+                if (good) tmem_st32(s_col, w);
+                arrived(x0);
+                if (good) {
+                    tmem_ld32(s_col + 96, x1);
+                    second(x0, w);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    mbar_arrive(c.bar(B_P + 2 * t));
+                    arrived(x1);
+                    second(x1, w + 16);
+                    const float sum1 = second.total();
+                    l += sum0;
+                    h = 1;
+                    if (__all_sync(0xffffffffu, sum1 <= kMostWeight)) {
+                        tmem_st32(s_col + 32, w);
+                        l += sum1;
+                        tmem_wait_st();
+                        tc_fence_before();
+                        mbar_arrive(c.bar(B_P + 2 * t + 1));
+                        h = 2;
+                    }
+                }
+            }
 #pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
-                const int left = seen - (s.step0 + j) * kPreTile - 64 * h;
-                bool careful = j + h == 0 || left < 64;
-                uint32_t w[32];
-                float sum = 0.f;
-                if (!__any_sync(0xffffffffu, careful)) {
-                    uint32_t a[32], b[32];
-                    tmem_ld32(s_col + 64 * h, a);
-                    tmem_ld32(s_col + 64 * h + 32, b);
-                    arrived(a, b);
-                    sum = weigh(a, b, m, p.scale_log2, w);
-                    careful = !(sum <= kMostWeight) || m == -INFINITY;
-                }
-                if (!__any_sync(0xffffffffu, careful)) {
-                    l += sum;
-                    tmem_st32(s_col + 32 * h, w);
-                } else {
-                    // products so far: the step before's, or this step's first half
-                    const Half x = {s_col + 64 * h, o_col, s_col + 32 * h, left, m, l, j + h == 0};
-                    const State y = careful_half(x, p.scale_log2, j + h == 0 ? nullptr : c.bar((h ? B_PV0 : B_PV) + t), (h ? phase : phase - 1) & 1, c.status);
-                    if (!y.ok) return;
-                    m = y.m;
-                    l = y.l;
-                }
+            for (; h < 2; ++h) {
+                // products so far: the step before's, or this step's first half
+                const Half x = {s_col + 64 * h, o_col, s_col + 32 * h, ahead - 64 * h, m, l, j + h == 0};
+                const State y = careful_half(x, p.scale_log2, j + h == 0 ? nullptr : c.bar((h ? B_PV0 : B_PV) + t), (h ? phase : phase - 1) & 1, c.status);
+                if (!y.ok) return;
+                m = y.m;
+                l = y.l;
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(c.bar(B_P + 2 * t + h));
@@ -631,7 +672,7 @@ __device__ void row_role(const PrefillParams &p, const Ctx &c, Items items, uint
         }
         if (!__all_sync(0xffffffffu, c.wait(B_PV + t, (phase - 1) & 1))) return;
         tc_fence_after();
-#pragma unroll
+#pragma unroll 1
         for (int i2 = 0; i2 < 2; ++i2) {
             uint32_t both[2][32];
             tmem_ld32(o_col + 64 * i2, both[0]);
