@@ -600,7 +600,9 @@ __device__ void row_role(const PrefillParams &p, const Ctx &c, Items items, uint
         const int head = s.head, steps = t ? s.steps_of[1] : s.steps_of[0];
         const int token = t * per + in_tile;
         const bool on = in_tile < per && token < s.tokens;
-        const int seen = !on ? 0 : p.causal ? pre_seen(s, token) : s.keys;
+        // A row of no query beside rows of queries follows the tile's last, so that its warp need not
+        // mask; a warp without queries has nothing in sight
+        const int seen = __any_sync(0xffffffffu, on) ? !on ? (t ? s.seen_of[1] : s.seen_of[0]) : p.causal ? pre_seen(s, token) : s.keys : 0;
         float m = -INFINITY, l = 0.f;  // reference (a raw score), sum of the weights
         for (int j = 0; j < steps; ++j, ++phase) {
             if (!__all_sync(0xffffffffu, c.wait(B_S + t, phase & 1))) return;
@@ -750,6 +752,13 @@ prefill_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         tma_prefetch_desc(&mk);
         if (kRope) tma_prefetch_desc(&mr);
         tma_prefetch_desc(&mv);
+    }
+    if (warp < 8 && (threadIdx.x & (kPreTile - 1)) >= p.tile_tokens * p.group) {
+        // rows that no query ever comes to
+        const int t = warp >> 2, r = threadIdx.x & (kPreTile - 1);
+        for (int i = 0; i < L::kChunks * 8; ++i)
+            sts128(smem_u32(c.base + (t * L::kChunks + i / 8) * kSlotBytes) + r * 128 + i % 8 * 16, 0, 0, 0, 0);
+        fence_proxy_async_smem();
     }
     if (warp == kMmaWarp) {
         tmem_alloc(&s_tmem, kTmemCols);
