@@ -596,7 +596,8 @@ __device__ void row_role(const PrefillParams &p, const Ctx &c, Items items, uint
     const int per = p.tile_tokens, in_tile = r / p.group, hh = r - in_tile * p.group;
     Item s;
     uint32_t phase = 0;  // steps of this tile so far
-    while (items.get(c, s)) {
+    bool more = items.get(c, s);
+    while (more) {
         const int head = s.head, steps = t ? s.steps_of[1] : s.steps_of[0];
         const int token = t * per + in_tile;
         const bool on = in_tile < per && token < s.tokens;
@@ -663,12 +664,14 @@ __device__ void row_role(const PrefillParams &p, const Ctx &c, Items items, uint
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const int64_t row = (int64_t)(s.q0 + token) * p.h_q + head * p.group + hh;
         const int64_t slot = (int64_t)s.part * p.h_kv + head;
+        const int part = s.part;
+        more = items.get(c, s);
         if (on) {
-            if (s.part < 0) p.lse[row] = lse;
+            if (part < 0) p.lse[row] = lse;
             else p.lse_part[slot * kPreRows + t * kPreTile + r] = lse;
         }
         if (steps == 0) {
-            if (on && s.part < 0)
+            if (on && part < 0)
                 for (int i = 0; i < kPreHead / 8; ++i) reinterpret_cast<uint4 *>(p.out + row * kPreHead)[i] = make_uint4(0, 0, 0, 0);
             continue;
         }
@@ -689,7 +692,7 @@ __device__ void row_role(const PrefillParams &p, const Ctx &c, Items items, uint
             for (int i1 = 0; i1 < 2; ++i1) {
                 const int i = 2 * i2 + i1;
                 uint32_t (&o)[32] = both[i1];
-                if (s.part < 0) {
+                if (part < 0) {
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         uint32_t w[8];
