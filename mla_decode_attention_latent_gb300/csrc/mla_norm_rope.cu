@@ -73,12 +73,13 @@ __device__ __forceinline__ float squares(uint4 x, float k = 1.f) {
 template <typename Sum>
 __device__ __forceinline__ float inverse_rms(Sum sum, int d, float eps) {
     float s = sum(1.f);
-    float inv = 1.f / sqrtf(s / (float)d + eps);
+    const float share = 1.f / (float)d;
+    float inv = rsqrtf(s * share + eps);
     const bool large = !(s < 0x1p120f), small = s < 0x1p-90f && eps < 0x1p-60f;
     if (__any_sync(0xffffffffu, large || small)) {
         const float k = large ? 0x1p-70f : 0x1p70f;
         s = sum(k);
-        if (large || small) inv = k / sqrtf(s / (float)d + eps * k * k);
+        if (large || small) inv = k * rsqrtf(s * share + eps * k * k);
     }
     return inv;
 }
@@ -88,6 +89,12 @@ __device__ __forceinline__ void scale8(float (&f)[8], uint4 w, float r) {
     widen8(w, g);
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] = f[i] * r * g[i];  // (x r first: at most sqrt(d))
+}
+
+__device__ __forceinline__ void turn(float &a, float &b, float c, float s) {
+    const float t = a;
+    a = t * c - b * s;
+    b = b * c + t * s;
 }
 
 // 8 values of the rotated part turned by the angles of their pairs.  Interleaved:
@@ -184,14 +191,39 @@ __global__ void __launch_bounds__(kThreads, kPairs == kReload ? 2 : kPieces <= 3
             }, p.d, p.eps);
         }
         const float2 *cs = s_angle + token * pairs;
+        if constexpr (kPairs == kOwn) {
+            // the halves are whole pieces of this lane: both are turned by the same angles
+            const int low = (rope0 - p.first / 8) / kGroup;
+            if (r >= count) continue;
+            float f[kPieces][8];
+#pragma unroll
+            for (int j = 0; j < kPieces; ++j) {
+                widen8(v.x[j], f[j]);
+                if constexpr (kNorm) scale8(f[j], s_weight[piece0 + kGroup * j], inv);
+            }
+#pragma unroll
+            for (int j = 0; j + 1 < kPieces; ++j) {
+                if (j != low) continue;
+                const float4 *from = reinterpret_cast<const float4 *>(cs + 8 * lane);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float4 two = from[k];
+                    turn(f[j][2 * k], f[j + 1][2 * k], two.x, two.y);
+                    turn(f[j][2 * k + 1], f[j + 1][2 * k + 1], two.z, two.w);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kPieces; ++j)
+                if (kNorm || j == low || j == low + 1) dst[piece0 + kGroup * j] = round8(f[j]);
+                else dst[piece0 + kGroup * j] = v.x[j];
+            continue;
+        }
 #pragma unroll
         for (int j = 0; j < kPieces; ++j) {
             const int at = piece0 + kGroup * j, part = at - rope0;
             const bool turned = part >= 0 && at < pieces, low = part < half;
             uint4 other = make_uint4(0, 0, 0, 0);
-            if constexpr (kPairs == kOwn) {
-                other = low ? v.x[j + 1 < kPieces ? j + 1 : j] : v.x[j > 0 ? j - 1 : 0];
-            } else if constexpr (kPairs == kOther) {
+            if constexpr (kPairs == kOther) {
                 if (__any_sync(0xffffffffu, turned)) {
                     other.x = __shfl_xor_sync(0xffffffffu, v.x[j].x, half);
                     other.y = __shfl_xor_sync(0xffffffffu, v.x[j].y, half);
@@ -234,7 +266,7 @@ template <int kGroup, int kPieces, bool kNorm>
 void (*heads_kernel(Pairs pairs))(NormRopeParams, int) {
     switch (pairs) {
         case kNeighbours: return norm_rope_kernel<kGroup, kPieces, kNorm, kNeighbours>;
-        case kOwn: return norm_rope_kernel<kGroup, kPieces, kNorm, kOwn>;
+        case kOwn: return norm_rope_kernel<kGroup, kPieces, kNorm, (kGroup == kNarrow && kPieces > 1) ? kOwn : kReload>;  // (halves of 64 values)
         case kOther: return norm_rope_kernel<kGroup, kPieces, kNorm, kOther>;
         default: return norm_rope_kernel<kGroup, kPieces, kNorm, kReload>;
     }
