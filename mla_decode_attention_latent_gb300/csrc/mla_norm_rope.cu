@@ -18,12 +18,18 @@
 // consecutive heads of consecutive tokens and computes the tokens' sines once, in
 // shared memory, for all of their heads.  Everything is loaded once and stays in
 // registers, the next head on its way while one is computed; the partner of a value in
-// the half layout comes from the lane that has it, or is loaded again where heads are cut
-// oddly, in both cases before anything of its head is stored, so that a call may be in place.
-// Bound by HBM on prompts and by the launch on single tokens.
+// the half layout is in the same lane (rotations of 128 values), comes from the lane that
+// has it, or is loaded again where heads are cut oddly, in all cases before anything of its
+// head is stored, so that a call may be in place.
+// Bound by HBM on prompts (4096 tokens of 128 heads of 192 values: 68.6 us, 5.9 TB/s), by
+// the launch on single tokens (64 tokens: 2.1 us), and between them, where the rows come out
+// of L2, by issue slots (1777 tokens of 40 heads of 128: 8.6 us; two heads under way per
+// group instead of one gained nothing).
 //
 // Rows: a warp per cached row, the 512 latent dims as 64 pieces over its lanes and
-// the RoPE key as 8 more; each lane computes one of the row's 32 angles.
+// the RoPE key as 8 more; each lane computes one of the row's 32 angles.  A step of 64 rows
+// takes 1.8 us, 5000 bf16 rows 4.1, 32,768 rows into e4m3 pages 17.6 (3.2 TB/s: two thirds of
+// the issue slots, the quotients above all).
 #include <cuda_runtime.h>
 
 #include "mla_internal.h"
@@ -281,8 +287,8 @@ cudaError_t launch_heads(const NormRopeParams &p, cudaStream_t stream) {
     cudaError_t e = device_sm_count(&sms);
     if (e != cudaSuccess) return e;
     // as many turns of the groups as leave about kCtas CTAs per SM, at most kTurns: they share
-    // the tokens' angles (1777 tokens of 40 heads of 128: 1 / 4 / 8 turns 13.6 / 12.7 / 11.8 us;
-    // 4096 tokens of 128 heads of 192: 115 / 80.8 / 80.7, 32 turns 99.7 with the last CTAs alone)
+    // the tokens' angles (at most 1 / 4 / 8 / 16 turns: 1777 tokens of 40 heads of 128 10.5 / 9.0 /
+    // 8.6 / 8.6 us, 4096 tokens of 128 heads of 192 81.8 / 68.8 / 68.7 / 69.0)
     constexpr int64_t kCtas = 3, kTurns = 8;
     const int64_t turns = (rows + kGroups * kCtas * sms - 1) / (kGroups * kCtas * sms);
     int per_cta = kGroups * (int)(turns < kTurns ? turns : kTurns);

@@ -18,7 +18,8 @@
 // One cluster of up to 8 CTAs runs the call: the words that are read by all and
 // may be updated in place (the lengths, the count of free pages) are written
 // behind a cluster barrier, so one launch does it and no workspace is kept.
-// Bound by latency: a chunk's lengths and bounds, its scan, one page id per row.
+// Bound by latency: a chunk's lengths and bounds, its scan, one page id per row.  64 sequences
+// of one row each take 4.6 us, 48 prompts of up to 4096 rows (100,000 rows) 11.
 #include <cuda_runtime.h>
 
 #include "mla_internal.h"

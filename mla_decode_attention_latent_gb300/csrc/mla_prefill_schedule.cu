@@ -20,10 +20,10 @@
 // of a moment then share no keys in L2.)
 //
 // One CTA.  Up to 1280 blocks, as many as there are where any is cut, are kept in shared
-// memory and sorted by counting, for each segment, those before it, which is stable: the
-// same call always cuts the same blocks.  More blocks are gone through twice (how many
-// have each length; their places), in an order of equal ones that has no influence on
-// a result.
+// memory; more are gone through twice.  The segments are put in order by counting how
+// many have each length (a rank for each, a loop over all, took 1.4 us longer for 200
+// blocks); the order of equal ones has no influence on a result.  12 prompts of 200 blocks take
+// 4 us, 9 where cuts are looked for.
 #include <cuda_runtime.h>
 
 #include <mutex>
@@ -35,11 +35,11 @@
 namespace mla {
 namespace {
 
-constexpr int kFixed = 8;        // units of an item beside its steps (2 / 4 / 8: three chunks 86 / 86 / 83 us)
+constexpr int kFixed = 8;        // units of an item beside its steps (2 / 4 / 8 / 12: three chunks 86 / 86 / 84 / 84 us)
 constexpr int kCombine = 3;      // units of the combine
 constexpr int kLeastPart = 4;    // steps of a part
 constexpr int kLengths = 1024;   // lengths that the counting sort tells apart
-constexpr int kStable = 1280;    // blocks or segments that are sorted stably: as many as there are where any is cut
+constexpr int kKept = 1280;      // blocks or segments kept in shared memory: as many as there are where any is cut
 constexpr int kMany = 1024, kFew = 256;  // threads; few: for as many sequences and blocks, whose barriers cost less
 
 template <int kThreads>
@@ -47,14 +47,13 @@ struct Shared {
     long long warp[kThreads / 32];
     long long end[kThreads];     // blocks up to and with each sequence of the chunk
     int q[kThreads], lq[kThreads], k[kThreads], lk[kThreads];
-    int count[kThreads == kMany ? kLengths : 1];  // blocks of each length; then their first place
+    int count[kLengths];         // blocks or segments of each length, longest first; then the next one's place
     int scan[kThreads / 32];
-    unsigned long long steps;    // of all blocks
     int cost[32];                // estimates of the values of c
     int cuts, parts;
-    PreSegment block[kStable];
-    int first[kStable];          // segments before each block
-    int length[kStable];         // of each segment
+    PreSegment block[kKept];
+    int first[kKept];            // segments before each block
+    int length[kKept], owner[kKept];  // of each segment, and its block
 };
 
 // f(block, its index) for every block, the threads sharing the blocks of kThreads sequences at a time; their number
@@ -125,26 +124,35 @@ __global__ void __launch_bounds__(kThreads) prefill_schedule_kernel(const Prefil
     sm103::griddep_wait();
     const PreWork work(p.metadata, p.max_blocks, p.sms);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if constexpr (kThreads == kMany) sh.count[threadIdx.x] = 0;
+    for (int i = threadIdx.x; i < kLengths; i += kThreads) sh.count[i] = 0;
     if (threadIdx.x == 0) {
         sh.cuts = sh.parts = 0;
-        sh.steps = 0;
     }
     __syncthreads();
-    // most steps first: bucket 0 holds the longest
+    // places instead of numbers, from the longest on
+    auto to_places = [&] {
+        constexpr int kOwn = kLengths / kThreads;
+        int here[kOwn], sum = 0, total;
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) sum += here[i] = sh.count[threadIdx.x * kOwn + i];
+        int at = block_exclusive_scan<kThreads>(sum, sh.scan, &total);
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) {
+            sh.count[threadIdx.x * kOwn + i] = at;
+            at += here[i];
+        }
+        __syncthreads();
+    };
     auto bucket = [](int steps) { return kLengths - 1 - min(steps, kLengths - 1); };
-    unsigned long long steps = 0;
+    long long steps = 0;  // of this thread's blocks
     const long long found = each_block(p, sh, false, [&](const PreSegment &x, long long i) {
-        if (i < kStable) sh.block[i] = x;
+        if (i < kKept) sh.block[i] = x;
         if constexpr (kThreads == kMany) atomicAdd(&sh.count[bucket(x.step1)], 1);
         steps += x.step1;
     });
     const int blocks = (int)min(found, (long long)p.max_blocks);
-    if (kThreads == kMany && blocks > kStable) {
-        int total;
-        const int here = sh.count[threadIdx.x];
-        sh.count[threadIdx.x] = block_exclusive_scan<kThreads>(here, sh.scan, &total);
-        __syncthreads();
+    if (kThreads == kMany && blocks > kKept) {
+        to_places();
         each_block(p, sh, true, [&](const PreSegment &x, long long i) {
             const int at = atomicAdd(&sh.count[bucket(x.step1)], 1);
             if (at < blocks) work.segments[at] = x;
@@ -156,11 +164,11 @@ __global__ void __launch_bounds__(kThreads) prefill_schedule_kernel(const Prefil
         return;
     }
     int most = 0x7fffffff;  // c
-    if (blocks > 0 && pre_may_cut(p.max_blocks, p.num_k, p.h_kv, p.sms) && kPreRounds * p.sms <= kStable) {
-        if (steps) atomicAdd(&sh.steps, steps);
-        __syncthreads();
+    if (blocks > 0 && pre_may_cut(p.max_blocks, p.num_k, p.h_kv, p.sms) && kPreRounds * p.sms <= kKept) {
+        long long all_steps;
+        block_exclusive_scan<kThreads>(steps, sh.warp, &all_steps);
         // values of c, one per warp at a time: the last none, the others from a quarter to four times an even share
-        const float share = (float)sh.steps * p.h_kv / p.sms;
+        const float share = (float)all_steps * p.h_kv / p.sms;
         auto value = [&](int w) { return w == 31 ? 0x7fffffff : max(kLeastPart, (int)ceilf(fminf(share * exp2f((float)w * (4.f / 30.f) - 2.f), 1e9f))); };
         for (int w = warp; w < 32; w += kThreads / 32) {
             const int c = value(w);
@@ -193,7 +201,10 @@ __global__ void __launch_bounds__(kThreads) prefill_schedule_kernel(const Prefil
         const unsigned mine = (unsigned)sh.cost[lane] * 32 + lane, least = __reduce_min_sync(0xffffffffu, mine);
         if ((long long)(least / 32) * 8 < (long long)sh.cost[31] * 7) most = value(least % 32);
     }
-    // segments: where each block's begin, and their lengths
+    if constexpr (kThreads == kMany) {
+        for (int i = threadIdx.x; i < kLengths; i += kThreads) sh.count[i] = 0;
+    }
+    // where each block's segments begin
     int segments = 0;
     for (int c0 = 0; c0 < blocks; c0 += kThreads) {
         const int i = c0 + threadIdx.x;
@@ -202,7 +213,6 @@ __global__ void __launch_bounds__(kThreads) prefill_schedule_kernel(const Prefil
         int total;
         const int first = segments + block_exclusive_scan<kThreads>(n, sh.scan, &total);
         if (i < blocks) sh.first[i] = first;
-        if (n == 1) sh.length[first] = shorter;
         if (n > 1) {
             const int part = atomicAdd(&sh.parts, n);  // (which slots a block has makes no difference)
             sh.block[i].part = part;
@@ -211,7 +221,7 @@ __global__ void __launch_bounds__(kThreads) prefill_schedule_kernel(const Prefil
         segments += total;
     }
     __syncthreads();
-    // a thread per segment: its block, its part of it, its place among all by length
+    // a thread per segment: its block and its part of it, then its place
     for (int at = threadIdx.x; at < segments; at += kThreads) {
         int i = 0, hi = blocks;  // first[i] <= at < first[i + 1]
         while (hi - i > 1) {
@@ -221,25 +231,22 @@ __global__ void __launch_bounds__(kThreads) prefill_schedule_kernel(const Prefil
         }
         int shorter, longer;
         cut(sh.block[i].step1, most, shorter, longer);
-        sh.length[at] = shorter + (at - sh.first[i] < longer);
+        const int mine = shorter + (at - sh.first[i] < longer);
+        sh.length[at] = mine;
+        sh.owner[at] = i;
+        atomicAdd(&sh.count[bucket(mine)], 1);
     }
     __syncthreads();
+    to_places();
     for (int at = threadIdx.x; at < segments; at += kThreads) {
-        int i = 0, hi = blocks;
-        while (hi - i > 1) {
-            const int mid = (i + hi) >> 1;
-            if (sh.first[mid] <= at) i = mid;
-            else hi = mid;
-        }
-        int shorter, longer;
-        const int n = cut(sh.block[i].step1, most, shorter, longer), k = at - sh.first[i], mine = sh.length[at];
-        int rank = 0;
-        for (int other = 0; other < segments; ++other) rank += sh.length[other] + (other < at) > mine;
+        const int i = sh.owner[at], mine = sh.length[at], k = at - sh.first[i];
         PreSegment x = sh.block[i];
+        int shorter, longer;
+        const int n = cut(x.step1, most, shorter, longer);
         x.step0 = k * shorter + min(k, longer);
         x.step1 = x.step0 + mine;
         x.part = n > 1 ? x.part + k : -1;
-        work.segments[rank] = x;
+        work.segments[atomicAdd(&sh.count[bucket(mine)], 1)] = x;
     }
     if (threadIdx.x == 0) {
         work.header->segments = segments;
@@ -270,7 +277,8 @@ cudaError_t launch(const PrefillParams &p, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_prefill_schedule(const PrefillParams &p, cudaStream_t stream) {
-    return p.batch <= kFew && p.max_blocks <= kFew ? launch<kFew>(p, stream) : launch<kMany>(p, stream);
+    const bool few = p.batch <= kFew && p.max_blocks <= kFew;
+    return few ? launch<kFew>(p, stream) : launch<kMany>(p, stream);
 }
 
 }  // namespace mla
