@@ -353,13 +353,13 @@ def _need_rows(name: str, t: torch.Tensor, cols: int, n: int, dev: torch.device,
     """bf16 [n, cols] with unit inner stride, 16-byte aligned rows; returns the row stride in elements."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if t.device != dev:
+    if t.dtype != torch.bfloat16 or t.device != dev:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+        if t.dtype != torch.bfloat16:
+            raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
         _same_device(dev, "cache", **{name: t})
-    if t.dim() != 2 or t.shape[0] != n or t.shape[1] != cols:
+    if t.shape != (n, cols):
         raise ValueError(f"{name} must be [{n}, {cols}]")
     stride, inner = t.stride()
     if n <= 1:
@@ -411,7 +411,7 @@ _FP8_PAGE = _lib.MLA_FP8_PAGE_BYTES(_lib.MLA_HEAD_DIM)
 def _vector(dev: torch.device, of: str, name: str, t: torch.Tensor, n: int) -> int:
     """Check an int32 [n] on ``dev``; returns its address."""
     ptr = _on(dev, of, name, t, torch.int32)
-    if t.dim() != 1 or t.shape[0] != n:
+    if t.shape != (n,):
         raise ValueError(f"{name} must be [{n}]")
     return ptr
 
@@ -788,7 +788,7 @@ def _free_list(dev, free_pages, num_free):
 def _slots(dev, of, slots, n):
     """Check an int64 [n] of slots; returns its address."""
     ptr = _on(dev, of, "slots", slots, torch.int64)
-    if slots.dim() != 1 or slots.shape[0] != n:
+    if slots.shape != (n,):
         raise ValueError(f"slots must be [{n}]")
     return ptr
 
@@ -812,7 +812,7 @@ def mla_rope_turns(rope_dim: int, base: float = 10000.0, factor: float = 1.0, or
 def _weight(dev, of, weight, d):
     """Check a norm's weight (bf16 [d]); returns its address."""
     ptr = _on(dev, of, "weight", weight, torch.bfloat16)
-    if weight.dim() != 1 or weight.shape[0] != d:
+    if weight.shape != (d,):
         raise ValueError(f"weight must be [{d}]")
     if ptr % 16:
         raise ValueError("weight must be 16-byte aligned")
@@ -887,13 +887,15 @@ def _place_rows(call, latent, k_rope, positions, turns, slots, cache, weight, ep
     if fp8:
         _need_cuda("kv_pages", cache, torch.uint8)
         d = _lib.MLA_HEAD_DIM
-        if cache.dim() != 2 or cache.shape[1] != _FP8_PAGE:
+        shape = cache.shape
+        if len(shape) != 2 or shape[1] != _FP8_PAGE:
             raise ValueError(f"kv_pages must be [num_blocks, {_FP8_PAGE}]")
     else:
         _need_cuda("kcache", cache, torch.bfloat16)
-        if cache.dim() != 4 or cache.shape[1] != _lib.MLA_PAGE_SIZE or cache.shape[2] != 1:
+        shape = cache.shape
+        if len(shape) != 4 or shape[1] != _lib.MLA_PAGE_SIZE or shape[2] != 1:
             raise ValueError("kcache must be [num_blocks, 64, 1, d]")
-        d = cache.shape[3]
+        d = shape[3]
     dev = cache.device
     n, rope = _row_count(latent), d - MLA_V_DIM
     ls = _need_rows("latent", latent, MLA_V_DIM, n, dev, False)
@@ -914,7 +916,7 @@ def _place_rows(call, latent, k_rope, positions, turns, slots, cache, weight, ep
     if k_rope_out is not None:
         ros, ro = _need_rows("k_rope_out", k_rope_out, rope, n, dev, True), k_rope_out.data_ptr()
     _call(call, dev, latent.data_ptr(), ls, rope_ptr, rs, n, w, eps, pos, trn, 1 if interleaved else 0, rope_scale, at, cache.data_ptr(),
-          cache.shape[0], d, lo, los, ro, ros)
+          shape[0], d, lo, los, ro, ros)
 
 
 def mla_norm_rope_cache_write(latent: torch.Tensor, k_rope: Optional[torch.Tensor], positions: Optional[torch.Tensor],
