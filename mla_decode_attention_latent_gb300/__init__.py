@@ -7,7 +7,10 @@ an LSE-weighted combine.  Around them: kernels that write and read the cache
 (``mla_cache_write`` / ``mla_cache_read``), keep a key per page and decode over
 the pages that a score selects (``mla_update_page_keys``,
 ``mla_decode_kvcache_blocks``), and decode trees of drafted tokens
-(``mla_decode_kvcache_tree``).  This package is the thin
+(``mla_decode_kvcache_tree``).  Before the decode: kernels that assign pages to
+requests (``mla_assign_pages``), normalise and rotate heads (``mla_norm_rope``),
+place normalised and rotated rows in the cache (``mla_norm_rope_cache_write``) and
+attend over packed prompts (``mla_prefill``).  This package is the thin
 Python binding (``api``), the in-tree build (``build``) and the seeded
 workload generator (``workloads``).
 """
