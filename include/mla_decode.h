@@ -625,7 +625,8 @@ MLA_API int mla_assign_pages(const int32_t *cache_seqlens, const int32_t *cu_row
  *   num_blocks     pages of the pool
  *   free_pages, max_free, num_free   as for mla_assign_pages, all in/out
  * An entry outside [0, num_blocks) is not pushed (MLA_DEVERR_BLOCK_ID); pages past
- * max_free are dropped (MLA_DEVERR_SEQLEN).  Errors: as mla_assign_pages.
+ * max_free are dropped (MLA_DEVERR_SEQLEN).  Uses of a page are not counted: one that
+ * several finished sequences name is pushed by each.  Errors: as mla_assign_pages.
  */
 MLA_API int mla_release_pages(int32_t *cache_seqlens, const int32_t *finished, int batch, int32_t *block_table,
                               int max_blocks_per_seq, int64_t num_blocks, int32_t *free_pages, int64_t max_free,
@@ -760,7 +761,8 @@ MLA_API int mla_get_metadata_prefill(const int32_t *cu_q, const int32_t *cu_k, i
  * Keys and values that some row of their sequence sees must be finite (one that is not
  * makes the rows that see it NaN, and may make those of the same 128-row tile); other
  * rows of k, k_rope and v may hold any bits.  A query row that is not finite leaves the
- * other rows as they are.
+ * other rows as they are.  Weights are summed against a reference that the largest may pass
+ * by 2^20, so values beyond 2^100 may overflow where the exact o would not.
  * Up to three kernels are enqueued (partition, attention, combine of cut blocks).  Stream
  * order and graph capture: as for mla_decode_kvcache.  Errors: MLA_ERR_INVALID_ARG,
  * MLA_ERR_UNSUPPORTED (widths, 2^30 rows), MLA_ERR_WORKSPACE, MLA_ERR_CUDA.

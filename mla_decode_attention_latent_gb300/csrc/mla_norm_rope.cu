@@ -97,10 +97,14 @@ __device__ __forceinline__ void scale8(float (&f)[8], uint4 w, float r) {
     for (int i = 0; i < 8; ++i) f[i] = f[i] * r * g[i];  // (x r first: at most sqrt(d))
 }
 
-__device__ __forceinline__ void turn(float &a, float &b, float c, float s) {
-    const float t = a;
-    a = t * c - b * s;
-    b = b * c + t * s;
+// A pair turned: rounded the same way wherever a partner comes from, so that a call in place has
+// the bits of one that is not.
+__device__ __forceinline__ float turned_low(float a, float b, float2 t) { return __fmaf_rn(a, t.x, -__fmul_rn(b, t.y)); }
+__device__ __forceinline__ float turned_high(float a, float b, float2 t) { return __fmaf_rn(b, t.x, __fmul_rn(a, t.y)); }
+__device__ __forceinline__ void turn(float &a, float &b, float2 t) {
+    const float x = a;
+    a = turned_low(x, b, t);
+    b = turned_high(x, b, t);
 }
 
 // 8 values of the rotated part turned by the angles of their pairs.  Interleaved:
@@ -109,14 +113,10 @@ template <bool kInterleaved>
 __device__ __forceinline__ void rotate8(float (&f)[8], const float (&other)[8], const float2 (&cs)[8], bool low) {
     if constexpr (kInterleaved) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float a = f[2 * k], b = f[2 * k + 1];
-            f[2 * k] = a * cs[k].x - b * cs[k].y;
-            f[2 * k + 1] = b * cs[k].x + a * cs[k].y;
-        }
+        for (int k = 0; k < 4; ++k) turn(f[2 * k], f[2 * k + 1], cs[k]);
     } else {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) f[k] = low ? f[k] * cs[k].x - other[k] * cs[k].y : f[k] * cs[k].x + other[k] * cs[k].y;
+        for (int k = 0; k < 8; ++k) f[k] = low ? turned_low(f[k], other[k], cs[k]) : turned_high(other[k], f[k], cs[k]);
     }
 }
 
@@ -214,8 +214,8 @@ __global__ void __launch_bounds__(kThreads, kPairs == kReload ? 2 : kPieces <= 3
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const float4 two = from[k];
-                    turn(f[j][2 * k], f[j + 1][2 * k], two.x, two.y);
-                    turn(f[j][2 * k + 1], f[j + 1][2 * k + 1], two.z, two.w);
+                    turn(f[j][2 * k], f[j + 1][2 * k], make_float2(two.x, two.y));
+                    turn(f[j][2 * k + 1], f[j + 1][2 * k + 1], make_float2(two.z, two.w));
                 }
             }
 #pragma unroll

@@ -268,3 +268,21 @@ def test_pages_beyond_32_bits(dev):
     for i, s in enumerate(slots.tolist()):
         assert torch.equal(pages[s // PAGE, (s % PAGE) * 576:(s % PAGE + 1) * 576], few[0, i * 576:(i + 1) * 576])
     assert mla.mla_device_status() == 0
+
+
+@pytest.mark.parametrize("d", [128, 136, 192, 256, 320])
+@pytest.mark.parametrize("norm", [False, True])
+def test_rotations_of_128_values(dev, d, norm):
+    """Halves of 64 values: in a lane's own pieces where the head has whole ones before them, elsewhere not."""
+    g = torch.Generator().manual_seed(d)
+    x = torch.randn((41, 5, d + 8), generator=g).to(torch.bfloat16).to(dev)[..., :d]
+    w = (1 + 0.5 * torch.randn((d,), generator=g)).to(torch.bfloat16).to(dev) if norm else None
+    turns = mla.mla_rope_turns(128, 5e5, 8.0, 8192, device=dev)
+    pos = torch.randint(0, 1 << 20, (41,), generator=g, dtype=torch.int32).to(dev)
+    got = mla.mla_norm_rope(x, pos, turns, weight=w, rope_scale=0.75)
+    near(got, *formula(x, pos, turns, w, 1e-6, False, 0.75))
+    if not norm:
+        assert torch.equal(got[..., :d - 128], x[..., :d - 128])
+    y = x.clone()
+    mla.mla_norm_rope(y, pos, turns, weight=w, rope_scale=0.75, out=y)
+    assert torch.equal(y, got)

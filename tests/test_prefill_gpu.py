@@ -307,3 +307,38 @@ def test_rows_beyond_32_bits(dev):
     check(out[-260:], lse[-260:], q[-260:], k[-260:], v[-260:], None, [260], [260], True, heads=[0, 77, 127])
     assert (out[:-260] == 5).all()
     assert mla.mla_device_status() == 0
+
+
+@pytest.mark.parametrize("hq,hkv", [(4, 4), (6, 2), (10, 2), (7, 1), (100, 2)])
+def test_tiles_with_rows_of_no_query(dev, hq, hkv):
+    """Tiles that groups do not fill, or that end inside a sequence, whose other rows are the next sequence's: finite or not."""
+    lq, lk = [20, 140, 33, 129, 1, 270], [300, 140, 700, 129, 400, 1500]
+    q, k, v, kr = make(dev, lq, lk, hq, hkv, True, seed=hq)
+    out, lse = mla.mla_prefill(q, k, v, cu_of(lq, dev), cu_of(lk, dev), k_rope=kr)
+    check(out, lse, q, k, v, kr, lq, lk, True)
+    at = cu_of(lq, dev).tolist()
+    for bad in (math.nan, math.inf, 3e38):
+        for odd in (0, 1):
+            q2 = q.clone()
+            for b in range(odd, len(lq), 2):
+                q2[at[b]:at[b + 1]] = bad
+            o2, l2 = mla.mla_prefill(q2, k, v, cu_of(lq, dev), cu_of(lk, dev), k_rope=kr)
+            for b in range(1 - odd, len(lq), 2):
+                assert torch.equal(o2[at[b]:at[b + 1]], out[at[b]:at[b + 1]]) and torch.equal(l2[at[b]:at[b + 1]], lse[at[b]:at[b + 1]])
+    assert mla.mla_device_status() == 0
+
+
+def test_weights_that_outgrow_their_reference_in_either_half(dev):
+    """Ordinary steps (no mask) in which some row's scores rise far in the first or the second 64 keys of a step."""
+    n, m = 150, 128 * 8
+    q, k, v, _ = make(dev, [n], [m], 2, 2, False, seed=21, gain=0.5)
+    up = torch.zeros((m,), device=dev)
+    for at, height in ((128 * 2 + 3, 30.0), (128 * 3 + 70, 65.0), (128 * 5, 66.0), (128 * 6 + 64, 110.0)):
+        up[at:] = height
+    q[..., 0] = 0
+    q[::3, :, 0] = 128 ** 0.5  # a row in three climbs, the others stay
+    k[..., 0] = up[:, None].to(torch.bfloat16)
+    for causal in (False, True):
+        out, lse = mla.mla_prefill(q, k, v, cu_of([n], dev), cu_of([m], dev), causal=causal)
+        check(out, lse, q, k, v, None, [n], [m], causal)
+    assert mla.mla_device_status() == 0
