@@ -15,12 +15,14 @@
 // Everything follows from prefix sums of the need, which every CTA computes for
 // itself, so nothing is exchanged between CTAs: the page of a position is an
 // entry of the table as it was (have_b and below) or an entry of the free list.
-// One cluster of up to 8 CTAs runs the call: the words that are read by all and
+// One cluster of up to 16 CTAs runs the call: the words that are read by all and
 // may be updated in place (the lengths, the count of free pages) are written
 // behind a cluster barrier, so one launch does it and no workspace is kept.
 // Bound by latency: a chunk's lengths and bounds, its scan, one page id per row.  64 sequences
-// of one row each take 4.6 us, 48 prompts of up to 4096 rows (100,000 rows) 11.
+// of one row each take 4.6 us, 48 prompts of up to 4096 rows (83,794) 8.2, and 12.4 on 8 CTAs.
 #include <cuda_runtime.h>
+
+#include <mutex>
 
 #include "mla_internal.h"
 #include "mla_schedule.cuh"
@@ -31,7 +33,7 @@ namespace {
 
 constexpr int kThreads = 1024;  // also the sequences of a chunk
 constexpr int kFewThreads = 128;  // of a call with few sequences and rows, whose barriers cost less
-constexpr int kMaxCtas = 8;     // portable cluster size
+constexpr int kPortableCtas = 8, kMostCtas = 16;  // of a cluster
 constexpr int kRun = 4;         // consecutive rows of a thread: one search, and mostly one page
 constexpr int kRunsInFlight = 2;
 
@@ -241,9 +243,44 @@ __global__ void __launch_bounds__(kThreads) release_pages_kernel(const ReleasePa
 
 }  // namespace
 
+// CTAs of the cluster of a call with many rows: 16 where the device takes such a cluster, or 8, which all do
+static cudaError_t many_ctas(int *ctas) {
+    constexpr int kMaxDevices = 64;
+    static std::mutex mutex;
+    static int known[kMaxDevices] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lock(mutex);
+    if (!known[dev]) {
+        e = cudaFuncSetAttribute(assign_pages_kernel<kThreads>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(kMostCtas);
+        cfg.blockDim = dim3(kThreads);
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = kMostCtas;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        int clusters = 0;
+        e = cudaOccupancyMaxActiveClusters(&clusters, assign_pages_kernel<kThreads>, &cfg);
+        if (e != cudaSuccess) return e;
+        known[dev] = clusters > 0 ? kMostCtas : kPortableCtas;
+    }
+    *ctas = known[dev];
+    return cudaSuccess;
+}
+
 cudaError_t launch_assign_pages(const AssignPagesParams &p, cudaStream_t stream) {
     const bool few = p.num_rows <= 4 * kFewThreads * kRun && p.batch <= kFewThreads;
-    const int ctas = few || p.num_rows <= kThreads * kRun ? 1 : kMaxCtas;
+    int ctas = few || p.num_rows <= kThreads * kRun ? 1 : kPortableCtas;
+    if (p.num_rows > kPortableCtas * kThreads * kRun) {
+        const cudaError_t e = many_ctas(&ctas);
+        if (e != cudaSuccess) return e;
+    }
     // whole runs are stored at once where the outputs allow it
     const bool wide = ((reinterpret_cast<uintptr_t>(p.positions) | reinterpret_cast<uintptr_t>(p.slots)) & 15) == 0;
     cudaLaunchConfig_t cfg = {};
