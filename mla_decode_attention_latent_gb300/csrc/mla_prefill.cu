@@ -595,6 +595,10 @@ __device__ __forceinline__ void store32(void *dst, const uint32_t (&w)[8]) {
                  : "memory");
 }
 
+// kWholeSteps: the two halves of a step in sight in one go, half 1's first scores under way while half 0's last are
+// weighed (all keys, d_qk = 128: 317 us against 336). At d_qk = 192 the MMAs set the pace, and half the code, for either
+// half, is better: prompt of 4096 at 128 heads 434 against 438, forty prompts of 300 62.7 against 64.6.
+template <bool kWholeSteps>
 __device__ void row_role(const PrefillParams &p, const Ctx &c, Items items, uint32_t tmem, int t) {
     const int warp = threadIdx.x >> 5, r = threadIdx.x & (kPreTile - 1);
     const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
@@ -615,9 +619,14 @@ __device__ void row_role(const PrefillParams &p, const Ctx &c, Items items, uint
             if (!__all_sync(0xffffffffu, c.wait(B_S + t, phase & 1))) return;
             tc_fence_after();
             const int ahead = seen - (s.step0 + j) * kPreTile;
+            auto handed = [&](int h) {
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(c.bar(B_P + 2 * t + h));
+            };
             int h = 0;
-            if (!__any_sync(0xffffffffu, j == 0 || ahead < kPreTile || m == -INFINITY)) {
-                // the ordinary step: 32 scores are on their way while 32 are weighed
+            if (kWholeSteps && !__any_sync(0xffffffffu, j == 0 || ahead < kPreTile || m == -INFINITY)) {
+                // 32 scores are on their way while 32 are weighed
                 uint32_t x0[32], x1[32], w[32];
                 Weigh first(m, p.scale_log2), second(m, p.scale_log2);
                 tmem_ld32(s_col, x0);
@@ -634,9 +643,7 @@ __device__ void row_role(const PrefillParams &p, const Ctx &c, Items items, uint
                 if (good) {
                     tmem_ld32(s_col + 96, x1);
                     second(x0, w);
-                    tmem_wait_st();
-                    tc_fence_before();
-                    mbar_arrive(c.bar(B_P + 2 * t));
+                    handed(0);
                     arrived(x1);
                     second(x1, w + 16);
                     const float sum1 = second.total();
@@ -645,24 +652,39 @@ __device__ void row_role(const PrefillParams &p, const Ctx &c, Items items, uint
                     if (__all_sync(0xffffffffu, sum1 <= kMostWeight)) {
                         tmem_st32(s_col + 32, w);
                         l += sum1;
-                        tmem_wait_st();
-                        tc_fence_before();
-                        mbar_arrive(c.bar(B_P + 2 * t + 1));
+                        handed(1);
                         h = 2;
                     }
                 }
             }
 #pragma unroll 1
             for (; h < 2; ++h) {
-                // products so far: the step before's, or this step's first half
-                const Half x = {s_col + 64 * h, o_col, s_col + 32 * h, ahead - 64 * h, m, l, j + h == 0};
-                const State y = careful_half(x, p.scale_log2, j + h == 0 ? nullptr : c.bar((h ? B_PV0 : B_PV) + t), (h ? phase : phase - 1) & 1, c.status);
-                if (!y.ok) return;
-                m = y.m;
-                l = y.l;
-                tmem_wait_st();
-                tc_fence_before();
-                mbar_arrive(c.bar(B_P + 2 * t + h));
+                bool weighed = false;
+                if (!kWholeSteps && !__any_sync(0xffffffffu, j + h == 0 || ahead - 64 * h < 64 || m == -INFINITY)) {
+                    uint32_t x0[32], x1[32], w[32];
+                    Weigh weigh(m, p.scale_log2);
+                    tmem_ld32(s_col + 64 * h, x0);
+                    arrived(x0);
+                    tmem_ld32(s_col + 64 * h + 32, x1);
+                    weigh(x0, w);
+                    arrived(x1);
+                    weigh(x1, w + 16);
+                    const float sum = weigh.total();
+                    weighed = __all_sync(0xffffffffu, sum <= kMostWeight);
+                    if (weighed) {
+                        tmem_st32(s_col + 32 * h, w);
+                        l += sum;
+                    }
+                }
+                if (!weighed) {
+                    // products so far: the step before's, or this step's first half
+                    const Half x = {s_col + 64 * h, o_col, s_col + 32 * h, ahead - 64 * h, m, l, j + h == 0};
+                    const State y = careful_half(x, p.scale_log2, j + h == 0 ? nullptr : c.bar((h ? B_PV0 : B_PV) + t), (h ? phase : phase - 1) & 1, c.status);
+                    if (!y.ok) return;
+                    m = y.m;
+                    l = y.l;
+                }
+                handed(h);
             }
         }
         // epilogue: o = O / l, lse
@@ -789,7 +811,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             tmem_wait_st();
         }
         griddep_wait();
-        row_role(p, c, items, tmem, warp >> 2);
+        row_role<!kRope>(p, c, items, tmem, warp >> 2);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         griddep_wait();
