@@ -22,12 +22,12 @@
 //             another sequence (weight 0 times an infinity would be NaN)
 // Products stop at multiples of 16 keys behind the last one that a tile sees.
 //
-// Bound by the tensor cores and what their turns leave idle: a step of both tiles is 2 x 128 x 128
-// x (d_qk + 128) products, 2560 cycles at d_qk = 192 of the 3300 that it takes, against
-// about 1000 issue slots per scheduler for the rows.  4096 tokens of 128 heads (d_qk = 192,
-// causal) 442-455 us, 1.55 PFLOP/s; d_qk = 128 without a mask 1.7.  A few rows behind long
-// contexts are bound by the loads, 3.2-3.7 TB/s: beside a step in use the ring has room for a
-// part of the next.
+// Bound by the tensor cores' operands: a step of both tiles is 2 x 128 x 128 x (d_qk + 128)
+// products, 2560 cycles at d_qk = 192, and takes 3280, as QK's MMAs read 8 KB of shared
+// memory each, as much as there is in their 64 cycles, and take 85.  4096 tokens of 128 heads
+// (d_qk = 192, causal) 435-455 us, 1.58 PFLOP/s; d_qk = 128 without a mask 1.7.  A few rows
+// behind long contexts take the same 2 us a step, on as many CTAs as equal parts give (4.1
+// TB/s of keys and values).
 //
 // The code is kept small: a CTA's roles share an instruction cache, and what comes once per
 // item (a first step, the output) is fetched anew each time.  The same work with its loops
