@@ -334,9 +334,12 @@ def _call(name: str, dev: torch.device, *args) -> None:
         check(name, st)
 
 
+_Tensor, _INT32, _INT64, _BF16 = torch.Tensor, torch.int32, torch.int64, torch.bfloat16
+
+
 def _on(dev: torch.device, of: str, name: str, t: torch.Tensor, dtype: torch.dtype) -> int:
     """Check a contiguous CUDA tensor on ``dev``; returns its address."""
-    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.device == dev and t.is_contiguous()):
+    if not (isinstance(t, _Tensor) and t.dtype is dtype and t.device == dev and t.is_contiguous()):
         _need_cuda(name, t, dtype)
         _same_device(dev, of, **{name: t})
     return t.data_ptr()
@@ -351,9 +354,9 @@ def _pairs(index: int) -> int:
 # ---------------------------------------------------------------- cache rows
 def _need_rows(name: str, t: torch.Tensor, cols: int, n: int, dev: torch.device, written: bool) -> int:
     """bf16 [n, cols] with unit inner stride, 16-byte aligned rows; returns the row stride in elements."""
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.bfloat16 or t.device != dev:
+    if t.dtype is not _BF16 or t.device != dev:
         if not t.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
         if t.dtype != torch.bfloat16:
@@ -410,10 +413,11 @@ _FP8_PAGE = _lib.MLA_FP8_PAGE_BYTES(_lib.MLA_HEAD_DIM)
 
 def _vector(dev: torch.device, of: str, name: str, t: torch.Tensor, n: int) -> int:
     """Check an int32 [n] on ``dev``; returns its address."""
-    ptr = _on(dev, of, name, t, torch.int32)
+    if not (isinstance(t, _Tensor) and t.dtype is _INT32 and t.device == dev and t.is_contiguous()):
+        _on(dev, of, name, t, _INT32)
     if t.shape != (n,):
         raise ValueError(f"{name} must be [{n}]")
-    return ptr
+    return t.data_ptr()
 
 
 def _cache_rows(call, cache, block_table, starts, num_rows, cu_rows, latent, k_rope, fp8, write):
@@ -787,7 +791,7 @@ def _free_list(dev, free_pages, num_free):
 
 def _slots(dev, of, slots, n):
     """Check an int64 [n] of slots; returns its address."""
-    ptr = _on(dev, of, "slots", slots, torch.int64)
+    ptr = _on(dev, of, "slots", slots, _INT64)
     if slots.shape != (n,):
         raise ValueError(f"slots must be [{n}]")
     return ptr
@@ -811,7 +815,7 @@ def mla_rope_turns(rope_dim: int, base: float = 10000.0, factor: float = 1.0, or
 
 def _weight(dev, of, weight, d):
     """Check a norm's weight (bf16 [d]); returns its address."""
-    ptr = _on(dev, of, "weight", weight, torch.bfloat16)
+    ptr = _on(dev, of, "weight", weight, _BF16)
     if weight.shape != (d,):
         raise ValueError(f"weight must be [{d}]")
     if ptr % 16:
@@ -822,9 +826,9 @@ def _weight(dev, of, weight, d):
 def _heads(name: str, t: torch.Tensor, dev: Optional[torch.device], of: str) -> Tuple[int, int, int]:
     """bf16 [n, heads, d] with unit inner stride, 16-byte aligned heads; returns the strides of a token and a head,
     and the address."""
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not _BF16:
         raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
     if t.device != dev:
         if not t.is_cuda:
@@ -945,7 +949,7 @@ def mla_norm_rope_cache_write_fp8(latent: torch.Tensor, k_rope: torch.Tensor, po
 
 
 # ---------------------------------------------------------------- prompt attention
-_HEAD = _lib.MLA_PREFILL_HEAD_DIM
+_HEAD, _ROPE = _lib.MLA_PREFILL_HEAD_DIM, _lib.MLA_HEAD_DIM - MLA_V_DIM
 
 
 @functools.lru_cache(maxsize=256)
@@ -1000,7 +1004,7 @@ def mla_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.T
     v_token, v_head, v_ptr = _heads("v", v, dev, "q")
     num_q, h_q, d_qk = q.shape
     num_k, h_kv, d_k = k.shape
-    rope = 0 if k_rope is None else _lib.MLA_HEAD_DIM - MLA_V_DIM
+    rope = 0 if k_rope is None else _ROPE
     if d_k != _HEAD or d_qk != _HEAD + rope or v.shape != (num_k, h_kv, _HEAD) or h_q % h_kv:
         raise ValueError(f"q must be [num_q, h_q, {_HEAD + rope}], k and v [num_k, h_kv, {_HEAD}], h_q a multiple of h_kv")
     rope_ptr, rope_stride = None, 0
