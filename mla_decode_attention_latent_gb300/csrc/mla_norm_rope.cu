@@ -28,7 +28,7 @@
 //
 // Rows: a warp per cached row, the 512 latent dims as 64 pieces over its lanes and
 // the RoPE key as 8 more; each lane computes one of the row's 32 angles.  A step of 64 rows
-// takes 1.8 us, 5000 bf16 rows 4.1, 32,768 rows into e4m3 pages 17.6 (3.2 TB/s: two thirds of
+// takes 1.9 us, 5000 bf16 rows 4.1, 32,768 rows into e4m3 pages 16.4 (3.5 TB/s: two thirds of
 // the issue slots, the quotients above all).
 #include <cuda_runtime.h>
 
@@ -316,21 +316,31 @@ constexpr int kRopeDims = kDqk - kDv;
 // within its last bit.  Two values per instruction.  A zero's code is +0.
 __device__ __forceinline__ uint2 quantise8(const float (&y)[8], float c, float inv) {
     uint32_t code[4];
-    if (c < 0x1p-100f) {  // the remainder and the reciprocal leave the normal range
+    const uint64_t inv2 = sm103::f2_pack(inv, inv), minus_c2 = sm103::f2_pack(-c, -c), zero2 = sm103::f2_pack(0.f, 0.f);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) code[k] = sm103::pack_e4m3x2(y[2 * k] / c + 0.f, y[2 * k + 1] / c + 0.f);
-    } else {
-        const uint64_t inv2 = sm103::f2_pack(inv, inv), minus_c2 = sm103::f2_pack(-c, -c), zero2 = sm103::f2_pack(0.f, 0.f);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const uint64_t v = sm103::f2_pack(y[2 * k], y[2 * k + 1]);
-            const uint64_t q = sm103::f2_fma(v, inv2, zero2), r = sm103::f2_fma(q, minus_c2, v);
-            float a, b;
-            sm103::f2_unpack(sm103::f2_fma(r, inv2, q), a, b);
-            code[k] = sm103::pack_e4m3x2(a, b);
-        }
+    for (int k = 0; k < 4; ++k) {
+        const uint64_t v = sm103::f2_pack(y[2 * k], y[2 * k + 1]);
+        const uint64_t q = sm103::f2_fma(v, inv2, zero2), r = sm103::f2_fma(q, minus_c2, v);
+        float a, b;
+        sm103::f2_unpack(sm103::f2_fma(r, inv2, q), a, b);
+        code[k] = sm103::pack_e4m3x2(a, b);
     }
     return make_uint2(code[0] | (code[1] << 16), code[2] | (code[3] << 16));
+}
+
+// the same for rows so small that the remainder and the reciprocal leave the normal range
+__device__ __forceinline__ uint2 quantise8_small(const float (&y)[8], float c) {
+    uint32_t code[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) code[k] = sm103::pack_e4m3x2(y[2 * k] / c + 0.f, y[2 * k + 1] / c + 0.f);
+    return make_uint2(code[0] | (code[1] << 16), code[2] | (code[3] << 16));
+}
+
+// max |y| / 448, rounded to nearest: with 1/448 rounded, one fused remainder makes it so
+__device__ __forceinline__ float row_scale(float top) {
+    constexpr float kInv = 1.f / 448.f;
+    const float q = top * kInv;
+    return fmaf(fmaf(q, -448.f, top), kInv, q);
 }
 
 template <int D, bool kE4m3>
@@ -405,7 +415,10 @@ __global__ void __launch_bounds__(kRowWarps * 32) place_rows_kernel(const PlaceR
 #pragma unroll
             for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(f[j][k]) & 0x7fffffffu);
         top = __reduce_max_sync(0xffffffffu, top);
-        const float c = top >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : top ? fmaxf(__uint_as_float(top) / 448.f, 0x1p-149f) : 1.f;
+        // (rows of values that fp32 holds to fewer bits take divisions)
+        const bool small = top < 0x12800000u;  // 2^-90: a scale below 2^-98
+        const float m = __uint_as_float(top);
+        const float c = top >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : !top ? 1.f : small ? fmaxf(m / 448.f, 0x1p-149f) : row_scale(m);
         uint8_t *page = static_cast<uint8_t *>(p.cache) + (slot / kPage) * (int64_t)MLA_FP8_PAGE_BYTES(kDqk);
         const int off = (int)(slot % kPage);
         if (lane == 0) {
@@ -413,10 +426,16 @@ __global__ void __launch_bounds__(kRowWarps * 32) place_rows_kernel(const PlaceR
             reinterpret_cast<float *>(page + kPage * kDqk)[off] = c;
         }
         uint2 *dst = reinterpret_cast<uint2 *>(page + off * kDqk);
-        const float inv = 1.f / c;
+        if (small && top) {
 #pragma unroll
-        for (int j = 0; j < 3; ++j)
-            if (j < 2 || lane < 8) dst[lane + 32 * j] = quantise8(f[j], c, inv);
+            for (int j = 0; j < 3; ++j)
+                if (j < 2 || lane < 8) dst[lane + 32 * j] = quantise8_small(f[j], c);
+        } else {
+            const float inv = 1.f / c;
+#pragma unroll
+            for (int j = 0; j < 3; ++j)
+                if (j < 2 || lane < 8) dst[lane + 32 * j] = quantise8(f[j], c, inv);
+        }
     }
 }
 
