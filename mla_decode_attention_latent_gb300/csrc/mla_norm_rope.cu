@@ -28,7 +28,7 @@
 //
 // Rows: a warp per cached row, the 512 latent dims as 64 pieces over its lanes and
 // the RoPE key as 8 more; each lane computes one of the row's 32 angles.  A step of 64 rows
-// takes 1.9 us, 5000 bf16 rows 4.1, 32,768 rows into e4m3 pages 16.4 (3.5 TB/s: two thirds of
+// takes 1.9 us, 5000 bf16 rows 3.6, 32,768 rows into e4m3 pages 15.3 (3.7 TB/s: two thirds of
 // the issue slots, the quotients above all).
 #include <cuda_runtime.h>
 
@@ -377,19 +377,21 @@ __global__ void __launch_bounds__(kRowWarps * 32) place_rows_kernel(const PlaceR
     if constexpr (kRope) {
         // lane i turns pair i; eight lanes (four groups of them, alike) need 8 or 4 pairs each
         const float2 mine = angle(p.rope.positions[r], p.rope.turns[lane], p.rope.scale);
-        float g[8];
-        widen8(key, f[2]);
-        widen8(other, g);
         const int i = lane & 7;
         float2 cs[8];
+        float g[8];
+        widen8(key, f[2]);
+        if (p.rope.interleaved) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int from = p.rope.interleaved ? 4 * i + (k & 3) : 8 * (i & 3) + k;
-            cs[k].x = __shfl_sync(0xffffffffu, mine.x, from);
-            cs[k].y = __shfl_sync(0xffffffffu, mine.y, from);
+            for (int k = 0; k < 4; ++k) cs[k] = make_float2(__shfl_sync(0xffffffffu, mine.x, 4 * i + k), __shfl_sync(0xffffffffu, mine.y, 4 * i + k));
+            rotate8<true>(f[2], g, cs, true);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                cs[k] = make_float2(__shfl_sync(0xffffffffu, mine.x, 8 * (i & 3) + k), __shfl_sync(0xffffffffu, mine.y, 8 * (i & 3) + k));
+            widen8(other, g);
+            rotate8<false>(f[2], g, cs, i < half);
         }
-        if (p.rope.interleaved) rotate8<true>(f[2], g, cs, true);
-        else rotate8<false>(f[2], g, cs, i < half);
     }
     if (p.latent_out) {
         uint4 *out = reinterpret_cast<uint4 *>(p.latent_out + r * p.latent_out_stride);
