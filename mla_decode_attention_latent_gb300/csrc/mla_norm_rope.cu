@@ -28,7 +28,7 @@
 //
 // Rows: a warp per cached row, the 512 latent dims as 64 pieces over its lanes and
 // the RoPE key as 8 more; each lane computes one of the row's 32 angles.  A step of 64 rows
-// takes 1.9 us, 5000 bf16 rows 3.6, 32,768 rows into e4m3 pages 15.3 (3.7 TB/s: two thirds of
+// takes 1.9 us, 5000 bf16 rows 3.6, 32,768 rows into e4m3 pages 15.1 (3.8 TB/s: two thirds of
 // the issue slots, the quotients above all).
 #include <cuda_runtime.h>
 
@@ -308,7 +308,7 @@ cudaError_t launch_heads(const NormRopeParams &p, cudaStream_t stream) {
 }
 
 // ---------------------------------------------------------------- rows into the cache
-constexpr int kRowWarps = 8;
+constexpr int kRowWarps = 4;  // (8: 32,768 e4m3 rows 15.3 us for 15.1, 5000 bf16 rows 3.64 for 3.55)
 constexpr int kRopeDims = kDqk - kDv;
 
 // e4m3(y / c) of 8 values.  With inv the rounded reciprocal of c, q = y inv, the remainder
