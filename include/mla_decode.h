@@ -750,8 +750,9 @@ MLA_API int mla_get_metadata_prefill(const int32_t *cu_q, const int32_t *cu_k, i
  *            MLA_DEVERR_SEQLEN
  *   h_q      a multiple of h_kv, at most 128 h_kv
  *   softmax_scale  > 0
- *   metadata from mla_get_metadata_prefill with the same bounds and shapes, or NULL:
- *            computed by this call, in the workspace
+ *   metadata from mla_get_metadata_prefill with the same bounds, shapes and mask, or NULL:
+ *            computed by this call, in the workspace.  One that was made for another mask or
+ *            other heads does nothing but set MLA_DEVERR_SEQLEN
  *   out      device bf16 [num_q][h_q][128], out, 32-byte aligned;  lse  device fp32
  *            [num_q][h_q], out:
  *            natural log of the sum of exp(softmax_scale q . k), for joining with other

@@ -98,7 +98,9 @@ struct Walk {
     PreSegment ahead;
     int ahead_head;
     __device__ Walk(const PrefillParams &p) : work(p.metadata, p.max_blocks, p.sms) {
-        segments = (int)min((long long)max(0, work.header->segments), (long long)pre_max_segments(p.max_blocks, p.sms));
+        const bool fits = pre_fits(*work.header, p);
+        if (!fits && blockIdx.x == 0 && (threadIdx.x & 31) == 0) atomicOr(p.status, MLA_DEVERR_SEQLEN);
+        segments = !fits ? 0 : (int)min((long long)max(0, work.header->segments), (long long)pre_max_segments(p.max_blocks, p.sms));
         fetch(p);
     }
     __device__ __forceinline__ void fetch(const PrefillParams &p) {
@@ -846,7 +848,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) prefill_combine_kernel(con
     const PreWork work(p.metadata, p.max_blocks, p.sms);
     const int lane = threadIdx.x & 31, per = pre_tile_tokens(p.group);
     constexpr int kUnits = kPreRows / 32 * (kPreHead / kCombineDims);  // of an item
-    const int n = max(0, min(work.header->cuts, pre_slots(p.sms)));
+    const int n = pre_fits(*work.header, p) ? max(0, min(work.header->cuts, pre_slots(p.sms))) : 0;
     const int64_t total = (int64_t)n * p.h_kv * kUnits, stride = gridDim.x * kCombineWarps;
     for (int64_t i = (int64_t)blockIdx.x * kCombineWarps + (threadIdx.x >> 5); i < total; i += stride) {
         const int unit = (int)(i % kUnits), head = (int)(i / kUnits % p.h_kv);

@@ -28,7 +28,9 @@ struct PreCut {
 };
 // Work of a call, as int32 words: a header, the segments (most steps first), the cut blocks.
 struct PreHeader {
-    int segments, cuts, pad[6];
+    int segments, cuts;
+    int causal, group, h_kv;  // of the call that it was made for
+    int pad[3];
 };
 
 // tokens of a query tile: its 128 rows hold `group` heads per token
@@ -50,6 +52,10 @@ __host__ __device__ inline int64_t pre_max_segments(int64_t max_blocks, int ctas
 }
 // slots of partial results, each of one part and key head
 __host__ __device__ constexpr int pre_slots(int ctas) { return 2 * ctas; }
+// whether a partition was made for such a call
+__device__ inline bool pre_fits(const PreHeader &h, const PrefillParams &p) {
+    return h.causal == (int)p.causal && h.group == p.group && h.h_kv == p.h_kv;
+}
 // keys that token i of a block sees
 __host__ __device__ inline int pre_seen(const PreSegment &b, int i) {
     const long long n = (long long)b.seen + i;

@@ -157,10 +157,7 @@ __global__ void __launch_bounds__(kThreads) prefill_schedule_kernel(const Prefil
             const int at = atomicAdd(&sh.count[bucket(x.step1)], 1);
             if (at < blocks) work.segments[at] = x;
         });
-        if (threadIdx.x == 0) {
-            work.header->segments = blocks;
-            work.header->cuts = 0;
-        }
+        if (threadIdx.x == 0) *work.header = {blocks, 0, (int)p.causal, p.group, p.h_kv, {}};
         return;
     }
     int most = 0x7fffffff;  // c
@@ -248,10 +245,7 @@ __global__ void __launch_bounds__(kThreads) prefill_schedule_kernel(const Prefil
         x.part = n > 1 ? x.part + k : -1;
         work.segments[atomicAdd(&sh.count[bucket(mine)], 1)] = x;
     }
-    if (threadIdx.x == 0) {
-        work.header->segments = segments;
-        work.header->cuts = sh.cuts;
-    }
+    if (threadIdx.x == 0) *work.header = {segments, sh.cuts, (int)p.causal, p.group, p.h_kv, {}};
 }
 
 template <int kThreads>

@@ -342,3 +342,24 @@ def test_weights_that_outgrow_their_reference_in_either_half(dev):
         out, lse = mla.mla_prefill(q, k, v, cu_of([n], dev), cu_of([m], dev), causal=causal)
         check(out, lse, q, k, v, None, [n], [m], causal)
     assert mla.mla_device_status() == 0
+
+
+def test_a_partition_of_another_call_is_reported(dev):
+    """Made for the other mask, or for more heads (of as many words): nothing is written, with cuts and without."""
+    for lq, lk in (([70, 33], [70, 50]), ([64], [9000])):
+        q, k, v, kr = make(dev, lq, lk, 4, 2, True)
+        cq, ck = cu_of(lq, dev), cu_of(lk, dev)
+        for heads, causal in (((4, 2), False), ((8, 4), True), ((4, 1), True)):
+            md = mla.mla_get_metadata_prefill(cq, ck, q.shape[0], k.shape[0], *heads, causal=causal)
+            out, lse = torch.full((q.shape[0], 4, 128), 5.0, dtype=torch.bfloat16, device=dev), torch.full((q.shape[0], 4), 5.0, device=dev)
+            try:
+                mla.mla_prefill(q, k, v, cq, ck, k_rope=kr, out=out, lse=lse, metadata=md)
+            except ValueError:  # another number of words
+                assert heads == (4, 1)
+                continue
+            assert mla.mla_device_status() == _lib.MLA_DEVERR_SEQLEN
+            assert (out == 5).all() and (lse == 5).all()
+        md = mla.mla_get_metadata_prefill(cq, ck, q.shape[0], k.shape[0], 4, 2)
+        out, lse = mla.mla_prefill(q, k, v, cq, ck, k_rope=kr, metadata=md)
+        check(out, lse, q, k, v, kr, lq, lk, True)
+        assert mla.mla_device_status() == 0
