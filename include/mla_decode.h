@@ -752,7 +752,8 @@ MLA_API int mla_get_metadata_prefill(const int32_t *cu_q, const int32_t *cu_k, i
  *   softmax_scale  > 0
  *   metadata from mla_get_metadata_prefill with the same bounds, shapes and mask, or NULL:
  *            computed by this call, in the workspace.  One that was made for another mask or
- *            other heads does nothing but set MLA_DEVERR_SEQLEN
+ *            other heads, or whose cut blocks a call of this num_q and num_k would not join,
+ *            does nothing but set MLA_DEVERR_SEQLEN
  *   out      device bf16 [num_q][h_q][128], out, 32-byte aligned;  lse  device fp32
  *            [num_q][h_q], out:
  *            natural log of the sum of exp(softmax_scale q . k), for joining with other

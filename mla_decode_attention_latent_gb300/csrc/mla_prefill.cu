@@ -100,7 +100,7 @@ struct Walk {
     __device__ Walk(const PrefillParams &p) : work(p.metadata, p.max_blocks, p.sms) {
         const bool fits = pre_fits(*work.header, p);
         if (!fits && blockIdx.x == 0 && (threadIdx.x & 31) == 0) atomicOr(p.status, MLA_DEVERR_SEQLEN);
-        segments = !fits ? 0 : (int)min((long long)max(0, work.header->segments), (long long)pre_max_segments(p.max_blocks, p.sms));
+        segments = !fits ? 0 : max(0, work.header->segments);
         fetch(p);
     }
     __device__ __forceinline__ void fetch(const PrefillParams &p) {

@@ -52,9 +52,12 @@ __host__ __device__ inline int64_t pre_max_segments(int64_t max_blocks, int ctas
 }
 // slots of partial results, each of one part and key head
 __host__ __device__ constexpr int pre_slots(int ctas) { return 2 * ctas; }
-// whether a partition was made for such a call
+// Whether a partition is one for such a call: of its mask and heads, with no more segments than there is room for,
+// and with cuts only where the host enqueues the combine (it goes by this call's rows and keys, which may be
+// padded otherwise than those that the partition was made for).
 __device__ inline bool pre_fits(const PreHeader &h, const PrefillParams &p) {
-    return h.causal == (int)p.causal && h.group == p.group && h.h_kv == p.h_kv;
+    return h.causal == (int)p.causal && h.group == p.group && h.h_kv == p.h_kv && h.segments <= pre_max_segments(p.max_blocks, p.sms) &&
+           (h.cuts <= 0 || pre_may_cut(p.max_blocks, p.num_k, p.h_kv, p.sms));
 }
 // keys that token i of a block sees
 __host__ __device__ inline int pre_seen(const PreSegment &b, int i) {
