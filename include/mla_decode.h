@@ -605,7 +605,8 @@ MLA_API int mla_decode_kvcache_tree_fp8(const void *q, const void *kv_pages, int
  *                  another word (the step is planned: free_pages is only read)
  *   new_seqlens    device int32 [batch], out; may be cache_seqlens
  *   positions, slots  device int32 / int64 [num_rows], out, or NULL
- * A sequence whose bounds or lengths make no sense, or that would pass its table,
+ * A sequence whose bounds or lengths make no sense (bounds that descend, leave the rows
+ * or begin before the end of an earlier sequence), or that would pass its table,
  * is not served and needs nothing, and sets MLA_DEVERR_SEQLEN; a table entry that is
  * no page where a row lands gives slot -1 and sets MLA_DEVERR_BLOCK_ID.
  * One kernel, no workspace.  Errors: MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED

@@ -12,6 +12,11 @@
 // are the top of the stack without gaps.)  Row r of sequence b is at position
 // p = len_b + r - cu_rows[b], in slot 64 * page + p % 64.
 //
+// Bounds that descend, leave the rows or begin before the end of an earlier sequence
+// (of those with 0 <= lo <= hi <= num_rows) belong to nobody.  A chunk of sequences that has
+// any takes, in place of such a bound, the largest end before it: bounds that ascend, in
+// which every other sequence keeps its own rows and each row is some chunk's.
+//
 // Everything follows from prefix sums of the need, which every CTA computes for
 // itself, so nothing is exchanged between CTAs: the page of a position is an
 // entry of the table as it was (have_b and below) or an entry of the free list.
@@ -40,17 +45,38 @@ constexpr int kRunsInFlight = 2;
 template <int kThreads>
 struct AssignShared {
     long long warp[kThreads / 32];
-    int cu[kThreads + 1];
+    int cu[kThreads + 1];     // ascending
     int len[kThreads];        // rows before the step; -1: not served
     long long first[kThreads];  // pages that earlier sequences need
     int taken;                // pages taken so far
 };
 
+// Bounds that ascend in sh.cu, the largest end before it in place of a senseless one; whether this thread's is one.
+// Out of line: a call without any does not fetch it.
+template <int kThreads>
+__device__ __noinline__ bool ascending_bounds(AssignShared<kThreads> &sh, int n, int covered, int lo, int hi, int64_t num_rows) {
+    const int tid = threadIdx.x;
+    const bool bad = lo < 0 || hi < lo || hi > num_rows;
+    int end = bad || tid >= n ? 0 : hi;  // the largest up to each sequence, by doubling distances
+    for (int off = 1; off < kThreads; off <<= 1) {
+        sh.len[tid] = end;
+        __syncthreads();
+        if (tid >= off) end = max(end, sh.len[tid - off]);
+        __syncthreads();
+    }
+    sh.len[tid] = end;
+    __syncthreads();
+    const int earlier = tid ? max(covered, sh.len[tid - 1]) : covered;
+    if (tid < n && (bad || lo < earlier)) sh.cu[tid] = earlier;
+    if (tid == n - 1) sh.cu[n] = max(covered, end);
+    return bad || lo < earlier;
+}
+
 template <int kThreads>
 __global__ void __launch_bounds__(kThreads) assign_pages_kernel(const AssignPagesParams p, bool wide) {
     __shared__ AssignShared<kThreads> sh;
     sm103::griddep_wait();
-    const int tid = threadIdx.x, lane = tid & 31;
+    const int tid = threadIdx.x;
     const int cta = blockIdx.x, ctas = gridDim.x;  // one cluster
     int left = *p.num_free;
     if (left < 0 || left > p.max_free) {
@@ -59,23 +85,34 @@ __global__ void __launch_bounds__(kThreads) assign_pages_kernel(const AssignPage
     }
     const long long cap = (long long)p.max_blocks * kPage;
     long long before = 0;  // pages needed by the chunks so far
+    int covered = 0;       // rows of the chunks so far
     if (tid == 0) sh.taken = 0;
     for (int c0 = 0; c0 < p.batch; c0 += kThreads) {
         const int n = min(kThreads, p.batch - c0), b = c0 + tid;
-        int len = 0, count = 0, need = 0;
+        int len = 0, count = 0, need = 0, lo = 0, hi = 0;
         bool bad = false;
         if (tid < n) {
-            const int lo = p.cu_rows[b], hi = p.cu_rows[b + 1];
+            lo = p.cu_rows[b], hi = p.cu_rows[b + 1];
             sh.cu[tid] = lo;
             if (tid == n - 1) sh.cu[n] = hi;
             len = p.seqlens[b];
-            count = hi - lo;
-            bad = lo < 0 || hi < lo || hi > p.num_rows || len < 0 || (long long)len + count > cap;
-            if (bad) atomicOr(p.status, MLA_DEVERR_SEQLEN);
-            else need = pages_of(len + count) - pages_of(len);
+            bad = lo < 0 || hi < lo || hi > p.num_rows;
         }
-        long long total;
-        const long long first = before + block_exclusive_scan<kThreads>((long long)need, sh.warp, &total);
+        // (a sequence's need is below 2^25; a senseless bound counts above all of them)
+        const bool odd = bad || (tid == 0 && lo < covered);
+        auto need_pages = [&] {
+            count = bad ? 0 : hi - lo;
+            bad = bad || len < 0 || (long long)len + count > cap;
+            need = bad ? 0 : pages_of(len + count) - pages_of(len);
+            return (long long)need;
+        };
+        long long total, earlier_need = block_exclusive_scan<kThreads>(need_pages() + (odd ? 1ll << 40 : 0), sh.warp, &total);
+        if (total >> 40) {
+            bad = ascending_bounds(sh, n, covered, lo, hi, p.num_rows) || tid >= n;
+            earlier_need = block_exclusive_scan<kThreads>(need_pages(), sh.warp, &total);
+        }
+        const long long first = before + earlier_need;
+        if (tid < n && bad) atomicOr(p.status, MLA_DEVERR_SEQLEN);
         const bool served = tid < n && !bad && (need == 0 || first + need <= left);
         if (tid < n) {
             sh.len[tid] = served ? len : -1;
@@ -98,7 +135,8 @@ __global__ void __launch_bounds__(kThreads) assign_pages_kernel(const AssignPage
             if (sh.len[i] >= 0) p.block_table[(size_t)(c0 + i) * p.max_blocks + pages_of(sh.len[i]) + (k - sh.first[i])] = p.free_pages[left - 1 - k];
         }
         // the chunk's rows (and those before the first sequence and behind the last)
-        const long long r0 = c0 == 0 ? 0 : max(0, sh.cu[0]), r1 = c0 + n == p.batch ? p.num_rows : min((long long)sh.cu[n], (long long)p.num_rows);
+        const long long r0 = covered, r1 = c0 + n == p.batch ? p.num_rows : sh.cu[n];
+        covered = sh.cu[n];
         const long long stride = (long long)ctas * kThreads * kRun;
         for (long long r = (r0 & ~(long long)(kRun - 1)) + ((long long)cta * kThreads + tid) * kRun; r < r1; r += stride * kRunsInFlight) {
             int pos[kRunsInFlight][kRun], page[kRunsInFlight][kRun];
