@@ -73,19 +73,43 @@ __device__ __forceinline__ float squares(uint4 x, float k = 1.f) {
     return s;
 }
 
+// 8 values times 2^90: exact for values below 2^-45, which stay bf16 values
+__device__ __forceinline__ uint4 raised8(uint4 x) {
+    auto raised = [](uint32_t pair) {
+        uint32_t y;
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(pair), "r"(0x6c806c80u));
+        return y;
+    };
+    return make_uint4(raised(x.x), raised(x.y), raised(x.z), raised(x.w));
+}
+
+// What is added to the mean of the squares: with nothing, the reciprocal of a root can leave fp32
+// (rows of bf16's subnormal values), with the smallest eps it is at most 2^75.
+enum Eps { kSome, kNone };
+
 // 1 / sqrt(mean of x^2 + eps) for a row whose sum of squares of k x is sum(k), the
 // same in all of its lanes.  Values near the ends of the type, whose squares leave
 // fp32, are scaled by a power of two first; the whole warp takes that way together.
-template <typename Sum>
-__device__ __forceinline__ float inverse_rms(Sum sum, int d, float eps) {
+// The power is in the result, but for small values (each below 2^-45) without an eps: they are to
+// be multiplied by 2^90 by raise(), and the result is theirs.
+template <Eps kEps, typename Sum, typename Raise>
+__device__ __forceinline__ float inverse_rms(Sum sum, Raise raise, int d, float eps) {
     float s = sum(1.f);
     const float share = 1.f / (float)d;
     float inv = rsqrtf(s * share + eps);
     const bool large = !(s < 0x1p120f), small = s < 0x1p-90f && eps < 0x1p-60f;
     if (__any_sync(0xffffffffu, large || small)) {
-        const float k = large ? 0x1p-70f : 0x1p70f;
+        const float k = large ? 0x1p-70f : kEps == kNone ? 0x1p90f : 0x1p70f;
         s = sum(k);
-        if (large || small) inv = k * rsqrtf(s * share + eps * k * k);
+        if constexpr (kEps == kNone) {
+            if (large) inv = k * rsqrtf(s * share);
+            if (small) {
+                inv = rsqrtf(s * share);
+                raise();
+            }
+        } else if (large || small) {
+            inv = k * rsqrtf(s * share + eps * k * k);
+        }
     }
     return inv;
 }
@@ -128,8 +152,8 @@ enum Pairs {
     kReload,      // any other place: loaded again
 };
 
-// kGroup: lanes of a head, kPieces: 16-byte pieces of a lane
-template <int kGroup, int kPieces, bool kNorm, Pairs kPairs>
+// kGroup: lanes of a head, kPieces: 16-byte pieces of a lane, kEps: of a norm
+template <int kGroup, int kPieces, bool kNorm, Pairs kPairs, Eps kEps>
 __global__ void __launch_bounds__(kThreads, kPairs == kReload ? 2 : kPieces <= 3 ? 4 : 3) norm_rope_kernel(const NormRopeParams p, int rows_per_cta) {
     constexpr int kGroups = kThreads / kGroup;
     extern __shared__ float2 s_angle[];  // [tokens of the CTA][rope_dim / 2]
@@ -179,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, kPairs == kReload ? 2 : kPieces <= 3
     if (pairs || kNorm) __syncthreads();
     // every group makes the same number of turns, for the shuffles
     for (int r = group; r - group < count; r += kGroups) {
-        const Pieces v = next;
+        Pieces v = next;
         if (r - group + kGroups < count) load(r + kGroups, next);
         if constexpr (kPairs == kReload) __syncwarp();  // in place: no lane stores a head before all have loaded it
         int token, head;
@@ -187,13 +211,19 @@ __global__ void __launch_bounds__(kThreads, kPairs == kReload ? 2 : kPieces <= 3
         uint4 *dst = reinterpret_cast<uint4 *>(p.out + (token0 + token) * p.out_token + head * p.out_head);
         float inv = 1.f;
         if constexpr (kNorm) {
-            inv = inverse_rms([&](float k) {
+            inv = inverse_rms<kEps>([&](float k) {
                 float s = 0.f;
 #pragma unroll
                 for (int j = 0; j < kPieces; ++j) s += squares(v.x[j], k);
 #pragma unroll
                 for (int off = 1; off < kGroup; off <<= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
                 return s;
+            }, [&] {
+#pragma unroll
+                for (int j = 0; j < kPieces; ++j) {
+                    v.x[j] = raised8(v.x[j]);
+                    if constexpr (kPairs == kReload) v.again[j] = raised8(v.again[j]);
+                }
             }, p.d, p.eps);
         }
         const float2 *cs = s_angle + token * pairs;
@@ -268,13 +298,13 @@ __global__ void __launch_bounds__(kThreads, kPairs == kReload ? 2 : kPieces <= 3
     }
 }
 
-template <int kGroup, int kPieces, bool kNorm>
+template <int kGroup, int kPieces, bool kNorm, Eps kEps>
 void (*heads_kernel(Pairs pairs))(NormRopeParams, int) {
     switch (pairs) {
-        case kNeighbours: return norm_rope_kernel<kGroup, kPieces, kNorm, kNeighbours>;
-        case kOwn: return norm_rope_kernel<kGroup, kPieces, kNorm, (kGroup == kNarrow && kPieces > 1) ? kOwn : kReload>;  // (halves of 64 values)
-        case kOther: return norm_rope_kernel<kGroup, kPieces, kNorm, kOther>;
-        default: return norm_rope_kernel<kGroup, kPieces, kNorm, kReload>;
+        case kNeighbours: return norm_rope_kernel<kGroup, kPieces, kNorm, kNeighbours, kEps>;
+        case kOwn: return norm_rope_kernel<kGroup, kPieces, kNorm, (kGroup == kNarrow && kPieces > 1) ? kOwn : kReload, kEps>;  // (halves of 64 values)
+        case kOther: return norm_rope_kernel<kGroup, kPieces, kNorm, kOther, kEps>;
+        default: return norm_rope_kernel<kGroup, kPieces, kNorm, kReload, kEps>;
     }
 }
 
@@ -303,8 +333,11 @@ cudaError_t launch_heads(const NormRopeParams &p, cudaStream_t stream) {
     const int half = pairs / 8, rel = (p.d - p.first) / 8 - pairs / 4;  // pieces of a half, and before the first
     const Pairs where = p.rope.interleaved || !pairs ? kNeighbours : half == kGroup && rel % kGroup == 0 ? kOwn
                         : 2 * half <= kGroup && (half & (half - 1)) == 0 && rel % (2 * half) == 0 ? kOther : kReload;
-    return launch_after(p.weight ? heads_kernel<kGroup, kPieces, true>(where) : heads_kernel<kGroup, kPieces, false>(where), dim3((unsigned)ctas),
-                        dim3(kThreads), smem, stream, p, per_cta);
+    // (the raised rows of calls without an eps in a kernel of their own: in the others, which never meet them, they cost
+    // 4096 tokens of 32 heads of 192, neighbours turned, 16.9 us for 15.9)
+    auto kernel = !p.weight ? heads_kernel<kGroup, kPieces, false, kSome>(where)
+                  : p.eps > 0.f ? heads_kernel<kGroup, kPieces, true, kSome>(where) : heads_kernel<kGroup, kPieces, true, kNone>(where);
+    return launch_after(kernel, dim3((unsigned)ctas), dim3(kThreads), smem, stream, p, per_cta);
 }
 
 // ---------------------------------------------------------------- rows into the cache
@@ -343,7 +376,7 @@ __device__ __forceinline__ float row_scale(float top) {
     return fmaf(fmaf(q, -448.f, top), kInv, q);
 }
 
-template <int D, bool kE4m3>
+template <int D, bool kE4m3, Eps kEps>
 __global__ void __launch_bounds__(kRowWarps * 32) place_rows_kernel(const PlaceRowsParams p) {
     constexpr bool kRope = D > kDv;
     sm103::griddep_wait();
@@ -364,11 +397,14 @@ __global__ void __launch_bounds__(kRowWarps * 32) place_rows_kernel(const PlaceR
     widen8(raw[0], f[0]);
     widen8(raw[1], f[1]);
     if (p.weight) {
-        const float inv = inverse_rms([&](float k) {
+        const float inv = inverse_rms<kEps>([&](float k) {
             float s = squares(raw[0], k) + squares(raw[1], k);
 #pragma unroll
             for (int off = 16; off; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
             return s;
+        }, [&] {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) f[0][k] *= 0x1p90f, f[1][k] *= 0x1p90f;
         }, kDv, p.eps);
         const uint4 *w = reinterpret_cast<const uint4 *>(p.weight);
         scale8(f[0], w[lane], inv);
@@ -454,9 +490,14 @@ cudaError_t launch_norm_rope(const NormRopeParams &p, cudaStream_t stream) {
     }
 }
 
+template <Eps kEps>
+static void (*rows_kernel(int d, bool e4m3))(PlaceRowsParams) {
+    return e4m3 ? place_rows_kernel<kDqk, true, kEps> : d == kDqk ? place_rows_kernel<kDqk, false, kEps> : place_rows_kernel<kDv, false, kEps>;
+}
+
 cudaError_t launch_place_rows(const PlaceRowsParams &p, int d, bool e4m3, cudaStream_t stream) {
     const unsigned grid = (unsigned)((p.num_rows + kRowWarps - 1) / kRowWarps);
-    void (*kernel)(PlaceRowsParams) = e4m3 ? place_rows_kernel<kDqk, true> : d == kDqk ? place_rows_kernel<kDqk, false> : place_rows_kernel<kDv, false>;
+    auto kernel = p.eps > 0.f ? rows_kernel<kSome>(d, e4m3) : rows_kernel<kNone>(d, e4m3);
     return launch_after(kernel, dim3(grid), dim3(kRowWarps * 32), 0, stream, p);
 }
 
