@@ -710,6 +710,7 @@ __device__ void row_role(const PrefillParams &p, const Ctx &c, Items items, uint
 #pragma unroll 1
         for (int i2 = 0; i2 < 2; ++i2) {
             uint32_t both[2][32];
+            __syncwarp();  // rows of no query come here ahead of the others, and the whole warp loads
             tmem_ld32(o_col + 64 * i2, both[0]);
             tmem_ld32(o_col + 64 * i2 + 32, both[1]);
             arrived(both[0], both[1]);
