@@ -7,9 +7,10 @@
 // in fp32 from bf16 values, rounded once when a value is stored.
 //
 // Angles.  A frequency is a whole number of 2^-64 turns per position, so the
-// phase of a position is one 64-bit product that drops whole turns by itself: exact
-// but for the frequency's own 2^-65, at any position, where an angle in radians
-// loses a bit for every doubling.  Its distance to the nearest whole turn goes to
+// phase of a position is one 64-bit product that drops whole turns by itself: exact,
+// at any position, where an angle in radians loses a bit for every doubling, but for the frequency's own
+// roundings, half a unit and those of the doubles that mla_rope_turns computes it in (2^-50 of it: at position
+// 2^31 2^-21 turns at most, 2^-24 measured).  Its distance to the nearest whole turn goes to
 // sincospif as a float, so a small angle keeps its 24 bits.
 //
 // Heads: a group of 8 lanes per head (32 above 256 values), lane l taking the 16-byte pieces l, l + 8, ...
@@ -23,13 +24,14 @@
 // head is stored, so that a call may be in place.
 // Bound by HBM on prompts (4096 tokens of 128 heads of 192 values: 68.6 us, 5.9 TB/s), by
 // the launch on single tokens (64 tokens: 2.1 us), and between them, where the rows come out
-// of L2, by issue slots (1777 tokens of 40 heads of 128: 8.6 us; two heads under way per
-// group instead of one gained nothing).
+// of L2, by latency (1777 tokens of 40 heads of 128: 8.6 us, one wave of CTAs at half of the issue
+// slots; two heads under way per group instead of one gained nothing).  The half layout of heads of 192
+// values with a norm spills 12 bytes at its 64 registers.
 //
 // Rows: a warp per cached row, the 512 latent dims as 64 pieces over its lanes and
 // the RoPE key as 8 more; each lane computes one of the row's 32 angles.  A step of 64 rows
-// takes 1.9 us, 5000 bf16 rows 3.6, 32,768 rows into e4m3 pages 15.1 (3.8 TB/s: two thirds of
-// the issue slots, the quotients above all).
+// takes 1.9 us, 5000 bf16 rows 3.6, 32,768 rows into e4m3 pages 15.1 (3.8 TB/s, two thirds of
+// the issue slots: a warp's row is one chain from its loads to its stores).
 #include <cuda_runtime.h>
 
 #include "mla_internal.h"
@@ -344,7 +346,8 @@ cudaError_t launch_heads(const NormRopeParams &p, cudaStream_t stream) {
 constexpr int kRowWarps = 4;  // (8: 32,768 e4m3 rows 15.3 us for 15.1, 5000 bf16 rows 3.64 for 3.55)
 constexpr int kRopeDims = kDqk - kDv;
 
-// e4m3(y / c) of 8 values.  With inv the rounded reciprocal of c, q = y inv, the remainder
+// e4m3(y / c) of 8 values, the quotient by a reciprocal and a fused remainder (Markstein's
+// method).  With inv the rounded reciprocal of c, q = y inv, the remainder
 // y - q c is exact in one fused operation, and q + (y - q c) inv is the quotient to
 // within its last bit.  Two values per instruction.  A zero's code is +0.
 __device__ __forceinline__ uint2 quantise8(const float (&y)[8], float c, float inv) {

@@ -24,7 +24,7 @@
 // may be updated in place (the lengths, the count of free pages) are written
 // behind a cluster barrier, so one launch does it and no workspace is kept.
 // Bound by latency: a chunk's lengths and bounds, its scan, one page id per row.  64 sequences
-// of one row each take 4.6 us, 48 prompts of up to 4096 rows (83,794) 8.2, and 12.4 on 8 CTAs.
+// of one row each take 4.6 us, 48 prompts of up to 4096 rows (83,794) 8.5, and 12.4 on 8 CTAs.
 #include <cuda_runtime.h>
 
 #include <mutex>
@@ -203,7 +203,9 @@ __global__ void __launch_bounds__(kThreads) assign_pages_kernel(const AssignPage
 }
 
 // Pages of finished sequences onto the stack, in the order of the sequences and
-// of their pages; one CTA.  An entry that is no page is reported and not pushed.
+// of their pages; one CTA, a warp per sequence.  An entry that is no page is reported and not pushed.
+// Bound by latency: 64 sequences of which none has finished take 2.4 us, of which 6 of up to 64
+// pages have 3.5, and 64 of them 5.2; of up to 2048 pages (66,985 in all) 64.
 struct ReleaseShared {
     long long warp[kThreads / 32];
     int count[kThreads];

@@ -25,7 +25,8 @@
 // Bound by the tensor cores' operands: a step of both tiles is 2 x 128 x 128 x (d_qk + 128)
 // products, 2560 cycles at d_qk = 192, and takes 3280, as QK's MMAs read 8 KB of shared
 // memory each, as much as there is in their 64 cycles, and take 85.  4096 tokens of 128 heads
-// (d_qk = 192, causal) 435-455 us, 1.58 PFLOP/s; d_qk = 128 without a mask 1.7.  A few rows
+// (d_qk = 192, causal) 445 us in a burst, 1.54 PFLOP/s, and 480 call after call, under the
+// power cap; d_qk = 128 without a mask 1.7.  A few rows
 // behind long contexts take the same 2 us a step, on as many CTAs as equal parts give (4.1
 // TB/s of keys and values).
 //
@@ -251,8 +252,8 @@ __device__ void load_role(const PrefillParams &p, const Ctx &c, Items items, con
         const Item s = next;
         const int head = s.head, n = max(s.steps_of[0], s.steps_of[1]);
         if (!(ok = look_ahead())) break;
-        // Q of the tiles that walk, behind the first keys: its place is free only when the
-        // products of the segment before have read it
+        // Q of the tiles that walk, ahead of the first keys, which so wait for its place too: it is
+        // free only when the products of the segment before have read it
 #pragma unroll
         for (int t = 0; t < kPreTiles; ++t) {
             if (!ok || s.steps_of[t] == 0) continue;
@@ -609,7 +610,7 @@ __device__ __forceinline__ void store32(void *dst, const uint32_t (&w)[8]) {
 
 // kWholeSteps: the two halves of a step in sight in one go, half 1's first scores under way while half 0's last are
 // weighed (all keys, d_qk = 128: 317 us against 336). At d_qk = 192 the MMAs set the pace, and half the code, for either
-// half, is better: prompt of 4096 at 128 heads 434 against 438, forty prompts of 300 62.7 against 64.6.
+// half, is better: forty prompts of 300 62.7 against 64.6 (a prompt of 4096 at 128 heads 434 against 438, in bursts).
 template <bool kWholeSteps>
 __device__ void row_role(const PrefillParams &p, const Ctx &c, Items items, uint32_t tmem, int t) {
     const int warp = threadIdx.x >> 5, r = threadIdx.x & (kPreTile - 1);

@@ -43,7 +43,10 @@ __host__ __device__ inline int64_t pre_max_blocks(int64_t num_q, int batch, int 
 // are even enough.  By the most blocks and steps that a call can have, which the host
 // knows: it then leaves out the combine.
 constexpr int kPreRounds = 8;
-constexpr int kPreWhole = 9;  // steps that are never worth a cut (by the costs in mla_prefill_schedule.cu)
+// Steps of calls that are left whole.  By the costs in mla_prefill_schedule.cu a lone block of 9 would be cut: 64
+// rows over 1152 keys at 16 heads 13.5 us for 17.9 with a partition in hand, but where nothing is cut the search and
+// the idle combine cost 1 to 4 us a call (one row of 128 heads over 1100 keys 26.4 for 22.2).
+constexpr int kPreWhole = 9;
 __host__ __device__ inline bool pre_may_cut(int64_t max_blocks, int64_t num_k, int h_kv, int ctas) {
     return max_blocks * h_kv <= (int64_t)kPreRounds * ctas && num_k > kPreWhole * kPreTile;
 }

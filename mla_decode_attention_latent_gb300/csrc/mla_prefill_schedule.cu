@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kThreads) prefill_schedule_kernel(const Prefil
             }
 #pragma unroll
             for (int off = 16; off; off >>= 1) units += __shfl_xor_sync(0xffffffffu, units, off);
-            n = __reduce_add_sync(0xffffffffu, n);  // (at most 1280 blocks of 2^23 steps, in parts of 4 or more: below 2^31)
+            n = __reduce_add_sync(0xffffffffu, n);  // (c is at least a quarter of an even share: at most the blocks and four times the CTAs)
             parts = __reduce_add_sync(0xffffffffu, parts);
             longest = __reduce_max_sync(0xffffffffu, longest);
             shortest = __reduce_min_sync(0xffffffffu, shortest);
