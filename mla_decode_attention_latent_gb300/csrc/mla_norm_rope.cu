@@ -254,48 +254,48 @@ __global__ void __launch_bounds__(kThreads, kPairs == kReload ? 2 : kPieces <= 3
             for (int j = 0; j < kPieces; ++j)
                 if (kNorm || j == low || j == low + 1) dst[piece0 + kGroup * j] = round8(f[j]);
                 else dst[piece0 + kGroup * j] = v.x[j];
-            continue;
-        }
+        } else {
 #pragma unroll
-        for (int j = 0; j < kPieces; ++j) {
-            const int at = piece0 + kGroup * j, part = at - rope0;
-            const bool turned = part >= 0 && at < pieces, low = part < half;
-            uint4 other = make_uint4(0, 0, 0, 0);
-            if constexpr (kPairs == kOther) {
-                if (__any_sync(0xffffffffu, turned)) {
-                    other.x = __shfl_xor_sync(0xffffffffu, v.x[j].x, half);
-                    other.y = __shfl_xor_sync(0xffffffffu, v.x[j].y, half);
-                    other.z = __shfl_xor_sync(0xffffffffu, v.x[j].z, half);
-                    other.w = __shfl_xor_sync(0xffffffffu, v.x[j].w, half);
+            for (int j = 0; j < kPieces; ++j) {
+                const int at = piece0 + kGroup * j, part = at - rope0;
+                const bool turned = part >= 0 && at < pieces, low = part < half;
+                uint4 other = make_uint4(0, 0, 0, 0);
+                if constexpr (kPairs == kOther) {
+                    if (__any_sync(0xffffffffu, turned)) {
+                        other.x = __shfl_xor_sync(0xffffffffu, v.x[j].x, half);
+                        other.y = __shfl_xor_sync(0xffffffffu, v.x[j].y, half);
+                        other.z = __shfl_xor_sync(0xffffffffu, v.x[j].z, half);
+                        other.w = __shfl_xor_sync(0xffffffffu, v.x[j].w, half);
+                    }
+                } else if constexpr (kPairs == kReload) {
+                    other = v.again[j];
                 }
-            } else if constexpr (kPairs == kReload) {
-                other = v.again[j];
-            }
-            if (r >= count || at >= pieces) continue;
-            uint4 y = v.x[j];
-            if (kNorm || turned) {
-                float f[8], g[8];
-                widen8(v.x[j], f);
-                if constexpr (kNorm) scale8(f, s_weight[at], inv);
-                if (turned) {
-                    float2 t[8];
-                    // two angles a load
-                    const float4 *from = reinterpret_cast<const float4 *>(cs + (kPairs == kNeighbours ? 4 * part : 8 * (low ? part : part - half)));
+                if (r >= count || at >= pieces) continue;
+                uint4 y = v.x[j];
+                if (kNorm || turned) {
+                    float f[8], g[8];
+                    widen8(v.x[j], f);
+                    if constexpr (kNorm) scale8(f, s_weight[at], inv);
+                    if (turned) {
+                        float2 t[8];
+                        // two angles a load
+                        const float4 *from = reinterpret_cast<const float4 *>(cs + (kPairs == kNeighbours ? 4 * part : 8 * (low ? part : part - half)));
 #pragma unroll
-                    for (int k = 0; k < (kPairs == kNeighbours ? 2 : 4); ++k) {
-                        const float4 two = from[k];
-                        t[2 * k] = make_float2(two.x, two.y);
-                        t[2 * k + 1] = make_float2(two.z, two.w);
+                        for (int k = 0; k < (kPairs == kNeighbours ? 2 : 4); ++k) {
+                            const float4 two = from[k];
+                            t[2 * k] = make_float2(two.x, two.y);
+                            t[2 * k + 1] = make_float2(two.z, two.w);
+                        }
+                        if constexpr (kPairs != kNeighbours) {
+                            widen8(other, g);
+                            if constexpr (kNorm) scale8(g, s_weight[low ? at + half : at - half], inv);
+                        }
+                        rotate8<kPairs == kNeighbours>(f, g, t, low);
                     }
-                    if constexpr (kPairs != kNeighbours) {
-                        widen8(other, g);
-                        if constexpr (kNorm) scale8(g, s_weight[low ? at + half : at - half], inv);
-                    }
-                    rotate8<kPairs == kNeighbours>(f, g, t, low);
+                    y = round8(f);
                 }
-                y = round8(f);
+                dst[at] = y;
             }
-            dst[at] = y;
         }
     }
 }
